@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libreplayssm.so")
 SOURCES = ["rsm_api.cu", "rsm_inst_f32.cu", "rsm_inst_bf16.cu", "rsm_inst_f16.cu", "rsm_inst_q8.cu", "rsm_inst_q8sr.cu",
-           "rsm_inst_tc.cu", "rsm_inst_q8tc.cu", "gdn_inst.cu"]
+           "rsm_inst_tc.cu", "rsm_inst_q8tc.cu", "gdn_inst.cu", "block_api.cu", "ssm_inst.cu", "norm_inst.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
@@ -30,7 +30,8 @@ def nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(ROOT, "include", "replayssm.h"), os.path.abspath(__file__)]
+    files += [os.path.join(ROOT, "include", f) for f in ("replayssm.h", "replayssm_block.h")]
+    files += [os.path.abspath(__file__)]
     return files
 
 

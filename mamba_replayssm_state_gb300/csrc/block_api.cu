@@ -1,0 +1,279 @@
+// block_api.cu -- host side of the layer operators (include/replayssm_block.h):
+// argument validation, choice of kernel, launch.  Nothing here reads device
+// memory, allocates or synchronizes.
+#include <cuda_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+
+#include "norm_params.h"
+#include "ssm_params.h"
+
+namespace {
+
+thread_local char g_error[512];
+
+int fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_error, sizeof g_error, fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int done() {
+  g_error[0] = '\0';
+  return RSM_OK;
+}
+
+struct Named {
+  const void* p;
+  const char* name;
+};
+
+template <int K>
+int need(const Named (&list)[K]) {
+  for (const Named& n : list)
+    if (n.p == nullptr) return fail(RSM_EINVAL, "%s is NULL", n.name);
+  return RSM_OK;
+}
+
+bool is_state(int dt, bool one_byte) {
+  return dt == RSM_F32 || dt == RSM_BF16 || dt == RSM_F16 || (one_byte && (dt == RSM_I8 || dt == RSM_FP8_E4M3));
+}
+
+template <typename A>
+int check_sizes(const A* a) {
+  if (a->num_heads <= 0 || a->num_groups <= 0 || a->num_heads % a->num_groups != 0)
+    return fail(RSM_EINVAL, "num_groups (%d) must divide num_heads (%d)", a->num_groups, a->num_heads);
+  if (a->dim <= 0 || a->dstate <= 0) return fail(RSM_EINVAL, "dim and dstate must be positive");
+  if (a->num_slots < 0) return fail(RSM_EINVAL, "num_slots must be >= 0 (got %d)", a->num_slots);
+  if (a->input_dtype != RSM_BF16 && a->input_dtype != RSM_F32)
+    return fail(RSM_EINVAL, "input_dtype must be BF16 or F32 (got %d)", a->input_dtype);
+  return RSM_OK;
+}
+
+int launch(const void* fn, int64_t grid, int threads, const void* params, void* stream) {
+  if (grid > 0x7FFFFFFFLL) return fail(RSM_EINVAL, "the call needs %lld blocks, more than 2^31-1", static_cast<long long>(grid));
+  void* kargs[] = {const_cast<void*>(params)};
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), kargs, 0,
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+  return done();
+}
+
+int validate(const rsm_ssm_prefill_args* a, bool pointers) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->num_seqs < 0 || a->tokens < 0) return fail(RSM_EINVAL, "num_seqs and tokens must be >= 0");
+  int rc = check_sizes(a);
+  if (rc != RSM_OK) return rc;
+  if (!is_state(a->state_dtype, false)) return fail(RSM_EINVAL, "state_dtype must be F32, BF16 or F16 (got %d)", a->state_dtype);
+  if (pointers && a->num_seqs > 0) {
+    rc = need({{a->A, "A"}, {a->cu_seqlens, "cu_seqlens"}});
+    if (rc != RSM_OK) return rc;
+    if (a->tokens > 0) {
+      rc = need({{a->x, "x"}, {a->B, "B"}, {a->C, "C"}, {a->dt, "dt"}, {a->out, "out"}});
+      if (rc != RSM_OK) return rc;
+    }
+    if ((a->initial_slots != nullptr || a->final_slots != nullptr) && a->state == nullptr)
+      return fail(RSM_EINVAL, "state is NULL and slots are given");
+  }
+  int threads;
+  if (ssm::seq_kernel(a->input_dtype, a->dim, a->dstate, &threads) == nullptr)
+    return fail(RSM_ENOTSUP, "no kernel compiled for dim %d, dstate %d", a->dim, a->dstate);
+  return RSM_OK;
+}
+
+template <typename A>
+int check_batch(const A* a) {
+  if (a->batch < 0) return fail(RSM_EINVAL, "batch must be >= 0 (got %d)", a->batch);
+  if (a->window < 1) return fail(RSM_EINVAL, "window must be >= 1 (got %d)", a->window);
+  const int rc = check_sizes(a);
+  if (rc != RSM_OK) return rc;
+  int threads;
+  if (ssm::seq_kernel(a->input_dtype, a->dim, a->dstate, &threads) == nullptr)
+    return fail(RSM_ENOTSUP, "no kernel compiled for dim %d, dstate %d", a->dim, a->dstate);
+  return a->batch == 0 ? RSM_OK
+                       : need({{a->x, "x"}, {a->B, "B"}, {a->C, "C"}, {a->dt, "dt"}, {a->A, "A"}, {a->out, "out"},
+                               {a->state, "state"}});
+}
+
+template <typename A>
+void fill_batch(const A* a, ssm::Params* p) {
+  p->x = a->x;
+  p->B = a->B;
+  p->C = a->C;
+  p->dt = a->dt;
+  p->A = a->A;
+  p->D = a->D;
+  p->out = a->out;
+  p->status = a->device_status;
+  p->x_bs = a->x_batch_stride;
+  p->x_ts = a->x_stride;
+  p->B_bs = a->B_batch_stride;
+  p->B_ts = a->B_stride;
+  p->C_bs = a->C_batch_stride;
+  p->C_ts = a->C_stride;
+  p->dt_bs = a->dt_batch_stride;
+  p->dt_ts = a->dt_stride;
+  p->out_ts = static_cast<int64_t>(a->num_heads) * a->dim;
+  p->out_bs = p->out_ts * a->window;
+  p->state_ss = a->state_slot_stride;
+  p->units = a->batch;
+  p->window = a->window;
+  p->num_slots = a->num_slots;
+  p->H = a->num_heads;
+  p->G = a->num_groups;
+  p->pad = a->pad_slot_id;
+  p->state_dtype = a->state_dtype;
+}
+
+int launch_seq(const ssm::Params& p, int input_dtype, int dim, int dstate, void* stream) {
+  int threads = 0;
+  const void* fn = ssm::seq_kernel(input_dtype, dim, dstate, &threads);
+  return launch(fn, static_cast<int64_t>(p.units) * p.H, threads, &p, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int rsm_ssm_prefill(const rsm_ssm_prefill_args* a, void* stream) {
+  int rc = validate(a, true);
+  if (rc != RSM_OK) return rc;
+  if (a->num_seqs == 0) return done();
+  ssm::Params p{};
+  p.x = a->x;
+  p.B = a->B;
+  p.C = a->C;
+  p.dt = a->dt;
+  p.A = a->A;
+  p.D = a->D;
+  p.cu_seqlens = a->cu_seqlens;
+  p.state = a->state;
+  p.src = a->initial_slots;
+  p.dst = a->final_slots;
+  p.out = a->out;
+  p.status = a->device_status;
+  p.tokens = a->tokens;
+  p.x_ts = a->x_stride;
+  p.B_ts = a->B_stride;
+  p.C_ts = a->C_stride;
+  p.dt_ts = a->dt_stride;
+  p.out_ts = a->out_stride;
+  p.state_ss = a->state_slot_stride;
+  p.units = a->num_seqs;
+  p.num_slots = a->num_slots;
+  p.H = a->num_heads;
+  p.G = a->num_groups;
+  p.pad = a->pad_slot_id;
+  p.mode = ssm::kPrefill;
+  p.state_dtype = a->state_dtype;
+  return launch_seq(p, a->input_dtype, a->dim, a->dstate, stream);
+}
+
+int64_t rsm_ssm_prefill_workspace(const rsm_ssm_prefill_args* a) {
+  const int rc = validate(a, false);
+  if (rc != RSM_OK) return rc;
+  done();
+  return 0;
+}
+
+int rsm_ssm_step(const rsm_ssm_step_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (!is_state(a->state_dtype, false))
+    return fail(RSM_EINVAL, "state_dtype must be F32, BF16 or F16 (got %d): one-byte states are read by rsm_replayssm_decode and committed by rsm_materialize", a->state_dtype);
+  int rc = check_batch(a);
+  if (rc != RSM_OK) return rc;
+  if (a->batch == 0) return done();
+  rc = need({{a->src_slots, "src_slots"}});
+  if (rc != RSM_OK) return rc;
+  ssm::Params p{};
+  fill_batch(a, &p);
+  p.state = a->state;
+  p.src = a->src_slots;
+  p.dst = a->dst_slots;
+  p.mode = ssm::kStep;
+  return launch_seq(p, a->input_dtype, a->dim, a->dstate, stream);
+}
+
+int rsm_replayssm_decode(const rsm_replayssm_decode_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (!is_state(a->state_dtype, true)) return fail(RSM_EINVAL, "unknown state_dtype %d", a->state_dtype);
+  int rc = check_batch(a);
+  if (rc != RSM_OK) return rc;
+  const bool one_byte = a->state_dtype == RSM_I8 || a->state_dtype == RSM_FP8_E4M3;
+  if (one_byte && (a->dim != 64 || a->dstate != 128))
+    return fail(RSM_EINVAL, "one-byte state requires dim=64 and dstate=128 (got %d, %d)", a->dim, a->dstate);
+  if (a->ring_buffer_len < 1) return fail(RSM_EINVAL, "ring_buffer_len must be >= 1 (got %d)", a->ring_buffer_len);
+  if (a->window > a->ring_buffer_len || a->window > 64)
+    return fail(RSM_EINVAL, "window (%d) must not exceed ring_buffer_len (%d) and 64", a->window, a->ring_buffer_len);
+  if (a->batch == 0) return done();
+  rc = need({{a->slots, "slots"}, {a->ring_start, "ring_start"}, {a->ring_len, "ring_len"}, {a->x_cache, "x_cache"},
+             {a->B_cache, "B_cache"}, {a->dt_cache, "dt_cache"}});
+  if (rc != RSM_OK) return rc;
+  if (one_byte && a->state_scale == nullptr) return fail(RSM_EINVAL, "one-byte state needs state_scale");
+  ssm::Params p{};
+  fill_batch(a, &p);
+  p.state = const_cast<void*>(a->state);
+  p.scale = one_byte ? a->state_scale : nullptr;
+  p.x_cache = a->x_cache;
+  p.B_cache = a->B_cache;
+  p.dt_cache = a->dt_cache;
+  p.src = a->slots;
+  p.ring_start = a->ring_start;
+  p.ring_len = a->ring_len;
+  p.scale_ss = a->scale_slot_stride;
+  p.xc_ss = a->x_cache_slot_stride;
+  p.Bc_ss = a->B_cache_slot_stride;
+  p.dtc_ss = a->dt_cache_slot_stride;
+  p.R = a->ring_buffer_len;
+  p.mode = ssm::kDecode;
+  return launch_seq(p, a->input_dtype, a->dim, a->dstate, stream);
+}
+
+int rsm_add_rms_norm(const rsm_add_rms_norm_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->rows < 0) return fail(RSM_EINVAL, "rows must be >= 0");
+  if (a->dim <= 0) return fail(RSM_EINVAL, "dim must be positive (got %d)", a->dim);
+  const void* fn = rmsnorm::kernel(0, a->input_dtype, a->residual_dtype);
+  if (fn == nullptr)
+    return fail(RSM_EINVAL, "input_dtype and residual_dtype must be BF16 or F32 (got %d, %d)", a->input_dtype, a->residual_dtype);
+  if (a->rows == 0) return done();
+  const int rc = need({{a->x, "x"}, {a->residual, "residual"}, {a->weight, "weight"}, {a->out, "out"}, {a->residual_out, "residual_out"}});
+  if (rc != RSM_OK) return rc;
+  rmsnorm::Params p{a->x, a->residual, a->weight, a->out, a->residual_out, a->rows, a->x_stride, a->residual_stride,
+                 a->out_stride, a->residual_out_stride, a->dim, a->dim, a->residual_scale, a->eps};
+  return launch(fn, a->rows, 256, &p, stream);
+}
+
+int rsm_gated_rms_norm(const rsm_gated_rms_norm_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->rows < 0) return fail(RSM_EINVAL, "rows must be >= 0");
+  if (a->dim <= 0) return fail(RSM_EINVAL, "dim must be positive (got %d)", a->dim);
+  if (a->group_size <= 0 || a->dim % a->group_size != 0)
+    return fail(RSM_EINVAL, "group_size (%d) must divide dim (%d)", a->group_size, a->dim);
+  const void* fn = rmsnorm::kernel(a->norm_before_gate ? 2 : 1, a->input_dtype, a->input_dtype);
+  if (fn == nullptr) return fail(RSM_EINVAL, "input_dtype must be BF16 or F32 (got %d)", a->input_dtype);
+  if (a->rows == 0) return done();
+  const int rc = need({{a->x, "x"}, {a->z, "z"}, {a->weight, "weight"}, {a->out, "out"}});
+  if (rc != RSM_OK) return rc;
+  rmsnorm::Params p{a->x, a->z, a->weight, a->out, nullptr, a->rows, a->x_stride, a->z_stride,
+                 a->out_stride, 0, a->dim, a->group_size, 1.0f, a->eps};
+  return launch(fn, a->rows * (a->dim / a->group_size), 256, &p, stream);
+}
+
+const char* rsm_block_last_error(void) { return g_error; }
+
+int rsm_block_args_size(int index) {
+  switch (index) {
+    case 0: return static_cast<int>(sizeof(rsm_ssm_prefill_args));
+    case 1: return static_cast<int>(sizeof(rsm_ssm_step_args));
+    case 2: return static_cast<int>(sizeof(rsm_replayssm_decode_args));
+    case 3: return static_cast<int>(sizeof(rsm_add_rms_norm_args));
+    case 4: return static_cast<int>(sizeof(rsm_gated_rms_norm_args));
+    default: return 0;
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,36 @@
+// ssm_params.h -- what the linear-attention kernels (prompts, running requests,
+// ring decode) are given, and the compiled (dim, dstate) sizes.
+#pragma once
+#include <cstdint>
+
+#include "../../include/replayssm_block.h"
+
+namespace ssm {
+
+// Where a unit's tokens and state come from.
+enum Mode : int32_t { kPrefill = 0, kStep = 1, kDecode = 2 };
+
+struct Params {
+  const void *x, *B, *C;
+  const float *dt, *A, *D;
+  const int32_t* cu_seqlens;
+  void* state;
+  const float* scale;
+  void *x_cache, *B_cache;
+  float* dt_cache;
+  const int32_t *src, *dst;  // prefill: initial and final slots; decode: dst unused
+  const int32_t *ring_start, *ring_len;
+  void* out;
+  uint32_t* status;
+  int64_t tokens;
+  int64_t x_bs, x_ts, B_bs, B_ts, C_bs, C_ts, dt_bs, dt_ts, out_bs, out_ts;  // batch and token strides, elements
+  int64_t state_ss, scale_ss, xc_ss, Bc_ss, dtc_ss;                         // slot strides, elements
+  int32_t units, window, num_slots, H, G, R, pad, mode, state_dtype;
+};
+
+constexpr int kSeqTokens = 16;  // tokens staged in shared memory at a time (sequential kernel)
+
+// The sequential kernel of an (input type, dim, dstate); NULL when not compiled.
+const void* seq_kernel(int input_dtype, int dim, int dstate, int* threads);
+
+}  // namespace ssm
