@@ -3,11 +3,14 @@
 // memory, allocates or synchronizes.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "norm_params.h"
 #include "ssm_params.h"
+#include "ssm_tc_params.h"
 
 namespace {
 
@@ -134,6 +137,150 @@ int launch_seq(const ssm::Params& p, int input_dtype, int dim, int dstate, void*
   return launch(fn, static_cast<int64_t>(p.units) * p.H, threads, &p, stream);
 }
 
+// ---------------------------------------------------------------------------
+// prompts on the tensor cores
+// ---------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_sms[kMaxDevices];
+bool g_tc_ready[kMaxDevices][4];
+
+int device_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (*dev < 0 || *dev >= kMaxDevices) return fail(RSM_ECUDA, "device ordinal %d out of range", *dev);
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_sms[*dev] == 0) {
+    e = cudaDeviceGetAttribute(&g_sms[*dev], cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) return fail(RSM_ECUDA, "device query failed: %s", cudaGetErrorString(e));
+  }
+  *sms = g_sms[*dev];
+  return RSM_OK;
+}
+
+using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+TensorMapEncodeFn tensor_map_encoder() {
+  static const TensorMapEncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<TensorMapEncodeFn>(nullptr);
+    return reinterpret_cast<TensorMapEncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A [tokens, cols] bf16 tensor in boxes of 128 rows x 64 columns, 128-byte swizzle.
+int token_map(CUtensorMap* map, const void* base, int64_t cols, int64_t tokens, int64_t stride, const char* name) {
+  const TensorMapEncodeFn encode = tensor_map_encoder();
+  if (encode == nullptr) return fail(RSM_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(tokens == 1 ? cols : stride) * 2u};
+  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(ssm::kChunk)}, ones[2] = {1u, 1u};
+  const CUresult cr = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2u, const_cast<void*>(base), dims, strides, box, ones,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS) return fail(RSM_ECUDA, "cuTensorMapEncodeTiled failed for %s (%d)", name, static_cast<int>(cr));
+  return RSM_OK;
+}
+
+// Tensor-map rows start on 16 bytes, output rows on 32 (their stores' width).
+bool rows_aligned(const void* base, int64_t stride, int64_t cols, int64_t tokens, int bytes) {
+  return reinterpret_cast<uintptr_t>(base) % bytes == 0 &&
+         (tokens == 1 || (stride >= cols && stride < (int64_t{1} << 38) && stride * 2 % bytes == 0));
+}
+
+// bf16 prompts with 64 x 128 states whose rows the tensor maps can address;
+// the rest runs on the sequential kernel.
+bool uses_tensor_cores(const rsm_ssm_prefill_args* a) {
+  return a->input_dtype == RSM_BF16 && a->dim == ssm::kDim && a->dstate == ssm::kState && a->tokens > 0 &&
+         a->tokens < 0x7FFFFF00LL && static_cast<int64_t>(a->num_heads) * ssm::kState <= 0x7FFFFFFFLL;
+}
+bool tensor_maps_fit(const rsm_ssm_prefill_args* a) {
+  const int64_t xc = static_cast<int64_t>(a->num_heads) * a->dim, bc = static_cast<int64_t>(a->num_groups) * a->dstate;
+  return rows_aligned(a->x, a->x_stride, xc, a->tokens, 16) && rows_aligned(a->B, a->B_stride, bc, a->tokens, 16) &&
+         rows_aligned(a->C, a->C_stride, bc, a->tokens, 16) && rows_aligned(a->out, a->out_stride, xc, a->tokens, 32);
+}
+
+struct PrefillPlan {
+  int heads;       // of a CTA
+  int pairs;       // CTAs' head groups in all
+  int64_t seg;     // tokens of a segment
+  int64_t segs;    // segments at most; 0: nothing is split
+};
+
+// Segment states and decays, the states first.
+int64_t workspace_bytes(const PrefillPlan& pl, int H) {
+  return pl.segs * H * (ssm::kDim * ssm::kState + 1) * 4;
+}
+
+PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
+  PrefillPlan pl;
+  pl.heads = a->num_heads / a->num_groups % 2 == 0 ? 2 : 1;
+  pl.pairs = a->num_heads / pl.heads;
+  pl.seg = int64_t{1} << 40;
+  pl.segs = 0;
+  (void)sms;
+  return pl;
+}
+
+int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream) {
+  int dev = 0, sms = 0;
+  int rc = device_sms(&dev, &sms);
+  if (rc != RSM_OK) return rc;
+  const PrefillPlan pl = plan_prefill(a, sms);
+  ssm::TcParams tp{};
+  rc = token_map(&tp.x_map, a->x, static_cast<int64_t>(a->num_heads) * ssm::kDim, a->tokens, a->x_stride, "x");
+  if (rc == RSM_OK)
+    rc = token_map(&tp.B_map, a->B, static_cast<int64_t>(a->num_groups) * ssm::kState, a->tokens, a->B_stride, "B");
+  if (rc == RSM_OK)
+    rc = token_map(&tp.C_map, a->C, static_cast<int64_t>(a->num_groups) * ssm::kState, a->tokens, a->C_stride, "C");
+  if (rc != RSM_OK) return rc;
+  tp.p = p;
+  tp.seg = pl.seg;
+  tp.pairs = pl.pairs;
+  int64_t units = static_cast<int64_t>(a->num_seqs) * pl.pairs;
+  if (pl.segs > 0) {
+    const int64_t need_bytes = workspace_bytes(pl, a->num_heads);
+    if (a->workspace == nullptr || a->workspace_bytes < need_bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0)
+      return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(need_bytes));
+    tp.seg_state = static_cast<float*>(a->workspace);
+    tp.seg_decay = tp.seg_state + pl.segs * a->num_heads * (ssm::kDim * ssm::kState);
+    units = pl.segs * pl.pairs;
+  }
+  // the state's terms keep 16 bits where the state that is kept has more than bf16's 8
+  const bool lo = a->final_slots != nullptr && a->state_dtype != RSM_BF16;
+  const void* fn = ssm::tc_kernel(pl.heads, lo);
+  const int ki = (pl.heads - 1) * 2 + (lo ? 1 : 0);
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_tc_ready[dev][ki]) {
+      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ssm::kTcSmem));
+      if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      g_tc_ready[dev][ki] = true;
+    }
+  }
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, sms));
+  auto run = [&](bool states_only) {
+    tp.states_only = states_only ? 1 : 0;
+    void* kargs[] = {&tp};
+    return cudaLaunchKernel(fn, dim3(grid), dim3(ssm::kTcThreads), kargs, ssm::kTcSmem, static_cast<cudaStream_t>(stream));
+  };
+  if (pl.segs > 0) {
+    cudaError_t e = run(true);
+    if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+    rc = launch(ssm::join_kernel(), static_cast<int64_t>(a->num_seqs) * a->num_heads, 256, &tp, stream);
+    if (rc != RSM_OK) return rc;
+  }
+  const cudaError_t e = run(false);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+  return done();
+}
+
 }  // namespace
 
 extern "C" {
@@ -169,14 +316,22 @@ int rsm_ssm_prefill(const rsm_ssm_prefill_args* a, void* stream) {
   p.pad = a->pad_slot_id;
   p.mode = ssm::kPrefill;
   p.state_dtype = a->state_dtype;
+  if (uses_tensor_cores(a) && tensor_maps_fit(a)) return launch_tc(a, p, stream);
   return launch_seq(p, a->input_dtype, a->dim, a->dstate, stream);
 }
 
 int64_t rsm_ssm_prefill_workspace(const rsm_ssm_prefill_args* a) {
-  const int rc = validate(a, false);
+  int rc = validate(a, false);
   if (rc != RSM_OK) return rc;
+  int64_t bytes = 0;
+  if (a->num_seqs > 0 && uses_tensor_cores(a)) {
+    int dev = 0, sms = 0;
+    rc = device_sms(&dev, &sms);
+    if (rc != RSM_OK) return rc;
+    bytes = workspace_bytes(plan_prefill(a, sms), a->num_heads);
+  }
   done();
-  return 0;
+  return bytes;
 }
 
 int rsm_ssm_step(const rsm_ssm_step_args* a, void* stream) {

@@ -1,0 +1,782 @@
+// ssm_tc_kernel.cuh -- prompts on the tensor cores: the chunked form of linear
+// attention with a decay for each head (bf16 inputs, 64 x 128 states).
+//
+// With a_t = dt_t A, a chunk of 128 tokens that starts from state S gives
+//   y_i = e^{a_0+..+a_i} S C_i + sum_{j<=i} (C_i . B_j) e^{a_{j+1}+..+a_i} dt_j x_j,
+//   S  <- e^{a_0+..+a_127} S + sum_j w_j x_j (x) B_j,    w_j = e^{a_{j+1}+..+a_127} dt_j,
+// four matrix products, all tcgen05.mma with M = 128:
+//   G  = C B^T           [i, j]       once for the CTA's heads, which share B and C
+//   Y1 = C S^T           [i, (h, d)]
+//   Y2 = P X             [i, d]       P = G o decay o dt, masked, in tensor memory as bf16
+//   U  = B^T (w X)       [n, (h, d)]  w X as bf16 hi + lo (16 bits), or hi alone for bf16 states
+// and y = e^{..} Y1 + Y2.  The skip term D x is a D on P's diagonal.
+//
+// Decays are products of factors that are all at most 1: a chunk is four blocks of
+// 32 tokens, and a pair (i, j) of blocks k > b decays by e^{sum over i's block up
+// to i} e^{blocks between} e^{rest of j's block}; only pairs of one block take an
+// exponential of their own.  Sums run inside a block, so their rounding does
+// not grow with the chunk, and nothing overflows or is divided.
+//
+// One persistent CTA per SM takes units (sequence, segment, two heads of one
+// group; one head where a group has an odd number), all chunks of a unit in order:
+//   warp 0      loads C, B (two stages) and x (one) with tensor-map copies
+//   warp 1      issues the MMAs; warps 2, 3 stage dt, a head each
+//   warps 4-7   P: a thread holds row i; G from tensor memory, P back into it
+//   warps 8-11  w X: a thread holds token t's row; x becomes hi in place
+//   warps 12-19 four a head: y out of Y1 and Y2; the state in registers as
+//               fp32, a thread per dstate column, and its bf16 copy for Y1
+// A sequence's last chunk may be partial: dt counts as 0 there, and the rows of
+// x and B past its end, which are a neighbour's or nobody's, are cleared
+// before an MMA multiplies them by 0.
+//
+// Every wait is bounded; one that runs out flags RSM_STATUS_WAIT_TIMEOUT, and
+// all roles leave, drain the copies in flight and free the tensor memory.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "rsm_formats.cuh"
+#include "rsm_ptx.cuh"
+#include "rsm_tc.cuh"
+#include "ssm_seq_kernel.cuh"
+#include "ssm_tc_params.h"
+
+namespace ssm {
+
+using rsm::fence_proxy_async_smem;
+using rsm::mbar_arrive;
+using rsm::mbar_init;
+using rsm::tc_commit;
+using rsm::tc_fence_after;
+using rsm::tc_fence_before;
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T; A: 128 lanes, two bf16 of K to a column.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor: K-major operand, 128-byte swizzle, groups of 8
+// rows 1024 bytes apart; 16 elements of K are 32 bytes inside the swizzle atom.
+__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// 16 columns of this thread's lane, as they are.  Whole warp.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 32 bytes of a row, streaming past L1
+__device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lds(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// the units of this CTA, walked alike by every role
+// ---------------------------------------------------------------------------
+struct Unit {
+  int64_t t0;   // first token
+  int len;      // tokens
+  int seq, seg, group;  // sequence, segment among all sequences', pair of heads
+  bool last;            // last segment of the sequence
+  bool split;           // its state comes from the segment states
+};
+
+struct Walk {
+  const TcParams& tp;
+  int64_t u;          // next unit
+  int seq = 0;        // sequence under the cursor
+  int64_t base = 0;   // segments before it
+  int64_t t0 = 0, len = 0, nseg = 0;
+  bool flagger;       // the one thread of the CTA that reports
+
+  __device__ Walk(const TcParams& tp_, bool flagger_) : tp(tp_), u(blockIdx.x), flagger(flagger_) { look(); }
+
+  __device__ void look() {
+    if (seq >= tp.p.units) return;
+    t0 = __ldg(tp.p.cu_seqlens + seq);
+    const int64_t t1 = __ldg(tp.p.cu_seqlens + seq + 1);
+    len = t1 - t0;
+    nseg = len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
+    if (t0 < 0 || t1 < t0 || t1 > tp.p.tokens) {
+      if (flagger) flag(tp.p.status, RSM_STATUS_BAD_SEQUENCE);
+      len = 0;
+      nseg = 0;  // no unit at all
+    }
+  }
+  __device__ bool next(Unit& w) {
+    for (;;) {
+      const int64_t sg = u / tp.pairs;
+      while (seq < tp.p.units && sg >= base + nseg) {
+        base += nseg;
+        ++seq;
+        look();
+      }
+      if (seq >= tp.p.units) return false;
+      const int64_t s = sg - base;
+      w.group = static_cast<int>(u - sg * tp.pairs);
+      u += gridDim.x;
+      w.last = s == nseg - 1;
+      w.split = nseg > 1;
+      if (tp.states_only && w.last) continue;  // nothing follows its state
+      w.seq = seq;
+      w.seg = static_cast<int>(sg);
+      w.t0 = t0 + s * tp.seg;
+      w.len = static_cast<int>(min(tp.seg, len - s * tp.seg));
+      return true;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// decays of a chunk's tokens, in units of log2
+// ---------------------------------------------------------------------------
+struct Scan {
+  float dt;     // this thread's token (block `warp`, place `lane`)
+  float upto;   // its block's sum up to and with it
+  float after;  // its block's sum after it
+  float t[4];   // the blocks' sums
+};
+
+__device__ __forceinline__ Scan scan_chunk(uint32_t dt_addr, float A2, int block, int lane) {
+  Scan s;
+  float a_own = 0.0f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float d = lds(dt_addr + static_cast<uint32_t>(b * 32 + lane) * 4u);
+    const float a = d * A2;
+    float t = a;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    s.t[b] = t;
+    if (b == block) {
+      s.dt = d;
+      a_own = a;
+    }
+  }
+  float up = a_own, down = a_own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_up_sync(0xFFFFFFFFu, up, o);
+    const float y = __shfl_down_sync(0xFFFFFFFFu, down, o);
+    if (lane >= o) up += x;
+    if (lane + o < 32) down += y;
+  }
+  s.upto = up;
+  down = __shfl_down_sync(0xFFFFFFFFu, down, 1);
+  s.after = lane == 31 ? 0.0f : down;
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+struct Cta {
+  const TcParams& tp;
+  unsigned char* smem;
+  uint32_t base;
+  uint32_t tmem;
+  int warp, lane;
+  volatile int* abort_flag;
+
+  __device__ uint32_t bar(uint32_t b) const { return base + kOffBar + 8u * b; }
+  // The phase of `parity` of a barrier has completed; false when the wait ran out or another role gave up.
+  __device__ bool wait(uint32_t b, uint32_t parity) const {
+    if (!rsm::mbar_wait(bar(b), parity & 1u, kTcTimeoutNs)) {
+      *abort_flag = 1;
+      flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
+      return false;
+    }
+    return *abort_flag == 0;
+  }
+  __device__ bool wait_warp(uint32_t b, uint32_t parity) const {
+    return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
+  }
+  __device__ void arrive_warp(uint32_t b) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  }
+};
+
+template <int NH>
+__device__ __forceinline__ void run_loader(const Cta& c) {
+  const TcParams& tp = c.tp;
+  Walk walk(tp, true);
+  Unit w;
+  uint32_t j = 0, n_bc = 0, n_x = 0;  // chunk; copies issued so far
+  const int per_group = tp.p.H / tp.p.G;
+  bool ok = true;
+  while (ok && walk.next(w)) {
+    const int h0 = w.group * NH, g = h0 / per_group;
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
+      const uint32_t st = j & 1u;
+      const int row = static_cast<int>(w.t0 + c0);
+      if (j >= 2 && !(ok = c.wait(kEmptyBC + st, (j >> 1) - 1u))) break;
+      const uint32_t bc = c.bar(kFullBC + st);
+      mbar_arrive_expect(bc, tp.states_only ? 2 * kTile : 4 * kTile);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!tp.states_only)
+          tma_load_2d(c.base + kOffC + (2 * st + half) * kTile, &tp.C_map, g * kState + 64 * half, row, bc);
+        tma_load_2d(c.base + kOffB + (2 * st + half) * kTile, &tp.B_map, g * kState + 64 * half, row, bc);
+      }
+      ++n_bc;
+      if (j >= 1 && !(ok = c.wait(kEmptyX, j - 1u))) break;
+      const uint32_t xb = c.bar(kFullX);
+      mbar_arrive_expect(xb, NH * kTile);
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+        tma_load_2d(c.base + kOffX + h * kTile, &tp.x_map, (h0 + h) * kDim, row, xb);
+      ++n_x;
+    }
+  }
+  // No copy may land after the CTA has gone: on the way out of a failed wait,
+  // wait (with the same limit) for what was issued.  Otherwise every copy has been consumed.
+  if (!ok) {
+    for (uint32_t k = n_bc >= 2 ? n_bc - 2 : 0; k < n_bc; ++k)
+      (void)rsm::mbar_wait(c.bar(kFullBC + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
+    if (n_x >= 1) (void)rsm::mbar_wait(c.bar(kFullX), (n_x - 1u) & 1u, kTcTimeoutNs);
+  }
+}
+
+template <int NH>
+__device__ __forceinline__ void run_dt(const Cta& c, int h) {
+  const TcParams& tp = c.tp;
+  Walk walk(tp, false);
+  Unit w;
+  uint32_t j = 0;
+  while (walk.next(w)) {
+    const float* dt = tp.p.dt + w.t0 * tp.p.dt_ts + (w.group * NH + h);
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
+      float v[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int t = c0 + 32 * b + c.lane;
+        v[b] = t < w.len ? __ldg(dt + static_cast<int64_t>(t) * tp.p.dt_ts) : 0.0f;
+      }
+      const uint32_t st = j & 1u;
+      if (j >= 2 && !c.wait_warp(kEmptyDt + st, (j >> 1) - 1u)) return;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        sts(c.base + kOffDt + ((st * 2 + h) * kChunk + 32 * b + c.lane) * 4u, v[b]);
+      c.arrive_warp(kFullDt + st);
+    }
+  }
+}
+
+template <int NH, bool LO>
+__device__ __forceinline__ void run_mma(const Cta& c) {
+  const TcParams& tp = c.tp;
+  Walk walk(tp, false);
+  Unit w;
+  uint32_t j = 0;
+  constexpr uint32_t kIdG = rsm::idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t kIdY1 = rsm::idesc_bf16_f32(128, 64 * NH, false, true);
+  constexpr uint32_t kIdPx = rsm::idesc_bf16_f32(128, 64, false, true);
+  constexpr uint32_t kIdU = rsm::idesc_bf16_f32(128, 64 * NH, true, true);
+  const uint32_t tm = c.tmem;
+
+  auto issue_G = [&](uint32_t jj) {
+    const uint32_t st = jj & 1u;
+    const uint64_t a = smem_desc_k_sw128(c.base + kOffC + 2 * st * kTile);
+    const uint64_t b = smem_desc_k_sw128(c.base + kOffB + 2 * st * kTile);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
+      const uint64_t o = static_cast<uint64_t>((k >> 2) * (kTile / 16) + (k & 3) * 2);
+      rsm::tc_mma_bf16(tm + kColG, a + o, b + o, kIdG, k > 0);
+    }
+    tc_commit(c.bar(kGFull));
+  };
+
+  while (walk.next(w)) {
+    const int chunks = (w.len + kChunk - 1) / kChunk;
+    for (int ci = 0; ci < chunks; ++ci, ++j) {
+      const uint32_t st = j & 1u;
+      if (!tp.states_only) {
+        if (ci == 0) {
+          if (!c.wait(kFullBC + st, j >> 1)) return;
+          // the last chunk's P has been read out of G: its P barriers were waited for below
+          tc_fence_after();
+          issue_G(j);
+        }
+        // Y1 = C S^T
+        if (!c.wait(kSFull, j)) return;
+        tc_fence_after();
+        {
+          const uint64_t a = smem_desc_k_sw128(c.base + kOffC + 2 * st * kTile);
+          const uint64_t b = rsm::smem_desc_mn_sw128(c.base + kOffS, kTile, 1024u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            rsm::tc_mma_bf16(tm + kColV, a + static_cast<uint64_t>((k >> 2) * (kTile / 16) + (k & 3) * 2),
+                             b + static_cast<uint64_t>(k * (2048 / 16)), kIdY1, k > 0);
+          tc_commit(c.bar(kY1Full));
+        }
+        // Y2 = P X
+        if (!c.wait(kFullX, j) || !c.wait(kClean, j)) return;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (!c.wait(kPFull + h, j)) return;
+          if (j >= 1 && !c.wait(kY2Empty + h, j - 1u)) return;
+          tc_fence_after();
+          const uint64_t b = rsm::smem_desc_mn_sw128(c.base + kOffX + h * kTile, kTile, 1024u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_bf16_ts(tm + kColY2 + 64 * h, tm + kColP + 64 * h + 8 * k, b + static_cast<uint64_t>(k * (2048 / 16)),
+                           kIdPx, k > 0);
+          tc_commit(c.bar(kPxDone + h));
+        }
+        // the next chunk's G while this one's w X is made
+        if (ci + 1 < chunks) {
+          if (!c.wait(kFullBC + (st ^ 1u), (j + 1u) >> 1)) return;
+          tc_fence_after();
+          issue_G(j + 1);
+        }
+      } else if (!c.wait(kFullBC + st, j >> 1)) {
+        return;
+      }
+      // U = B^T (w X), where Y1 was
+      if (!c.wait(kWFull, j)) return;
+      if (tp.states_only) {
+        if (j >= 1 && !c.wait(kVRead, j - 1u)) return;
+      } else if (!c.wait(kVRead, j)) {
+        return;
+      }
+      tc_fence_after();
+      const uint64_t a = rsm::smem_desc_mn_sw128(c.base + kOffB + 2 * st * kTile, kTile, 1024u);
+      const uint64_t hi = rsm::smem_desc_mn_sw128(c.base + kOffX, kTile, 1024u);
+      const uint64_t lo = rsm::smem_desc_mn_sw128(c.base + kOffLo, kTile, 1024u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t o = static_cast<uint64_t>(k * (2048 / 16));
+        rsm::tc_mma_bf16(tm + kColV, a + o, hi + o, kIdU, k > 0);
+        if constexpr (LO) rsm::tc_mma_bf16(tm + kColV, a + o, lo + o, kIdU, 1u);
+      }
+      tc_commit(c.bar(kUFull));
+      tc_commit(c.bar(kEmptyBC + st));
+      tc_commit(c.bar(kEmptyX));
+    }
+  }
+}
+
+// P = G o decay o dt (+ D on the diagonal), a thread per row.
+template <int NH>
+__device__ __forceinline__ void run_p(const Cta& c) {
+  const TcParams& tp = c.tp;
+  if (tp.states_only) return;
+  const int k = c.warp & 3, lane = c.lane;
+  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
+  // the blocks above the diagonal are zero for good
+  {
+    uint32_t zero[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero[i] = 0u;
+    for (int h = 0; h < NH; ++h)
+      for (int b = k + 1; b < 4; ++b) tmem_st16(trow + kColP + 64 * h + 16 * b, zero);
+    rsm::tmem_st_wait();
+  }
+  Walk walk(tp, false);
+  Unit w;
+  uint32_t j = 0, vs = 0;
+  while (walk.next(w)) {
+    float A2[NH], skip[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      A2[h] = __ldg(tp.p.A + w.group * NH + h) * 1.4426950408889634f;
+      skip[h] = tp.p.D != nullptr ? __ldg(tp.p.D + w.group * NH + h) : 0.0f;
+    }
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
+      const uint32_t st = j & 1u;
+      if (!c.wait_warp(kFullDt + st, j >> 1)) return;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const uint32_t dta = c.base + kOffDt + (st * 2 + h) * (kChunk * 4u);
+        const uint32_t va = c.base + kOffV + (NH == 2 ? h : j & 1u) * (96 * 4u);
+        const Scan s = scan_chunk(dta, A2[h], k, lane);
+        if (k < 3) sts(va + static_cast<uint32_t>(32 * k + lane) * 4u, s.dt * exp2_approx(s.after));
+        // the four warps' v; a buffer is written again only after a sync in between
+        c.arrive_warp(kVSync);
+        if (!c.wait_warp(kVSync, vs++)) return;
+        if (h == 0 && !c.wait_warp(kGFull, j)) return;
+        if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return;  // the last P has been multiplied
+        tc_fence_after();
+        const uint32_t tp_row = trow + kColP + 64 * h;
+        float between = s.upto;  // row i back to the end of block b
+#pragma unroll
+        for (int b = 2; b >= 0; --b) {
+          if (b >= k) continue;
+          const float f = exp2_approx(between);
+          between += s.t[b];
+          float g[32];
+          rsm::tmem_ld32(trow + kColG + 32 * b, g);
+          uint32_t r[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 v = lds4(va + static_cast<uint32_t>(32 * b + 4 * q) * 4u);
+            const float2 ff = make_float2(f, f);
+            const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y)), ff);
+            const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w)), ff);
+            r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
+            r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
+          }
+          tmem_st16(tp_row + 16 * b, r);
+        }
+        {
+          float g[32];
+          rsm::tmem_ld32(trow + kColG + 32 * k, g);
+          uint32_t r[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 d4 = lds4(dta + static_cast<uint32_t>(32 * k + 4 * q) * 4u);
+            const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
+            float e[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int jj = 4 * q + m;
+              const float pj = __shfl_sync(0xFFFFFFFFu, s.upto, jj);
+              const float v = g[jj] * (exp2_approx(s.upto - pj) * dd[m]);
+              e[m] = jj < lane ? v : jj == lane ? fmaf(g[jj], dd[m], skip[h]) : 0.0f;
+            }
+            r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
+            r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
+          }
+          tmem_st16(tp_row + 16 * k, r);
+        }
+        rsm::tmem_st_wait();
+        tc_fence_before();
+        c.arrive_warp(kPFull + h);
+      }
+      c.arrive_warp(kEmptyDt + st);
+    }
+  }
+}
+
+// w X, a thread per token row; hi over x, lo beside it.
+template <int NH, bool LO>
+__device__ __forceinline__ void run_w(const Cta& c) {
+  const TcParams& tp = c.tp;
+  Walk walk(tp, false);
+  Unit w;
+  uint32_t j = 0;
+  const int k = c.warp & 3, lane = c.lane, t = 32 * k + lane;
+  const uint32_t row = static_cast<uint32_t>(t) * 128u;
+  const uint32_t swz = static_cast<uint32_t>(t & 7) << 4;
+  while (walk.next(w)) {
+    float A2[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) A2[h] = __ldg(tp.p.A + w.group * NH + h) * 1.4426950408889634f;
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
+      const uint32_t st = j & 1u;
+      const bool partial = w.len - c0 < kChunk, live = c0 + t < w.len;
+      float wt[NH];
+      if (!c.wait_warp(kFullDt + st, j >> 1)) return;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), A2[h], k, lane);
+        float rest = s.after;
+#pragma unroll
+        for (int b = 1; b < 4; ++b) rest += b > k ? s.t[b] : 0.0f;
+        wt[h] = s.dt * exp2_approx(rest);
+      }
+      c.arrive_warp(kEmptyDt + st);
+      if (partial) {
+        if (!c.wait_warp(kFullX, j) || !c.wait_warp(kFullBC + st, j >> 1)) return;
+        if (!live) {
+#pragma unroll
+          for (uint32_t q = 0; q < 8; ++q) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) sts128(c.base + kOffX + h * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
+            sts128(c.base + kOffB + (2 * st) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
+            sts128(c.base + kOffB + (2 * st + 1) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      if (!tp.states_only) c.arrive_warp(kClean);
+      if (!c.wait_warp(kFullX, j)) return;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        if (!tp.states_only && !c.wait_warp(kPxDone + h, j)) return;
+        const uint32_t xa = c.base + kOffX + h * kTile + row, la = c.base + kOffLo + h * kTile + row;
+        const float2 w2 = make_float2(wt[h], wt[h]);
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) {
+          const uint32_t at = (q << 4) ^ swz;
+          const uint4 v = rsm::lds128(xa + at);
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t hw[4], lw[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float2 u = __fmul2_rn(make_float2(rsm::bf16lo(in[m]), rsm::bf16hi(in[m])), w2);
+            hw[m] = rsm::pack_bf16x2(u.x, u.y);
+            if constexpr (LO) {
+              // u - hi is exact; rounded to bf16, hi + lo is within 2^-17 of u
+              const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
+              lw[m] = rsm::pack_bf16x2(l.x, l.y);
+            }
+          }
+          if (!live) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) hw[m] = lw[m] = 0u;
+          }
+          sts128(xa + at, hw[0], hw[1], hw[2], hw[3]);
+          if constexpr (LO) sts128(la + at, lw[0], lw[1], lw[2], lw[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      c.arrive_warp(kWFull);
+    }
+  }
+}
+
+// One head's outputs and state.
+template <int NH>
+__device__ __forceinline__ void run_head(const Cta& c, int h) {
+  const TcParams& tp = c.tp;
+  const Params& p = tp.p;
+  Walk walk(tp, false);
+  Unit w;
+  uint32_t j = 0;
+  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;  // output row, and dstate column
+  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
+  const uint32_t srow = c.base + kOffS + h * kTile + static_cast<uint32_t>(r) * 128u;
+  const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
+  while (walk.next(w)) {
+    const int head = w.group * NH + h;
+    const float A2 = __ldg(p.A + head) * 1.4426950408889634f;
+    const int64_t tile = static_cast<int64_t>(head) * (kDim * kState) + r;
+    float S[kDim];
+    const bool say = w.group == 0 && h == 0 && r == 0 && !tp.states_only;
+    if (w.split && !tp.states_only) {
+      const float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
+#pragma unroll
+      for (int d = 0; d < kDim; ++d) S[d] = at[d * kState];
+    } else {
+      const int src = tp.states_only ? -1 : slot_of(p, p.src, w.seq, say);
+#pragma unroll
+      for (int d = 0; d < kDim; ++d)
+        S[d] = src >= 0 ? load_state(p.state, src * p.state_ss + tile + d * kState, p.state_dtype) : 0.0f;
+    }
+    float decay = 0.0f;  // of the segment, log2
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
+      const uint32_t st = j & 1u;
+      if (!tp.states_only) {
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q)
+          sts128(srow + ((q << 4) ^ swz), rsm::pack_bf16x2(S[8 * q], S[8 * q + 1]),
+                 rsm::pack_bf16x2(S[8 * q + 2], S[8 * q + 3]), rsm::pack_bf16x2(S[8 * q + 4], S[8 * q + 5]),
+                 rsm::pack_bf16x2(S[8 * q + 6], S[8 * q + 7]));
+        fence_proxy_async_smem();
+        tc_fence_before();
+        c.arrive_warp(kSFull);
+      }
+      if (!c.wait_warp(kFullDt + st, j >> 1)) return;
+      const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), A2, k, lane);
+      c.arrive_warp(kEmptyDt + st);
+      const float total = (s.t[0] + s.t[1]) + (s.t[2] + s.t[3]);
+      decay += total;
+      if (!tp.states_only) {
+        float up = s.upto;
+#pragma unroll
+        for (int b = 0; b < 3; ++b) up += b < k ? s.t[b] : 0.0f;
+        const float e = exp2_approx(up);
+        if (!c.wait_warp(kY1Full, j) || !c.wait_warp(kPxDone + h, j)) return;
+        tc_fence_after();
+        unsigned char* out = static_cast<unsigned char*>(p.out) + ((w.t0 + c0 + r) * p.out_ts + head * kDim) * 2;
+        const bool live = c0 + r < w.len;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y1[16], y2[16];
+          rsm::tmem_ld16(trow + kColV + 64 * h + 16 * q, y1);
+          rsm::tmem_ld16(trow + kColY2 + 64 * h + 16 * q, y2);
+          uint32_t v[8];
+#pragma unroll
+          for (int m = 0; m < 8; ++m)
+            v[m] = rsm::pack_bf16x2(fmaf(e, y1[2 * m], y2[2 * m]), fmaf(e, y1[2 * m + 1], y2[2 * m + 1]));
+          if (live) stg256(out + 32 * q, v);
+        }
+        tc_fence_before();
+        c.arrive_warp(kVRead);
+        if (c.lane == 0) mbar_arrive(c.bar(kY2Empty + h));
+      }
+      if (!c.wait_warp(kUFull, j)) return;
+      tc_fence_after();
+      const float a = exp2_approx(total);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float u[16];
+        rsm::tmem_ld16(trow + kColV + 64 * h + 16 * q, u);
+#pragma unroll
+        for (int m = 0; m < 16; ++m) S[16 * q + m] = fmaf(a, S[16 * q + m], u[m]);
+      }
+      if (tp.states_only) {
+        tc_fence_before();
+        c.arrive_warp(kVRead);
+      }
+    }
+    if (tp.states_only) {
+      float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
+#pragma unroll
+      for (int d = 0; d < kDim; ++d) at[d * kState] = S[d];
+      if (r == 0) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + head] = decay;
+    } else if (w.last) {
+      const int dst = slot_of(p, p.dst, w.seq, say);
+      if (dst >= 0) {
+#pragma unroll
+        for (int d = 0; d < kDim; ++d)
+          store_state(p.state, dst * p.state_ss + tile + d * kState, p.state_dtype, S[d]);
+      }
+    }
+  }
+}
+
+template <int NH, bool LO>
+__global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_constant__ TcParams tp) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = rsm::smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((base & 1023u) != 0u) {  // the swizzled tiles need it (never seen otherwise)
+    if (threadIdx.x == 0) flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
+    return;
+  }
+  if (warp == 1) {
+    rsm::tmem_alloc(base + kOffTmem, 512u);
+    rsm::tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    const uint32_t bars = base + kOffBar;
+    auto init = [&](uint32_t b, uint32_t n, int how_many = 1) {
+      for (int i = 0; i < how_many; ++i) mbar_init(bars + 8u * (b + i), n);
+    };
+    init(kFullBC, 1, 2);
+    init(kEmptyBC, 1, 2);
+    init(kFullX, 1);
+    init(kEmptyX, 1);
+    init(kFullDt, NH, 2);
+    init(kEmptyDt, (tp.states_only ? 4 : 8) + 4 * NH, 2);
+    init(kGFull, 1);
+    init(kPFull, 4, 2);
+    init(kPxDone, 1, 2);
+    init(kY2Empty, 4, 2);
+    init(kSFull, 4 * NH);
+    init(kY1Full, 1);
+    init(kVRead, 4 * NH);
+    init(kWFull, 4);
+    init(kClean, 4);
+    init(kUFull, 1);
+    init(kVSync, 4);
+    init(kExit, 1);
+    *reinterpret_cast<volatile int*>(smem + kOffAbort) = 0;
+    rsm::fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane,
+              reinterpret_cast<volatile int*>(smem + kOffAbort)};
+  if (warp == 0) {
+    if (lane == 0) run_loader<NH>(c);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      run_mma<NH, LO>(c);
+      // no MMA may be in flight when the tensor memory is freed, whichever way the role ended
+      tc_commit(c.bar(kExit));
+      (void)rsm::mbar_wait(c.bar(kExit), 0u, kTcTimeoutNs);
+    }
+  } else if (warp < 4) {
+    if (warp - 2 < NH) run_dt<NH>(c, warp - 2);
+  } else if (warp < 8) {
+    run_p<NH>(c);
+  } else if (warp < 12) {
+    run_w<NH, LO>(c);
+  } else if ((warp - 12) / 4 < NH) {
+    run_head<NH>(c, (warp - 12) / 4);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) rsm::tmem_dealloc(c.tmem, 512u);
+}
+
+// R = the sequence's initial state; for each of its segments: the segment
+// starts from R, and R = its decay R + its own state.  One CTA per (sequence,
+// head); the same elements belong to the same thread throughout.
+__global__ void __launch_bounds__(256) ssm_join_kernel(const __grid_constant__ TcParams tp) {
+  const Params& p = tp.p;
+  const int seq = static_cast<int>(blockIdx.x / static_cast<uint32_t>(p.H));
+  const int h = static_cast<int>(blockIdx.x % static_cast<uint32_t>(p.H));
+  auto segs_of = [&](int s) -> int64_t {
+    const int64_t a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
+    if (a < 0 || b < a || b > p.tokens) return 0;
+    return b - a <= tp.seg ? 1 : (b - a + tp.seg - 1) / tp.seg;
+  };
+  const int64_t n = segs_of(seq);
+  if (n <= 1) return;
+  int64_t sg = 0;  // segments before the sequence's
+  for (int s = 0; s < seq; ++s) sg += segs_of(s);
+  const int src = slot_of(p, p.src, seq, false);
+  constexpr int kPer = kDim * kState / 256;
+  float R[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    R[i] = src >= 0 ? load_state(p.state, src * p.state_ss + static_cast<int64_t>(h) * (kDim * kState) + threadIdx.x + 256 * i,
+                                 p.state_dtype)
+                    : 0.0f;
+  for (int64_t s = 0; s < n; ++s) {
+    float* at = tp.seg_state + ((sg + s) * p.H + h) * (kDim * kState) + threadIdx.x;
+    const float a = s + 1 < n ? exp2f(tp.seg_decay[(sg + s) * p.H + h]) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float own = s + 1 < n ? at[256 * i] : 0.0f;
+      at[256 * i] = R[i];
+      R[i] = fmaf(a, R[i], own);
+    }
+  }
+}
+
+}  // namespace ssm

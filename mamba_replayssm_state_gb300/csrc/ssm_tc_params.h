@@ -1,0 +1,58 @@
+// ssm_tc_params.h -- the tensor-core prompt kernel: its parameters, shared
+// memory and tensor memory plan.
+#pragma once
+#include <cuda.h>
+
+#include "ssm_params.h"
+
+namespace ssm {
+
+constexpr int kChunk = 128;  // tokens of a chunk: the MMAs' M, and the K of two of them
+constexpr int kDim = 64, kState = 128;
+constexpr int kTile = kChunk * 128;  // bytes of a [128 rows x 64 bf16] tile, 128-byte swizzled
+
+struct TcParams {
+  CUtensorMap x_map, B_map, C_map;  // [tokens, H * 64], [tokens, G * 128] bf16, boxes of 128 rows x 64 columns
+  Params p;
+  int64_t seg;         // tokens of a segment, a multiple of kChunk
+  float* seg_state;    // [segments, H, 64, 128]: states between segments (NULL when nothing is split)
+  float* seg_decay;    // [segments, H]
+  int32_t pairs;       // head groups of a CTA in all: H / NH
+  int32_t states_only; // the pass that makes the segments' own states
+};
+
+// shared memory, bytes: two stages of C and B, the heads' x (hi in place), lo,
+// the bf16 state, then the small things
+constexpr uint32_t kOffC = 0;
+constexpr uint32_t kOffB = kOffC + 4 * kTile;
+constexpr uint32_t kOffX = kOffB + 4 * kTile;
+constexpr uint32_t kOffLo = kOffX + 2 * kTile;
+constexpr uint32_t kOffS = kOffLo + 2 * kTile;
+constexpr uint32_t kOffDt = kOffS + 2 * kTile;          // [2 stages][2 heads][128] fp32
+constexpr uint32_t kOffV = kOffDt + 2 * 2 * kChunk * 4; // [2 heads][96] fp32
+constexpr uint32_t kOffBar = kOffV + 2 * 96 * 4;
+enum Bar : uint32_t {
+  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 5, kFullDt = 6, kEmptyDt = 8, kGFull = 10, kPFull = 11,
+  kPxDone = 13, kY2Empty = 15, kSFull = 17, kY1Full = 18, kVRead = 19, kWFull = 20, kClean = 21, kUFull = 22,
+  kVSync = 23, kExit = 24, kBars = 25
+};
+constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
+constexpr uint32_t kOffAbort = kOffTmem + 4;
+constexpr uint32_t kTcSmem = kOffAbort + 4;
+static_assert(kTcSmem <= 232448, "shared memory of one CTA");
+
+// tensor memory, columns: G = C B^T, the heads' P (bf16 pairs), P X, and one
+// region that holds C S^T and then the state update
+constexpr uint32_t kColG = 0, kColP = 128, kColY2 = 256, kColV = 384;
+
+constexpr int kTcThreads = 640;  // loader, MMA, two dt warps, then P, W and two head warpgroups
+constexpr uint64_t kTcTimeoutNs = 2000000000ull;
+
+// heads: 1 or 2 a CTA; lo: the state update keeps 16 bits of w x
+const void* tc_kernel(int heads, bool lo);
+
+// Between the two passes of a split call: the state every segment starts from.
+// Grid: (num_seqs * H), 256 threads.
+const void* join_kernel();
+
+}  // namespace ssm
