@@ -209,7 +209,7 @@ bool tensor_maps_fit(const rsm_ssm_prefill_args* a) {
 struct PrefillPlan {
   int heads;       // of a CTA
   int pairs;       // CTAs' head groups in all
-  int64_t seg;     // tokens of a segment
+  uint32_t seg;    // tokens of a segment
   int64_t segs;    // segments at most; 0: nothing is split
 };
 
@@ -222,7 +222,7 @@ PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
   PrefillPlan pl;
   pl.heads = a->num_heads / a->num_groups % 2 == 0 ? 2 : 1;
   pl.pairs = a->num_heads / pl.heads;
-  pl.seg = int64_t{1} << 40;
+  pl.seg = 0x7FFFFF80u;
   pl.segs = 0;
   (void)sms;
   return pl;
@@ -264,6 +264,8 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
       g_tc_ready[dev][ki] = true;
     }
   }
+  // (a unit's number and the next one's after it stay below 2^32)
+  if (units > 0x7FFFFFFFLL) return fail(RSM_EINVAL, "%lld units of work, more than 2^31-1", static_cast<long long>(units));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, sms));
   auto run = [&](bool states_only) {
     tp.states_only = states_only ? 1 : 0;

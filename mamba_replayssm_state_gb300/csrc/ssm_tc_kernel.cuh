@@ -61,21 +61,46 @@ __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes)
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T; A: 128 lanes, two bf16 of K to a column.
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
-// Shared-memory descriptor: K-major operand, 128-byte swizzle, groups of 8
-// rows 1024 bytes apart; 16 elements of K are 32 bytes inside the swizzle atom.
-__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory descriptors with the 128-byte swizzle, as (low, high) words:
+// the low word holds the start address and the first stride, both in 16 bytes,
+// so that moving along K adds to it alone.  K-major: groups of 8 rows 1024
+// bytes apart, 16 elements of K 32 bytes inside the swizzle atom.  MN-major:
+// 64 elements of M or N to an atom, atoms a tile apart along M or N and 1024
+// bytes (8 rows of K) along K.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) { return (saddr >> 4) | ((kTile >> 4) << 16); }
+
+// D[tmem] (+)= A * B^T, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+// The same with A in tensor memory: 128 lanes, two bf16 of K to a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
 }
 
 // 16 columns of this thread's lane, as they are.  Whole warp.
@@ -94,6 +119,8 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -122,19 +149,20 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // the units of this CTA, walked alike by every role
 // ---------------------------------------------------------------------------
 struct Unit {
-  int64_t t0;   // first token
-  int len;      // tokens
-  int seq, seg, group;  // sequence, segment among all sequences', pair of heads
+  int64_t t0;           // first token
+  int len;              // tokens
+  int seq, seg, group;  // sequence, segment among all sequences', heads' group
   bool last;            // last segment of the sequence
   bool split;           // its state comes from the segment states
 };
 
 struct Walk {
   const TcParams& tp;
-  int64_t u;          // next unit
+  uint32_t u;         // next unit
   int seq = 0;        // sequence under the cursor
-  int64_t base = 0;   // segments before it
-  int64_t t0 = 0, len = 0, nseg = 0;
+  uint32_t base = 0;  // segments before it
+  int64_t t0 = 0;
+  uint32_t len = 0, nseg = 0;
   bool flagger;       // the one thread of the CTA that reports
 
   __device__ Walk(const TcParams& tp_, bool flagger_) : tp(tp_), u(blockIdx.x), flagger(flagger_) { look(); }
@@ -143,32 +171,33 @@ struct Walk {
     if (seq >= tp.p.units) return;
     t0 = __ldg(tp.p.cu_seqlens + seq);
     const int64_t t1 = __ldg(tp.p.cu_seqlens + seq + 1);
-    len = t1 - t0;
-    nseg = len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
+    len = static_cast<uint32_t>(t1 - t0);
     if (t0 < 0 || t1 < t0 || t1 > tp.p.tokens) {
       if (flagger) flag(tp.p.status, RSM_STATUS_BAD_SEQUENCE);
       len = 0;
       nseg = 0;  // no unit at all
+    } else {
+      nseg = len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
     }
   }
   __device__ bool next(Unit& w) {
     for (;;) {
-      const int64_t sg = u / tp.pairs;
+      const uint32_t sg = u / static_cast<uint32_t>(tp.pairs);
       while (seq < tp.p.units && sg >= base + nseg) {
         base += nseg;
         ++seq;
         look();
       }
       if (seq >= tp.p.units) return false;
-      const int64_t s = sg - base;
-      w.group = static_cast<int>(u - sg * tp.pairs);
+      const uint32_t s = sg - base;
+      w.group = static_cast<int>(u - sg * static_cast<uint32_t>(tp.pairs));
       u += gridDim.x;
       w.last = s == nseg - 1;
       w.split = nseg > 1;
       if (tp.states_only && w.last) continue;  // nothing follows its state
       w.seq = seq;
       w.seg = static_cast<int>(sg);
-      w.t0 = t0 + s * tp.seg;
+      w.t0 = t0 + static_cast<int64_t>(s) * tp.seg;
       w.len = static_cast<int>(min(tp.seg, len - s * tp.seg));
       return true;
     }
@@ -225,14 +254,16 @@ struct Cta {
   volatile int* abort_flag;
 
   __device__ uint32_t bar(uint32_t b) const { return base + kOffBar + 8u * b; }
-  // The phase of `parity` of a barrier has completed; false when the wait ran out or another role gave up.
-  __device__ bool wait(uint32_t b, uint32_t parity) const {
-    if (!rsm::mbar_wait(bar(b), parity & 1u, kTcTimeoutNs)) {
-      *abort_flag = 1;
-      flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
-      return false;
+  // The phase of `parity` of a barrier has completed; false when the wait ran
+  // out or another role has given up.
+  __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
+    const uint32_t at = bar(b);
+    if (rsm::mbar_try_wait(at, parity & 1u)) return true;
+    const uint64_t t0 = rsm::global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (rsm::mbar_try_wait(at, parity & 1u)) return true;
+      if ((it & 255u) == 0u && (*abort_flag != 0 || rsm::global_timer_ns() - t0 > kTcTimeoutNs)) return false;
     }
-    return *abort_flag == 0;
   }
   __device__ bool wait_warp(uint32_t b, uint32_t parity) const {
     return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
@@ -244,48 +275,52 @@ struct Cta {
 };
 
 template <int NH>
-__device__ __forceinline__ void run_loader(const Cta& c) {
+__device__ __forceinline__ bool run_loader(const Cta& c) {
   const TcParams& tp = c.tp;
-  Walk walk(tp, true);
+  Walk walk(tp, c.lane == 0);
   Unit w;
   uint32_t j = 0, n_bc = 0, n_x = 0;  // chunk; copies issued so far
-  const int per_group = tp.p.H / tp.p.G;
+  const uint32_t per_group = static_cast<uint32_t>(tp.p.H / tp.p.G);
+  const bool one = elect_one();
   bool ok = true;
   while (ok && walk.next(w)) {
-    const int h0 = w.group * NH, g = h0 / per_group;
+    const int h0 = w.group * NH, g = static_cast<int>(static_cast<uint32_t>(h0) / per_group);
+#pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       const int row = static_cast<int>(w.t0 + c0);
-      if (j >= 2 && !(ok = c.wait(kEmptyBC + st, (j >> 1) - 1u))) break;
-      const uint32_t bc = c.bar(kFullBC + st);
-      mbar_arrive_expect(bc, tp.states_only ? 2 * kTile : 4 * kTile);
+      if (j >= 2 && !(ok = c.wait_warp(kEmptyBC + st, (j >> 1) - 1u))) break;
+      if (one) {
+        const uint32_t bc = c.bar(kFullBC + st);
+        mbar_arrive_expect(bc, tp.states_only ? 2 * kTile : 4 * kTile);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!tp.states_only)
-          tma_load_2d(c.base + kOffC + (2 * st + half) * kTile, &tp.C_map, g * kState + 64 * half, row, bc);
-        tma_load_2d(c.base + kOffB + (2 * st + half) * kTile, &tp.B_map, g * kState + 64 * half, row, bc);
+        for (int half = 0; half < 2; ++half) {
+          if (!tp.states_only)
+            tma_load_2d(c.base + kOffC + (2 * st + half) * kTile, &tp.C_map, g * kState + 64 * half, row, bc);
+          tma_load_2d(c.base + kOffB + (2 * st + half) * kTile, &tp.B_map, g * kState + 64 * half, row, bc);
+        }
       }
       ++n_bc;
-      if (j >= 1 && !(ok = c.wait(kEmptyX, j - 1u))) break;
-      const uint32_t xb = c.bar(kFullX);
-      mbar_arrive_expect(xb, NH * kTile);
+      if (j >= 1 && !(ok = c.wait_warp(kEmptyX, j - 1u))) break;
+      if (one) {
+        const uint32_t xb = c.bar(kFullX);
+        mbar_arrive_expect(xb, NH * kTile);
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
-        tma_load_2d(c.base + kOffX + h * kTile, &tp.x_map, (h0 + h) * kDim, row, xb);
+        for (int h = 0; h < NH; ++h)
+          tma_load_2d(c.base + kOffX + h * kTile, &tp.x_map, (h0 + h) * kDim, row, xb);
+      }
       ++n_x;
     }
   }
-  // No copy may land after the CTA has gone: on the way out of a failed wait,
-  // wait (with the same limit) for what was issued.  Otherwise every copy has been consumed.
-  if (!ok) {
-    for (uint32_t k = n_bc >= 2 ? n_bc - 2 : 0; k < n_bc; ++k)
-      (void)rsm::mbar_wait(c.bar(kFullBC + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
-    if (n_x >= 1) (void)rsm::mbar_wait(c.bar(kFullX), (n_x - 1u) & 1u, kTcTimeoutNs);
-  }
+  // no copy may land after the CTA has gone, whichever way the roles end
+  for (uint32_t k = n_bc >= 2 ? n_bc - 2 : 0; k < n_bc; ++k)
+    (void)rsm::mbar_wait(c.bar(kFullBC + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
+  if (n_x >= 1) (void)rsm::mbar_wait(c.bar(kFullX), (n_x - 1u) & 1u, kTcTimeoutNs);
+  return ok;
 }
 
 template <int NH>
-__device__ __forceinline__ void run_dt(const Cta& c, int h) {
+__device__ __forceinline__ bool run_dt(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   Walk walk(tp, false);
   Unit w;
@@ -300,17 +335,19 @@ __device__ __forceinline__ void run_dt(const Cta& c, int h) {
         v[b] = t < w.len ? __ldg(dt + static_cast<int64_t>(t) * tp.p.dt_ts) : 0.0f;
       }
       const uint32_t st = j & 1u;
-      if (j >= 2 && !c.wait_warp(kEmptyDt + st, (j >> 1) - 1u)) return;
+      if (j >= 2 && !c.wait_warp(kEmptyDt + st, (j >> 1) - 1u)) return false;
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         sts(c.base + kOffDt + ((st * 2 + h) * kChunk + 32 * b + c.lane) * 4u, v[b]);
       c.arrive_warp(kFullDt + st);
     }
   }
+  return true;
 }
 
+// The whole warp walks and waits, so that addresses stay uniform; one thread issues.
 template <int NH, bool LO>
-__device__ __forceinline__ void run_mma(const Cta& c) {
+__device__ __forceinline__ bool run_mma(const Cta& c) {
   const TcParams& tp = c.tp;
   Walk walk(tp, false);
   Unit w;
@@ -319,95 +356,97 @@ __device__ __forceinline__ void run_mma(const Cta& c) {
   constexpr uint32_t kIdY1 = rsm::idesc_bf16_f32(128, 64 * NH, false, true);
   constexpr uint32_t kIdPx = rsm::idesc_bf16_f32(128, 64, false, true);
   constexpr uint32_t kIdU = rsm::idesc_bf16_f32(128, 64 * NH, true, true);
+  constexpr uint32_t kStepMn = 2048 / 16;  // 16 rows of K
   const uint32_t tm = c.tmem;
+  const bool one = elect_one();
 
-  auto issue_G = [&](uint32_t jj) {
-    const uint32_t st = jj & 1u;
-    const uint64_t a = smem_desc_k_sw128(c.base + kOffC + 2 * st * kTile);
-    const uint64_t b = smem_desc_k_sw128(c.base + kOffB + 2 * st * kTile);
+  auto issue_G = [&](uint32_t st) {
+    tc_fence_after();
+    if (one) {
+      const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_k(c.base + kOffB + 2 * st * kTile);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
-      const uint64_t o = static_cast<uint64_t>((k >> 2) * (kTile / 16) + (k & 3) * 2);
-      rsm::tc_mma_bf16(tm + kColG, a + o, b + o, kIdG, k > 0);
+      for (uint32_t k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
+        const uint32_t o = (k >> 2) * (kTile / 16) + (k & 3) * 2;
+        mma_ss(tm + kColG, a + o, b + o, kIdG, k > 0);
+      }
+      tc_commit(c.bar(kGFull));
     }
-    tc_commit(c.bar(kGFull));
+    __syncwarp();
   };
 
   while (walk.next(w)) {
-    const int chunks = (w.len + kChunk - 1) / kChunk;
-    for (int ci = 0; ci < chunks; ++ci, ++j) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       if (!tp.states_only) {
-        if (ci == 0) {
-          if (!c.wait(kFullBC + st, j >> 1)) return;
-          // the last chunk's P has been read out of G: its P barriers were waited for below
-          tc_fence_after();
-          issue_G(j);
+        // (the last chunk's P has been read out of G: its P barriers were waited for below)
+        if (c0 == 0) {
+          if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
+          issue_G(st);
         }
         // Y1 = C S^T
-        if (!c.wait(kSFull, j)) return;
+        if (!c.wait_warp(kSFull, j)) return false;
         tc_fence_after();
-        {
-          const uint64_t a = smem_desc_k_sw128(c.base + kOffC + 2 * st * kTile);
-          const uint64_t b = rsm::smem_desc_mn_sw128(c.base + kOffS, kTile, 1024u);
+        if (one) {
+          const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_mn(c.base + kOffS);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            rsm::tc_mma_bf16(tm + kColV, a + static_cast<uint64_t>((k >> 2) * (kTile / 16) + (k & 3) * 2),
-                             b + static_cast<uint64_t>(k * (2048 / 16)), kIdY1, k > 0);
+          for (uint32_t k = 0; k < 8; ++k)
+            mma_ss(tm + kColV, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
           tc_commit(c.bar(kY1Full));
         }
+        __syncwarp();
         // Y2 = P X
-        if (!c.wait(kFullX, j) || !c.wait(kClean, j)) return;
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          if (!c.wait(kPFull + h, j)) return;
-          if (j >= 1 && !c.wait(kY2Empty + h, j - 1u)) return;
+        if (!c.wait_warp(kFullX, j) || !c.wait_warp(kClean, j)) return false;
+#pragma unroll 1
+        for (uint32_t h = 0; h < NH; ++h) {
+          if (!c.wait_warp(kPFull + h, j)) return false;
+          if (j >= 1 && !c.wait_warp(kY2Empty + h, j - 1u)) return false;
           tc_fence_after();
-          const uint64_t b = rsm::smem_desc_mn_sw128(c.base + kOffX + h * kTile, kTile, 1024u);
+          if (one) {
+            const uint32_t b = desc_mn(c.base + kOffX + h * kTile);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_bf16_ts(tm + kColY2 + 64 * h, tm + kColP + 64 * h + 8 * k, b + static_cast<uint64_t>(k * (2048 / 16)),
-                           kIdPx, k > 0);
-          tc_commit(c.bar(kPxDone + h));
+            for (uint32_t k = 0; k < 8; ++k)
+              mma_ts(tm + kColY2 + 64 * h, tm + kColP + 64 * h + 8 * k, b + k * kStepMn, kIdPx, k > 0);
+            tc_commit(c.bar(kPxDone + h));
+          }
+          __syncwarp();
         }
         // the next chunk's G while this one's w X is made
-        if (ci + 1 < chunks) {
-          if (!c.wait(kFullBC + (st ^ 1u), (j + 1u) >> 1)) return;
-          tc_fence_after();
-          issue_G(j + 1);
+        if (c0 + kChunk < w.len) {
+          if (!c.wait_warp(kFullBC + (st ^ 1u), (j + 1u) >> 1)) return false;
+          issue_G(st ^ 1u);
         }
-      } else if (!c.wait(kFullBC + st, j >> 1)) {
-        return;
+      } else if (!c.wait_warp(kFullBC + st, j >> 1)) {
+        return false;
       }
       // U = B^T (w X), where Y1 was
-      if (!c.wait(kWFull, j)) return;
-      if (tp.states_only) {
-        if (j >= 1 && !c.wait(kVRead, j - 1u)) return;
-      } else if (!c.wait(kVRead, j)) {
-        return;
-      }
+      if (!c.wait_warp(kWFull, j)) return false;
+      if (!tp.states_only || j >= 1)
+        if (!c.wait_warp(kVRead, tp.states_only ? j - 1u : j)) return false;
       tc_fence_after();
-      const uint64_t a = rsm::smem_desc_mn_sw128(c.base + kOffB + 2 * st * kTile, kTile, 1024u);
-      const uint64_t hi = rsm::smem_desc_mn_sw128(c.base + kOffX, kTile, 1024u);
-      const uint64_t lo = rsm::smem_desc_mn_sw128(c.base + kOffLo, kTile, 1024u);
+      if (one) {
+        const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint64_t o = static_cast<uint64_t>(k * (2048 / 16));
-        rsm::tc_mma_bf16(tm + kColV, a + o, hi + o, kIdU, k > 0);
-        if constexpr (LO) rsm::tc_mma_bf16(tm + kColV, a + o, lo + o, kIdU, 1u);
+        for (uint32_t k = 0; k < 8; ++k) {
+          mma_ss(tm + kColV, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
+          if constexpr (LO)
+            mma_ss(tm + kColV, a + k * kStepMn, hi + k * kStepMn + (kOffLo - kOffX) / 16, kIdU, 1u);
+        }
+        tc_commit(c.bar(kUFull));
+        tc_commit(c.bar(kEmptyBC + st));
+        tc_commit(c.bar(kEmptyX));
       }
-      tc_commit(c.bar(kUFull));
-      tc_commit(c.bar(kEmptyBC + st));
-      tc_commit(c.bar(kEmptyX));
+      __syncwarp();
     }
   }
+  return true;
 }
 
 // P = G o decay o dt (+ D on the diagonal), a thread per row.
 template <int NH>
-__device__ __forceinline__ void run_p(const Cta& c) {
+__device__ __forceinline__ bool run_p(const Cta& c) {
   const TcParams& tp = c.tp;
-  if (tp.states_only) return;
+  if (tp.states_only) return true;
   const int k = c.warp & 3, lane = c.lane;
   const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
   // the blocks above the diagonal are zero for good
@@ -415,7 +454,9 @@ __device__ __forceinline__ void run_p(const Cta& c) {
     uint32_t zero[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) zero[i] = 0u;
+#pragma unroll 1
     for (int h = 0; h < NH; ++h)
+#pragma unroll 1
       for (int b = k + 1; b < 4; ++b) tmem_st16(trow + kColP + 64 * h + 16 * b, zero);
     rsm::tmem_st_wait();
   }
@@ -423,36 +464,36 @@ __device__ __forceinline__ void run_p(const Cta& c) {
   Unit w;
   uint32_t j = 0, vs = 0;
   while (walk.next(w)) {
-    float A2[NH], skip[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      A2[h] = __ldg(tp.p.A + w.group * NH + h) * 1.4426950408889634f;
-      skip[h] = tp.p.D != nullptr ? __ldg(tp.p.D + w.group * NH + h) : 0.0f;
+    const float A0 = __ldg(tp.p.A + w.group * NH) * kLog2e, A1 = __ldg(tp.p.A + w.group * NH + NH - 1) * kLog2e;
+    float skip0 = 0.0f, skip1 = 0.0f;
+    if (tp.p.D != nullptr) {
+      skip0 = __ldg(tp.p.D + w.group * NH);
+      skip1 = __ldg(tp.p.D + w.group * NH + NH - 1);
     }
+#pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
-      if (!c.wait_warp(kFullDt + st, j >> 1)) return;
-#pragma unroll
+      if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
+#pragma unroll 1
       for (int h = 0; h < NH; ++h) {
         const uint32_t dta = c.base + kOffDt + (st * 2 + h) * (kChunk * 4u);
         const uint32_t va = c.base + kOffV + (NH == 2 ? h : j & 1u) * (96 * 4u);
-        const Scan s = scan_chunk(dta, A2[h], k, lane);
+        const Scan s = scan_chunk(dta, h ? A1 : A0, k, lane);
         if (k < 3) sts(va + static_cast<uint32_t>(32 * k + lane) * 4u, s.dt * exp2_approx(s.after));
         // the four warps' v; a buffer is written again only after a sync in between
         c.arrive_warp(kVSync);
-        if (!c.wait_warp(kVSync, vs++)) return;
-        if (h == 0 && !c.wait_warp(kGFull, j)) return;
-        if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return;  // the last P has been multiplied
+        if (!c.wait_warp(kVSync, vs++)) return false;
+        if (h == 0 && !c.wait_warp(kGFull, j)) return false;
+        if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return false;  // the last P has been multiplied
         tc_fence_after();
         const uint32_t tp_row = trow + kColP + 64 * h;
         float between = s.upto;  // row i back to the end of block b
-#pragma unroll
-        for (int b = 2; b >= 0; --b) {
-          if (b >= k) continue;
-          const float f = exp2_approx(between);
-          between += s.t[b];
+#pragma unroll 1
+        for (int b = k - 1; b >= 0; --b) {
           float g[32];
           rsm::tmem_ld32(trow + kColG + 32 * b, g);
+          const float f = exp2_approx(between);
+          between += b == 2 ? s.t[2] : s.t[1];
           uint32_t r[16];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -468,6 +509,7 @@ __device__ __forceinline__ void run_p(const Cta& c) {
         {
           float g[32];
           rsm::tmem_ld32(trow + kColG + 32 * k, g);
+          const float skip = h ? skip1 : skip0;
           uint32_t r[16];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -479,7 +521,8 @@ __device__ __forceinline__ void run_p(const Cta& c) {
               const int jj = 4 * q + m;
               const float pj = __shfl_sync(0xFFFFFFFFu, s.upto, jj);
               const float v = g[jj] * (exp2_approx(s.upto - pj) * dd[m]);
-              e[m] = jj < lane ? v : jj == lane ? fmaf(g[jj], dd[m], skip[h]) : 0.0f;
+              // the diagonal: no decay, and the skip term
+              e[m] = jj < lane ? v : jj == lane ? v + skip : 0.0f;
             }
             r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
             r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
@@ -493,11 +536,12 @@ __device__ __forceinline__ void run_p(const Cta& c) {
       c.arrive_warp(kEmptyDt + st);
     }
   }
+  return true;
 }
 
 // w X, a thread per token row; hi over x, lo beside it.
 template <int NH, bool LO>
-__device__ __forceinline__ void run_w(const Cta& c) {
+__device__ __forceinline__ bool run_w(const Cta& c) {
   const TcParams& tp = c.tp;
   Walk walk(tp, false);
   Unit w;
@@ -506,27 +550,28 @@ __device__ __forceinline__ void run_w(const Cta& c) {
   const uint32_t row = static_cast<uint32_t>(t) * 128u;
   const uint32_t swz = static_cast<uint32_t>(t & 7) << 4;
   while (walk.next(w)) {
-    float A2[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) A2[h] = __ldg(tp.p.A + w.group * NH + h) * 1.4426950408889634f;
+    const float A0 = __ldg(tp.p.A + w.group * NH) * kLog2e, A1 = __ldg(tp.p.A + w.group * NH + NH - 1) * kLog2e;
+#pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
-      const bool partial = w.len - c0 < kChunk, live = c0 + t < w.len;
-      float wt[NH];
-      if (!c.wait_warp(kFullDt + st, j >> 1)) return;
-#pragma unroll
+      const bool live = c0 + t < w.len;
+      if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
+      float w0 = 0.0f, w1 = 0.0f;
+#pragma unroll 1
       for (int h = 0; h < NH; ++h) {
-        const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), A2[h], k, lane);
+        const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), h ? A1 : A0, k, lane);
         float rest = s.after;
 #pragma unroll
         for (int b = 1; b < 4; ++b) rest += b > k ? s.t[b] : 0.0f;
-        wt[h] = s.dt * exp2_approx(rest);
+        w0 = w1;
+        w1 = s.dt * exp2_approx(rest);
       }
+      if (NH == 1) w0 = w1;
       c.arrive_warp(kEmptyDt + st);
-      if (partial) {
-        if (!c.wait_warp(kFullX, j) || !c.wait_warp(kFullBC + st, j >> 1)) return;
+      if (w.len - c0 < kChunk) {
+        if (!c.wait_warp(kFullX, j) || !c.wait_warp(kFullBC + st, j >> 1)) return false;
         if (!live) {
-#pragma unroll
+#pragma unroll 1
           for (uint32_t q = 0; q < 8; ++q) {
 #pragma unroll
             for (int h = 0; h < NH; ++h) sts128(c.base + kOffX + h * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
@@ -537,16 +582,17 @@ __device__ __forceinline__ void run_w(const Cta& c) {
         fence_proxy_async_smem();
       }
       if (!tp.states_only) c.arrive_warp(kClean);
-      if (!c.wait_warp(kFullX, j)) return;
-#pragma unroll
+      if (!c.wait_warp(kFullX, j)) return false;
+#pragma unroll 1
       for (int h = 0; h < NH; ++h) {
-        if (!tp.states_only && !c.wait_warp(kPxDone + h, j)) return;
-        const uint32_t xa = c.base + kOffX + h * kTile + row, la = c.base + kOffLo + h * kTile + row;
-        const float2 w2 = make_float2(wt[h], wt[h]);
-#pragma unroll
+        if (!tp.states_only && !c.wait_warp(kPxDone + h, j)) return false;
+        const uint32_t xa = c.base + kOffX + h * kTile + row;
+        const float wt = h ? w1 : w0;
+        const float2 w2 = make_float2(wt, wt);
+#pragma unroll 2
         for (uint32_t q = 0; q < 8; ++q) {
-          const uint32_t at = (q << 4) ^ swz;
-          const uint4 v = rsm::lds128(xa + at);
+          const uint32_t at = xa + ((q << 4) ^ swz);
+          const uint4 v = rsm::lds128(at);
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t hw[4], lw[4];
 #pragma unroll
@@ -559,23 +605,63 @@ __device__ __forceinline__ void run_w(const Cta& c) {
               lw[m] = rsm::pack_bf16x2(l.x, l.y);
             }
           }
-          if (!live) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) hw[m] = lw[m] = 0u;
-          }
-          sts128(xa + at, hw[0], hw[1], hw[2], hw[3]);
-          if constexpr (LO) sts128(la + at, lw[0], lw[1], lw[2], lw[3]);
+          sts128(at, hw[0], hw[1], hw[2], hw[3]);
+          if constexpr (LO) sts128(at + (kOffLo - kOffX), lw[0], lw[1], lw[2], lw[3]);
         }
       }
       fence_proxy_async_smem();
       c.arrive_warp(kWFull);
     }
   }
+  return true;
+}
+
+// A dstate column of a slot's head: 64 elements kState apart.
+__device__ __forceinline__ void load_column(float (&S)[kDim], const Params& p, int slot, int64_t tile) {
+  if (slot < 0) {
+#pragma unroll
+    for (int d = 0; d < kDim; ++d) S[d] = 0.0f;
+    return;
+  }
+  const int64_t at = slot * p.state_ss + tile;
+  if (p.state_dtype == RSM_F32) {
+    const float* s = static_cast<const float*>(p.state) + at;
+#pragma unroll
+    for (int d = 0; d < kDim; ++d) S[d] = s[d * kState];
+  } else {
+    const uint16_t* s = static_cast<const uint16_t*>(p.state) + at;
+    uint16_t raw[kDim];
+#pragma unroll
+    for (int d = 0; d < kDim; ++d) raw[d] = s[d * kState];
+    if (p.state_dtype == RSM_BF16) {
+#pragma unroll
+      for (int d = 0; d < kDim; ++d) S[d] = __uint_as_float(static_cast<uint32_t>(raw[d]) << 16);
+    } else {
+#pragma unroll
+      for (int d = 0; d < kDim; ++d) S[d] = __half2float(__ushort_as_half(raw[d]));
+    }
+  }
+}
+__device__ __forceinline__ void store_column(const float (&S)[kDim], const Params& p, int slot, int64_t tile) {
+  const int64_t at = slot * p.state_ss + tile;
+  if (p.state_dtype == RSM_F32) {
+    float* s = static_cast<float*>(p.state) + at;
+#pragma unroll
+    for (int d = 0; d < kDim; ++d) s[d * kState] = S[d];
+  } else if (p.state_dtype == RSM_BF16) {
+    uint16_t* s = static_cast<uint16_t*>(p.state) + at;
+#pragma unroll
+    for (int d = 0; d < kDim; ++d) s[d * kState] = static_cast<uint16_t>(rsm::pack_bf16x2(S[d], 0.0f));
+  } else {
+    __half* s = static_cast<__half*>(p.state) + at;
+#pragma unroll
+    for (int d = 0; d < kDim; ++d) s[d * kState] = __float2half_rn(S[d]);
+  }
 }
 
 // One head's outputs and state.
 template <int NH>
-__device__ __forceinline__ void run_head(const Cta& c, int h) {
+__device__ __forceinline__ bool run_head(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   const Params& p = tp.p;
   Walk walk(tp, false);
@@ -587,7 +673,7 @@ __device__ __forceinline__ void run_head(const Cta& c, int h) {
   const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
   while (walk.next(w)) {
     const int head = w.group * NH + h;
-    const float A2 = __ldg(p.A + head) * 1.4426950408889634f;
+    const float A2 = __ldg(p.A + head) * kLog2e;
     const int64_t tile = static_cast<int64_t>(head) * (kDim * kState) + r;
     float S[kDim];
     const bool say = w.group == 0 && h == 0 && r == 0 && !tp.states_only;
@@ -597,11 +683,10 @@ __device__ __forceinline__ void run_head(const Cta& c, int h) {
       for (int d = 0; d < kDim; ++d) S[d] = at[d * kState];
     } else {
       const int src = tp.states_only ? -1 : slot_of(p, p.src, w.seq, say);
-#pragma unroll
-      for (int d = 0; d < kDim; ++d)
-        S[d] = src >= 0 ? load_state(p.state, src * p.state_ss + tile + d * kState, p.state_dtype) : 0.0f;
+      load_column(S, p, src, tile);
     }
     float decay = 0.0f;  // of the segment, log2
+#pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       if (!tp.states_only) {
@@ -614,7 +699,7 @@ __device__ __forceinline__ void run_head(const Cta& c, int h) {
         tc_fence_before();
         c.arrive_warp(kSFull);
       }
-      if (!c.wait_warp(kFullDt + st, j >> 1)) return;
+      if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
       const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), A2, k, lane);
       c.arrive_warp(kEmptyDt + st);
       const float total = (s.t[0] + s.t[1]) + (s.t[2] + s.t[3]);
@@ -624,11 +709,11 @@ __device__ __forceinline__ void run_head(const Cta& c, int h) {
 #pragma unroll
         for (int b = 0; b < 3; ++b) up += b < k ? s.t[b] : 0.0f;
         const float e = exp2_approx(up);
-        if (!c.wait_warp(kY1Full, j) || !c.wait_warp(kPxDone + h, j)) return;
+        if (!c.wait_warp(kY1Full, j) || !c.wait_warp(kPxDone + h, j)) return false;
         tc_fence_after();
         unsigned char* out = static_cast<unsigned char*>(p.out) + ((w.t0 + c0 + r) * p.out_ts + head * kDim) * 2;
         const bool live = c0 + r < w.len;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float y1[16], y2[16];
           rsm::tmem_ld16(trow + kColV + 64 * h + 16 * q, y1);
@@ -643,7 +728,7 @@ __device__ __forceinline__ void run_head(const Cta& c, int h) {
         c.arrive_warp(kVRead);
         if (c.lane == 0) mbar_arrive(c.bar(kY2Empty + h));
       }
-      if (!c.wait_warp(kUFull, j)) return;
+      if (!c.wait_warp(kUFull, j)) return false;
       tc_fence_after();
       const float a = exp2_approx(total);
 #pragma unroll
@@ -665,13 +750,10 @@ __device__ __forceinline__ void run_head(const Cta& c, int h) {
       if (r == 0) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + head] = decay;
     } else if (w.last) {
       const int dst = slot_of(p, p.dst, w.seq, say);
-      if (dst >= 0) {
-#pragma unroll
-        for (int d = 0; d < kDim; ++d)
-          store_state(p.state, dst * p.state_ss + tile + d * kState, p.state_dtype, S[d]);
-      }
+      if (dst >= 0) store_column(S, p, dst, tile);
     }
   }
+  return true;
 }
 
 template <int NH, bool LO>
@@ -718,23 +800,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
   tc_fence_after();
   const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane,
               reinterpret_cast<volatile int*>(smem + kOffAbort)};
-  if (warp == 0) {
-    if (lane == 0) run_loader<NH>(c);
-  } else if (warp == 1) {
-    if (lane == 0) {
-      run_mma<NH, LO>(c);
+  // Registers: the launch's 5 x 96 a thread of each warpgroup, shared out anew
+  // (56 + 96 + 72 + 2 x 128 = 480): a head warp holds a column of 64 state values.
+  bool ok = true;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      ok = run_loader<NH>(c);
+    } else if (warp == 1) {
+      ok = run_mma<NH, LO>(c);
       // no MMA may be in flight when the tensor memory is freed, whichever way the role ended
-      tc_commit(c.bar(kExit));
+      __syncwarp();
+      if (elect_one()) tc_commit(c.bar(kExit));
+      __syncwarp();
       (void)rsm::mbar_wait(c.bar(kExit), 0u, kTcTimeoutNs);
+    } else if (warp - 2 < NH) {
+      ok = run_dt<NH>(c, warp - 2);
     }
-  } else if (warp < 4) {
-    if (warp - 2 < NH) run_dt<NH>(c, warp - 2);
   } else if (warp < 8) {
-    run_p<NH>(c);
+    ok = run_p<NH>(c);
   } else if (warp < 12) {
-    run_w<NH, LO>(c);
-  } else if ((warp - 12) / 4 < NH) {
-    run_head<NH>(c, (warp - 12) / 4);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    ok = run_w<NH, LO>(c);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if ((warp - 12) / 4 < NH) ok = run_head<NH>(c, (warp - 12) / 4);
+  }
+  if (!ok) {
+    *c.abort_flag = 1;
+    flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
   }
   __syncwarp();
   tc_fence_before();
@@ -750,12 +844,13 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const __grid_constant__ T
   const Params& p = tp.p;
   const int seq = static_cast<int>(blockIdx.x / static_cast<uint32_t>(p.H));
   const int h = static_cast<int>(blockIdx.x % static_cast<uint32_t>(p.H));
-  auto segs_of = [&](int s) -> int64_t {
+  auto segs_of = [&](int s) -> uint32_t {
     const int64_t a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
     if (a < 0 || b < a || b > p.tokens) return 0;
-    return b - a <= tp.seg ? 1 : (b - a + tp.seg - 1) / tp.seg;
+    const uint32_t len = static_cast<uint32_t>(b - a);
+    return len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
   };
-  const int64_t n = segs_of(seq);
+  const uint32_t n = segs_of(seq);
   if (n <= 1) return;
   int64_t sg = 0;  // segments before the sequence's
   for (int s = 0; s < seq; ++s) sg += segs_of(s);
@@ -767,7 +862,7 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const __grid_constant__ T
     R[i] = src >= 0 ? load_state(p.state, src * p.state_ss + static_cast<int64_t>(h) * (kDim * kState) + threadIdx.x + 256 * i,
                                  p.state_dtype)
                     : 0.0f;
-  for (int64_t s = 0; s < n; ++s) {
+  for (uint32_t s = 0; s < n; ++s) {
     float* at = tp.seg_state + ((sg + s) * p.H + h) * (kDim * kState) + threadIdx.x;
     const float a = s + 1 < n ? exp2f(tp.seg_decay[(sg + s) * p.H + h]) : 0.0f;
 #pragma unroll

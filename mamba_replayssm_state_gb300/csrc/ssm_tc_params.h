@@ -14,7 +14,7 @@ constexpr int kTile = kChunk * 128;  // bytes of a [128 rows x 64 bf16] tile, 12
 struct TcParams {
   CUtensorMap x_map, B_map, C_map;  // [tokens, H * 64], [tokens, G * 128] bf16, boxes of 128 rows x 64 columns
   Params p;
-  int64_t seg;         // tokens of a segment, a multiple of kChunk
+  uint32_t seg;        // tokens of a segment, a multiple of kChunk, below 2^31
   float* seg_state;    // [segments, H, 64, 128]: states between segments (NULL when nothing is split)
   float* seg_decay;    // [segments, H]
   int32_t pairs;       // head groups of a CTA in all: H / NH
