@@ -19,12 +19,12 @@
 //
 // One persistent CTA per SM takes units (sequence, segment, two heads of one
 // group; one head where a group has an odd number), all chunks of a unit in order:
-//   warp 0      loads C, B (two stages) and x (one) with tensor-map copies
-//   warp 1      issues the MMAs; warps 2, 3 stage dt, a head each
-//   warps 4-7   P: a thread holds row i; G from tensor memory, P back into it
-//   warps 8-11  w X: a thread holds token t's row; x becomes hi in place
-//   warps 12-19 four a head: y out of Y1 and Y2; the state in registers as
-//               fp32, a thread per dstate column, and its bf16 copy for Y1
+//   warp 0       loads C, B and x (two stages each) with tensor-map copies
+//   warp 1       issues the MMAs; warps 2, 3 stage dt, a head each
+//   warps 4-11   four a head: P; a thread holds row i; G from tensor memory, P back into it
+//   warps 12-15  w X: a thread holds token t's row; x becomes w x in place
+//   warps 16-23  four a head: y out of Y1 and Y2; the state in registers as
+//                fp32, a thread per dstate column, and its bf16 copy for Y1
 // A sequence's last chunk may be partial: dt counts as 0 there, and the rows of
 // x and B past its end, which are a neighbour's or nobody's, are cleared
 // before an MMA multiplies them by 0.
@@ -111,6 +111,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// 16 columns of this thread's lane from each of two places.  Whole warp.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+  uint32_t r[16], s[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+        "=&r"(s[0]), "=&r"(s[1]), "=&r"(s[2]), "=&r"(s[3]), "=&r"(s[4]), "=&r"(s[5]), "=&r"(s[6]), "=&r"(s[7]),
+        "=&r"(s[8]), "=&r"(s[9]), "=&r"(s[10]), "=&r"(s[11]), "=&r"(s[12]), "=&r"(s[13]), "=&r"(s[14]), "=&r"(s[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    a[i] = __uint_as_float(r[i]);
+    b[i] = __uint_as_float(s[i]);
+  }
 }
 
 // 32 bytes of a row, streaming past L1
@@ -274,9 +296,10 @@ struct Cta {
   }
 };
 
-template <int NH>
+template <int NH, bool LO>
 __device__ __forceinline__ bool run_loader(const Cta& c) {
   const TcParams& tp = c.tp;
+  const bool state_in_x = LO && !tp.states_only;
   Walk walk(tp, c.lane == 0);
   Unit w;
   uint32_t j = 0, n_bc = 0, n_x = 0;  // chunk; copies issued so far
@@ -301,13 +324,16 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
         }
       }
       ++n_bc;
-      if (j >= 1 && !(ok = c.wait_warp(kEmptyX, j - 1u))) break;
+      // the stage is free after the update two chunks ago, or, where that chunk's
+      // state took it, after the Y1 of the last one
+      if (state_in_x ? j >= 1 : j >= 2)
+        if (!(ok = c.wait_warp(kEmptyX + st, state_in_x ? (j - 1u) >> 1 : (j >> 1) - 1u))) break;
       if (one) {
-        const uint32_t xb = c.bar(kFullX);
+        const uint32_t xb = c.bar(kFullX + st);
         mbar_arrive_expect(xb, NH * kTile);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-          tma_load_2d(c.base + kOffX + h * kTile, &tp.x_map, (h0 + h) * kDim, row, xb);
+          tma_load_2d(c.base + kOffX + (2 * st + h) * kTile, &tp.x_map, (h0 + h) * kDim, row, xb);
       }
       ++n_x;
     }
@@ -315,7 +341,8 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
   // no copy may land after the CTA has gone, whichever way the roles end
   for (uint32_t k = n_bc >= 2 ? n_bc - 2 : 0; k < n_bc; ++k)
     (void)rsm::mbar_wait(c.bar(kFullBC + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
-  if (n_x >= 1) (void)rsm::mbar_wait(c.bar(kFullX), (n_x - 1u) & 1u, kTcTimeoutNs);
+  for (uint32_t k = n_x >= 2 ? n_x - 2 : 0; k < n_x; ++k)
+    (void)rsm::mbar_wait(c.bar(kFullX + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
   return ok;
 }
 
@@ -384,26 +411,15 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
           if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
           issue_G(st);
         }
-        // Y1 = C S^T
-        if (!c.wait_warp(kSFull, j)) return false;
-        tc_fence_after();
-        if (one) {
-          const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_mn(c.base + kOffS);
-#pragma unroll
-          for (uint32_t k = 0; k < 8; ++k)
-            mma_ss(tm + kColV, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
-          tc_commit(c.bar(kY1Full));
-        }
-        __syncwarp();
         // Y2 = P X
-        if (!c.wait_warp(kFullX, j) || !c.wait_warp(kClean, j)) return false;
+        if (!c.wait_warp(kFullX + st, j >> 1) || !c.wait_warp(kClean, j)) return false;
 #pragma unroll 1
         for (uint32_t h = 0; h < NH; ++h) {
           if (!c.wait_warp(kPFull + h, j)) return false;
           if (j >= 1 && !c.wait_warp(kY2Empty + h, j - 1u)) return false;
           tc_fence_after();
           if (one) {
-            const uint32_t b = desc_mn(c.base + kOffX + h * kTile);
+            const uint32_t b = desc_mn(c.base + kOffX + (2 * st + h) * kTile);
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k)
               mma_ts(tm + kColY2 + 64 * h, tm + kColP + 64 * h + 8 * k, b + k * kStepMn, kIdPx, k > 0);
@@ -411,6 +427,19 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
           }
           __syncwarp();
         }
+        // Y1 = C S^T
+        if (!c.wait_warp(kSFull, j)) return false;
+        tc_fence_after();
+        if (one) {
+          const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile);
+          const uint32_t b = desc_mn(c.base + (LO ? kOffX + 2 * (st ^ 1u) * kTile : kOffMore));
+#pragma unroll
+          for (uint32_t k = 0; k < 8; ++k)
+            mma_ss(tm + kColV, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
+          tc_commit(c.bar(kY1Full));
+          if (LO) tc_commit(c.bar(kEmptyX + (st ^ 1u)));
+        }
+        __syncwarp();
         // the next chunk's G while this one's w X is made
         if (c0 + kChunk < w.len) {
           if (!c.wait_warp(kFullBC + (st ^ 1u), (j + 1u) >> 1)) return false;
@@ -425,16 +454,17 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
         if (!c.wait_warp(kVRead, tp.states_only ? j - 1u : j)) return false;
       tc_fence_after();
       if (one) {
-        const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX);
+        const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX + 2 * st * kTile);
+        const uint32_t lo = desc_mn(c.base + kOffMore);
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) {
           mma_ss(tm + kColV, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
           if constexpr (LO)
-            mma_ss(tm + kColV, a + k * kStepMn, hi + k * kStepMn + (kOffLo - kOffX) / 16, kIdU, 1u);
+            mma_ss(tm + kColV, a + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
         }
         tc_commit(c.bar(kUFull));
         tc_commit(c.bar(kEmptyBC + st));
-        tc_commit(c.bar(kEmptyX));
+        if (!LO || tp.states_only) tc_commit(c.bar(kEmptyX + st));
       }
       __syncwarp();
     }
@@ -442,97 +472,87 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
   return true;
 }
 
-// P = G o decay o dt (+ D on the diagonal), a thread per row.
+// P = G o decay o dt (+ D on the diagonal) of one head, a thread per row.
 template <int NH>
-__device__ __forceinline__ bool run_p(const Cta& c) {
+__device__ __forceinline__ bool run_p(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   if (tp.states_only) return true;
   const int k = c.warp & 3, lane = c.lane;
   const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
+  const uint32_t prow = trow + kColP + 64 * h;
+  const uint32_t va = c.base + kOffV + h * (96 * 4u);
   // the blocks above the diagonal are zero for good
   {
     uint32_t zero[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) zero[i] = 0u;
 #pragma unroll 1
-    for (int h = 0; h < NH; ++h)
-#pragma unroll 1
-      for (int b = k + 1; b < 4; ++b) tmem_st16(trow + kColP + 64 * h + 16 * b, zero);
+    for (int b = k + 1; b < 4; ++b) tmem_st16(prow + 16 * b, zero);
     rsm::tmem_st_wait();
   }
   Walk walk(tp, false);
   Unit w;
-  uint32_t j = 0, vs = 0;
+  uint32_t j = 0;
   while (walk.next(w)) {
-    const float A0 = __ldg(tp.p.A + w.group * NH) * kLog2e, A1 = __ldg(tp.p.A + w.group * NH + NH - 1) * kLog2e;
-    float skip0 = 0.0f, skip1 = 0.0f;
-    if (tp.p.D != nullptr) {
-      skip0 = __ldg(tp.p.D + w.group * NH);
-      skip1 = __ldg(tp.p.D + w.group * NH + NH - 1);
-    }
+    const float A2 = __ldg(tp.p.A + w.group * NH + h) * kLog2e;
+    const float skip = tp.p.D != nullptr ? __ldg(tp.p.D + w.group * NH + h) : 0.0f;
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
+      const uint32_t dta = c.base + kOffDt + (st * 2 + h) * (kChunk * 4u);
       if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
+      const Scan s = scan_chunk(dta, A2, k, lane);
+      // the last P has been multiplied: every warp is done with it and with the v it was made of
+      if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return false;
+      if (k < 3) sts(va + static_cast<uint32_t>(32 * k + lane) * 4u, s.dt * exp2_approx(s.after));
+      c.arrive_warp(kVSync + h);
+      if (!c.wait_warp(kVSync + h, j)) return false;
+      if (!c.wait_warp(kGFull, j)) return false;
+      tc_fence_after();
+      float between = s.upto;  // row i back to the end of block b
 #pragma unroll 1
-      for (int h = 0; h < NH; ++h) {
-        const uint32_t dta = c.base + kOffDt + (st * 2 + h) * (kChunk * 4u);
-        const uint32_t va = c.base + kOffV + (NH == 2 ? h : j & 1u) * (96 * 4u);
-        const Scan s = scan_chunk(dta, h ? A1 : A0, k, lane);
-        if (k < 3) sts(va + static_cast<uint32_t>(32 * k + lane) * 4u, s.dt * exp2_approx(s.after));
-        // the four warps' v; a buffer is written again only after a sync in between
-        c.arrive_warp(kVSync);
-        if (!c.wait_warp(kVSync, vs++)) return false;
-        if (h == 0 && !c.wait_warp(kGFull, j)) return false;
-        if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return false;  // the last P has been multiplied
-        tc_fence_after();
-        const uint32_t tp_row = trow + kColP + 64 * h;
-        float between = s.upto;  // row i back to the end of block b
-#pragma unroll 1
-        for (int b = k - 1; b >= 0; --b) {
-          float g[32];
-          rsm::tmem_ld32(trow + kColG + 32 * b, g);
-          const float f = exp2_approx(between);
-          between += b == 2 ? s.t[2] : s.t[1];
-          uint32_t r[16];
+      for (int b = k - 1; b >= 0; --b) {
+        float g[32];
+        rsm::tmem_ld32(trow + kColG + 32 * b, g);
+        const float f = exp2_approx(between);
+        between += b == 2 ? s.t[2] : s.t[1];
+        uint32_t r[16];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 v = lds4(va + static_cast<uint32_t>(32 * b + 4 * q) * 4u);
-            const float2 ff = make_float2(f, f);
-            const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y)), ff);
-            const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w)), ff);
-            r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
-            r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
-          }
-          tmem_st16(tp_row + 16 * b, r);
+        for (int q = 0; q < 8; ++q) {
+          const float4 v = lds4(va + static_cast<uint32_t>(32 * b + 4 * q) * 4u);
+          const float2 ff = make_float2(f, f);
+          const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y)), ff);
+          const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w)), ff);
+          r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
+          r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
         }
-        {
-          float g[32];
-          rsm::tmem_ld32(trow + kColG + 32 * k, g);
-          const float skip = h ? skip1 : skip0;
-          uint32_t r[16];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 d4 = lds4(dta + static_cast<uint32_t>(32 * k + 4 * q) * 4u);
-            const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
-            float e[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int jj = 4 * q + m;
-              const float pj = __shfl_sync(0xFFFFFFFFu, s.upto, jj);
-              const float v = g[jj] * (exp2_approx(s.upto - pj) * dd[m]);
-              // the diagonal: no decay, and the skip term
-              e[m] = jj < lane ? v : jj == lane ? v + skip : 0.0f;
-            }
-            r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
-            r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
-          }
-          tmem_st16(tp_row + 16 * k, r);
-        }
-        rsm::tmem_st_wait();
-        tc_fence_before();
-        c.arrive_warp(kPFull + h);
+        tmem_st16(prow + 16 * b, r);
       }
+      {
+        float g[32];
+        rsm::tmem_ld32(trow + kColG + 32 * k, g);
+        uint32_t r[16];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float4 d4 = lds4(dta + static_cast<uint32_t>(32 * k + 4 * q) * 4u);
+          const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
+          float e[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int jj = 4 * q + m;
+            const float pj = __shfl_sync(0xFFFFFFFFu, s.upto, jj);
+            const float v = g[jj] * (exp2_approx(s.upto - pj) * dd[m]);
+            // the diagonal: no decay, and the skip term
+            e[m] = jj < lane ? v : jj == lane ? v + skip : 0.0f;
+          }
+          r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
+          r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
+        }
+        tmem_st16(prow + 16 * k, r);
+      }
+      rsm::tmem_st_wait();
+      tc_fence_before();
+      c.arrive_warp(kPFull + h);
       c.arrive_warp(kEmptyDt + st);
     }
   }
@@ -569,12 +589,12 @@ __device__ __forceinline__ bool run_w(const Cta& c) {
       if (NH == 1) w0 = w1;
       c.arrive_warp(kEmptyDt + st);
       if (w.len - c0 < kChunk) {
-        if (!c.wait_warp(kFullX, j) || !c.wait_warp(kFullBC + st, j >> 1)) return false;
+        if (!c.wait_warp(kFullX + st, j >> 1) || !c.wait_warp(kFullBC + st, j >> 1)) return false;
         if (!live) {
 #pragma unroll 1
           for (uint32_t q = 0; q < 8; ++q) {
 #pragma unroll
-            for (int h = 0; h < NH; ++h) sts128(c.base + kOffX + h * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
+            for (int h = 0; h < NH; ++h) sts128(c.base + kOffX + (2 * st + h) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
             sts128(c.base + kOffB + (2 * st) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
             sts128(c.base + kOffB + (2 * st + 1) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
           }
@@ -582,31 +602,40 @@ __device__ __forceinline__ bool run_w(const Cta& c) {
         fence_proxy_async_smem();
       }
       if (!tp.states_only) c.arrive_warp(kClean);
-      if (!c.wait_warp(kFullX, j)) return false;
+      if (!c.wait_warp(kFullX + st, j >> 1)) return false;
+      if (LO && j >= 1 && !c.wait_warp(kUFull, j - 1u)) return false;  // the lo tiles have been multiplied
 #pragma unroll 1
       for (int h = 0; h < NH; ++h) {
         if (!tp.states_only && !c.wait_warp(kPxDone + h, j)) return false;
-        const uint32_t xa = c.base + kOffX + h * kTile + row;
+        const uint32_t xa = c.base + kOffX + (2 * st + h) * kTile + row;
+        const uint32_t la = c.base + kOffMore + h * kTile + row;
         const float wt = h ? w1 : w0;
         const float2 w2 = make_float2(wt, wt);
-#pragma unroll 2
-        for (uint32_t q = 0; q < 8; ++q) {
-          const uint32_t at = xa + ((q << 4) ^ swz);
-          const uint4 v = rsm::lds128(at);
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t hw[4], lw[4];
+#pragma unroll 1
+        for (uint32_t q0 = 0; q0 < 8; q0 += 4) {
+          uint4 v[4];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 u = __fmul2_rn(make_float2(rsm::bf16lo(in[m]), rsm::bf16hi(in[m])), w2);
-            hw[m] = rsm::pack_bf16x2(u.x, u.y);
-            if constexpr (LO) {
-              // u - hi is exact; rounded to bf16, hi + lo is within 2^-17 of u
-              const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
-              lw[m] = rsm::pack_bf16x2(l.x, l.y);
+          for (uint32_t q = 0; q < 4; ++q) v[q] = rsm::lds128(xa + (((q0 + q) << 4) ^ swz));
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) {
+            const uint32_t at = ((q0 + q) << 4) ^ swz;
+            const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float2 u = __fmul2_rn(make_float2(rsm::bf16lo(in[m]), rsm::bf16hi(in[m])), w2);
+              hw[m] = rsm::pack_bf16x2(u.x, u.y);
+              if constexpr (LO) {
+                // u - hi is exact; rounded to bf16, hi + lo is within 2^-17 of u
+                const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
+                lw[m] = rsm::pack_bf16x2(l.x, l.y);
+              }
+              hw[m] = live ? hw[m] : 0u;
+              if constexpr (LO) lw[m] = live ? lw[m] : 0u;
             }
+            sts128(xa + at, hw[0], hw[1], hw[2], hw[3]);
+            if constexpr (LO) sts128(la + at, lw[0], lw[1], lw[2], lw[3]);
           }
-          sts128(at, hw[0], hw[1], hw[2], hw[3]);
-          if constexpr (LO) sts128(at + (kOffLo - kOffX), lw[0], lw[1], lw[2], lw[3]);
         }
       }
       fence_proxy_async_smem();
@@ -660,7 +689,7 @@ __device__ __forceinline__ void store_column(const float (&S)[kDim], const Param
 }
 
 // One head's outputs and state.
-template <int NH>
+template <int NH, bool LO>
 __device__ __forceinline__ bool run_head(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   const Params& p = tp.p;
@@ -669,7 +698,7 @@ __device__ __forceinline__ bool run_head(const Cta& c, int h) {
   uint32_t j = 0;
   const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;  // output row, and dstate column
   const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
-  const uint32_t srow = c.base + kOffS + h * kTile + static_cast<uint32_t>(r) * 128u;
+  const uint32_t srow = c.base + (LO ? kOffX : kOffMore) + h * kTile + static_cast<uint32_t>(r) * 128u;
   const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
   while (walk.next(w)) {
     const int head = w.group * NH + h;
@@ -692,7 +721,7 @@ __device__ __forceinline__ bool run_head(const Cta& c, int h) {
       if (!tp.states_only) {
 #pragma unroll
         for (uint32_t q = 0; q < 8; ++q)
-          sts128(srow + ((q << 4) ^ swz), rsm::pack_bf16x2(S[8 * q], S[8 * q + 1]),
+          sts128(srow + (LO ? 2 * (st ^ 1u) * kTile : 0u) + ((q << 4) ^ swz), rsm::pack_bf16x2(S[8 * q], S[8 * q + 1]),
                  rsm::pack_bf16x2(S[8 * q + 2], S[8 * q + 3]), rsm::pack_bf16x2(S[8 * q + 4], S[8 * q + 5]),
                  rsm::pack_bf16x2(S[8 * q + 6], S[8 * q + 7]));
         fence_proxy_async_smem();
@@ -716,8 +745,7 @@ __device__ __forceinline__ bool run_head(const Cta& c, int h) {
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float y1[16], y2[16];
-          rsm::tmem_ld16(trow + kColV + 64 * h + 16 * q, y1);
-          rsm::tmem_ld16(trow + kColY2 + 64 * h + 16 * q, y2);
+          tmem_ld16x2(trow + kColV + 64 * h + 16 * q, trow + kColY2 + 64 * h + 16 * q, y1, y2);
           uint32_t v[8];
 #pragma unroll
           for (int m = 0; m < 8; ++m)
@@ -732,11 +760,11 @@ __device__ __forceinline__ bool run_head(const Cta& c, int h) {
       tc_fence_after();
       const float a = exp2_approx(total);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float u[16];
-        rsm::tmem_ld16(trow + kColV + 64 * h + 16 * q, u);
+      for (int q = 0; q < 2; ++q) {
+        float u[32];
+        rsm::tmem_ld32(trow + kColV + 64 * h + 32 * q, u);
 #pragma unroll
-        for (int m = 0; m < 16; ++m) S[16 * q + m] = fmaf(a, S[16 * q + m], u[m]);
+        for (int m = 0; m < 32; ++m) S[32 * q + m] = fmaf(a, S[32 * q + m], u[m]);
       }
       if (tp.states_only) {
         tc_fence_before();
@@ -776,10 +804,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     };
     init(kFullBC, 1, 2);
     init(kEmptyBC, 1, 2);
-    init(kFullX, 1);
-    init(kEmptyX, 1);
+    init(kFullX, 1, 2);
+    init(kEmptyX, 1, 2);
     init(kFullDt, NH, 2);
-    init(kEmptyDt, (tp.states_only ? 4 : 8) + 4 * NH, 2);
+    init(kEmptyDt, (tp.states_only ? 4 : 4 + 4 * NH) + 4 * NH, 2);
     init(kGFull, 1);
     init(kPFull, 4, 2);
     init(kPxDone, 1, 2);
@@ -790,7 +818,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     init(kWFull, 4);
     init(kClean, 4);
     init(kUFull, 1);
-    init(kVSync, 4);
+    init(kVSync, 4, 2);
     init(kExit, 1);
     *reinterpret_cast<volatile int*>(smem + kOffAbort) = 0;
     rsm::fence_mbar_init();
@@ -800,13 +828,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
   tc_fence_after();
   const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane,
               reinterpret_cast<volatile int*>(smem + kOffAbort)};
-  // Registers: the launch's 5 x 96 a thread of each warpgroup, shared out anew
-  // (56 + 96 + 72 + 2 x 128 = 480): a head warp holds a column of 64 state values.
+  // Registers: the launch's 6 x 80 a thread of each warpgroup, shared out anew
+  // (56 + 2 x 72 + 56 + 2 x 112 = 480): a head warp holds a column of 64 state values.
   bool ok = true;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
-      ok = run_loader<NH>(c);
+      ok = run_loader<NH, LO>(c);
     } else if (warp == 1) {
       ok = run_mma<NH, LO>(c);
       // no MMA may be in flight when the tensor memory is freed, whichever way the role ended
@@ -817,14 +845,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     } else if (warp - 2 < NH) {
       ok = run_dt<NH>(c, warp - 2);
     }
-  } else if (warp < 8) {
-    ok = run_p<NH>(c);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if ((warp - 4) / 4 < NH) ok = run_p<NH>(c, (warp - 4) / 4);
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     ok = run_w<NH, LO>(c);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    if ((warp - 12) / 4 < NH) ok = run_head<NH>(c, (warp - 12) / 4);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    if ((warp - 16) / 4 < NH) ok = run_head<NH, LO>(c, (warp - 16) / 4);
   }
   if (!ok) {
     *c.abort_flag = 1;

@@ -21,20 +21,22 @@ struct TcParams {
   int32_t states_only; // the pass that makes the segments' own states
 };
 
-// shared memory, bytes: two stages of C and B, the heads' x (hi in place), lo,
-// the bf16 state, then the small things
+// Shared memory, bytes: two stages each of C, B and the heads' x (where w x or
+// its hi part replaces x), and one more pair of tiles.  Those hold the bf16
+// state, or, where the update has a lo part, that; the state then takes the x
+// stage of the chunk that made it, which is free from that chunk's update until
+// the next one's Y1 has read the state.  Then the small things.
 constexpr uint32_t kOffC = 0;
 constexpr uint32_t kOffB = kOffC + 4 * kTile;
 constexpr uint32_t kOffX = kOffB + 4 * kTile;
-constexpr uint32_t kOffLo = kOffX + 2 * kTile;
-constexpr uint32_t kOffS = kOffLo + 2 * kTile;
-constexpr uint32_t kOffDt = kOffS + 2 * kTile;          // [2 stages][2 heads][128] fp32
+constexpr uint32_t kOffMore = kOffX + 4 * kTile;
+constexpr uint32_t kOffDt = kOffMore + 2 * kTile;       // [2 stages][2 heads][128] fp32
 constexpr uint32_t kOffV = kOffDt + 2 * 2 * kChunk * 4; // [2 heads][96] fp32
 constexpr uint32_t kOffBar = kOffV + 2 * 96 * 4;
 enum Bar : uint32_t {
-  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 5, kFullDt = 6, kEmptyDt = 8, kGFull = 10, kPFull = 11,
-  kPxDone = 13, kY2Empty = 15, kSFull = 17, kY1Full = 18, kVRead = 19, kWFull = 20, kClean = 21, kUFull = 22,
-  kVSync = 23, kExit = 24, kBars = 25
+  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 6, kFullDt = 8, kEmptyDt = 10, kGFull = 12, kPFull = 13,
+  kPxDone = 15, kY2Empty = 17, kSFull = 19, kY1Full = 20, kVRead = 21, kWFull = 22, kClean = 23, kUFull = 24,
+  kVSync = 25, kExit = 27, kBars = 28
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
 constexpr uint32_t kOffAbort = kOffTmem + 4;
@@ -45,7 +47,7 @@ static_assert(kTcSmem <= 232448, "shared memory of one CTA");
 // region that holds C S^T and then the state update
 constexpr uint32_t kColG = 0, kColP = 128, kColY2 = 256, kColV = 384;
 
-constexpr int kTcThreads = 640;  // loader, MMA, two dt warps, then P, W and two head warpgroups
+constexpr int kTcThreads = 768;  // one warpgroup for loader, MMA and dt, two for P, one for w X, two for y and S
 constexpr uint64_t kTcTimeoutNs = 2000000000ull;
 
 // heads: 1 or 2 a CTA; lo: the state update keeps 16 bits of w x
