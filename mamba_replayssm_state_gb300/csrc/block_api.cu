@@ -188,10 +188,10 @@ int token_map(CUtensorMap* map, const void* base, int64_t cols, int64_t tokens, 
   return RSM_OK;
 }
 
-// Tensor-map rows start on 16 bytes, output rows on 32 (their stores' width).
-bool rows_aligned(const void* base, int64_t stride, int64_t cols, int64_t tokens, int bytes) {
-  return reinterpret_cast<uintptr_t>(base) % bytes == 0 &&
-         (tokens == 1 || (stride >= cols && stride < (int64_t{1} << 38) && stride * 2 % bytes == 0));
+// Tensor-map rows, and the output's, start on 16 bytes.
+bool rows_aligned(const void* base, int64_t stride, int64_t cols, int64_t tokens) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 &&
+         (tokens == 1 || (stride >= cols && stride < (int64_t{1} << 38) && stride % 8 == 0));
 }
 
 // bf16 prompts with 64 x 128 states whose rows the tensor maps can address;
@@ -202,8 +202,8 @@ bool uses_tensor_cores(const rsm_ssm_prefill_args* a) {
 }
 bool tensor_maps_fit(const rsm_ssm_prefill_args* a) {
   const int64_t xc = static_cast<int64_t>(a->num_heads) * a->dim, bc = static_cast<int64_t>(a->num_groups) * a->dstate;
-  return rows_aligned(a->x, a->x_stride, xc, a->tokens, 16) && rows_aligned(a->B, a->B_stride, bc, a->tokens, 16) &&
-         rows_aligned(a->C, a->C_stride, bc, a->tokens, 16) && rows_aligned(a->out, a->out_stride, xc, a->tokens, 32);
+  return rows_aligned(a->x, a->x_stride, xc, a->tokens) && rows_aligned(a->B, a->B_stride, bc, a->tokens) &&
+         rows_aligned(a->C, a->C_stride, bc, a->tokens) && rows_aligned(a->out, a->out_stride, xc, a->tokens);
 }
 
 struct PrefillPlan {
@@ -218,13 +218,34 @@ int64_t workspace_bytes(const PrefillPlan& pl, int H) {
   return pl.segs * H * (ssm::kDim * ssm::kState + 1) * 4;
 }
 
+// Whether the sequences are cut into segments, whose states then come from a
+// pass of their own (x and B read twice, no outputs) and a join.  Lengths are on
+// the device, so sequences are taken as equally long.  Times are in chunks of one
+// CTA: a unit (a segment of a head group) takes its chunks and half a chunk to
+// begin and end; a states-only chunk measured 0.45 of a whole one; the two launches
+// more cost about three chunks.  One prompt of 32768 tokens and 80 heads: 40 units of
+// 256 chunks on 152 SMs without the cut.
 PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
   PrefillPlan pl;
   pl.heads = a->num_heads / a->num_groups % 2 == 0 ? 2 : 1;
   pl.pairs = a->num_heads / pl.heads;
   pl.seg = 0x7FFFFF80u;
   pl.segs = 0;
-  (void)sms;
+  const int64_t chunks = (a->tokens + static_cast<int64_t>(a->num_seqs) * ssm::kChunk - 1) /
+                         (static_cast<int64_t>(a->num_seqs) * ssm::kChunk);
+  const int64_t units = static_cast<int64_t>(a->num_seqs) * pl.pairs;
+  auto waves = [&](int64_t n) { return static_cast<double>((n + sms - 1) / sms); };
+  double best = waves(units) * (static_cast<double>(chunks) + 0.5);
+  for (int64_t n = 2; n <= 64 && n <= chunks; ++n) {
+    const int64_t per = (chunks + n - 1) / n;
+    const double t = waves(units * n) * (static_cast<double>(per) + 0.5) +
+                     waves(units * (n - 1)) * (0.45 * static_cast<double>(per) + 0.5) + 3.0;
+    if (t < best) {
+      best = t;
+      pl.seg = static_cast<uint32_t>(per * ssm::kChunk);
+      pl.segs = a->tokens / pl.seg + a->num_seqs;  // no more than this, however the lengths fall
+    }
+  }
   return pl;
 }
 
@@ -234,11 +255,10 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   if (rc != RSM_OK) return rc;
   const PrefillPlan pl = plan_prefill(a, sms);
   ssm::TcParams tp{};
-  rc = token_map(&tp.x_map, a->x, static_cast<int64_t>(a->num_heads) * ssm::kDim, a->tokens, a->x_stride, "x");
-  if (rc == RSM_OK)
-    rc = token_map(&tp.B_map, a->B, static_cast<int64_t>(a->num_groups) * ssm::kState, a->tokens, a->B_stride, "B");
-  if (rc == RSM_OK)
-    rc = token_map(&tp.C_map, a->C, static_cast<int64_t>(a->num_groups) * ssm::kState, a->tokens, a->C_stride, "C");
+  const int64_t xc = static_cast<int64_t>(a->num_heads) * ssm::kDim, bc = static_cast<int64_t>(a->num_groups) * ssm::kState;
+  rc = token_map(&tp.x_map, a->x, xc, a->tokens, a->x_stride, "x");
+  if (rc == RSM_OK) rc = token_map(&tp.B_map, a->B, bc, a->tokens, a->B_stride, "B");
+  if (rc == RSM_OK) rc = token_map(&tp.C_map, a->C, bc, a->tokens, a->C_stride, "C");
   if (rc != RSM_OK) return rc;
   tp.p = p;
   tp.seg = pl.seg;

@@ -8,19 +8,22 @@
 //   G  = C B^T           [i, j]       once for the CTA's heads, which share B and C
 //   Y1 = C S^T           [i, (h, d)]
 //   Y2 = P X             [i, d]       P = G o decay o dt, masked, in tensor memory as bf16
-//   U  = B^T (w X)       [n, (h, d)]  w X as bf16 hi + lo (16 bits), or hi alone for bf16 states
-// and y = e^{..} Y1 + Y2.  The skip term D x is a D on P's diagonal.
+//   U  = B^T (w X)       [n, d]       w X as bf16 hi + lo (16 bits), or hi alone for bf16 states
+// The skip term D x is a D on P's diagonal.
 //
-// Decays are products of factors that are all at most 1: a chunk is four blocks of
-// 32 tokens, and a pair (i, j) of blocks k > b decays by e^{sum over i's block up
-// to i} e^{blocks between} e^{rest of j's block}; only pairs of one block take an
-// exponential of their own.  Sums run inside a block, so their rounding does
-// not grow with the chunk, and nothing overflows or is divided.
+// Decays.  With p_i the sum of a from the start of i's half of the chunk, a pair
+// (i, j) of one half decays by e^{p_i} e^{-p_j}: the column factor goes into P (one
+// product an element, no exponential), the row factor onto Y2 when y = m1 Y1 + m2
+// Y2 leaves.  A pair across the halves is e^{p_i} e^{rest of the first half}.  e^{-p}
+// would overflow in a half that decays by more than 2^100 ("steep", a mean dt A
+// above 1.08): its rows take an exponential of p_i - p_j an element instead.  Sums
+// run inside blocks of 32 tokens first, so small decays keep their precision
+// next to large ones, and weights towards a chunk's end are summed from there.
 //
 // One persistent CTA per SM takes units (sequence, segment, two heads of one
 // group; one head where a group has an odd number), all chunks of a unit in order:
 //   warp 0       loads C, B and x (two stages each) with tensor-map copies
-//   warp 1       issues the MMAs; warps 2, 3 stage dt, a head each
+//   warp 1       issues the MMAs; warps 2, 3 make the decay tables, a head each
 //   warps 4-11   four a head: P; a thread holds row i; G from tensor memory, P back into it
 //   warps 12-15  w X: a thread holds token t's row; x becomes w x in place
 //   warps 16-23  four a head: y out of Y1 and Y2; the state in registers as
@@ -113,36 +116,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// 16 columns of this thread's lane from each of two places.  Whole warp.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
-  uint32_t r[16], s[16];
+// 8 columns of this thread's lane from each of two places.  Whole warp.
+__device__ __forceinline__ void tmem_ld8x2(uint32_t ta, uint32_t tb, float (&a)[8], float (&b)[8]) {
+  uint32_t r[8], s[8];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
-        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
-        "=&r"(s[0]), "=&r"(s[1]), "=&r"(s[2]), "=&r"(s[3]), "=&r"(s[4]), "=&r"(s[5]), "=&r"(s[6]), "=&r"(s[7]),
-        "=&r"(s[8]), "=&r"(s[9]), "=&r"(s[10]), "=&r"(s[11]), "=&r"(s[12]), "=&r"(s[13]), "=&r"(s[14]), "=&r"(s[15])
+        "=&r"(s[0]), "=&r"(s[1]), "=&r"(s[2]), "=&r"(s[3]), "=&r"(s[4]), "=&r"(s[5]), "=&r"(s[6]), "=&r"(s[7])
       : "r"(ta), "r"(tb)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     a[i] = __uint_as_float(r[i]);
     b[i] = __uint_as_float(s[i]);
   }
 }
 
-// 32 bytes of a row, streaming past L1
-__device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSteep = 100.0f;  // decay of a half chunk, log2, past which 2^-p is not formed
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -160,8 +153,8 @@ __device__ __forceinline__ float4 lds4(uint32_t addr) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ void sts(uint32_t addr, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void sts4(uint32_t addr, const float (&v)[4]) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -227,66 +220,37 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------------------
-// decays of a chunk's tokens, in units of log2
-// ---------------------------------------------------------------------------
-struct Scan {
-  float dt;     // this thread's token (block `warp`, place `lane`)
-  float upto;   // its block's sum up to and with it
-  float after;  // its block's sum after it
-  float t[4];   // the blocks' sums
-};
-
-__device__ __forceinline__ Scan scan_chunk(uint32_t dt_addr, float A2, int block, int lane) {
-  Scan s;
-  float a_own = 0.0f;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const float d = lds(dt_addr + static_cast<uint32_t>(b * 32 + lane) * 4u);
-    const float a = d * A2;
-    float t = a;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    s.t[b] = t;
-    if (b == block) {
-      s.dt = d;
-      a_own = a;
-    }
-  }
-  float up = a_own, down = a_own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float x = __shfl_up_sync(0xFFFFFFFFu, up, o);
-    const float y = __shfl_down_sync(0xFFFFFFFFu, down, o);
-    if (lane >= o) up += x;
-    if (lane + o < 32) down += y;
-  }
-  s.upto = up;
-  down = __shfl_down_sync(0xFFFFFFFFu, down, 1);
-  s.after = lane == 31 ? 0.0f : down;
-  return s;
+// A few instructions, since every role's code shares the instruction cache.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %4;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(kTcTries), "n"(kTcRestNs)
+      : "memory");
+  return ok != 0;
 }
 
-// ---------------------------------------------------------------------------
 struct Cta {
   const TcParams& tp;
   unsigned char* smem;
   uint32_t base;
   uint32_t tmem;
   int warp, lane;
-  volatile int* abort_flag;
 
   __device__ uint32_t bar(uint32_t b) const { return base + kOffBar + 8u * b; }
-  // The phase of `parity` of a barrier has completed; false when the wait ran
-  // out or another role has given up.
-  __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
-    const uint32_t at = bar(b);
-    if (rsm::mbar_try_wait(at, parity & 1u)) return true;
-    const uint64_t t0 = rsm::global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-      if (rsm::mbar_try_wait(at, parity & 1u)) return true;
-      if ((it & 255u) == 0u && (*abort_flag != 0 || rsm::global_timer_ns() - t0 > kTcTimeoutNs)) return false;
-    }
-  }
+  __device__ uint32_t table(uint32_t stage, int h) const { return base + kOffTab + (2 * stage + h) * kTabBytes; }
+  // The phase of `parity` of a barrier has completed; false when the tries ran out.
+  __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const { return wait_bounded(bar(b), parity & 1u); }
   __device__ bool wait_warp(uint32_t b, uint32_t parity) const {
     return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
   }
@@ -296,10 +260,9 @@ struct Cta {
   }
 };
 
-template <int NH, bool LO>
+template <int NH>
 __device__ __forceinline__ bool run_loader(const Cta& c) {
   const TcParams& tp = c.tp;
-  const bool state_in_x = LO && !tp.states_only;
   Walk walk(tp, c.lane == 0);
   Unit w;
   uint32_t j = 0, n_bc = 0, n_x = 0;  // chunk; copies issued so far
@@ -324,10 +287,10 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
         }
       }
       ++n_bc;
-      // the stage is free after the update two chunks ago, or, where that chunk's
-      // state took it, after the Y1 of the last one
-      if (state_in_x ? j >= 1 : j >= 2)
-        if (!(ok = c.wait_warp(kEmptyX + st, state_in_x ? (j - 1u) >> 1 : (j >> 1) - 1u))) break;
+      // the stage is free once the last chunk's Y1 has read the state that took it
+      // (without a Y1: after the update two chunks ago)
+      if (tp.states_only ? j >= 2 : j >= 1)
+        if (!(ok = c.wait_warp(kEmptyX + st, tp.states_only ? (j >> 1) - 1u : (j - 1u) >> 1))) break;
       if (one) {
         const uint32_t xb = c.bar(kFullX + st);
         mbar_arrive_expect(xb, NH * kTile);
@@ -340,33 +303,83 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
   }
   // no copy may land after the CTA has gone, whichever way the roles end
   for (uint32_t k = n_bc >= 2 ? n_bc - 2 : 0; k < n_bc; ++k)
-    (void)rsm::mbar_wait(c.bar(kFullBC + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
+    (void)c.wait(kFullBC + (k & 1u), k >> 1);
   for (uint32_t k = n_x >= 2 ? n_x - 2 : 0; k < n_x; ++k)
-    (void)rsm::mbar_wait(c.bar(kFullX + (k & 1u)), (k >> 1) & 1u, kTcTimeoutNs);
+    (void)c.wait(kFullX + (k & 1u), k >> 1);
   return ok;
 }
 
+// The decay tables of a head's chunks; a lane has four tokens in a row, half a warp a half chunk.
 template <int NH>
-__device__ __forceinline__ bool run_dt(const Cta& c, int h) {
+__device__ __forceinline__ bool run_tables(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   Walk walk(tp, false);
   Unit w;
   uint32_t j = 0;
+  const int lane = c.lane;
+  const bool second = lane >= 16;
   while (walk.next(w)) {
-    const float* dt = tp.p.dt + w.t0 * tp.p.dt_ts + (w.group * NH + h);
+    const int head = w.group * NH + h;
+    const float* dt = tp.p.dt + w.t0 * tp.p.dt_ts + head;
+    const float A2 = __ldg(tp.p.A + head) * kLog2e;
+    const float skip = tp.p.D != nullptr ? __ldg(tp.p.D + head) : 0.0f;
+#pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      float v[4];
+      float d[4], upto[4], after[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int t = c0 + 32 * b + c.lane;
-        v[b] = t < w.len ? __ldg(dt + static_cast<int64_t>(t) * tp.p.dt_ts) : 0.0f;
+      for (int m = 0; m < 4; ++m) {
+        const int i = c0 + 4 * lane + m;
+        d[m] = i < w.len ? __ldg(dt + static_cast<int64_t>(i) * tp.p.dt_ts) : 0.0f;
       }
-      const uint32_t st = j & 1u;
-      if (j >= 2 && !c.wait_warp(kEmptyDt + st, (j >> 1) - 1u)) return false;
+      // sums over the lane's tokens, then over the half's lanes from either end
+      upto[0] = d[0] * A2;
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        sts(c.base + kOffDt + ((st * 2 + h) * kChunk + 32 * b + c.lane) * 4u, v[b]);
-      c.arrive_warp(kFullDt + st);
+      for (int m = 1; m < 4; ++m) upto[m] = fmaf(d[m], A2, upto[m - 1]);
+      after[3] = 0.0f;
+#pragma unroll
+      for (int m = 2; m >= 0; --m) after[m] = fmaf(d[m + 1], A2, after[m + 1]);
+      float before = upto[3], beyond = upto[3];
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const float x = __shfl_up_sync(0xFFFFFFFFu, before, o, 16);
+        const float y = __shfl_down_sync(0xFFFFFFFFu, beyond, o, 16);
+        if ((lane & 15) >= o) before += x;
+        if ((lane & 15) + o < 16) beyond += y;
+      }
+      const float half0 = __shfl_sync(0xFFFFFFFFu, before, 15), half1 = __shfl_sync(0xFFFFFFFFu, before, 31);
+      const float bx = __shfl_up_sync(0xFFFFFFFFu, before, 1, 16), by = __shfl_down_sync(0xFFFFFFFFu, beyond, 1, 16);
+      before = (lane & 15) == 0 ? 0.0f : bx;
+      beyond = (lane & 15) == 15 ? 0.0f : by;
+      const bool steep = !(fabsf(second ? half1 : half0) <= kSteep);
+      const uint32_t st = j & 1u;
+      if (j >= 2 && !c.wait_warp(kEmptyTab + st, (j >> 1) - 1u)) return false;
+      const uint32_t at = c.table(st, h) + 16u * lane;
+      float col[4], v[4], ww[4], m1[4], m2[4], sk[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float p = before + upto[m], rest = after[m] + beyond;
+        const float e = exp2_approx(p), inv = exp2_approx(-p), ev = exp2_approx(rest);
+        col[m] = steep ? p : d[m] * inv;
+        v[m] = d[m] * ev;
+        ww[m] = second ? v[m] : d[m] * exp2_approx(rest + half1);
+        m1[m] = second ? exp2_approx(half0 + p) : e;
+        m2[m] = steep ? 1.0f : e;
+        sk[m] = steep ? skip : skip * inv;
+      }
+      sts4(at + kTabCol, col);
+      sts4(at + kTabDt, d);
+      if (!second) sts4(at + kTabV, v);
+      sts4(at + kTabW, ww);
+      sts4(at + kTabM1, m1);
+      sts4(at + kTabM2, m2);
+      sts4(at + kTabSkip, sk);
+      const float flagged = steep ? 1.0f : 0.0f;
+      const float steep0 = __shfl_sync(0xFFFFFFFFu, flagged, 0), steep1 = __shfl_sync(0xFFFFFFFFu, flagged, 31);
+      if (lane == 0) {
+        const float misc[4] = {exp2_approx(half0 + half1), half0 + half1, steep0, steep1};
+        sts4(at + kTabMisc, misc);
+      }
+      c.arrive_warp(kFullTab + st);
     }
   }
   return true;
@@ -382,7 +395,7 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
   constexpr uint32_t kIdG = rsm::idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdY1 = rsm::idesc_bf16_f32(128, 64 * NH, false, true);
   constexpr uint32_t kIdPx = rsm::idesc_bf16_f32(128, 64, false, true);
-  constexpr uint32_t kIdU = rsm::idesc_bf16_f32(128, 64 * NH, true, true);
+  constexpr uint32_t kIdU = rsm::idesc_bf16_f32(128, 64, true, true);
   constexpr uint32_t kStepMn = 2048 / 16;  // 16 rows of K
   const uint32_t tm = c.tmem;
   const bool one = elect_one();
@@ -391,7 +404,7 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
     tc_fence_after();
     if (one) {
       const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_k(c.base + kOffB + 2 * st * kTile);
-#pragma unroll
+#pragma unroll 2
       for (uint32_t k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
         const uint32_t o = (k >> 2) * (kTile / 16) + (k & 3) * 2;
         mma_ss(tm + kColG, a + o, b + o, kIdG, k > 0);
@@ -406,38 +419,36 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       if (!tp.states_only) {
-        // (the last chunk's P has been read out of G: its P barriers were waited for below)
+        // (G is free: the last chunk's P was waited for)
         if (c0 == 0) {
           if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
           issue_G(st);
         }
-        // Y2 = P X
-        if (!c.wait_warp(kFullX + st, j >> 1) || !c.wait_warp(kClean, j)) return false;
+        // Y2 = P X (x has come, or W would not have looked at it; the last outputs were waited for below)
+        if (!c.wait_warp(kClean, j) || !c.wait_warp(kPFull, j)) return false;
+        tc_fence_after();
+        if (one) {
 #pragma unroll 1
-        for (uint32_t h = 0; h < NH; ++h) {
-          if (!c.wait_warp(kPFull + h, j)) return false;
-          if (j >= 1 && !c.wait_warp(kY2Empty + h, j - 1u)) return false;
-          tc_fence_after();
-          if (one) {
+          for (uint32_t h = 0; h < NH; ++h) {
             const uint32_t b = desc_mn(c.base + kOffX + (2 * st + h) * kTile);
-#pragma unroll
+#pragma unroll 2
             for (uint32_t k = 0; k < 8; ++k)
               mma_ts(tm + kColY2 + 64 * h, tm + kColP + 64 * h + 8 * k, b + k * kStepMn, kIdPx, k > 0);
             tc_commit(c.bar(kPxDone + h));
           }
-          __syncwarp();
         }
+        __syncwarp();
         // Y1 = C S^T
         if (!c.wait_warp(kSFull, j)) return false;
         tc_fence_after();
         if (one) {
           const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile);
-          const uint32_t b = desc_mn(c.base + (LO ? kOffX + 2 * (st ^ 1u) * kTile : kOffMore));
-#pragma unroll
+          const uint32_t b = desc_mn(c.base + kOffX + 2 * (st ^ 1u) * kTile);
+#pragma unroll 2
           for (uint32_t k = 0; k < 8; ++k)
             mma_ss(tm + kColV, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
           tc_commit(c.bar(kY1Full));
-          if (LO) tc_commit(c.bar(kEmptyX + (st ^ 1u)));
+          tc_commit(c.bar(kEmptyX + (st ^ 1u)));
         }
         __syncwarp();
         // the next chunk's G while this one's w X is made
@@ -449,30 +460,34 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
         return false;
       }
       // U = B^T (w X), where Y1 was
-      if (!c.wait_warp(kWFull, j)) return false;
-      if (!tp.states_only || j >= 1)
-        if (!c.wait_warp(kVRead, tp.states_only ? j - 1u : j)) return false;
-      tc_fence_after();
-      if (one) {
-        const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX + 2 * st * kTile);
-        const uint32_t lo = desc_mn(c.base + kOffMore);
-#pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-          mma_ss(tm + kColV, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
-          if constexpr (LO)
-            mma_ss(tm + kColV, a + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
+      if (!tp.states_only && !c.wait_warp(kYRead, j)) return false;
+#pragma unroll 1
+      for (uint32_t h = 0; h < NH; ++h) {
+        if (!c.wait_warp(kWFull + h, j)) return false;
+        if (tp.states_only && j >= 1 && !c.wait_warp(kURead + h, j - 1u)) return false;
+        tc_fence_after();
+        if (one) {
+          const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX + (2 * st + h) * kTile);
+          const uint32_t lo = desc_mn(c.base + kOffC + (2 * st + h) * kTile);
+#pragma unroll 2
+          for (uint32_t k = 0; k < 8; ++k) {
+            mma_ss(tm + kColV + 64 * h, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
+            if constexpr (LO) mma_ss(tm + kColV + 64 * h, a + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
+          }
+          tc_commit(c.bar(kUFull + h));
+          if (h == NH - 1) {
+            tc_commit(c.bar(kEmptyBC + st));
+            if (tp.states_only) tc_commit(c.bar(kEmptyX + st));
+          }
         }
-        tc_commit(c.bar(kUFull));
-        tc_commit(c.bar(kEmptyBC + st));
-        if (!LO || tp.states_only) tc_commit(c.bar(kEmptyX + st));
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
   return true;
 }
 
-// P = G o decay o dt (+ D on the diagonal) of one head, a thread per row.
+// P of one head, a thread per row; the row factor 2^p is left to the output.
 template <int NH>
 __device__ __forceinline__ bool run_p(const Cta& c, int h) {
   const TcParams& tp = c.tp;
@@ -480,7 +495,6 @@ __device__ __forceinline__ bool run_p(const Cta& c, int h) {
   const int k = c.warp & 3, lane = c.lane;
   const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
   const uint32_t prow = trow + kColP + 64 * h;
-  const uint32_t va = c.base + kOffV + h * (96 * 4u);
   // the blocks above the diagonal are zero for good
   {
     uint32_t zero[16];
@@ -494,66 +508,77 @@ __device__ __forceinline__ bool run_p(const Cta& c, int h) {
   Unit w;
   uint32_t j = 0;
   while (walk.next(w)) {
-    const float A2 = __ldg(tp.p.A + w.group * NH + h) * kLog2e;
-    const float skip = tp.p.D != nullptr ? __ldg(tp.p.D + w.group * NH + h) : 0.0f;
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      const uint32_t st = j & 1u;
-      const uint32_t dta = c.base + kOffDt + (st * 2 + h) * (kChunk * 4u);
-      if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
-      const Scan s = scan_chunk(dta, A2, k, lane);
-      // the last P has been multiplied: every warp is done with it and with the v it was made of
-      if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return false;
-      if (k < 3) sts(va + static_cast<uint32_t>(32 * k + lane) * 4u, s.dt * exp2_approx(s.after));
-      c.arrive_warp(kVSync + h);
-      if (!c.wait_warp(kVSync + h, j)) return false;
+      const uint32_t st = j & 1u, tab = c.table(st, h);
+      if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
+      const float skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
+      const bool steep = lds(tab + kTabMisc + 8u + 4u * (k >> 1)) != 0.0f;
+      if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return false;  // the last P has been multiplied
       if (!c.wait_warp(kGFull, j)) return false;
       tc_fence_after();
-      float between = s.upto;  // row i back to the end of block b
+      if (!steep) {
 #pragma unroll 1
-      for (int b = k - 1; b >= 0; --b) {
-        float g[32];
-        rsm::tmem_ld32(trow + kColG + 32 * b, g);
-        const float f = exp2_approx(between);
-        between += b == 2 ? s.t[2] : s.t[1];
-        uint32_t r[16];
+        for (int b = 0; b <= k; ++b) {
+          const uint32_t col = tab + (k >= 2 && b < 2 ? kTabV : kTabCol) + 128u * b;
+          float g[32];
+          rsm::tmem_ld32(trow + kColG + 32 * b, g);
+          uint32_t r[16];
+          if (b < k) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 v = lds4(va + static_cast<uint32_t>(32 * b + 4 * q) * 4u);
-          const float2 ff = make_float2(f, f);
-          const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y)), ff);
-          const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w)), ff);
-          r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
-          r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
-        }
-        tmem_st16(prow + 16 * b, r);
-      }
-      {
-        float g[32];
-        rsm::tmem_ld32(trow + kColG + 32 * k, g);
-        uint32_t r[16];
+            for (int q = 0; q < 8; ++q) {
+              const float4 v = lds4(col + 16u * q);
+              const float2 lo = __fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y));
+              const float2 hi = __fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w));
+              r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
+              r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
+            }
+          } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 d4 = lds4(dta + static_cast<uint32_t>(32 * k + 4 * q) * 4u);
-          const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
-          float e[4];
+            for (int q = 0; q < 8; ++q) {
+              const float4 v = lds4(col + 16u * q);
+              float e[4] = {g[4 * q] * v.x, g[4 * q + 1] * v.y, g[4 * q + 2] * v.z, g[4 * q + 3] * v.w};
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const int jj = 4 * q + m;
-            const float pj = __shfl_sync(0xFFFFFFFFu, s.upto, jj);
-            const float v = g[jj] * (exp2_approx(s.upto - pj) * dd[m]);
-            // the diagonal: no decay, and the skip term
-            e[m] = jj < lane ? v : jj == lane ? v + skip : 0.0f;
+              for (int m = 0; m < 4; ++m) {
+                if (4 * q + m == lane) e[m] += skip;
+                if (4 * q + m > lane) e[m] = 0.0f;
+              }
+              r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
+              r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
+            }
           }
-          r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
-          r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
+          tmem_st16(prow + 16 * b, r);
         }
-        tmem_st16(prow + 16 * k, r);
+      } else {
+        const float pi = lds(tab + kTabCol + 4u * (32 * k + lane));
+        const float ui = exp2_approx(pi);
+#pragma unroll 1
+        for (int b = 0; b <= k; ++b) {
+          const bool same = (b >> 1) == (k >> 1);
+          float g[32];
+          rsm::tmem_ld32(trow + kColG + 32 * b, g);
+          uint32_t r[16];
+#pragma unroll
+          for (int q = 0; q < 32; q += 2) {
+            float e[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const uint32_t o = 128u * b + 4u * (q + m);
+              const bool in = b < k || q + m <= lane;
+              const float f = same ? exp2_approx(pi - lds(tab + kTabCol + o)) * lds(tab + kTabDt + o)
+                                   : ui * lds(tab + kTabV + o);
+              e[m] = in ? g[q + m] * f : 0.0f;
+              if (b == k && q + m == lane) e[m] += skip;
+            }
+            r[q / 2] = rsm::pack_bf16x2(e[0], e[1]);
+          }
+          tmem_st16(prow + 16 * b, r);
+        }
       }
       rsm::tmem_st_wait();
       tc_fence_before();
-      c.arrive_warp(kPFull + h);
-      c.arrive_warp(kEmptyDt + st);
+      c.arrive_warp(kPFull);
+      if (lane == 0) mbar_arrive(c.bar(kEmptyTab + st));
     }
   }
   return true;
@@ -570,27 +595,16 @@ __device__ __forceinline__ bool run_w(const Cta& c) {
   const uint32_t row = static_cast<uint32_t>(t) * 128u;
   const uint32_t swz = static_cast<uint32_t>(t & 7) << 4;
   while (walk.next(w)) {
-    const float A0 = __ldg(tp.p.A + w.group * NH) * kLog2e, A1 = __ldg(tp.p.A + w.group * NH + NH - 1) * kLog2e;
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
-      const bool live = c0 + t < w.len;
-      if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
-      float w0 = 0.0f, w1 = 0.0f;
-#pragma unroll 1
-      for (int h = 0; h < NH; ++h) {
-        const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), h ? A1 : A0, k, lane);
-        float rest = s.after;
-#pragma unroll
-        for (int b = 1; b < 4; ++b) rest += b > k ? s.t[b] : 0.0f;
-        w0 = w1;
-        w1 = s.dt * exp2_approx(rest);
-      }
-      if (NH == 1) w0 = w1;
-      c.arrive_warp(kEmptyDt + st);
-      if (w.len - c0 < kChunk) {
-        if (!c.wait_warp(kFullX + st, j >> 1) || !c.wait_warp(kFullBC + st, j >> 1)) return false;
-        if (!live) {
+      if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
+      const float w0 = lds(c.table(st, 0) + kTabW + 4u * t), w1 = lds(c.table(st, NH - 1) + kTabW + 4u * t);
+      c.arrive_warp(kEmptyTab + st);
+      if (!c.wait_warp(kFullX + st, j >> 1)) return false;
+      if (w.len - c0 < kChunk) {  // rows past the end: zero, whatever is there
+        if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
+        if (c0 + t >= w.len) {
 #pragma unroll 1
           for (uint32_t q = 0; q < 8; ++q) {
 #pragma unroll
@@ -602,13 +616,12 @@ __device__ __forceinline__ bool run_w(const Cta& c) {
         fence_proxy_async_smem();
       }
       if (!tp.states_only) c.arrive_warp(kClean);
-      if (!c.wait_warp(kFullX + st, j >> 1)) return false;
-      if (LO && j >= 1 && !c.wait_warp(kUFull, j - 1u)) return false;  // the lo tiles have been multiplied
 #pragma unroll 1
       for (int h = 0; h < NH; ++h) {
         if (!tp.states_only && !c.wait_warp(kPxDone + h, j)) return false;
+        if (LO && !tp.states_only && h == 0 && !c.wait_warp(kY1Full, j)) return false;  // lo takes the place of C
         const uint32_t xa = c.base + kOffX + (2 * st + h) * kTile + row;
-        const uint32_t la = c.base + kOffMore + h * kTile + row;
+        const uint32_t la = c.base + kOffC + (2 * st + h) * kTile + row;
         const float wt = h ? w1 : w0;
         const float2 w2 = make_float2(wt, wt);
 #pragma unroll 1
@@ -630,66 +643,67 @@ __device__ __forceinline__ bool run_w(const Cta& c) {
                 const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
                 lw[m] = rsm::pack_bf16x2(l.x, l.y);
               }
-              hw[m] = live ? hw[m] : 0u;
-              if constexpr (LO) lw[m] = live ? lw[m] : 0u;
             }
             sts128(xa + at, hw[0], hw[1], hw[2], hw[3]);
             if constexpr (LO) sts128(la + at, lw[0], lw[1], lw[2], lw[3]);
           }
         }
+        fence_proxy_async_smem();
+        c.arrive_warp(kWFull + h);
       }
-      fence_proxy_async_smem();
-      c.arrive_warp(kWFull);
     }
   }
   return true;
 }
 
 // A dstate column of a slot's head: 64 elements kState apart.
-__device__ __forceinline__ void load_column(float (&S)[kDim], const Params& p, int slot, int64_t tile) {
+__device__ __forceinline__ void load_column(float2 (&S)[kDim / 2], const Params& p, int slot, int64_t tile) {
   if (slot < 0) {
 #pragma unroll
-    for (int d = 0; d < kDim; ++d) S[d] = 0.0f;
+    for (int d = 0; d < kDim / 2; ++d) S[d] = make_float2(0.0f, 0.0f);
     return;
   }
   const int64_t at = slot * p.state_ss + tile;
   if (p.state_dtype == RSM_F32) {
     const float* s = static_cast<const float*>(p.state) + at;
 #pragma unroll
-    for (int d = 0; d < kDim; ++d) S[d] = s[d * kState];
+    for (int d = 0; d < kDim / 2; ++d) S[d] = make_float2(s[2 * d * kState], s[(2 * d + 1) * kState]);
   } else {
     const uint16_t* s = static_cast<const uint16_t*>(p.state) + at;
     uint16_t raw[kDim];
 #pragma unroll
     for (int d = 0; d < kDim; ++d) raw[d] = s[d * kState];
-    if (p.state_dtype == RSM_BF16) {
+    const bool bf = p.state_dtype == RSM_BF16;
 #pragma unroll
-      for (int d = 0; d < kDim; ++d) S[d] = __uint_as_float(static_cast<uint32_t>(raw[d]) << 16);
-    } else {
-#pragma unroll
-      for (int d = 0; d < kDim; ++d) S[d] = __half2float(__ushort_as_half(raw[d]));
+    for (int d = 0; d < kDim; ++d) {
+      const float v = bf ? __uint_as_float(static_cast<uint32_t>(raw[d]) << 16) : __half2float(__ushort_as_half(raw[d]));
+      if (d & 1)
+        S[d / 2].y = v;
+      else
+        S[d / 2].x = v;
     }
   }
 }
-__device__ __forceinline__ void store_column(const float (&S)[kDim], const Params& p, int slot, int64_t tile) {
+__device__ __forceinline__ void store_column(const float2 (&S)[kDim / 2], const Params& p, int slot, int64_t tile) {
   const int64_t at = slot * p.state_ss + tile;
   if (p.state_dtype == RSM_F32) {
     float* s = static_cast<float*>(p.state) + at;
 #pragma unroll
-    for (int d = 0; d < kDim; ++d) s[d * kState] = S[d];
-  } else if (p.state_dtype == RSM_BF16) {
-    uint16_t* s = static_cast<uint16_t*>(p.state) + at;
-#pragma unroll
-    for (int d = 0; d < kDim; ++d) s[d * kState] = static_cast<uint16_t>(rsm::pack_bf16x2(S[d], 0.0f));
+    for (int d = 0; d < kDim; ++d) s[d * kState] = d & 1 ? S[d / 2].y : S[d / 2].x;
   } else {
-    __half* s = static_cast<__half*>(p.state) + at;
+    uint16_t* s = static_cast<uint16_t*>(p.state) + at;
+    const bool bf = p.state_dtype == RSM_BF16;
 #pragma unroll
-    for (int d = 0; d < kDim; ++d) s[d * kState] = __float2half_rn(S[d]);
+    for (int d = 0; d < kDim / 2; ++d) {
+      const uint32_t v = bf ? rsm::pack_bf16x2(S[d].x, S[d].y) : rsm::pack_f16x2(S[d].x, S[d].y);
+      s[2 * d * kState] = static_cast<uint16_t>(v);
+      s[(2 * d + 1) * kState] = static_cast<uint16_t>(v >> 16);
+    }
   }
 }
 
 // One head's outputs and state.
-template <int NH, bool LO>
+template <int NH>
 __device__ __forceinline__ bool run_head(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   const Params& p = tp.p;
@@ -697,84 +711,103 @@ __device__ __forceinline__ bool run_head(const Cta& c, int h) {
   Unit w;
   uint32_t j = 0;
   const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;  // output row, and dstate column
-  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
-  const uint32_t srow = c.base + (LO ? kOffX : kOffMore) + h * kTile + static_cast<uint32_t>(r) * 128u;
+  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + 64 * h;
+  const uint32_t srow = c.base + kOffX + h * kTile + static_cast<uint32_t>(r) * 128u;
   const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
+  // a warp's 32 rows of 64 bytes; 16-byte pieces of a row change places by its number / 2
+  const uint32_t ywarp = c.base + kOffY + (4 * h + k) * kYBytes;
+  const uint32_t yput = ywarp + 64u * lane, yswz = static_cast<uint32_t>((lane >> 1) & 3) << 4;
+  const uint32_t yget = ywarp + 64u * (lane >> 2) + ((static_cast<uint32_t>(lane & 3) ^ ((lane >> 3) & 3)) << 4);
   while (walk.next(w)) {
     const int head = w.group * NH + h;
-    const float A2 = __ldg(p.A + head) * kLog2e;
     const int64_t tile = static_cast<int64_t>(head) * (kDim * kState) + r;
-    float S[kDim];
+    float2 S[kDim / 2];
     const bool say = w.group == 0 && h == 0 && r == 0 && !tp.states_only;
     if (w.split && !tp.states_only) {
       const float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
 #pragma unroll
-      for (int d = 0; d < kDim; ++d) S[d] = at[d * kState];
+      for (int d = 0; d < kDim / 2; ++d) S[d] = make_float2(at[2 * d * kState], at[(2 * d + 1) * kState]);
     } else {
-      const int src = tp.states_only ? -1 : slot_of(p, p.src, w.seq, say);
-      load_column(S, p, src, tile);
+      load_column(S, p, tp.states_only ? -1 : slot_of(p, p.src, w.seq, say), tile);
     }
     float decay = 0.0f;  // of the segment, log2
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      const uint32_t st = j & 1u;
+      const uint32_t st = j & 1u, tab = c.table(st, h);
       if (!tp.states_only) {
+        const uint32_t at = srow + 2 * (st ^ 1u) * kTile;
 #pragma unroll
         for (uint32_t q = 0; q < 8; ++q)
-          sts128(srow + (LO ? 2 * (st ^ 1u) * kTile : 0u) + ((q << 4) ^ swz), rsm::pack_bf16x2(S[8 * q], S[8 * q + 1]),
-                 rsm::pack_bf16x2(S[8 * q + 2], S[8 * q + 3]), rsm::pack_bf16x2(S[8 * q + 4], S[8 * q + 5]),
-                 rsm::pack_bf16x2(S[8 * q + 6], S[8 * q + 7]));
+          sts128(at + ((q << 4) ^ swz), rsm::pack_bf16x2(S[4 * q].x, S[4 * q].y),
+                 rsm::pack_bf16x2(S[4 * q + 1].x, S[4 * q + 1].y), rsm::pack_bf16x2(S[4 * q + 2].x, S[4 * q + 2].y),
+                 rsm::pack_bf16x2(S[4 * q + 3].x, S[4 * q + 3].y));
         fence_proxy_async_smem();
         tc_fence_before();
         c.arrive_warp(kSFull);
       }
-      if (!c.wait_warp(kFullDt + st, j >> 1)) return false;
-      const Scan s = scan_chunk(c.base + kOffDt + (st * 2 + h) * (kChunk * 4u), A2, k, lane);
-      c.arrive_warp(kEmptyDt + st);
-      const float total = (s.t[0] + s.t[1]) + (s.t[2] + s.t[3]);
-      decay += total;
+      if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
+      const float m1 = lds(tab + kTabM1 + 4u * r), m2 = lds(tab + kTabM2 + 4u * r);
+      const float a = lds(tab + kTabMisc);
+      decay += lds(tab + kTabMisc + 4u);
+      c.arrive_warp(kEmptyTab + st);
       if (!tp.states_only) {
-        float up = s.upto;
-#pragma unroll
-        for (int b = 0; b < 3; ++b) up += b < k ? s.t[b] : 0.0f;
-        const float e = exp2_approx(up);
         if (!c.wait_warp(kY1Full, j) || !c.wait_warp(kPxDone + h, j)) return false;
         tc_fence_after();
-        unsigned char* out = static_cast<unsigned char*>(p.out) + ((w.t0 + c0 + r) * p.out_ts + head * kDim) * 2;
-        const bool live = c0 + r < w.len;
+        // 32 columns at a time, turned in shared memory so that four lanes store
+        // a row's 64 bytes (a row a lane touched 32 lines an instruction: 1650 cycles a chunk,
+        // during which the other roles' shared-memory accesses wait; tensor-map stores
+        // of such small boxes were slower still)
+        const float2 f1 = make_float2(m1, m1), f2 = make_float2(m2, m2);
+        uint16_t* out = static_cast<uint16_t*>(p.out) + (w.t0 + c0 + 32 * k + (lane >> 2)) * p.out_ts + head * kDim + 8 * (lane & 3);
+        const int rows = w.len - c0 - 32 * k - (lane >> 2);  // rows from this lane's first on
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          float y1[16], y2[16];
-          tmem_ld16x2(trow + kColV + 64 * h + 16 * q, trow + kColY2 + 64 * h + 16 * q, y1, y2);
-          uint32_t v[8];
+        for (uint32_t part = 0; part < 2; ++part) {
+#pragma unroll 2
+          for (uint32_t q = 0; q < 4; ++q) {
+            float y1[8], y2[8];
+            tmem_ld8x2(trow + kColV + 32 * part + 8 * q, trow + kColY2 + 32 * part + 8 * q, y1, y2);
+            uint32_t v[4];
 #pragma unroll
-          for (int m = 0; m < 8; ++m)
-            v[m] = rsm::pack_bf16x2(fmaf(e, y1[2 * m], y2[2 * m]), fmaf(e, y1[2 * m + 1], y2[2 * m + 1]));
-          if (live) stg256(out + 32 * q, v);
+            for (int m = 0; m < 4; ++m) {
+              const float2 y = __ffma2_rn(f1, make_float2(y1[2 * m], y1[2 * m + 1]),
+                                          __fmul2_rn(f2, make_float2(y2[2 * m], y2[2 * m + 1])));
+              v[m] = rsm::pack_bf16x2(y.x, y.y);
+            }
+            sts128(yput + ((16u * q) ^ yswz), v[0], v[1], v[2], v[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = rsm::lds128(yget + 512u * i);
+            if (8 * i < rows) *reinterpret_cast<uint4*>(out + 8 * i * p.out_ts + 32 * part) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
-        c.arrive_warp(kVRead);
-        if (c.lane == 0) mbar_arrive(c.bar(kY2Empty + h));
+        c.arrive_warp(kYRead);
       }
-      if (!c.wait_warp(kUFull, j)) return false;
+      if (!c.wait_warp(kUFull + h, j)) return false;
       tc_fence_after();
-      const float a = exp2_approx(total);
+      const float2 a2 = make_float2(a, a);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float u[32];
-        rsm::tmem_ld32(trow + kColV + 64 * h + 32 * q, u);
+        rsm::tmem_ld32(trow + kColV + 32 * q, u);
 #pragma unroll
-        for (int m = 0; m < 32; ++m) S[32 * q + m] = fmaf(a, S[32 * q + m], u[m]);
+        for (int m = 0; m < 16; ++m) S[16 * q + m] = __ffma2_rn(a2, S[16 * q + m], make_float2(u[2 * m], u[2 * m + 1]));
       }
       if (tp.states_only) {
         tc_fence_before();
-        c.arrive_warp(kVRead);
+        c.arrive_warp(kURead + h);
       }
     }
     if (tp.states_only) {
       float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
 #pragma unroll
-      for (int d = 0; d < kDim; ++d) at[d * kState] = S[d];
+      for (int d = 0; d < kDim / 2; ++d) {
+        at[2 * d * kState] = S[d].x;
+        at[(2 * d + 1) * kState] = S[d].y;
+      }
       if (r == 0) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + head] = decay;
     } else if (w.last) {
       const int dst = slot_of(p, p.dst, w.seq, say);
@@ -806,59 +839,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     init(kEmptyBC, 1, 2);
     init(kFullX, 1, 2);
     init(kEmptyX, 1, 2);
-    init(kFullDt, NH, 2);
-    init(kEmptyDt, (tp.states_only ? 4 : 4 + 4 * NH) + 4 * NH, 2);
+    init(kFullTab, NH, 2);
+    init(kEmptyTab, (tp.states_only ? 4 : 4 + 4 * NH) + 4 * NH, 2);
     init(kGFull, 1);
-    init(kPFull, 4, 2);
+    init(kPFull, 4 * NH);
     init(kPxDone, 1, 2);
-    init(kY2Empty, 4, 2);
     init(kSFull, 4 * NH);
     init(kY1Full, 1);
-    init(kVRead, 4 * NH);
-    init(kWFull, 4);
+    init(kYRead, 4 * NH);
+    init(kWFull, 4, 2);
     init(kClean, 4);
-    init(kUFull, 1);
-    init(kVSync, 4, 2);
+    init(kUFull, 1, 2);
+    init(kURead, 4, 2);
     init(kExit, 1);
-    *reinterpret_cast<volatile int*>(smem + kOffAbort) = 0;
     rsm::fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane,
-              reinterpret_cast<volatile int*>(smem + kOffAbort)};
+  const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane};
   // Registers: the launch's 6 x 80 a thread of each warpgroup, shared out anew
-  // (56 + 2 x 72 + 56 + 2 x 112 = 480): a head warp holds a column of 64 state values.
+  // (56 + 2 x 64 + 56 + 2 x 120 = 480): a head warp holds a column of 64 state values.
   bool ok = true;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
-      ok = run_loader<NH, LO>(c);
+      ok = run_loader<NH>(c);
     } else if (warp == 1) {
       ok = run_mma<NH, LO>(c);
       // no MMA may be in flight when the tensor memory is freed, whichever way the role ended
       __syncwarp();
       if (elect_one()) tc_commit(c.bar(kExit));
       __syncwarp();
-      (void)rsm::mbar_wait(c.bar(kExit), 0u, kTcTimeoutNs);
+      (void)c.wait(kExit, 0u);
     } else if (warp - 2 < NH) {
-      ok = run_dt<NH>(c, warp - 2);
+      ok = run_tables<NH>(c, warp - 2);
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if ((warp - 4) / 4 < NH) ok = run_p<NH>(c, (warp - 4) / 4);
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     ok = run_w<NH, LO>(c);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-    if ((warp - 16) / 4 < NH) ok = run_head<NH, LO>(c, (warp - 16) / 4);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    if ((warp - 16) / 4 < NH) ok = run_head<NH>(c, (warp - 16) / 4);
   }
-  if (!ok) {
-    *c.abort_flag = 1;
-    flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
-  }
+  if (!ok) flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -22,33 +22,48 @@ struct TcParams {
 };
 
 // Shared memory, bytes: two stages each of C, B and the heads' x (where w x or
-// its hi part replaces x), and one more pair of tiles.  Those hold the bf16
-// state, or, where the update has a lo part, that; the state then takes the x
-// stage of the chunk that made it, which is free from that chunk's update until
-// the next one's Y1 has read the state.  Then the small things.
+// its hi part replaces x), the outputs on their way out, and the decay tables.
+// Two things live in what others leave free: the lo part of w x in its chunk's C
+// stage, from Y1, the last to read C, to the update; the bf16 state in the x stage
+// of the chunk that made it, from that chunk's update to the next one's Y1.
 constexpr uint32_t kOffC = 0;
 constexpr uint32_t kOffB = kOffC + 4 * kTile;
 constexpr uint32_t kOffX = kOffB + 4 * kTile;
-constexpr uint32_t kOffMore = kOffX + 4 * kTile;
-constexpr uint32_t kOffDt = kOffMore + 2 * kTile;       // [2 stages][2 heads][128] fp32
-constexpr uint32_t kOffV = kOffDt + 2 * 2 * kChunk * 4; // [2 heads][96] fp32
-constexpr uint32_t kOffBar = kOffV + 2 * 96 * 4;
+constexpr uint32_t kOffY = kOffX + 4 * kTile;  // a head warp: two times 32 rows x 16 columns, 32-byte swizzled
+constexpr uint32_t kYBytes = 2 * 32 * 32;
+// A table of [stage][head], made by a dt warp; fp32, 128 tokens where not said otherwise.
+// p is the decay (log2) from the start of a token's half of the chunk up to and with it.
+enum Table : uint32_t {
+  kTabCol = 0,     // dt 2^-p: what a column of P is scaled by in its own half (a steep half: p itself)
+  kTabDt = 512,    // dt
+  kTabV = 1024,    // [64] first half: dt 2^(decay after the token up to the half's end)
+  kTabW = 1280,    // dt 2^(decay after the token up to the chunk's end)
+  kTabM1 = 1792,   // y = m1 Y1 + m2 Y2: 2^(decay from the chunk's start)
+  kTabM2 = 2304,   //                    2^p (a steep half: 1)
+  kTabSkip = 2816, // D 2^-p (a steep half: D)
+  kTabMisc = 3328, // 2^(decay of the chunk); its log2; whether each half is steep
+  kTabBytes = 3344
+};
+constexpr uint32_t kOffTab = kOffY + 8 * kYBytes;
+constexpr uint32_t kOffBar = kOffTab + 4 * kTabBytes;
 enum Bar : uint32_t {
-  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 6, kFullDt = 8, kEmptyDt = 10, kGFull = 12, kPFull = 13,
-  kPxDone = 15, kY2Empty = 17, kSFull = 19, kY1Full = 20, kVRead = 21, kWFull = 22, kClean = 23, kUFull = 24,
-  kVSync = 25, kExit = 27, kBars = 28
+  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 6, kFullTab = 8, kEmptyTab = 10, kGFull = 12, kPFull = 13,
+  kPxDone = 14, kSFull = 16, kY1Full = 17, kYRead = 18, kWFull = 19, kClean = 21, kUFull = 22, kURead = 24, kExit = 26,
+  kBars = 27
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
-constexpr uint32_t kOffAbort = kOffTmem + 4;
-constexpr uint32_t kTcSmem = kOffAbort + 4;
+constexpr uint32_t kTcSmem = kOffTmem + 8;
 static_assert(kTcSmem <= 232448, "shared memory of one CTA");
 
 // tensor memory, columns: G = C B^T, the heads' P (bf16 pairs), P X, and one
 // region that holds C S^T and then the state update
 constexpr uint32_t kColG = 0, kColP = 128, kColY2 = 256, kColV = 384;
 
-constexpr int kTcThreads = 768;  // one warpgroup for loader, MMA and dt, two for P, one for w X, two for y and S
-constexpr uint64_t kTcTimeoutNs = 2000000000ull;
+constexpr int kTcThreads = 768;  // one warpgroup for loader, MMA and tables, two for P, one for w X, two for y and S
+// A wait gives up after this many tries, each of which may rest for up to kTcRestNs:
+// two seconds at most, and tens of milliseconds if no try ever rests.
+constexpr uint32_t kTcTries = 1u << 21;
+constexpr uint32_t kTcRestNs = 1000;
 
 // heads: 1 or 2 a CTA; lo: the state update keeps 16 bits of w x
 const void* tc_kernel(int heads, bool lo);
