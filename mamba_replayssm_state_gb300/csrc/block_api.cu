@@ -295,7 +295,8 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   if (pl.segs > 0) {
     cudaError_t e = run(true);
     if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
-    rc = launch(ssm::join_kernel(), static_cast<int64_t>(a->num_seqs) * a->num_heads, 256, &tp, stream);
+    rc = launch(ssm::join_kernel(), static_cast<int64_t>(a->num_seqs) * a->num_heads * (ssm::kDim * ssm::kState) / (4 * ssm::kJoinThreads),
+                ssm::kJoinThreads, &tp, stream);
     if (rc != RSM_OK) return rc;
   }
   const cudaError_t e = run(false);

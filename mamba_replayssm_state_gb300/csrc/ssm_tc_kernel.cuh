@@ -895,11 +895,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
 
 // R = the sequence's initial state; for each of its segments: the segment
 // starts from R, and R = its decay R + its own state.  One CTA per (sequence,
-// head); the same elements belong to the same thread throughout.
-__global__ void __launch_bounds__(256) ssm_join_kernel(const __grid_constant__ TcParams tp) {
+// head, part of the state); a thread keeps four elements throughout and asks for
+// eight segments' at a time, which no store of its own comes before.
+__global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(const __grid_constant__ TcParams tp) {
   const Params& p = tp.p;
-  const int seq = static_cast<int>(blockIdx.x / static_cast<uint32_t>(p.H));
-  const int h = static_cast<int>(blockIdx.x % static_cast<uint32_t>(p.H));
+  constexpr uint32_t kParts = kDim * kState / (4 * kJoinThreads);
+  const uint32_t part = blockIdx.x % kParts, unit = blockIdx.x / kParts;
+  const int seq = static_cast<int>(unit / static_cast<uint32_t>(p.H));
+  const int h = static_cast<int>(unit % static_cast<uint32_t>(p.H));
   auto segs_of = [&](int s) -> uint32_t {
     const int64_t a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
     if (a < 0 || b < a || b > p.tokens) return 0;
@@ -911,21 +914,33 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const __grid_constant__ T
   int64_t sg = 0;  // segments before the sequence's
   for (int s = 0; s < seq; ++s) sg += segs_of(s);
   const int src = slot_of(p, p.src, seq, false);
-  constexpr int kPer = kDim * kState / 256;
-  float R[kPer];
+  const uint32_t e = 4 * (part * kJoinThreads + threadIdx.x);
+  float R[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (src >= 0) {
+    const int64_t at = src * p.state_ss + static_cast<int64_t>(h) * (kDim * kState) + e;
+    for (int i = 0; i < 4; ++i) R[i] = load_state(p.state, at + i, p.state_dtype);
+  }
+  const int64_t step = static_cast<int64_t>(p.H) * (kDim * kState);
+  float* at = tp.seg_state + (sg * p.H + h) * (kDim * kState) + e;
+  const float* decay = tp.seg_decay + sg * p.H + h;
+  constexpr uint32_t kAhead = 8;
+  for (uint32_t s0 = 0; s0 < n; s0 += kAhead) {
+    float4 own[kAhead];
+    float a[kAhead];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    R[i] = src >= 0 ? load_state(p.state, src * p.state_ss + static_cast<int64_t>(h) * (kDim * kState) + threadIdx.x + 256 * i,
-                                 p.state_dtype)
-                    : 0.0f;
-  for (uint32_t s = 0; s < n; ++s) {
-    float* at = tp.seg_state + ((sg + s) * p.H + h) * (kDim * kState) + threadIdx.x;
-    const float a = s + 1 < n ? exp2f(tp.seg_decay[(sg + s) * p.H + h]) : 0.0f;
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      const bool have = s0 + i + 1 < n;  // nothing follows the last
+      own[i] = have ? *reinterpret_cast<const float4*>(at + (s0 + i) * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      a[i] = have ? exp2f(decay[static_cast<int64_t>(s0 + i) * p.H]) : 0.0f;
+    }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float own = s + 1 < n ? at[256 * i] : 0.0f;
-      at[256 * i] = R[i];
-      R[i] = fmaf(a, R[i], own);
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      if (s0 + i >= n) break;
+      *reinterpret_cast<float4*>(at + (s0 + i) * step) = make_float4(R[0], R[1], R[2], R[3]);
+      R[0] = fmaf(a[i], R[0], own[i].x);
+      R[1] = fmaf(a[i], R[1], own[i].y);
+      R[2] = fmaf(a[i], R[2], own[i].z);
+      R[3] = fmaf(a[i], R[3], own[i].w);
     }
   }
 }

@@ -69,7 +69,8 @@ constexpr uint32_t kTcRestNs = 1000;
 const void* tc_kernel(int heads, bool lo);
 
 // Between the two passes of a split call: the state every segment starts from.
-// Grid: (num_seqs * H), 256 threads.
+// Grid: num_seqs * H * the state's elements / (4 kJoinThreads).
+constexpr int kJoinThreads = 128;
 const void* join_kernel();
 
 }  // namespace ssm
