@@ -304,6 +304,40 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   return done();
 }
 
+// ---------------------------------------------------------------------------
+// norms
+// ---------------------------------------------------------------------------
+bool is_input(int dt) { return dt == RSM_F32 || dt == RSM_BF16; }
+
+// Eight columns at a time: every row of a tensor starts on 16 bytes (32 hold the eight of fp32).
+bool vectors_fit(const void* base, int64_t stride, int64_t rows, int dt) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (rows == 1 || stride * (dt == RSM_F32 ? 4 : 2) % 16 == 0);
+}
+
+int launch_norm(int kind, int input_dtype, int other_dtype, const rmsnorm::Params& p, void* stream) {
+  const bool fits = p.group % 8 == 0 && vectors_fit(p.x, p.x_rs, p.rows, input_dtype) &&
+                    vectors_fit(p.other, p.other_rs, p.rows, other_dtype) &&
+                    vectors_fit(p.out, p.out_rs, p.rows, input_dtype) &&
+                    (kind != 0 || vectors_fit(p.residual_out, p.res_rs, p.rows, other_dtype)) &&
+                    reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
+  const int64_t units = p.rows * p.groups;
+  const int vecs = p.group / 8;
+  if (!fits || vecs > 4096) return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, 0, false), units, 256, &p, stream);
+  int dev = 0, sms = 0;
+  const int rc = device_sms(&dev, &sms);
+  if (rc != RSM_OK) return rc;
+  // Few groups: as many threads as there are vectors, for the shortest way
+  // through; many: two vectors a thread, for more bytes in flight.
+  const bool many = units >= 4 * static_cast<int64_t>(sms);
+  if (vecs <= (many ? 64 : 32)) {
+    const int v = vecs <= 32 ? 1 : 2, warps = many ? 4 : 1;
+    return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, v, true), (units + warps - 1) / warps, 32 * warps, &p, stream);
+  }
+  const int v = vecs > 2048 ? 4 : vecs > 1024 || many ? 2 : 1;
+  const int threads = ((vecs + v - 1) / v + 31) / 32 * 32;
+  return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, v, false), units, threads, &p, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -414,15 +448,14 @@ int rsm_add_rms_norm(const rsm_add_rms_norm_args* a, void* stream) {
   if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
   if (a->rows < 0) return fail(RSM_EINVAL, "rows must be >= 0");
   if (a->dim <= 0) return fail(RSM_EINVAL, "dim must be positive (got %d)", a->dim);
-  const void* fn = rmsnorm::kernel(0, a->input_dtype, a->residual_dtype);
-  if (fn == nullptr)
+  if (!is_input(a->input_dtype) || !is_input(a->residual_dtype))
     return fail(RSM_EINVAL, "input_dtype and residual_dtype must be BF16 or F32 (got %d, %d)", a->input_dtype, a->residual_dtype);
   if (a->rows == 0) return done();
   const int rc = need({{a->x, "x"}, {a->residual, "residual"}, {a->weight, "weight"}, {a->out, "out"}, {a->residual_out, "residual_out"}});
   if (rc != RSM_OK) return rc;
-  rmsnorm::Params p{a->x, a->residual, a->weight, a->out, a->residual_out, a->rows, a->x_stride, a->residual_stride,
-                 a->out_stride, a->residual_out_stride, a->dim, a->dim, a->residual_scale, a->eps};
-  return launch(fn, a->rows, 256, &p, stream);
+  const rmsnorm::Params p{a->x, a->residual, a->weight, a->out, a->residual_out, a->rows, a->x_stride, a->residual_stride,
+                          a->out_stride, a->residual_out_stride, a->dim, a->dim, 1, a->residual_scale, a->eps};
+  return launch_norm(0, a->input_dtype, a->residual_dtype, p, stream);
 }
 
 int rsm_gated_rms_norm(const rsm_gated_rms_norm_args* a, void* stream) {
@@ -431,14 +464,13 @@ int rsm_gated_rms_norm(const rsm_gated_rms_norm_args* a, void* stream) {
   if (a->dim <= 0) return fail(RSM_EINVAL, "dim must be positive (got %d)", a->dim);
   if (a->group_size <= 0 || a->dim % a->group_size != 0)
     return fail(RSM_EINVAL, "group_size (%d) must divide dim (%d)", a->group_size, a->dim);
-  const void* fn = rmsnorm::kernel(a->norm_before_gate ? 2 : 1, a->input_dtype, a->input_dtype);
-  if (fn == nullptr) return fail(RSM_EINVAL, "input_dtype must be BF16 or F32 (got %d)", a->input_dtype);
+  if (!is_input(a->input_dtype)) return fail(RSM_EINVAL, "input_dtype must be BF16 or F32 (got %d)", a->input_dtype);
   if (a->rows == 0) return done();
   const int rc = need({{a->x, "x"}, {a->z, "z"}, {a->weight, "weight"}, {a->out, "out"}});
   if (rc != RSM_OK) return rc;
-  rmsnorm::Params p{a->x, a->z, a->weight, a->out, nullptr, a->rows, a->x_stride, a->z_stride,
-                 a->out_stride, 0, a->dim, a->group_size, 1.0f, a->eps};
-  return launch(fn, a->rows * (a->dim / a->group_size), 256, &p, stream);
+  const rmsnorm::Params p{a->x, a->z, a->weight, a->out, nullptr, a->rows, a->x_stride, a->z_stride, a->out_stride, 0,
+                          a->dim, a->group_size, a->dim / a->group_size, 1.0f, a->eps};
+  return launch_norm(a->norm_before_gate ? 2 : 1, a->input_dtype, a->input_dtype, p, stream);
 }
 
 const char* rsm_block_last_error(void) { return g_error; }

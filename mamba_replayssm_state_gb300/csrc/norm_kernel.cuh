@@ -3,7 +3,14 @@
 //   kind 0: r = residual + scale x,  out = r / sqrt(mean(r^2) + eps) w, r kept
 //   kind 1: v = x silu(z),           out = v / sqrt(mean(v^2) + eps) w
 //   kind 2: out = x / sqrt(mean(x^2) + eps) w silu(z)
-// One CTA per (row, group); two passes over the group, sums in fp32.
+// Sums and norms in fp32; r is normalised unrounded.
+//
+// Memory bounds it: each input read once, each output written once.  A group
+// (a row's columns that share a norm) is held in registers from its one read to
+// its one write, eight columns to a vector, V vectors to a thread, so that the
+// reduction in between costs no second pass.  A warp takes a group of up to 32 V
+// vectors, whole CTAs the longer ones.  Groups whose columns are not whole
+// aligned vectors, or more than 4096 of them, go through the two-pass kernel.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -12,21 +19,113 @@
 
 namespace rmsnorm {
 
-constexpr int kThreads = 256;
+constexpr int kPlainThreads = 256;
 
 __device__ __forceinline__ float get(const float* p) { return *p; }
 __device__ __forceinline__ float get(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(rsm::pack_bf16x2(v, 0.0f)); }
 
-__device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
+// silu(z); for bf16 inputs the exponential and the quotient are the fast ones,
+// within 2^-17 for |z| < 80, far below the inputs' own 2^-8.
+template <typename IT>
+__device__ __forceinline__ float silu(float z) {
+  if constexpr (sizeof(IT) == 2)
+    return __fdividef(z, 1.0f + __expf(-z));
+  else
+    return z / (1.0f + expf(-z));
+}
 
+// eight columns
+__device__ __forceinline__ void get8(const uint16_t* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = rsm::bf16lo(w[i]);
+    v[2 * i + 1] = rsm::bf16hi(w[i]);
+  }
+}
+__device__ __forceinline__ void get8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void put8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(rsm::pack_bf16x2(v[0], v[1]), rsm::pack_bf16x2(v[2], v[3]),
+                                            rsm::pack_bf16x2(v[4], v[5]), rsm::pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// WARP: a group a warp, blockDim / 32 groups a CTA; otherwise a group a CTA.
+template <int KIND, typename IT, typename RT, int V, bool WARP>
+__global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ Params p) {
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int threads = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
+  const int64_t unit = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  const int64_t row = unit / p.groups;
+  const int c0 = static_cast<int>(unit - row * p.groups) * p.group;
+  if (WARP && row >= p.rows) return;
+  const IT* x = static_cast<const IT*>(p.x) + row * p.x_rs + c0;
+  const RT* other = static_cast<const RT*>(p.other) + row * p.other_rs + c0;
+  float val[V][8], oth[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = 8 * (tid + v * threads);
+    if (c < p.group) {
+      get8(x + c, val[v]);
+      get8(other + c, oth[v]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) val[v][i] = oth[v][i] = 0.0f;
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (KIND == 0) val[v][i] = fmaf(p.scale, val[v][i], oth[v][i]);
+      if constexpr (KIND == 1) val[v][i] *= silu<IT>(oth[v][i]);
+      sum = fmaf(val[v][i], val[v][i], sum);
+    }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if constexpr (!WARP) {
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    sum = lane < (threads >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  }
+  const float r = rsqrtf(sum / static_cast<float>(p.group) + p.eps);
+  IT* out = static_cast<IT*>(p.out) + row * p.out_rs + c0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = 8 * (tid + v * threads);
+    if (c >= p.group) break;
+    float w[8];
+    get8(p.weight + c0 + c, w);
+    if constexpr (KIND == 0) put8(static_cast<RT*>(p.residual_out) + row * p.res_rs + c0 + c, val[v]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] *= val[v][i] * r;
+      if constexpr (KIND == 2) w[i] *= silu<IT>(oth[v][i]);
+    }
+    put8(out + c, w);
+  }
+}
+
+// Any size, stride and alignment: a group a CTA, read twice.
 template <int KIND, typename IT, typename RT>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Params p) {
-  __shared__ float part[kThreads / 32];
-  const int groups = p.dim / p.group;
-  const int64_t row = blockIdx.x / groups;
-  const int c0 = static_cast<int>(blockIdx.x % groups) * p.group;
+__global__ void __launch_bounds__(kPlainThreads) norm_plain_kernel(const __grid_constant__ Params p) {
+  __shared__ float part[kPlainThreads / 32];
+  const int64_t row = blockIdx.x / static_cast<uint32_t>(p.groups);
+  const int c0 = static_cast<int>(blockIdx.x % static_cast<uint32_t>(p.groups)) * p.group;
   const IT* x = static_cast<const IT*>(p.x) + row * p.x_rs + c0;
   const RT* other = static_cast<const RT*>(p.other) + row * p.other_rs + c0;
   IT* out = static_cast<IT*>(p.out) + row * p.out_rs + c0;
@@ -34,11 +133,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   auto value = [&](int i) {
     const float v = get(x + i);
     if constexpr (KIND == 0) return fmaf(p.scale, v, get(other + i));
-    if constexpr (KIND == 1) return v * silu(get(other + i));
+    if constexpr (KIND == 1) return v * silu<IT>(get(other + i));
     return v;
   };
   float sum = 0.0f;
-  for (int i = threadIdx.x; i < p.group; i += kThreads) {
+  for (int i = threadIdx.x; i < p.group; i += kPlainThreads) {
     const float v = value(i);
     sum = fmaf(v, v, sum);
   }
@@ -46,13 +145,13 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
   __syncthreads();
   sum = 0.0f;
-  for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
-  const float r = 1.0f / sqrtf(sum / static_cast<float>(p.group) + p.eps);
-  for (int i = threadIdx.x; i < p.group; i += kThreads) {
+  for (int i = 0; i < kPlainThreads / 32; ++i) sum += part[i];
+  const float r = rsqrtf(sum / static_cast<float>(p.group) + p.eps);
+  for (int i = threadIdx.x; i < p.group; i += kPlainThreads) {
     const float v = value(i);
     if constexpr (KIND == 0) put(static_cast<RT*>(p.residual_out) + row * p.res_rs + c0 + i, v);
     float y = v * r * __ldg(w + i);
-    if constexpr (KIND == 2) y *= silu(get(other + i));
+    if constexpr (KIND == 2) y *= silu<IT>(get(other + i));
     put(out + i, y);
   }
 }

@@ -11,12 +11,13 @@ struct Params {
   const float* weight;
   void *out, *residual_out;
   int64_t rows, x_rs, other_rs, out_rs, res_rs;  // row strides, elements
-  int32_t dim, group;                            // group: columns of one norm
+  int32_t dim, group, groups;                    // columns of a row, of one norm; norms of a row
   float scale, eps;
 };
 
 // kind 0: add, 1: gate then norm, 2: norm then gate; types are rsm_dtype codes
-// (other_dtype: the residual's; the gate has the input's).
-const void* kernel(int kind, int input_dtype, int other_dtype);
+// (other_dtype: the residual's; the gate has the input's).  vectors: of a
+// thread (1, 2 or 4; 0: the two-pass kernel); warp: a group a warp.
+const void* kernel(int kind, int input_dtype, int other_dtype, int vectors, bool warp);
 
 }  // namespace rmsnorm
