@@ -304,6 +304,26 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   return done();
 }
 
+// New tokens: 64 x 128 states whose rows are whole vectors, up to 16 tokens a
+// request; the rest runs on the sequential kernel.
+int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* stream) {
+  const int es = p.state_dtype == RSM_F32 ? 4 : p.state_dtype == RSM_BF16 || p.state_dtype == RSM_F16 ? 2 : 1;
+  const bool fits = dim == ssm::kDim && dstate == ssm::kState && p.window <= ssm::kTokenMaxNew &&
+                    reinterpret_cast<uintptr_t>(p.state) % 16 == 0 && p.state_ss * es % 16 == 0;
+  if (!fits) return launch_seq(p, input_dtype, dim, dstate, stream);
+  int dev = 0, sms = 0;
+  const int rc = device_sms(&dev, &sms);
+  if (rc != RSM_OK) return rc;
+  // A CTA works on two heads at a time.  Few heads in all: two a CTA, to spread
+  // over the SMs; many: eight, so that most loads are asked for ahead of their use.
+  const int hpg = p.H / p.G;
+  const bool many = static_cast<int64_t>(p.units) * p.H >= 32 * static_cast<int64_t>(sms);
+  p.heads_per_cta = std::min(hpg, many ? 8 : 2);
+  const int64_t parts = (hpg + p.heads_per_cta - 1) / p.heads_per_cta;
+  return launch(ssm::token_kernel(input_dtype, p.state_dtype, p.mode != ssm::kStep ? 0 : p.window == 1 ? 1 : 2),
+                static_cast<int64_t>(p.units) * p.G * parts, ssm::kTokenThreads, &p, stream);
+}
+
 // ---------------------------------------------------------------------------
 // norms
 // ---------------------------------------------------------------------------
@@ -406,7 +426,7 @@ int rsm_ssm_step(const rsm_ssm_step_args* a, void* stream) {
   p.src = a->src_slots;
   p.dst = a->dst_slots;
   p.mode = ssm::kStep;
-  return launch_seq(p, a->input_dtype, a->dim, a->dstate, stream);
+  return launch_tokens(p, a->input_dtype, a->dim, a->dstate, stream);
 }
 
 int rsm_replayssm_decode(const rsm_replayssm_decode_args* a, void* stream) {
@@ -441,7 +461,7 @@ int rsm_replayssm_decode(const rsm_replayssm_decode_args* a, void* stream) {
   p.dtc_ss = a->dt_cache_slot_stride;
   p.R = a->ring_buffer_len;
   p.mode = ssm::kDecode;
-  return launch_seq(p, a->input_dtype, a->dim, a->dstate, stream);
+  return launch_tokens(p, a->input_dtype, a->dim, a->dstate, stream);
 }
 
 int rsm_add_rms_norm(const rsm_add_rms_norm_args* a, void* stream) {

@@ -3,6 +3,13 @@
 
 namespace ssm {
 
+const void* token_kernel_bf16(int state_dtype, int mode);  // ssm_token_bf16.cu
+const void* token_kernel_f32(int state_dtype, int mode);   // ssm_token_f32.cu
+
+const void* token_kernel(int input_dtype, int state_dtype, int mode) {
+  return input_dtype == RSM_BF16 ? token_kernel_bf16(state_dtype, mode) : token_kernel_f32(state_dtype, mode);
+}
+
 namespace {
 template <typename IT>
 const void* pick(int dim, int dstate, int* threads) {

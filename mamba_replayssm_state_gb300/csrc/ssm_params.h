@@ -26,11 +26,18 @@ struct Params {
   int64_t x_bs, x_ts, B_bs, B_ts, C_bs, C_ts, dt_bs, dt_ts, out_bs, out_ts;  // batch and token strides, elements
   int64_t state_ss, scale_ss, xc_ss, Bc_ss, dtc_ss;                         // slot strides, elements
   int32_t units, window, num_slots, H, G, R, pad, mode, state_dtype;
+  int32_t heads_per_cta;  // token kernel
 };
 
 constexpr int kSeqTokens = 16;  // tokens staged in shared memory at a time (sequential kernel)
 
 // The sequential kernel of an (input type, dim, dstate); NULL when not compiled.
 const void* seq_kernel(int input_dtype, int dim, int dstate, int* threads);
+
+// The new-token kernel of 64 x 128 states, 256 threads; NULL when not compiled.
+// mode: 0 the ring form, 1 one token a request, state to state, 2 several.
+const void* token_kernel(int input_dtype, int state_dtype, int mode);
+constexpr int kTokenThreads = 256;
+constexpr int kTokenMaxNew = 16;  // new tokens of a request
 
 }  // namespace ssm
