@@ -56,10 +56,10 @@ int check_sizes(const A* a) {
   return RSM_OK;
 }
 
-int launch(const void* fn, int64_t grid, int threads, const void* params, void* stream) {
+int launch(const void* fn, int64_t grid, int threads, const void* params, void* stream, size_t smem = 0) {
   if (grid > 0x7FFFFFFFLL) return fail(RSM_EINVAL, "the call needs %lld blocks, more than 2^31-1", static_cast<long long>(grid));
   void* kargs[] = {const_cast<void*>(params)};
-  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), kargs, 0,
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), kargs, smem,
                                          static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return done();
@@ -314,14 +314,35 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
   int dev = 0, sms = 0;
   const int rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  // A CTA works on two heads at a time.  Few heads in all: two a CTA, to spread
-  // over the SMs; many: eight, so that most loads are asked for ahead of their use.
-  const int hpg = p.H / p.G;
-  const bool many = static_cast<int64_t>(p.units) * p.H >= 32 * static_cast<int64_t>(sms);
-  p.heads_per_cta = std::min(hpg, many ? 8 : 2);
-  const int64_t parts = (hpg + p.heads_per_cta - 1) / p.heads_per_cta;
-  return launch(ssm::token_kernel(input_dtype, p.state_dtype, p.mode != ssm::kStep ? 0 : p.window == 1 ? 1 : 2),
-                static_cast<int64_t>(p.units) * p.G * parts, ssm::kTokenThreads, &p, stream);
+  const bool step = p.mode == ssm::kStep;
+  const int ie = input_dtype == RSM_F32 ? 4 : 2, hpg = p.H / p.G;
+  p.tokens_max = step ? p.window : std::min(p.R, ssm::kTokenMaxAll);
+  // rows of a head's x or a group's B start on 16 bytes wherever they are
+  auto even = [&](const void* base, int64_t bs, int64_t ts) {
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (p.units == 1 || bs * ie % 16 == 0) && (p.window == 1 || ts * ie % 16 == 0);
+  };
+  p.wide = even(p.x, p.x_bs, p.x_ts) &&
+           (step || (even(p.B, p.B_bs, p.B_ts) && reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(p.B_cache) % 16 == 0 && p.Bc_ss * ie % 16 == 0));
+  // A CTA works on two heads at a time.  Many heads in all: as many a CTA, up to
+  // sixteen, as leave eight CTAs an SM, since a CTA's first loads wait for nothing to
+  // do meanwhile; few: two a CTA, to spread over the SMs.  Long rings take fewer, to
+  // fit 64 KB of shared memory.
+  int per = 2;
+  while (per < 16 && static_cast<int64_t>(p.units) * p.H / (2 * per) >= 8 * static_cast<int64_t>(sms)) per *= 2;
+  per = std::min(per, hpg);
+  const int mode = step ? (p.window == 1 ? 1 : 2)
+                   : input_dtype == RSM_BF16 && p.state_dtype != RSM_F32 && p.state_dtype != RSM_F16 ? (p.window <= 8 ? 3 : 4) : 0;
+  auto smem = [&](int n) { return ssm::token_smem(mode, ie, n, p.window, p.tokens_max); };
+  while (per > 1 && smem(per) > 64 * 1024) per = (per + 1) / 2;
+  p.heads_per_cta = per;
+  const int64_t parts = (hpg + per - 1) / per, grid = static_cast<int64_t>(p.units) * p.G * parts;
+  const void* fn = ssm::token_kernel(input_dtype, p.state_dtype, mode);
+  if (smem(per) > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem(per)));
+    if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  }
+  return launch(fn, grid, ssm::kTokenThreads, &p, stream, smem(per));
 }
 
 // ---------------------------------------------------------------------------

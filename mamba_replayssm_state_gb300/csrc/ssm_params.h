@@ -26,7 +26,7 @@ struct Params {
   int64_t x_bs, x_ts, B_bs, B_ts, C_bs, C_ts, dt_bs, dt_ts, out_bs, out_ts;  // batch and token strides, elements
   int64_t state_ss, scale_ss, xc_ss, Bc_ss, dtc_ss;                         // slot strides, elements
   int32_t units, window, num_slots, H, G, R, pad, mode, state_dtype;
-  int32_t heads_per_cta;  // token kernel
+  int32_t heads_per_cta, tokens_max, wide;  // token kernel: tokens of a request at most; rows of x and B are 16-byte vectors
 };
 
 constexpr int kSeqTokens = 16;  // tokens staged in shared memory at a time (sequential kernel)
@@ -35,9 +35,12 @@ constexpr int kSeqTokens = 16;  // tokens staged in shared memory at a time (seq
 const void* seq_kernel(int input_dtype, int dim, int dstate, int* threads);
 
 // The new-token kernel of 64 x 128 states, 256 threads; NULL when not compiled.
-// mode: 0 the ring form, 1 one token a request, state to state, 2 several.
+// mode: 0 the ring form, 1 one token a request, state to state, 2 several;
+// 3 and 4 the ring form on the tensor cores, up to 8 and up to 16 new tokens.
 const void* token_kernel(int input_dtype, int state_dtype, int mode);
 constexpr int kTokenThreads = 256;
 constexpr int kTokenMaxNew = 16;  // new tokens of a request
+constexpr int kTokenMaxAll = 64;  // with the ring's
+uint32_t token_smem(int mode, int input_bytes, int heads, int fresh, int all);
 
 }  // namespace ssm

@@ -6,6 +6,7 @@ namespace ssm {
 namespace {
 template <int SF>
 const void* pick(int mode) {
+  if (mode >= 3) return nullptr;
   if (mode == 0) return reinterpret_cast<const void*>(&ssm_token_kernel<float, SF, 0>);
   if constexpr (SF == RSM_F32 || SF == RSM_BF16 || SF == RSM_F16)
     return mode == 1 ? reinterpret_cast<const void*>(&ssm_token_kernel<float, SF, 1>)

@@ -8,23 +8,35 @@
 // C_t belong to the group, not the head.
 //
 // Memory bounds both: the states' bytes, once (ring form) or once each way.  A CTA
-// takes heads of one request and group; four warps share a head, 16 dim rows each,
-// and go through the CTA's heads two at a time, asking for the next head's rows as
-// soon as the last's have had their use, before the sums and the ring's part.  A lane holds eight dstate columns of eight
-// rows: sixteen lanes to a row, a 16-byte load (16-bit states) an instruction and two
-// rows.  Sums over a row's sixteen lanes are taken for eight rows at once, halving the
-// values at each exchange: eight shuffles, not 32; lane l then has row 2 ((l >> 1) & 7)
-// + (l >> 4), the same in lanes 2i and 2i + 1, which split the ring's tokens by parity.
+// takes heads of one request and group.  One round of loads stages what their
+// tokens need; then four warps share a head, 16 dim rows each, and go through the
+// CTA's heads two at a time, asking for the next head's rows as soon as the last's
+// have had their use.
+//
+// The ring form with bf16 inputs and bf16, int8 or fp8 states takes its products on
+// the tensor cores (mma.sync m16n8k16: 16 rows, 8 tokens; such states' elements are
+// exact in bf16, so only the weights of the ring's tokens are rounded).  A lane's 16
+// bytes of a row serve two k-steps, k being numbered to suit.  Without it a state
+// element costs an unpacking, an FMA a token and its share of a reduction: 88% of the
+// memory's rate at one token on bf16 states, 21% at four on int8 ones.
+//
+// Otherwise a lane holds eight dstate columns of eight rows: sixteen lanes to a
+// row, a 16-byte load (16-bit states) an instruction and two rows.  Sums over a
+// row's sixteen lanes are taken for eight rows at once, halving the values at each
+// exchange: eight shuffles, not 32; lane l then has row 2 ((l >> 1) & 7) + (l >> 4), the
+// same in lanes 2i and 2i + 1, which split the ring's tokens by parity.
 #pragma once
 #include <cuda_runtime.h>
 
+#include "rsm_ptx.cuh"
 #include "ssm_seq_kernel.cuh"
 
 namespace ssm {
 
 constexpr int kTokThreads = kTokenThreads;
 constexpr int kTokMaxNew = kTokenMaxNew;
-constexpr int kTokMaxAll = 64;    // with the ring's
+constexpr int kTokMaxAll = kTokenMaxAll;
+constexpr int kTokD = 64, kTokN = 128;
 constexpr int kTokRows = 16;      // dim rows of a warp
 constexpr int kTokLoads = 8;      // row pairs of a warp
 
@@ -36,14 +48,14 @@ template <> struct Raw<RSM_FP8_E4M3> { uint2 v; };
 
 __device__ __forceinline__ uint4 ldg128_once(const void* p) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint2 ldg64_once(const void* p) {
   uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 
@@ -121,21 +133,101 @@ __device__ __forceinline__ float fold8(float (&v)[8], int lane) {
   return v[0];
 }
 
-// MODE: 0 the ring form, 1 one new token a request, state to state, 2 several.
+// Shared memory of a CTA, in bytes: what its heads' tokens need, staged by one
+// round of loads; `all` is the most tokens a request can have (ring and new).
+struct TokLayout {
+  uint32_t C, B, x, dt, dot, w, e, bytes;
+};
+// elements between staged rows of x
+__host__ __device__ constexpr int tok_x_row(int mode, int heads) { return heads * kTokD + (mode >= 3 ? 8 : 0); }
+__host__ __device__ inline TokLayout tok_layout(int mode, int input_bytes, int heads, int fresh, int all) {
+  const bool ring_form = mode == 0 || mode >= 3;
+  TokLayout l{};
+  uint32_t at = 0;
+  auto take = [&](uint32_t n) {
+    const uint32_t o = at;
+    at += (n + 15u) & ~15u;
+    return o;
+  };
+  const uint32_t all16 = (all + 15u) & ~15u, fresh8 = (fresh + 7u) & ~7u;
+  l.C = take(fresh * kTokN * 4);
+  l.B = take(all * kTokN * (ring_form ? input_bytes : 4));  // ring form: as stored, for the dots alone
+  // tensor cores: whole k-steps, rows 16 bytes off a multiple of 128
+  l.x = take(mode >= 3 ? all16 * tok_x_row(mode, heads) * input_bytes : all * heads * kTokD * input_bytes);
+  l.dt = take(all * heads * 4);
+  l.dot = take(ring_form ? fresh * all * 4 : 0);
+  l.w = take(mode >= 3 ? heads * fresh8 * all16 * 2 : mode == 0 ? heads * fresh * all * 4 : 0);
+  l.e = take(heads * fresh * 4);
+  l.bytes = at;
+  return l;
+}
+
+// Copies `rows` rows of `n` contiguous elements into shared memory, `stride` apart, row r from
+// from(r); 16 bytes at a time where every row allows it.  also(r), where not null, gets
+// the same elements.
+template <typename IT, typename From, typename Also>
+__device__ __forceinline__ void stage_rows(IT* to, int stride, int rows, int n, bool wide, From from, Also also) {
+  constexpr int V = 16 / sizeof(IT);
+  if (wide) {
+    const int nv = n / V;
+    for (int i = threadIdx.x; i < rows * nv; i += kTokThreads) {
+      const int r = i / nv, k = i - r * nv;
+      const uint4 v = *reinterpret_cast<const uint4*>(from(r) + k * V);
+      *reinterpret_cast<uint4*>(to + r * stride + k * V) = v;
+      if (IT* a = also(r)) *reinterpret_cast<uint4*>(a + k * V) = v;
+    }
+  } else {
+    for (int i = threadIdx.x; i < rows * n; i += kTokThreads) {
+      const int r = i / n, k = i - r * n;
+      const IT v = from(r)[k];
+      to[r * stride + k] = v;
+      if (IT* a = also(r)) a[k] = v;
+    }
+  }
+}
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+// The eight elements of a lane's load as bf16 pairs, exactly.
+template <int SF>
+__device__ __forceinline__ void as_bf16(const Raw<SF>& r, uint32_t (&v)[4]) {
+  if constexpr (SF == RSM_BF16) {
+    v[0] = r.v.x, v[1] = r.v.y, v[2] = r.v.z, v[3] = r.v.w;
+  } else {
+    float2 f[4];
+    unpack<SF>(r, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = rsm::pack_bf16x2(f[i].x, f[i].y);
+  }
+}
+
+// D += A B: 16 rows x 16 k, 16 k x 8 columns, bf16 in, fp32 sums
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// MODE: 0 the ring form, 1 one new token a request, state to state, 2 several; 3
+// and 4 the ring form on the tensor cores, up to 8 and up to 16 new tokens.
 template <typename IT, int SF, int MODE>
-__global__ void __launch_bounds__(kTokThreads, MODE == 2 ? 2 : 3) ssm_token_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MODE == 2 || MODE == 4 ? 2 : 3) ssm_token_kernel(const __grid_constant__ Params p) {
   constexpr int ES = SF == RSM_F32 ? 4 : (SF == RSM_BF16 || SF == RSM_F16) ? 2 : 1;
-  constexpr int D = 64, N = 128;
-  constexpr bool STEP = MODE != 0;
-  __shared__ __align__(16) float sC[kTokMaxNew][N];
-  __shared__ __align__(16) float sB[STEP ? kTokMaxNew : 1][N];
-  __shared__ float sdot[STEP ? 1 : kTokMaxNew][kTokMaxAll];
+  constexpr int D = kTokD, N = kTokN;
+  constexpr bool STEP = MODE == 1 || MODE == 2;
+  constexpr bool MMA = MODE >= 3;
+  constexpr int NT = MODE == 4 ? 2 : 1;  // eights of new tokens
+  extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hpg = p.H / p.G, per = p.heads_per_cta, parts = (hpg + per - 1) / per;
   const uint32_t bg = blockIdx.x / static_cast<uint32_t>(parts);
   const int part = static_cast<int>(blockIdx.x - bg * static_cast<uint32_t>(parts));
   const int b = static_cast<int>(bg / static_cast<uint32_t>(p.G)), g = static_cast<int>(bg - static_cast<uint32_t>(b) * p.G);
-  const int h0 = g * hpg + part * per, h1 = min(h0 + per, (g + 1) * hpg);
+  const int h0 = g * hpg + part * per, nh = min(per, (g + 1) * hpg - h0);
   const int T = p.window;
   const bool say = g == 0 && part == 0 && tid == 0;
 
@@ -147,98 +239,230 @@ __global__ void __launch_bounds__(kTokThreads, MODE == 2 ? 2 : 3) ssm_token_kern
   } else if (live) {
     ring0 = __ldg(p.ring_start + b);
     n_ring = __ldg(p.ring_len + b);
-    uint32_t bad = 0;
-    if (ring0 < 0 || ring0 >= p.R) bad |= RSM_STATUS_BAD_RING_START;
-    if (n_ring < 0 || n_ring > p.R - T || n_ring > kTokMaxAll - T) bad |= RSM_STATUS_BAD_PREFIX_LEN;
-    if (say) flag(p.status, bad);
-    live = bad == 0;
   }
-  IT* out = static_cast<IT*>(p.out) + static_cast<int64_t>(b) * p.out_bs;
+  // this lane's eight columns of its warp's row pairs, in a head's tile (tensor
+  // cores: rows lane / 4 and that + 8, columns 8 (lane % 4) on, and 32, 64, 96 further)
+  const int row0 = kTokRows * (warp & 3) + (MMA ? lane >> 2 : lane >> 4);
+  const int64_t off = static_cast<int64_t>(row0 * N + 8 * (MMA ? lane & 3 : lane & 15)) * ES + h0 * (static_cast<int64_t>(D) * N * ES);
+  constexpr int64_t kTileBytes = static_cast<int64_t>(D) * N * ES;
+  const unsigned char* from = static_cast<const unsigned char*>(p.state) + src * p.state_ss * ES + off;
+  Raw<SF> raw[kTokLoads];
+  auto load_head = [&](int hl) {
+    if (hl < nh) {
+#pragma unroll
+      for (int i = 0; i < kTokLoads; ++i)
+        load_raw<SF>(raw[i], from + hl * kTileBytes + (MMA ? (i & 1) * (8 * N * ES) + (i >> 1) * (32 * ES) : i * (2 * N * ES)));
+    }
+  };
+  if (live) load_head(warp >> 2);
+  if constexpr (!STEP) {
+    if (live) {
+      uint32_t bad = 0;
+      if (ring0 < 0 || ring0 >= p.R) bad |= RSM_STATUS_BAD_RING_START;
+      if (n_ring < 0 || n_ring > p.R - T || n_ring > kTokMaxAll - T) bad |= RSM_STATUS_BAD_PREFIX_LEN;
+      if (say) flag(p.status, bad);
+      live = bad == 0;
+    }
+  }
+  IT* out = static_cast<IT*>(p.out) + static_cast<int64_t>(b) * p.out_bs + static_cast<int64_t>(h0) * D;
   if (!live) {
-    const int n = (h1 - h0) * D;
-    for (int i = tid; i < T * n; i += kTokThreads) store_in(out + (i / n) * p.out_ts + h0 * D + i % n, 0.0f);
+    const int n = nh * D;
+    for (int i = tid; i < T * n; i += kTokThreads) store_in(out + (i / n) * p.out_ts + i % n, 0.0f);
     return;
   }
 
-  // this lane's eight columns of its warp's row pairs, in a head's tile
-  const int row0 = kTokRows * (warp & 3) + (lane >> 4);
-  const int64_t off = static_cast<int64_t>(row0 * N + 8 * (lane & 15)) * ES;
-  const int64_t tile = static_cast<int64_t>(D) * N * ES;
-  const unsigned char* from = static_cast<const unsigned char*>(p.state) + src * p.state_ss * ES + off;
-  const int hfirst = h0 + (warp >> 2);
-  Raw<SF> raw[kTokLoads];
-  if (hfirst < h1) {
-#pragma unroll
-    for (int i = 0; i < kTokLoads; ++i) load_raw<SF>(raw[i], from + hfirst * tile + i * (2 * N * ES));
-  }
-
-  // the group's part: C (and B, or the dots B . C) of the tokens
+  // one round of loads for everything but the state
+  const TokLayout l = tok_layout(MODE, sizeof(IT), per, T, p.tokens_max);
+  const int xs = tok_x_row(MODE, nh);
+  float* sC = reinterpret_cast<float*>(smem + l.C);
+  IT* sx = reinterpret_cast<IT*>(smem + l.x);
+  float* sdt = reinterpret_cast<float*>(smem + l.dt);
+  float* se = reinterpret_cast<float*>(smem + l.e);
+  const IT* xn = static_cast<const IT*>(p.x) + static_cast<int64_t>(b) * p.x_bs + static_cast<int64_t>(h0) * D;
   const IT* Bn = static_cast<const IT*>(p.B) + static_cast<int64_t>(b) * p.B_bs + static_cast<int64_t>(g) * N;
   const IT* Cn = static_cast<const IT*>(p.C) + static_cast<int64_t>(b) * p.C_bs + static_cast<int64_t>(g) * N;
-  const IT* Bc = STEP ? nullptr : static_cast<const IT*>(p.B_cache) + src * p.Bc_ss + static_cast<int64_t>(g) * N;
+  const float* dtn = p.dt + static_cast<int64_t>(b) * p.dt_bs + h0;
   const int m = n_ring + T;
-  for (int i = tid; i < T * N; i += kTokThreads) {
-    const int t = i / N, n = i % N;
-    sC[t][n] = load_in(Cn + t * p.C_ts + n);
-    if constexpr (STEP) sB[t][n] = load_in(Bn + t * p.B_ts + n);
-  }
-  if constexpr (!STEP) {
-    for (int s = warp; s < m; s += kTokThreads / 32) {
-      const int64_t ring_row = (ring0 + s) % p.R;
-      const IT* Bs = s < n_ring ? Bc + ring_row * p.G * N : Bn + static_cast<int64_t>(s - n_ring) * p.B_ts;
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = load_in(Bs + lane + 32 * k);
-      if (s >= n_ring && part == 0) {  // a new token's B joins the ring, once for the group
-        IT* to = static_cast<IT*>(p.B_cache) + src * p.Bc_ss + (ring_row * p.G + g) * N;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) store_in(to + lane + 32 * k, v[k]);
-      }
-      for (int t = max(0, s - n_ring); t < T; ++t) {
-        const IT* Ct = Cn + t * p.C_ts;
-        float dot = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) dot = fmaf(v[k], load_in(Ct + lane + 32 * k), dot);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-        if (lane == 0) sdot[t][s] = dot;
-      }
+  for (int i = tid; i < T * N; i += kTokThreads) sC[i] = as_float(Cn[(i / N) * p.C_ts + i % N]);
+  if constexpr (STEP) {
+    float* sB = reinterpret_cast<float*>(smem + l.B);
+    for (int i = tid; i < T * N; i += kTokThreads) sB[i] = as_float(Bn[(i / N) * p.B_ts + i % N]);
+    stage_rows(sx, xs, T, nh * D, p.wide != 0, [&](int r) { return xn + r * p.x_ts; }, [](int) -> IT* { return nullptr; });
+    for (int i = tid; i < T * nh; i += kTokThreads) sdt[i] = __ldg(dtn + (i / nh) * p.dt_ts + i % nh);
+  } else {
+    auto ring_row = [&](int s) {
+      const int r = ring0 + s;
+      return static_cast<int64_t>(r < p.R ? r : r - p.R);  // ring0 < R, s < R
+    };
+    IT* xc = static_cast<IT*>(p.x_cache) + src * p.xc_ss + static_cast<int64_t>(h0) * D;
+    IT* Bc = static_cast<IT*>(p.B_cache) + src * p.Bc_ss + static_cast<int64_t>(g) * N;
+    float* dtc = p.dt_cache + src * p.dtc_ss + h0;
+    const int64_t xrow = static_cast<int64_t>(p.H) * D, Brow = static_cast<int64_t>(p.G) * N;
+    stage_rows(sx, xs, m, nh * D, p.wide != 0,
+               [&](int s) -> const IT* { return s < n_ring ? xc + ring_row(s) * xrow : xn + (s - n_ring) * p.x_ts; },
+               [&](int s) -> IT* { return s < n_ring ? nullptr : xc + ring_row(s) * xrow; });
+    stage_rows(reinterpret_cast<IT*>(smem + l.B), N, m, N, p.wide != 0,
+               [&](int s) -> const IT* { return s < n_ring ? Bc + ring_row(s) * Brow : Bn + (s - n_ring) * p.B_ts; },
+               [&](int s) -> IT* { return s < n_ring || part != 0 ? nullptr : Bc + ring_row(s) * Brow; });
+    for (int i = tid; i < m * nh; i += kTokThreads) {
+      const int s = i / nh, hl = i - s * nh;
+      float* ring = dtc + ring_row(s) * p.H + hl;
+      const float v = s < n_ring ? *ring : __ldg(dtn + (s - n_ring) * p.dt_ts + hl);
+      sdt[i] = v;
+      if (s >= n_ring) *ring = v;
+    }
+    if constexpr (MMA) {  // the rest of the last k-step: weight 0, and so finite
+      const int rest = ((m + 15) & ~15) - m;
+      for (int i = tid; i < rest * xs; i += kTokThreads) sx[m * xs + i] = IT(0);
     }
   }
   __syncthreads();
 
+  if constexpr (!STEP) {
+    // the dots B_s . C_t, four lanes each
+    const IT* sB = reinterpret_cast<const IT*>(smem + l.B);
+    float* sdot = reinterpret_cast<float*>(smem + l.dot);
+    const int T8 = (T + 7) & ~7, m16 = (m + 15) & ~15;
+    for (int i = tid >> 2; i < ((m * T + 7) & ~7); i += kTokThreads / 4) {  // whole warps
+      const int s = i % m, t = i / m;
+      float dot = 0.0f;
+      if (t < T) {
+#pragma unroll 8
+        for (int k = 0; k < N / 4; ++k) dot = fmaf(as_float(sB[s * N + 4 * k + (tid & 3)]), sC[t * N + 4 * k + (tid & 3)], dot);
+      }
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
+      if ((tid & 3) == 0 && t < T) sdot[t * m + s] = dot;
+    }
+    __syncthreads();
+    // the tokens' weights, a warp per head: token s in lane s % 32's word s / 32
+    for (int hl = warp; hl < nh; hl += kTokThreads / 32) {
+      const float A = __ldg(p.A + h0 + hl), skip = p.D != nullptr ? __ldg(p.D + h0 + hl) : 0.0f;
+      float dt[2], c[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int s = lane + 32 * k;
+        dt[k] = s < m ? sdt[s * nh + hl] : 0.0f;
+        c[k] = dt[k] * A;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float v = __shfl_up_sync(0xFFFFFFFFu, c[k], o);
+          if (lane >= o) c[k] += v;
+        }
+      }
+      c[1] += __shfl_sync(0xFFFFFFFFu, c[0], 31);
+      for (int t = 0; t < (MMA ? T8 : T); ++t) {
+        const int now = n_ring + t;
+        const float ct = __shfl_sync(0xFFFFFFFFu, now < 32 ? c[0] : c[1], now & 31);
+        if (lane == 0 && t < T) se[hl * T + t] = expf(ct);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int s = lane + 32 * k;
+          float w = 0.0f;
+          if (s <= now && t < T) w = fmaf(expf(ct - c[k]) * dt[k], sdot[t * m + s], s == now ? skip : 0.0f);
+          if constexpr (MMA) {
+            if (s < m16) store_in(reinterpret_cast<uint16_t*>(smem + l.w) + (hl * T8 + t) * m16 + s, w);
+          } else {
+            if (s < m) reinterpret_cast<float*>(smem + l.w)[(hl * T + t) * m + s] = w;
+          }
+        }
+      }
+    }
+  } else {
+    for (int i = tid; i < nh * T; i += kTokThreads) se[i] = expf(sdt[(i % T) * nh + i / T] * __ldg(p.A + h0 + i / T));
+  }
+  __syncthreads();
+
+  if constexpr (MMA) {
+    const int gq = lane >> 2, tq = lane & 3, T8 = (T + 7) & ~7, m16 = (m + 15) & ~15;
+    // tokens' C as the second operand: k-steps 2j and 2j + 1 take columns 32 j + 8 tq .. + 7
+    uint32_t cf[NT][4][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int t = 8 * nt + gq;
+          const float2 v = t < T ? *reinterpret_cast<const float2*>(sC + t * N + 32 * jj + 8 * tq + 2 * q) : make_float2(0.0f, 0.0f);
+          cf[nt][jj][q] = rsm::pack_bf16x2(v.x, v.y);
+        }
+    const uint16_t* sw = reinterpret_cast<const uint16_t*>(smem + l.w);
+    // rows of x for ldmatrix: lanes 0-7 tokens 0-7, columns 0-7; 8-15 columns 8-15; 16-31 tokens 8-15
+    const uint32_t xm = rsm::smem_addr(sx) + 2u * (((lane & 7) + ((lane >> 4) << 3)) * xs + kTokRows * (warp & 3) + 8 * ((lane >> 3) & 1));
+#pragma unroll 1
+    for (int hl = warp >> 2; hl < nh; hl += 2) {
+      float acc[NT][4], ring[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[nt][q] = ring[nt][q] = 0.0f;
+      float scale[2] = {1.0f, 1.0f};
+      if constexpr (ES == 1) {
+        const float* sc = p.scale + src * p.scale_ss + static_cast<int64_t>(h0 + hl) * D + kTokRows * (warp & 3) + gq;
+        scale[0] = __ldg(sc);
+        scale[1] = __ldg(sc + 8);
+      }
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        uint32_t lo[4], hi[4];  // rows gq and gq + 8
+        as_bf16<SF>(raw[2 * jj], lo);
+        as_bf16<SF>(raw[2 * jj + 1], hi);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(acc[nt], lo[0], hi[0], lo[1], hi[1], cf[nt][jj][0], cf[nt][jj][1]);
+          mma16816(acc[nt], lo[2], hi[2], lo[3], hi[3], cf[nt][jj][2], cf[nt][jj][3]);
+        }
+      }
+      load_head(hl + 2);
+#pragma unroll 1
+      for (int s0 = 0; s0 < m; s0 += 16) {
+        uint32_t a0, a1, a2, a3;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                     : "r"(xm + 2u * (s0 * xs + hl * D)));
+        const uint16_t* wt = sw + (hl * T8 + gq) * m16 + s0 + 2 * tq;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816(ring[nt], a0, a1, a2, a3, *reinterpret_cast<const uint32_t*>(wt + nt * 8 * m16),
+                   *reinterpret_cast<const uint32_t*>(wt + nt * 8 * m16 + 8));
+      }
+      IT* outh = out + hl * D + kTokRows * (warp & 3) + gq;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int t = 8 * nt + 2 * tq + (q & 1);
+          if (t < T) store_in(outh + t * p.out_ts + 8 * (q >> 1), fmaf(acc[nt][q], se[hl * T + t] * scale[q >> 1], ring[nt][q]));
+        }
+    }
+    return;
+  }
   const int r = 2 * ((lane >> 1) & 7) + (lane >> 4);      // the row this lane ends with
   const int d = kTokRows * (warp & 3) + r, odd = lane & 1;
-  const IT* xn = static_cast<const IT*>(p.x) + static_cast<int64_t>(b) * p.x_bs;
-  const float* dtn = p.dt + static_cast<int64_t>(b) * p.dt_bs;
-
-  for (int h = hfirst; h < h1; h += 2) {
-    const float A = __ldg(p.A + h);
-    const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
-    const bool more = h + 2 < h1;
-    auto load_next = [&] {
-      if (more) {
-#pragma unroll
-        for (int i = 0; i < kTokLoads; ++i) load_raw<SF>(raw[i], from + (h + 2) * tile + i * (2 * N * ES));
-      }
-    };
+#pragma unroll 1
+  for (int hl = warp >> 2; hl < nh; hl += 2) {
+    IT* outh = out + hl * D + d;
+    const IT* xh = sx + hl * D + d;
     if constexpr (STEP) {
-      unsigned char* to = static_cast<unsigned char*>(p.state) + dst * p.state_ss * ES + off + h * tile;
+      const float* sB = reinterpret_cast<const float*>(smem + l.B);
+      const float skip = p.D != nullptr ? __ldg(p.D + h0 + hl) : 0.0f;
+      unsigned char* to = static_cast<unsigned char*>(p.state) + dst * p.state_ss * ES + off + hl * kTileBytes;
       constexpr int kHold = MODE == 2 ? kTokLoads : 1;  // row pairs held as fp32
       float2 S[kHold][4];
       if constexpr (MODE == 2) {
 #pragma unroll
         for (int i = 0; i < kTokLoads; ++i) unpack<SF>(raw[i], S[i]);
-        if constexpr (ES < 4) load_next();
       }
 #pragma unroll 1
       for (int t = 0; t < T; ++t) {
-        const float dt = __ldg(dtn + t * p.dt_ts + h), x = load_in(xn + t * p.x_ts + static_cast<int64_t>(h) * D + d);
-        const float a = expf(dt * A), u = dt * x;
-        const float4 b0 = *reinterpret_cast<const float4*>(&sB[t][8 * (lane & 15)]);
-        const float4 b1 = *reinterpret_cast<const float4*>(&sB[t][8 * (lane & 15) + 4]);
-        const float4 c0 = *reinterpret_cast<const float4*>(&sC[t][8 * (lane & 15)]);
-        const float4 c1 = *reinterpret_cast<const float4*>(&sC[t][8 * (lane & 15) + 4]);
+        const float a = se[hl * T + t], x = as_float(xh[t * xs]), u = sdt[t * nh + hl] * x;
+        const float4* Bt = reinterpret_cast<const float4*>(sB + t * N + 8 * (lane & 15));
+        const float4* Ct = reinterpret_cast<const float4*>(sC + t * N + 8 * (lane & 15));
+        const float4 b0 = Bt[0], b1 = Bt[1], c0 = Ct[0], c1 = Ct[1];
         const float2 B2[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y), make_float2(b1.z, b1.w)};
         const float2 C2[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y), make_float2(c1.z, c1.w)};
         const float2 a2 = make_float2(a, a);
@@ -259,59 +483,26 @@ __global__ void __launch_bounds__(kTokThreads, MODE == 2 ? 2 : 3) ssm_token_kern
           if constexpr (MODE == 1)
             if (dst >= 0) store_eight<SF>(to + i * (2 * N * ES), S[0]);
         }
-        if constexpr (MODE == 1) load_next();
+        if constexpr (MODE == 1) load_head(hl + 2);
         float y = fold8(acc, lane);
         y += __shfl_xor_sync(0xFFFFFFFFu, y, 1);
-        if (!odd) store_in(out + t * p.out_ts + static_cast<int64_t>(h) * D + d, fmaf(skip, x, y));
+        if (!odd) store_in(outh + t * p.out_ts, fmaf(skip, x, y));
       }
       if constexpr (MODE == 2) {
         if (dst >= 0) {
 #pragma unroll
           for (int i = 0; i < kTokLoads; ++i) store_eight<SF>(to + i * (2 * N * ES), S[i]);
         }
-        if constexpr (ES == 4) load_next();
+        load_head(hl + 2);
       }
-    } else {
-      // the tokens' decays: token s in lane s % 32's word s / 32
-      float dts[2], c[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int s = lane + 32 * k;
-        dts[k] = 0.0f;
-        if (s < m) {
-          float* ring = p.dt_cache + src * p.dtc_ss + static_cast<int64_t>((ring0 + s) % p.R) * p.H + h;
-          dts[k] = s < n_ring ? __ldg(ring) : __ldg(dtn + static_cast<int64_t>(s - n_ring) * p.dt_ts + h);
-          if (s >= n_ring && (warp & 3) == 0) *ring = dts[k];
-        }
-        c[k] = dts[k] * A;
-      }
+    } else if constexpr (MODE == 0) {
+      const float* sw = reinterpret_cast<const float*>(smem + l.w);
       const float scale = (SF == RSM_I8 || SF == RSM_FP8_E4M3)
-                              ? __ldg(p.scale + src * p.scale_ss + static_cast<int64_t>(h) * D + d) : 1.0f;
-      // the first tokens' x of this lane's row; lanes 2i, 2i + 1 take every other token
-      const IT* xr = static_cast<const IT*>(p.x_cache) + src * p.xc_ss + static_cast<int64_t>(h) * D + d;
-      auto x_of = [&](int s) -> float {
-        return s < n_ring ? load_in(xr + static_cast<int64_t>((ring0 + s) % p.R) * p.H * D)
-                          : load_in(xn + static_cast<int64_t>(s - n_ring) * p.x_ts + static_cast<int64_t>(h) * D + d);
-      };
-      constexpr int kHeld = 4;  // tokens of a lane held in registers
-      float x[kHeld];
-#pragma unroll
-      for (int k = 0; k < kHeld; ++k) x[k] = 2 * k + odd < m ? x_of(2 * k + odd) : 0.0f;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float v = __shfl_up_sync(0xFFFFFFFFu, c[k], o);
-          if (lane >= o) c[k] += v;
-        }
-      }
-      c[1] += __shfl_sync(0xFFFFFFFFu, c[0], 31);
-
+                              ? __ldg(p.scale + src * p.scale_ss + static_cast<int64_t>(h0 + hl) * D + d) : 1.0f;
 #pragma unroll 1
       for (int t = 0; t < T; ++t) {
-        const int now = n_ring + t;
-        const float4 c0 = *reinterpret_cast<const float4*>(&sC[t][8 * (lane & 15)]);
-        const float4 c1 = *reinterpret_cast<const float4*>(&sC[t][8 * (lane & 15) + 4]);
+        const float4* Ct = reinterpret_cast<const float4*>(sC + t * N + 8 * (lane & 15));
+        const float4 c0 = Ct[0], c1 = Ct[1];
         const float2 C2[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y), make_float2(c1.z, c1.w)};
         float acc[8];
 #pragma unroll
@@ -323,32 +514,12 @@ __global__ void __launch_bounds__(kTokThreads, MODE == 2 ? 2 : 3) ssm_token_kern
           for (int q = 1; q < 4; ++q) sum = __ffma2_rn(S[q], C2[q], sum);
           acc[i] = sum.x + sum.y;
         }
-        if (t == T - 1) load_next();  // the rows have had their last use
-        const float ct = __shfl_sync(0xFFFFFFFFu, now < 32 ? c[0] : c[1], now & 31);
-        float y = fold8(acc, lane) * (expf(ct) * scale);
-        float w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int s = lane + 32 * k;
-          w[k] = s <= now ? expf(ct - c[k]) * dts[k] * sdot[t][s] : 0.0f;
-          if (s == now) w[k] += skip;
-        }
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-          const float ws = __shfl_sync(0xFFFFFFFFu, w[0], 2 * k + odd);
-          y = 2 * k + odd <= now ? fmaf(ws, x[k], y) : y;
-        }
-        for (int k = kHeld; 2 * k <= now; ++k) {
-          const int s = 2 * k + odd;
-          const float ws = __shfl_sync(0xFFFFFFFFu, s < 32 ? w[0] : w[1], s & 31);
-          if (s <= now) y = fmaf(ws, x_of(s), y);
-        }
+        if (t == T - 1) load_head(hl + 2);  // the rows have had their last use
+        float y = fold8(acc, lane) * (se[hl * T + t] * scale);
+        const float* wt = sw + (hl * T + t) * m;
+        for (int s = odd; s <= n_ring + t; s += 2) y = fmaf(wt[s], as_float(xh[s * xs]), y);
         y += __shfl_xor_sync(0xFFFFFFFFu, y, 1);
-        if (!odd) store_in(out + t * p.out_ts + static_cast<int64_t>(h) * D + d, y);
-        // the token's x joins the ring
-        if (odd == (now & 1))
-          store_in(const_cast<IT*>(xr) + static_cast<int64_t>((ring0 + now) % p.R) * p.H * D,
-                   load_in(xn + t * p.x_ts + static_cast<int64_t>(h) * D + d));
+        if (!odd) store_in(outh + t * p.out_ts, y);
       }
     }
   }
