@@ -322,19 +322,19 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (p.units == 1 || bs * ie % 16 == 0) && (p.window == 1 || ts * ie % 16 == 0);
   };
   p.wide = even(p.x, p.x_bs, p.x_ts) &&
-           (step || (even(p.B, p.B_bs, p.B_ts) && reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
+           (step || (even(p.B, p.B_bs, p.B_ts) && even(p.C, p.C_bs, p.C_ts) && reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(p.B_cache) % 16 == 0 && p.Bc_ss * ie % 16 == 0));
   // A CTA works on two heads at a time.  Many heads in all: as many a CTA, up to
   // sixteen, as leave eight CTAs an SM, since a CTA's first loads wait for nothing to
   // do meanwhile; few: two a CTA, to spread over the SMs.  Long rings take fewer, to
-  // fit 64 KB of shared memory.
+  // leave three CTAs an SM.
   int per = 2;
   while (per < 16 && static_cast<int64_t>(p.units) * p.H / (2 * per) >= 8 * static_cast<int64_t>(sms)) per *= 2;
   per = std::min(per, hpg);
   const int mode = step ? (p.window == 1 ? 1 : 2)
                    : input_dtype == RSM_BF16 && p.state_dtype != RSM_F32 && p.state_dtype != RSM_F16 ? (p.window <= 8 ? 3 : 4) : 0;
   auto smem = [&](int n) { return ssm::token_smem(mode, ie, n, p.window, p.tokens_max); };
-  while (per > 1 && smem(per) > 64 * 1024) per = (per + 1) / 2;
+  while (per > 1 && smem(per) > 75 * 1024) per = (per + 1) / 2;
   p.heads_per_cta = per;
   const int64_t parts = (hpg + per - 1) / per, grid = static_cast<int64_t>(p.units) * p.G * parts;
   const void* fn = ssm::token_kernel(input_dtype, p.state_dtype, mode);

@@ -15,10 +15,10 @@
 //
 // The ring form with bf16 inputs and bf16, int8 or fp8 states takes its products on
 // the tensor cores (mma.sync m16n8k16: 16 rows, 8 tokens; such states' elements are
-// exact in bf16, so only the weights of the ring's tokens are rounded).  A lane's 16
-// bytes of a row serve two k-steps, k being numbered to suit.  Without it a state
-// element costs an unpacking, an FMA a token and its share of a reduction: 88% of the
-// memory's rate at one token on bf16 states, 21% at four on int8 ones.
+// exact in bf16, so only the weights of the ring's tokens are rounded).  A lane takes 16
+// bytes of a row at a time, k being numbered to suit.  (Rows through shared memory by
+// bulk copies, two or three heads ahead, measured slower: what they take of it is CTAs,
+// and with them the heads in whose time another CTA's staging passes.)
 //
 // Otherwise a lane holds eight dstate columns of eight rows: sixteen lanes to a
 // row, a 16-byte load (16-bit states) an instruction and two rows.  Sums over a
@@ -136,9 +136,10 @@ __device__ __forceinline__ float fold8(float (&v)[8], int lane) {
 // Shared memory of a CTA, in bytes: what its heads' tokens need, staged by one
 // round of loads; `all` is the most tokens a request can have (ring and new).
 struct TokLayout {
-  uint32_t C, B, x, dt, dot, w, e, bytes;
+  uint32_t C, B, x, dt, c, dot, w, e, bytes;
 };
-// elements between staged rows of x
+// elements between staged rows of B, and of x: on the tensor cores 16 bytes off a multiple of 128
+__host__ __device__ constexpr int tok_B_row(int mode) { return kTokN + (mode >= 3 ? 8 : 0); }
 __host__ __device__ constexpr int tok_x_row(int mode, int heads) { return heads * kTokD + (mode >= 3 ? 8 : 0); }
 __host__ __device__ inline TokLayout tok_layout(int mode, int input_bytes, int heads, int fresh, int all) {
   const bool ring_form = mode == 0 || mode >= 3;
@@ -150,11 +151,12 @@ __host__ __device__ inline TokLayout tok_layout(int mode, int input_bytes, int h
     return o;
   };
   const uint32_t all16 = (all + 15u) & ~15u, fresh8 = (fresh + 7u) & ~7u;
-  l.C = take(fresh * kTokN * 4);
-  l.B = take(all * kTokN * (ring_form ? input_bytes : 4));  // ring form: as stored, for the dots alone
-  // tensor cores: whole k-steps, rows 16 bytes off a multiple of 128
+  // (ring form: B as stored, for the dots alone; tensor cores: C too)
+  l.C = take(mode >= 3 ? fresh * tok_B_row(mode) * input_bytes : fresh * kTokN * 4);
+  l.B = take((mode >= 3 ? all16 * tok_B_row(mode) : all * kTokN) * (ring_form ? input_bytes : 4));
   l.x = take(mode >= 3 ? all16 * tok_x_row(mode, heads) * input_bytes : all * heads * kTokD * input_bytes);
   l.dt = take(all * heads * 4);
+  l.c = take(ring_form ? all * heads * 4 : 0);
   l.dot = take(ring_form ? fresh * all * 4 : 0);
   l.w = take(mode >= 3 ? heads * fresh8 * all16 * 2 : mode == 0 ? heads * fresh * all * 4 : 0);
   l.e = take(heads * fresh * 4);
@@ -162,43 +164,63 @@ __host__ __device__ inline TokLayout tok_layout(int mode, int input_bytes, int h
   return l;
 }
 
-// Copies `rows` rows of `n` contiguous elements into shared memory, `stride` apart, row r from
-// from(r); 16 bytes at a time where every row allows it.  also(r), where not null, gets
-// the same elements.
-template <typename IT, typename From, typename Also>
-__device__ __forceinline__ void stage_rows(IT* to, int stride, int rows, int n, bool wide, From from, Also also) {
+// Copies `rows` rows of `n` contiguous elements into shared memory, `stride` apart, a warp
+// a row, row r from from(r): asynchronously, 16 bytes at a time, where every row allows it.
+template <typename IT, typename From>
+__device__ __forceinline__ void stage_rows(IT* to, int stride, int rows, int n, bool wide, From from) {
   constexpr int V = 16 / sizeof(IT);
-  if (wide) {
-    const int nv = n / V;
-    for (int i = threadIdx.x; i < rows * nv; i += kTokThreads) {
-      const int r = i / nv, k = i - r * nv;
-      const uint4 v = *reinterpret_cast<const uint4*>(from(r) + k * V);
-      *reinterpret_cast<uint4*>(to + r * stride + k * V) = v;
-      if (IT* a = also(r)) *reinterpret_cast<uint4*>(a + k * V) = v;
-    }
-  } else {
-    for (int i = threadIdx.x; i < rows * n; i += kTokThreads) {
-      const int r = i / n, k = i - r * n;
-      const IT v = from(r)[k];
-      to[r * stride + k] = v;
-      if (IT* a = also(r)) a[k] = v;
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < rows; r += kTokThreads / 32) {
+    const IT* f = from(r);
+    IT* t = to + r * stride;
+    if (wide) {
+      for (int k = lane * V; k < n; k += 32 * V) rsm::cp_async_16(rsm::smem_addr(t + k), f + k);
+    } else {
+      for (int k = lane; k < n; k += 32) t[k] = f[k];
     }
   }
 }
+// ... and out of it, to to(r)
+template <typename IT, typename To>
+__device__ __forceinline__ void put_rows(const IT* from, int stride, int rows, int n, bool wide, To to) {
+  constexpr int V = 16 / sizeof(IT);
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < rows; r += kTokThreads / 32) {
+    const IT* f = from + r * stride;
+    IT* t = to(r);
+    if (wide) {
+      for (int k = lane * V; k < n; k += 32 * V) *reinterpret_cast<uint4*>(t + k) = *reinterpret_cast<const uint4*>(f + k);
+    } else {
+      for (int k = lane; k < n; k += 32) t[k] = f[k];
+    }
+  }
+}
+__device__ __forceinline__ void staged() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 
-// The eight elements of a lane's load as bf16 pairs, exactly.
+// A lane's share of a row, 32 elements, as the bf16 pairs of eight k-steps, two a step:
+// element pair_at(i, tq) and its neighbour (int8: the next but one) in pair i.
+//
+// An int8 code is 128 + its low seven bits, which is bf16 0x4300 with those for its
+// mantissa, and -128, or -256 where it is negative: 3.5 instructions a pair against 5
+// through fp32.  Its pairs are bytes 0 and 2, then 1 and 3, of each word.
 template <int SF>
-__device__ __forceinline__ void as_bf16(const Raw<SF>& r, uint32_t (&v)[4]) {
-  if constexpr (SF == RSM_BF16) {
-    v[0] = r.v.x, v[1] = r.v.y, v[2] = r.v.z, v[3] = r.v.w;
+__device__ __forceinline__ constexpr int pair_at(int i, int tq) {
+  return SF == RSM_BF16 ? 32 * (i >> 2) + 8 * tq + 2 * (i & 3)
+                        : 64 * (i >> 3) + 16 * tq + 4 * ((i >> 1) & 3) + (i & 1) * (SF == RSM_I8 ? 1 : 2);
+}
+template <int SF>
+__device__ __forceinline__ void word_pairs(uint32_t w, uint32_t& a, uint32_t& b) {  // of one-byte states
+  if constexpr (SF == RSM_I8) {
+    const uint32_t u = w >> 8;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"((w & 0x007F007Fu) | 0x43004300u), "r"((w & 0x00800080u) | 0xC300C300u));
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"((u & 0x007F007Fu) | 0x43004300u), "r"((u & 0x00800080u) | 0xC300C300u));
   } else {
-    float2 f[4];
-    unpack<SF>(r, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = rsm::pack_bf16x2(f[i].x, f[i].y);
+    const float2 lo = rsm::e4m3x2_to_f32(w & 0xFFFFu), hi = rsm::e4m3x2_to_f32(w >> 16);
+    a = rsm::pack_bf16x2(lo.x, lo.y);
+    b = rsm::pack_bf16x2(hi.x, hi.y);
   }
 }
 
@@ -231,27 +253,40 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
   const int T = p.window;
   const bool say = g == 0 && part == 0 && tid == 0;
 
-  const int src = slot_of(p, p.src, b, say);
-  int dst = src, n_ring = 0, ring0 = 0;
-  bool live = src >= 0;
-  if constexpr (STEP) {
-    if (p.dst != nullptr) dst = slot_of(p, p.dst, b, say);
-  } else if (live) {
+  int n_ring = 0, ring0 = 0;
+  if constexpr (!STEP) {
     ring0 = __ldg(p.ring_start + b);
     n_ring = __ldg(p.ring_len + b);
   }
+  const int src = slot_of(p, p.src, b, say);
+  int dst = src;
+  bool live = src >= 0;
+  if constexpr (STEP) {
+    if (p.dst != nullptr) dst = slot_of(p, p.dst, b, say);
+  }
   // this lane's eight columns of its warp's row pairs, in a head's tile (tensor
-  // cores: rows lane / 4 and that + 8, columns 8 (lane % 4) on, and 32, 64, 96 further)
+  // cores: 16 bytes of row lane / 4, and of that + 8, and those 64 bytes on)
   const int row0 = kTokRows * (warp & 3) + (MMA ? lane >> 2 : lane >> 4);
-  const int64_t off = static_cast<int64_t>(row0 * N + 8 * (MMA ? lane & 3 : lane & 15)) * ES + h0 * (static_cast<int64_t>(D) * N * ES);
+  const int64_t off = static_cast<int64_t>(row0) * (N * ES) + (MMA ? 16 * (lane & 3) : 8 * ES * (lane & 15)) +
+                      h0 * (static_cast<int64_t>(D) * N * ES);
   constexpr int64_t kTileBytes = static_cast<int64_t>(D) * N * ES;
   const unsigned char* from = static_cast<const unsigned char*>(p.state) + src * p.state_ss * ES + off;
-  Raw<SF> raw[kTokLoads];
+  Raw<SF> raw[MMA ? 1 : kTokLoads];
+  constexpr int kPieces = 2 * ES;
+  uint4 rows[MMA ? 2 : 1][MMA ? kPieces : 1];
   auto load_head = [&](int hl) {
     if (hl < nh) {
+      const unsigned char* at = from + hl * kTileBytes;
+      if constexpr (MMA) {
 #pragma unroll
-      for (int i = 0; i < kTokLoads; ++i)
-        load_raw<SF>(raw[i], from + hl * kTileBytes + (MMA ? (i & 1) * (8 * N * ES) + (i >> 1) * (32 * ES) : i * (2 * N * ES)));
+        for (int c = 0; c < kPieces; ++c) {
+          rows[0][c] = ldg128_once(at + 64 * c);
+          rows[1][c] = ldg128_once(at + 8 * N * ES + 64 * c);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTokLoads; ++i) load_raw<SF>(raw[i], at + i * (2 * N * ES));
+      }
     }
   };
   if (live) load_head(warp >> 2);
@@ -283,13 +318,23 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
   const IT* Cn = static_cast<const IT*>(p.C) + static_cast<int64_t>(b) * p.C_bs + static_cast<int64_t>(g) * N;
   const float* dtn = p.dt + static_cast<int64_t>(b) * p.dt_bs + h0;
   const int m = n_ring + T;
-  for (int i = tid; i < T * N; i += kTokThreads) sC[i] = as_float(Cn[(i / N) * p.C_ts + i % N]);
+  const bool wide = p.wide != 0;
+  if constexpr (!MMA)
+    for (int i = tid; i < T * N; i += kTokThreads) sC[i] = as_float(Cn[(i / N) * p.C_ts + i % N]);
   if constexpr (STEP) {
     float* sB = reinterpret_cast<float*>(smem + l.B);
     for (int i = tid; i < T * N; i += kTokThreads) sB[i] = as_float(Bn[(i / N) * p.B_ts + i % N]);
-    stage_rows(sx, xs, T, nh * D, p.wide != 0, [&](int r) { return xn + r * p.x_ts; }, [](int) -> IT* { return nullptr; });
-    for (int i = tid; i < T * nh; i += kTokThreads) sdt[i] = __ldg(dtn + (i / nh) * p.dt_ts + i % nh);
+    stage_rows(sx, xs, T, nh * D, wide, [&](int r) { return xn + r * p.x_ts; });
+    for (int t = tid >> 4; t < T; t += kTokThreads / 16)  // sixteen lanes a token, one a head
+      if ((tid & 15) < nh) sdt[t * nh + (tid & 15)] = __ldg(dtn + t * p.dt_ts + (tid & 15));
+    staged();
+    __syncthreads();
   } else {
+    constexpr int BS = tok_B_row(MODE);
+    IT* sB = reinterpret_cast<IT*>(smem + l.B);
+    float* sc = reinterpret_cast<float*>(smem + l.c);
+    float* sdot = reinterpret_cast<float*>(smem + l.dot);
+    const int T8 = (T + 7) & ~7, m16 = (m + 15) & ~15;
     auto ring_row = [&](int s) {
       const int r = ring0 + s;
       return static_cast<int64_t>(r < p.R ? r : r - p.R);  // ring0 < R, s < R
@@ -298,98 +343,133 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
     IT* Bc = static_cast<IT*>(p.B_cache) + src * p.Bc_ss + static_cast<int64_t>(g) * N;
     float* dtc = p.dt_cache + src * p.dtc_ss + h0;
     const int64_t xrow = static_cast<int64_t>(p.H) * D, Brow = static_cast<int64_t>(p.G) * N;
-    stage_rows(sx, xs, m, nh * D, p.wide != 0,
-               [&](int s) -> const IT* { return s < n_ring ? xc + ring_row(s) * xrow : xn + (s - n_ring) * p.x_ts; },
-               [&](int s) -> IT* { return s < n_ring ? nullptr : xc + ring_row(s) * xrow; });
-    stage_rows(reinterpret_cast<IT*>(smem + l.B), N, m, N, p.wide != 0,
-               [&](int s) -> const IT* { return s < n_ring ? Bc + ring_row(s) * Brow : Bn + (s - n_ring) * p.B_ts; },
-               [&](int s) -> IT* { return s < n_ring || part != 0 ? nullptr : Bc + ring_row(s) * Brow; });
-    for (int i = tid; i < m * nh; i += kTokThreads) {
-      const int s = i / nh, hl = i - s * nh;
-      float* ring = dtc + ring_row(s) * p.H + hl;
-      const float v = s < n_ring ? *ring : __ldg(dtn + (s - n_ring) * p.dt_ts + hl);
-      sdt[i] = v;
-      if (s >= n_ring) *ring = v;
-    }
-    if constexpr (MMA) {  // the rest of the last k-step: weight 0, and so finite
-      const int rest = ((m + 15) & ~15) - m;
-      for (int i = tid; i < rest * xs; i += kTokThreads) sx[m * xs + i] = IT(0);
-    }
-  }
-  __syncthreads();
+    stage_rows(sx, xs, m, nh * D, wide,
+               [&](int s) -> const IT* { return s < n_ring ? xc + ring_row(s) * xrow : xn + (s - n_ring) * p.x_ts; });
+    stage_rows(sB, BS, m, N, wide,
+               [&](int s) -> const IT* { return s < n_ring ? Bc + ring_row(s) * Brow : Bn + (s - n_ring) * p.B_ts; });
+    if constexpr (MMA) stage_rows(reinterpret_cast<IT*>(smem + l.C), BS, T, N, wide, [&](int t) { return Cn + t * p.C_ts; });
+    const int hq = tid & 15;  // sixteen lanes a token, one a head
+    for (int s = tid >> 4; s < m; s += kTokThreads / 16)
+      if (hq < nh)
+        rsm::cp_async_4(rsm::smem_addr(sdt + s * nh + hq), s < n_ring ? dtc + ring_row(s) * p.H + hq : dtn + (s - n_ring) * p.dt_ts + hq);
+    if constexpr (MMA)  // the rest of the last k-step: weight 0, and so finite
+      for (int i = tid; i < (m16 - m) * xs; i += kTokThreads) sx[m * xs + i] = IT(0);
+    staged();
+    __syncthreads();
 
-  if constexpr (!STEP) {
-    // the dots B_s . C_t, four lanes each
-    const IT* sB = reinterpret_cast<const IT*>(smem + l.B);
-    float* sdot = reinterpret_cast<float*>(smem + l.dot);
-    const int T8 = (T + 7) & ~7, m16 = (m + 15) & ~15;
-    for (int i = tid >> 2; i < ((m * T + 7) & ~7); i += kTokThreads / 4) {  // whole warps
-      const int s = i % m, t = i / m;
-      float dot = 0.0f;
-      if (t < T) {
-#pragma unroll 8
-        for (int k = 0; k < N / 4; ++k) dot = fmaf(as_float(sB[s * N + 4 * k + (tid & 3)]), sC[t * N + 4 * k + (tid & 3)], dot);
+    // the new tokens join the ring, B once for the group
+    put_rows(sx + n_ring * xs, xs, T, nh * D, wide, [&](int t) { return xc + ring_row(n_ring + t) * xrow; });
+    if (part == 0) put_rows(sB + n_ring * BS, BS, T, N, wide, [&](int t) { return Bc + ring_row(n_ring + t) * Brow; });
+    for (int t = tid >> 4; t < T; t += kTokThreads / 16)
+      if (hq < nh) dtc[ring_row(n_ring + t) * p.H + hq] = sdt[(n_ring + t) * nh + hq];
+
+    // the decays up to and with each token; the dots B_s . C_t
+    if (hq < nh) {
+      const float A = __ldg(p.A + h0 + hq);
+      for (int s = tid >> 4; s < m; s += kTokThreads / 16) {
+        float sum = 0.0f;
+        for (int k = 0; k <= s; ++k) sum += sdt[k * nh + hq];
+        sc[s * nh + hq] = sum * A;
       }
-      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
-      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
-      if ((tid & 3) == 0 && t < T) sdot[t * m + s] = dot;
+    }
+    if constexpr (MMA) {
+      // sixteen tokens' B a warp against the new tokens' C (rows past m: whatever is there, for dots nobody takes)
+      const IT* sCb = reinterpret_cast<const IT*>(smem + l.C);
+      for (int s0 = 16 * (kTokThreads / 32 - 1 - warp); s0 < m; s0 += 16 * (kTokThreads / 32)) {
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[nt][q] = 0.0f;
+        const uint32_t bm = rsm::smem_addr(sB) + 2u * ((s0 + (lane & 15)) * BS + 8 * (lane >> 4));
+        const IT* ct[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) ct[nt] = sCb + min(8 * nt + (lane >> 2), T - 1) * BS + 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < N; k += 16) {
+          uint32_t a0, a1, a2, a3;
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                       : "r"(bm + 2u * k));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(acc[nt], a0, a1, a2, a3, *reinterpret_cast<const uint32_t*>(ct[nt] + k),
+                     *reinterpret_cast<const uint32_t*>(ct[nt] + k + 8));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int s = s0 + (lane >> 2) + 8 * (q >> 1), t = 8 * nt + 2 * (lane & 3) + (q & 1);
+            if (s < m && t < T) sdot[t * m + s] = acc[nt][q];
+          }
+      }
+    } else {
+      for (int i = tid >> 2; i < ((m * T + 7) & ~7); i += kTokThreads / 4) {  // four lanes a dot, whole warps
+        const int s = i % m, t = i / m;
+        float dot = 0.0f;
+        if (t < T) {
+#pragma unroll 8
+          for (int k = 0; k < N / 4; ++k) dot = fmaf(as_float(sB[s * N + 4 * k + (tid & 3)]), sC[t * N + 4 * k + (tid & 3)], dot);
+        }
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
+        if ((tid & 3) == 0 && t < T) sdot[t * m + s] = dot;
+      }
     }
     __syncthreads();
-    // the tokens' weights, a warp per head: token s in lane s % 32's word s / 32
+
+    // the tokens' weights, a warp per head
     for (int hl = warp; hl < nh; hl += kTokThreads / 32) {
-      const float A = __ldg(p.A + h0 + hl), skip = p.D != nullptr ? __ldg(p.D + h0 + hl) : 0.0f;
-      float dt[2], c[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int s = lane + 32 * k;
-        dt[k] = s < m ? sdt[s * nh + hl] : 0.0f;
-        c[k] = dt[k] * A;
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float v = __shfl_up_sync(0xFFFFFFFFu, c[k], o);
-          if (lane >= o) c[k] += v;
-        }
-      }
-      c[1] += __shfl_sync(0xFFFFFFFFu, c[0], 31);
-      for (int t = 0; t < (MMA ? T8 : T); ++t) {
+      const float skip = p.D != nullptr ? __ldg(p.D + h0 + hl) : 0.0f;
+      auto weight = [&](int s, int t) {
         const int now = n_ring + t;
-        const float ct = __shfl_sync(0xFFFFFFFFu, now < 32 ? c[0] : c[1], now & 31);
-        if (lane == 0 && t < T) se[hl * T + t] = expf(ct);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int s = lane + 32 * k;
-          float w = 0.0f;
-          if (s <= now && t < T) w = fmaf(expf(ct - c[k]) * dt[k], sdot[t * m + s], s == now ? skip : 0.0f);
-          if constexpr (MMA) {
-            if (s < m16) store_in(reinterpret_cast<uint16_t*>(smem + l.w) + (hl * T8 + t) * m16 + s, w);
-          } else {
-            if (s < m) reinterpret_cast<float*>(smem + l.w)[(hl * T + t) * m + s] = w;
-          }
+        if (s > now || t >= T) return 0.0f;
+        return fmaf(__expf(sc[now * nh + hl] - sc[s * nh + hl]) * sdt[s * nh + hl], sdot[t * m + s], s == now ? skip : 0.0f);
+      };
+      for (int t = lane; t < T; t += 32) se[hl * T + t] = __expf(sc[(n_ring + t) * nh + hl]);
+      if constexpr (MMA) {
+        // pairs of tokens, eight lanes to sixteen of them
+        const uint32_t q = m16 >> 4, inv = 65536u / q + 1u;
+        uint32_t* w = reinterpret_cast<uint32_t*>(smem + l.w) + hl * T8 * (m16 >> 1);
+        for (uint32_t i = lane; i < static_cast<uint32_t>(T8 * (m16 >> 1)); i += 32) {
+          const uint32_t t = ((i >> 3) * inv) >> 16, s = 2 * (i - t * (m16 >> 1));
+          w[i] = rsm::pack_bf16x2(weight(s, t), weight(s + 1, t));
         }
+      } else {
+        float* w = reinterpret_cast<float*>(smem + l.w) + hl * T * m;
+        for (int t = 0; t < T; ++t)
+          for (int s = lane; s < m; s += 32) w[t * m + s] = weight(s, t);
       }
     }
-  } else {
-    for (int i = tid; i < nh * T; i += kTokThreads) se[i] = expf(sdt[(i % T) * nh + i / T] * __ldg(p.A + h0 + i / T));
+    __syncthreads();
   }
-  __syncthreads();
+  if constexpr (STEP) {
+    for (int i = tid; i < nh * T; i += kTokThreads) se[i] = expf(sdt[(i % T) * nh + i / T] * __ldg(p.A + h0 + i / T));
+    __syncthreads();
+  }
 
   if constexpr (MMA) {
     const int gq = lane >> 2, tq = lane & 3, T8 = (T + 7) & ~7, m16 = (m + 15) & ~15;
-    // tokens' C as the second operand: k-steps 2j and 2j + 1 take columns 32 j + 8 tq .. + 7
-    uint32_t cf[NT][4][4];
+    uint32_t cf[NT][16];  // tokens' C as the second operand
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int t = 8 * nt + gq;
+      const uint32_t* ct = reinterpret_cast<const uint32_t*>(smem + l.C) + min(t, T - 1) * (tok_B_row(MODE) / 2);
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj)
+      for (int i = 0; i < 16; i += 2) {
+        uint32_t v[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int t = 8 * nt + gq;
-          const float2 v = t < T ? *reinterpret_cast<const float2*>(sC + t * N + 32 * jj + 8 * tq + 2 * q) : make_float2(0.0f, 0.0f);
-          cf[nt][jj][q] = rsm::pack_bf16x2(v.x, v.y);
+        for (int k = 0; k < 2; ++k) v[k] = ct[pair_at<SF>(i + (SF == RSM_I8 ? 0 : k), tq) / 2 + (SF == RSM_I8 ? k : 0)];
+        if constexpr (SF == RSM_I8) {  // elements 0 and 2, 1 and 3 of four
+          const uint32_t even = __byte_perm(v[0], v[1], 0x5410), other = __byte_perm(v[0], v[1], 0x7632);
+          v[0] = even;
+          v[1] = other;
         }
+        cf[nt][i] = t < T ? v[0] : 0u;
+        cf[nt][i + 1] = t < T ? v[1] : 0u;
+      }
+    }
     const uint16_t* sw = reinterpret_cast<const uint16_t*>(smem + l.w);
     // rows of x for ldmatrix: lanes 0-7 tokens 0-7, columns 0-7; 8-15 columns 8-15; 16-31 tokens 8-15
     const uint32_t xm = rsm::smem_addr(sx) + 2u * (((lane & 7) + ((lane >> 4) << 3)) * xs + kTokRows * (warp & 3) + 8 * ((lane >> 3) & 1));
@@ -407,17 +487,28 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
         scale[1] = __ldg(sc + 8);
       }
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        uint32_t lo[4], hi[4];  // rows gq and gq + 8
-        as_bf16<SF>(raw[2 * jj], lo);
-        as_bf16<SF>(raw[2 * jj + 1], hi);
+      for (int c = 0; c < kPieces; ++c) {
+        const uint4 r0 = rows[0][c], r1 = rows[1][c];
+        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+        if constexpr (ES == 2) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(acc[nt], lo[0], hi[0], lo[1], hi[1], cf[nt][jj][0], cf[nt][jj][1]);
-          mma16816(acc[nt], lo[2], hi[2], lo[3], hi[3], cf[nt][jj][2], cf[nt][jj][3]);
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(acc[nt], w0[2 * k], w1[2 * k], w0[2 * k + 1], w1[2 * k + 1], cf[nt][4 * c + 2 * k], cf[nt][4 * c + 2 * k + 1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t a0, a1, a2, a3;
+            word_pairs<SF>(w0[k], a0, a2);
+            word_pairs<SF>(w1[k], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(acc[nt], a0, a1, a2, a3, cf[nt][8 * c + 2 * k], cf[nt][8 * c + 2 * k + 1]);
+          }
         }
       }
-      load_head(hl + 2);
+      load_head(hl + 2);  // the rows have had their use
 #pragma unroll 1
       for (int s0 = 0; s0 < m; s0 += 16) {
         uint32_t a0, a1, a2, a3;
