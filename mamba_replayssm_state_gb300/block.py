@@ -89,6 +89,13 @@ def _raise(name, rc):
 _INPUTS = {torch.bfloat16: _dtype_code(torch.bfloat16), torch.float32: RSM_F32}
 _STATES = {t: _dtype_code(t) for t in (torch.float32, torch.bfloat16, torch.float16, torch.int8, torch.float8_e4m3fn)}
 _I32, _F32 = torch.int32, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+# A decode step makes a few of these calls a layer, so what a call checks it
+# checks first in one expression that the usual tensors pass; only where that
+# fails do the _check functions go over it, and name what is wrong or let it pass
+# (strides of dimensions of one element, for instance).
 
 
 def _need(ok, message):
@@ -96,87 +103,86 @@ def _need(ok, message):
         raise ValueError(message)
 
 
-def _device(x, *others):
-    """The CUDA device index all the tensors are on, which has to be the current one."""
-    d = x.get_device()
-    _need(d >= 0, "tensors must be CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != d:
-            raise ValueError("all tensors must be on one CUDA device")
-    _need(d == torch.cuda.current_device(), "tensors must be on the current CUDA device")
-    return d
+def _check_device(*tensors):
+    """All tensors are on the current CUDA device."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    _need(devices != set() and min(devices) >= 0, "tensors must be CUDA tensors")
+    _need(len(devices) == 1, "all tensors must be on one CUDA device")
+    _need(devices == {torch.cuda.current_device()}, "tensors must be on the current CUDA device")
 
 
-def _stream(stream, device):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _empty(shape, dtype, device, stream):
-    """A result tensor of the stream that the kernels run on."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and int(stream) != torch._C._cuda_getCurrentRawStream(device.index):
-        raise ValueError("a raw stream handle needs the results to be passed in (out=...)")
-    return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _input(t, name, lead, inner, dtype):
-    """Checks a [*lead, *inner] tensor whose inner dimensions are contiguous."""
+def _check_rows(t, name, shape, inner, dtype):
+    """t has the shape, and its last `inner` dimensions are contiguous."""
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (*lead, *inner):
-        raise ValueError(f"{name} must be {[*lead, *inner]}, got {list(t.shape)}")
-    s = t.stride()
-    if (s[-1] != 1 and inner[-1] != 1) or (len(inner) == 2 and s[-2] != inner[1] and inner[0] != 1):
-        raise ValueError(f"{name} must be contiguous in its last {len(inner)} dimension(s)")
-    return s
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    size = 1
+    for n, stride in zip(reversed(shape[len(shape) - inner:]), reversed(t.stride())):
+        if n != 1 and stride != size:
+            raise ValueError(f"{name} must be contiguous in its last {inner} dimension(s)")
+        size *= n
 
 
-def _vector(t, name, n, dtype):
+def _check_vector(t, name, n, dtype):
     if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
-    return t.data_ptr()
+
+
+def _check_tokens(x, dt, A, B, C, D, k):
+    """The token tensors, with k leading dimensions."""
+    _need(x.dtype in _INPUTS, f"x must be bfloat16 or float32, got {x.dtype}")
+    _need(x.dim() == k + 2 and B.dim() == k + 2, f"x and B must have {k + 2} dimensions")
+    lead, heads, groups = x.shape[:k], x.shape[k:], B.shape[k:]
+    _check_rows(x, "x", (*lead, *heads), 2, x.dtype)
+    _check_rows(B, "B", (*lead, *groups), 2, x.dtype)
+    _check_rows(C, "C", (*lead, *groups), 2, x.dtype)
+    _check_rows(dt, "dt", (*lead, heads[0]), 1, _F32)
+    _check_vector(A, "A", heads[0], _F32)
+    if D is not None:
+        _check_vector(D, "D", heads[0], _F32)
+
+
+def _check_state(state, H, dim, N):
+    _need(state.dtype in _STATES, f"unsupported state dtype {state.dtype}")
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dim, N) or not state[0:1].is_contiguous():
+        raise ValueError(f"state must be [slots, {H}, {dim}, {N}] with contiguous slots, got {list(state.shape)}")
+
+
+def _check_out(out, x):
+    if out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError(f"out must be {x.dtype} {list(x.shape)}")
 
 
 def _status(t):
     if t is None:
-        return None
+        return 0
     _need(t.numel() == 1 and t.element_size() == 4, "device_status must be one 32-bit word")
     return t.data_ptr()
 
 
-def _heads(x, dt, A, B, C, D, lead):
-    """Checks the token tensors; (heads, groups, dim, dstate, input code, their strides, A, D)."""
-    k = len(lead)
-    _need(x.dim() == k + 2 and B.dim() == k + 2, f"x and B must have {k + 2} dimensions")
-    code = _INPUTS.get(x.dtype)
-    _need(code is not None, f"x must be bfloat16 or float32, got {x.dtype}")
-    H, dim = x.shape[k:]
-    G, N = B.shape[k:]
-    sx, sB = _input(x, "x", lead, (H, dim), x.dtype), _input(B, "B", lead, (G, N), x.dtype)
-    sC, sdt = _input(C, "C", lead, (G, N), x.dtype), _input(dt, "dt", lead, (H,), _F32)
-    a = _vector(A, "A", H, _F32)
-    d = None if D is None else _vector(D, "D", H, _F32)
-    return H, G, dim, N, code, sx, sB, sC, sdt, a, d
+def _handle(stream, device):
+    """The raw handle of `stream`, or of the current one."""
+    if stream is None:
+        return _raw_stream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _state(state, H, dim, N):
-    code = _STATES.get(state.dtype)
-    _need(code is not None, f"unsupported state dtype {state.dtype}")
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dim, N) or not state[0:1].is_contiguous():
-        raise ValueError(f"state must be [slots, {H}, {dim}, {N}] with contiguous slots, got {list(state.shape)}")
-    return code
+def _new_on(stream, make):
+    """A tensor of the stream that the kernels run on."""
+    if hasattr(stream, "cuda_stream"):
+        with torch.cuda.stream(stream):
+            return make()
+    if int(stream) != _raw_stream(_current_device()):
+        raise ValueError("a raw stream handle needs the results to be passed in (out=...)")
+    return make()
 
 
-def _out(out, x, shape, stream):
-    if out is None:
-        return _empty(shape, x.dtype, x.device, stream)
-    if out.dtype != x.dtype or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out must be {x.dtype} {list(shape)}")
-    return out
+def _like(x, stream):
+    """A contiguous tensor like x."""
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _new_on(stream, lambda: torch.empty_like(x, memory_format=torch.contiguous_format))
 
 
 def ssm_prefill(x, dt, A, B, C, cu_seqlens, state=None, *, initial_slots=None, final_slots=None, D=None,
@@ -188,38 +194,82 @@ def ssm_prefill(x, dt, A, B, C, cu_seqlens, state=None, *, initial_slots=None, f
     Sequence s starts from state[initial_slots[s]] (default: from zero) and
     leaves its state in state[final_slots[s]] (default: nowhere); the pool
     `state` is [slots, H, dim, dstate] fp32, bf16 or fp16.  Returns the outputs,
-    [tokens, H, dim].  `workspace` (optional) is a uint8 CUDA tensor of at least
-    ssm_prefill_workspace_bytes(...) bytes.
+    [tokens, H, dim].  A long call of few sequences needs a workspace, which is
+    allocated where `workspace` (a contiguous uint8 CUDA tensor) is not given.
     """
     lib = _lib or _load()
-    T = x.shape[0]
-    H, G, dim, N, code, sx, sB, sC, sdt, a, d = _heads(x, dt, A, B, C, D, (T,))
-    dev = _device(x, dt, A, B, C, D, cu_seqlens, state, initial_slots, final_slots, out, workspace, device_status)
+    sx, sB, sC, sd = x.stride(), B.stride(), C.stride(), dt.stride()
+    shape, code, dev = x.shape, _INPUTS.get(x.dtype), x.get_device()
+    if not (code is not None and len(shape) == 3 and B.shape == C.shape and len(sB) == 3 and dt.shape == shape[:2]
+            and shape[0] == B.shape[0] and x.dtype is B.dtype and x.dtype is C.dtype and dt.dtype is _F32
+            and A.dtype is _F32 and A.shape == shape[1:2] and A.is_contiguous() and sx[2] == 1 and sx[1] == shape[2]
+            and sB[2] == 1 and sB[1] == B.shape[2] and sC[2] == 1 and sC[1] == B.shape[2] and sd[1] == 1
+            and (D is None or (D.dtype is _F32 and D.shape == shape[1:2] and D.is_contiguous()))):
+        _check_tokens(x, dt, A, B, C, D, 1)
+    T, H, dim = shape
+    G, N = B.shape[1:]
     seqs = cu_seqlens.shape[0] - 1
     _need(seqs >= 0, "cu_seqlens must have at least one entry")
-    _need(state is not None or (initial_slots is None and final_slots is None), "slots need a state pool")
-    sd, ss, slots = (RSM_F32, 0, 0) if state is None else (_state(state, H, dim, N), state.stride(0), state.shape[0])
-    out = _out(out, x, (T, H, dim), stream)
-    so = _input(out, "out", (T,), (H, dim), x.dtype)
-    _need(T < 2 or so[0] >= H * dim, "rows of out overlap")
-    args = [x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), a, d or 0,
-            _vector(cu_seqlens, "cu_seqlens", seqs + 1, _I32), 0 if state is None else state.data_ptr(),
-            0 if initial_slots is None else _vector(initial_slots, "initial_slots", seqs, _I32),
-            0 if final_slots is None else _vector(final_slots, "final_slots", seqs, _I32), out.data_ptr(), 0,
-            _status(device_status) or 0, T, sx[0], sB[0], sC[0], sdt[0], so[0], ss, 0, seqs, slots, H, G, dim, N, sd,
-            code, int(pad_slot_id)]
-    size = lib.rsm_ssm_prefill_workspace(_pack_prefill(*args))
+    if not (dev >= 0 and dev == B.get_device() == C.get_device() == dt.get_device() == A.get_device()
+            == cu_seqlens.get_device() and dev == _current_device()
+            and D is None and state is None and device_status is None and workspace is None and out is None):
+        _check_device(x, dt, A, B, C, D, cu_seqlens, state, initial_slots, final_slots, out, workspace, device_status)
+    _check_vector(cu_seqlens, "cu_seqlens", seqs + 1, _I32)
+    sd_code, ss, slots, ps, pi, pf = RSM_F32, 0, 0, 0, 0, 0
+    if state is not None:
+        _check_state(state, H, dim, N)
+        sd_code, ss, slots, ps = _STATES[state.dtype], state.stride(0), state.shape[0], state.data_ptr()
+    else:
+        _need(initial_slots is None and final_slots is None, "slots need a state pool")
+    if initial_slots is not None:
+        _check_vector(initial_slots, "initial_slots", seqs, _I32)
+        pi = initial_slots.data_ptr()
+    if final_slots is not None:
+        _check_vector(final_slots, "final_slots", seqs, _I32)
+        pf = final_slots.data_ptr()
+    if out is None:
+        out, so = _like(x, stream), H * dim
+    else:
+        _check_out(out, x)
+        _check_rows(out, "out", shape, 2, x.dtype)
+        so = out.stride(0)
+        _need(T < 2 or so >= H * dim, "rows of out overlap")
+    args = [x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A.data_ptr(), 0 if D is None else D.data_ptr(),
+            cu_seqlens.data_ptr(), ps, pi, pf, out.data_ptr(), 0, _status(device_status), T, sx[0], sB[0], sC[0], sd[0],
+            so, ss, 0, seqs, slots, H, G, dim, N, sd_code, code, int(pad_slot_id)]
+    packed = _pack_prefill(*args)
+    size = lib.rsm_ssm_prefill_workspace(packed)
     if size < 0:
         _raise("ssm_prefill", size)
     if size > 0:
         if workspace is None:
-            workspace = _empty((size,), torch.uint8, x.device, stream)
+            make = lambda: torch.empty(size, dtype=torch.uint8, device=x.device)  # noqa: E731
+            workspace = make() if stream is None else _new_on(stream, make)
         _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a contiguous uint8 tensor")
         args[11], args[20] = workspace.data_ptr(), workspace.numel()
-    rc = lib.rsm_ssm_prefill(_pack_prefill(*args), _stream(stream, dev))
+        packed = _pack_prefill(*args)
+    rc = lib.rsm_ssm_prefill(packed, _handle(stream, dev))
     if rc != 0:
         _raise("ssm_prefill", rc)
     return out
+
+
+def _batch(x, dt, A, B, C, D):
+    """Checks the token tensors of running requests, with or without the window dimension; the input code, (batch,
+    window, H, G, dim, dstate) and the batch and token strides of x, B, C and dt."""
+    sx, sB, sC, sd = x.stride(), B.stride(), C.stride(), dt.stride()
+    shape, bshape, code, k = x.shape, B.shape, _INPUTS.get(x.dtype), len(sx) - 2
+    _need(k in (1, 2), "x must be [batch, window, H, dim] or [batch, H, dim]")
+    if not (code is not None and len(sB) == k + 2 and bshape == C.shape and bshape[:k] == shape[:k]
+            and dt.shape == shape[:-1] and x.dtype is B.dtype and x.dtype is C.dtype and dt.dtype is _F32
+            and A.dtype is _F32 and A.shape == shape[k:-1] and A.is_contiguous() and sx[-1] == 1 and sx[-2] == shape[-1]
+            and sB[-1] == 1 and sB[-2] == bshape[-1] and sC[-1] == 1 and sC[-2] == bshape[-1] and sd[-1] == 1
+            and (D is None or (D.dtype is _F32 and D.shape == A.shape and D.is_contiguous()))):
+        _check_tokens(x, dt, A, B, C, D, k)
+    if k == 1:
+        return (code, shape[0], 1, shape[1], bshape[1], shape[2], bshape[2], sx[0], 0, sB[0], 0, sC[0], 0, sd[0], 0)
+    return (code, shape[0], shape[1], shape[2], bshape[2], shape[3], bshape[3], sx[0], sx[1], sB[0], sB[1], sC[0], sC[1],
+            sd[0], sd[1])
 
 
 def ssm_step(state, slots, x, dt, A, B, C, *, dst_slots=None, D=None, pad_slot_id=-1, out=None, device_status=None,
@@ -233,24 +283,40 @@ def ssm_step(state, slots, x, dt, A, B, C, *, dst_slots=None, D=None, pad_slot_i
     x; rows of a request with the pad slot are zero.
     """
     lib = _lib or _load()
-    one = x.dim() == 3
-    if one:
-        x, dt, B, C = x.unsqueeze(1), dt.unsqueeze(1), B.unsqueeze(1), C.unsqueeze(1)
-        out = None if out is None else out.unsqueeze(1)
-    b, T = x.shape[:2]
-    H, G, dim, N, code, sx, sB, sC, sdt, a, d = _heads(x, dt, A, B, C, D, (b, T))
-    dev = _device(x, dt, A, B, C, D, state, slots, dst_slots, out, device_status)
-    sd = _state(state, H, dim, N)
-    out = _out(out, x, (b, T, H, dim), stream)
-    _need(out.is_contiguous(), "out must be contiguous")
+    code, b, T, H, G, dim, N, *strides = _batch(x, dt, A, B, C, D)
+    dev = x.get_device()
+    if not (dev >= 0 and dev == B.get_device() == C.get_device() == dt.get_device() == A.get_device()
+            == state.get_device() == slots.get_device() and dev == _current_device() and device_status is None
+            and (D is None or D.get_device() == dev) and (dst_slots is None or dst_slots.get_device() == dev)
+            and (out is None or out.get_device() == dev)):
+        _check_device(x, dt, A, B, C, D, state, slots, dst_slots, out, device_status)
+    sd = _STATES.get(state.dtype)
+    if not (sd is not None and state.is_contiguous() and state.shape[1:] == (H, dim, N)):
+        _check_state(state, H, dim, N)
+    if not (slots.dtype is _I32 and slots.shape == (b,) and slots.is_contiguous()):
+        _check_vector(slots, "slots", b, _I32)
+    pd = 0
+    if dst_slots is not None:
+        if not (dst_slots.dtype is _I32 and dst_slots.shape == (b,) and dst_slots.is_contiguous()):
+            _check_vector(dst_slots, "dst_slots", b, _I32)
+        pd = dst_slots.data_ptr()
+    if out is None:
+        out = _like(x, stream)
+    else:
+        _check_out(out, x)
+        _need(out.is_contiguous(), "out must be contiguous")
     rc = lib.rsm_ssm_step(_pack_step(
-        x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), a, d or 0, state.data_ptr(),
-        _vector(slots, "slots", b, _I32), 0 if dst_slots is None else _vector(dst_slots, "dst_slots", b, _I32),
-        out.data_ptr(), _status(device_status) or 0, sx[0], sx[1], sB[0], sB[1], sC[0], sC[1], sdt[0], sdt[1],
-        state.stride(0), b, T, state.shape[0], H, G, dim, N, sd, code, int(pad_slot_id)), _stream(stream, dev))
+        x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A.data_ptr(), 0 if D is None else D.data_ptr(),
+        state.data_ptr(), slots.data_ptr(), pd, out.data_ptr(), _status(device_status), *strides, state.stride(0), b, T,
+        state.shape[0], H, G, dim, N, sd, code, int(pad_slot_id)), _handle(stream, dev))
     if rc != 0:
         _raise("ssm_step", rc)
-    return out.squeeze(1) if one else out
+    return out
+
+
+def _check_cache(t, name, shape, dtype):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t[0:1].is_contiguous():
+        raise ValueError(f"{name} must be {dtype} {list(shape)} with contiguous slots")
 
 
 def replayssm_decode(state, slots, x_cache, B_cache, dt_cache, ring_start, ring_len, x, dt, A, B, C, *,
@@ -266,53 +332,77 @@ def replayssm_decode(state, slots, x_cache, B_cache, dt_cache, ring_start, ring_
     Returns the outputs, shaped like x; rows of a skipped request are zero.
     """
     lib = _lib or _load()
-    one = x.dim() == 3
-    if one:
-        x, dt, B, C = x.unsqueeze(1), dt.unsqueeze(1), B.unsqueeze(1), C.unsqueeze(1)
-        out = None if out is None else out.unsqueeze(1)
-    b, T = x.shape[:2]
-    H, G, dim, N, code, sx, sB, sC, sdt, a, d = _heads(x, dt, A, B, C, D, (b, T))
-    dev = _device(x, dt, A, B, C, D, state, slots, x_cache, B_cache, dt_cache, ring_start, ring_len, state_scale, out,
-                  device_status)
-    sd = _state(state, H, dim, N)
-    S = state.shape[0]
-    _need(x_cache.dim() == 4, "x_cache must be [slots, R, H, dim]")
-    R = x_cache.shape[1]
-    for name, t, shape, dtype in (("x_cache", x_cache, (S, R, H, dim), x.dtype), ("B_cache", B_cache, (S, R, G, N), x.dtype),
-                                  ("dt_cache", dt_cache, (S, R, H), _F32)):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t[0:1].is_contiguous():
-            raise ValueError(f"{name} must be {dtype} {list(shape)} with contiguous slots")
-    if state_scale is not None and (state_scale.dtype != _F32 or tuple(state_scale.shape) != (S, H, dim)
-                                    or not state_scale[0:1].is_contiguous()):
-        raise ValueError(f"state_scale must be float32 {[S, H, dim]} with contiguous slots")
-    out = _out(out, x, (b, T, H, dim), stream)
-    _need(out.is_contiguous(), "out must be contiguous")
+    code, b, T, H, G, dim, N, *strides = _batch(x, dt, A, B, C, D)
+    dev = x.get_device()
+    if not (dev >= 0 and dev == B.get_device() == C.get_device() == dt.get_device() == A.get_device()
+            == state.get_device() == slots.get_device() == x_cache.get_device() == B_cache.get_device()
+            == dt_cache.get_device() == ring_start.get_device() == ring_len.get_device() and dev == _current_device()
+            and device_status is None and (D is None or D.get_device() == dev)
+            and (state_scale is None or state_scale.get_device() == dev) and (out is None or out.get_device() == dev)):
+        _check_device(x, dt, A, B, C, D, state, slots, x_cache, B_cache, dt_cache, ring_start, ring_len, state_scale,
+                      out, device_status)
+    sd, sshape, xshape = _STATES.get(state.dtype), state.shape, x_cache.shape
+    if not (sd is not None and state.is_contiguous() and sshape[1:] == (H, dim, N)):
+        _check_state(state, H, dim, N)
+    S = sshape[0]
+    _need(len(xshape) == 4, "x_cache must be [slots, R, H, dim]")
+    R = xshape[1]
+    if not (x_cache.dtype is x.dtype and xshape == (S, R, H, dim) and x_cache.is_contiguous()
+            and B_cache.dtype is x.dtype and B_cache.shape == (S, R, G, N) and B_cache.is_contiguous()
+            and dt_cache.dtype is _F32 and dt_cache.shape == (S, R, H) and dt_cache.is_contiguous()):
+        _check_cache(x_cache, "x_cache", (S, R, H, dim), x.dtype)
+        _check_cache(B_cache, "B_cache", (S, R, G, N), x.dtype)
+        _check_cache(dt_cache, "dt_cache", (S, R, H), _F32)
+    if not (slots.dtype is _I32 and slots.shape == (b,) and slots.is_contiguous()
+            and ring_start.dtype is _I32 and ring_start.shape == (b,) and ring_start.is_contiguous()
+            and ring_len.dtype is _I32 and ring_len.shape == (b,) and ring_len.is_contiguous()):
+        for name, t in (("slots", slots), ("ring_start", ring_start), ("ring_len", ring_len)):
+            _check_vector(t, name, b, _I32)
+    pq, sq = 0, 0
+    if state_scale is not None:
+        _check_cache(state_scale, "state_scale", (S, H, dim), _F32)
+        pq, sq = state_scale.data_ptr(), state_scale.stride(0)
+    if out is None:
+        out = _like(x, stream)
+    else:
+        _check_out(out, x)
+        _need(out.is_contiguous(), "out must be contiguous")
     rc = lib.rsm_replayssm_decode(_pack_decode(
-        x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), a, d or 0, state.data_ptr(),
-        0 if state_scale is None else state_scale.data_ptr(), x_cache.data_ptr(), B_cache.data_ptr(),
-        dt_cache.data_ptr(), _vector(slots, "slots", b, _I32), _vector(ring_start, "ring_start", b, _I32),
-        _vector(ring_len, "ring_len", b, _I32), out.data_ptr(), _status(device_status) or 0, sx[0], sx[1], sB[0],
-        sB[1], sC[0], sC[1], sdt[0], sdt[1], state.stride(0), 0 if state_scale is None else state_scale.stride(0),
-        x_cache.stride(0), B_cache.stride(0), dt_cache.stride(0), b, T, S, H, G, dim, N, R, sd, code,
-        int(pad_slot_id)), _stream(stream, dev))
+        x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A.data_ptr(), 0 if D is None else D.data_ptr(),
+        state.data_ptr(), pq, x_cache.data_ptr(), B_cache.data_ptr(), dt_cache.data_ptr(), slots.data_ptr(),
+        ring_start.data_ptr(), ring_len.data_ptr(), out.data_ptr(), _status(device_status), *strides, state.stride(0), sq,
+        x_cache.stride(0), B_cache.stride(0), dt_cache.stride(0), b, T, S, H, G, dim, N, R, sd, code, int(pad_slot_id)),
+        _handle(stream, dev))
     if rc != 0:
         _raise("replayssm_decode", rc)
-    return out.squeeze(1) if one else out
+    return out
 
 
 def _rows(t, name, shape, dtype):
     """(address, row stride) of a [..., dim] tensor seen as rows."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.dim() == 2:
-        if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    if len(shape) == 2:
+        if shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{name} must be contiguous in its last dimension")
         return t.data_ptr(), t.stride(0)
     try:
-        v = t.view(-1, t.shape[-1])
+        v = t.view(-1, shape[-1])
     except RuntimeError:
         raise ValueError(f"the leading dimensions of {name} must be one stride apart") from None
     return _rows(v, name, v.shape, dtype)
+
+
+def _result(out, name, like, shape, stream):
+    """(tensor, address, row stride) of a result like `like`."""
+    if out is None:
+        out = _like(like, stream)
+        return out, out.data_ptr(), shape[-1]
+    ptr, stride = _rows(out, name, shape, like.dtype)
+    _need(out.numel() <= shape[-1] or stride >= shape[-1], f"rows of {name} overlap")
+    return out, ptr, stride
 
 
 def add_rms_norm(x, residual, weight, *, residual_scale=1.0, eps=1e-5, out=None, residual_out=None, stream=None):
@@ -323,19 +413,20 @@ def add_rms_norm(x, residual, weight, *, residual_scale=1.0, eps=1e-5, out=None,
     r), weight fp32.  `out` may be x, `residual_out` may be residual.
     """
     lib = _lib or _load()
-    _need(x.dim() >= 1 and x.shape[-1] > 0, "x must have a last dimension")
-    code, rcode = _INPUTS.get(x.dtype), _INPUTS.get(residual.dtype)
+    shape, code, rcode, dev = x.shape, _INPUTS.get(x.dtype), _INPUTS.get(residual.dtype), x.get_device()
+    _need(len(shape) >= 1 and shape[-1] > 0, "x must have a last dimension")
     _need(code is not None and rcode is not None, "x and residual must be bfloat16 or float32")
-    dev = _device(x, residual, weight, out, residual_out)
-    dim, shape = x.shape[-1], x.shape
-    out = _out(out, x, shape, stream)
-    residual_out = _out(residual_out, residual, shape, stream)
-    (px, sx), (pr, sr) = _rows(x, "x", shape, x.dtype), _rows(residual, "residual", shape, residual.dtype)
-    (po, so), (pq, sq) = _rows(out, "out", shape, x.dtype), _rows(residual_out, "residual_out", shape, residual.dtype)
-    _need(x.numel() <= dim or (so >= dim and sq >= dim), "rows of out or residual_out overlap")
-    rc = lib.rsm_add_rms_norm(_pack_add(px, pr, _vector(weight, "weight", dim, _F32), po, pq, x.numel() // dim, sx, sr,
-                                        so, sq, dim, code, rcode, float(residual_scale), float(eps)),
-                              _stream(stream, dev))
+    if not (dev >= 0 and dev == residual.get_device() == weight.get_device() and dev == _current_device()
+            and out is None and residual_out is None):
+        _check_device(x, residual, weight, out, residual_out)
+    dim = shape[-1]
+    px, sx = _rows(x, "x", shape, x.dtype)
+    pr, sr = _rows(residual, "residual", shape, residual.dtype)
+    _check_vector(weight, "weight", dim, _F32)
+    out, po, so = _result(out, "out", x, shape, stream)
+    residual_out, pq, sq = _result(residual_out, "residual_out", residual, shape, stream)
+    rc = lib.rsm_add_rms_norm(_pack_add(px, pr, weight.data_ptr(), po, pq, x.numel() // dim, sx, sr, so, sq, dim, code,
+                                        rcode, float(residual_scale), float(eps)), _handle(stream, dev))
     if rc != 0:
         _raise("add_rms_norm", rc)
     return out, residual_out
@@ -349,18 +440,19 @@ def gated_rms_norm(x, z, weight, *, group_size=None, eps=1e-5, norm_before_gate=
     x and z are bf16 or fp32, alike, weight fp32.  `out` may be x.
     """
     lib = _lib or _load()
-    _need(x.dim() >= 1 and x.shape[-1] > 0, "x must have a last dimension")
-    code = _INPUTS.get(x.dtype)
+    shape, code, dev = x.shape, _INPUTS.get(x.dtype), x.get_device()
+    _need(len(shape) >= 1 and shape[-1] > 0, "x must have a last dimension")
     _need(code is not None, f"x must be bfloat16 or float32, got {x.dtype}")
-    dev = _device(x, z, weight, out)
-    dim, shape = x.shape[-1], x.shape
-    out = _out(out, x, shape, stream)
-    (px, sx), (pz, sz), (po, so) = (_rows(x, "x", shape, x.dtype), _rows(z, "z", shape, x.dtype),
-                                    _rows(out, "out", shape, x.dtype))
-    _need(x.numel() <= dim or so >= dim, "rows of out overlap")
-    rc = lib.rsm_gated_rms_norm(_pack_gated(px, pz, _vector(weight, "weight", dim, _F32), po, x.numel() // dim, sx, sz,
-                                            so, dim, dim if group_size is None else int(group_size), code,
-                                            int(bool(norm_before_gate)), float(eps), 0), _stream(stream, dev))
+    if not (dev >= 0 and dev == z.get_device() == weight.get_device() and dev == _current_device() and out is None):
+        _check_device(x, z, weight, out)
+    dim = shape[-1]
+    px, sx = _rows(x, "x", shape, x.dtype)
+    pz, sz = _rows(z, "z", shape, x.dtype)
+    _check_vector(weight, "weight", dim, _F32)
+    out, po, so = _result(out, "out", x, shape, stream)
+    rc = lib.rsm_gated_rms_norm(_pack_gated(px, pz, weight.data_ptr(), po, x.numel() // dim, sx, sz, so, dim,
+                                            dim if group_size is None else int(group_size), code,
+                                            1 if norm_before_gate else 0, float(eps), 0), _handle(stream, dev))
     if rc != 0:
         _raise("gated_rms_norm", rc)
     return out

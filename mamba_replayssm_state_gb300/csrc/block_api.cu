@@ -329,7 +329,7 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
   // do meanwhile; few: two a CTA, to spread over the SMs.  Long rings take fewer, to
   // leave three CTAs an SM.
   int per = 2;
-  while (per < 16 && static_cast<int64_t>(p.units) * p.H / (2 * per) >= 8 * static_cast<int64_t>(sms)) per *= 2;
+  while (per < ssm::kTokenMaxHeads && static_cast<int64_t>(p.units) * p.H / (2 * per) >= 8 * static_cast<int64_t>(sms)) per *= 2;
   per = std::min(per, hpg);
   const int mode = step ? (p.window == 1 ? 1 : 2)
                    : input_dtype == RSM_BF16 && p.state_dtype != RSM_F32 && p.state_dtype != RSM_F16 ? (p.window <= 8 ? 3 : 4) : 0;

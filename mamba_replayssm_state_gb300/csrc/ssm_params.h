@@ -41,6 +41,7 @@ const void* token_kernel(int input_dtype, int state_dtype, int mode);
 constexpr int kTokenThreads = 256;
 constexpr int kTokenMaxNew = 16;  // new tokens of a request
 constexpr int kTokenMaxAll = 64;  // with the ring's
+constexpr int kTokenMaxHeads = 16;  // of a CTA
 uint32_t token_smem(int mode, int input_bytes, int heads, int fresh, int all);
 
 }  // namespace ssm

@@ -38,6 +38,7 @@ constexpr int kTokMaxNew = kTokenMaxNew;
 constexpr int kTokMaxAll = kTokenMaxAll;
 constexpr int kTokD = 64, kTokN = 128;
 constexpr int kTokRows = 16;      // dim rows of a warp
+constexpr int kTokMaxHeads = kTokenMaxHeads;  // of a CTA
 constexpr int kTokLoads = 8;      // row pairs of a warp
 
 // raw bytes of eight consecutive state elements
@@ -354,6 +355,11 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
         rsm::cp_async_4(rsm::smem_addr(sdt + s * nh + hq), s < n_ring ? dtc + ring_row(s) * p.H + hq : dtn + (s - n_ring) * p.dt_ts + hq);
     if constexpr (MMA)  // the rest of the last k-step: weight 0, and so finite
       for (int i = tid; i < (m16 - m) * xs; i += kTokThreads) sx[m * xs + i] = IT(0);
+    const float A = hq < nh ? __ldg(p.A + h0 + hq) : 0.0f;
+    static_assert(kTokMaxHeads <= 2 * (kTokThreads / 32), "a warp has two heads' weights at most");
+    const bool has_skip = p.D != nullptr;
+    const float skip0 = has_skip && warp < nh ? __ldg(p.D + h0 + warp) : 0.0f;
+    const float skip1 = has_skip && warp + kTokThreads / 32 < nh ? __ldg(p.D + h0 + warp + kTokThreads / 32) : 0.0f;
     staged();
     __syncthreads();
 
@@ -365,9 +371,9 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
 
     // the decays up to and with each token; the dots B_s . C_t
     if (hq < nh) {
-      const float A = __ldg(p.A + h0 + hq);
       for (int s = tid >> 4; s < m; s += kTokThreads / 16) {
         float sum = 0.0f;
+#pragma unroll 4
         for (int k = 0; k <= s; ++k) sum += sdt[k * nh + hq];
         sc[s * nh + hq] = sum * A;
       }
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
 
     // the tokens' weights, a warp per head
     for (int hl = warp; hl < nh; hl += kTokThreads / 32) {
-      const float skip = p.D != nullptr ? __ldg(p.D + h0 + hl) : 0.0f;
+      const float skip = hl == warp ? skip0 : skip1;
       auto weight = [&](int s, int t) {
         const int now = n_ring + t;
         if (s > now || t >= T) return 0.0f;
