@@ -1,4 +1,5 @@
-"""Builds libreplayssm.so in-tree with nvcc for sm_103a.
+"""Builds libreplayssm.so in-tree with nvcc for sm_103a, and _blockcall.so, the
+C++ side of block.py's calls, with g++ against the installed torch.
 
 Each translation unit compiles in its own nvcc process (in parallel), then
 nvcc links them into one shared library (CUDA runtime linked statically).
@@ -22,6 +23,10 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibilit
               "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
 
 
+CALL_SOURCE = os.path.join(CSRC, "blockcall.cpp")
+CALL_LIB = os.path.join(PKG, "_blockcall.so")
+
+
 def nvcc() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -30,7 +35,7 @@ def nvcc() -> str:
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if os.path.join(CSRC, f) != CALL_SOURCE]
     files += [os.path.join(ROOT, "include", f) for f in ("replayssm.h", "replayssm_block.h")]
     files += [os.path.abspath(__file__)]
     return files
@@ -42,8 +47,35 @@ def up_to_date() -> bool:
     return os.path.getmtime(LIB) >= max(os.path.getmtime(f) for f in _deps())
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """Compiles _blockcall.so: a Python extension on torch's C++ tensors."""
+    import sysconfig
+
+    import torch
+    deps = [CALL_SOURCE, os.path.abspath(__file__), torch.__file__]
+    deps += [os.path.join(ROOT, "include", f) for f in ("replayssm.h", "replayssm_block.h")]
+    if not force and os.path.exists(CALL_LIB) and os.path.getmtime(CALL_LIB) >= max(os.path.getmtime(f) for f in deps):
+        return CALL_LIB
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = CALL_LIB + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(at, "include"), "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], CALL_SOURCE, "-o", tmp,
+           "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on blockcall.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL_LIB)
+    return CALL_LIB
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and not extra_flags and up_to_date():
+        build_calls(False, verbose)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -60,8 +92,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(build_calls, force, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        calls.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
