@@ -174,15 +174,17 @@ TensorMapEncodeFn tensor_map_encoder() {
   return fn;
 }
 
-// A [tokens, cols] bf16 tensor in boxes of 128 rows x 64 columns, 128-byte swizzle.
-int token_map(CUtensorMap* map, const void* base, int64_t cols, int64_t tokens, int64_t stride, const char* name) {
+// A [tokens, cols] bf16 tensor in boxes of rows x columns, swizzled over a box's row (64 or 32 columns).
+int token_map(CUtensorMap* map, const void* base, int64_t cols, int64_t tokens, int64_t stride, unsigned box_cols,
+              unsigned box_rows, const char* name) {
   const TensorMapEncodeFn encode = tensor_map_encoder();
   if (encode == nullptr) return fail(RSM_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(tokens == 1 ? cols : stride) * 2u};
-  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(ssm::kChunk)}, ones[2] = {1u, 1u};
+  const cuuint32_t box[2] = {box_cols, box_rows}, ones[2] = {1u, 1u};
   const CUresult cr = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2u, const_cast<void*>(base), dims, strides, box, ones,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return fail(RSM_ECUDA, "cuTensorMapEncodeTiled failed for %s (%d)", name, static_cast<int>(cr));
   return RSM_OK;
@@ -256,9 +258,10 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   const PrefillPlan pl = plan_prefill(a, sms);
   ssm::TcParams tp{};
   const int64_t xc = static_cast<int64_t>(a->num_heads) * ssm::kDim, bc = static_cast<int64_t>(a->num_groups) * ssm::kState;
-  rc = token_map(&tp.x_map, a->x, xc, a->tokens, a->x_stride, "x");
-  if (rc == RSM_OK) rc = token_map(&tp.B_map, a->B, bc, a->tokens, a->B_stride, "B");
-  if (rc == RSM_OK) rc = token_map(&tp.C_map, a->C, bc, a->tokens, a->C_stride, "C");
+  rc = token_map(&tp.x_map, a->x, xc, a->tokens, a->x_stride, 64, ssm::kChunk, "x");
+  if (rc == RSM_OK) rc = token_map(&tp.B_map, a->B, bc, a->tokens, a->B_stride, 64, ssm::kChunk, "B");
+  if (rc == RSM_OK) rc = token_map(&tp.C_map, a->C, bc, a->tokens, a->C_stride, 64, ssm::kChunk, "C");
+  if (rc == RSM_OK) rc = token_map(&tp.y_map, a->out, xc, a->tokens, a->out_stride, 32, 32, "out");
   if (rc != RSM_OK) return rc;
   tp.p = p;
   tp.seg = pl.seg;

@@ -8,7 +8,7 @@
 //   G  = C B^T           [i, j]       once for the CTA's heads, which share B and C
 //   Y1 = C S^T           [i, (h, d)]
 //   Y2 = P X             [i, d]       P = G o decay o dt, masked, in tensor memory as bf16
-//   U  = B^T (w X)       [n, d]       w X as bf16 hi + lo (16 bits), or hi alone for bf16 states
+//   U  = B^T (w X)       [n, (h, d)]  w X as bf16 hi + lo (16 bits), or hi alone for bf16 states
 // The skip term D x is a D on P's diagonal.
 //
 // Decays.  With p_i the sum of a from the start of i's half of the chunk, a pair
@@ -24,10 +24,15 @@
 // group; one head where a group has an odd number), all chunks of a unit in order:
 //   warp 0       loads C, B and x (two stages each) with tensor-map copies
 //   warp 1       issues the MMAs; warps 2, 3 make the decay tables, a head each
-//   warps 4-11   four a head: P; a thread holds row i; G from tensor memory, P back into it
+//   warps 4-11   P, four warps the columns of either half: a thread holds row i, and
+//                puts the heads' P where it read G
 //   warps 12-15  w X: a thread holds token t's row; x becomes w x in place
-//   warps 16-23  four a head: y out of Y1 and Y2; the state in registers as
-//                fp32, a thread per dstate column, and its bf16 copy for Y1
+//   warps 16-19  the state in registers as fp32, a thread per dstate column, and its
+//                bf16 copy for Y1
+//   warps 20-27  four a head: y out of Y1 and Y2
+// What bounds it is the way round: G to P to Y2 to the next G, and Y1 to y to the
+// next Y1, each about 3000 cycles a chunk and pair of heads, of which the four
+// products are 2050 (2560 with lo).
 // A sequence's last chunk may be partial: dt counts as 0 there, and the rows of
 // x and B past its end, which are a neighbour's or nobody's, are cleared
 // before an MMA multiplies them by 0.
@@ -59,6 +64,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+               "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// this thread's stores have read shared memory
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -116,6 +130,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// 8 columns of this thread's lane.  Whole warp.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 // 8 columns of this thread's lane from each of two places.  Whole warp.
 __device__ __forceinline__ void tmem_ld8x2(uint32_t ta, uint32_t tb, float (&a)[8], float (&b)[8]) {
   uint32_t r[8], s[8];
@@ -164,7 +190,7 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // the units of this CTA, walked alike by every role
 // ---------------------------------------------------------------------------
 struct Unit {
-  int64_t t0;           // first token
+  int t0;               // first token
   int len;              // tokens
   int seq, seg, group;  // sequence, segment among all sequences', heads' group
   bool last;            // last segment of the sequence
@@ -176,45 +202,35 @@ struct Walk {
   uint32_t u;         // next unit
   int seq = 0;        // sequence under the cursor
   uint32_t base = 0;  // segments before it
-  int64_t t0 = 0;
-  uint32_t len = 0, nseg = 0;
   bool flagger;       // the one thread of the CTA that reports
 
-  __device__ Walk(const TcParams& tp_, bool flagger_) : tp(tp_), u(blockIdx.x), flagger(flagger_) { look(); }
+  __device__ Walk(const TcParams& tp_, bool flagger_) : tp(tp_), u(blockIdx.x), flagger(flagger_) {}
 
-  __device__ void look() {
-    if (seq >= tp.p.units) return;
-    t0 = __ldg(tp.p.cu_seqlens + seq);
-    const int64_t t1 = __ldg(tp.p.cu_seqlens + seq + 1);
-    len = static_cast<uint32_t>(t1 - t0);
-    if (t0 < 0 || t1 < t0 || t1 > tp.p.tokens) {
-      if (flagger) flag(tp.p.status, RSM_STATUS_BAD_SEQUENCE);
-      len = 0;
-      nseg = 0;  // no unit at all
-    } else {
-      nseg = len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
-    }
-  }
+  // Little is kept from unit to unit: a role's registers are few.
   __device__ bool next(Unit& w) {
-    for (;;) {
-      const uint32_t sg = u / static_cast<uint32_t>(tp.pairs);
-      while (seq < tp.p.units && sg >= base + nseg) {
-        base += nseg;
-        ++seq;
-        look();
-      }
+    for (;; ++seq) {
       if (seq >= tp.p.units) return false;
-      const uint32_t s = sg - base;
-      w.group = static_cast<int>(u - sg * static_cast<uint32_t>(tp.pairs));
-      u += gridDim.x;
-      w.last = s == nseg - 1;
-      w.split = nseg > 1;
-      if (tp.states_only && w.last) continue;  // nothing follows its state
-      w.seq = seq;
-      w.seg = static_cast<int>(sg);
-      w.t0 = t0 + static_cast<int64_t>(s) * tp.seg;
-      w.len = static_cast<int>(min(tp.seg, len - s * tp.seg));
-      return true;
+      const int t0 = __ldg(tp.p.cu_seqlens + seq), t1 = __ldg(tp.p.cu_seqlens + seq + 1);
+      if (t0 < 0 || t1 < t0 || t1 > tp.p.tokens) {
+        if (flagger) flag(tp.p.status, RSM_STATUS_BAD_SEQUENCE);
+        continue;  // no unit at all
+      }
+      const uint32_t len = static_cast<uint32_t>(t1 - t0);
+      const uint32_t nseg = len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
+      for (uint32_t sg; (sg = u / static_cast<uint32_t>(tp.pairs)) < base + nseg;) {
+        const uint32_t s = sg - base;
+        w.group = static_cast<int>(u - sg * static_cast<uint32_t>(tp.pairs));
+        u += gridDim.x;
+        w.last = s == nseg - 1;
+        w.split = nseg > 1;
+        if (tp.states_only && w.last) continue;  // nothing follows its state
+        w.seq = seq;
+        w.seg = static_cast<int>(sg);
+        w.t0 = t0 + static_cast<int>(s * tp.seg);
+        w.len = static_cast<int>(min(tp.seg, len - s * tp.seg));
+        return true;
+      }
+      base += nseg;
     }
   }
 };
@@ -227,7 +243,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
       "mov.u32 n, %3;\n\t"
       "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %4;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE;\n\t"
       "sub.u32 n, n, 1;\n\t"
       "setp.ne.u32 q, n, 0;\n\t"
@@ -235,7 +251,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(kTcTries), "n"(kTcRestNs)
+      : "r"(bar), "r"(parity), "n"(kTcTries)
       : "memory");
   return ok != 0;
 }
@@ -274,7 +290,7 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
-      const int row = static_cast<int>(w.t0 + c0);
+      const int row = w.t0 + c0;
       if (j >= 2 && !(ok = c.wait_warp(kEmptyBC + st, (j >> 1) - 1u))) break;
       if (one) {
         const uint32_t bc = c.bar(kFullBC + st);
@@ -320,7 +336,7 @@ __device__ __forceinline__ bool run_tables(const Cta& c, int h) {
   const bool second = lane >= 16;
   while (walk.next(w)) {
     const int head = w.group * NH + h;
-    const float* dt = tp.p.dt + w.t0 * tp.p.dt_ts + head;
+    const float* dt = tp.p.dt + static_cast<int64_t>(w.t0) * tp.p.dt_ts + head;
     const float A2 = __ldg(tp.p.A + head) * kLog2e;
     const float skip = tp.p.D != nullptr ? __ldg(tp.p.D + head) : 0.0f;
 #pragma unroll 1
@@ -392,50 +408,32 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
   Walk walk(tp, false);
   Unit w;
   uint32_t j = 0;
-  constexpr uint32_t kIdG = rsm::idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdY1 = rsm::idesc_bf16_f32(128, 64 * NH, false, true);
   constexpr uint32_t kIdPx = rsm::idesc_bf16_f32(128, 64, false, true);
-  constexpr uint32_t kIdU = rsm::idesc_bf16_f32(128, 64, true, true);
+  constexpr uint32_t kIdU = rsm::idesc_bf16_f32(128, 64 * NH, true, true);
   constexpr uint32_t kStepMn = 2048 / 16;  // 16 rows of K
   const uint32_t tm = c.tmem;
   const bool one = elect_one();
-
-  auto issue_G = [&](uint32_t st) {
-    tc_fence_after();
-    if (one) {
-      const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_k(c.base + kOffB + 2 * st * kTile);
-#pragma unroll 2
-      for (uint32_t k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
-        const uint32_t o = (k >> 2) * (kTile / 16) + (k & 3) * 2;
-        mma_ss(tm + kColG, a + o, b + o, kIdG, k > 0);
-      }
-      tc_commit(c.bar(kGFull));
-    }
-    __syncwarp();
-  };
 
   while (walk.next(w)) {
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       if (!tp.states_only) {
-        // (G is free: the last chunk's P was waited for)
-        if (c0 == 0) {
-          if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
-          issue_G(st);
-        }
-        // Y2 = P X (x has come, or W would not have looked at it; the last outputs were waited for below)
-        if (!c.wait_warp(kClean, j) || !c.wait_warp(kPFull, j)) return false;
+        // Y2 = P X (x has come, or W would not have looked at it)
+        if (!c.wait_warp(kClean, j) || !c.wait_warp(kPFull + st, j >> 1)) return false;
+        if (j >= 1 && !c.wait_warp(kYRead, j - 1u)) return false;
         tc_fence_after();
         if (one) {
+          const uint32_t P = tm + kColG + 128 * st;
 #pragma unroll 1
           for (uint32_t h = 0; h < NH; ++h) {
             const uint32_t b = desc_mn(c.base + kOffX + (2 * st + h) * kTile);
 #pragma unroll 2
-            for (uint32_t k = 0; k < 8; ++k)
-              mma_ts(tm + kColY2 + 64 * h, tm + kColP + 64 * h + 8 * k, b + k * kStepMn, kIdPx, k > 0);
-            tc_commit(c.bar(kPxDone + h));
+            for (uint32_t k = 0; k < 8; ++k)  // 16 tokens each, two to a block
+              mma_ts(tm + kColY2 + 64 * h, P + 32 * (k >> 1) + 16 * h + 8 * (k & 1), b + k * kStepMn, kIdPx, k > 0);
           }
+          tc_commit(c.bar(kPxDone));
         }
         __syncwarp();
         // Y1 = C S^T
@@ -446,85 +444,93 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
           const uint32_t b = desc_mn(c.base + kOffX + 2 * (st ^ 1u) * kTile);
 #pragma unroll 2
           for (uint32_t k = 0; k < 8; ++k)
-            mma_ss(tm + kColV, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
+            mma_ss(tm + kColY1, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
           tc_commit(c.bar(kY1Full));
           tc_commit(c.bar(kEmptyX + (st ^ 1u)));
         }
         __syncwarp();
-        // the next chunk's G while this one's w X is made
-        if (c0 + kChunk < w.len) {
-          if (!c.wait_warp(kFullBC + (st ^ 1u), (j + 1u) >> 1)) return false;
-          issue_G(st ^ 1u);
-        }
       } else if (!c.wait_warp(kFullBC + st, j >> 1)) {
         return false;
       }
-      // U = B^T (w X), where Y1 was
-      if (!tp.states_only && !c.wait_warp(kYRead, j)) return false;
-#pragma unroll 1
-      for (uint32_t h = 0; h < NH; ++h) {
-        if (!c.wait_warp(kWFull + h, j)) return false;
-        if (tp.states_only && j >= 1 && !c.wait_warp(kURead + h, j - 1u)) return false;
-        tc_fence_after();
-        if (one) {
-          const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX + (2 * st + h) * kTile);
-          const uint32_t lo = desc_mn(c.base + kOffC + (2 * st + h) * kTile);
+      // U = B^T (w X); P, where it goes, has been multiplied
+      if (!c.wait_warp(kWFull + st, j >> 1)) return false;
+      if (tp.states_only && j >= 2 && !c.wait_warp(kURead + st, (j >> 1) - 1u)) return false;
+      tc_fence_after();
+      if (one) {
+        const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX + 2 * st * kTile);
+        const uint32_t lo = desc_mn(c.base + kOffC + 2 * st * kTile);
 #pragma unroll 2
-          for (uint32_t k = 0; k < 8; ++k) {
-            mma_ss(tm + kColV + 64 * h, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
-            if constexpr (LO) mma_ss(tm + kColV + 64 * h, a + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
-          }
-          tc_commit(c.bar(kUFull + h));
-          if (h == NH - 1) {
-            tc_commit(c.bar(kEmptyBC + st));
-            if (tp.states_only) tc_commit(c.bar(kEmptyX + st));
-          }
+        for (uint32_t k = 0; k < 8; ++k) {
+          mma_ss(tm + kColG + 128 * st, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
+          if constexpr (LO) mma_ss(tm + kColG + 128 * st, a + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
         }
-        __syncwarp();
+        tc_commit(c.bar(kUFull + st));
+        tc_commit(c.bar(kEmptyBC + st));
+        if (tp.states_only) tc_commit(c.bar(kEmptyX + st));
       }
+      __syncwarp();
     }
   }
   return true;
 }
 
-// P of one head, a thread per row; the row factor 2^p is left to the output.
+// G = C B^T of a stage.  One thread.
+__device__ __forceinline__ void issue_G(const Cta& c, uint32_t st) {
+  constexpr uint32_t kIdG = rsm::idesc_bf16_f32(128, 128, false, false);
+  const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_k(c.base + kOffB + 2 * st * kTile);
+#pragma unroll 2
+  for (uint32_t k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
+    const uint32_t o = (k >> 2) * (kTile / 16) + (k & 3) * 2;
+    mma_ss(c.tmem + kColG + 128 * st, a + o, b + o, kIdG, k > 0);
+  }
+  tc_commit(c.bar(kGFull + st));
+}
+
+// P of the heads in 64 of its columns (`cols` 0 or 1), a thread per row; the row
+// factor 2^p is left to the output.  The warp whose blocks are all above the
+// diagonal has the time to issue G.
 template <int NH>
-__device__ __forceinline__ bool run_p(const Cta& c, int h) {
+__device__ __forceinline__ bool run_p(const Cta& c, int cols) {
   const TcParams& tp = c.tp;
   if (tp.states_only) return true;
   const int k = c.warp & 3, lane = c.lane;
-  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16);
-  const uint32_t prow = trow + kColP + 64 * h;
-  // the blocks above the diagonal are zero for good
-  {
-    uint32_t zero[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) zero[i] = 0u;
-#pragma unroll 1
-    for (int b = k + 1; b < 4; ++b) tmem_st16(prow + 16 * b, zero);
-    rsm::tmem_st_wait();
-  }
+  const uint32_t trow0 = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + kColG;
+  const bool issuer = cols == 1 && k == 0, one = elect_one();
   Walk walk(tp, false);
   Unit w;
   uint32_t j = 0;
   while (walk.next(w)) {
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      const uint32_t st = j & 1u, tab = c.table(st, h);
-      if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
-      const float skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
-      const bool steep = lds(tab + kTabMisc + 8u + 4u * (k >> 1)) != 0.0f;
-      if (j >= 1 && !c.wait_warp(kPxDone + h, j - 1u)) return false;  // the last P has been multiplied
-      if (!c.wait_warp(kGFull, j)) return false;
+      const uint32_t st = j & 1u, tab0 = c.table(st, 0), trow = trow0 + 128 * st;
+      if (issuer) {
+        if (j >= 2 && !c.wait_warp(kURead + st, (j >> 1) - 1u)) return false;
+        if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
+        tc_fence_after();
+        if (one) issue_G(c, st);
+        __syncwarp();
+      }
+      if (!c.wait_warp(kFullTab + st, j >> 1) || !c.wait_warp(kGFull + st, j >> 1)) return false;
       tc_fence_after();
-      if (!steep) {
 #pragma unroll 1
-        for (int b = 0; b <= k; ++b) {
+      for (int b = 2 * cols; b < 2 * cols + 2; ++b) {
+        if (b > k) {  // above the diagonal
+          uint32_t zero[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) zero[i] = 0u;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) tmem_st16(trow + 32 * b + 16 * h, zero);
+          continue;
+        }
+        float g[32];
+        rsm::tmem_ld32(trow + 32 * b, g);
+#pragma unroll 1
+        for (int h = 0; h < NH; ++h) {
+          const uint32_t tab = tab0 + h * kTabBytes;
+          const bool steep = lds(tab + kTabMisc + 8u + 4u * (k >> 1)) != 0.0f;
           const uint32_t col = tab + (k >= 2 && b < 2 ? kTabV : kTabCol) + 128u * b;
-          float g[32];
-          rsm::tmem_ld32(trow + kColG + 32 * b, g);
           uint32_t r[16];
-          if (b < k) {
+          if (!steep && b < k) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const float4 v = lds4(col + 16u * q);
@@ -533,60 +539,56 @@ __device__ __forceinline__ bool run_p(const Cta& c, int h) {
               r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
               r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
             }
-          } else {
+          } else if (!steep) {
+            const float skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const float4 v = lds4(col + 16u * q);
-              float e[4] = {g[4 * q] * v.x, g[4 * q + 1] * v.y, g[4 * q + 2] * v.z, g[4 * q + 3] * v.w};
+              const float f[4] = {v.x, v.y, v.z, v.w};
+              float e[4];
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                if (4 * q + m == lane) e[m] += skip;
-                if (4 * q + m > lane) e[m] = 0.0f;
+              for (int m = 0; m < 4; ++m) {  // selections, not branches
+                const float on_diagonal = 4 * q + m == lane ? skip : 0.0f;
+                const float y = fmaf(g[4 * q + m], f[m], on_diagonal);
+                e[m] = 4 * q + m <= lane ? y : 0.0f;
               }
               r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
               r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
             }
-          }
-          tmem_st16(prow + 16 * b, r);
-        }
-      } else {
-        const float pi = lds(tab + kTabCol + 4u * (32 * k + lane));
-        const float ui = exp2_approx(pi);
-#pragma unroll 1
-        for (int b = 0; b <= k; ++b) {
-          const bool same = (b >> 1) == (k >> 1);
-          float g[32];
-          rsm::tmem_ld32(trow + kColG + 32 * b, g);
-          uint32_t r[16];
+          } else {
+            const float pi = lds(tab + kTabCol + 4u * (32 * k + lane));
+            const float ui = exp2_approx(pi), skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
+            const bool same = (b >> 1) == (k >> 1);
 #pragma unroll
-          for (int q = 0; q < 32; q += 2) {
-            float e[2];
+            for (int q = 0; q < 32; q += 2) {
+              float e[2];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const uint32_t o = 128u * b + 4u * (q + m);
-              const bool in = b < k || q + m <= lane;
-              const float f = same ? exp2_approx(pi - lds(tab + kTabCol + o)) * lds(tab + kTabDt + o)
-                                   : ui * lds(tab + kTabV + o);
-              e[m] = in ? g[q + m] * f : 0.0f;
-              if (b == k && q + m == lane) e[m] += skip;
+              for (int m = 0; m < 2; ++m) {
+                const uint32_t o = 128u * b + 4u * (q + m);
+                const bool in = b < k || q + m <= lane;
+                const float f = same ? exp2_approx(pi - lds(tab + kTabCol + o)) * lds(tab + kTabDt + o)
+                                     : ui * lds(tab + kTabV + o);
+                const float y = fmaf(g[q + m], f, b == k && q + m == lane ? skip : 0.0f);
+                e[m] = in ? y : 0.0f;
+              }
+              r[q / 2] = rsm::pack_bf16x2(e[0], e[1]);
             }
-            r[q / 2] = rsm::pack_bf16x2(e[0], e[1]);
           }
-          tmem_st16(prow + 16 * b, r);
+          tmem_st16(trow + 32 * b + 16 * h, r);
         }
       }
       rsm::tmem_st_wait();
       tc_fence_before();
-      c.arrive_warp(kPFull);
+      c.arrive_warp(kPFull + st);
       if (lane == 0) mbar_arrive(c.bar(kEmptyTab + st));
     }
   }
   return true;
 }
 
-// w X, a thread per token row; hi over x, lo beside it.
+// w X of a head, a thread per token row; hi over x, lo in C's place.
 template <int NH, bool LO>
-__device__ __forceinline__ bool run_w(const Cta& c) {
+__device__ __forceinline__ bool run_w(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   Walk walk(tp, false);
   Unit w;
@@ -599,58 +601,55 @@ __device__ __forceinline__ bool run_w(const Cta& c) {
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
-      const float w0 = lds(c.table(st, 0) + kTabW + 4u * t), w1 = lds(c.table(st, NH - 1) + kTabW + 4u * t);
+      const float wt = lds(c.table(st, h) + kTabW + 4u * t);
       c.arrive_warp(kEmptyTab + st);
       if (!c.wait_warp(kFullX + st, j >> 1)) return false;
+      const uint32_t xa = c.base + kOffX + (2 * st + h) * kTile + row;
+      const uint32_t la = c.base + kOffC + (2 * st + h) * kTile + row;
       if (w.len - c0 < kChunk) {  // rows past the end: zero, whatever is there
         if (!c.wait_warp(kFullBC + st, j >> 1)) return false;
         if (c0 + t >= w.len) {
 #pragma unroll 1
           for (uint32_t q = 0; q < 8; ++q) {
+            sts128(xa + 16u * q, 0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int h = 0; h < NH; ++h) sts128(c.base + kOffX + (2 * st + h) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
-            sts128(c.base + kOffB + (2 * st) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
-            sts128(c.base + kOffB + (2 * st + 1) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
+            for (int i = h; i < 2; i += NH) sts128(c.base + kOffB + (2 * st + i) * kTile + row + 16u * q, 0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
       }
       if (!tp.states_only) c.arrive_warp(kClean);
-#pragma unroll 1
-      for (int h = 0; h < NH; ++h) {
-        if (!tp.states_only && !c.wait_warp(kPxDone + h, j)) return false;
-        if (LO && !tp.states_only && h == 0 && !c.wait_warp(kY1Full, j)) return false;  // lo takes the place of C
-        const uint32_t xa = c.base + kOffX + (2 * st + h) * kTile + row;
-        const uint32_t la = c.base + kOffC + (2 * st + h) * kTile + row;
-        const float wt = h ? w1 : w0;
-        const float2 w2 = make_float2(wt, wt);
-#pragma unroll 1
-        for (uint32_t q0 = 0; q0 < 8; q0 += 4) {
-          uint4 v[4];
+      if (!tp.states_only && !c.wait_warp(kPxDone, j)) return false;
+      const float2 w2 = make_float2(wt, wt);
+      uint32_t lw[LO ? 32 : 1];
+#pragma unroll(LO ? 8 : 2)
+      for (uint32_t q = 0; q < 8; ++q) {
+        const uint32_t at = (xa + swz) ^ (q << 4);  // a row is 128 bytes
+        const uint4 v = rsm::lds128(at);
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hw[4];
 #pragma unroll
-          for (uint32_t q = 0; q < 4; ++q) v[q] = rsm::lds128(xa + (((q0 + q) << 4) ^ swz));
-#pragma unroll
-          for (uint32_t q = 0; q < 4; ++q) {
-            const uint32_t at = ((q0 + q) << 4) ^ swz;
-            const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-            uint32_t hw[4], lw[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const float2 u = __fmul2_rn(make_float2(rsm::bf16lo(in[m]), rsm::bf16hi(in[m])), w2);
-              hw[m] = rsm::pack_bf16x2(u.x, u.y);
-              if constexpr (LO) {
-                // u - hi is exact; rounded to bf16, hi + lo is within 2^-17 of u
-                const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
-                lw[m] = rsm::pack_bf16x2(l.x, l.y);
-              }
-            }
-            sts128(xa + at, hw[0], hw[1], hw[2], hw[3]);
-            if constexpr (LO) sts128(la + at, lw[0], lw[1], lw[2], lw[3]);
+        for (int m = 0; m < 4; ++m) {
+          const float2 u = __fmul2_rn(make_float2(rsm::bf16lo(in[m]), rsm::bf16hi(in[m])), w2);
+          hw[m] = rsm::pack_bf16x2(u.x, u.y);
+          if constexpr (LO) {
+            // u - hi is exact; rounded to bf16, hi + lo is within 2^-17 of u
+            const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
+            lw[4 * q + m] = rsm::pack_bf16x2(l.x, l.y);
           }
         }
-        fence_proxy_async_smem();
-        c.arrive_warp(kWFull + h);
+        if constexpr (LO)  // here and now: two registers a pair until then are too many
+          asm volatile("" : "+r"(lw[4 * q]), "+r"(lw[4 * q + 1]), "+r"(lw[4 * q + 2]), "+r"(lw[4 * q + 3]));
+        sts128(at, hw[0], hw[1], hw[2], hw[3]);
       }
+      if constexpr (LO) {
+        if (!tp.states_only && !c.wait_warp(kY1Full, j)) return false;  // the last to read C
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q)
+          sts128((la + swz) ^ (q << 4), lw[4 * q], lw[4 * q + 1], lw[4 * q + 2], lw[4 * q + 3]);
+      }
+      fence_proxy_async_smem();
+      c.arrive_warp(kWFull + st);
     }
   }
   return true;
@@ -702,116 +701,157 @@ __device__ __forceinline__ void store_column(const float2 (&S)[kDim / 2], const 
   }
 }
 
-// One head's outputs and state.
+// The heads' states.
 template <int NH>
-__device__ __forceinline__ bool run_head(const Cta& c, int h) {
+__device__ __forceinline__ bool run_state(const Cta& c) {
   const TcParams& tp = c.tp;
   const Params& p = tp.p;
   Walk walk(tp, false);
   Unit w;
   uint32_t j = 0;
-  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;  // output row, and dstate column
-  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + 64 * h;
-  const uint32_t srow = c.base + kOffX + h * kTile + static_cast<uint32_t>(r) * 128u;
+  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;  // dstate column
+  const uint32_t trow0 = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + kColG;
+  const uint32_t srow = c.base + kOffX + static_cast<uint32_t>(r) * 128u;
   const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
-  // a warp's 32 rows of 64 bytes; 16-byte pieces of a row change places by its number / 2
-  const uint32_t ywarp = c.base + kOffY + (4 * h + k) * kYBytes;
-  const uint32_t yput = ywarp + 64u * lane, yswz = static_cast<uint32_t>((lane >> 1) & 3) << 4;
-  const uint32_t yget = ywarp + 64u * (lane >> 2) + ((static_cast<uint32_t>(lane & 3) ^ ((lane >> 3) & 3)) << 4);
   while (walk.next(w)) {
-    const int head = w.group * NH + h;
-    const int64_t tile = static_cast<int64_t>(head) * (kDim * kState) + r;
-    float2 S[kDim / 2];
-    const bool say = w.group == 0 && h == 0 && r == 0 && !tp.states_only;
+    const int64_t tile = static_cast<int64_t>(w.group) * NH * (kDim * kState) + r;
+    float2 S[NH][kDim / 2];
+    const bool say = w.group == 0 && r == 0 && !tp.states_only;
     if (w.split && !tp.states_only) {
       const float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
 #pragma unroll
-      for (int d = 0; d < kDim / 2; ++d) S[d] = make_float2(at[2 * d * kState], at[(2 * d + 1) * kState]);
+      for (int d = 0; d < NH * kDim / 2; ++d)
+        S[d / (kDim / 2)][d % (kDim / 2)] = make_float2(at[2 * d * kState], at[(2 * d + 1) * kState]);
     } else {
-      load_column(S, p, tp.states_only ? -1 : slot_of(p, p.src, w.seq, say), tile);
+      const int src = tp.states_only ? -1 : slot_of(p, p.src, w.seq, say);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) load_column(S[h], p, src, tile + h * (kDim * kState));
     }
-    float decay = 0.0f;  // of the segment, log2
+    float decay[NH];  // of the segment, log2
+#pragma unroll
+    for (int h = 0; h < NH; ++h) decay[h] = 0.0f;
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      const uint32_t st = j & 1u, tab = c.table(st, h);
+      const uint32_t st = j & 1u;
       if (!tp.states_only) {
-        const uint32_t at = srow + 2 * (st ^ 1u) * kTile;
+        const uint32_t at = srow + 2 * (st ^ 1u) * kTile + swz;
 #pragma unroll
-        for (uint32_t q = 0; q < 8; ++q)
-          sts128(at + ((q << 4) ^ swz), rsm::pack_bf16x2(S[4 * q].x, S[4 * q].y),
-                 rsm::pack_bf16x2(S[4 * q + 1].x, S[4 * q + 1].y), rsm::pack_bf16x2(S[4 * q + 2].x, S[4 * q + 2].y),
-                 rsm::pack_bf16x2(S[4 * q + 3].x, S[4 * q + 3].y));
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (uint32_t q = 0; q < 8; ++q)
+            sts128((at + h * kTile) ^ (q << 4), rsm::pack_bf16x2(S[h][4 * q].x, S[h][4 * q].y),
+                   rsm::pack_bf16x2(S[h][4 * q + 1].x, S[h][4 * q + 1].y), rsm::pack_bf16x2(S[h][4 * q + 2].x, S[h][4 * q + 2].y),
+                   rsm::pack_bf16x2(S[h][4 * q + 3].x, S[h][4 * q + 3].y));
         fence_proxy_async_smem();
         tc_fence_before();
         c.arrive_warp(kSFull);
       }
       if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
-      const float m1 = lds(tab + kTabM1 + 4u * r), m2 = lds(tab + kTabM2 + 4u * r);
-      const float a = lds(tab + kTabMisc);
-      decay += lds(tab + kTabMisc + 4u);
+      float a[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        a[h] = lds(c.table(st, h) + kTabMisc);
+        decay[h] += lds(c.table(st, h) + kTabMisc + 4u);
+      }
       c.arrive_warp(kEmptyTab + st);
-      if (!tp.states_only) {
-        if (!c.wait_warp(kY1Full, j) || !c.wait_warp(kPxDone + h, j)) return false;
-        tc_fence_after();
-        // 32 columns at a time, turned in shared memory so that four lanes store
-        // a row's 64 bytes (a row a lane touched 32 lines an instruction: 1650 cycles a chunk,
-        // during which the other roles' shared-memory accesses wait; tensor-map stores
-        // of such small boxes were slower still)
-        const float2 f1 = make_float2(m1, m1), f2 = make_float2(m2, m2);
-        uint16_t* out = static_cast<uint16_t*>(p.out) + (w.t0 + c0 + 32 * k + (lane >> 2)) * p.out_ts + head * kDim + 8 * (lane & 3);
-        const int rows = w.len - c0 - 32 * k - (lane >> 2);  // rows from this lane's first on
-#pragma unroll 1
-        for (uint32_t part = 0; part < 2; ++part) {
-#pragma unroll 2
-          for (uint32_t q = 0; q < 4; ++q) {
-            float y1[8], y2[8];
-            tmem_ld8x2(trow + kColV + 32 * part + 8 * q, trow + kColY2 + 32 * part + 8 * q, y1, y2);
-            uint32_t v[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const float2 y = __ffma2_rn(f1, make_float2(y1[2 * m], y1[2 * m + 1]),
-                                          __fmul2_rn(f2, make_float2(y2[2 * m], y2[2 * m + 1])));
-              v[m] = rsm::pack_bf16x2(y.x, y.y);
-            }
-            sts128(yput + ((16u * q) ^ yswz), v[0], v[1], v[2], v[3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = rsm::lds128(yget + 512u * i);
-            if (8 * i < rows) *reinterpret_cast<uint4*>(out + 8 * i * p.out_ts + 32 * part) = v;
-          }
-          __syncwarp();
-        }
-        tc_fence_before();
-        c.arrive_warp(kYRead);
-      }
-      if (!c.wait_warp(kUFull + h, j)) return false;
+      if (!c.wait_warp(kUFull + st, j >> 1)) return false;
       tc_fence_after();
-      const float2 a2 = make_float2(a, a);
+      const uint32_t trow = trow0 + 128 * st;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float u[32];
-        rsm::tmem_ld32(trow + kColV + 32 * q, u);
+      for (int h = 0; h < NH; ++h) {
+        const float2 a2 = make_float2(a[h], a[h]);
 #pragma unroll
-        for (int m = 0; m < 16; ++m) S[16 * q + m] = __ffma2_rn(a2, S[16 * q + m], make_float2(u[2 * m], u[2 * m + 1]));
+        for (int q = 0; q < 8; ++q) {
+          float u[8];
+          tmem_ld8(trow + 64 * h + 8 * q, u);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) S[h][4 * q + m] = __ffma2_rn(a2, S[h][4 * q + m], make_float2(u[2 * m], u[2 * m + 1]));
+        }
       }
-      if (tp.states_only) {
-        tc_fence_before();
-        c.arrive_warp(kURead + h);
-      }
+      tc_fence_before();
+      c.arrive_warp(kURead + st);
     }
     if (tp.states_only) {
       float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
 #pragma unroll
-      for (int d = 0; d < kDim / 2; ++d) {
-        at[2 * d * kState] = S[d].x;
-        at[(2 * d + 1) * kState] = S[d].y;
+      for (int d = 0; d < NH * kDim / 2; ++d) {
+        at[2 * d * kState] = S[d / (kDim / 2)][d % (kDim / 2)].x;
+        at[(2 * d + 1) * kState] = S[d / (kDim / 2)][d % (kDim / 2)].y;
       }
-      if (r == 0) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + head] = decay;
+      if (r == 0) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + w.group * NH + h] = decay[h];
+      }
     } else if (w.last) {
       const int dst = slot_of(p, p.dst, w.seq, say);
-      if (dst >= 0) store_column(S, p, dst, tile);
+      if (dst >= 0) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) store_column(S[h], p, dst, tile + h * (kDim * kState));
+      }
+    }
+  }
+  return true;
+}
+
+// One head's outputs, a thread per row.
+template <int NH>
+__device__ __forceinline__ bool run_y(const Cta& c, int h) {
+  const TcParams& tp = c.tp;
+  const Params& p = tp.p;
+  if (tp.states_only) return true;
+  Walk walk(tp, false);
+  Unit w;
+  uint32_t j = 0;
+  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;
+  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + 64 * h;
+  // A warp's rows leave 32 columns at a time, by a tensor-map store from shared
+  // memory: the shared memory's rate is what the kernel lives on, and rows stored by
+  // their threads take it 32 lines an instruction.  16-byte pieces of a row change
+  // places by its number / 2.
+  const uint32_t ywarp = c.base + kOffY + (4 * h + k) * kYBytes;
+  const uint32_t yput = ywarp + 64u * lane, yswz = static_cast<uint32_t>((lane >> 1) & 3) << 4;
+  while (walk.next(w)) {
+    const int col = (w.group * NH + h) * kDim;
+#pragma unroll 1
+    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
+      const uint32_t st = j & 1u, tab = c.table(st, h);
+      if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
+      const float m1 = lds(tab + kTabM1 + 4u * r), m2 = lds(tab + kTabM2 + 4u * r);
+      c.arrive_warp(kEmptyTab + st);
+      const float2 f1 = make_float2(m1, m1), f2 = make_float2(m2, m2);
+      if (!c.wait_warp(kPxDone, j) || !c.wait_warp(kY1Full, j)) return false;
+      tc_fence_after();
+      const int rows = w.len - c0 - 32 * k;  // of this warp's that exist
+#pragma unroll 1
+      for (uint32_t part = 0; part < 2; ++part) {
+        if (lane == 0) tma_store_wait_read();  // the last store from here
+        __syncwarp();
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+          float y1[8], y2[8];
+          tmem_ld8x2(trow + kColY1 + 32 * part + 8 * q, trow + kColY2 + 32 * part + 8 * q, y1, y2);
+          uint32_t v[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float2 y = __ffma2_rn(f1, make_float2(y1[2 * m], y1[2 * m + 1]), __fmul2_rn(f2, make_float2(y2[2 * m], y2[2 * m + 1])));
+            v[m] = rsm::pack_bf16x2(y.x, y.y);
+          }
+          sts128(yput + ((16u * q) ^ yswz), v[0], v[1], v[2], v[3]);
+        }
+        if (part == 1) {
+          tc_fence_before();
+          c.arrive_warp(kYRead);
+        }
+        if (rows >= 32) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&tp.y_map, col + 32 * part, w.t0 + c0 + 32 * k, ywarp);
+        } else if (lane < rows) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(w.t0 + c0 + r) * p.out_ts + col + 32 * part);
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) out[q] = rsm::lds128(yput + ((16u * q) ^ yswz));
+        }
+      }
     }
   }
   return true;
@@ -840,50 +880,60 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     init(kFullX, 1, 2);
     init(kEmptyX, 1, 2);
     init(kFullTab, NH, 2);
-    init(kEmptyTab, (tp.states_only ? 4 : 4 + 4 * NH) + 4 * NH, 2);
-    init(kGFull, 1);
-    init(kPFull, 4 * NH);
-    init(kPxDone, 1, 2);
-    init(kSFull, 4 * NH);
+    init(kEmptyTab, 4 * NH + 4 + (tp.states_only ? 0 : 8 + 4 * NH), 2);  // W and S; P and y
+    init(kGFull, 1, 2);
+    init(kPFull, 8, 2);
+    init(kPxDone, 1);
+    init(kSFull, 4);
     init(kY1Full, 1);
     init(kYRead, 4 * NH);
-    init(kWFull, 4, 2);
-    init(kClean, 4);
+    init(kWFull, 4 * NH, 2);
+    init(kClean, 4 * NH);
     init(kUFull, 1, 2);
     init(kURead, 4, 2);
-    init(kExit, 1);
+    init(kExit, 1, 2);
     rsm::fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane};
-  // Registers: the launch's 6 x 80 a thread of each warpgroup, shared out anew
-  // (56 + 2 x 64 + 56 + 2 x 120 = 480): a head warp holds a column of 64 state values.
+  // Registers: the launch's 8 x 64 a thread of each warpgroup, shared out anew
+  // (40 + 2 x 64 + 2 x 56 + 152 + 2 x 40 = 512): a state warp holds two columns of 64 values.
   bool ok = true;
+  // no MMA may be in flight when the tensor memory is freed, whichever way its issuer ended
+  auto drain = [&](uint32_t bar) {
+    __syncwarp();
+    if (elect_one()) tc_commit(c.bar(bar));
+    __syncwarp();
+    (void)c.wait(bar, 0u);
+  };
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       ok = run_loader<NH>(c);
     } else if (warp == 1) {
       ok = run_mma<NH, LO>(c);
-      // no MMA may be in flight when the tensor memory is freed, whichever way the role ended
-      __syncwarp();
-      if (elect_one()) tc_commit(c.bar(kExit));
-      __syncwarp();
-      (void)c.wait(kExit, 0u);
+      drain(kExit);
     } else if (warp - 2 < NH) {
       ok = run_tables<NH>(c, warp - 2);
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if ((warp - 4) / 4 < NH) ok = run_p<NH>(c, (warp - 4) / 4);
-  } else if (warp < 16) {
+    ok = run_p<NH>(c, (warp - 4) / 4);
+    if (warp == 8) drain(kExit + 1);
+  } else if (warp < 20) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    ok = run_w<NH, LO>(c);
+    if ((warp - 12) / 4 < NH) ok = run_w<NH, LO>(c, (warp - 12) / 4);
+  } else if (warp < 24) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    ok = run_state<NH>(c);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-    if ((warp - 16) / 4 < NH) ok = run_head<NH>(c, (warp - 16) / 4);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if ((warp - 24) / 4 < NH) {
+      ok = run_y<NH>(c, (warp - 24) / 4);
+      if (lane == 0) tma_store_wait_read();  // shared memory outlives the stores that read it
+    }
   }
   if (!ok) flag(tp.p.status, RSM_STATUS_WAIT_TIMEOUT);
   __syncwarp();

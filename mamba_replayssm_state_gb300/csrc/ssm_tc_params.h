@@ -13,6 +13,7 @@ constexpr int kTile = kChunk * 128;  // bytes of a [128 rows x 64 bf16] tile, 12
 
 struct TcParams {
   CUtensorMap x_map, B_map, C_map;  // [tokens, H * 64], [tokens, G * 128] bf16, boxes of 128 rows x 64 columns
+  CUtensorMap y_map;                // [tokens, H * 64], boxes of 32 rows x 32 columns
   Params p;
   uint32_t seg;        // tokens of a segment, a multiple of kChunk, below 2^31
   float* seg_state;    // [segments, H, 64, 128]: states between segments (NULL when nothing is split)
@@ -29,7 +30,7 @@ struct TcParams {
 constexpr uint32_t kOffC = 0;
 constexpr uint32_t kOffB = kOffC + 4 * kTile;
 constexpr uint32_t kOffX = kOffB + 4 * kTile;
-constexpr uint32_t kOffY = kOffX + 4 * kTile;  // a head warp: two times 32 rows x 16 columns, 32-byte swizzled
+constexpr uint32_t kOffY = kOffX + 4 * kTile;  // of a head's 32 rows: 32 columns, 64-byte swizzled
 constexpr uint32_t kYBytes = 2 * 32 * 32;
 // A table of [stage][head], made by a dt warp; fp32, 128 tokens where not said otherwise.
 // p is the decay (log2) from the start of a token's half of the chunk up to and with it.
@@ -47,23 +48,23 @@ enum Table : uint32_t {
 constexpr uint32_t kOffTab = kOffY + 8 * kYBytes;
 constexpr uint32_t kOffBar = kOffTab + 4 * kTabBytes;
 enum Bar : uint32_t {
-  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 6, kFullTab = 8, kEmptyTab = 10, kGFull = 12, kPFull = 13,
-  kPxDone = 14, kSFull = 16, kY1Full = 17, kYRead = 18, kWFull = 19, kClean = 21, kUFull = 22, kURead = 24, kExit = 26,
-  kBars = 27
+  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 6, kFullTab = 8, kEmptyTab = 10, kGFull = 12, kPFull = 14,
+  kWFull = 16, kUFull = 18, kURead = 20, kPxDone = 22, kSFull = 23, kY1Full = 24, kYRead = 25, kClean = 26, kExit = 27,
+  kBars = 29
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
 constexpr uint32_t kTcSmem = kOffTmem + 8;
 static_assert(kTcSmem <= 232448, "shared memory of one CTA");
 
-// tensor memory, columns: G = C B^T, the heads' P (bf16 pairs), P X, and one
-// region that holds C S^T and then the state update
-constexpr uint32_t kColG = 0, kColP = 128, kColY2 = 256, kColV = 384;
+// tensor memory, columns: of every other chunk G = C B^T, P in its place (a block
+// of 32 columns becomes the two heads' 16 of bf16 pairs) and then the state update
+// in P's; P X; C S^T
+constexpr uint32_t kColG = 0, kColY2 = 256, kColY1 = 384;
 
-constexpr int kTcThreads = 768;  // one warpgroup for loader, MMA and tables, two for P, one for w X, two for y and S
-// A wait gives up after this many tries, each of which may rest for up to kTcRestNs:
-// two seconds at most, and tens of milliseconds if no try ever rests.
-constexpr uint32_t kTcTries = 1u << 21;
-constexpr uint32_t kTcRestNs = 1000;
+constexpr int kTcThreads = 1024;  // a warpgroup for loader, MMA and tables, two for P, two for w X, one for the states, two for y
+// A wait gives up after this many tries, each of which rests for up to 2700 cycles
+// (measured): after a second and a half at most.
+constexpr uint32_t kTcTries = 1u << 20;
 
 // heads: 1 or 2 a CTA; lo: the state update keeps 16 bits of w x
 const void* tc_kernel(int heads, bool lo);
