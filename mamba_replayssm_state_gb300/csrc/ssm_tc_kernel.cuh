@@ -701,72 +701,97 @@ __device__ __forceinline__ void store_column(const float2 (&S)[kDim / 2], const 
   }
 }
 
-// The heads' states.
+// One head's state, a thread per dstate column, and between its two uses the head's
+// outputs, a thread per row.
 template <int NH>
-__device__ __forceinline__ bool run_state(const Cta& c) {
+__device__ __forceinline__ bool run_state(const Cta& c, int h) {
   const TcParams& tp = c.tp;
   const Params& p = tp.p;
   Walk walk(tp, false);
   Unit w;
   uint32_t j = 0;
-  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;  // dstate column
-  const uint32_t trow0 = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + kColG;
-  const uint32_t srow = c.base + kOffX + static_cast<uint32_t>(r) * 128u;
-  const uint32_t swz = static_cast<uint32_t>(r & 7) << 4;
+  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;
+  const uint32_t lanes = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + 64 * h;
+  const uint32_t srow = c.base + kOffX + h * kTile + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(r & 7) << 4);
+  // A warp's rows leave 32 columns at a time, by a tensor-map store from shared
+  // memory: rows stored by their threads take its pipe 32 lines an instruction.
+  // 16-byte pieces of a row change places by its number / 2.
+  const uint32_t ywarp = c.base + kOffY + (4 * h + k) * kYBytes;
+  const uint32_t yput = ywarp + 64u * lane + (static_cast<uint32_t>((lane >> 1) & 3) << 4);
   while (walk.next(w)) {
-    const int64_t tile = static_cast<int64_t>(w.group) * NH * (kDim * kState) + r;
-    float2 S[NH][kDim / 2];
-    const bool say = w.group == 0 && r == 0 && !tp.states_only;
+    const int64_t tile = (static_cast<int64_t>(w.group) * NH + h) * (kDim * kState) + r;
+    float2 S[kDim / 2];
+    const bool say = w.group == 0 && h == 0 && r == 0 && !tp.states_only;
     if (w.split && !tp.states_only) {
       const float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
 #pragma unroll
-      for (int d = 0; d < NH * kDim / 2; ++d)
-        S[d / (kDim / 2)][d % (kDim / 2)] = make_float2(at[2 * d * kState], at[(2 * d + 1) * kState]);
+      for (int d = 0; d < kDim / 2; ++d) S[d] = make_float2(at[2 * d * kState], at[(2 * d + 1) * kState]);
     } else {
-      const int src = tp.states_only ? -1 : slot_of(p, p.src, w.seq, say);
-#pragma unroll
-      for (int h = 0; h < NH; ++h) load_column(S[h], p, src, tile + h * (kDim * kState));
+      load_column(S, p, tp.states_only ? -1 : slot_of(p, p.src, w.seq, say), tile);
     }
-    float decay[NH];  // of the segment, log2
-#pragma unroll
-    for (int h = 0; h < NH; ++h) decay[h] = 0.0f;
+    float decay = 0.0f;  // of the segment, log2
+    const int col = (w.group * NH + h) * kDim;
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      const uint32_t st = j & 1u;
+      const uint32_t st = j & 1u, tab = c.table(st, h);
       if (!tp.states_only) {
-        const uint32_t at = srow + 2 * (st ^ 1u) * kTile + swz;
+        const uint32_t at = srow + 2 * (st ^ 1u) * kTile;
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-#pragma unroll
-          for (uint32_t q = 0; q < 8; ++q)
-            sts128((at + h * kTile) ^ (q << 4), rsm::pack_bf16x2(S[h][4 * q].x, S[h][4 * q].y),
-                   rsm::pack_bf16x2(S[h][4 * q + 1].x, S[h][4 * q + 1].y), rsm::pack_bf16x2(S[h][4 * q + 2].x, S[h][4 * q + 2].y),
-                   rsm::pack_bf16x2(S[h][4 * q + 3].x, S[h][4 * q + 3].y));
+        for (uint32_t q = 0; q < 8; ++q)
+          sts128(at ^ (q << 4), rsm::pack_bf16x2(S[4 * q].x, S[4 * q].y), rsm::pack_bf16x2(S[4 * q + 1].x, S[4 * q + 1].y),
+                 rsm::pack_bf16x2(S[4 * q + 2].x, S[4 * q + 2].y), rsm::pack_bf16x2(S[4 * q + 3].x, S[4 * q + 3].y));
         fence_proxy_async_smem();
-        tc_fence_before();
         c.arrive_warp(kSFull);
       }
       if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
-      float a[NH];
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        a[h] = lds(c.table(st, h) + kTabMisc);
-        decay[h] += lds(c.table(st, h) + kTabMisc + 4u);
-      }
+      const float a = lds(tab + kTabMisc), m1 = lds(tab + kTabM1 + 4u * r), m2 = lds(tab + kTabM2 + 4u * r);
+      decay += lds(tab + kTabMisc + 4u);
       c.arrive_warp(kEmptyTab + st);
+      if (!tp.states_only) {
+        const float2 f1 = make_float2(m1, m1), f2 = make_float2(m2, m2);
+        if (!c.wait_warp(kPxDone, j) || !c.wait_warp(kY1Full, j)) return false;
+        tc_fence_after();
+        const int rows = w.len - c0 - 32 * k;  // of this warp's that exist
+#pragma unroll 1
+        for (uint32_t part = 0; part < 2; ++part) {
+          if (lane == 0) tma_store_wait_read();  // the last store from here
+          __syncwarp();
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) {
+            float y1[8], y2[8];
+            tmem_ld8x2(lanes + kColY1 + 32 * part + 8 * q, lanes + kColY2 + 32 * part + 8 * q, y1, y2);
+            uint32_t v[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float2 y = __ffma2_rn(f1, make_float2(y1[2 * m], y1[2 * m + 1]), __fmul2_rn(f2, make_float2(y2[2 * m], y2[2 * m + 1])));
+              v[m] = rsm::pack_bf16x2(y.x, y.y);
+            }
+            sts128(yput ^ (16u * q), v[0], v[1], v[2], v[3]);
+          }
+          if (part == 1) {
+            tc_fence_before();
+            c.arrive_warp(kYRead);
+          }
+          if (rows >= 32) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&tp.y_map, col + 32 * part, w.t0 + c0 + 32 * k, ywarp);
+          } else if (lane < rows) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(w.t0 + c0 + r) * p.out_ts + col + 32 * part);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) out[q] = rsm::lds128(yput ^ (16u * q));
+          }
+        }
+      }
       if (!c.wait_warp(kUFull + st, j >> 1)) return false;
       tc_fence_after();
-      const uint32_t trow = trow0 + 128 * st;
+      const float2 a2 = make_float2(a, a);
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const float2 a2 = make_float2(a[h], a[h]);
+      for (int q = 0; q < 4; ++q) {
+        float u[16];
+        rsm::tmem_ld16(lanes + kColG + 128 * st + 16 * q, u);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float u[8];
-          tmem_ld8(trow + 64 * h + 8 * q, u);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) S[h][4 * q + m] = __ffma2_rn(a2, S[h][4 * q + m], make_float2(u[2 * m], u[2 * m + 1]));
-        }
+        for (int m = 0; m < 8; ++m) S[8 * q + m] = __ffma2_rn(a2, S[8 * q + m], make_float2(u[2 * m], u[2 * m + 1]));
       }
       tc_fence_before();
       c.arrive_warp(kURead + st);
@@ -774,84 +799,14 @@ __device__ __forceinline__ bool run_state(const Cta& c) {
     if (tp.states_only) {
       float* at = tp.seg_state + static_cast<int64_t>(w.seg) * p.H * (kDim * kState) + tile;
 #pragma unroll
-      for (int d = 0; d < NH * kDim / 2; ++d) {
-        at[2 * d * kState] = S[d / (kDim / 2)][d % (kDim / 2)].x;
-        at[(2 * d + 1) * kState] = S[d / (kDim / 2)][d % (kDim / 2)].y;
+      for (int d = 0; d < kDim / 2; ++d) {
+        at[2 * d * kState] = S[d].x;
+        at[(2 * d + 1) * kState] = S[d].y;
       }
-      if (r == 0) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + w.group * NH + h] = decay[h];
-      }
+      if (r == 0) tp.seg_decay[static_cast<int64_t>(w.seg) * p.H + w.group * NH + h] = decay;
     } else if (w.last) {
       const int dst = slot_of(p, p.dst, w.seq, say);
-      if (dst >= 0) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) store_column(S[h], p, dst, tile + h * (kDim * kState));
-      }
-    }
-  }
-  return true;
-}
-
-// One head's outputs, a thread per row.
-template <int NH>
-__device__ __forceinline__ bool run_y(const Cta& c, int h) {
-  const TcParams& tp = c.tp;
-  const Params& p = tp.p;
-  if (tp.states_only) return true;
-  Walk walk(tp, false);
-  Unit w;
-  uint32_t j = 0;
-  const int k = c.warp & 3, lane = c.lane, r = 32 * k + lane;
-  const uint32_t trow = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + 64 * h;
-  // A warp's rows leave 32 columns at a time, by a tensor-map store from shared
-  // memory: the shared memory's rate is what the kernel lives on, and rows stored by
-  // their threads take it 32 lines an instruction.  16-byte pieces of a row change
-  // places by its number / 2.
-  const uint32_t ywarp = c.base + kOffY + (4 * h + k) * kYBytes;
-  const uint32_t yput = ywarp + 64u * lane, yswz = static_cast<uint32_t>((lane >> 1) & 3) << 4;
-  while (walk.next(w)) {
-    const int col = (w.group * NH + h) * kDim;
-#pragma unroll 1
-    for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
-      const uint32_t st = j & 1u, tab = c.table(st, h);
-      if (!c.wait_warp(kFullTab + st, j >> 1)) return false;
-      const float m1 = lds(tab + kTabM1 + 4u * r), m2 = lds(tab + kTabM2 + 4u * r);
-      c.arrive_warp(kEmptyTab + st);
-      const float2 f1 = make_float2(m1, m1), f2 = make_float2(m2, m2);
-      if (!c.wait_warp(kPxDone, j) || !c.wait_warp(kY1Full, j)) return false;
-      tc_fence_after();
-      const int rows = w.len - c0 - 32 * k;  // of this warp's that exist
-#pragma unroll 1
-      for (uint32_t part = 0; part < 2; ++part) {
-        if (lane == 0) tma_store_wait_read();  // the last store from here
-        __syncwarp();
-#pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) {
-          float y1[8], y2[8];
-          tmem_ld8x2(trow + kColY1 + 32 * part + 8 * q, trow + kColY2 + 32 * part + 8 * q, y1, y2);
-          uint32_t v[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 y = __ffma2_rn(f1, make_float2(y1[2 * m], y1[2 * m + 1]), __fmul2_rn(f2, make_float2(y2[2 * m], y2[2 * m + 1])));
-            v[m] = rsm::pack_bf16x2(y.x, y.y);
-          }
-          sts128(yput + ((16u * q) ^ yswz), v[0], v[1], v[2], v[3]);
-        }
-        if (part == 1) {
-          tc_fence_before();
-          c.arrive_warp(kYRead);
-        }
-        if (rows >= 32) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tma_store_2d(&tp.y_map, col + 32 * part, w.t0 + c0 + 32 * k, ywarp);
-        } else if (lane < rows) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(w.t0 + c0 + r) * p.out_ts + col + 32 * part);
-#pragma unroll
-          for (uint32_t q = 0; q < 4; ++q) out[q] = rsm::lds128(yput + ((16u * q) ^ yswz));
-        }
-      }
+      if (dst >= 0) store_column(S, p, dst, tile);
     }
   }
   return true;
@@ -880,17 +835,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     init(kFullX, 1, 2);
     init(kEmptyX, 1, 2);
     init(kFullTab, NH, 2);
-    init(kEmptyTab, 4 * NH + 4 + (tp.states_only ? 0 : 8 + 4 * NH), 2);  // W and S; P and y
+    init(kEmptyTab, 8 * NH + (tp.states_only ? 0 : 8), 2);  // W and S; P
     init(kGFull, 1, 2);
     init(kPFull, 8, 2);
     init(kPxDone, 1);
-    init(kSFull, 4);
+    init(kSFull, 4 * NH);
     init(kY1Full, 1);
     init(kYRead, 4 * NH);
     init(kWFull, 4 * NH, 2);
     init(kClean, 4 * NH);
     init(kUFull, 1, 2);
-    init(kURead, 4, 2);
+    init(kURead, 4 * NH, 2);
     init(kExit, 1, 2);
     rsm::fence_mbar_init();
   }
@@ -898,8 +853,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane};
-  // Registers: the launch's 8 x 64 a thread of each warpgroup, shared out anew
-  // (40 + 2 x 64 + 2 x 56 + 152 + 2 x 40 = 512): a state warp holds two columns of 64 values.
+  // Registers: the launch's 7 x 72 a thread of each warpgroup, shared out anew
+  // (40 + 2 x 64 + 2 x 56 + 2 x 112 = 504): a state warp holds columns of 64 values.
   bool ok = true;
   // no MMA may be in flight when the tensor memory is freed, whichever way its issuer ended
   auto drain = [&](uint32_t bar) {
@@ -925,13 +880,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
   } else if (warp < 20) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if ((warp - 12) / 4 < NH) ok = run_w<NH, LO>(c, (warp - 12) / 4);
-  } else if (warp < 24) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    ok = run_state<NH>(c);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if ((warp - 24) / 4 < NH) {
-      ok = run_y<NH>(c, (warp - 24) / 4);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    if ((warp - 20) / 4 < NH) {
+      ok = run_state<NH>(c, (warp - 20) / 4);
       if (lane == 0) tma_store_wait_read();  // shared memory outlives the stores that read it
     }
   }

@@ -61,7 +61,7 @@ static_assert(kTcSmem <= 232448, "shared memory of one CTA");
 // in P's; P X; C S^T
 constexpr uint32_t kColG = 0, kColY2 = 256, kColY1 = 384;
 
-constexpr int kTcThreads = 1024;  // a warpgroup for loader, MMA and tables, two for P, two for w X, one for the states, two for y
+constexpr int kTcThreads = 896;  // a warpgroup for loader, MMA and tables, two each for P, for w X, for the states and y
 // A wait gives up after this many tries, each of which rests for up to 2700 cycles
 // (measured): after a second and a half at most.
 constexpr uint32_t kTcTries = 1u << 20;
