@@ -486,16 +486,69 @@ __device__ __forceinline__ void issue_G(const Cta& c, uint32_t st) {
   tc_commit(c.bar(kGFull + st));
 }
 
-// P of the heads in 64 of its columns (`cols` 0 or 1), a thread per row; the row
-// factor 2^p is left to the output.  The warp whose blocks are all above the
-// diagonal has the time to issue G.
-template <int NH>
-__device__ __forceinline__ bool run_p(const Cta& c, int cols) {
+// 32 columns of a row by their factors.
+__device__ __forceinline__ void scale_block(const float (&g)[32], uint32_t col, uint32_t (&r)[16]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 v = lds4(col + 16u * q);
+    const float2 lo = __fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y));
+    const float2 hi = __fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w));
+    r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
+    r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
+  }
+}
+
+// A row's blocks (the one on the diagonal, or those below it) where a head's decay is
+// steep; the other head may be as usual.
+template <int NH, bool DIAG>
+__device__ __forceinline__ void steep_rows(uint32_t tab0, uint32_t trow, int k, int lane) {
+#pragma unroll 1
+  for (int b = DIAG ? k : 0; b < (DIAG ? k + 1 : k); ++b) {
+    float g[32];
+    rsm::tmem_ld32(trow + 32 * b, g);
+    const bool same = (b >> 1) == (k >> 1);
+#pragma unroll 1
+    for (int h = 0; h < NH; ++h) {
+      const uint32_t tab = tab0 + h * kTabBytes;
+      const bool steep = lds(tab + kTabMisc + 8u + 4u * (k >> 1)) != 0.0f;
+      const float pi = lds(tab + kTabCol + 4u * (32 * k + lane)), skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
+      const float ui = steep ? exp2_approx(pi) : 1.0f;
+      uint32_t r[16];
+#pragma unroll
+      for (int q = 0; q < 32; q += 2) {
+        float e[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t o = 128u * b + 4u * (q + m);
+          const bool in = !DIAG || q + m <= lane;
+          float f;
+          if (!same)
+            f = ui * lds(tab + kTabV + o);
+          else if (steep)
+            f = exp2_approx(pi - lds(tab + kTabCol + o)) * lds(tab + kTabDt + o);
+          else
+            f = lds(tab + kTabCol + o);
+          const float y = fmaf(g[q + m], f, DIAG && q + m == lane ? skip : 0.0f);
+          e[m] = in ? y : 0.0f;
+        }
+        r[q / 2] = rsm::pack_bf16x2(e[0], e[1]);
+      }
+      tmem_st16(trow + 32 * b + 16 * h, r);
+    }
+  }
+}
+
+// P of the heads, a thread per row; the row factor 2^p is left to the output.  A row's
+// warp has one block of 32 columns on the diagonal, which is one warpgroup's work
+// (DIAG), and 0 to 3 below it, which with zeros above are the other's.  The warp with
+// zeros alone has the time to issue G.
+template <int NH, bool DIAG>
+__device__ __forceinline__ bool run_p(const Cta& c) {
   const TcParams& tp = c.tp;
   if (tp.states_only) return true;
   const int k = c.warp & 3, lane = c.lane;
   const uint32_t trow0 = c.tmem + (static_cast<uint32_t>(32 * k) << 16) + kColG;
-  const bool issuer = cols == 1 && k == 0, one = elect_one();
+  const bool issuer = !DIAG && k == 0, one = elect_one();
   Walk walk(tp, false);
   Unit w;
   uint32_t j = 0;
@@ -512,69 +565,50 @@ __device__ __forceinline__ bool run_p(const Cta& c, int cols) {
       }
       if (!c.wait_warp(kFullTab + st, j >> 1) || !c.wait_warp(kGFull + st, j >> 1)) return false;
       tc_fence_after();
-#pragma unroll 1
-      for (int b = 2 * cols; b < 2 * cols + 2; ++b) {
-        if (b > k) {  // above the diagonal
-          uint32_t zero[16];
+      // whether the rows' half is steep for either head
+      const bool steep = lds(tab0 + kTabMisc + 8u + 4u * (k >> 1)) + lds(c.table(st, NH - 1) + kTabMisc + 8u + 4u * (k >> 1)) != 0.0f;
+      if (steep) {
+        steep_rows<NH, DIAG>(tab0, trow, k, lane);
+      } else if constexpr (DIAG) {
+        float g[32], gd = 0.0f;
+        rsm::tmem_ld32(trow + 32 * k, g);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) zero[i] = 0u;
-#pragma unroll
-          for (int h = 0; h < NH; ++h) tmem_st16(trow + 32 * b + 16 * h, zero);
-          continue;
+        for (int i = 0; i < 32; ++i) {  // once for the heads: what is below the diagonal, and what is on it
+          gd = i == lane ? g[i] : gd;
+          g[i] = i < lane ? g[i] : 0.0f;
         }
-        float g[32];
-        rsm::tmem_ld32(trow + 32 * b, g);
 #pragma unroll 1
         for (int h = 0; h < NH; ++h) {
           const uint32_t tab = tab0 + h * kTabBytes;
-          const bool steep = lds(tab + kTabMisc + 8u + 4u * (k >> 1)) != 0.0f;
-          const uint32_t col = tab + (k >= 2 && b < 2 ? kTabV : kTabCol) + 128u * b;
           uint32_t r[16];
-          if (!steep && b < k) {
+          scale_block(g, tab + kTabCol + 128u * k, r);
+          const float on = fmaf(gd, lds(tab + kTabCol + 4u * (32 * k + lane)), lds(tab + kTabSkip + 4u * (32 * k + lane)));
+          const uint32_t bits = rsm::pack_bf16x2(lane & 1 ? 0.0f : on, lane & 1 ? on : 0.0f);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 v = lds4(col + 16u * q);
-              const float2 lo = __fmul2_rn(make_float2(g[4 * q], g[4 * q + 1]), make_float2(v.x, v.y));
-              const float2 hi = __fmul2_rn(make_float2(g[4 * q + 2], g[4 * q + 3]), make_float2(v.z, v.w));
-              r[2 * q] = rsm::pack_bf16x2(lo.x, lo.y);
-              r[2 * q + 1] = rsm::pack_bf16x2(hi.x, hi.y);
-            }
-          } else if (!steep) {
-            const float skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 v = lds4(col + 16u * q);
-              const float f[4] = {v.x, v.y, v.z, v.w};
-              float e[4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {  // selections, not branches
-                const float on_diagonal = 4 * q + m == lane ? skip : 0.0f;
-                const float y = fmaf(g[4 * q + m], f[m], on_diagonal);
-                e[m] = 4 * q + m <= lane ? y : 0.0f;
-              }
-              r[2 * q] = rsm::pack_bf16x2(e[0], e[1]);
-              r[2 * q + 1] = rsm::pack_bf16x2(e[2], e[3]);
-            }
-          } else {
-            const float pi = lds(tab + kTabCol + 4u * (32 * k + lane));
-            const float ui = exp2_approx(pi), skip = lds(tab + kTabSkip + 4u * (32 * k + lane));
-            const bool same = (b >> 1) == (k >> 1);
-#pragma unroll
-            for (int q = 0; q < 32; q += 2) {
-              float e[2];
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                const uint32_t o = 128u * b + 4u * (q + m);
-                const bool in = b < k || q + m <= lane;
-                const float f = same ? exp2_approx(pi - lds(tab + kTabCol + o)) * lds(tab + kTabDt + o)
-                                     : ui * lds(tab + kTabV + o);
-                const float y = fmaf(g[q + m], f, b == k && q + m == lane ? skip : 0.0f);
-                e[m] = in ? y : 0.0f;
-              }
-              r[q / 2] = rsm::pack_bf16x2(e[0], e[1]);
-            }
+          for (int q = 0; q < 16; ++q) r[q] |= lane >> 1 == q ? bits : 0u;
+          tmem_st16(trow + 32 * k + 16 * h, r);
+        }
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < k; ++b) {
+          float g[32];
+          rsm::tmem_ld32(trow + 32 * b, g);
+#pragma unroll 1
+          for (int h = 0; h < NH; ++h) {
+            uint32_t r[16];
+            scale_block(g, tab0 + h * kTabBytes + (k >= 2 && b < 2 ? kTabV : kTabCol) + 128u * b, r);
+            tmem_st16(trow + 32 * b + 16 * h, r);
           }
-          tmem_st16(trow + 32 * b + 16 * h, r);
+        }
+      }
+      if constexpr (!DIAG) {
+        uint32_t zero[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0u;
+#pragma unroll 1
+        for (int b = k + 1; b < 4; ++b) {
+          tmem_st16(trow + 32 * b, zero);
+          if (NH == 2) tmem_st16(trow + 32 * b + 16, zero);
         }
       }
       rsm::tmem_st_wait();
@@ -854,7 +888,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
   tc_fence_after();
   const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane};
   // Registers: the launch's 7 x 72 a thread of each warpgroup, shared out anew
-  // (40 + 2 x 64 + 2 x 56 + 2 x 112 = 504): a state warp holds columns of 64 values.
+  // (40 + 2 x 72 + 2 x 56 + 2 x 104 = 504): a state warp holds columns of 64 values.
   bool ok = true;
   // no MMA may be in flight when the tensor memory is freed, whichever way its issuer ended
   auto drain = [&](uint32_t bar) {
@@ -874,14 +908,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
       ok = run_tables<NH>(c, warp - 2);
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    ok = run_p<NH>(c, (warp - 4) / 4);
-    if (warp == 8) drain(kExit + 1);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    ok = warp < 8 ? run_p<NH, false>(c) : run_p<NH, true>(c);
+    if (warp == 4) drain(kExit + 1);
   } else if (warp < 20) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if ((warp - 12) / 4 < NH) ok = run_w<NH, LO>(c, (warp - 12) / 4);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if ((warp - 20) / 4 < NH) {
       ok = run_state<NH>(c, (warp - 20) / 4);
       if (lane == 0) tma_store_wait_read();  // shared memory outlives the stores that read it
