@@ -53,7 +53,9 @@ enum Bar : uint32_t {
   kBars = 29
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
-constexpr uint32_t kTcSmem = kOffTmem + 8;
+constexpr uint32_t kOffOrder = kOffTmem + 8;  // the sequences, longest first, if they are few
+constexpr int kSorted = 32;
+constexpr uint32_t kTcSmem = kOffOrder + 4 * kSorted;
 static_assert(kTcSmem <= 232448, "shared memory of one CTA");
 
 // tensor memory, columns: of every other chunk G = C B^T, P in its place (a block
