@@ -31,8 +31,8 @@
  * [num_heads, dim, dstate], contiguous; slots are state_slot_stride elements apart.
  *
  * A value that is not finite spreads to where the recurrence takes it, and may
- * also reach earlier tokens of its own chunk of up to 128 tokens of a prompt; it
- * never reaches another sequence, request or head of another group.
+ * also reach earlier tokens of its own chunk of up to 128 tokens of a prompt, or of
+ * its own call where the new tokens are several; it never reaches another sequence, request or head of another group.
  */
 #ifndef REPLAYSSM_BLOCK_H
 #define REPLAYSSM_BLOCK_H
