@@ -228,24 +228,25 @@ int64_t workspace_bytes(const PrefillPlan& pl, int H) {
 // more cost about three chunks.  One prompt of 32768 tokens and 80 heads: 40 units of
 // 256 chunks on 152 SMs without the cut.
 PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
-  PrefillPlan pl;
-  pl.heads = a->num_heads / a->num_groups % 2 == 0 ? 2 : 1;
-  pl.pairs = a->num_heads / pl.heads;
-  pl.seg = 0x7FFFFF80u;
-  pl.segs = 0;
+  PrefillPlan pl{};
   const int64_t chunks = (a->tokens + static_cast<int64_t>(a->num_seqs) * ssm::kChunk - 1) /
                          (static_cast<int64_t>(a->num_seqs) * ssm::kChunk);
-  const int64_t units = static_cast<int64_t>(a->num_seqs) * pl.pairs;
-  auto waves = [&](int64_t n) { return static_cast<double>((n + sms - 1) / sms); };
-  double best = waves(units) * (static_cast<double>(chunks) + 0.5);
-  for (int64_t n = 2; n <= 64 && n <= chunks; ++n) {
-    const int64_t per = (chunks + n - 1) / n;
-    const double t = waves(units * n) * (static_cast<double>(per) + 0.5) +
-                     waves(units * (n - 1)) * (0.45 * static_cast<double>(per) + 0.5) + 3.0;
-    if (t < best) {
+  double best = 1e300;
+  for (int heads = a->num_heads / a->num_groups % 2 == 0 ? 2 : 1; heads >= 1; --heads) {
+    const int pairs = a->num_heads / heads;
+    const int64_t units = static_cast<int64_t>(a->num_seqs) * pairs;
+    const double chunk = heads == 2 ? 1.0 : 0.83;
+    auto pass = [&](int64_t n, double per) { return static_cast<double>((n + sms - 1) / sms) * (per + 0.7); };
+    for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(chunks, 1); ++n) {
+      const int64_t per = (chunks + n - 1) / n;
+      double t = pass(units * n, chunk * static_cast<double>(per));
+      if (n > 1) t += pass(units * (n - 1), 0.5 * chunk * static_cast<double>(per)) + 5.0;
+      if (t >= best) continue;
       best = t;
-      pl.seg = static_cast<uint32_t>(per * ssm::kChunk);
-      pl.segs = a->tokens / pl.seg + a->num_seqs;  // no more than this, however the lengths fall
+      pl.heads = heads;
+      pl.pairs = pairs;
+      pl.seg = n == 1 ? 0x7FFFFF80u : static_cast<uint32_t>(per * ssm::kChunk);
+      pl.segs = n == 1 ? 0 : a->tokens / pl.seg + a->num_seqs;  // no more than this, however the lengths fall
     }
   }
   return pl;

@@ -65,6 +65,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// into L2
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
                "r"(y), "r"(src)
@@ -311,6 +315,9 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
       const int row = w.t0 + c0;
+      if (one) {  // the stages are taken yet, but x can come nearer
+        for (int h = 0; h < NH; ++h) tma_prefetch_2d(&tp.x_map, (h0 + h) * kDim, row);
+      }
       if (j >= 2 && !(ok = c.wait_warp(kEmptyBC + st, (j >> 1) - 1u))) break;
       if (one) {
         const uint32_t bc = c.bar(kFullBC + st);
