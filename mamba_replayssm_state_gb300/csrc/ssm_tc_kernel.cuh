@@ -69,6 +69,9 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
                "r"(y), "r"(src)
@@ -311,6 +314,15 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
   bool ok = true;
   while (ok && walk.next(w)) {
     const int h0 = w.group * NH, g = static_cast<int>(static_cast<uint32_t>(h0) / per_group);
+    if (one && !tp.states_only && !w.split) {  // the state it starts from is wanted in a chunk or two
+      const int src = slot_of(tp.p, tp.p.src, w.seq, false);
+      if (src >= 0) {
+        const uint32_t size = tp.p.state_dtype == RSM_F32 ? 4u : 2u;
+        const char* at = static_cast<const char*>(tp.p.state) +
+                         (src * tp.p.state_ss + static_cast<int64_t>(h0) * (kDim * kState)) * static_cast<int64_t>(size);
+        if (reinterpret_cast<uintptr_t>(at) % 16 == 0) prefetch_l2(at, NH * kDim * kState * size);
+      }
+    }
 #pragma unroll 1
     for (int c0 = 0; c0 < w.len; c0 += kChunk, ++j) {
       const uint32_t st = j & 1u;
