@@ -196,10 +196,12 @@ bool rows_aligned(const void* base, int64_t stride, int64_t cols, int64_t tokens
          (tokens == 1 || (stride >= cols && stride < (int64_t{1} << 38) && stride % 8 == 0));
 }
 
-// bf16 prompts with 64 x 128 states whose rows the tensor maps can address;
-// the rest runs on the sequential kernel.
+// bf16 prompts with 64 x 128 states whose rows the tensor maps can address; the rest
+// runs on the sequential kernel, and so do the fewest tokens, which it has done before a
+// chunk has gone round.  (One sequence, 80 heads: 1, 4, 8, 16 and 2048 tokens take 6.1, 8.2,
+// 11.1, 17 and 1561 us there, 10.5 to 11.6 and 42 on the tensor cores.)
 bool uses_tensor_cores(const rsm_ssm_prefill_args* a) {
-  return a->input_dtype == RSM_BF16 && a->dim == ssm::kDim && a->dstate == ssm::kState && a->tokens > 0 &&
+  return a->input_dtype == RSM_BF16 && a->dim == ssm::kDim && a->dstate == ssm::kState && a->tokens > 7 &&
          a->tokens < 0x7FFFFF00LL && static_cast<int64_t>(a->num_heads) * ssm::kState <= 0x7FFFFFFFLL;
 }
 bool tensor_maps_fit(const rsm_ssm_prefill_args* a) {
@@ -220,13 +222,14 @@ int64_t workspace_bytes(const PrefillPlan& pl, int H) {
   return pl.segs * H * (ssm::kDim * ssm::kState + 1) * 4;
 }
 
-// Whether the sequences are cut into segments, whose states then come from a
-// pass of their own (x and B read twice, no outputs) and a join.  Lengths are on
-// the device, so sequences are taken as equally long.  Times are in chunks of one
-// CTA: a unit (a segment of a head group) takes its chunks and half a chunk to
-// begin and end; a states-only chunk measured 0.45 of a whole one; the two launches
-// more cost about three chunks.  One prompt of 32768 tokens and 80 heads: 40 units of
-// 256 chunks on 152 SMs without the cut.
+// How many heads a CTA takes, and whether the sequences are cut into segments, whose
+// states then come from a pass of their own (x and B read twice, no outputs) and a join.
+// Lengths are on the device, so sequences are taken as equally long.  Times are in chunks
+// of a CTA with two heads, about 3.3 us, and measured: a chunk of one head 0.83; a
+// states-only chunk half of a whole one; a unit (a segment of a head group) takes 0.7 to
+// begin and end; the two launches more about five.  80 heads: one sequence of 32768 tokens
+// takes 386 us cut, where 40 units of 256 chunks on 152 SMs would take 850; one of 1024
+// takes 23.7 us with a head a CTA and 31.5 with two.
 PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
   PrefillPlan pl{};
   const int64_t chunks = (a->tokens + static_cast<int64_t>(a->num_seqs) * ssm::kChunk - 1) /
@@ -310,6 +313,11 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
 
 // New tokens: 64 x 128 states whose rows are whole vectors, up to 16 tokens a
 // request; the rest runs on the sequential kernel.
+// The token kernel for 64 x 128 states on 16 bytes and up to 16 new tokens, the sequential
+// kernel for the rest.  (Ring of 16, 4 new tokens, 64 requests of 256 heads, bf16: 52 us
+// and 603; one token to the state itself: 93 and 578; one request of 80 heads, fp32: 6.7
+// and 8.7.)  The ring form's products go to the tensor cores where the state is exact in
+// bf16: 52 us there, 108 for fp16 states of the same size, which are not.
 int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* stream) {
   const int es = p.state_dtype == RSM_F32 ? 4 : p.state_dtype == RSM_BF16 || p.state_dtype == RSM_F16 ? 2 : 1;
   const bool fits = dim == ssm::kDim && dstate == ssm::kState && p.window <= ssm::kTokenMaxNew &&

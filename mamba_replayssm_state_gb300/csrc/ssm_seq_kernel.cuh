@@ -9,8 +9,9 @@
 // output is a sum over its four threads (two shuffles).
 //
 // It serves every size, type and stride: prompts whose inputs are fp32 or
-// whose state is not 64 x 128, and unaligned slices.  A token costs about 2
-// dim dstate FMAs on one SM with nothing to overlap them but other heads.
+// whose state is not 64 x 128, unaligned slices, and the shortest.  What bounds it is
+// the way through a token, 0.75 us (one sequence of 2048 tokens, 80 heads of 64 x 128:
+// 1561 us): 2 dim dstate FMAs on one SM with nothing to overlap them but other heads.
 #pragma once
 #include <cuda_runtime.h>
 

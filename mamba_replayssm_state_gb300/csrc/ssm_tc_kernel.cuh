@@ -16,23 +16,25 @@
 // product an element, no exponential), the row factor onto Y2 when y = m1 Y1 + m2
 // Y2 leaves.  A pair across the halves is e^{p_i} e^{rest of the first half}.  e^{-p}
 // would overflow in a half that decays by more than 2^100 ("steep", a mean dt A
-// above 1.08): its rows take an exponential of p_i - p_j an element instead.  Sums
-// run inside blocks of 32 tokens first, so small decays keep their precision
-// next to large ones, and weights towards a chunk's end are summed from there.
+// above 1.08): its rows take an exponential of p_i - p_j an element instead.  The
+// weights towards a chunk's end are summed from there, so that small decays near it
+// keep their precision next to large ones before them.
 //
-// One persistent CTA per SM takes units (sequence, segment, two heads of one
-// group; one head where a group has an odd number), all chunks of a unit in order:
+// One persistent CTA per SM takes units (sequence, segment, two heads of one group; one
+// head where a group has an odd number or SMs would idle), all chunks of a unit in order:
 //   warp 0       loads C, B and x (two stages each) with tensor-map copies
-//   warp 1       issues the MMAs; warps 2, 3 make the decay tables, a head each
-//   warps 4-11   P, four warps the columns of either half: a thread holds row i, and
-//                puts the heads' P where it read G
-//   warps 12-15  w X: a thread holds token t's row; x becomes w x in place
-//   warps 16-19  the state in registers as fp32, a thread per dstate column, and its
-//                bf16 copy for Y1
-//   warps 20-27  four a head: y out of Y1 and Y2
-// What bounds it is the way round: G to P to Y2 to the next G, and Y1 to y to the
-// next Y1, each about 3000 cycles a chunk and pair of heads, of which the four
-// products are 2050 (2560 with lo).
+//   warp 1       issues the MMAs but G; warps 2, 3 make the decay tables, a head each
+//   warps 4-7    P below the diagonal: a thread holds row i, and puts the heads' P where
+//                it read G; warp 4 has no such block and issues G
+//   warps 8-11   P's blocks on the diagonal
+//   warps 12-19  w X, a head each four: a thread holds token t's row; x becomes w x in place
+//   warps 20-27  a head each four: the state in registers as fp32, a thread per dstate
+//                column, and its bf16 copy for Y1; between the two, y out of Y1 and Y2
+// What bounds it is latency, the way round of a chunk: U to the next load of B and C, G,
+// P, Y2, w X and U again (bf16 states), and S to Y1 to lo to U to S (others).  Measured on
+// a GB300: a chunk and pair of heads takes 2.8 us with bf16 states and 3.3 with fp32 ones
+// (5400 and 6300 cycles), of which the four products are 2050 and 2560 cycles; 4
+// sequences of 8192 tokens in all, 256 heads, bf16 states: 177 us, 390 TFLOP/s.
 // A sequence's last chunk may be partial: dt counts as 0 there, and the rows of
 // x and B past its end, which are a neighbour's or nobody's, are cleared
 // before an MMA multiplies them by 0.

@@ -7,7 +7,11 @@
 // so the state is read once, whatever T and the ring's length, and the dots B_s .
 // C_t belong to the group, not the head.
 //
-// Memory bounds both: the states' bytes, once (ring form) or once each way.  A CTA
+// Memory bounds both: the states' bytes, once (ring form) or once each way.  Measured on
+// a GB300, 256 requests of 256 heads, bf16: one token to the state itself 343 us, 6.3
+// TB/s; one token after a ring of 8 174 us, 6.4 TB/s.  Instructions bound one-byte states
+// (64 requests, 4 tokens, int8: 55 us, 3.2 TB/s), and several tokens of the recurrent form
+// or of fp16 and fp32 states, at 2.7 to 3.7 TB/s.  A CTA
 // takes heads of one request and group.  One round of loads stages what their
 // tokens need; then four warps share a head, 16 dim rows each, and go through the
 // CTA's heads two at a time, asking for the next head's rows as soon as the last's
