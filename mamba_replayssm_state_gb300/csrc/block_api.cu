@@ -329,12 +329,16 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
   const bool step = p.mode == ssm::kStep;
   const int ie = input_dtype == RSM_F32 ? 4 : 2, hpg = p.H / p.G;
   p.tokens_max = step ? p.window : std::min(p.R, ssm::kTokenMaxAll);
+  const bool exact = p.state_dtype != RSM_F32 && p.state_dtype != RSM_F16;  // in bf16
+  const bool tc = input_dtype == RSM_BF16 && (step ? p.window > 1 && p.window <= 8 : exact || p.window > 1);
+  const int mode = step ? (tc ? 5 : p.window == 1 ? 1 : 2) : !tc ? 0 : p.window <= 8 ? 3 : 4;
   // rows of a head's x or a group's B start on 16 bytes wherever they are
   auto even = [&](const void* base, int64_t bs, int64_t ts) {
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (p.units == 1 || bs * ie % 16 == 0) && (p.window == 1 || ts * ie % 16 == 0);
   };
   p.wide = even(p.x, p.x_bs, p.x_ts) &&
-           (step || (even(p.B, p.B_bs, p.B_ts) && even(p.C, p.C_bs, p.C_ts) && reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
+           ((step && !tc) || (even(p.B, p.B_bs, p.B_ts) && even(p.C, p.C_bs, p.C_ts))) &&
+           (step || (reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(p.B_cache) % 16 == 0 && p.Bc_ss * ie % 16 == 0));
   // A CTA works on two heads at a time.  Many heads in all: as many a CTA, up to
   // sixteen, as leave eight CTAs an SM, since a CTA's first loads wait for nothing to
@@ -343,8 +347,6 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
   int per = 2;
   while (per < ssm::kTokenMaxHeads && static_cast<int64_t>(p.units) * p.H / (2 * per) >= 8 * static_cast<int64_t>(sms)) per *= 2;
   per = std::min(per, hpg);
-  const int mode = step ? (p.window == 1 ? 1 : 2)
-                   : input_dtype == RSM_BF16 && p.state_dtype != RSM_F32 && p.state_dtype != RSM_F16 ? (p.window <= 8 ? 3 : 4) : 0;
   auto smem = [&](int n) { return ssm::token_smem(mode, ie, n, p.window, p.tokens_max); };
   while (per > 1 && smem(per) > 75 * 1024) per = (per + 1) / 2;
   p.heads_per_cta = per;

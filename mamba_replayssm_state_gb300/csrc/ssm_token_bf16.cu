@@ -5,22 +5,17 @@ namespace ssm {
 
 namespace {
 template <int SF>
-const void* pick_step(int mode) {
-  if constexpr (SF == RSM_F32 || SF == RSM_BF16 || SF == RSM_F16)
-    return mode == 1 ? reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 1>)
-                     : reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 2>);
-  return nullptr;
-}
-
-// The ring form is on the tensor cores wherever the state's elements are exact in bf16.
-template <int SF>
 const void* pick(int mode) {
-  if constexpr (SF == RSM_BF16 || SF == RSM_I8 || SF == RSM_FP8_E4M3)
-    return mode == 0 ? nullptr : mode == 3 ? reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 3>)
-                     : mode == 4  ? reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 4>)
-                                  : pick_step<SF>(mode);
-  else
-    return mode == 0 ? reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 0>) : mode >= 3 ? nullptr : pick_step<SF>(mode);
+  if (mode == 3) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 3>);
+  if (mode == 4) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 4>);
+  if constexpr (SF == RSM_F32 || SF == RSM_BF16 || SF == RSM_F16) {
+    if (mode == 1) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 1>);
+    if (mode == 2) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 2>);
+    if (mode == 5) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 5>);
+  }
+  // (one token after a ring: where the state is exact in bf16, on the tensor cores too)
+  if constexpr (SF == RSM_F32 || SF == RSM_F16) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 0>);
+  return nullptr;
 }
 }  // namespace
 

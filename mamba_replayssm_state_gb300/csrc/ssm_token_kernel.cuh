@@ -213,7 +213,8 @@ __device__ __forceinline__ float as_float(uint16_t v) { return __uint_as_float(s
 // through fp32.  Its pairs are bytes 0 and 2, then 1 and 3, of each word.
 template <int SF>
 __device__ __forceinline__ constexpr int pair_at(int i, int tq) {
-  return SF == RSM_BF16 ? 32 * (i >> 2) + 8 * tq + 2 * (i & 3)
+  return SF == RSM_F32 ? 16 * (i >> 1) + 4 * tq + 2 * (i & 1)
+       : SF == RSM_BF16 || SF == RSM_F16 ? 32 * (i >> 2) + 8 * tq + 2 * (i & 3)
                         : 64 * (i >> 3) + 16 * tq + 4 * ((i >> 1) & 3) + (i & 1) * (SF == RSM_I8 ? 1 : 2);
 }
 template <int SF>
@@ -229,6 +230,27 @@ __device__ __forceinline__ void word_pairs(uint32_t w, uint32_t& a, uint32_t& b)
   }
 }
 
+// Pair i of a lane's share of a row of a wider state, and as bf16 hi + lo: exact for
+// fp16, within 2^-17 for fp32.
+template <int SF, int P>
+__device__ __forceinline__ float2 state_pair(const uint4 (&row)[P], int i) {
+  if constexpr (SF == RSM_F32) {
+    const uint4 u = row[i >> 1];
+    return i & 1 ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w)) : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  } else {
+    const uint4 u = row[i >> 2];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (SF == RSM_F16)
+      return rsm::f16x2_to_f32(w[i & 3]);
+    else
+      return make_float2(rsm::bf16lo(w[i & 3]), rsm::bf16hi(w[i & 3]));
+  }
+}
+__device__ __forceinline__ void split_pair(float2 v, uint32_t& hi, uint32_t& lo) {
+  hi = rsm::pack_bf16x2(v.x, v.y);
+  lo = rsm::pack_bf16x2(v.x - rsm::bf16lo(hi), v.y - rsm::bf16hi(hi));
+}
+
 // D += A B: 16 rows x 16 k, 16 k x 8 columns, bf16 in, fp32 sums
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -240,13 +262,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // MODE: 0 the ring form, 1 one new token a request, state to state, 2 several; 3
-// and 4 the ring form on the tensor cores, up to 8 and up to 16 new tokens.
+// and 4 the ring form on the tensor cores, up to 8 and up to 16 new tokens; 5 up to 8
+// new tokens, state to state, in the ring form with an empty ring.
 template <typename IT, int SF, int MODE>
-__global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MODE == 2 || MODE == 4 ? 2 : 3) ssm_token_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MODE == 2 || MODE >= 4 ? 2 : 3) ssm_token_kernel(const __grid_constant__ Params p) {
   constexpr int ES = SF == RSM_F32 ? 4 : (SF == RSM_BF16 || SF == RSM_F16) ? 2 : 1;
   constexpr int D = kTokD, N = kTokN;
   constexpr bool STEP = MODE == 1 || MODE == 2;
-  constexpr bool MMA = MODE >= 3;
+  constexpr bool MMA = MODE >= 3, KEEP = MODE == 5;  // on the tensor cores; whose states are stored
   constexpr int NT = MODE == 4 ? 2 : 1;  // eights of new tokens
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -259,14 +282,14 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
   const bool say = g == 0 && part == 0 && tid == 0;
 
   int n_ring = 0, ring0 = 0;
-  if constexpr (!STEP) {
+  if constexpr (!STEP && !KEEP) {
     ring0 = __ldg(p.ring_start + b);
     n_ring = __ldg(p.ring_len + b);
   }
   const int src = slot_of(p, p.src, b, say);
   int dst = src;
   bool live = src >= 0;
-  if constexpr (STEP) {
+  if constexpr (STEP || KEEP) {
     if (p.dst != nullptr) dst = slot_of(p, p.dst, b, say);
   }
   // this lane's eight columns of its warp's row pairs, in a head's tile (tensor
@@ -295,7 +318,7 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
     }
   };
   if (live) load_head(warp >> 2);
-  if constexpr (!STEP) {
+  if constexpr (!STEP && !KEEP) {
     if (live) {
       uint32_t bad = 0;
       if (ring0 < 0 || ring0 >= p.R) bad |= RSM_STATUS_BAD_RING_START;
@@ -368,10 +391,12 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
     __syncthreads();
 
     // the new tokens join the ring, B once for the group
-    put_rows(sx + n_ring * xs, xs, T, nh * D, wide, [&](int t) { return xc + ring_row(n_ring + t) * xrow; });
-    if (part == 0) put_rows(sB + n_ring * BS, BS, T, N, wide, [&](int t) { return Bc + ring_row(n_ring + t) * Brow; });
-    for (int t = tid >> 4; t < T; t += kTokThreads / 16)
-      if (hq < nh) dtc[ring_row(n_ring + t) * p.H + hq] = sdt[(n_ring + t) * nh + hq];
+    if constexpr (!KEEP) {
+      put_rows(sx + n_ring * xs, xs, T, nh * D, wide, [&](int t) { return xc + ring_row(n_ring + t) * xrow; });
+      if (part == 0) put_rows(sB + n_ring * BS, BS, T, N, wide, [&](int t) { return Bc + ring_row(n_ring + t) * Brow; });
+      for (int t = tid >> 4; t < T; t += kTokThreads / 16)
+        if (hq < nh) dtc[ring_row(n_ring + t) * p.H + hq] = sdt[(n_ring + t) * nh + hq];
+    }
 
     // the decays up to and with each token; the dots B_s . C_t
     if (hq < nh) {
@@ -480,6 +505,16 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
         cf[nt][i + 1] = t < T ? v[1] : 0u;
       }
     }
+    uint32_t bf[KEEP ? 16 : 1];  // tokens' B likewise, for the update: k is the token, twice
+    if constexpr (KEEP) {
+      const uint16_t* bt = reinterpret_cast<const uint16_t*>(smem + l.B) + 2 * tq * tok_B_row(MODE) + (gq & 1);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int el = pair_at<SF>(i, gq >> 1);
+        const uint32_t lo = 2 * tq < T ? bt[el] : 0u, hi = 2 * tq + 1 < T ? bt[tok_B_row(MODE) + el] : 0u;
+        bf[i] = lo | hi << 16;
+      }
+    }
     const uint16_t* sw = reinterpret_cast<const uint16_t*>(smem + l.w);
     // rows of x for ldmatrix: lanes 0-7 tokens 0-7, columns 0-7; 8-15 columns 8-15; 16-31 tokens 8-15
     const uint32_t xm = rsm::smem_addr(sx) + 2u * (((lane & 7) + ((lane >> 4) << 3)) * xs + kTokRows * (warp & 3) + 8 * ((lane >> 3) & 1));
@@ -496,25 +531,79 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
         scale[0] = __ldg(sc);
         scale[1] = __ldg(sc + 8);
       }
+      if constexpr (SF == RSM_F32 || SF == RSM_F16) {
 #pragma unroll
-      for (int c = 0; c < kPieces; ++c) {
-        const uint4 r0 = rows[0][c], r1 = rows[1][c];
-        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-        if constexpr (ES == 2) {
+        for (int i = 0; i < 16; i += 2) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int q = 0; q < 4; ++q) split_pair(state_pair<SF>(rows[q & 1], i + (q >> 1)), hi[q], lo[q]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(acc[nt], w0[2 * k], w1[2 * k], w0[2 * k + 1], w1[2 * k + 1], cf[nt][4 * c + 2 * k], cf[nt][4 * c + 2 * k + 1]);
-        } else {
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(acc[nt], hi[0], hi[1], hi[2], hi[3], cf[nt][i], cf[nt][i + 1]);
+            mma16816(acc[nt], lo[0], lo[1], lo[2], lo[3], cf[nt][i], cf[nt][i + 1]);
+          }
+        }
+      } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t a0, a1, a2, a3;
-            word_pairs<SF>(w0[k], a0, a2);
-            word_pairs<SF>(w1[k], a1, a3);
+        for (int c = 0; c < kPieces; ++c) {
+          const uint4 r0 = rows[0][c], r1 = rows[1][c];
+          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+          if constexpr (ES == 2) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(acc[nt], a0, a1, a2, a3, cf[nt][8 * c + 2 * k], cf[nt][8 * c + 2 * k + 1]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(acc[nt], w0[2 * k], w1[2 * k], w0[2 * k + 1], w1[2 * k + 1], cf[nt][4 * c + 2 * k], cf[nt][4 * c + 2 * k + 1]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t a0, a1, a2, a3;
+              word_pairs<SF>(w0[k], a0, a2);
+              word_pairs<SF>(w1[k], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(acc[nt], a0, a1, a2, a3, cf[nt][8 * c + 2 * k], cf[nt][8 * c + 2 * k + 1]);
+            }
+          }
+        }
+      }
+      if constexpr (KEEP) {
+        // S <- e^{c_last} S + sum_s (e^{c_last - c_s} dt_s x_s) (x) B_s, a product over the tokens: w x as
+        // bf16 hi in k = 0..7 and lo in 8..15 (16 bits), the decays after a token summed from the end
+        const float A = __ldg(p.A + h0 + hl), e = se[hl * T + T - 1];
+        float after = 0.0f, w0 = 0.0f, w1 = 0.0f;
+        for (int s = T - 1; s >= 0; --s) {
+          const float d = sdt[s * nh + hl];
+          if (s == 2 * tq) w0 = expf(after * A) * d;
+          if (s == 2 * tq + 1) w1 = expf(after * A) * d;
+          after += d;
+        }
+        const IT* xr = sx + 2 * tq * xs + hl * D + kTokRows * (warp & 3) + gq;  // (past T: zeros)
+        uint32_t a[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          split_pair(make_float2(w0 * as_float(xr[8 * q]), w1 * as_float(xr[xs + 8 * q])), a[q], a[q + 2]);
+        unsigned char* to = static_cast<unsigned char*>(p.state) + dst * p.state_ss * ES + off + hl * kTileBytes;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+          uint32_t out0[4], out1[4];
+#pragma unroll
+          for (int q = 0; q < 8 / ES; ++q) {
+            const int i = (8 / ES) * c + q;
+            const float2 r0 = state_pair<SF>(rows[0], i), r1 = state_pair<SF>(rows[1], i);
+            float v[4] = {e * r0.x, e * r0.y, e * r1.x, e * r1.y};
+            mma16816(v, a[0], a[1], a[2], a[3], bf[i], bf[i]);
+            if constexpr (SF == RSM_F32) {
+              out0[2 * q] = __float_as_uint(v[0]), out0[2 * q + 1] = __float_as_uint(v[1]);
+              out1[2 * q] = __float_as_uint(v[2]), out1[2 * q + 1] = __float_as_uint(v[3]);
+            } else {
+              out0[q] = SF == RSM_F16 ? rsm::pack_f16x2(v[0], v[1]) : rsm::pack_bf16x2(v[0], v[1]);
+              out1[q] = SF == RSM_F16 ? rsm::pack_f16x2(v[2], v[3]) : rsm::pack_bf16x2(v[2], v[3]);
+            }
+          }
+          if (dst >= 0) {
+            *reinterpret_cast<uint4*>(to + 64 * c) = make_uint4(out0[0], out0[1], out0[2], out0[3]);
+            *reinterpret_cast<uint4*>(to + 8 * N * ES + 64 * c) = make_uint4(out1[0], out1[1], out1[2], out1[3]);
           }
         }
       }
