@@ -316,8 +316,12 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
 // The token kernel for 64 x 128 states on 16 bytes and up to 16 new tokens, the sequential
 // kernel for the rest.  (Ring of 16, 4 new tokens, 64 requests of 256 heads, bf16: 52 us
 // and 603; one token to the state itself: 93 and 578; one request of 80 heads, fp32: 6.7
-// and 8.7.)  The ring form's products go to the tensor cores where the state is exact in
-// bf16: 52 us there, 108 for fp16 states of the same size, which are not.
+// and 8.7.)  With bf16 inputs the products go to the tensor cores, but for a single
+// token of the recurrent form, whose lanes keep up with the memory, or after a ring on
+// fp16 states, which cost more to split than they save.  (64 requests of 256 heads, 4
+// tokens after a ring of 16, fp16: 58 us and 108; 32 requests, fp32, 4 tokens: 59 and
+// 118, one after a ring of 8: 54 and 63; 64 requests, fp16, one after a ring of 8: 55
+// and 48; to the states: 4 tokens, bf16, 116 and 190, one, fp16, 136 and 94.)
 int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* stream) {
   const int es = p.state_dtype == RSM_F32 ? 4 : p.state_dtype == RSM_BF16 || p.state_dtype == RSM_F16 ? 2 : 1;
   const bool fits = dim == ssm::kDim && dstate == ssm::kState && p.window <= ssm::kTokenMaxNew &&
@@ -329,8 +333,7 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
   const bool step = p.mode == ssm::kStep;
   const int ie = input_dtype == RSM_F32 ? 4 : 2, hpg = p.H / p.G;
   p.tokens_max = step ? p.window : std::min(p.R, ssm::kTokenMaxAll);
-  const bool exact = p.state_dtype != RSM_F32 && p.state_dtype != RSM_F16;  // in bf16
-  const bool tc = input_dtype == RSM_BF16 && (step ? p.window > 1 && p.window <= 8 : exact || p.window > 1);
+  const bool tc = input_dtype == RSM_BF16 && (step ? p.window > 1 && p.window <= 8 : p.window > 1 || p.state_dtype != RSM_F16);
   const int mode = step ? (tc ? 5 : p.window == 1 ? 1 : 2) : !tc ? 0 : p.window <= 8 ? 3 : 4;
   // rows of a head's x or a group's B start on 16 bytes wherever they are
   auto even = [&](const void* base, int64_t bs, int64_t ts) {

@@ -13,8 +13,7 @@ const void* pick(int mode) {
     if (mode == 2) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 2>);
     if (mode == 5) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 5>);
   }
-  // (one token after a ring: where the state is exact in bf16, on the tensor cores too)
-  if constexpr (SF == RSM_F32 || SF == RSM_F16) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 0>);
+  if constexpr (SF == RSM_F16) return reinterpret_cast<const void*>(&ssm_token_kernel<uint16_t, SF, 0>);
   return nullptr;
 }
 }  // namespace

@@ -9,22 +9,24 @@
 //
 // Memory bounds both: the states' bytes, once (ring form) or once each way.  Measured on
 // a GB300, 256 requests of 256 heads, bf16: one token to the state itself 343 us, 6.3
-// TB/s; one token after a ring of 8 174 us, 6.4 TB/s.  Instructions bound one-byte states
-// (64 requests, 4 tokens, int8: 55 us, 3.2 TB/s), and several tokens of the recurrent form
-// or of fp16 and fp32 states, at 2.7 to 3.7 TB/s.  A CTA
+// TB/s; one token after a ring of 8 174 us, 6.4 TB/s; 64 requests: 4 tokens to the state
+// 116 us, 4.6 TB/s, 4 after a ring of 16 52 us, 5.2 TB/s.  Instructions bound one-byte
+// states (64 requests, 4 tokens, int8: 55 us, 3.2 TB/s).  A CTA
 // takes heads of one request and group.  One round of loads stages what their
 // tokens need; then four warps share a head, 16 dim rows each, and go through the
 // CTA's heads two at a time, asking for the next head's rows as soon as the last's
 // have had their use.
 //
-// The ring form with bf16 inputs and bf16, int8 or fp8 states takes its products on
-// the tensor cores (mma.sync m16n8k16: 16 rows, 8 tokens; such states' elements are
-// exact in bf16, so only the weights of the ring's tokens are rounded).  A lane takes 16
+// With bf16 inputs the products are on the tensor cores (mma.sync m16n8k16: 16 rows, 8
+// tokens), the state as bf16: exact for bf16, int8 and fp8, as hi + lo for fp16 (exact)
+// and fp32 (within 2^-17); only the weights of the tokens are rounded.  Several tokens to
+// the state itself are an empty ring's, and the update one product more.  A lane takes 16
 // bytes of a row at a time, k being numbered to suit.  (Rows through shared memory by
 // bulk copies, two or three heads ahead, measured slower: what they take of it is CTAs,
 // and with them the heads in whose time another CTA's staging passes.)
 //
-// Otherwise a lane holds eight dstate columns of eight rows: sixteen lanes to a
+// Otherwise (fp32 inputs, one token to the state, one after a ring on fp16 states, more
+// than eight to the state) a lane holds eight dstate columns of eight rows: sixteen lanes to a
 // row, a 16-byte load (16-bit states) an instruction and two rows.  Sums over a
 // row's sixteen lanes are taken for eight rows at once, halving the values at each
 // exchange: eight shuffles, not 32; lane l then has row 2 ((l >> 1) & 7) + (l >> 4), the
