@@ -83,6 +83,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
 // this thread's stores have read shared memory
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -332,16 +335,28 @@ __device__ __forceinline__ bool run_loader(const Cta& c) {
       if (one) {  // the stages are taken yet, but x can come nearer
         for (int h = 0; h < NH; ++h) tma_prefetch_2d(&tp.x_map, (h0 + h) * kDim, row);
       }
-      if (j >= 2 && !(ok = c.wait_warp(kEmptyBC + st, (j >> 1) - 1u))) break;
-      if (one) {
-        const uint32_t bc = c.bar(kFullBC + st);
-        mbar_arrive_expect(bc, tp.states_only ? 2 * kTile : 4 * kTile);
+      const uint32_t bc = c.bar(kFullBC + st);
+      if (!tp.states_only) {  // C's place is free before B's, but for lo, which is there until the update
+        if (j >= 2 && !(ok = c.wait_warp(kEmptyC + st, (j >> 1) - 1u))) break;
+        if (one) {
+          mbar_expect(bc, 2 * kTile);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!tp.states_only)
+          for (int half = 0; half < 2; ++half)
             tma_load_2d(c.base + kOffC + (2 * st + half) * kTile, &tp.C_map, g * kState + 64 * half, row, bc);
-          tma_load_2d(c.base + kOffB + (2 * st + half) * kTile, &tp.B_map, g * kState + 64 * half, row, bc);
         }
+      }
+      if (j >= 2 && !(ok = c.wait_warp(kEmptyB + st, (j >> 1) - 1u))) {
+        if (!tp.states_only) {  // C is on its way, and to be waited for
+          if (one) mbar_arrive(bc);
+          ++n_bc;
+        }
+        break;
+      }
+      if (one) {
+        mbar_arrive_expect(bc, 2 * kTile);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          tma_load_2d(c.base + kOffB + (2 * st + half) * kTile, &tp.B_map, g * kState + 64 * half, row, bc);
       }
       ++n_bc;
       // the stage is free once the last chunk's Y1 has read the state that took it
@@ -470,7 +485,7 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
 #pragma unroll 1
           for (uint32_t h = 0; h < NH; ++h) {
             const uint32_t b = desc_mn(c.base + kOffX + (2 * st + h) * kTile);
-#pragma unroll 2
+#pragma unroll 4
             for (uint32_t k = 0; k < 8; ++k)  // 16 tokens each, two to a block
               mma_ts(tm + kColY2 + 64 * h, P + 32 * (k >> 1) + 16 * h + 8 * (k & 1), b + k * kStepMn, kIdPx, k > 0);
           }
@@ -483,10 +498,11 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
         if (one) {
           const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile);
           const uint32_t b = desc_mn(c.base + kOffX + 2 * (st ^ 1u) * kTile);
-#pragma unroll 2
+#pragma unroll 4
           for (uint32_t k = 0; k < 8; ++k)
             mma_ss(tm + kColY1, a + (k >> 2) * (kTile / 16) + (k & 3) * 2, b + k * kStepMn, kIdY1, k > 0);
           tc_commit(c.bar(kY1Full));
+          if constexpr (!LO) tc_commit(c.bar(kEmptyC + st));
           tc_commit(c.bar(kEmptyX + (st ^ 1u)));
         }
         __syncwarp();
@@ -497,16 +513,26 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
       if (!c.wait_warp(kWFull + st, j >> 1)) return false;
       if (tp.states_only && j >= 2 && !c.wait_warp(kURead + st, (j >> 1) - 1u)) return false;
       tc_fence_after();
+      const uint32_t ua = desc_mn(c.base + kOffB + 2 * st * kTile);
       if (one) {
-        const uint32_t a = desc_mn(c.base + kOffB + 2 * st * kTile), hi = desc_mn(c.base + kOffX + 2 * st * kTile);
-        const uint32_t lo = desc_mn(c.base + kOffC + 2 * st * kTile);
-#pragma unroll 2
-        for (uint32_t k = 0; k < 8; ++k) {
-          mma_ss(tm + kColG + 128 * st, a + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
-          if constexpr (LO) mma_ss(tm + kColG + 128 * st, a + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
+        const uint32_t hi = desc_mn(c.base + kOffX + 2 * st * kTile);
+#pragma unroll 4
+        for (uint32_t k = 0; k < 8; ++k) mma_ss(tm + kColG + 128 * st, ua + k * kStepMn, hi + k * kStepMn, kIdU, k > 0);
+      }
+      __syncwarp();
+      if constexpr (LO) {
+        if (!c.wait_warp(kLoFull + st, j >> 1)) return false;
+        tc_fence_after();
+        if (one) {
+          const uint32_t lo = desc_mn(c.base + kOffC + 2 * st * kTile);
+#pragma unroll 4
+          for (uint32_t k = 0; k < 8; ++k) mma_ss(tm + kColG + 128 * st, ua + k * kStepMn, lo + k * kStepMn, kIdU, 1u);
         }
+      }
+      if (one) {
         tc_commit(c.bar(kUFull + st));
-        tc_commit(c.bar(kEmptyBC + st));
+        tc_commit(c.bar(kEmptyB + st));
+        if constexpr (LO) tc_commit(c.bar(kEmptyC + st));
         if (tp.states_only) tc_commit(c.bar(kEmptyX + st));
       }
       __syncwarp();
@@ -519,7 +545,7 @@ __device__ __forceinline__ bool run_mma(const Cta& c) {
 __device__ __forceinline__ void issue_G(const Cta& c, uint32_t st) {
   constexpr uint32_t kIdG = rsm::idesc_bf16_f32(128, 128, false, false);
   const uint32_t a = desc_k(c.base + kOffC + 2 * st * kTile), b = desc_k(c.base + kOffB + 2 * st * kTile);
-#pragma unroll 2
+#pragma unroll 4
   for (uint32_t k = 0; k < 8; ++k) {  // 16 dstate columns each: 32 bytes, four to a 64-column tile
     const uint32_t o = (k >> 2) * (kTile / 16) + (k & 3) * 2;
     mma_ss(c.tmem + kColG + 128 * st, a + o, b + o, kIdG, k > 0);
@@ -717,14 +743,16 @@ __device__ __forceinline__ bool run_w(const Cta& c, int h) {
           asm volatile("" : "+r"(lw[4 * q]), "+r"(lw[4 * q + 1]), "+r"(lw[4 * q + 2]), "+r"(lw[4 * q + 3]));
         sts128(at, hw[0], hw[1], hw[2], hw[3]);
       }
+      fence_proxy_async_smem();
+      c.arrive_warp(kWFull + st);
       if constexpr (LO) {
         if (!tp.states_only && !c.wait_warp(kY1Full, j)) return false;  // the last to read C
 #pragma unroll
         for (uint32_t q = 0; q < 8; ++q)
           sts128((la + swz) ^ (q << 4), lw[4 * q], lw[4 * q + 1], lw[4 * q + 2], lw[4 * q + 3]);
+        fence_proxy_async_smem();
+        c.arrive_warp(kLoFull + st);
       }
-      fence_proxy_async_smem();
-      c.arrive_warp(kWFull + st);
     }
   }
   return true;
@@ -907,7 +935,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
       for (int i = 0; i < how_many; ++i) mbar_init(bars + 8u * (b + i), n);
     };
     init(kFullBC, 1, 2);
-    init(kEmptyBC, 1, 2);
+    init(kEmptyB, 1, 2);
+    init(kEmptyC, 1, 2);
     init(kFullX, 1, 2);
     init(kEmptyX, 1, 2);
     init(kFullTab, NH, 2);
@@ -919,6 +948,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     init(kY1Full, 1);
     init(kYRead, 4 * NH);
     init(kWFull, 4 * NH, 2);
+    init(kLoFull, 4 * NH, 2);
     init(kClean, 4 * NH);
     init(kUFull, 1, 2);
     init(kURead, 4 * NH, 2);

@@ -48,9 +48,9 @@ enum Table : uint32_t {
 constexpr uint32_t kOffTab = kOffY + 8 * kYBytes;
 constexpr uint32_t kOffBar = kOffTab + 4 * kTabBytes;
 enum Bar : uint32_t {
-  kFullBC = 0, kEmptyBC = 2, kFullX = 4, kEmptyX = 6, kFullTab = 8, kEmptyTab = 10, kGFull = 12, kPFull = 14,
-  kWFull = 16, kUFull = 18, kURead = 20, kPxDone = 22, kSFull = 23, kY1Full = 24, kYRead = 25, kClean = 26, kExit = 27,
-  kBars = 29
+  kFullBC = 0, kEmptyB = 2, kEmptyC = 4, kFullX = 6, kEmptyX = 8, kFullTab = 10, kEmptyTab = 12, kGFull = 14, kPFull = 16,
+  kWFull = 18, kLoFull = 20, kUFull = 22, kURead = 24, kPxDone = 26, kSFull = 27, kY1Full = 28, kYRead = 29, kClean = 30,
+  kExit = 31, kBars = 33
 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
 constexpr uint32_t kOffOrder = kOffTmem + 8;  // the sequences, longest first, if they are few
