@@ -959,8 +959,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const Cta c{tp, smem, base, *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem), warp, lane};
-  // Registers: the launch's 7 x 72 a thread of each warpgroup, shared out anew
-  // (40 + 2 x 72 + 2 x 56 + 2 x 104 = 504): a state warp holds columns of 64 values.
+  // Registers: the launch's 7 x 72 a thread of each warpgroup, shared out anew (40 + 2 x
+  // 72 + 2 x 56 + 2 x 104 = 504; without lo w X needs 48 and the states have 112): P has to
+  // fit (64 a thread: 92 -> 98 us, 304 heads of 4096 tokens), a state warp holds columns of 64 values.
   bool ok = true;
   // no MMA may be in flight when the tensor memory is freed, whichever way its issuer ended
   auto drain = [&](uint32_t bar) {
@@ -984,10 +985,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_kernel(const __grid_cons
     ok = warp < 8 ? run_p<NH, false>(c) : run_p<NH, true>(c);
     if (warp == 4) drain(kExit + 1);
   } else if (warp < 20) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LO ? 56 : 48));
     if ((warp - 12) / 4 < NH) ok = run_w<NH, LO>(c, (warp - 12) / 4);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LO ? 104 : 112));
     if ((warp - 20) / 4 < NH) {
       ok = run_state<NH>(c, (warp - 20) / 4);
       if (lane == 0) tma_store_wait_read();  // shared memory outlives the stores that read it
