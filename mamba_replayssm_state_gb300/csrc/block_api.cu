@@ -225,11 +225,11 @@ int64_t workspace_bytes(const PrefillPlan& pl, int H) {
 // How many heads a CTA takes, and whether the sequences are cut into segments, whose
 // states then come from a pass of their own (x and B read twice, no outputs) and a join.
 // Lengths are on the device, so sequences are taken as equally long.  Times are in chunks
-// of a CTA with two heads, about 3.3 us, and measured: a chunk of one head 0.83; a
-// states-only chunk half of a whole one; a unit (a segment of a head group) takes 0.7 to
-// begin and end; the two launches more about five.  80 heads: one sequence of 32768 tokens
-// takes 386 us cut, where 40 units of 256 chunks on 152 SMs would take 850; one of 1024
-// takes 23.7 us with a head a CTA and 31.5 with two.
+// of a CTA with two heads, about 3 us, and measured: a chunk of one head 0.83; a
+// states-only chunk half of a whole one; a unit (a segment of a head group) one to begin
+// and end; the two launches more about four.  80 heads, cut into 1, 3, 7, 11 and 19
+// segments: one sequence of 32768 tokens takes 696, 391, 359, 360 and 370 us, one of 4096
+// 96, 68, 71, 73 and more; one of 1024 takes 23 us with a head a CTA and 31 with two.
 PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
   PrefillPlan pl{};
   const int64_t chunks = (a->tokens + static_cast<int64_t>(a->num_seqs) * ssm::kChunk - 1) /
@@ -239,11 +239,11 @@ PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
     const int pairs = a->num_heads / heads;
     const int64_t units = static_cast<int64_t>(a->num_seqs) * pairs;
     const double chunk = heads == 2 ? 1.0 : 0.83;
-    auto pass = [&](int64_t n, double per) { return static_cast<double>((n + sms - 1) / sms) * (per + 0.7); };
+    auto pass = [&](int64_t n, double per) { return static_cast<double>((n + sms - 1) / sms) * (per + 1.0); };
     for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(chunks, 1); ++n) {
       const int64_t per = (chunks + n - 1) / n;
       double t = pass(units * n, chunk * static_cast<double>(per));
-      if (n > 1) t += pass(units * (n - 1), 0.5 * chunk * static_cast<double>(per)) + 5.0;
+      if (n > 1) t += pass(units * (n - 1), 0.5 * chunk * static_cast<double>(per)) + 4.0;
       if (t >= best) continue;
       best = t;
       pl.heads = heads;
