@@ -344,11 +344,15 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
            (step || (reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(p.B_cache) % 16 == 0 && p.Bc_ss * ie % 16 == 0));
   // A CTA works on two heads at a time.  Many heads in all: as many a CTA, up to
-  // sixteen, as leave eight CTAs an SM, since a CTA's first loads wait for nothing to
-  // do meanwhile; few: two a CTA, to spread over the SMs.  Long rings take fewer, to
-  // leave three CTAs an SM.
+  // sixteen, as leave four CTAs an SM, since a CTA's first loads wait for nothing to do
+  // meanwhile, and two for one-byte states, whose heads take little time beside them; few:
+  // two a CTA, to spread over the SMs.  (After a ring of 16, left with 2, 4 and 8: int8, 16
+  // requests of 256 heads, 4 tokens: 16.7, 19.6 and 19.8 us; bf16, 32 requests, one: -, 29.9
+  // and 33; 64 requests, 4 tokens: int8 43.7, 44 and 51, bf16 -, 54 and 52.)  Long rings
+  // take fewer, to leave three CTAs an SM.
+  const int64_t leave = static_cast<int64_t>(es == 1 ? 2 : 4) * sms;
   int per = 2;
-  while (per < ssm::kTokenMaxHeads && static_cast<int64_t>(p.units) * p.H / (2 * per) >= 8 * static_cast<int64_t>(sms)) per *= 2;
+  while (per < ssm::kTokenMaxHeads && static_cast<int64_t>(p.units) * p.H / (2 * per) >= leave) per *= 2;
   per = std::min(per, hpg);
   auto smem = [&](int n) { return ssm::token_smem(mode, ie, n, p.window, p.tokens_max); };
   while (per > 1 && smem(per) > 75 * 1024) per = (per + 1) / 2;
