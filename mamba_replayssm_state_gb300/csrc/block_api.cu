@@ -319,8 +319,8 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
 // and 8.7.)  With bf16 inputs the products go to the tensor cores, but for a single
 // token of the recurrent form, whose lanes keep up with the memory, or after a ring on
 // fp16 states, which cost more to split than they save.  (64 requests of 256 heads, 4
-// tokens after a ring of 16, fp16: 58 us and 108; 32 requests, fp32, 4 tokens: 59 and
-// 118, one after a ring of 8: 54 and 63; 64 requests, fp16, one after a ring of 8: 55
+// tokens after a ring of 16, fp16: 58 us and 108; 32 requests, fp32, 4 tokens: 51 and
+// 118, one after a ring of 8: 48 and 63; 64 requests, fp16, one after a ring of 8: 55
 // and 48; to the states: 4 tokens, bf16, 116 and 190, one, fp16, 136 and 94.)
 int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* stream) {
   const int es = p.state_dtype == RSM_F32 ? 4 : p.state_dtype == RSM_BF16 || p.state_dtype == RSM_F16 ? 2 : 1;
@@ -343,16 +343,17 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
            ((step && !tc) || (even(p.B, p.B_bs, p.B_ts) && even(p.C, p.C_bs, p.C_ts))) &&
            (step || (reinterpret_cast<uintptr_t>(p.x_cache) % 16 == 0 && p.xc_ss * ie % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(p.B_cache) % 16 == 0 && p.Bc_ss * ie % 16 == 0));
-  // A CTA works on two heads at a time.  Many heads in all: as many a CTA, up to
-  // sixteen, as leave four CTAs an SM, since a CTA's first loads wait for nothing to do
+  // A CTA works on two heads at a time.  Many heads in all: as many a CTA as leave four
+  // CTAs an SM, eight for sixteen heads, since a CTA's first loads wait for nothing to do
   // meanwhile, and two for one-byte states, whose heads take little time beside them; few:
   // two a CTA, to spread over the SMs.  (After a ring of 16, left with 2, 4 and 8: int8, 16
   // requests of 256 heads, 4 tokens: 16.7, 19.6 and 19.8 us; bf16, 32 requests, one: -, 29.9
-  // and 33; 64 requests, 4 tokens: int8 43.7, 44 and 51, bf16 -, 54 and 52.)  Long rings
-  // take fewer, to leave three CTAs an SM.
-  const int64_t leave = static_cast<int64_t>(es == 1 ? 2 : 4) * sms;
+  // and 33.  64 requests, 4 tokens, with 16 heads and 8: int8 44 and 51, bf16 54 and 52, to
+  // bf16 states 124 and 116.)  Long rings take fewer, to leave three CTAs an SM.
   int per = 2;
-  while (per < ssm::kTokenMaxHeads && static_cast<int64_t>(p.units) * p.H / (2 * per) >= leave) per *= 2;
+  while (per < ssm::kTokenMaxHeads &&
+         static_cast<int64_t>(p.units) * p.H / (2 * per) >= static_cast<int64_t>(es == 1 ? 2 : per < 8 ? 4 : 8) * sms)
+    per *= 2;
   per = std::min(per, hpg);
   auto smem = [&](int n) { return ssm::token_smem(mode, ie, n, p.window, p.tokens_max); };
   while (per > 1 && smem(per) > 75 * 1024) per = (per + 1) / 2;

@@ -30,11 +30,11 @@
 //   warps 12-19  w X, a head each four: a thread holds token t's row; x becomes w x in place
 //   warps 20-27  a head each four: the state in registers as fp32, a thread per dstate
 //                column, and its bf16 copy for Y1; between the two, y out of Y1 and Y2
-// What bounds it is latency, the way round of a chunk: U to the next load of B and C, G,
-// P, Y2, w X and U again (bf16 states), and S to Y1 to lo to U to S (others).  Measured on
-// a GB300: a chunk and pair of heads takes 2.8 us with bf16 states and 3.3 with fp32 ones
-// (5400 and 6300 cycles), of which the four products are 2050 and 2560 cycles; 4
-// sequences of 8192 tokens in all, 256 heads, bf16 states: 177 us, 390 TFLOP/s.
+// What bounds it is latency, the way round of a chunk: Y2 and Y1 to y and the next Y2 (bf16
+// states), and S to Y1 to lo to U to S (others).  Measured on a GB300: a chunk and pair of
+// heads takes 2.55 us with bf16 states and 2.95 with fp32 ones (4900 and 5600 cycles), of
+// which the four products are 2050 and 2560 cycles; 4 sequences of 8192 tokens in all, 256
+// heads, bf16 states: 170 to 180 us, 390 TFLOP/s.
 // A sequence's last chunk may be partial: dt counts as 0 there, and the rows of
 // x and B past its end, which are a neighbour's or nobody's, are cleared
 // before an MMA multiplies them by 0.

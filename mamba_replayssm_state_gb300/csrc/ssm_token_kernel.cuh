@@ -11,7 +11,7 @@
 // a GB300, 256 requests of 256 heads, bf16: one token to the state itself 343 us, 6.3
 // TB/s; one token after a ring of 8 174 us, 6.4 TB/s; 64 requests: 4 tokens to the state
 // 116 us, 4.6 TB/s, 4 after a ring of 16 52 us, 5.2 TB/s.  Instructions bound one-byte
-// states (64 requests, 4 tokens, int8: 55 us, 3.2 TB/s).  A CTA
+// states (64 requests, 4 tokens, int8: 49 us, 3.7 TB/s).  A CTA
 // takes heads of one request and group.  One round of loads stages what their
 // tokens need; then four warps share a head, 16 dim rows each, and go through the
 // CTA's heads two at a time, asking for the next head's rows as soon as the last's
