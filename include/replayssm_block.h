@@ -43,7 +43,7 @@
 extern "C" {
 #endif
 
-#define RSM_STATUS_BAD_SEQUENCE 32u /* cu_seqlens decreasing, or outside [0, tokens] */
+#define RSM_STATUS_BAD_SEQUENCE 32u /* cu_seqlens goes back, or lies outside [0, tokens] */
 
 /*
  * Prompts.  Sequence s is tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 of the
@@ -51,8 +51,9 @@ extern "C" {
  * state[initial_slots[s]] (NULL, or pad_slot_id: from zero) and ends in
  * state[final_slots[s]] (NULL, or pad_slot_id: not kept).  Final slots are
  * distinct and are no other sequence's initial slot; a sequence's own may
- * coincide.  Output rows outside every sequence are not written.  A slot out
- * of range counts as pad_slot_id, and a bad sequence is skipped; both are flagged.
+ * coincide.  Output rows outside every sequence are not written.  A sequence that
+ * lies outside [0, tokens] is skipped, and so are all from where cu_seqlens goes
+ * back; a slot out of range counts as pad_slot_id.  Both are flagged.
  */
 typedef struct rsm_ssm_prefill_args {
   const void *x, *B, *C; /* [tokens, ...] input_dtype */

@@ -249,7 +249,7 @@ PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
       pl.heads = heads;
       pl.pairs = pairs;
       pl.seg = n == 1 ? 0x7FFFFF80u : static_cast<uint32_t>(per * ssm::kChunk);
-      pl.segs = n == 1 ? 0 : a->tokens / pl.seg + a->num_seqs;  // no more than this, however the lengths fall
+      pl.segs = n == 1 ? 0 : ssm::segments_at_most(a->tokens, pl.seg, a->num_seqs);
     }
   }
   return pl;

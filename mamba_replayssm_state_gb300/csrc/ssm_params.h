@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "../../include/replayssm_block.h"
+#include "ssm_sequences.h"
 
 namespace ssm {
 

@@ -213,9 +213,13 @@ struct Unit {
 // are short: the prompts of a batch differ, and a CTA has few units.  (16 of 8192 tokens
 // in all, the longest 2011, 128 heads: 159 us in their own order, 144 us like this.)
 __device__ __forceinline__ bool in_order(const TcParams& tp) { return tp.p.units > kSorted || tp.seg_state != nullptr; }
+// Where they go back ends the walk: it and those after it come last, it before them.
 __device__ __forceinline__ void sort_sequences(const TcParams& tp, uint32_t order, int lane) {  // one warp
   const int n = tp.p.units;
-  const int len = lane < n ? __ldg(tp.p.cu_seqlens + lane + 1) - __ldg(tp.p.cu_seqlens + lane) : 0;
+  const int t0 = lane < n ? __ldg(tp.p.cu_seqlens + lane) : 0, t1 = lane < n ? __ldg(tp.p.cu_seqlens + lane + 1) : 0;
+  const uint32_t back = __ballot_sync(0xFFFFFFFFu, goes_back(t0, t1));
+  const bool before = (back & (2u * (1u << lane) - 1u)) == 0u;  // none at it or before it
+  const int len = before ? static_cast<int>(min(static_cast<uint32_t>(t1) - static_cast<uint32_t>(t0), 0x7FFFFFFFu)) : -1;
   uint32_t longer = 0;
   for (int i = 0; i < n; ++i) {
     const int other = __shfl_sync(0xFFFFFFFFu, len, i);
@@ -242,12 +246,13 @@ struct Walk {
       int seq = at;
       if (!in_order(tp)) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(seq) : "r"(order + 4u * at));
       const int t0 = __ldg(tp.p.cu_seqlens + seq), t1 = __ldg(tp.p.cu_seqlens + seq + 1);
-      if (t0 < 0 || t1 < t0 || t1 > tp.p.tokens) {
+      if (!within(t0, t1, tp.p.tokens)) {
         if (flagger) flag(tp.p.status, RSM_STATUS_BAD_SEQUENCE);
-        continue;  // no unit at all
+        if (goes_back(t0, t1)) return false;  // nor any after it
+        continue;                             // no unit at all
       }
       const uint32_t len = static_cast<uint32_t>(t1 - t0);
-      const uint32_t nseg = len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
+      const uint32_t nseg = segments_of(len, tp.seg);
       for (uint32_t sg; (sg = u / static_cast<uint32_t>(tp.pairs)) < base + nseg;) {
         const uint32_t s = sg - base;
         w.group = static_cast<int>(u - sg * static_cast<uint32_t>(tp.pairs));
@@ -1012,16 +1017,15 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(const __grid_con
   const uint32_t part = blockIdx.x % kParts, unit = blockIdx.x / kParts;
   const int seq = static_cast<int>(unit / static_cast<uint32_t>(p.H));
   const int h = static_cast<int>(unit % static_cast<uint32_t>(p.H));
-  auto segs_of = [&](int s) -> uint32_t {
-    const int64_t a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
-    if (a < 0 || b < a || b > p.tokens) return 0;
-    const uint32_t len = static_cast<uint32_t>(b - a);
-    return len <= tp.seg ? 1 : (len + tp.seg - 1) / tp.seg;
-  };
-  const uint32_t n = segs_of(seq);
-  if (n <= 1) return;
   int64_t sg = 0;  // segments before the sequence's
-  for (int s = 0; s < seq; ++s) sg += segs_of(s);
+  uint32_t n = 0;  // its own
+  for (int s = 0; s <= seq; ++s) {
+    const int a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
+    if (goes_back(a, b)) return;
+    sg += n;
+    n = within(a, b, p.tokens) ? segments_of(static_cast<uint32_t>(b - a), tp.seg) : 0;
+  }
+  if (n <= 1) return;
   const int src = slot_of(p, p.src, seq, false);
   const uint32_t e = 4 * (part * kJoinThreads + threadIdx.x);
   float R[4] = {0.0f, 0.0f, 0.0f, 0.0f};

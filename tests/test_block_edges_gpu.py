@@ -1,0 +1,82 @@
+"""The layer operators where a call's metadata, magnitudes or callers are unusual.  Bounds and references are
+test_block_ops_gpu's, or stated at the test."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_reference as ref  # noqa: E402
+import mamba_replayssm_state_gb300 as rsm  # noqa: E402
+import test_block_ops_gpu as base  # noqa: E402
+from mamba_replayssm_state_gb300 import block  # noqa: E402
+from test_block_ops_gpu import BF16, F16, F32, i32  # noqa: E402
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+def word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def prefill_workspace(T, seqs, H, G):
+    """Bytes that a bf16 call of this size needs; 0 where it is not cut into segments."""
+    a = block.SsmPrefillArgs()
+    a.tokens, a.num_seqs, a.num_heads, a.num_groups, a.dim, a.dstate = T, seqs, H, G, 64, 128
+    a.state_dtype, a.input_dtype = rsm.RSM_F32, rsm.RSM_BF16
+    return block._load().rsm_ssm_prefill_workspace(bytes(a))
+
+
+@pytest.mark.parametrize("case", ["cut", "longest first", "many", "one by one"])
+def test_prefill_sequences_that_start_over_are_skipped(case):
+    """cu_seqlens that goes back and starts over: what would lie over an earlier sequence is skipped and flagged,
+    whichever way the call runs, and nothing is written but the first sequence's outputs, its state and, within the
+    bytes asked for, the workspace."""
+    H, G = 2, 1
+    T, inputs = {"cut": (5000, BF16), "longest first": (300, BF16), "many": (300, BF16), "one by one": (150, F32)}[case]
+    cu = [0, T, 0, T] if case != "many" else [0, T] + [0, T] * 20
+    S = len(cu) - 1
+    x, dt, A, B, C, D = base.tokens((T,), H, G, 64, 128, inputs, 3)
+    st = base.pool(S + 1, H, 64, 128, F32, 4)
+    first = base.pool(S + 1, H, 64, 128, F32, 4)
+    want = rsm.ssm_prefill(x, dt, A, B, C, i32([0, T]), first, initial_slots=i32([0]), final_slots=i32([1]), D=D)
+    before, status = st.clone(), word()
+    size = prefill_workspace(T, S, H, G) if inputs == BF16 else 0
+    assert (size > 0) == (case == "cut")
+    workspace = torch.full((size + (64 << 20),), 77, dtype=torch.uint8, device="cuda")
+    workspace, beyond = workspace[:size], workspace[size:]
+    y = rsm.ssm_prefill(x, dt, A, B, C, i32(cu), st, initial_slots=i32([0] + [-1] * (S - 1)),
+                        final_slots=i32(list(range(1, S + 1))), D=D, device_status=status, workspace=workspace)
+    assert int(status) == rsm.STATUS_BITS["bad_sequence"]
+    assert bool((beyond == 77).all())
+    wy, wm, ws, wsm = ref.prefill(x, dt, A, B, C, [0, T], before, [0], D)
+    base.close(y, wy, base.HALF_UNIT[inputs], wm, base.y_terms(inputs, T), "y")
+    base.close(st[1:2], ws, base.HALF_UNIT[F32], wsm, base.state_terms(inputs, F32, T), "state")
+    assert torch.equal(st[0], before[0]) and torch.equal(st[2:], before[2:])
+    if case != "cut":  # (cut for another number of sequences, sums differ in their order)
+        assert torch.equal(y, want) and torch.equal(st[1], first[1])
+
+
+@pytest.mark.parametrize("case", ["cut", "longest first", "one by one"])
+def test_prefill_runs_what_is_good_before_bad_sequences(case):
+    """Sequences that start before the tokens, that end past them, and a step back, around good ones."""
+    H, G = 2, 1
+    n, inputs = {"cut": (2000, BF16), "longest first": (150, BF16), "one by one": (40, F32)}[case]
+    T = 3 * n
+    cu = [-9, -5, 0, n, n, 2 * n, T + 1, T + 7, 2 * n, T]
+    good = {2: (0, n), 3: (n, n), 4: (n, 2 * n)}
+    S = len(cu) - 1
+    x, dt, A, B, C, D = base.tokens((T,), H, G, 64, 128, inputs, 5)
+    st = base.pool(2 * S, H, 64, 128, F32, 6)
+    before, status = st.clone(), word()
+    out = torch.full_like(x, 9.0)
+    rsm.ssm_prefill(x, dt, A, B, C, i32(cu), st, initial_slots=i32(list(range(S))), final_slots=i32(list(range(S, 2 * S))),
+                    D=D, device_status=status, out=out)
+    assert int(status) == rsm.STATUS_BITS["bad_sequence"]
+    for s, (a, b) in good.items():
+        if a == b:
+            assert torch.equal(st[S + s], before[s])
+            continue
+        wy, wm, ws, wsm = ref.prefill(x, dt, A, B, C, [a, b], before, [s], D)
+        base.close(out[a:b], wy[a:b], base.HALF_UNIT[inputs], wm[a:b], base.y_terms(inputs, n), "y")
+        base.close(st[S + s:S + s + 1], ws, base.HALF_UNIT[F32], wsm, base.state_terms(inputs, F32, n), "state")
+    keep = [i for i in range(2 * S) if i - S not in good]
+    assert torch.equal(st[keep], before[keep]) and bool((out[2 * n:] == 9).all())
