@@ -144,6 +144,18 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
 bool g_tc_ready[kMaxDevices][4];
+bool g_token_ready[kMaxDevices][2][5][6];  // input type, state type, mode
+
+// Lets a kernel take up to `bytes` of dynamic shared memory: once, since the limit is the
+// kernel's and not the call's, and calls come from several threads.
+int allow_smem(bool* ready, const void* fn, int bytes) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (*ready) return RSM_OK;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  *ready = true;
+  return RSM_OK;
+}
 
 int device_sms(int* dev, int* sms) {
   cudaError_t e = cudaGetDevice(dev);
@@ -283,14 +295,8 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   const bool lo = a->final_slots != nullptr && a->state_dtype != RSM_BF16;
   const void* fn = ssm::tc_kernel(pl.heads, lo);
   const int ki = (pl.heads - 1) * 2 + (lo ? 1 : 0);
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_tc_ready[dev][ki]) {
-      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ssm::kTcSmem));
-      if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-      g_tc_ready[dev][ki] = true;
-    }
-  }
+  rc = allow_smem(&g_tc_ready[dev][ki], fn, static_cast<int>(ssm::kTcSmem));
+  if (rc != RSM_OK) return rc;
   // (a unit's number and the next one's after it stay below 2^32)
   if (units > 0x7FFFFFFFLL) return fail(RSM_EINVAL, "%lld units of work, more than 2^31-1", static_cast<long long>(units));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, sms));
@@ -328,7 +334,7 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
                     reinterpret_cast<uintptr_t>(p.state) % 16 == 0 && p.state_ss * es % 16 == 0;
   if (!fits) return launch_seq(p, input_dtype, dim, dstate, stream);
   int dev = 0, sms = 0;
-  const int rc = device_sms(&dev, &sms);
+  int rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
   const bool step = p.mode == ssm::kStep;
   const int ie = input_dtype == RSM_F32 ? 4 : 2, hpg = p.H / p.G;
@@ -356,13 +362,13 @@ int launch_tokens(ssm::Params& p, int input_dtype, int dim, int dstate, void* st
     per *= 2;
   per = std::min(per, hpg);
   auto smem = [&](int n) { return ssm::token_smem(mode, ie, n, p.window, p.tokens_max); };
-  while (per > 1 && smem(per) > 75 * 1024) per = (per + 1) / 2;
+  while (per > 1 && smem(per) > ssm::kTokenMaxSmem) per = (per + 1) / 2;
   p.heads_per_cta = per;
   const int64_t parts = (hpg + per - 1) / per, grid = static_cast<int64_t>(p.units) * p.G * parts;
   const void* fn = ssm::token_kernel(input_dtype, p.state_dtype, mode);
   if (smem(per) > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem(per)));
-    if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    rc = allow_smem(&g_token_ready[dev][input_dtype == RSM_F32 ? 1 : 0][p.state_dtype][mode], fn, ssm::kTokenMaxSmem);
+    if (rc != RSM_OK) return rc;
   }
   return launch(fn, grid, ssm::kTokenThreads, &p, stream, smem(per));
 }

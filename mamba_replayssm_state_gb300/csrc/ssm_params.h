@@ -43,6 +43,7 @@ constexpr int kTokenThreads = 256;
 constexpr int kTokenMaxNew = 16;  // new tokens of a request
 constexpr int kTokenMaxAll = 64;  // with the ring's
 constexpr int kTokenMaxHeads = 16;  // of a CTA
+constexpr int kTokenMaxSmem = 75 * 1024;  // of a CTA: three an SM (one head of the longest ring takes 67 KB)
 uint32_t token_smem(int mode, int input_bytes, int heads, int fresh, int all);
 
 }  // namespace ssm

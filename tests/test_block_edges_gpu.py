@@ -1,5 +1,7 @@
 """The layer operators where a call's metadata, magnitudes or callers are unusual.  Bounds and references are
 test_block_ops_gpu's, or stated at the test."""
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -80,3 +82,50 @@ def test_prefill_runs_what_is_good_before_bad_sequences(case):
         base.close(st[S + s:S + s + 1], ws, base.HALF_UNIT[F32], wsm, base.state_terms(inputs, F32, n), "state")
     keep = [i for i in range(2 * S) if i - S not in good]
     assert torch.equal(st[keep], before[keep]) and bool((out[2 * n:] == 9).all())
+
+
+def test_decode_from_two_threads():
+    """Rings of 50 and of 64 rows run on one kernel with different amounts of shared memory; neither thread's calls
+    are refused for the other's, and each gets what it gets alone."""
+    H, T = 2, 4
+    lib, calls = block._load(), []
+    for R in (50, 64):
+        x, dt, A, B, C, D = base.tokens((1, T), H, 1, 64, 128, F32, R)
+        xc, dtc, _, Bc, _, _ = base.tokens((1, R), H, 1, 64, 128, F32, R + 1)
+        st, zero, have = base.pool(1, H, 64, 128, BF16, R + 2), i32([0]), i32([5])
+        want = rsm.replayssm_decode(st, zero, xc, Bc, dtc, zero, have, x, dt, A, B, C, D=D)
+        out = torch.zeros_like(x)
+        a = block.ReplaySsmDecodeArgs()
+        tensors = dict(x=x, B=B, C=C, dt=dt, A=A, D=D, state=st, x_cache=xc, B_cache=Bc, dt_cache=dtc, slots=zero,
+                       ring_start=zero, ring_len=have, out=out)
+        for name, t in tensors.items():
+            setattr(a, name, t.data_ptr())
+        for name, t in (("x", x), ("B", B), ("C", C), ("dt", dt)):
+            setattr(a, name + "_batch_stride", t.stride(0))
+            setattr(a, name + "_stride", t.stride(1))
+        for name, t in (("state", st), ("x_cache", xc), ("B_cache", Bc), ("dt_cache", dtc)):
+            setattr(a, name + "_slot_stride", t.stride(0))
+        a.batch, a.window, a.num_slots, a.num_heads, a.num_groups, a.dim, a.dstate, a.ring_buffer_len = 1, T, 1, H, 1, 64, 128, R
+        a.state_dtype, a.input_dtype, a.pad_slot_id = rsm.RSM_BF16, rsm.RSM_F32, -1
+        calls.append((bytes(a), want, tensors))
+    torch.cuda.synchronize()
+    stream, refused, together = torch.cuda.current_stream().cuda_stream, [], threading.Barrier(2)
+
+    def work(args):
+        torch.cuda.set_device(0)
+        together.wait()
+        for k in range(20000):
+            rc = lib.rsm_replayssm_decode(args, stream)
+            if rc != 0:
+                refused.append((rc, lib.rsm_block_last_error().decode()))
+            if k % 200 == 199:
+                torch.cuda.synchronize()
+
+    threads = [threading.Thread(target=work, args=(c[0],)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, f"{len(refused)} calls refused: {refused[0]}"
+    assert all(torch.equal(c[2]["out"], c[1]) for c in calls)
