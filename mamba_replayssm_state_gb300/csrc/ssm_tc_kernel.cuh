@@ -1026,7 +1026,7 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(const __grid_con
     n = within(a, b, p.tokens) ? segments_of(static_cast<uint32_t>(b - a), tp.seg) : 0;
   }
   if (n <= 1) return;
-  const int src = slot_of(p, p.src, seq, false);
+  const int src = slot_of(p, p.src, seq, h == 0 && part == 0 && threadIdx.x == 0);  // (the segments do not look at it)
   const uint32_t e = 4 * (part * kJoinThreads + threadIdx.x);
   float R[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (src >= 0) {

@@ -129,3 +129,19 @@ def test_decode_from_two_threads():
     torch.cuda.synchronize()
     assert not refused, f"{len(refused)} calls refused: {refused[0]}"
     assert all(torch.equal(c[2]["out"], c[1]) for c in calls)
+
+
+def test_prefill_flags_a_bad_initial_slot_of_a_cut_sequence():
+    """One long sequence of few heads, cut into segments: a slot out of range starts from zero and is flagged, the
+    pad starts from zero and is not."""
+    T, H = 3001, 2
+    assert prefill_workspace(T, 1, H, 1) > 0
+    x, dt, A, B, C, D = base.tokens((T,), H, 1, 64, 128, BF16, 3)
+    st = base.pool(3, H, 64, 128, F32, 4)
+    out = []
+    for slot, bits in ((-1, 0), (3, rsm.STATUS_BITS["bad_slot"]), (-7, rsm.STATUS_BITS["bad_slot"])):
+        status, pool = word(), st.clone()
+        out.append((rsm.ssm_prefill(x, dt, A, B, C, i32([0, T]), pool, initial_slots=i32([slot]), final_slots=i32([2]),
+                                    D=D, device_status=status), pool))
+        assert int(status) == bits, slot
+    assert all(torch.equal(y, out[0][0]) and torch.equal(p, out[0][1]) for y, p in out)
