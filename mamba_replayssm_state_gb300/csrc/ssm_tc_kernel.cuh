@@ -14,9 +14,10 @@
 // Decays.  With p_i the sum of a from the start of i's half of the chunk, a pair
 // (i, j) of one half decays by e^{p_i} e^{-p_j}: the column factor goes into P (one
 // product an element, no exponential), the row factor onto Y2 when y = m1 Y1 + m2
-// Y2 leaves.  A pair across the halves is e^{p_i} e^{rest of the first half}.  e^{-p}
-// would overflow in a half that decays by more than 2^100 ("steep", a mean dt A
-// above 1.08): its rows take an exponential of p_i - p_j an element instead.  The
+// Y2 leaves.  A pair across the halves is e^{p_i} e^{rest of the first half}.  Both factors
+// are taken from p's middle, the half's decay's square root: e^{mid - p_j} and e^{p_i - mid},
+// which leaves G, x and their sums 2^77 either way where a half decays by 2^-100.  One that
+// decays by more ("steep", a mean dt A above 1.08) takes an exponential of p_i - p_j an element.  The
 // weights towards a chunk's end are summed from there, so that small decays near it
 // keep their precision next to large ones before them.
 //
@@ -173,7 +174,7 @@ __device__ __forceinline__ void tmem_ld8x2(uint32_t ta, uint32_t tb, float (&a)[
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSteep = 100.0f;  // decay of a half chunk, log2, past which 2^-p is not formed
+constexpr float kSteep = 100.0f;  // decay of a half chunk, log2, past which 2^(mid - p) is not formed
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -428,19 +429,22 @@ __device__ __forceinline__ bool run_tables(const Cta& c, int h) {
       before = (lane & 15) == 0 ? 0.0f : bx;
       beyond = (lane & 15) == 15 ? 0.0f : by;
       const bool steep = !(fabsf(second ? half1 : half0) <= kSteep);
+      const float mid = steep ? 0.0f : 0.5f * (second ? half1 : half0), mid1 = __shfl_sync(0xFFFFFFFFu, mid, 31);
+      const float start = second ? half0 + mid : mid, rest1 = second ? 0.0f : half1;
+      before -= mid;
       const uint32_t st = j & 1u;
       if (j >= 2 && !c.wait_warp(kEmptyTab + st, (j >> 1) - 1u)) return false;
       const uint32_t at = c.table(st, h) + 16u * lane;
       float col[4], v[4], ww[4], m1[4], m2[4], sk[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float p = before + upto[m], rest = after[m] + beyond;
-        const float e = exp2_approx(p), inv = exp2_approx(-p), ev = exp2_approx(rest);
+        const float p = before + upto[m], rest = after[m] + beyond;  // (p less mid)
+        const float inv = exp2_approx(-p);
         col[m] = steep ? p : d[m] * inv;
-        v[m] = d[m] * ev;
-        ww[m] = second ? v[m] : d[m] * exp2_approx(rest + half1);
-        m1[m] = second ? exp2_approx(half0 + p) : e;
-        m2[m] = steep ? 1.0f : e;
+        v[m] = d[m] * exp2_approx(rest + mid1);
+        ww[m] = d[m] * exp2_approx(rest + rest1);
+        m1[m] = exp2_approx(start + p);
+        m2[m] = steep ? 1.0f : exp2_approx(p);
         sk[m] = steep ? skip : skip * inv;
       }
       sts4(at + kTabCol, col);
@@ -610,7 +614,7 @@ __device__ __forceinline__ void steep_rows(uint32_t tab0, uint32_t trow, int k, 
   }
 }
 
-// P of the heads, a thread per row; the row factor 2^p is left to the output.  A row's
+// P of the heads, a thread per row; the row factor 2^(p - mid) is left to the output.  A row's
 // warp has one block of 32 columns on the diagonal, which is one warpgroup's work
 // (DIAG), and 0 to 3 below it, which with zeros above are the other's.  The warp with
 // zeros alone has the time to issue G.

@@ -33,15 +33,16 @@ constexpr uint32_t kOffX = kOffB + 4 * kTile;
 constexpr uint32_t kOffY = kOffX + 4 * kTile;  // of a head's 32 rows: 32 columns, 64-byte swizzled
 constexpr uint32_t kYBytes = 2 * 32 * 32;
 // A table of [stage][head], made by a dt warp; fp32, 128 tokens where not said otherwise.
-// p is the decay (log2) from the start of a token's half of the chunk up to and with it.
+// p is the decay (log2) from the start of a token's half of the chunk up to and with it, mid
+// half of the half's (a steep half: 0).
 enum Table : uint32_t {
-  kTabCol = 0,     // dt 2^-p: what a column of P is scaled by in its own half (a steep half: p itself)
+  kTabCol = 0,     // dt 2^(mid-p): what a column of P is scaled by in its own half (a steep half: p itself)
   kTabDt = 512,    // dt
-  kTabV = 1024,    // [64] first half: dt 2^(decay after the token up to the half's end)
+  kTabV = 1024,    // [64] first half: dt 2^(decay after the token up to the half's end + the second's mid)
   kTabW = 1280,    // dt 2^(decay after the token up to the chunk's end)
   kTabM1 = 1792,   // y = m1 Y1 + m2 Y2: 2^(decay from the chunk's start)
-  kTabM2 = 2304,   //                    2^p (a steep half: 1)
-  kTabSkip = 2816, // D 2^-p (a steep half: D)
+  kTabM2 = 2304,   //                    2^(p-mid) (a steep half: 1)
+  kTabSkip = 2816, // D 2^(mid-p) (a steep half: D)
   kTabMisc = 3328, // 2^(decay of the chunk); its log2; whether each half is steep
   kTabBytes = 3344
 };

@@ -145,3 +145,54 @@ def test_prefill_flags_a_bad_initial_slot_of_a_cut_sequence():
                                     D=D, device_status=status), pool))
         assert int(status) == bits, slot
     assert all(torch.equal(y, out[0][0]) and torch.equal(p, out[0][1]) for y, p in out)
+
+
+def check_decays(rates, state=F32, size=1.0, T=300, skip=True):
+    """A prompt whose tokens decay by rates [T, H] nats, with x, B and C of about `size`."""
+    H = rates.shape[1]
+    x, _, _, B, C, D = base.tokens((T,), H, 1, 64, 128, BF16, 8)
+    x, B, C = x * size, B * size, C * size
+    A = -(0.5 + torch.rand(H, generator=base.gen(9), device="cuda"))
+    dt = (rates / -A).float()
+    st = base.pool(2, H, 64, 128, state, 10)
+    before = st.clone()
+    D = D if skip else None
+    y = rsm.ssm_prefill(x, dt, A, B, C, i32([0, T]), st, initial_slots=i32([0]), final_slots=i32([1]), D=D)
+    wy, wm, ws, wsm = ref.prefill(x, dt, A, B, C, [0, T], before, [0], D)
+    base.close(y, wy, 2.0 ** -8, wm, base.y_terms(BF16, T), "y")
+    base.close(st[1:], ws, base.HALF_UNIT[state], wsm, base.state_terms(BF16, state, T), "state")
+
+
+LN2 = 0.6931471805599453
+
+
+@pytest.mark.parametrize("log2", [40.0, 90.0, 99.5, 100.5, 140.0])
+@pytest.mark.parametrize("size", [1.0, 4096.0])
+def test_prefill_decays_of_a_half_chunk(log2, size):
+    """64 tokens decay by about 2^-log2, on either side of where the kernel changes its way, values small and large
+    (the largest sums, near 2^45, are far inside every type here)."""
+    g = base.gen(11)
+    rates = LN2 * log2 / 64 * (0.8 + 0.4 * torch.rand((300, 4), generator=g, device="cuda"))
+    check_decays(rates, size=size)
+    check_decays(torch.full((300, 3), LN2 * log2 / 64, device="cuda"), state=BF16, size=size, skip=False)
+
+
+@pytest.mark.parametrize("heads", [[0], [1], [1, 2]])
+@pytest.mark.parametrize("halves", [[0], [1], [2, 3], [0, 3], [1, 2]])
+def test_prefill_steep_heads_and_halves_mixed(heads, halves):
+    """Some heads, and some halves of their chunks, decay by more than 2^-100, their neighbours mildly."""
+    g = base.gen(12)
+    rates = 0.001 + 0.1 * torch.rand((300, 4), generator=g, device="cuda")
+    for h in heads:
+        for k in halves:
+            rates[64 * k:64 * k + 64, h] = 1.2 + torch.rand(64, generator=g, device="cuda")
+    check_decays(rates)
+    check_decays(rates, state=BF16, size=64.0)
+
+
+def test_prefill_one_steep_token():
+    """A single token that decays everything before it to nothing, first, in the middle or last of a half."""
+    for at in (0, 31, 32, 63, 64, 100, 127, 128, 255):
+        rates = 0.001 + 0.1 * torch.rand((300, 3), generator=base.gen(13), device="cuda")
+        rates[at, 1] = 150.0
+        check_decays(rates)
