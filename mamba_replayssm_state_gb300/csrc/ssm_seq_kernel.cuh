@@ -29,6 +29,15 @@ __device__ __forceinline__ void store_in(uint16_t* p, float v) {
   *p = static_cast<uint16_t>(rsm::pack_bf16x2(v, 0.0f) & 0xFFFFu);
 }
 
+// The lo half of values split into bf16 hi + lo, from value - hi.  Where hi is infinite that
+// is no number, and takes an infinite sum with it: lo is kept within 2^119, which the
+// remainder of a finite value never exceeds.
+__device__ __forceinline__ uint32_t bounded_lo(uint32_t lo) {
+  uint32_t v;
+  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(lo), "r"(0x7B007B00u));
+  return v;
+}
+
 __device__ __forceinline__ float load_state(const void* base, int64_t at, int fmt) {
   switch (fmt) {
     case RSM_F32: return static_cast<const float*>(base)[at];

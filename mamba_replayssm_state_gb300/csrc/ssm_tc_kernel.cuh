@@ -745,7 +745,7 @@ __device__ __forceinline__ bool run_w(const Cta& c, int h) {
           if constexpr (LO) {
             // u - hi is exact; rounded to bf16, hi + lo is within 2^-17 of u
             const float2 l = __ffma2_rn(make_float2(rsm::bf16lo(hw[m]), rsm::bf16hi(hw[m])), make_float2(-1.0f, -1.0f), u);
-            lw[4 * q + m] = rsm::pack_bf16x2(l.x, l.y);
+            lw[4 * q + m] = bounded_lo(rsm::pack_bf16x2(l.x, l.y));
           }
         }
         if constexpr (LO)  // here and now: two registers a pair until then are too many

@@ -250,7 +250,7 @@ __device__ __forceinline__ float2 state_pair(const uint4 (&row)[P], int i) {
 }
 __device__ __forceinline__ void split_pair(float2 v, uint32_t& hi, uint32_t& lo) {
   hi = rsm::pack_bf16x2(v.x, v.y);
-  lo = rsm::pack_bf16x2(v.x - rsm::bf16lo(hi), v.y - rsm::bf16hi(hi));
+  lo = bounded_lo(rsm::pack_bf16x2(v.x - rsm::bf16lo(hi), v.y - rsm::bf16hi(hi)));
 }
 
 // D += A B: 16 rows x 16 k, 16 k x 8 columns, bf16 in, fp32 sums

@@ -196,3 +196,46 @@ def test_prefill_one_steep_token():
         rates = 0.001 + 0.1 * torch.rand((300, 3), generator=base.gen(13), device="cuda")
         rates[at, 1] = 150.0
         check_decays(rates)
+
+
+@pytest.mark.parametrize("state", [F32, F16, BF16])
+@pytest.mark.parametrize("inf", [float("inf"), -float("inf")])
+def test_an_infinite_input_leaves_an_infinite_state(state, inf):
+    """S += dt x (x) B with one infinite x: that row of the state is infinite with B's signs, and nothing else is."""
+    H, d, h = 4, 5, 3
+    for way in ("prompt", "step"):
+        T, at = (40, 10) if way == "prompt" else (4, 1)
+        x, dt, A, B, C, D = base.tokens((T,), H, 2, 64, 128, BF16, 5)
+        B = torch.where(B == 0, torch.ones_like(B), B)
+        x[at, h, d] = inf
+        st = base.pool(2, H, 64, 128, state, 6)
+        before = st.clone()
+        if way == "prompt":
+            y = rsm.ssm_prefill(x, dt, A, B, C, i32([0, T]), st, initial_slots=i32([0]), final_slots=i32([1]), D=D)
+        else:
+            y = rsm.ssm_step(st, i32([0]), x[None], dt[None], A, B[None], C[None], dst_slots=i32([1]), D=D)[0]
+        wy, wm, ws, wsm = ref.prefill(x, dt, A, B, C, [0, T], before, [0], D)
+        assert torch.equal(st[1, h, d].double(), ws[0, h, d]) and bool(torch.isinf(ws[0, h, d]).all()), way
+        keep = torch.ones(H, 64, dtype=torch.bool, device="cuda")
+        keep[h, d] = False
+        base.close(st[1][keep], ws[0][keep], base.HALF_UNIT[state], wsm[0][keep], base.state_terms(BF16, state, T), "state")
+        base.close(y[:, keep], wy[:, keep], 2.0 ** -8, wm[:, keep], base.y_terms(BF16, T), "y")
+
+
+@pytest.mark.parametrize("state", [F32, F16, BF16])
+@pytest.mark.parametrize("T", [1, 2, 12])
+def test_an_infinite_state_is_read_as_one(state, T):
+    """One infinite element of a checkpoint: its row's outputs are infinite with C's signs, the others as ever."""
+    H, d, h, n = 4, 9, 2, 77
+    x, dt, A, B, C, D = base.tokens((1, T), H, 2, 64, 128, BF16, 5)
+    C = torch.where(C == 0, torch.ones_like(C), C)
+    xc, dtc, _, Bc, _, _ = base.tokens((1, 16), H, 2, 64, 128, BF16, 6)
+    st = base.pool(1, H, 64, 128, state, 7)
+    args = lambda s: (s, i32([0]), xc.clone(), Bc.clone(), dtc.clone(), i32([2]), i32([3]), x, dt, A, B, C)  # noqa: E731
+    clean = rsm.replayssm_decode(*args(st), D=D)
+    st2 = st.clone()
+    st2[0, h, d, n] = float("inf")
+    y = rsm.replayssm_decode(*args(st2), D=D)
+    assert torch.equal(y[0, :, h, d].double(), C[0, :, h // 2, n].double() * float("inf"))
+    y[0, :, h, d] = clean[0, :, h, d]
+    assert torch.equal(y, clean)
