@@ -400,10 +400,38 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
         if (hq < nh) dtc[ring_row(n_ring + t) * p.H + hq] = sdt[(n_ring + t) * nh + hq];
     }
 
-    // the decays up to and with each token; the dots B_s . C_t
-    // (few: each by itself; many: a warp scans.  256 heads, rings of 64, 32 requests, 4 tokens,
-    // fp32: 76 us, 80 without the scan; rings of 8, 256 requests, bf16: 177 us with it, 175 without)
-    if (m <= 16) {
+    // The decays (dt A summed) and the dots B_s . C_t.  With bf16 inputs the decays are those up
+    // to and with each token, and a pair's is the difference of two: sums up to 2^14 leave it
+    // the weight's own 2^-9.  With fp32 inputs a strong decay would take from the pairs after it,
+    // so a ring token's is from it to the ring's end, a new one's from there up to and
+    // with it, and a pair's their sum, of one sign, or for two new tokens that of the tokens between.
+    // (For bf16 inputs too: 256 requests, rings of 8, 186 us for 175; 32 requests, rings of 64, 90 for 79.
+    // With fp32 inputs it costs nothing: 32 requests of 256 heads, 4 tokens, rings of 16, 71 us; 8, rings of 64, 585.)
+    // (bf16, few: each by itself; many: a warp scans.  256 heads, rings of 64, 32 requests, 4 tokens,
+    // fp32 states: 76 us, 80 without the scan; rings of 8, 256 requests, bf16: 177 us with it, 175 without)
+    constexpr bool BY_PARTS = sizeof(IT) == 4;
+    if constexpr (BY_PARTS) {
+      for (int hl = warp; hl < nh; hl += kTokThreads / 32) {
+        const float Ah = __ldg(p.A + h0 + hl);
+        auto scan = [&](float v) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += w;
+          }
+          return v;
+        };
+        float sum = 0.0f;  // of the ring's tokens after these 32
+        for (int s0 = n_ring - 1; s0 >= 0; s0 -= 32) {
+          const int s = s0 - lane;
+          const float v = scan(s >= 0 && s + 1 < n_ring ? sdt[(s + 1) * nh + hl] : 0.0f) + sum;
+          if (s >= 0) sc[s * nh + hl] = v * Ah;
+          sum = __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        const float v = scan(lane < T ? sdt[(n_ring + lane) * nh + hl] : 0.0f);  // (T <= 16)
+        if (lane < T) sc[(n_ring + lane) * nh + hl] = v * Ah;
+      }
+    } else if (m <= 16) {
       if (hq < nh) {
         for (int s = tid >> 4; s < m; s += kTokThreads / 16) {
           float sum = 0.0f;
@@ -480,24 +508,42 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
     // the tokens' weights, a warp per head
     for (int hl = warp; hl < nh; hl += kTokThreads / 32) {
       const float skip = hl == warp ? skip0 : skip1;
-      auto weight = [&](int s, int t) {
+      const float Ah = BY_PARTS ? __ldg(p.A + h0 + hl) : 0.0f;
+      auto weight = [&](int s, int t, float between) {  // between: dt of the tokens between two new ones (by parts)
         const int now = n_ring + t;
         if (s > now || t >= T) return 0.0f;
-        return fmaf(__expf(sc[now * nh + hl] - sc[s * nh + hl]) * sdt[s * nh + hl], sdot[t * m + s], s == now ? skip : 0.0f);
+        const float decay = !BY_PARTS ? __expf(sc[now * nh + hl] - sc[s * nh + hl])
+                                      : expf(s < n_ring ? sc[s * nh + hl] + sc[now * nh + hl] : between * Ah);
+        return fmaf(decay * sdt[s * nh + hl], sdot[t * m + s], s == now ? skip : 0.0f);
       };
-      for (int t = lane; t < T; t += 32) se[hl * T + t] = __expf(sc[(n_ring + t) * nh + hl]);
+      if constexpr (BY_PARTS) {
+        const float ring = n_ring > 0 ? fmaf(sdt[hl], Ah, sc[hl]) : 0.0f;
+        for (int t = lane; t < T; t += 32) se[hl * T + t] = expf(ring + sc[(n_ring + t) * nh + hl]);
+      } else {
+        for (int t = lane; t < T; t += 32) se[hl * T + t] = __expf(sc[(n_ring + t) * nh + hl]);
+      }
       if constexpr (MMA) {
         // pairs of tokens, eight lanes to sixteen of them
         const uint32_t q = m16 >> 4, inv = 65536u / q + 1u;
         uint32_t* w = reinterpret_cast<uint32_t*>(smem + l.w) + hl * T8 * (m16 >> 1);
         for (uint32_t i = lane; i < static_cast<uint32_t>(T8 * (m16 >> 1)); i += 32) {
           const uint32_t t = ((i >> 3) * inv) >> 16, s = 2 * (i - t * (m16 >> 1));
-          w[i] = rsm::pack_bf16x2(weight(s, t), weight(s + 1, t));
+          w[i] = rsm::pack_bf16x2(weight(s, t, 0.0f), weight(s + 1, t, 0.0f));
         }
       } else {
         float* w = reinterpret_cast<float*>(smem + l.w) + hl * T * m;
-        for (int t = 0; t < T; ++t)
-          for (int s = lane; s < m; s += 32) w[t * m + s] = weight(s, t);
+        if constexpr (BY_PARTS) {
+          for (int s = lane; s < m; s += 32) {
+            float between = 0.0f;
+            for (int t = 0; t < T; ++t) {
+              if (s >= n_ring && n_ring + t > s) between += sdt[(n_ring + t) * nh + hl];
+              w[t * m + s] = weight(s, t, between);
+            }
+          }
+        } else {
+          for (int t = 0; t < T; ++t)
+            for (int s = lane; s < m; s += 32) w[t * m + s] = weight(s, t, 0.0f);
+        }
       }
     }
     __syncthreads();

@@ -239,3 +239,28 @@ def test_an_infinite_state_is_read_as_one(state, T):
     assert torch.equal(y[0, :, h, d].double(), C[0, :, h // 2, n].double() * float("inf"))
     y[0, :, h, d] = clean[0, :, h, d]
     assert torch.equal(y, clean)
+
+
+@pytest.mark.parametrize("inputs", [F32, BF16])
+@pytest.mark.parametrize("early", ["ring", "new"])
+def test_decode_mild_tokens_after_strong_ones(inputs, early):
+    """Tokens whose decay is mild, after ring rows or new tokens that decay the state to nothing: a pair's decay is
+    what lies between its tokens, whatever lies before."""
+    R, T, H, G = 64, 8, 4, 2
+    have = R - T if early == "ring" else 1
+    x, dt, A, B, C, D = base.tokens((1, T), H, G, 64, 128, inputs, 1)
+    xc, dtc, _, Bc, _, _ = base.tokens((1, R), H, G, 64, 128, inputs, 2)
+    A = -(16.0 + 16.0 * torch.rand(H, generator=base.gen(3), device="cuda"))
+    dtc, dt = 0.1 * dtc, 0.1 * dt
+    strong = 4.0 + 4.0 * torch.rand((40, H), generator=base.gen(4), device="cuda")
+    if early == "ring":
+        dtc[0, :40] = strong
+    else:
+        dt[0, :4] = strong[:4] * 40.0
+    st = base.pool(1, H, 64, 128, F32, 5)
+    y = rsm.replayssm_decode(st, i32([0]), xc.clone(), Bc.clone(), dtc.clone(), i32([0]), i32([have]), x, dt, A, B, C, D=D)
+    cat = lambda c, t: torch.cat([ref.f64(c[0, :have]), ref.f64(t[0])])  # noqa: E731
+    S = ref.f64(st[0])
+    Cs = torch.cat([torch.zeros(have, G, 128, dtype=torch.float64, device="cuda"), ref.f64(C[0])])
+    wy, wm, _, _ = ref.run_tokens(S, S.abs(), cat(xc, x), cat(dtc, dt), ref.f64(A), cat(Bc, B), Cs, ref.f64(D))
+    base.close(y[0], wy[have:], base.HALF_UNIT[inputs], wm[have:], base.y_terms(inputs, R), "y")
