@@ -174,6 +174,12 @@ def _check_out(out, x):
         raise ValueError(f"out must be {x.dtype} {list(x.shape)}")
 
 
+def _int32(value, name):
+    value = int(value)
+    _need(-2 ** 31 <= value < 2 ** 31, f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def _status(t):
     if t is None:
         return 0
@@ -260,7 +266,7 @@ def ssm_prefill(x, dt, A, B, C, cu_seqlens, state=None, *, initial_slots=None, f
         _need(T < 2 or so >= H * dim, "rows of out overlap")
     args = [x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A.data_ptr(), 0 if D is None else D.data_ptr(),
             cu_seqlens.data_ptr(), ps, pi, pf, out.data_ptr(), 0, _status(device_status), T, sx[0], sB[0], sC[0], sd[0],
-            so, ss, 0, seqs, slots, H, G, dim, N, sd_code, code, int(pad_slot_id)]
+            so, ss, 0, seqs, slots, H, G, dim, N, sd_code, code, _int32(pad_slot_id, "pad_slot_id")]
     packed = _pack_prefill(*args)
     size = lib.rsm_ssm_prefill_workspace(packed)
     if size < 0:
@@ -336,7 +342,7 @@ def ssm_step(state, slots, x, dt, A, B, C, *, dst_slots=None, D=None, pad_slot_i
     rc = lib.rsm_ssm_step(_pack_step(
         x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A.data_ptr(), 0 if D is None else D.data_ptr(),
         state.data_ptr(), slots.data_ptr(), pd, out.data_ptr(), _status(device_status), *strides, state.stride(0), b, T,
-        state.shape[0], H, G, dim, N, sd, code, int(pad_slot_id)), _handle(stream, dev))
+        state.shape[0], H, G, dim, N, sd, code, _int32(pad_slot_id, "pad_slot_id")), _handle(stream, dev))
     if rc != 0:
         _raise("ssm_step", rc)
     return out
@@ -404,8 +410,8 @@ def replayssm_decode(state, slots, x_cache, B_cache, dt_cache, ring_start, ring_
         x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), A.data_ptr(), 0 if D is None else D.data_ptr(),
         state.data_ptr(), pq, x_cache.data_ptr(), B_cache.data_ptr(), dt_cache.data_ptr(), slots.data_ptr(),
         ring_start.data_ptr(), ring_len.data_ptr(), out.data_ptr(), _status(device_status), *strides, state.stride(0), sq,
-        x_cache.stride(0), B_cache.stride(0), dt_cache.stride(0), b, T, S, H, G, dim, N, R, sd, code, int(pad_slot_id)),
-        _handle(stream, dev))
+        x_cache.stride(0), B_cache.stride(0), dt_cache.stride(0), b, T, S, H, G, dim, N, R, sd, code,
+        _int32(pad_slot_id, "pad_slot_id")), _handle(stream, dev))
     if rc != 0:
         _raise("replayssm_decode", rc)
     return out
@@ -492,7 +498,7 @@ def gated_rms_norm(x, z, weight, *, group_size=None, eps=1e-5, norm_before_gate=
     _check_vector(weight, "weight", dim, _F32)
     out, po, so = _result(out, "out", x, shape, stream)
     rc = lib.rsm_gated_rms_norm(_pack_gated(px, pz, weight.data_ptr(), po, x.numel() // dim, sx, sz, so, dim,
-                                            dim if group_size is None else int(group_size), code,
+                                            dim if group_size is None else _int32(group_size, "group_size"), code,
                                             1 if norm_before_gate else 0, float(eps), 0), _handle(stream, dev))
     if rc != 0:
         _raise("gated_rms_norm", rc)

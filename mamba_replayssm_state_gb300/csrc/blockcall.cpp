@@ -73,6 +73,17 @@ bool is(const Tensor& t, at::IntArrayRef sizes, at::ScalarType type) {
 
 bool fits(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
 
+// a Python integer of 32 bits
+bool int32(PyObject* o, int32_t* v) {
+  const long long n = PyLong_AsLongLong(o);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    return false;
+  }
+  *v = static_cast<int32_t>(n);
+  return *v == n;
+}
+
 // x [lead.., H, dim], dt [lead.., H], A [H], B and C [lead.., G, N], D [H] or
 // nothing, with `k` leading dimensions and contiguous inner ones.
 struct Tokens {
@@ -138,8 +149,8 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (initial || final_) {
       return none();
     }
-    const long pad = PyLong_AsLong(a[10]);
-    if (pad == -1 && PyErr_Occurred()) throw 0;
+    int32_t pad;
+    if (!int32(a[10], &pad)) return none();
     const Tensor out = like(*x);
     p.x = x->data_ptr(), p.B = B->data_ptr(), p.C = C->data_ptr();
     p.dt = dt->const_data_ptr<float>(), p.A = A->const_data_ptr<float>(), p.D = static_cast<const float*>(ptr(D));
@@ -150,7 +161,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.x_stride = x->stride(0), p.B_stride = B->stride(0), p.C_stride = C->stride(0), p.dt_stride = dt->stride(0);
     p.out_stride = static_cast<int64_t>(k.H) * k.dim;
     p.num_seqs = static_cast<int32_t>(seqs), p.num_heads = k.H, p.num_groups = k.G, p.dim = k.dim, p.dstate = k.N;
-    p.input_dtype = k.code, p.pad_slot_id = static_cast<int32_t>(pad);
+    p.input_dtype = k.code, p.pad_slot_id = pad;
     const int64_t bytes = abi.prefill_workspace(&p);
     if (bytes < 0) return PyLong_FromLongLong(bytes);
     Tensor workspace;
@@ -193,13 +204,13 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.state_dtype = state_code(*state);
     if (p.state_dtype < 0 || !pool(*state, k) || !vector(*slots, p.batch, at::kInt) || (dst && !vector(*dst, p.batch, at::kInt)))
       return none();
-    const long pad = PyLong_AsLong(a[9]);
-    if (pad == -1 && PyErr_Occurred()) throw 0;
+    int32_t pad;
+    if (!int32(a[9], &pad)) return none();
     const Tensor out = like(*x);
     p.state = state->data_ptr(), p.src_slots = slots->const_data_ptr<int32_t>(), p.dst_slots = static_cast<const int32_t*>(ptr(dst));
     p.out = out.data_ptr();
     p.state_slot_stride = state->stride(0), p.num_slots = static_cast<int32_t>(state->size(0));
-    p.pad_slot_id = static_cast<int32_t>(pad);
+    p.pad_slot_id = pad;
     const int rc = abi.step(&p, c10::cuda::getCurrentCUDAStream(dev).stream());
     return rc != 0 ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
   });
@@ -227,8 +238,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i : {1, 5, 6})
       if (!vector(*t[i], p.batch, at::kInt)) return none();
     if (t[12] != nullptr && !is(*t[12], {S, k.H, k.dim}, at::kFloat)) return none();
-    const long pad = PyLong_AsLong(a[14]);
-    if (pad == -1 && PyErr_Occurred()) throw 0;
+    int32_t pad;
+    if (!int32(a[14], &pad)) return none();
     const Tensor out = like(x);
     p.state = state.data_ptr(), p.state_scale = static_cast<const float*>(ptr(t[12]));
     p.x_cache = xc.data_ptr(), p.B_cache = Bc.data_ptr(), p.dt_cache = dtc.data_ptr<float>();
@@ -236,7 +247,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.out = out.data_ptr();
     p.state_slot_stride = state.stride(0), p.scale_slot_stride = t[12] == nullptr ? 0 : t[12]->stride(0);
     p.x_cache_slot_stride = xc.stride(0), p.B_cache_slot_stride = Bc.stride(0), p.dt_cache_slot_stride = dtc.stride(0);
-    p.num_slots = static_cast<int32_t>(S), p.ring_buffer_len = static_cast<int32_t>(R), p.pad_slot_id = static_cast<int32_t>(pad);
+    p.num_slots = static_cast<int32_t>(S), p.ring_buffer_len = static_cast<int32_t>(R), p.pad_slot_id = pad;
     const int rc = abi.decode(&p, c10::cuda::getCurrentCUDAStream(dev).stream());
     return rc != 0 ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
   });
@@ -294,11 +305,11 @@ PyObject* gated_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return none();
     rsm_gated_rms_norm_args p{};
     p.dim = static_cast<int32_t>(x->size(-1));
-    const long group = a[3] == Py_None ? p.dim : PyLong_AsLong(a[3]);
+    p.group_size = p.dim;
+    if (a[3] != Py_None && !int32(a[3], &p.group_size)) return none();
     p.eps = static_cast<float>(PyFloat_AsDouble(a[4]));
     p.norm_before_gate = PyObject_IsTrue(a[5]);
-    if (PyErr_Occurred() || !fits(group)) throw 0;
-    p.group_size = static_cast<int32_t>(group);
+    if (PyErr_Occurred()) throw 0;
     p.x_stride = row_stride(*x), p.z_stride = row_stride(*z);
     if (p.x_stride < 0 || p.z_stride < 0) return none();
     const Tensor out = like(*x);

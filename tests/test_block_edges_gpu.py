@@ -264,3 +264,31 @@ def test_decode_mild_tokens_after_strong_ones(inputs, early):
     Cs = torch.cat([torch.zeros(have, G, 128, dtype=torch.float64, device="cuda"), ref.f64(C[0])])
     wy, wm, _, _ = ref.run_tokens(S, S.abs(), cat(xc, x), cat(dtc, dt), ref.f64(A), cat(Bc, B), Cs, ref.f64(D))
     base.close(y[0], wy[have:], base.HALF_UNIT[inputs], wm[have:], base.y_terms(inputs, R), "y")
+
+
+def every_call(T=2):
+    """The operators with a pad slot, as functions of it."""
+    x, dt, A, B, C, D = base.tokens((3, T), 4, 2, 64, 128, BF16, 1)
+    xc, dtc, _, Bc, _, _ = base.tokens((3, 8), 4, 2, 64, 128, BF16, 2)
+    st = base.pool(3, 4, 64, 128, F32, 3)
+    slots, zero = i32([0, 1, 2]), i32([0, 0, 0])
+    flat = lambda t: t.flatten(0, 1)  # noqa: E731
+    return {
+        "prefill": lambda **k: rsm.ssm_prefill(flat(x), flat(dt), A, flat(B), flat(C), i32([0, 1, 2, 3 * T]), st,
+                                               initial_slots=slots, final_slots=slots, **k),
+        "step": lambda **k: rsm.ssm_step(st, slots, x, dt, A, B, C, **k),
+        "decode": lambda **k: rsm.replayssm_decode(st, slots, xc, Bc, dtc, zero, zero, x, dt, A, B, C, **k)}
+
+
+@pytest.mark.parametrize("name", ["prefill", "step", "decode"])
+@pytest.mark.parametrize("pad", [2 ** 32 - 1, 2 ** 31, -2 ** 31 - 1, 2 ** 70])
+def test_a_pad_slot_past_32_bits_is_refused(name, pad):
+    call = every_call()[name]
+    with pytest.raises(ValueError, match="pad_slot_id"):
+        call(pad_slot_id=pad)
+
+
+def test_a_group_size_past_32_bits_is_refused():
+    x, w = torch.ones(2, 64, device="cuda"), torch.ones(64, device="cuda")
+    with pytest.raises(ValueError, match="group_size"):
+        rsm.gated_rms_norm(x, x, w, group_size=2 ** 32 + 64)
