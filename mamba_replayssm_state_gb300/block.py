@@ -12,7 +12,8 @@ Each call checks its tensors, passes their addresses and strides to the C ABI
 (include/replayssm_block.h, which states the semantics) and enqueues the
 kernels on the current CUDA stream, or on `stream`.  Results and workspaces
 that the caller does not pass are allocated on that stream.  There is no
-fallback: without the library the calls raise.
+fallback: without the library the calls raise.  While gradients are recorded,
+a tensor that requires one is refused: there is no backward pass to take it.
 
 The usual calls (the current stream, results allocated, no status word, tensors
 as the kernels take them) are checked and marshalled by _blockcall, a C++
@@ -131,6 +132,13 @@ def _check_device(*tensors):
     _need(devices == {torch.cuda.current_device()}, "tensors must be on the current CUDA device")
 
 
+def _check_grad(*tensors):
+    """None wants a gradient that the call would not pass on."""
+    if torch.is_grad_enabled():
+        _need(not any(t is not None and t.requires_grad for t in tensors),
+              "the operators are forward only, and a tensor requires a gradient: detach it, or call under torch.no_grad()")
+
+
 def _check_rows(t, name, shape, inner, dtype):
     """t has the shape, and its last `inner` dimensions are contiguous."""
     if t.dtype != dtype:
@@ -228,6 +236,7 @@ def ssm_prefill(x, dt, A, B, C, cu_seqlens, state=None, *, initial_slots=None, f
         r = _calls.prefill(x, dt, A, B, C, cu_seqlens, state, initial_slots, final_slots, D, pad_slot_id)
         if r is not None:
             return r if type(r) is not int else _raise("ssm_prefill", r)
+    _check_grad(x, dt, A, B, C, D, state, out)
     sx, sB, sC, sd = x.stride(), B.stride(), C.stride(), dt.stride()
     shape, code, dev = x.shape, _INPUTS.get(x.dtype), x.get_device()
     if not (code is not None and len(shape) == 3 and B.shape == C.shape and len(sB) == 3 and dt.shape == shape[:2]
@@ -317,6 +326,7 @@ def ssm_step(state, slots, x, dt, A, B, C, *, dst_slots=None, D=None, pad_slot_i
         r = _calls.step(state, slots, x, dt, A, B, C, dst_slots, D, pad_slot_id)
         if r is not None:
             return r if type(r) is not int else _raise("ssm_step", r)
+    _check_grad(x, dt, A, B, C, D, state, out)
     code, b, T, H, G, dim, N, *strides = _batch(x, dt, A, B, C, D)
     dev = x.get_device()
     if not (dev >= 0 and dev == B.get_device() == C.get_device() == dt.get_device() == A.get_device()
@@ -371,6 +381,7 @@ def replayssm_decode(state, slots, x_cache, B_cache, dt_cache, ring_start, ring_
                           pad_slot_id)
         if r is not None:
             return r if type(r) is not int else _raise("replayssm_decode", r)
+    _check_grad(x, dt, A, B, C, D, state, x_cache, B_cache, dt_cache, state_scale, out)
     code, b, T, H, G, dim, N, *strides = _batch(x, dt, A, B, C, D)
     dev = x.get_device()
     if not (dev >= 0 and dev == B.get_device() == C.get_device() == dt.get_device() == A.get_device()
@@ -456,6 +467,7 @@ def add_rms_norm(x, residual, weight, *, residual_scale=1.0, eps=1e-5, out=None,
         r = _calls.add_norm(x, residual, weight, residual_scale, eps)
         if r is not None:
             return r if type(r) is not int else _raise("add_rms_norm", r)
+    _check_grad(x, residual, weight, out, residual_out)
     shape, code, rcode, dev = x.shape, _INPUTS.get(x.dtype), _INPUTS.get(residual.dtype), x.get_device()
     _need(len(shape) >= 1 and shape[-1] > 0, "x must have a last dimension")
     _need(code is not None and rcode is not None, "x and residual must be bfloat16 or float32")
@@ -487,6 +499,7 @@ def gated_rms_norm(x, z, weight, *, group_size=None, eps=1e-5, norm_before_gate=
         r = _calls.gated_norm(x, z, weight, group_size, eps, norm_before_gate)
         if r is not None:
             return r if type(r) is not int else _raise("gated_rms_norm", r)
+    _check_grad(x, z, weight, out)
     shape, code, dev = x.shape, _INPUTS.get(x.dtype), x.get_device()
     _need(len(shape) >= 1 and shape[-1] > 0, "x must have a last dimension")
     _need(code is not None, f"x must be bfloat16 or float32, got {x.dtype}")

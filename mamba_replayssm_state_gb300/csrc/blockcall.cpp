@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -37,12 +38,13 @@ PyObject* none() { Py_RETURN_NONE; }
 // The tensor, or nullptr for anything else.
 const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// All tensors on the current device (nullptr: not given); its index, or -1.
+// All tensors on the current device, and none wants a gradient (nullptr: not given); its index, or -1.
 template <int N>
 int device_of(const Tensor* const (&ts)[N]) {
   const int d = c10::cuda::current_device();
+  const bool grad = c10::GradMode::is_enabled();
   for (const Tensor* t : ts)
-    if (t != nullptr && !(t->is_cuda() && t->get_device() == d)) return -1;
+    if (t != nullptr && !(t->is_cuda() && t->get_device() == d && !(grad && t->requires_grad()))) return -1;
   return d;
 }
 

@@ -292,3 +292,36 @@ def test_a_group_size_past_32_bits_is_refused():
     x, w = torch.ones(2, 64, device="cuda"), torch.ones(64, device="cuda")
     with pytest.raises(ValueError, match="group_size"):
         rsm.gated_rms_norm(x, x, w, group_size=2 ** 32 + 64)
+
+
+def grad_calls():
+    """(operator, its tensor arguments that could want a gradient)."""
+    x, dt, A, B, C, D = base.tokens((3, 2), 4, 2, 64, 128, BF16, 1)
+    xc, dtc, _, Bc, _, _ = base.tokens((3, 8), 4, 2, 64, 128, BF16, 2)
+    st = base.pool(3, 4, 64, 128, F32, 3)
+    slots, zero = i32([0, 1, 2]), i32([0, 0, 0])
+    flat = lambda t: t.detach().flatten(0, 1).requires_grad_(t.requires_grad)  # noqa: E731
+    g, r, w = torch.randn(4, 64, device="cuda"), torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    return [
+        (lambda x, dt, A, B, C, D, **k: rsm.ssm_prefill(flat(x), flat(dt), A, flat(B), flat(C), i32([0, 6]), D=D, **k),
+         [x, dt, A, B, C, D]),
+        (lambda x, dt, A, B, C, D, **k: rsm.ssm_step(st.clone(), slots, x, dt, A, B, C, D=D, **k), [x, dt, A, B, C, D]),
+        (lambda x, dt, A, B, C, D, **k: rsm.replayssm_decode(st, slots, xc.clone(), Bc.clone(), dtc.clone(), zero, zero, x,
+                                                             dt, A, B, C, D=D, **k), [x, dt, A, B, C, D]),
+        (lambda x, r, w, **k: rsm.add_rms_norm(x, r, w, **k)[0], [g, r, w]),
+        (lambda x, z, w, **k: rsm.gated_rms_norm(x, z, w, **k), [g, r, w])]
+
+
+@pytest.mark.parametrize("op", range(5), ids=["prefill", "step", "decode", "add_norm", "gated_norm"])
+def test_a_gradient_that_would_be_lost_is_refused(op):
+    """The operators are forward only: an input that wants a gradient is refused while gradients are recorded, by
+    either way into the library, and served as ever where they are not."""
+    call, tensors = grad_calls()[op]
+    want = call(*tensors)
+    for i, t in enumerate(tensors):
+        args = [*tensors[:i], t.clone().requires_grad_(), *tensors[i + 1:]]
+        for way in ({}, {"out": torch.empty_like(want)}):
+            with pytest.raises(ValueError, match="forward only"):
+                call(*args, **way)
+            with torch.no_grad():
+                assert torch.equal(call(*args, **way), want)
