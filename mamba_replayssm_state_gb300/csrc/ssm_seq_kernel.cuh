@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(4 * D) ssm_seq_kernel(const __grid_constant__ 
   const float* dt = p.dt + batch * p.dt_bs + t0 * p.dt_ts + h;
   IT* out = static_cast<IT*>(p.out) + batch * p.out_bs + t0 * p.out_ts + static_cast<int64_t>(h) * D;
   if (!live) {
-    for (int i = tid; i < n_new * D; i += kThreads) store_in(out + (i / D) * p.out_ts + i % D, 0.0f);
+    for (int64_t i = tid; i < static_cast<int64_t>(n_new) * D; i += kThreads) store_in(out + (i / D) * p.out_ts + i % D, 0.0f);
     return;
   }
 

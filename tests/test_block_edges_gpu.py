@@ -325,3 +325,14 @@ def test_a_gradient_that_would_be_lost_is_refused(op):
                 call(*args, **way)
             with torch.no_grad():
                 assert torch.equal(call(*args, **way), want)
+
+
+def test_a_skipped_request_of_a_window_past_32_bit_offsets_is_zero():
+    """Its output rows hold more than 2^31 values (4.3 GB)."""
+    T = (1 << 31) // 16 + 3
+    x = torch.zeros((1, 1, 1, 16), dtype=BF16, device="cuda").expand(1, T, 1, 16)
+    dt = torch.zeros((1, 1, 1), device="cuda").expand(1, T, 1)
+    out = torch.full((1, T, 1, 16), 7.0, dtype=BF16, device="cuda")
+    st = torch.zeros((1, 1, 16, 16), device="cuda")
+    rsm.ssm_step(st, i32([-1]), x, dt, torch.zeros(1, device="cuda"), x, x, out=out)
+    assert not bool(out.any())
