@@ -336,3 +336,116 @@ def test_a_skipped_request_of_a_window_past_32_bit_offsets_is_zero():
     st = torch.zeros((1, 1, 16, 16), device="cuda")
     rsm.ssm_step(st, i32([-1]), x, dt, torch.zeros(1, device="cuda"), x, x, out=out)
     assert not bool(out.any())
+
+
+def same_both_ways(make, call):
+    """The call with and without a status word (marshalled by block.py, and by _blockcall): equal to the bit."""
+    a, b = make(), make()
+    ya, yb = call(a, device_status=word()), call(b)
+    assert torch.equal(ya, yb)
+    for p, q in zip(a, b):
+        assert p is q or p is None or torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+@pytest.mark.parametrize("state", [F32, BF16, F16, torch.int8, torch.float8_e4m3fn], ids=str)
+@pytest.mark.parametrize("inputs,T,sliced,skip", [(BF16, 1, 0, True), (BF16, 4, 3, False), (F32, 2, 8, True), (BF16, 0, 0, False)])
+def test_decode_marshalled_either_way(state, inputs, T, sliced, skip):
+    """T = 0: tokens without the window dimension."""
+    b, R, H, G = 4, 16, 6, 2
+    x, dt, A, B, C, D = base.tokens((b, T) if T else (b,), H, G, 64, 128, inputs, 3, sliced)
+    xc, dtc, _, Bc, _, _ = base.tokens((b + 1, R), H, G, 64, 128, inputs, 4)
+    scale = None
+    if state in (torch.int8, torch.float8_e4m3fn):
+        st = torch.randint(-127, 128, (b + 1, H, 64, 128), generator=base.gen(5), device="cuda", dtype=torch.int8)
+        st = st if state == torch.int8 else st.to(F16).to(state)
+        scale = 0.01 + 0.05 * torch.rand((b + 1, H, 64), generator=base.gen(6), device="cuda")
+    else:
+        st = base.pool(b + 1, H, 64, 128, state, 5)
+    same_both_ways(lambda: (st.clone(), xc.clone(), Bc.clone(), dtc.clone()),
+                   lambda m, **k: rsm.replayssm_decode(m[0], i32([3, -1, 1, 4]), *m[1:], i32([0, 3, 15, 9]), i32([5, 0, 12, 1]),
+                                                       x, dt, A, B, C, state_scale=scale, D=D if skip else None, **k))
+
+
+@pytest.mark.parametrize("state", [F32, BF16, F16], ids=str)
+@pytest.mark.parametrize("inputs,T,sliced,skip", [(BF16, 1, 0, True), (BF16, 4, 3, False), (F32, 2, 8, True), (BF16, 0, 0, False)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_step_marshalled_either_way(state, inputs, T, sliced, skip, in_place):
+    b, H, G = 4, 6, 2
+    x, dt, A, B, C, D = base.tokens((b, T) if T else (b,), H, G, 64, 128, inputs, 3, sliced)
+    st = base.pool(2 * b, H, 64, 128, state, 5)
+    same_both_ways(lambda: (st.clone(),),
+                   lambda m, **k: rsm.ssm_step(m[0], i32([3, -1, 1, 0]), x, dt, A, B, C, dst_slots=None if in_place else i32([7, 6, -1, 4]),
+                                               D=D if skip else None, **k))
+
+
+@pytest.mark.parametrize("state", [F32, BF16, F16, None], ids=str)
+@pytest.mark.parametrize("inputs,lens,sliced,skip", [(BF16, [3], 0, True), (BF16, [140, 0, 33], 8, False), (F32, [20, 7], 0, True),
+                                                     (BF16, [30, 90], 3, True), (BF16, [2500], 0, False)])
+def test_prefill_marshalled_either_way(state, inputs, lens, sliced, skip):
+    S, H, G = len(lens), 6, 2
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0, dtype=torch.int32)
+    x, dt, A, B, C, D = base.tokens((sum(lens),), H, G, 64, 128, inputs, 3, sliced)
+    st = None if state is None else base.pool(2 * S, H, 64, 128, state, 5)
+    final = list(range(2 * S - 1, S - 1, -1))
+    if S > 1:
+        final[-1] = -1
+    slots = {} if state is None else dict(initial_slots=i32([-1] + list(range(1, S))), final_slots=i32(final))
+    same_both_ways(lambda: (None if st is None else st.clone(),),
+                   lambda m, **k: rsm.ssm_prefill(x, dt, A, B, C, cu, m[0], D=D if skip else None, **slots, **k))
+
+
+def test_calls_recorded_in_a_graph():
+    """Each operator as a graph replays it, results and workspaces from the graph's pool, on inputs that changed since."""
+    x, dt, A, B, C, D = base.tokens((2500,), 4, 2, 64, 128, BF16, 1)
+    xt, dtt, _, Bt, Ct, _ = base.tokens((2, 3), 4, 2, 64, 128, BF16, 2)
+    xc, dtc, _, Bc, _, _ = base.tokens((2, 16), 4, 2, 64, 128, BF16, 3)
+    st, w = base.pool(2, 4, 64, 128, F32, 4), torch.ones(256, device="cuda")
+    cu, slots, start, have = i32([0, 2500]), i32([0, 1]), i32([3, 9]), i32([2, 5])
+    rows = torch.randn(4, 256, device="cuda")
+    results = lambda: (rsm.ssm_prefill(x, dt, A, B, C, cu, D=D), rsm.ssm_step(st, slots, xt, dtt, A, Bt, Ct, D=D),  # noqa: E731
+                       rsm.replayssm_decode(st, slots, xc, Bc, dtc, start, have, xt, dtt, A, Bt, Ct, D=D),
+                       *rsm.add_rms_norm(rows, rows, w), rsm.gated_rms_norm(rows, rows, w))
+    before = st.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        results()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        recorded = results()
+    for t in (x, xt, rows):
+        t.neg_()
+    st.copy_(before)
+    graph.replay()
+    got = [t.clone() for t in recorded]
+    st.copy_(before)
+    for a, b in zip(got, results()):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("inputs", [BF16, F32])
+def test_rows_that_no_token_reaches_may_hold_anything(inputs):
+    """NaN in ring rows outside the window, in other slots, in tokens of no sequence and in a skipped request."""
+    nan = float("nan")
+    x, dt, A, B, C, D = base.tokens((3, 2), 4, 2, 64, 128, inputs, 1)
+    xc, dtc, _, Bc, _, _ = base.tokens((4, 16), 4, 2, 64, 128, inputs, 2)
+    st = base.pool(4, 4, 64, 128, F32, 3)
+    args = lambda s, x, B, C, dt, c: (s, i32([2, -1, 0]), *c, i32([14, 0, 3]), i32([5, 0, 0]), x, dt, A, B, C)  # noqa: E731
+    clean = [t.clone() for t in (xc, Bc, dtc)]
+    want = rsm.replayssm_decode(*args(st, x, B, C, dt, clean), D=D)
+    used = torch.zeros(4, 16, dtype=torch.bool, device="cuda")
+    used[2, [14, 15, 0, 1, 2]] = True
+    dirty = [torch.where(used.view(4, 16, *[1] * (t.dim() - 2)), t, nan) for t in (xc, Bc, dtc)]
+    st2, x2, B2, C2, dt2 = (t.clone() for t in (st, x, B, C, dt))
+    st2[[1, 3]] = nan
+    for t in (x2, B2, C2, dt2):
+        t[1] = nan
+    assert torch.equal(rsm.replayssm_decode(*args(st2, x2, B2, C2, dt2, dirty), D=D), want)
+    for n in (5, 40, 150):
+        p = base.tokens((200,), 4, 2, 64, 128, inputs, 4)
+        want = rsm.ssm_prefill(*p[:5], i32([20, 20 + n]), D=p[5])[20:20 + n].clone()
+        for t in (p[0], p[1], p[3], p[4]):
+            t[:20] = nan
+            t[20 + n:] = nan
+        assert torch.equal(rsm.ssm_prefill(*p[:5], i32([20, 20 + n]), D=p[5])[20:20 + n], want)
