@@ -23,7 +23,20 @@
  * written, but may overflow before it would in exact arithmetic).  States: fp32,
  * bf16, fp16; the ring form also reads int8 and fp8 e4m3 with a scale per (head,
  * dim row).  (dim, dstate): (16,16), (64,64), (64,128); one-byte (64,128) only.
- * Arithmetic is fp32; the state is rounded once, when it is stored.
+ *
+ * Arithmetic.  Sums and states are fp32 everywhere, and a state is rounded to its
+ * type once a call, when it is stored.  With fp32 inputs, and states that are not 64
+ * x 128, all else is fp32 too.  With bf16 inputs and 64 x 128 states products may run
+ * on the tensor cores, and their operands are rounded:
+ *   prompts (8 tokens and more whose rows are whole 16-byte vectors): the weight of a
+ *     token pair, D in a token's own, and the state as outputs read it, to bf16; what a
+ *     token adds to the state to 16 bits, or to bf16 where no final state is kept or it is bf16
+ *   2 to 8 tokens of a step, and up to 16 after a ring (but one, on fp16 states):
+ *     the weights, D in them, to bf16; an fp32 state as outputs read it, and what a
+ *     token adds to a state, to 16 bits
+ * With M the sum of the absolute values of the terms an element is made of, such an
+ * output is within 2^-8 |y| + (2^-8 + 2^-15) M, and a state within 2^-15 M (bf16
+ * states after a prompt: as outputs) and the rounding to its type.
  *
  * Layout.  A token's x is [num_heads, dim], B and C [num_groups, dstate], dt
  * [num_heads], all contiguous; strides between tokens (and requests) are given
@@ -83,7 +96,9 @@ RSM_API int64_t rsm_ssm_prefill_workspace(const rsm_ssm_prefill_args *args);
  * order to state[src_slots[b]] and stored to state[dst_slots[b]] (NULL: in
  * place).  A request whose source slot is pad_slot_id is skipped: its output
  * rows are zero and nothing is stored; a destination of pad_slot_id is not
- * stored.  Slots out of range count as pad_slot_id and are flagged.
+ * stored.  Destinations are distinct and are no other request's source (requests
+ * have no order among themselves); a request's own may coincide.  Slots out of
+ * range count as pad_slot_id and are flagged.
  */
 typedef struct rsm_ssm_step_args {
   const void *x, *B, *C;   /* [batch, window, ...] input_dtype */

@@ -226,9 +226,9 @@ def ssm_prefill(x, dt, A, B, C, cu_seqlens, state=None, *, initial_slots=None, f
     x [tokens, H, dim], B and C [tokens, G, dstate] (bf16 or fp32), dt
     [tokens, H], A [H], D [H] or None (fp32); cu_seqlens [seqs + 1] int32.
     Sequence s starts from state[initial_slots[s]] (default: from zero) and
-    leaves its state in state[final_slots[s]] (default: nowhere); the pool
-    `state` is [slots, H, dim, dstate] fp32, bf16 or fp16.  Returns the outputs,
-    [tokens, H, dim].  A long call of few sequences needs a workspace, which is
+    leaves its state in state[final_slots[s]] (default: nowhere), a slot that is
+    no other sequence's; the pool `state` is [slots, H, dim, dstate] fp32, bf16 or
+    fp16.  Returns the outputs, [tokens, H, dim].  A long call of few sequences needs a workspace, which is
     allocated where `workspace` (a contiguous uint8 CUDA tensor) is not given.
     """
     lib = _lib or _load()
@@ -318,8 +318,9 @@ def ssm_step(state, slots, x, dt, A, B, C, *, dst_slots=None, D=None, pad_slot_i
     x [batch, window, H, dim], dt [batch, window, H], B and C [batch, window, G,
     dstate]; without the window dimension, one token each.  The tokens are
     applied in order to state[slots[b]] and the result is stored to
-    state[dst_slots[b]] (default: in place).  Returns the outputs, shaped like
-    x; rows of a request with the pad slot are zero.
+    state[dst_slots[b]] (default: in place); destinations are distinct and no
+    other request's source.  Returns the outputs, shaped like x; rows of a
+    request with the pad slot are zero.
     """
     lib = _lib or _load()
     if stream is None and out is None and device_status is None:
@@ -370,7 +371,7 @@ def replayssm_decode(state, slots, x_cache, B_cache, dt_cache, ring_start, ring_
     Request b's state is state[slots[b]] advanced by ring rows ring_start[b] ..
     ring_start[b] + ring_len[b] - 1 (modulo the ring's length); the new tokens
     (x, dt, B, C as for ssm_step) follow, and are written to the ring rows after
-    those.  The caller advances ring_len.  Caches are one layer's x [slots, R, H,
+    those.  The slots are distinct.  The caller advances ring_len.  Caches are one layer's x [slots, R, H,
     dim], B [slots, R, G, dstate] and dt [slots, R, H], as replayssm_materialize
     reads them; one-byte states come with state_scale [slots, H, dim].
     Returns the outputs, shaped like x; rows of a skipped request are zero.

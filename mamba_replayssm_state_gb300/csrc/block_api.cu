@@ -240,8 +240,8 @@ int64_t workspace_bytes(const PrefillPlan& pl, int H) {
 // of a CTA with two heads, about 3 us, and measured: a chunk of one head 0.83; a
 // states-only chunk half of a whole one; a unit (a segment of a head group) one to begin
 // and end; the two launches more about four.  80 heads, cut into 1, 3, 7, 11 and 19
-// segments: one sequence of 32768 tokens takes 696, 391, 359, 360 and 370 us, one of 4096
-// 96, 68, 71, 73 and more; one of 1024 takes 23 us with a head a CTA and 31 with two.
+// segments: one sequence of 32768 tokens takes 719, 414, 381, 377 and 390 us, one of 4096
+// 102, 78, 82, 84 and 94 (L2 flushed before each); one of 1024 takes 23 us with a head a CTA and 31 with two.
 PrefillPlan plan_prefill(const rsm_ssm_prefill_args* a, int sms) {
   PrefillPlan pl{};
   const int64_t chunks = (a->tokens + static_cast<int64_t>(a->num_seqs) * ssm::kChunk - 1) /
@@ -317,9 +317,7 @@ int launch_tc(const rsm_ssm_prefill_args* a, const ssm::Params& p, void* stream)
   return done();
 }
 
-// New tokens: 64 x 128 states whose rows are whole vectors, up to 16 tokens a
-// request; the rest runs on the sequential kernel.
-// The token kernel for 64 x 128 states on 16 bytes and up to 16 new tokens, the sequential
+// New tokens: the token kernel for 64 x 128 states on 16 bytes and up to 16 new tokens, the sequential
 // kernel for the rest.  (Ring of 16, 4 new tokens, 64 requests of 256 heads, bf16: 52 us
 // and 603; one token to the state itself: 93 and 578; one request of 80 heads, fp32: 6.7
 // and 8.7.)  With bf16 inputs the products go to the tensor cores, but for a single

@@ -9,7 +9,9 @@
 //   Y1 = C S^T           [i, (h, d)]
 //   Y2 = P X             [i, d]       P = G o decay o dt, masked, in tensor memory as bf16
 //   U  = B^T (w X)       [n, (h, d)]  w X as bf16 hi + lo (16 bits), or hi alone for bf16 states
-// The skip term D x is a D on P's diagonal.
+// The skip term D x is a D on P's diagonal, rounded to bf16 with it.  P, the state's copy
+// and w x are what is rounded on the way: each term of an output once, within 2^-8, as the output
+// itself is; what a state sums keeps 16 bits unless it is stored in 8.
 //
 // Decays.  With p_i the sum of a from the start of i's half of the chunk, a pair
 // (i, j) of one half decays by e^{p_i} e^{-p_j}: the column factor goes into P (one
@@ -33,7 +35,7 @@
 //                column, and its bf16 copy for Y1; between the two, y out of Y1 and Y2
 // What bounds it is latency, the way round of a chunk: Y2 and Y1 to y and the next Y2 (bf16
 // states), and S to Y1 to lo to U to S (others).  Measured on a GB300: a chunk and pair of
-// heads takes 2.55 us with bf16 states and 2.95 with fp32 ones (4900 and 5600 cycles), of
+// heads takes 2.5 us with bf16 states and 3.0 with fp32 ones (4900 and 5800 cycles), of
 // which the four products are 2050 and 2560 cycles; 4 sequences of 8192 tokens in all, 256
 // heads, bf16 states: 170 to 180 us, 390 TFLOP/s.
 // A sequence's last chunk may be partial: dt counts as 0 there, and the rows of

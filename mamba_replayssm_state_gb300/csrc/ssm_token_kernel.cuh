@@ -19,9 +19,9 @@
 //
 // With bf16 inputs the products are on the tensor cores (mma.sync m16n8k16: 16 rows, 8
 // tokens), the state as bf16: exact for bf16, int8 and fp8, as hi + lo for fp16 (exact)
-// and fp32 (within 2^-17); only the weights of the tokens are rounded.  Several tokens to
-// the state itself are an empty ring's, and the update one product more.  A lane takes 16
-// bytes of a row at a time, k being numbered to suit.  (Rows through shared memory by
+// and fp32 (within 2^-17).  The weights of the tokens, D in a token's own, are rounded to
+// bf16.  Several tokens to the state itself are an empty ring's, and the update, of the state
+// as it is, one product more, w x in it as hi + lo (within 2^-17).  A lane takes 16 bytes of a row at a time, k being numbered to suit.  (Rows through shared memory by
 // bulk copies, two or three heads ahead, measured slower: what they take of it is CTAs,
 // and with them the heads in whose time another CTA's staging passes.)
 //
@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(kTokThreads, SF == RSM_F32 || MODE == 1 || MOD
     }
 
     // The decays (dt A summed) and the dots B_s . C_t.  With bf16 inputs the decays are those up
-    // to and with each token, and a pair's is the difference of two: sums up to 2^14 leave it
-    // the weight's own 2^-9.  With fp32 inputs a strong decay would take from the pairs after it,
+    // to and with each token, and a pair's is the difference of two: sums up to 2^14 leave the
+    // weight within 2^-9, half its rounding.  With fp32 inputs a strong decay would take from the pairs after it,
     // so a ring token's is from it to the ring's end, a new one's from there up to and
     // with it, and a pair's their sum, of one sign, or for two new tokens that of the tokens between.
     // (For bf16 inputs too: 256 requests, rings of 8, 186 us for 175; 32 requests, rings of 64, 90 for 79.
