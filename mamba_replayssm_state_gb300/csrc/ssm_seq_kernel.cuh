@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(4 * D) ssm_seq_kernel(const __grid_constant__ 
     t0 = __ldg(p.cu_seqlens + unit);
     const int64_t t1 = __ldg(p.cu_seqlens + unit + 1);
     int runs = within(static_cast<int>(t0), static_cast<int>(t1), p.tokens) ? 1 : 0;
-    if (unit > 0) {
+    if (unit > 0) {  // nor does cu_seqlens go back before it
       for (int i = tid; i < unit; i += kThreads) runs &= goes_back(__ldg(p.cu_seqlens + i), __ldg(p.cu_seqlens + i + 1)) ? 0 : 1;
       runs = __syncthreads_and(runs);
     }

@@ -16,10 +16,12 @@
 // Decays.  With p_i the sum of a from the start of i's half of the chunk, a pair
 // (i, j) of one half decays by e^{p_i} e^{-p_j}: the column factor goes into P (one
 // product an element, no exponential), the row factor onto Y2 when y = m1 Y1 + m2
-// Y2 leaves.  A pair across the halves is e^{p_i} e^{rest of the first half}.  Both factors
-// are taken from p's middle, the half's decay's square root: e^{mid - p_j} and e^{p_i - mid},
-// which leaves G, x and their sums 2^77 either way where a half decays by 2^-100.  One that
-// decays by more ("steep", a mean dt A above 1.08) takes an exponential of p_i - p_j an element.  The
+// Y2 leaves.  A pair across the halves is e^{p_i} e^{rest of the first half}.  Where a half
+// decays by more than 2^-32 both factors are taken from its middle, e^{mid - p_j} and e^{p_i -
+// mid}: none is beyond 2^50 then, and G, x and their sums have 2^77 left either way.  A half
+// that decays by more than 2^-100 ("steep", a mean dt A above 1.08) takes an exponential of p_i -
+// p_j an element.  (From the middle always: weights near 1 then round differently from those of
+// new tokens, and a prompt differs more from the same tokens in pieces, 1.1e-2 -> 1.35e-2.)  The
 // weights towards a chunk's end are summed from there, so that small decays near it
 // keep their precision next to large ones before them.
 //
@@ -177,6 +179,7 @@ __device__ __forceinline__ void tmem_ld8x2(uint32_t ta, uint32_t tb, float (&a)[
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSteep = 100.0f;  // decay of a half chunk, log2, past which 2^(mid - p) is not formed
+constexpr float kMild = 32.0f;    // ... and up to which mid is 0
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -431,7 +434,8 @@ __device__ __forceinline__ bool run_tables(const Cta& c, int h) {
       before = (lane & 15) == 0 ? 0.0f : bx;
       beyond = (lane & 15) == 15 ? 0.0f : by;
       const bool steep = !(fabsf(second ? half1 : half0) <= kSteep);
-      const float mid = steep ? 0.0f : 0.5f * (second ? half1 : half0), mid1 = __shfl_sync(0xFFFFFFFFu, mid, 31);
+      const float mid = steep || fabsf(second ? half1 : half0) <= kMild ? 0.0f : 0.5f * (second ? half1 : half0);
+      const float mid1 = __shfl_sync(0xFFFFFFFFu, mid, 31);
       const float start = second ? half0 + mid : mid, rest1 = second ? 0.0f : half1;
       before -= mid;
       const uint32_t st = j & 1u;

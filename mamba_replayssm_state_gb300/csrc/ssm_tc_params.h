@@ -34,7 +34,7 @@ constexpr uint32_t kOffY = kOffX + 4 * kTile;  // of a head's 32 rows: 32 column
 constexpr uint32_t kYBytes = 2 * 32 * 32;
 // A table of [stage][head], made by a dt warp; fp32, 128 tokens where not said otherwise.
 // p is the decay (log2) from the start of a token's half of the chunk up to and with it, mid
-// half of the half's (a steep half: 0).
+// half of the half's (a mild or a steep one: 0).
 enum Table : uint32_t {
   kTabCol = 0,     // dt 2^(mid-p): what a column of P is scaled by in its own half (a steep half: p itself)
   kTabDt = 512,    // dt

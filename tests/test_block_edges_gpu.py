@@ -166,11 +166,11 @@ def check_decays(rates, state=F32, size=1.0, T=300, skip=True):
 LN2 = 0.6931471805599453
 
 
-@pytest.mark.parametrize("log2", [40.0, 90.0, 99.5, 100.5, 140.0])
-@pytest.mark.parametrize("size", [1.0, 4096.0])
+@pytest.mark.parametrize("log2", [20.0, 31.0, 33.0, 40.0, 90.0, 99.5, 100.5, 140.0])
+@pytest.mark.parametrize("size", [1.0, 4096.0, 2.0 ** -20])
 def test_prefill_decays_of_a_half_chunk(log2, size):
     """64 tokens decay by about 2^-log2, on either side of where the kernel changes its way, values small and large
-    (the largest sums, near 2^45, are far inside every type here)."""
+    (sums from 2^-60 to 2^45 are far inside every type here)."""
     g = base.gen(11)
     rates = LN2 * log2 / 64 * (0.8 + 0.4 * torch.rand((300, 4), generator=g, device="cuda"))
     check_decays(rates, size=size)
