@@ -9,8 +9,10 @@ passes pointers.  There is no fallback: if the library is missing or cannot
 load, calls raise.
 
 The operators of the layer around that call (ssm_prefill, ssm_step,
-replayssm_decode, add_rms_norm, gated_rms_norm) are block.py's; it is imported
-when one of them is first asked for, since it needs torch.
+replayssm_decode, add_rms_norm, gated_rms_norm) are block.py's, those of a hybrid
+stack's convolutions and attention layers (causal_conv, causal_conv_step,
+rotary_append, paged_attention, copy_pages, rotary_frequencies) hybrid.py's; they
+are imported when one of them is first asked for, since they need torch.
 
 The torch.compile dependency anchors of the API page (dependency_inputs /
 dependency_outputs) are accepted and ignored: they carry no data.
@@ -22,14 +24,15 @@ import os
 
 __all__ = ["replayssm_materialize", "gated_delta_rule_replayssm_commit", "prepare", "launch_config", "kernel_name",
            "pointer_table", "stride_table", "library_path", "load_library", "ReplaySSMError", "STATUS_BITS",
-           "ssm_prefill", "ssm_step", "replayssm_decode", "add_rms_norm", "gated_rms_norm"]
+           "ssm_prefill", "ssm_step", "replayssm_decode", "add_rms_norm", "gated_rms_norm",
+           "causal_conv", "causal_conv_step", "rotary_append", "paged_attention", "copy_pages", "rotary_frequencies"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libreplayssm.so")
 
 RSM_F32, RSM_BF16, RSM_F16, RSM_I8, RSM_FP8_E4M3 = 0, 1, 2, 3, 4
 STATUS_BITS = {"bad_active_index": 1, "bad_ring_start": 2, "bad_prefix_len": 4, "bad_slot": 8,
-               "wait_timeout": 16, "bad_sequence": 32}
+               "wait_timeout": 16, "bad_sequence": 32, "bad_position": 64, "bad_page": 128}
 
 
 class ReplaySSMError(RuntimeError):
@@ -70,7 +73,9 @@ class RsmArgs(ctypes.Structure):
 EXPORTS = ("rsm_materialize", "rsm_last_error", "rsm_args_size", "rsm_abi_version", "rsm_launch_config",
            "rsm_kernel_name", "rsm_gdn_commit", "rsm_gdn_args_size",
            "rsm_ssm_prefill", "rsm_ssm_prefill_workspace", "rsm_ssm_step", "rsm_replayssm_decode",
-           "rsm_add_rms_norm", "rsm_gated_rms_norm", "rsm_block_last_error", "rsm_block_args_size")
+           "rsm_add_rms_norm", "rsm_gated_rms_norm", "rsm_block_last_error", "rsm_block_args_size",
+           "rsm_causal_conv", "rsm_causal_conv_step", "rsm_rotary_append", "rsm_paged_attention",
+           "rsm_paged_attention_workspace", "rsm_copy_pages", "rsm_hybrid_last_error", "rsm_hybrid_args_size")
 
 _lib = None
 
@@ -385,13 +390,17 @@ def gated_delta_rule_replayssm_commit(checkpoint_state, rawv_cache, rawk_cache, 
         raise ReplaySSMError(rc, lib.rsm_last_error().decode())
 
 
-_BLOCK = ("ssm_prefill", "ssm_step", "replayssm_decode", "add_rms_norm", "gated_rms_norm")
+_LATER = {"block": ("ssm_prefill", "ssm_step", "replayssm_decode", "add_rms_norm", "gated_rms_norm"),
+          "hybrid": ("causal_conv", "causal_conv_step", "rotary_append", "paged_attention", "copy_pages",
+                     "rotary_frequencies")}
 
 
 def __getattr__(name):
-    if name in _BLOCK:
-        from . import block
-        for n in _BLOCK:
-            globals()[n] = getattr(block, n)
-        return globals()[name]
+    for module, names in _LATER.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

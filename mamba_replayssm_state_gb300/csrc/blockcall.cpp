@@ -7,17 +7,7 @@
 // type, shape, stride or device than the kernels take as they are, or anything
 // wrong): block.py then goes over them itself and names what is wrong or lets it
 // pass.  So nothing here raises, and nothing is accepted that block.py refuses.
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-
-#include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <c10/core/GradMode.h>
-#include <c10/cuda/CUDAFunctions.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include "../../include/replayssm_block.h"
+#include "callutil.h"
 
 namespace {
 
@@ -31,28 +21,6 @@ struct Abi {
   decltype(&rsm_gated_rms_norm) gated_norm;
 } abi;
 
-using Tensor = at::Tensor;
-
-PyObject* none() { Py_RETURN_NONE; }
-
-// The tensor, or nullptr for anything else.
-const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
-
-// All tensors on the current device, and none wants a gradient (nullptr: not given); its index, or -1.
-template <int N>
-int device_of(const Tensor* const (&ts)[N]) {
-  const int d = c10::cuda::current_device();
-  const bool grad = c10::GradMode::is_enabled();
-  for (const Tensor* t : ts)
-    if (t != nullptr && !(t->is_cuda() && t->get_device() == d && !(grad && t->requires_grad()))) return -1;
-  return d;
-}
-
-int input_code(const Tensor& t) {
-  const auto s = t.scalar_type();
-  return s == at::kBFloat16 ? RSM_BF16 : s == at::kFloat ? RSM_F32 : -1;
-}
-
 int state_code(const Tensor& t) {
   switch (t.scalar_type()) {
     case at::kFloat: return RSM_F32;
@@ -62,28 +30,6 @@ int state_code(const Tensor& t) {
     case at::kFloat8_e4m3fn: return RSM_FP8_E4M3;
     default: return -1;
   }
-}
-
-// contiguous [n] of a type
-bool vector(const Tensor& t, int64_t n, at::ScalarType type) {
-  return t.scalar_type() == type && t.dim() == 1 && t.size(0) == n && (n <= 1 || t.stride(0) == 1);
-}
-
-bool is(const Tensor& t, at::IntArrayRef sizes, at::ScalarType type) {
-  return t.scalar_type() == type && t.sizes() == sizes && t.is_contiguous();
-}
-
-bool fits(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
-
-// a Python integer of 32 bits
-bool int32(PyObject* o, int32_t* v) {
-  const long long n = PyLong_AsLongLong(o);
-  if (PyErr_Occurred()) {
-    PyErr_Clear();
-    return false;
-  }
-  *v = static_cast<int32_t>(n);
-  return *v == n;
 }
 
 // x [lead.., H, dim], dt [lead.., H], A [H], B and C [lead.., G, N], D [H] or
@@ -108,20 +54,6 @@ struct Tokens {
 // a pool [slots, H, dim, N] with contiguous slots, laid out without gaps
 bool pool(const Tensor& t, const Tokens& k) {
   return t.dim() == 4 && t.is_contiguous() && t.size(1) == k.H && t.size(2) == k.dim && t.size(3) == k.N && fits(t.size(0));
-}
-
-void* ptr(const Tensor* t) { return t == nullptr ? nullptr : t->data_ptr(); }
-
-Tensor like(const Tensor& x) { return at::empty(x.sizes(), x.options()); }
-
-template <typename F>
-PyObject* guarded(F f) {
-  try {
-    return f();
-  } catch (...) {  // block.py meets the same, and says so
-    PyErr_Clear();
-    return none();
-  }
 }
 
 // prefill(x, dt, A, B, C, cu_seqlens, state, initial_slots, final_slots, D, pad_slot_id)
@@ -345,7 +277,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(prefill), FAST(step), FAST(decode), FAST(add_norm), FAST(gated_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_blockcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,309 @@
+// hybrid_api.cu -- host side of the operators of hybrid stacks
+// (include/replayssm_hybrid.h): argument validation, choice of kernel, launch.
+// Nothing here reads device memory, allocates or synchronizes.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+
+#include "hybrid_params.h"
+
+namespace {
+
+thread_local char g_error[512];
+
+int fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_error, sizeof g_error, fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int done() {
+  g_error[0] = '\0';
+  return RSM_OK;
+}
+
+struct Named {
+  const void* p;
+  const char* name;
+};
+
+template <int K>
+int need(const Named (&list)[K]) {
+  for (const Named& n : list)
+    if (n.p == nullptr) return fail(RSM_EINVAL, "%s is NULL", n.name);
+  return RSM_OK;
+}
+
+bool is_input(int dt) { return dt == RSM_F32 || dt == RSM_BF16; }
+int input_size(int dt) { return dt == RSM_F32 ? 4 : 2; }
+
+int launch(const void* fn, int64_t grid, int threads, const void* params, void* stream, size_t smem = 0) {
+  if (grid > 0x7FFFFFFFLL) return fail(RSM_EINVAL, "the call needs %lld blocks, more than 2^31-1", static_cast<long long>(grid));
+  void* kargs[] = {const_cast<void*>(params)};
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), kargs, smem,
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+  return done();
+}
+
+// Rows of a tensor start on 16 bytes; a stride that no second row needs is not looked at.
+bool rows_fit(const void* base, int es, int64_t n0, int64_t s0, int64_t n1 = 1, int64_t s1 = 0, int64_t n2 = 1, int64_t s2 = 0) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (n0 <= 1 || s0 * es % 16 == 0) && (n1 <= 1 || s1 * es % 16 == 0) &&
+         (n2 <= 1 || s2 * es % 16 == 0);
+}
+
+// ---------------------------------------------------------------------------
+// convolution
+// ---------------------------------------------------------------------------
+template <typename A>
+int check_conv(const A* a) {
+  if (a->channels <= 0) return fail(RSM_EINVAL, "channels must be positive (got %d)", a->channels);
+  if (a->width < 2 || a->width > 4) return fail(RSM_ENOTSUP, "no kernel compiled for width %d: 2, 3 or 4", a->width);
+  if (!is_input(a->input_dtype)) return fail(RSM_EINVAL, "input_dtype must be BF16 or F32 (got %d)", a->input_dtype);
+  if (a->num_slots < 0) return fail(RSM_EINVAL, "num_slots must be >= 0 (got %d)", a->num_slots);
+  return RSM_OK;
+}
+
+template <typename A>
+hybrid::ConvParams conv_params(const A* a) {
+  hybrid::ConvParams p{};
+  p.x = a->x;
+  p.weight = a->weight;
+  p.bias = a->bias;
+  p.cache = a->cache;
+  p.slots = a->slots;
+  p.positions = a->positions;
+  p.out = a->out;
+  p.status = a->device_status;
+  p.x_ts = a->x_stride;
+  p.cache_ss = a->cache_slot_stride;
+  p.num_slots = a->num_slots;
+  p.C = a->channels;
+  p.R = a->cache_rows;
+  p.silu = a->silu != 0;
+  p.pad = a->pad_slot_id;
+  return p;
+}
+
+// Eight bf16 or four fp32 channels at a time: every row, and the weights', starts on 16 bytes.
+bool conv_vec(const hybrid::ConvParams& p, int dt, int width) {
+  const int es = input_size(dt), v = 16 / es;
+  return p.C % v == 0 && reinterpret_cast<uintptr_t>(p.weight) % 16 == 0 && width * v % 4 == 0 &&
+         rows_fit(p.x, es, p.seqs, p.x_bs, 2, p.x_ts) && rows_fit(p.out, es, 2, p.out_ts) &&
+         (p.cache == nullptr || rows_fit(p.cache, es, 2, p.C, p.num_slots, p.cache_ss));
+}
+
+// ---------------------------------------------------------------------------
+// pages
+// ---------------------------------------------------------------------------
+int check_pages(const rsm_pages& pg, int heads, int kv_heads, int dim, int dt) {
+  if (kv_heads <= 0 || heads <= 0 || heads % kv_heads != 0)
+    return fail(RSM_EINVAL, "num_kv_heads (%d) must divide num_heads (%d)", kv_heads, heads);
+  if (dim <= 0) return fail(RSM_EINVAL, "dim must be positive (got %d)", dim);
+  if (dim > 256) return fail(RSM_ENOTSUP, "no kernel compiled for dim %d: at most 256", dim);
+  if (!is_input(dt)) return fail(RSM_EINVAL, "input_dtype must be BF16 or F32 (got %d)", dt);
+  if (pg.requests < 0) return fail(RSM_EINVAL, "requests must be >= 0 (got %d)", pg.requests);
+  if (pg.page_size < 1) return fail(RSM_EINVAL, "page_size must be >= 1 (got %d)", pg.page_size);
+  if (pg.num_pages < 0 || pg.table_width < 0) return fail(RSM_EINVAL, "num_pages and table_width must be >= 0");
+  return RSM_OK;
+}
+
+int need_pages(const rsm_pages& pg) {
+  const int rc = need({{pg.lengths, "lengths"}});
+  return rc != RSM_OK || pg.table_width == 0 ? rc : need({{pg.k, "k pages"}, {pg.v, "v pages"}, {pg.page_table, "page_table"}});
+}
+
+bool pages_fit(const rsm_pages& pg, int es, int kv_heads) {
+  return rows_fit(pg.k, es, pg.num_pages, pg.k_page_stride, pg.page_size, pg.k_row_stride, kv_heads, pg.k_head_stride) &&
+         rows_fit(pg.v, es, pg.num_pages, pg.v_page_stride, pg.page_size, pg.v_row_stride, kv_heads, pg.v_head_stride);
+}
+
+int validate(const rsm_paged_attention_args* a, bool pointers) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->window < 1) return fail(RSM_EINVAL, "window must be >= 1 (got %d)", a->window);
+  int rc = check_pages(a->pages, a->num_heads, a->num_kv_heads, a->dim, a->input_dtype);
+  if (rc == RSM_OK && pointers && a->pages.requests > 0) {
+    rc = need({{a->q, "q"}, {a->out, "out"}});
+    if (rc == RSM_OK) rc = need_pages(a->pages);
+  }
+  return rc;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rsm_causal_conv(const rsm_causal_conv_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->num_seqs < 0 || a->tokens < 0) return fail(RSM_EINVAL, "num_seqs and tokens must be >= 0");
+  int rc = check_conv(a);
+  if (rc != RSM_OK) return rc;
+  if (a->cache != nullptr && a->cache_rows < a->width - 1)
+    return fail(RSM_EINVAL, "cache_rows (%d) must be at least width - 1 (%d)", a->cache_rows, a->width - 1);
+  if (a->num_seqs == 0 || a->tokens == 0) return done();
+  rc = need({{a->x, "x"}, {a->weight, "weight"}, {a->out, "out"}, {a->cu_seqlens, "cu_seqlens"}});
+  if (rc != RSM_OK) return rc;
+  if ((a->cache == nullptr) != (a->slots == nullptr)) return fail(RSM_EINVAL, "cache and slots go together");
+  if (a->cache == nullptr && a->positions != nullptr) return fail(RSM_EINVAL, "positions need a cache");
+  if (a->out == a->x) return fail(RSM_EINVAL, "out must not be x");
+  hybrid::ConvParams p = conv_params(a);
+  p.cu = a->cu_seqlens;
+  p.tokens = a->tokens;
+  p.out_ts = a->out_stride;
+  p.seqs = a->num_seqs;
+  const bool vec = conv_vec(p, a->input_dtype, a->width);
+  const int per = hybrid::kConvThreads * hybrid::conv_channels(a->input_dtype, vec);
+  p.cblocks = (a->channels + per - 1) / per;
+  const int64_t blocks = (a->tokens + hybrid::kConvTokens - 1) / hybrid::kConvTokens;
+  return launch(hybrid::conv_kernel(a->input_dtype, a->width, vec), blocks * p.cblocks, hybrid::kConvThreads, &p, stream);
+}
+
+int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->batch < 0) return fail(RSM_EINVAL, "batch must be >= 0 (got %d)", a->batch);
+  if (a->window < 1) return fail(RSM_EINVAL, "window must be >= 1 (got %d)", a->window);
+  int rc = check_conv(a);
+  if (rc != RSM_OK) return rc;
+  if (a->cache_rows < static_cast<int64_t>(a->width) - 1 + a->window)
+    return fail(RSM_EINVAL, "cache_rows (%d) must be at least width - 1 + window (%lld)", a->cache_rows,
+                static_cast<long long>(a->width) - 1 + a->window);
+  if (a->batch == 0) return done();
+  rc = need({{a->x, "x"}, {a->weight, "weight"}, {a->out, "out"}, {a->cache, "cache"}, {a->slots, "slots"}, {a->positions, "positions"}});
+  if (rc != RSM_OK) return rc;
+  if (a->out == a->x) return fail(RSM_EINVAL, "out must not be x");
+  hybrid::ConvParams p = conv_params(a);
+  p.x_bs = a->x_batch_stride;
+  if (a->window == 1) p.x_ts = 0;
+  p.out_ts = a->channels;
+  p.seqs = a->batch;
+  p.window = a->window;
+  const bool vec = conv_vec(p, a->input_dtype, a->width);
+  const int per = hybrid::kConvThreads * hybrid::conv_channels(a->input_dtype, vec);
+  p.cblocks = (a->channels + per - 1) / per;
+  const int requests = vec && static_cast<int64_t>(a->batch) * p.cblocks > 1024 ? 2 : 1;
+  const int64_t groups = (a->batch + requests - 1) / requests;
+  return launch(hybrid::conv_step_kernel(a->input_dtype, a->width, vec, requests), groups * p.cblocks, hybrid::kConvThreads, &p,
+                stream);
+}
+
+int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  const bool packed = a->cu_seqlens != nullptr;
+  if (!packed && a->window < 1) return fail(RSM_EINVAL, "window must be >= 1 (got %d)", a->window);
+  if (packed && a->tokens < 0) return fail(RSM_EINVAL, "tokens must be >= 0");
+  int rc = check_pages(a->pages, a->num_heads, a->num_kv_heads, a->dim, a->input_dtype);
+  if (rc != RSM_OK) return rc;
+  if (a->rotary_dim < 0 || a->rotary_dim % 2 != 0 || a->rotary_dim > a->dim)
+    return fail(RSM_EINVAL, "rotary_dim (%d) must be even and at most dim (%d)", a->rotary_dim, a->dim);
+  if (a->pages.requests == 0 || (packed && a->tokens == 0)) return done();
+  rc = need({{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->q_out, "q_out"}});
+  if (rc == RSM_OK && a->rotary_dim > 0) rc = need({{a->inv_freq, "inv_freq"}});
+  if (rc == RSM_OK) rc = need_pages(a->pages);
+  if (rc != RSM_OK) return rc;
+  const int64_t b = packed ? 1 : a->pages.requests, n = packed ? a->tokens : a->window;
+  hybrid::RotaryParams p{};
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.inv_freq = a->inv_freq;
+  p.cu = a->cu_seqlens;
+  p.q_out = a->q_out;
+  p.status = a->device_status;
+  p.pages = a->pages;
+  p.tokens = b * n;
+  p.q_bs = a->q_batch_stride;
+  p.q_ts = a->q_stride;
+  p.k_bs = a->k_batch_stride;
+  p.k_ts = a->k_stride;
+  p.v_bs = a->v_batch_stride;
+  p.v_ts = a->v_stride;
+  p.out_bs = a->out_batch_stride;
+  p.out_ts = a->out_stride;
+  p.window = a->window;
+  p.H = a->num_heads;
+  p.G = a->num_kv_heads;
+  p.dim = a->dim;
+  p.half = a->rotary_dim / 2;
+  p.interleaved = a->interleaved != 0;
+  p.amplitude = a->amplitude;
+  const int es = input_size(a->input_dtype), v = 16 / es;
+  const bool vec = a->dim % v == 0 && (a->interleaved ? a->rotary_dim : p.half) % v == 0 && rows_fit(p.q, es, b, p.q_bs, n, p.q_ts) &&
+                   rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
+                   rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads);
+  p.block_tokens = p.tokens >= 4096 ? 4 : 1;
+  return launch(hybrid::rotary_kernel(a->input_dtype, vec), (p.tokens + p.block_tokens - 1) / p.block_tokens, hybrid::kRotaryThreads, &p,
+                stream);
+}
+
+int64_t rsm_paged_attention_workspace(const rsm_paged_attention_args* a) {
+  const int rc = validate(a, false);
+  if (rc != RSM_OK) return rc;
+  done();
+  return 0;
+}
+
+int rsm_paged_attention(const rsm_paged_attention_args* a, void* stream) {
+  const int rc = validate(a, true);
+  if (rc != RSM_OK) return rc;
+  if (a->pages.requests == 0) return done();
+  hybrid::AttnParams p{};
+  p.q = a->q;
+  p.out = a->out;
+  p.status = a->device_status;
+  p.pages = a->pages;
+  p.q_bs = a->q_batch_stride;
+  p.q_ts = a->q_stride;
+  p.window = a->window;
+  p.H = a->num_heads;
+  p.G = a->num_kv_heads;
+  p.per = a->num_heads / a->num_kv_heads;
+  p.dim = a->dim;
+  p.scale_log2 = a->scale * 1.44269504088896340736f;
+  return launch(hybrid::attn_plain_kernel(a->input_dtype), static_cast<int64_t>(a->pages.requests) * a->window * a->num_heads,
+                hybrid::kAttnPlainThreads, &p, stream);
+}
+
+int rsm_copy_pages(const rsm_copy_pages_args* a, void* stream) {
+  if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
+  if (a->num_pools < 0 || a->num_pairs < 0 || a->num_pages < 0) return fail(RSM_EINVAL, "num_pools, num_pairs and num_pages must be >= 0");
+  if (a->page_elements < 1) return fail(RSM_EINVAL, "page_elements must be >= 1 (got %lld)", static_cast<long long>(a->page_elements));
+  if (a->dtype < RSM_F32 || a->dtype > RSM_FP8_E4M3) return fail(RSM_EINVAL, "unknown dtype %d", a->dtype);
+  if (a->num_pools == 0 || a->num_pairs == 0) return done();
+  const int rc = need({{a->page_ptrs, "page_ptrs"}, {a->page_strides, "page_strides"}, {a->src_pages, "src_pages"}, {a->dst_pages, "dst_pages"}});
+  if (rc != RSM_OK) return rc;
+  hybrid::CopyParams p{};
+  p.ptrs = a->page_ptrs;
+  p.strides = a->page_strides;
+  p.src = a->src_pages;
+  p.dst = a->dst_pages;
+  p.status = a->device_status;
+  p.esize = a->dtype == RSM_F32 ? 4 : a->dtype == RSM_BF16 || a->dtype == RSM_F16 ? 2 : 1;
+  if (a->page_elements > (int64_t{1} << 40)) return fail(RSM_EINVAL, "page_elements must be at most 2^40");
+  p.page_bytes = a->page_elements * p.esize;
+  p.pools = a->num_pools;
+  p.pairs = a->num_pairs;
+  p.pages = a->num_pages;
+  const int64_t pieces = (p.page_bytes + hybrid::kCopyBytes - 1) / hybrid::kCopyBytes;
+  const int64_t units = static_cast<int64_t>(a->num_pools) * a->num_pairs;  // < 2^62; the product below could pass 2^63
+  if (units > 0x7FFFFFFFLL || units * pieces > 0x7FFFFFFFLL) return fail(RSM_EINVAL, "the call needs more than 2^31-1 blocks");
+  return launch(hybrid::copy_kernel(), units * pieces, hybrid::kCopyThreads, &p, stream);
+}
+
+const char* rsm_hybrid_last_error(void) { return g_error; }
+
+int rsm_hybrid_args_size(int index) {
+  switch (index) {
+    case 0: return static_cast<int>(sizeof(rsm_causal_conv_args));
+    case 1: return static_cast<int>(sizeof(rsm_causal_conv_step_args));
+    case 2: return static_cast<int>(sizeof(rsm_rotary_append_args));
+    case 3: return static_cast<int>(sizeof(rsm_paged_attention_args));
+    case 4: return static_cast<int>(sizeof(rsm_copy_pages_args));
+    default: return 0;
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,76 @@
+// hybrid_params.h -- what the convolution, rotary, attention and page kernels are given.
+#pragma once
+#include <cstdint>
+
+#include "../../include/replayssm_hybrid.h"
+
+namespace hybrid {
+
+struct ConvParams {
+  const void* x;
+  const float *weight, *bias;
+  const int32_t* cu;  // packed prompts
+  void* cache;
+  const int32_t *slots, *positions;
+  void* out;
+  uint32_t* status;
+  int64_t tokens, x_bs, x_ts, out_ts, cache_ss;
+  int32_t seqs, window, num_slots, C, R, silu, pad;
+  int32_t cblocks;  // CTAs across the channels
+};
+
+constexpr int kConvThreads = 128;
+constexpr int kConvTokens = 32;  // tokens of a CTA of the prompts' kernel
+
+// vec: eight bf16 or four fp32 channels a thread, on 16 bytes; else one channel.
+const void* conv_kernel(int input_dtype, int width, bool vec);
+// requests: of a thread, 1 or 2
+const void* conv_step_kernel(int input_dtype, int width, bool vec, int requests);
+constexpr int conv_channels(int input_dtype, bool vec) { return !vec ? 1 : input_dtype == RSM_BF16 ? 8 : 4; }
+
+struct RotaryParams {
+  const void *q, *k, *v;
+  const float* inv_freq;
+  const int32_t* cu;
+  void* q_out;
+  uint32_t* status;
+  rsm_pages pages;
+  int64_t tokens, q_bs, q_ts, k_bs, k_ts, v_bs, v_ts, out_bs, out_ts;
+  int32_t window, H, G, dim, half, interleaved;  // half: rotary_dim / 2
+  float amplitude;
+  int32_t block_tokens;  // tokens of a CTA
+};
+
+constexpr int kRotaryThreads = 256;
+const void* rotary_kernel(int input_dtype, bool vec);
+
+struct AttnParams {
+  const void* q;
+  void* out;
+  uint32_t* status;
+  rsm_pages pages;
+  int64_t q_bs, q_ts;
+  int32_t window, H, G, per, dim;  // per: heads of a key head
+  float scale_log2;                // scale * log2(e)
+  // the tiled kernel
+  float* part;                     // partial outputs, then their maxima and sums
+  int32_t row_tiles, ctas, page_shift;  // page_shift: log2(page_size), or -1
+  int32_t q_pairs;                 // queries may be read two at a time
+};
+
+constexpr int kAttnPlainThreads = 128;
+const void* attn_plain_kernel(int input_dtype);
+
+struct CopyParams {
+  const int64_t *ptrs, *strides;
+  const int32_t *src, *dst;
+  uint32_t* status;
+  int64_t page_bytes;
+  int32_t pools, pairs, pages, esize;
+};
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyBytes = 16384;  // of a CTA
+const void* copy_kernel();
+
+}  // namespace hybrid

@@ -1,0 +1,172 @@
+// rotary_kernel.cuh -- rotary positions on the queries and keys of new tokens, keys
+// and values to their pages.
+//
+// The angle p f of a far position has to be taken modulo a turn before it is rounded
+// to 24 bits.  Here the fraction of a turn that one position makes, f / (2 pi) mod 1,
+// is a 64-bit integer (in units of 2^-64 turns, from two-term fp64 products), so that
+// times the position it wraps by itself: the error, a unit a position, stays below
+// 2^-32 turns, and the upper 32 bits are what sine and cosine are taken of.
+//
+// Memory bounds it: q, k, v read once and written once.  A CTA takes a few tokens,
+// makes their sines and cosines once for all heads, and then moves 16 bytes (twice
+// that for two halves of a head) a thread at a time.
+#pragma once
+#include "hybrid_device.cuh"
+
+namespace hybrid {
+
+constexpr int kRotaryMaxTokens = 8, kRotaryMaxHalf = 128;
+
+struct RotaryToken {
+  int64_t q, k, v, out;   // element offsets of the token's rows
+  int64_t k_row, v_row;   // of its rows in the pages; -1: none
+  uint32_t pos;
+  int live;               // 0: no sequence's, 1: a skipped request's, 2: to be done
+};
+
+// f / (2 pi) mod 1 in units of 2^-64.  1 / (2 pi) is given to 106 bits, as the sum of two doubles.
+__device__ __forceinline__ uint64_t turns_per_position(float f) {
+  constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  const double d = fabs(static_cast<double>(f)), t = d * hi, e = fma(d, hi, -t) + d * lo;
+  const double part = t - floor(t);  // exact: part has no bits that t has not
+  const uint64_t n = __double2ull_rz(part * 0x1p64) + static_cast<uint64_t>(__double2ll_rn(e * 0x1p64));
+  return f < 0.0f ? 0 - n : n;
+}
+
+template <typename IT, int V>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
+  __shared__ RotaryToken token[kRotaryMaxTokens];
+  __shared__ uint64_t step[kRotaryMaxHalf];
+  __shared__ float2 turn[kRotaryMaxTokens * kRotaryMaxHalf];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.block_tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.block_tokens), p.tokens - first));
+  const rsm_pages& pg = p.pages;
+  int live = 0;
+  if (p.cu != nullptr) live = live_sequences(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
+  for (int j = threadIdx.x; j < p.half; j += kRotaryThreads) step[j] = turns_per_position(p.inv_freq[j]);
+  if (static_cast<int>(threadIdx.x) < nt) {
+    RotaryToken k;
+    const int64_t i = first + threadIdx.x;
+    int64_t b, t, n;
+    k.live = 1;
+    if (p.cu != nullptr) {
+      b = sequence_at(p.cu, live, i);
+      t = n = 0;
+      if (b == live || p.cu[b] < 0 || p.cu[b] > i || p.cu[b + 1] > p.tokens)
+        k.live = 0;
+      else
+        t = i - p.cu[b], n = p.cu[b + 1] - p.cu[b];
+      k.q = i * p.q_ts, k.k = i * p.k_ts, k.v = i * p.v_ts, k.out = i * p.out_ts;
+    } else {
+      b = i / p.window, t = i - b * p.window, n = p.window;
+      k.q = b * p.q_bs + t * p.q_ts, k.k = b * p.k_bs + t * p.k_ts, k.v = b * p.v_bs + t * p.v_ts;
+      k.out = b * p.out_bs + t * p.out_ts;
+    }
+    k.pos = 0;
+    k.k_row = k.v_row = -1;
+    if (k.live != 0) {
+      const int64_t len = pg.lengths[b];
+      if (len < n || len > static_cast<int64_t>(pg.table_width) * pg.page_size) {
+        if (len != 0) flag(p.status, RSM_STATUS_BAD_POSITION);
+      } else {
+        k.live = 2;
+        k.pos = static_cast<uint32_t>(len - n + t);
+        const uint32_t at = k.pos / static_cast<uint32_t>(pg.page_size);
+        const int64_t row = k.pos - at * static_cast<uint32_t>(pg.page_size);
+        const int page = pg.page_table[b * pg.table_stride + at];
+        if (page < 0 || page >= pg.num_pages)
+          flag(p.status, RSM_STATUS_BAD_PAGE);
+        else
+          k.k_row = page * pg.k_page_stride + row * pg.k_row_stride, k.v_row = page * pg.v_page_stride + row * pg.v_row_stride;
+      }
+    }
+    token[threadIdx.x] = k;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * p.half; i += kRotaryThreads) {
+    const int t = i / p.half, j = i - t * p.half;
+    const int32_t upper = static_cast<int32_t>(static_cast<uint32_t>((token[t].pos * step[j]) >> 32));
+    float s, c;
+    sincospif(static_cast<float>(upper) * 0x1p-31f, &s, &c);
+    turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
+  }
+  __syncthreads();
+
+  // A head's parts: those that turn (V pairs from two halves, or V / 2 neighbouring
+  // ones), then those that are copied; a value head is copied whole.
+  const bool near = V > 1 && p.interleaved;
+  const uint32_t turning = V > 1 ? (near ? 2 * p.half / V : p.half / V) : p.half;
+  const uint32_t parts = turning + (p.dim - 2 * p.half) / V, copied = p.dim / V;
+  const uint32_t heads = (p.H + p.G) * parts, per = heads + p.G * copied;
+  for (uint32_t i = threadIdx.x; i < nt * per; i += kRotaryThreads) {
+    const uint32_t t = i / per;
+    uint32_t r = i - t * per;
+    const RotaryToken& k = token[t];
+    if (k.live == 0) continue;
+    if (r >= heads) {
+      r -= heads;
+      if (k.v_row < 0) continue;
+      const uint32_t g = r / copied, part = r - g * copied;
+      Row<IT, V> row;
+      row.load(static_cast<const IT*>(p.v) + k.v + static_cast<int64_t>(g) * p.dim + part * V);
+      row.store(static_cast<IT*>(pg.v) + k.v_row + g * pg.v_head_stride + part * V);
+      continue;
+    }
+    const uint32_t h = r / parts, part = r - h * parts;
+    const bool key = h >= static_cast<uint32_t>(p.H);
+    if (key && k.k_row < 0) continue;
+    const IT* from = key ? static_cast<const IT*>(p.k) + k.k + static_cast<int64_t>(h - p.H) * p.dim
+                         : static_cast<const IT*>(p.q) + k.q + static_cast<int64_t>(h) * p.dim;
+    IT* to = key ? static_cast<IT*>(pg.k) + k.k_row + (h - p.H) * pg.k_head_stride
+                 : static_cast<IT*>(p.q_out) + k.out + static_cast<int64_t>(h) * p.dim;
+    const float2* cs = turn + t * p.half;
+    Row<IT, V> a, b;
+    if (k.live == 1) {  // a skipped request's queries
+      a.zero();
+      if (part >= turning) {
+        a.store(to + 2 * p.half + (part - turning) * V);
+      } else if (near) {
+        a.store(to + part * V);
+      } else {
+        const uint32_t ca = V == 1 && p.interleaved ? 2 * part : part * V;
+        a.store(to + ca);
+        a.store(to + (V == 1 && p.interleaved ? ca + 1 : ca + p.half));
+      }
+    } else if (part >= turning) {
+      a.load(from + 2 * p.half + (part - turning) * V);
+      a.store(to + 2 * p.half + (part - turning) * V);
+    } else if (near) {
+      float x[V], y[V];
+      a.load(from + part * V);
+      a.values(x);
+#pragma unroll
+      for (int j = 0; j + 1 < V; j += 2) {
+        const float2 w = cs[part * (V / 2) + j / 2];
+        y[j] = x[j] * w.x - x[j + 1] * w.y;
+        y[j + 1] = x[j + 1] * w.x + x[j] * w.y;
+      }
+      a.round(y);
+      a.store(to + part * V);
+    } else {
+      const uint32_t ca = V == 1 && p.interleaved ? 2 * part : part * V;
+      const uint32_t cb = V == 1 && p.interleaved ? ca + 1 : ca + p.half;
+      float x[V], y[V], u[V], v[V];
+      a.load(from + ca);
+      b.load(from + cb);
+      a.values(x);
+      b.values(y);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 w = cs[part * V + j];
+        u[j] = x[j] * w.x - y[j] * w.y;
+        v[j] = y[j] * w.x + x[j] * w.y;
+      }
+      a.round(u);
+      b.round(v);
+      a.store(to + ca);
+      b.store(to + cb);
+    }
+  }
+}
+
+}  // namespace hybrid
