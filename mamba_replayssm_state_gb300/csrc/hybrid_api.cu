@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "hybrid_params.h"
 
@@ -133,6 +134,100 @@ int validate(const rsm_paged_attention_args* a, bool pointers) {
   return rc;
 }
 
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_sms[kMaxDevices];
+bool g_attn_ready[kMaxDevices][2][3][2];  // input type, dim 64, 128, 256, groups of rows
+
+int device_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (*dev < 0 || *dev >= kMaxDevices) return fail(RSM_ECUDA, "device ordinal %d out of range", *dev);
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_sms[*dev] == 0) {
+    e = cudaDeviceGetAttribute(&g_sms[*dev], cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) return fail(RSM_ECUDA, "device query failed: %s", cudaGetErrorString(e));
+  }
+  *sms = g_sms[*dev];
+  return RSM_OK;
+}
+
+// How a call runs on the tiled kernel.
+struct AttnPlan {
+  int groups;     // of 16 rows a unit; 0: the plain kernel
+  int row_tiles;  // units of a key head
+  int ctas;
+  int64_t units;
+  bool split;     // units may have more than one tile, so the join has to run
+  int64_t bytes;  // of workspace
+};
+
+// The tiled kernel is for dims of 64, 128 and 256 (fp32: 64 and 128).  A unit has 16 rows or
+// 32: more than 32 are several units, which read the same keys and values (from the L2).
+AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
+  AttnPlan pl{};
+  const int64_t rows = static_cast<int64_t>(a->num_heads / a->num_kv_heads) * a->window;
+  int groups = rows > 16 && hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, 2) != nullptr ? 2 : 1;
+  if (hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, groups) == nullptr) return pl;
+  const int64_t tiles = (rows + 16 * groups - 1) / (16 * groups);
+  if (rows > 0x7FFFFFF0LL || tiles * a->num_kv_heads > 0x7FFFFFFFLL) return pl;
+  pl.groups = groups;
+  pl.row_tiles = static_cast<int>(tiles);
+  pl.units = tiles * a->num_kv_heads * a->pages.requests;
+  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size;
+  const int64_t most = (longest + hybrid::kAttnTile - 1) / hybrid::kAttnTile;
+  pl.split = most > 1;
+  const int64_t resident = static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(input_size(a->input_dtype), a->dim);
+  pl.ctas = static_cast<int>(std::max<int64_t>(1, std::min(resident, most > resident ? resident : pl.units * std::max<int64_t>(most, 1))));
+  if (pl.split) pl.bytes = 2LL * pl.ctas * 16 * groups * (a->dim + 2) * 4;
+  return pl;
+}
+
+int launch_tiles(const rsm_paged_attention_args* a, hybrid::AttnParams& p, const AttnPlan& pl, int dev, void* stream) {
+  if (pl.split && (a->workspace == nullptr || a->workspace_bytes < pl.bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
+    return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(pl.bytes));
+  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, a->dim);
+  p.part = static_cast<float*>(a->workspace);
+  p.row_tiles = pl.row_tiles;
+  p.ctas = pl.ctas;
+  p.page_shift = -1;
+  for (int k = 0; k < 31; ++k)
+    if (a->pages.page_size == 1 << k) p.page_shift = k;
+  p.q_pairs = reinterpret_cast<uintptr_t>(a->q) % 4 == 0 && (a->pages.requests == 1 || a->q_batch_stride % 2 == 0) &&
+              (a->window == 1 || a->q_stride % 2 == 0);
+  const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, pl.groups);
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    bool& ready = g_attn_ready[dev][a->input_dtype == RSM_F32][a->dim / 128][pl.groups - 1];
+    if (!ready) {
+      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      ready = true;
+    }
+  }
+  const int rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &p, stream, smem);
+  if (rc != RSM_OK || !pl.split) return rc;
+  // The join's CTAs come while the first kernel's finish, and wait for it.  A CTA of the first
+  // has one unit's first piece at most; where few units are in many pieces, their rows are
+  // shared out.
+  const int64_t pieces = pl.ctas / std::max<int64_t>(pl.units, 1) + 1;
+  const int rows = static_cast<int>(std::min<int64_t>(16 * pl.groups, static_cast<int64_t>(p.per) * p.window));
+  int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, pieces / 2)));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.ctas * parts));
+  cfg.blockDim = dim3(hybrid::kAttnJoinThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* kargs[] = {&p, &parts};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, hybrid::attn_join_kernel_of(a->input_dtype, a->dim, pl.groups), kargs);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+  return done();
+}
+
 }  // namespace
 
 extern "C" {
@@ -240,14 +335,21 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
 }
 
 int64_t rsm_paged_attention_workspace(const rsm_paged_attention_args* a) {
-  const int rc = validate(a, false);
+  int rc = validate(a, false);
   if (rc != RSM_OK) return rc;
+  int64_t bytes = 0;
+  if (a->pages.requests > 0) {
+    int dev = 0, sms = 0;
+    rc = device_sms(&dev, &sms);
+    if (rc != RSM_OK) return rc;
+    bytes = plan_attention(a, sms).bytes;
+  }
   done();
-  return 0;
+  return bytes;
 }
 
 int rsm_paged_attention(const rsm_paged_attention_args* a, void* stream) {
-  const int rc = validate(a, true);
+  int rc = validate(a, true);
   if (rc != RSM_OK) return rc;
   if (a->pages.requests == 0) return done();
   hybrid::AttnParams p{};
@@ -263,6 +365,13 @@ int rsm_paged_attention(const rsm_paged_attention_args* a, void* stream) {
   p.per = a->num_heads / a->num_kv_heads;
   p.dim = a->dim;
   p.scale_log2 = a->scale * 1.44269504088896340736f;
+  if (pages_fit(a->pages, input_size(a->input_dtype), a->num_kv_heads)) {
+    int dev = 0, sms = 0;
+    rc = device_sms(&dev, &sms);
+    if (rc != RSM_OK) return rc;
+    const AttnPlan pl = plan_attention(a, sms);
+    if (pl.groups > 0) return launch_tiles(a, p, pl, dev, stream);
+  }
   return launch(hybrid::attn_plain_kernel(a->input_dtype), static_cast<int64_t>(a->pages.requests) * a->window * a->num_heads,
                 hybrid::kAttnPlainThreads, &p, stream);
 }

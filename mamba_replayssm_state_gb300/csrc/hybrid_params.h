@@ -58,6 +58,18 @@ struct AttnParams {
   int32_t q_pairs;                 // queries may be read two at a time
 };
 
+// The tiled kernel: a warp takes kAttnStep tokens at a time, a CTA's four warps kAttnTile; `stages`
+// of them are on the way at once, 96 KB a CTA where two of them share an SM.
+constexpr int kAttnThreads = 128, kAttnStep = 16, kAttnTile = 64, kAttnJoinThreads = 256;
+constexpr int attn_stages(int esize, int dim) { return esize * dim <= 128 ? 6 : 3; }
+constexpr int attn_smem(int esize, int dim) {
+  return attn_stages(esize, dim) * kAttnTile * 2 * dim * esize + (esize == 4 ? 128 * dim : 0);
+}
+constexpr int attn_ctas_per_sm(int esize, int dim) { return attn_smem(esize, dim) > 112 * 1024 ? 1 : 2; }
+// dim 64 and 128, and 256 for bf16; groups of 16 rows, 1 or (bf16, dim up to 128) 2: null otherwise.
+const void* attn_tile_kernel_of(int input_dtype, int dim, int groups);
+const void* attn_join_kernel_of(int input_dtype, int dim, int groups);
+
 constexpr int kAttnPlainThreads = 128;
 const void* attn_plain_kernel(int input_dtype);
 
