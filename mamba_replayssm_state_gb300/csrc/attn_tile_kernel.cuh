@@ -4,88 +4,115 @@
 // of one matrix Q: S = Q K^T, P = 2^(scale S - m), O = P V, with a running maximum m
 // and sum l a row, so the cache is gone through once.
 //
-// Memory bounds it: 16 rows of 128 columns make 16 multiplications of a byte of keys and
+// Memory bounds it: 8 rows of 128 columns make 8 multiplications of a byte of keys and
 // values.  So the cache is what is organised.  A CTA has four warps, and
-// each streams 16 tokens at a time through shared memory of its own (cp.async, S
-// stages ahead): no barrier holds a load back, and warps are joined only at the end of
-// a request's part.  The products are m16n8k16 (bf16) or m16n8k8 (tf32) instructions on
-// registers: with 16 or 32 rows a 128-row tcgen05 tile would be mostly empty.
+// each streams 16 tokens at a time through shared memory of its own, S stages ahead
+// (boxes of 16 rows by TMA where pages are whole groups of 16 tokens, else cp.async):
+// no barrier of the CTA holds a load back, and warps are joined only at the end of
+// a request's part.  The running maximum is one only to within 2^8: sums and outputs are
+// scaled anew where a score passes it by more, which takes a few steps of a request
+// instead of most.
 //
-// The work of a call is its (request, key head, 16 or 32 rows) units' tiles of 64 tokens,
-// one after the other; every CTA takes the same number of them, wherever they begin and
-// end, so that lengths (which only the device knows) may differ as they like.  A unit that
-// a CTA has to itself is finished by it; pieces of others go to the workspace, two a CTA at
-// most, and attn_join_kernel puts them together.
+// The products are m16n8k16 (bf16) and m16n8k8 (tf32) instructions on registers: with a
+// few rows a 128-row tcgen05 tile would be mostly empty.  bf16 takes the products the other
+// way round, S^T = K Q^T and O^T = V^T P^T, so that rows come in eights, and turns P^T
+// between them with movmatrix.
+//
+// The work of a call is its (request, key head, group of rows) units' tiles of 64 tokens,
+// one after the other, and with each unit kAttnUnit tiles more for what its end takes; every CTA
+// takes the same number of them, wherever they begin and end, so that lengths (which only
+// the device knows) may differ as they like.  A unit that a CTA has to itself is finished
+// by it; pieces of others go to the workspace, two a CTA at most, and attn_join_kernel puts
+// them together.
 #pragma once
+#include <type_traits>
+
 #include "attn_plain_kernel.cuh"
 #include "rsm_ptx.cuh"
 
 namespace hybrid {
 
-// How the calls' tiles are dealt out: the same in both kernels.
+__device__ __forceinline__ int tiles_of(int64_t len) { return static_cast<int>((len + kAttnTile - 1) / kAttnTile); }
+
+// What a unit of that many tiles counts.
+__device__ __forceinline__ int64_t counts(int tiles) { return tiles == 0 ? 0 : tiles + kAttnUnit; }
+
+// How a call's tiles are dealt out: the same in both kernels.
 struct AttnDeal {
-  int64_t total;  // tiles
+  int64_t total;  // tiles, the units' ends among them
   int64_t ctas;   // that have any
   __device__ __forceinline__ int64_t begin(int64_t c) const { return c * total / ctas; }
   __device__ __forceinline__ int64_t owner(int64_t tile) const { return ((tile + 1) * ctas - 1) / total; }
 };
 
-__device__ __forceinline__ int tiles_of(int64_t len) { return static_cast<int>((len + kAttnTile - 1) / kAttnTile); }
-
-// All tiles of the call; by the whole CTA.
-template <int THREADS>
-__device__ __forceinline__ int64_t deal_total(const AttnParams& p, bool report) {
-  __shared__ int64_t sums[THREADS / 32];
-  int64_t n = 0;
-  for (int b = threadIdx.x; b < p.pages.requests; b += THREADS) n += tiles_of(request_tokens(p.pages, b, p.window, p.status, report));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = n;
-  __syncthreads();
-  n = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) n += sums[i];
-  return n * (p.G * p.row_tiles);
-}
-
 struct Place {
-  int b;          // request
+  int b;          // a request
   int64_t first;  // its first tile
 };
 
-// The request that has tile number `tile`; by the whole CTA.
+// The requests' tiles, in order; every function by the whole CTA.
 template <int THREADS>
-__device__ __forceinline__ Place deal_find(const AttnParams& p, int64_t tile) {
-  __shared__ int64_t sums[THREADS / 32];
-  __shared__ Place place;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t before = 0;
-  for (int base = 0;; base += THREADS) {
-    const int b = base + static_cast<int>(threadIdx.x);
-    const int64_t own = b < p.pages.requests
-                            ? static_cast<int64_t>(tiles_of(request_tokens(p.pages, b, p.window, nullptr, false))) * (p.G * p.row_tiles)
-                            : 0;
-    int64_t upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    int64_t all = before;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < warp) upto += sums[i];
-      all += sums[i];
-    }
-    upto += before;
-    if (tile < upto && tile >= upto - own) place = Place{b, upto - own};
-    __syncthreads();
-    if (tile < all || base + THREADS >= p.pages.requests) return place;
-    before = all;
+struct Deal {
+  int64_t own, total;  // own: of request threadIdx.x
+  __device__ __forceinline__ static int64_t of(const AttnParams& p, int b, bool report) {
+    if (b >= p.pages.requests) return 0;
+    return counts(tiles_of(request_tokens(p.pages, b, p.window, p.status, report))) * (p.G * p.row_tiles);
   }
-}
+  __device__ __forceinline__ static int64_t sum(int64_t n) {
+    __shared__ int64_t sums[THREADS / 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) n += sums[i];
+    return n;
+  }
+  __device__ __forceinline__ Deal(const AttnParams& p, bool report) {
+    own = of(p, threadIdx.x, report);
+    int64_t n = own;
+    for (int b = threadIdx.x + THREADS; b < p.pages.requests; b += THREADS) n += of(p, b, report);
+    total = sum(n);
+  }
+  // Tiles of the requests before b.
+  __device__ __forceinline__ int64_t before(const AttnParams& p, int b) const {
+    int64_t n = static_cast<int>(threadIdx.x) < b ? own : 0;
+    for (int i = threadIdx.x + THREADS; i < b; i += THREADS) n += of(p, i, false);
+    return sum(n);
+  }
+  // The request that has tile number `tile` (below the total).
+  __device__ __forceinline__ Place find(const AttnParams& p, int64_t tile) const {
+    __shared__ int64_t sums[THREADS / 32];
+    __shared__ Place place;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t before = 0;
+    for (int base = 0;; base += THREADS) {
+      const int b = base + static_cast<int>(threadIdx.x);
+      const int64_t n = base == 0 ? own : of(p, b, false);
+      int64_t upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      int64_t all = before;
+#pragma unroll
+      for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) upto += sums[i];
+        all += sums[i];
+      }
+      upto += before;
+      if (tile < upto && tile >= upto - n) place = Place{b, upto - n};
+      __syncthreads();
+      if (tile < all || base + THREADS >= p.pages.requests) return place;
+      before = all;
+    }
+  }
+};
 
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool yes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(yes ? 16 : 0) : "memory");
@@ -94,6 +121,17 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The box of 16 tokens and 128 bytes at (column, head, row, page).
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int column, int head, int row, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(column), "r"(head), "r"(row), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
@@ -116,6 +154,12 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Lane 4 i + j's values (i, 2 j) and (i, 2 j + 1) of an 8 x 8 matrix become (2 j, i) and (2 j + 1, i).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ uint32_t to_tf32(float v) {
   uint32_t r;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
@@ -132,463 +176,628 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
-// A row's 16-byte chunks are stored in an order of its own, so that what the lanes of
-// an instruction read lies in different banks.
+// Where a 16-byte chunk of a token's row lies: boxes of 16 rows of 128 bytes, the chunks
+// of a row in an order of its own (the boxes' 128-byte swizzle; keys of fp32 another), so
+// that what the lanes of an instruction read lies in different banks.
 template <typename IT>
-__device__ __forceinline__ int key_order(int token) {
-  return sizeof(IT) == 2 ? token & 7 : (token & 1) << 2 | (token >> 1 & 3);
+__device__ __forceinline__ int key_chunk(int token, int chunk) {
+  const int order = sizeof(IT) == 2 ? token & 7 : (token & 1) << 2 | (token >> 1 & 3);
+  return (chunk >> 3) * (kAttnStep * 128) + token * 128 + ((chunk & 7) ^ order) * 16;
 }
-__device__ __forceinline__ int value_order(int token) { return token & 7; }
+__device__ __forceinline__ int value_chunk(int token, int chunk) {
+  return (chunk >> 3) * (kAttnStep * 128) + token * 128 + ((chunk & 7) ^ (token & 7)) * 16;
+}
+
+constexpr float kAttnSlack = 8.0f;
+constexpr uint64_t kAttnTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
 
 template <typename IT, int DIM>
 struct AttnShape {
   static constexpr int kChunks = DIM * static_cast<int>(sizeof(IT)) / 16;  // of a row
-  static constexpr int kRow = DIM * static_cast<int>(sizeof(IT));
-  static constexpr int kHalf = kAttnStep * kRow;                           // a warp's keys of a stage
+  static constexpr int kHalf = kAttnStep * DIM * static_cast<int>(sizeof(IT));  // a warp's keys of a stage
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = attn_stages(sizeof(IT), DIM);
   static constexpr int kQuery = sizeof(IT) == 4 ? 2 * 16 * DIM * 4 : 0;    // fp32: Q's parts as the products take them
 };
 
-// Where a unit's tiles are, as one walks along them.
+// A place among the tiles, as one walks along them: request, key head, rows, tile.
 struct AttnCursor {
-  int b, u, tile, tiles, len;
+  int b, g, rt, tile, tiles, len;
   __device__ __forceinline__ void at_request(const AttnParams& p) {
     len = static_cast<int>(request_tokens(p.pages, b, p.window, nullptr, false));
     tiles = tiles_of(len);
   }
-  __device__ __forceinline__ void next(const AttnParams& p, int units) {
-    if (++tile < tiles) return;
+  __device__ __forceinline__ void next_unit(const AttnParams& p) {
     tile = 0;
-    if (++u < units) return;
-    u = 0;
+    if (++rt < p.row_tiles) return;
+    rt = 0;
+    if (++g < p.G) return;
+    g = 0;
     do {
       if (++b >= p.pages.requests) return;
       at_request(p);
     } while (len == 0);
   }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    if (++tile == tiles) next_unit(p);
+  }
+  // Row r of the unit: its queries (null: there is none) and the last token that it sees.
+  template <typename IT, int DIM>
+  __device__ __forceinline__ const IT* query(const AttnParams& p, int rows, int row, int& last) const {
+    const int r = rt * rows + row, t = r / p.per;
+    last = len - p.window + t;
+    if (r >= p.per * p.window) return nullptr;
+    return static_cast<const IT*>(p.q) + b * p.q_bs + t * p.q_ts + static_cast<int64_t>(g * p.per + r - t * p.per) * DIM;
+  }
 };
 
-template <typename IT, int DIM, int M>
-__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(IT), DIM)) attn_tile_kernel(const __grid_constant__ AttnParams p) {
+// What a warp has seen of a step: 16 tokens at token0, those of the bits `seen`.
+struct AttnStep {
+  uint32_t keys, values;  // shared memory
+  char* held;             // the values, to change them
+  uint32_t seen;
+  int token0;
+  bool differ;            // rows differ in what they see
+  int first_new;          // of the 16, the first that is not seen by all rows
+};
+
+// New tokens' values that are not finite go to the rows that see them, by add(token), and not
+// into the product, where a weight of zero would not keep them from the others.
+template <typename IT, int DIM, typename F>
+__device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
+  constexpr int kChunks = AttnShape<IT, DIM>::kChunks;
+  bool odd = false;
+  for (int c = lane; c < kAttnStep * kChunks; c += 32) {
+    if ((c >> 3) % kAttnStep < a.first_new) continue;
+    const uint4 v = rsm::lds128(a.values + c * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      odd |= (w[k] & 0x7F800000u) == 0x7F800000u;
+      if (sizeof(IT) == 2) odd |= (w[k] & 0x7F80u) == 0x7F80u;
+    }
+  }
+  if (!__any_sync(0xFFFFFFFFu, odd)) return;
+  for (int j = a.first_new; j < kAttnStep; ++j)
+    if (a.seen >> j & 1u) add(j);
+  __syncwarp();
+  for (int c = lane; c < kAttnStep * kChunks; c += 32) {
+    if ((c >> 3) % kAttnStep < a.first_new) continue;
+    IT* v = reinterpret_cast<IT*>(a.held + c * 16);
+#pragma unroll
+    for (int k = 0; k < 16 / static_cast<int>(sizeof(IT)); ++k)
+      if (!isfinite(get(v + k))) v[k] = IT(0);
+  }
+  rsm::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <typename IT>
+__device__ __forceinline__ float held_value(const AttnStep& a, int token, int column) {
+  const int c = column * static_cast<int>(sizeof(IT));
+  return get(reinterpret_cast<const IT*>(a.held + value_chunk(token, c / 16) + c % 16));
+}
+
+// A warp's part of a unit, bf16: 8 N rows.  Lane (quad, four) holds of S^T tokens quad and quad
+// + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.
+template <int DIM, int N>
+struct AttnBf16 {
+  using IT = uint16_t;
+  static constexpr int kRows = 8 * N, kSteps = DIM / 16;
+  static constexpr int kChains = N == 1 ? 4 : N == 2 ? 2 : 1;  // sums that do not wait for one another
+  uint32_t q[N][kSteps][2];
+  int limit[N][2];
+  float o[kSteps][N][4], m[N][2], l[N][2];
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+  }
+  __device__ __forceinline__ void queries(const AttnParams& p, const AttnCursor& at, int lane, char*) {
+    const int quad = lane >> 2, four = lane & 3;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      int last;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) (void)at.query<IT, DIM>(p, kRows, 8 * n + 2 * four + e, limit[n][e]);
+      const IT* from = at.query<IT, DIM>(p, kRows, 8 * n + quad, last);
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t v = 0;
+          if (from != nullptr) {
+            const IT* s = from + 16 * ks + 8 * e + 2 * four;
+            v = p.q_pairs ? *reinterpret_cast<const uint32_t*>(s) : static_cast<uint32_t>(s[0]) | static_cast<uint32_t>(s[1]) << 16;
+          }
+          q[n][ks][e] = v;
+        }
+    }
+  }
+  __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, int lane, const char*) {
+    const int quad = lane >> 2, four = lane & 3;
+    float part[kChains][N][4], s[N][4];
+#pragma unroll
+    for (int c = 0; c < kChains; ++c)
+#pragma unroll
+      for (int n = 0; n < N; ++n) part[c][n][0] = part[c][n][1] = part[c][n][2] = part[c][n][3] = 0.0f;
+    {
+      const int token = lane & 15, odd = lane >> 4;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        uint32_t ka[4];
+        ldmatrix4(ka, a.keys + key_chunk<IT>(token, 2 * ks + odd));
+#pragma unroll
+        for (int n = 0; n < N; ++n) mma_bf16(part[ks % kChains][n], ka, q[n][ks][0], q[n][ks][1]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = part[0][n][e];
+#pragma unroll
+        for (int c = 1; c < kChains; ++c) v += part[c][n][e];
+        s[n][e] = v * p.scale_log2;
+      }
+    if (a.differ || a.seen != (1u << kAttnStep) - 1u) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = quad + 8 * (e >> 1);
+          if (!(a.seen >> j & 1u) || a.token0 + j > limit[n][e & 1]) s[n][e] = -INFINITY;
+        }
+    }
+    bool moved = false;
+    float keep[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = fmaxf(s[n][e], s[n][e + 2]);
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        const float next = top > m[n][e] + kAttnSlack ? top : m[n][e], base = next == -INFINITY ? 0.0f : next;
+        keep[n][e] = exp2_fast(m[n][e] - base);
+        moved |= next != m[n][e];
+        m[n][e] = next;
+        s[n][e] = exp2_fast(s[n][e] - base);
+        s[n][e + 2] = exp2_fast(s[n][e + 2] - base);
+        l[n][e] = fmaf(l[n][e], keep[n][e], s[n][e] + s[n][e + 2]);
+      }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][n][e] *= keep[n][e & 1];
+    }
+    if (a.differ && p.window > 1)
+      odd_values<IT, DIM>(a, lane, [&](int j) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w = __shfl_sync(0xFFFFFFFFu, j & 8 ? s[n][e + 2] : s[n][e], (j & 7) * 4 + four);
+            if (a.token0 + j > limit[n][e]) continue;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float v = held_value<IT>(a, j, 16 * i + 8 * h + quad);
+                if (!isfinite(v)) o[i][n][2 * h + e] += w * v;
+              }
+          }
+      });
+    uint32_t pb[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pb[n][h] = transpose8(rsm::pack_bf16x2(s[n][2 * h], s[n][2 * h + 1]));
+    const int token = (lane >> 4) * 8 + (lane & 7), odd = lane >> 3 & 1;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      uint32_t va[4];
+      ldmatrix4_trans(va, a.values + value_chunk(token, 2 * i + odd));
+#pragma unroll
+      for (int n = 0; n < N; ++n) mma_bf16(o[i][n], va, pb[n][0], pb[n][1]);
+    }
+  }
+  __device__ __forceinline__ void stats(float* ms, float* ls, int lane) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+        if (lane < 4) ms[8 * n + 2 * lane + e] = m[n][e], ls[8 * n + 2 * lane + e] = sum;
+      }
+  }
+  // Rows 16 pass and up, 16 of them at most, as own[row][DIM]: columns in the order of place().
+  __device__ __forceinline__ static int place(int row, int column) { return row * DIM + (column ^ (row >> 1 & 3) << 3); }
+  template <int PASS>
+  __device__ __forceinline__ void outputs(float* own, int lane) const {
+    const int quad = lane >> 2, four = lane & 3;
+#pragma unroll
+    for (int n = 2 * PASS; n < (2 * PASS + 2 < N ? 2 * PASS + 2 : N); ++n)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own[place(8 * (n & 1) + 2 * four + (e & 1), 16 * i + 8 * (e >> 1) + quad)] = o[i][n][e];
+  }
+};
+
+// The same for fp32, 16 rows: each product is three of tf32 (hi hi, hi lo, lo hi).  Lane
+// (quad, four) holds of S rows quad and quad + 8, tokens 8 n + 2 four + {0, 1}; of O the same rows.
+template <int DIM>
+struct AttnF32 {
+  using IT = float;
+  static constexpr int kRows = 16, kN = DIM / 8;
+  int limit[2];
+  float o[kN][4], m[2], l[2];
+
+  // The column of o[n][e], e = 0 or 1: values are taken four columns at a time.
+  __device__ __forceinline__ static int column(int four, int n, int e) { return 32 * (n / 4) + 4 * (2 * four + e) + (n & 3); }
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
+  }
+  // Q to shared memory: for each 8 columns the four registers of the left operand of every lane,
+  // hi and then lo; columns 16 kk + 4 f + {0, 1} and {2, 3} are those of four = f in two products.
+  __device__ __forceinline__ void queries(const AttnParams& p, const AttnCursor& at, int lane, char* smem) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) (void)at.query<IT, DIM>(p, kRows, 8 * h + (lane >> 2), limit[h]);
+    __syncthreads();  // the last unit's are read
+    for (int i = threadIdx.x; i < 32 * (DIM / 8); i += kAttnThreads) {
+      const int ks = i / 32, ln = i & 31, qd = ln >> 2, fr = ln & 3;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int last;
+        const IT* q = at.query<IT, DIM>(p, kRows, 8 * h + qd, last);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          split_tf32(q == nullptr ? 0.0f : q[16 * (ks / 2) + 4 * fr + 2 * (ks & 1) + e], hi[2 * e + h], lo[2 * e + h]);
+      }
+      uint4* to = reinterpret_cast<uint4*>(smem) + 2 * 32 * ks + ln;
+      to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      to[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, int lane, const char* smem) {
+    const int quad = lane >> 2, four = lane & 3;
+    float s[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    const uint32_t qs = rsm::smem_addr(smem) + lane * 16;
+#pragma unroll 4
+    for (int kk = 0; kk < DIM / 16; ++kk) {
+      uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint4 v = rsm::lds128(a.keys + key_chunk<IT>(8 * n + quad, 4 * kk + four));
+        split_tf32(__uint_as_float(v.x), hi[n][0], lo[n][0]);
+        split_tf32(__uint_as_float(v.y), hi[n][1], lo[n][1]);
+        split_tf32(__uint_as_float(v.z), hi[n][2], lo[n][2]);
+        split_tf32(__uint_as_float(v.w), hi[n][3], lo[n][3]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 h4 = rsm::lds128(qs + (2 * kk + e) * 1024), l4 = rsm::lds128(qs + (2 * kk + e) * 1024 + 512);
+        const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mma_tf32(s[n], al, hi[n][2 * e], hi[n][2 * e + 1]);
+          mma_tf32(s[n], ah, lo[n][2 * e], lo[n][2 * e + 1]);
+          mma_tf32(s[n], ah, hi[n][2 * e], hi[n][2 * e + 1]);
+        }
+      }
+    }
+    const bool masked = a.differ || a.seen != (1u << kAttnStep) - 1u;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 8 * n + 2 * four + (e & 1);
+        s[n][e] = masked && (!(a.seen >> j & 1u) || a.token0 + j > limit[e >> 1]) ? -INFINITY : s[n][e] * p.scale_log2;
+      }
+    bool moved = false;
+    float keep[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const float next = top > m[h] + kAttnSlack ? top : m[h], base = next == -INFINITY ? 0.0f : next;
+      keep[h] = exp2_fast(m[h] - base);
+      moved |= next != m[h];
+      m[h] = next;
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][2 * h + e] = exp2_fast(s[n][2 * h + e] - base);
+          sum += s[n][2 * h + e];
+        }
+      l[h] = fmaf(l[h], keep[h], sum);
+    }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] *= keep[e >> 1];
+    }
+    if (a.differ && p.window > 1)
+      odd_values<IT, DIM>(a, lane, [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float even = j & 8 ? s[1][2 * h] : s[0][2 * h], other = j & 8 ? s[1][2 * h + 1] : s[0][2 * h + 1];
+          const float w = __shfl_sync(0xFFFFFFFFu, j & 1 ? other : even, (lane & ~3) + (j & 7) / 2);
+          if (a.token0 + j > limit[h]) continue;
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float v = held_value<IT>(a, j, column(four, n, e));
+              if (!isfinite(v)) o[n][2 * h + e] += w * v;
+            }
+        }
+      });
+    // tokens 2 f and 2 f + 1 of eight are those of four = f, as S's columns are
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      uint32_t ph[4], pl[4];
+      split_tf32(s[kt][0], ph[0], pl[0]);
+      split_tf32(s[kt][2], ph[1], pl[1]);
+      split_tf32(s[kt][1], ph[2], pl[2]);
+      split_tf32(s[kt][3], ph[3], pl[3]);
+      const int t0 = 8 * kt + 2 * four, t1 = t0 + 1;
+#pragma unroll
+      for (int n = 0; n < kN; n += 4) {
+        const uint4 x = rsm::lds128(a.values + value_chunk(t0, 2 * n + quad)), y = rsm::lds128(a.values + value_chunk(t1, 2 * n + quad));
+        const uint32_t va[4] = {x.x, x.y, x.z, x.w}, vb[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h0, l0, h1, l1;
+          split_tf32(__uint_as_float(va[k]), h0, l0);
+          split_tf32(__uint_as_float(vb[k]), h1, l1);
+          mma_tf32(o[n + k], pl, h0, h1);
+          mma_tf32(o[n + k], ph, l0, l1);
+          mma_tf32(o[n + k], ph, h0, h1);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void stats(float* ms, float* ls, int lane) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float sum = l[h];
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      if ((lane & 3) == 0) ms[8 * h + (lane >> 2)] = m[h], ls[8 * h + (lane >> 2)] = sum;
+    }
+  }
+  __device__ __forceinline__ static int place(int row, int column) { return row * DIM + (column ^ (row & 3) << 3); }
+  template <int PASS>
+  __device__ __forceinline__ void outputs(float* own, int lane) const {
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) own[place(8 * (e >> 1) + (lane >> 2), column(lane & 3, n, e & 1))] = o[n][e];
+  }
+};
+
+// BOXES: loads by TMA; the pages are whole groups of 16 tokens.
+template <typename Math, int DIM, bool BOXES>
+__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM))
+    attn_tile_kernel(const __grid_constant__ AttnTileParams tp) {
+  using IT = typename Math::IT;
   using Shape = AttnShape<IT, DIM>;
-  constexpr bool kF32 = sizeof(IT) == 4;
-  constexpr int kWarps = kAttnThreads / 32, kRows = 16 * M, kN = DIM / 8;  // kN: n-tiles of 8 columns
-  constexpr int S = Shape::kStages, kChunks = Shape::kChunks;
-  static_assert(!kF32 || M == 1);
-  extern __shared__ __align__(128) char smem[];
+  constexpr int kWarps = kAttnThreads / 32, kRows = Math::kRows, S = Shape::kStages, kChunks = Shape::kChunks;
+  constexpr uint32_t kAll = (1u << kAttnStep) - 1u;
+  extern __shared__ __align__(1024) char smem[];
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
   __shared__ uint32_t seen_s[kWarps][S];
+  __shared__ __align__(8) uint64_t full_s[kWarps][S];  // BOXES: a stage's loads
+  const AttnParams& p = tp.p;
   const rsm_pages& pg = p.pages;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = lane >> 2, four = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (BOXES) {
+    if (lane == 0) {
+      for (int i = 0; i < S; ++i) rsm::mbar_init(rsm::smem_addr(&full_s[warp][i]), 1);
+      rsm::fence_mbar_init();
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&tp.k_map) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&tp.v_map) : "memory");
+    }
+    __syncwarp();
+  }
 
   for (int b = blockIdx.x; b < pg.requests; b += gridDim.x)  // rows of skipped requests
     if (request_tokens(pg, b, p.window, nullptr, false) == 0) {
-      IT* out = static_cast<IT*>(p.out) + static_cast<int64_t>(b) * p.window * p.H * DIM;
       const int64_t n = static_cast<int64_t>(p.window) * p.H * DIM;
+      IT* out = static_cast<IT*>(p.out) + b * n;
       for (int64_t i = threadIdx.x; i < n; i += kAttnThreads) out[i] = IT(0);
     }
-  AttnDeal deal;
-  deal.total = deal_total<kAttnThreads>(p, blockIdx.x == 0);
-  deal.ctas = min(static_cast<int64_t>(gridDim.x), deal.total);
+  const Deal<kAttnThreads> requests(p, blockIdx.x == 0);
+  const AttnDeal deal{requests.total, min(static_cast<int64_t>(gridDim.x), requests.total)};
   if (blockIdx.x >= deal.ctas) return;
   const int64_t begin = deal.begin(blockIdx.x);
-  const int count = static_cast<int>(deal.begin(blockIdx.x + 1) - begin);
-  const Place place = deal_find<kAttnThreads>(p, begin);
-  const int units = p.G * p.row_tiles;
+  const Place place = requests.find(p, begin);
+  // `room` is what is left of this CTA's share where `at` stands.
+  int64_t room = deal.begin(blockIdx.x + 1) - begin;
   AttnCursor at;
   at.b = place.b;
   at.at_request(p);
-  at.u = static_cast<int>((begin - place.first) / at.tiles);
-  at.tile = static_cast<int>(begin - place.first - static_cast<int64_t>(at.u) * at.tiles);
+  {
+    const int64_t into = begin - place.first;
+    const int unit = static_cast<int>(into / counts(at.tiles)), tile = static_cast<int>(into - unit * counts(at.tiles));
+    at.g = unit / p.row_tiles;
+    at.rt = unit - at.g * p.row_tiles;
+    at.tile = tile;
+    if (tile >= at.tiles) {  // the share begins in what a unit's end counts
+      room -= counts(at.tiles) - tile;
+      if (room <= 0) return;
+      at.next_unit(p);
+    }
+  }
   AttnCursor ask = at;
+  int64_t ask_room = room;
 
-  // ---- loads: a warp's 16 tokens of a tile.  The page is looked up a step ahead. ----
+  // ---- loads: a warp's 16 tokens of a tile ----
   const uint32_t ring = rsm::smem_addr(smem) + Shape::kQuery + warp * (S * Shape::kStage);
-  const bool one_page = pg.page_size % kAttnStep == 0;  // the 16 tokens lie in one page
-  auto page_of = [&](const AttnCursor& c) {
-    const int token = c.tile * kAttnTile + warp * kAttnStep + (one_page ? 0 : lane % kAttnStep);
-    if (token >= c.len) return -1;  // no token
-    const int i = p.page_shift >= 0 ? token >> p.page_shift : token / pg.page_size;
-    return __ldg(pg.page_table + c.b * pg.table_stride + i);
+  const uint32_t full = rsm::smem_addr(&full_s[warp][0]);
+  const bool one_page = BOXES || pg.page_size % kAttnStep == 0;  // the 16 tokens lie in one page
+  auto page_at = [&](int64_t token) {
+    if (token >= ask.len) return -1;  // no token
+    const int i = p.page_shift >= 0 ? static_cast<int>(token) >> p.page_shift : static_cast<int>(token) / pg.page_size;
+    return __ldg(pg.page_table + ask.b * pg.table_stride + i);
   };
-  int page = page_of(ask), left = count;
+  // One page a step: a lane looks up that of the tile lane of each 32, all at once; else a lane a token, a step ahead.
+  int looked = -1, pages = -1;
+  auto look_up = [&](bool request) {
+    if (one_page) {
+      const int group = ask.tile >> 5;
+      if (!request && group == looked) return;
+      looked = group;
+      pages = page_at((static_cast<int64_t>(group) * 32 + lane) * kAttnTile + warp * kAttnStep);
+    } else {
+      pages = page_at(static_cast<int64_t>(ask.tile) * kAttnTile + warp * kAttnStep + lane % kAttnStep);
+    }
+  };
+  look_up(true);
   auto load = [&](int stage) {
-    if (left <= 0) {
-      cp_async_commit();
+    if (ask_room <= 0) {
+      if constexpr (!BOXES) cp_async_commit();
       return;
     }
-    const int g = ask.u / p.row_tiles, token0 = ask.tile * kAttnTile + warp * kAttnStep;
+    const int g = ask.g, token0 = ask.tile * kAttnTile + warp * kAttnStep;
+    const int page = one_page ? __shfl_sync(0xFFFFFFFFu, pages, ask.tile & 31) : pages;
     const bool good = page >= 0 && page < pg.num_pages;
     if (!good && token0 + (one_page ? 0 : lane % kAttnStep) < ask.len) flag(p.status, RSM_STATUS_BAD_PAGE);
     const uint32_t base = ring + stage * Shape::kStage;
-    constexpr int kPer = kChunks > 32 ? kChunks / 32 : 1;  // chunks of a row a lane
-    constexpr int kAt = kChunks > 32 ? 1 : 32 / kChunks;   // rows at a time
-    const int row0 = kChunks > 32 ? 0 : lane / kChunks, chunk0 = lane % kChunks;
     uint32_t seen;
-    if (one_page) {
-      const int row = p.page_shift >= 0 ? token0 & (pg.page_size - 1) : token0 % pg.page_size;
-      const int64_t ko = good ? page * pg.k_page_stride + row * pg.k_row_stride + g * pg.k_head_stride : 0;
-      const int64_t vo = good ? page * pg.v_page_stride + row * pg.v_row_stride + g * pg.v_head_stride : 0;
-      const int n = good ? min(kAttnStep, ask.len - token0) : 0;
-      seen = (1u << n) - 1u;
-      const char* k = reinterpret_cast<const char*>(static_cast<const IT*>(pg.k) + ko);
-      const char* v = reinterpret_cast<const char*>(static_cast<const IT*>(pg.v) + vo);
-      const int64_t ks = pg.k_row_stride * static_cast<int64_t>(sizeof(IT)), vs = pg.v_row_stride * static_cast<int64_t>(sizeof(IT));
+    if constexpr (BOXES) {
+      seen = good ? (1u << min(kAttnStep, ask.len - token0)) - 1u : 0u;
+      if (lane == 0) {
+        const uint32_t bar = full + stage * 8;
+        if (good) {
+          const int row = p.page_shift >= 0 ? token0 & (pg.page_size - 1) : token0 % pg.page_size;
+          arrive_expect(bar, Shape::kStage);
 #pragma unroll
-      for (int i = 0; i < kAttnStep / kAt; ++i) {
-        const int r = i * kAt + row0;
-        const bool yes = r < n;
-        const char* kr = yes ? k + r * ks : static_cast<const char*>(pg.k);
-        const char* vr = yes ? v + r * vs : static_cast<const char*>(pg.v);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int chunk = chunk0 + 32 * j;
-          cp_async_16_or_zero(base + r * Shape::kRow + (chunk ^ key_order<IT>(r)) * 16, kr + chunk * 16, yes);
-          cp_async_16_or_zero(base + Shape::kHalf + r * Shape::kRow + (chunk ^ value_order(r)) * 16, vr + chunk * 16, yes);
+          for (int c = 0; c < DIM / 64; ++c) {
+            box_load(base + c * (kAttnStep * 128), &tp.k_map, 64 * c, g, row, page, bar);
+            box_load(base + Shape::kHalf + c * (kAttnStep * 128), &tp.v_map, 64 * c, g, row, page, bar);
+          }
+        } else {
+          rsm::mbar_arrive(bar);
         }
       }
     } else {
-      seen = __ballot_sync(0xFFFFFFFFu, good) & ((1u << kAttnStep) - 1u);
-      const int token = token0 + lane % kAttnStep;
+      constexpr int kAt = 32 / kChunks;  // rows at a time
+      const int row0 = lane / kChunks, chunk = lane % kChunks;
+      const int token = token0 + (one_page ? 0 : lane % kAttnStep);
       const int row = p.page_shift >= 0 ? token & (pg.page_size - 1) : token % pg.page_size;
-#pragma unroll 1
+      seen = one_page ? (good ? (1u << min(kAttnStep, ask.len - token0)) - 1u : 0u) : __ballot_sync(0xFFFFFFFFu, good) & kAll;
+#pragma unroll 4
       for (int i = 0; i < kAttnStep / kAt; ++i) {
         const int r = i * kAt + row0;
-        const int pr = __shfl_sync(0xFFFFFFFFu, page, r), rr = __shfl_sync(0xFFFFFFFFu, row, r);
+        int pr = page, rr = row + r;
+        if (!one_page) pr = __shfl_sync(0xFFFFFFFFu, page, r), rr = __shfl_sync(0xFFFFFFFFu, row, r);
         const bool yes = seen >> r & 1u;
-        const char* kr = reinterpret_cast<const char*>(static_cast<const IT*>(pg.k) +
-                                                       (yes ? pr * pg.k_page_stride + rr * pg.k_row_stride + g * pg.k_head_stride : 0));
-        const char* vr = reinterpret_cast<const char*>(static_cast<const IT*>(pg.v) +
-                                                       (yes ? pr * pg.v_page_stride + rr * pg.v_row_stride + g * pg.v_head_stride : 0));
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int chunk = chunk0 + 32 * j;
-          cp_async_16_or_zero(base + r * Shape::kRow + (chunk ^ key_order<IT>(r)) * 16, kr + chunk * 16, yes);
-          cp_async_16_or_zero(base + Shape::kHalf + r * Shape::kRow + (chunk ^ value_order(r)) * 16, vr + chunk * 16, yes);
-        }
+        const IT* kr = static_cast<const IT*>(pg.k) + (yes ? pr * pg.k_page_stride + rr * pg.k_row_stride + g * pg.k_head_stride : 0);
+        const IT* vr = static_cast<const IT*>(pg.v) + (yes ? pr * pg.v_page_stride + rr * pg.v_row_stride + g * pg.v_head_stride : 0);
+        cp_async_16_or_zero(base + key_chunk<IT>(r, chunk), reinterpret_cast<const char*>(kr) + chunk * 16, yes);
+        cp_async_16_or_zero(base + Shape::kHalf + value_chunk(r, chunk), reinterpret_cast<const char*>(vr) + chunk * 16, yes);
       }
+      cp_async_commit();
     }
     if (lane == 0) seen_s[warp][stage] = seen;
-    cp_async_commit();
-    if (--left > 0) {
-      ask.next(p, units);
-      page = page_of(ask);
+    ask_room -= ask.tile + 1 == ask.tiles ? 1 + kAttnUnit : 1;
+    if (ask_room > 0) {
+      const int b = ask.b;
+      ask.next(p);
+      look_up(ask.b != b);
     }
   };
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) load(s);
 
-  // ---- a unit's queries ----
-  const int rows_all = p.per * p.window;
-  uint32_t qa[kF32 ? 1 : M][kF32 ? 1 : DIM / 16][4];
-  int limit[M][2];  // the last token that a row sees
-  auto query = [&](int row, int rt, int g, int& last) -> const IT* {
-    const int r = rt * kRows + row;
-    const int t = r / p.per;
-    last = at.len - p.window + t;
-    if (r >= rows_all) return nullptr;
-    return static_cast<const IT*>(p.q) + at.b * p.q_bs + t * p.q_ts + static_cast<int64_t>(g * p.per + r - t * p.per) * DIM;
-  };
-  auto load_queries = [&]() {
-    const int g = at.u / p.row_tiles, rt = at.u - g * p.row_tiles;
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const IT* q = query(16 * i + 8 * h + quad, rt, g, limit[i][h]);
-        if constexpr (!kF32) {
-#pragma unroll
-          for (int ks = 0; ks < DIM / 16; ++ks)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t v = 0;
-              if (q != nullptr) {
-                const IT* s = q + 16 * ks + 8 * e + 2 * four;
-                v = p.q_pairs ? *reinterpret_cast<const uint32_t*>(s) : static_cast<uint32_t>(s[0]) | static_cast<uint32_t>(s[1]) << 16;
-              }
-              qa[i][ks][2 * e + h] = v;
-            }
-        }
-      }
-    if constexpr (kF32) {
-      // for each 8 columns the four registers of the left operand of every lane, hi and
-      // then lo; column 16 kk + 4 f + {0, 1} and {2, 3} are those of four = f in two products
-      __syncthreads();  // the last unit's are read
-      for (int i = threadIdx.x; i < 32 * (DIM / 8); i += kAttnThreads) {
-        const int ks = i / 32, ln = i & 31, qd = ln >> 2, fr = ln & 3;
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int last;
-          const IT* q = query(8 * h + qd, rt, g, last);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            split_tf32(q == nullptr ? 0.0f : q[16 * (ks / 2) + 4 * fr + 2 * (ks & 1) + e], hi[2 * e + h], lo[2 * e + h]);
-        }
-        uint4* to = reinterpret_cast<uint4*>(smem) + 2 * 32 * ks + ln;
-        to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        to[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      __syncthreads();
-    }
-  };
-
-  float o[M][kN][4], m[M][2], l[M][2];
-  auto reset = [&]() {
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
-      m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.0f;
-    }
-  };
-  // The column of o[.][n][e], e = 0 or 1: products of fp32 take values four columns at a time.
-  auto column = [&](int n, int e) { return kF32 ? 32 * (n / 4) + 4 * (2 * four + e) + (n & 3) : 8 * n + 2 * four + e; };
-
-  load_queries();
-  reset();
+  Math math;
+  math.queries(p, at, lane, smem);
+  math.reset();
   int from = at.tile;  // the piece's first tile
-  for (int i = 0, stage = 0; i < count; ++i, stage = stage + 1 == S ? 0 : stage + 1) {
-    cp_async_wait<S - 2>();
+  uint32_t phase = 0;
+  for (int stage = 0;;) {
+    if constexpr (BOXES) {
+      if (!rsm::mbar_wait(full + stage * 8, phase, kAttnTimeoutNs)) {  // (never expected)
+        flag(p.status, RSM_STATUS_WAIT_TIMEOUT);
+        for (int k = 0; k < S; ++k) (void)rsm::mbar_wait(full + k * 8, k < stage ? phase ^ 1u : phase, 1000000ull);  // copies on the way
+        return;
+      }
+    } else {
+      cp_async_wait<S - 2>();
+    }
     __syncwarp();
     load(stage == 0 ? S - 1 : stage - 1);
-    const uint32_t keys = ring + stage * Shape::kStage, values = keys + Shape::kHalf;
-    const uint32_t seen = seen_s[warp][stage];
-    const int token0 = at.tile * kAttnTile + warp * kAttnStep;
-    const bool diagonal = token0 + kAttnStep - 1 > at.len - p.window;  // rows differ in what they see
-
-    if (seen != 0) {
-      float s[M][2][4];
-#pragma unroll
-      for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) s[i2][n][0] = s[i2][n][1] = s[i2][n][2] = s[i2][n][3] = 0.0f;
-      if constexpr (!kF32) {
-        const int token = (lane >> 4) * 8 + (lane & 7), odd = lane >> 3 & 1;
-#pragma unroll
-        for (int ks = 0; ks < DIM / 16; ++ks) {
-          uint32_t kb[4];
-          ldmatrix4(kb, keys + token * Shape::kRow + ((2 * ks + odd) ^ key_order<IT>(token)) * 16);
-#pragma unroll
-          for (int i2 = 0; i2 < M; ++i2) {
-            mma_bf16(s[i2][0], qa[i2][ks], kb[0], kb[1]);
-            mma_bf16(s[i2][1], qa[i2][ks], kb[2], kb[3]);
-          }
-        }
-      } else {
-        const uint32_t qs = rsm::smem_addr(smem) + lane * 16;
-#pragma unroll 4
-        for (int kk = 0; kk < DIM / 16; ++kk) {
-          uint32_t hi[2][4], lo[2][4];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int token = 8 * n + quad;
-            const uint4 v = rsm::lds128(keys + token * Shape::kRow + ((4 * kk + four) ^ key_order<IT>(token)) * 16);
-            split_tf32(__uint_as_float(v.x), hi[n][0], lo[n][0]);
-            split_tf32(__uint_as_float(v.y), hi[n][1], lo[n][1]);
-            split_tf32(__uint_as_float(v.z), hi[n][2], lo[n][2]);
-            split_tf32(__uint_as_float(v.w), hi[n][3], lo[n][3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint4 h4 = rsm::lds128(qs + (2 * kk + e) * 1024), l4 = rsm::lds128(qs + (2 * kk + e) * 1024 + 512);
-            const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              mma_tf32(s[0][n], al, hi[n][2 * e], hi[n][2 * e + 1]);
-              mma_tf32(s[0][n], ah, lo[n][2 * e], lo[n][2 * e + 1]);
-              mma_tf32(s[0][n], ah, hi[n][2 * e], hi[n][2 * e + 1]);
-            }
-          }
-        }
-      }
-      // ---- what is not seen, the running maximum, the weights ----
-#pragma unroll
-      for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i2][n][e] *= p.scale_log2;
-      if (diagonal || seen != (1u << kAttnStep) - 1u) {
-#pragma unroll
-        for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = 8 * n + 2 * four + (e & 1);
-              if (!(seen >> j & 1u) || token0 + j > limit[i2][e >> 1]) s[i2][n][e] = -INFINITY;
-            }
-      }
-      bool moved = false;
-      float keep[M][2];
-#pragma unroll
-      for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float top = fmaxf(fmaxf(s[i2][0][2 * h], s[i2][0][2 * h + 1]), fmaxf(s[i2][1][2 * h], s[i2][1][2 * h + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const float next = fmaxf(m[i2][h], top), base = next == -INFINITY ? 0.0f : next;
-          keep[i2][h] = exp2_fast(m[i2][h] - base);
-          moved |= next != m[i2][h];
-          m[i2][h] = next;
-          float sum = 0.0f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float w = exp2_fast(s[i2][n][2 * h + e] - base);
-              s[i2][n][2 * h + e] = w;
-              sum += w;
-            }
-          l[i2][h] = fmaf(l[i2][h], keep[i2][h], sum);
-        }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-        for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-          for (int n = 0; n < kN; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i2][n][e] *= keep[i2][e >> 1];
-      }
-      // ---- a new token's values that are not finite go to the rows that see it, and not
-      // into the product, where a weight of zero would not keep them from the others ----
-      if (diagonal && p.window > 1) {
-        const int first_new = max(at.len - p.window - token0, 0);
-        bool odd = false;
-        for (int c = lane; c < kAttnStep * kChunks; c += 32) {
-          const int j = c / kChunks;
-          if (j < first_new) continue;
-          const uint4 v = rsm::lds128(values + c * 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            odd |= (w[k] & 0x7F800000u) == 0x7F800000u;
-            if (!kF32) odd |= (w[k] & 0x7F80u) == 0x7F80u;
-          }
-        }
-        if (__any_sync(0xFFFFFFFFu, odd)) {
-          for (int j = first_new; j < kAttnStep; ++j) {
-            if (!(seen >> j & 1u)) continue;
-            const char* row = smem + (values - rsm::smem_addr(smem)) + j * Shape::kRow;
-#pragma unroll
-            for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float even = j & 8 ? s[i2][1][2 * h] : s[i2][0][2 * h], other = j & 8 ? s[i2][1][2 * h + 1] : s[i2][0][2 * h + 1];
-                const float w = __shfl_sync(0xFFFFFFFFu, j & 1 ? other : even, (lane & ~3) + (j & 7) / 2);
-                if (token0 + j <= limit[i2][h]) {
-#pragma unroll
-                  for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      const int c = column(n, e) * static_cast<int>(sizeof(IT));
-                      const float v = get(reinterpret_cast<const IT*>(row + ((c / 16) ^ value_order(j)) * 16 + c % 16));
-                      if (!isfinite(v)) o[i2][n][2 * h + e] += w * v;
-                    }
-                }
-              }
-          }
-          __syncwarp();
-          for (int c = lane; c < kAttnStep * kChunks; c += 32) {
-            if (c / kChunks < first_new) continue;
-            IT* v = reinterpret_cast<IT*>(smem + (values - rsm::smem_addr(smem)) + c * 16);
-#pragma unroll
-            for (int k = 0; k < 16 / static_cast<int>(sizeof(IT)); ++k)
-              if (!isfinite(get(v + k))) v[k] = IT(0);
-          }
+    AttnStep a;
+    a.seen = seen_s[warp][stage];
+    if (a.seen != 0) {
+      a.keys = ring + stage * Shape::kStage;
+      a.values = a.keys + Shape::kHalf;
+      a.held = smem + (a.values - rsm::smem_addr(smem));
+      a.token0 = at.tile * kAttnTile + warp * kAttnStep;
+      a.differ = a.token0 + kAttnStep - 1 > at.len - p.window;
+      a.first_new = max(at.len - p.window + 1 - a.token0, 0);
+      if constexpr (BOXES) {  // rows behind the last token came with the box
+        if (a.seen != kAll) {
+          for (int c = lane; c < kAttnStep * kChunks; c += 32)
+            if (!(a.seen >> ((c >> 3) % kAttnStep) & 1u)) *reinterpret_cast<uint4*>(a.held + c * 16) = make_uint4(0, 0, 0, 0);
+          rsm::fence_proxy_async_smem();
           __syncwarp();
         }
       }
-      if constexpr (!kF32) {
-        uint32_t pa[M][4];
-#pragma unroll
-        for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            pa[i2][2 * n] = rsm::pack_bf16x2(s[i2][n][0], s[i2][n][1]);
-            pa[i2][2 * n + 1] = rsm::pack_bf16x2(s[i2][n][2], s[i2][n][3]);
-          }
-        const int token = (lane >> 3 & 1) * 8 + (lane & 7);
-#pragma unroll
-        for (int n = 0; n < kN; n += 2) {
-          uint32_t vb[4];
-          ldmatrix4_trans(vb, values + token * Shape::kRow + ((n + (lane >> 4)) ^ value_order(token)) * 16);
-#pragma unroll
-          for (int i2 = 0; i2 < M; ++i2) {
-            mma_bf16(o[i2][n], pa[i2], vb[0], vb[1]);
-            mma_bf16(o[i2][n + 1], pa[i2], vb[2], vb[3]);
-          }
-        }
-      } else {
-        // tokens 2 f and 2 f + 1 of eight are those of four = f, as S's columns are
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          uint32_t ph[4], pl[4];
-          split_tf32(s[0][kt][0], ph[0], pl[0]);
-          split_tf32(s[0][kt][2], ph[1], pl[1]);
-          split_tf32(s[0][kt][1], ph[2], pl[2]);
-          split_tf32(s[0][kt][3], ph[3], pl[3]);
-          const int t0 = 8 * kt + 2 * four, t1 = t0 + 1;
-#pragma unroll
-          for (int n = 0; n < kN; n += 4) {
-            const uint4 a = rsm::lds128(values + t0 * Shape::kRow + ((2 * n + quad) ^ value_order(t0)) * 16);
-            const uint4 b = rsm::lds128(values + t1 * Shape::kRow + ((2 * n + quad) ^ value_order(t1)) * 16);
-            const uint32_t va[4] = {a.x, a.y, a.z, a.w}, vb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t h0, l0, h1, l1;
-              split_tf32(__uint_as_float(va[k]), h0, l0);
-              split_tf32(__uint_as_float(vb[k]), h1, l1);
-              mma_tf32(o[0][n + k], pl, h0, h1);
-              mma_tf32(o[0][n + k], ph, l0, l1);
-              mma_tf32(o[0][n + k], ph, h0, h1);
-            }
-          }
-        }
-      }
+      math.step(p, a, lane, smem);
     }
 
     // ---- the end of a unit, or of this CTA's part of it ----
     const bool last_tile = at.tile + 1 == at.tiles;
-    if (last_tile || i + 1 == count) {
-      const int g = at.u / p.row_tiles, rt = at.u - g * p.row_tiles;
+    room -= last_tile ? 1 + kAttnUnit : 1;
+    const bool over = room <= 0;
+    if (last_tile || over) {
+      const AttnCursor was = at;
       const bool whole = from == 0 && last_tile;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
-#pragma unroll
-      for (int i2 = 0; i2 < M; ++i2)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float sum = l[i2][h];
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          if (four == 0) m_s[warp][16 * i2 + 8 * h + quad] = m[i2][h], l_s[warp][16 * i2 + 8 * h + quad] = sum;
-        }
+      math.stats(m_s[warp], l_s[warp], lane);
+      // the next unit's queries are on their way meanwhile (fp32: see below)
+      if (!over) {
+        at.next(p);
+        if constexpr (Shape::kQuery == 0) math.queries(p, at, lane, smem);
+      }
       // the warps' outputs pass through the stages just read, 16 rows at a time
-      const uint32_t pass = Shape::kQuery + stage * Shape::kStage;
-#pragma unroll
-      for (int i2 = 0; i2 < M; ++i2) {
-        float* own = reinterpret_cast<float*>(smem + pass + warp * (S * Shape::kStage));
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = 8 * h + quad;
-            if constexpr (kF32) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) own[row * DIM + (column(n, e) ^ (row & 3) << 3)] = o[i2][n][2 * h + e];
-            } else {
-              *reinterpret_cast<float2*>(own + row * DIM + (column(n, 0) ^ (row & 3) << 3)) = make_float2(o[i2][n][2 * h], o[i2][n][2 * h + 1]);
-            }
-          }
+      char* const pass_at = smem + Shape::kQuery + stage * Shape::kStage;
+      auto pass = [&](auto index) {
+        constexpr int kPass = decltype(index)::value, kHere = kRows - 16 * kPass < 16 ? kRows - 16 * kPass : 16;
+        math.template outputs<kPass>(reinterpret_cast<float*>(pass_at + warp * (S * Shape::kStage)), lane);
         __syncthreads();
-        for (int c = threadIdx.x; c < 16 * DIM / 4; c += kAttnThreads) {
-          const int row = c / (DIM / 4), col = (c - row * (DIM / 4)) * 4, r = 16 * i2 + row, all = rt * kRows + r;
-          if (all >= rows_all) continue;
+        for (int c = threadIdx.x; c < kHere * DIM / 4; c += kAttnThreads) {
+          const int row = c / (DIM / 4), col = (c - row * (DIM / 4)) * 4, r = 16 * kPass + row, all = was.rt * kRows + r;
+          if (all >= p.per * p.window) continue;
           float top = -INFINITY, sum = 0.0f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][r]);
@@ -596,95 +805,133 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(IT), DIM
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float f = top == -INFINITY ? 0.0f : exp2_fast(m_s[w][r] - top);
-            const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + pass + w * (S * Shape::kStage)) +
-                                                              row * DIM + (col ^ (row & 3) << 3));
+            const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(pass_at + w * (S * Shape::kStage)) + Math::place(row, col));
             y.x = fmaf(v.x, f, y.x), y.y = fmaf(v.y, f, y.y), y.z = fmaf(v.z, f, y.z), y.w = fmaf(v.w, f, y.w);
             sum = fmaf(l_s[w][r], f, sum);
           }
           if (whole) {
             const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
             const int t = all / p.per;
-            IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(at.b) * p.window + t) * p.H + g * p.per + all - t * p.per) * DIM + col;
-            if constexpr (kF32)
+            IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(was.b) * p.window + t) * p.H + was.g * p.per + all - t * p.per) * DIM + col;
+            if constexpr (sizeof(IT) == 4)
               *reinterpret_cast<float4*>(out) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
             else
               *reinterpret_cast<uint2*>(out) = make_uint2(rsm::pack_bf16x2(y.x * f, y.y * f), rsm::pack_bf16x2(y.z * f, y.w * f));
           } else {
             *reinterpret_cast<float4*>(p.part + (slot * kRows + r) * DIM + col) = y;
-            if (col == 0) {
-              float* ml = p.part + 2 * static_cast<int64_t>(p.ctas) * kRows * DIM + (slot * kRows + r) * 2;
-              ml[0] = top;
-              ml[1] = sum;
-            }
+            if (col == 0)
+              *reinterpret_cast<float2*>(p.part + 2 * static_cast<int64_t>(p.ctas) * kRows * DIM + (slot * kRows + r) * 2) = make_float2(top, sum);
           }
         }
+        if constexpr (BOXES) rsm::fence_proxy_async_smem();  // the boxes to come write here too
         __syncthreads();
-      }
-    }
-    if (i + 1 == count) break;
-    at.next(p, units);
-    if (last_tile) {
+      };
+      pass(std::integral_constant<int, 0>{});
+      if constexpr (kRows > 16) pass(std::integral_constant<int, 1>{});
+      if (over) break;
+      if constexpr (Shape::kQuery != 0) math.queries(p, at, lane, smem);
+      math.reset();
       from = 0;
-      load_queries();
-      reset();
+    } else {
+      ++at.tile;
     }
+    if (++stage == S) stage = 0, phase ^= 1u;
   }
-  cp_async_wait<0>();
+  if constexpr (!BOXES) cp_async_wait<0>();
 }
 
-// Units in pieces, each by the CTAs of the one that has its first piece: `parts` of
-// them, which share its rows out.
-template <typename IT, int DIM, int M>
-__global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p, int parts) {
-  constexpr int kRows = 16 * M, kWarps = kAttnJoinThreads / 32, kPer = DIM / 32;
-  __shared__ float acc_s[kWarps][DIM], l_s[kWarps];
-  const int c0 = blockIdx.x / parts, part = blockIdx.x - c0 * parts;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  AttnDeal deal;
-  deal.total = deal_total<kAttnJoinThreads>(p, false);
-  deal.ctas = min(static_cast<int64_t>(p.ctas), deal.total);
+// Units in pieces, `parts` CTAs each, which share the rows out.  By unit, where there
+// are no more of them than CTAs of the first kernel; else by such a CTA: it has at most one
+// unit's first piece.
+template <typename Math, int DIM>
+__global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p, int parts, int by_unit) {
+  using IT = typename Math::IT;
+  constexpr int kRows = Math::kRows, kLanes = DIM / 4, kGroups = kAttnJoinThreads / kLanes;  // kLanes threads take a row's columns, four each
+  constexpr int kU = 8;  // rows asked for at a time
+  __shared__ float4 acc_s[kGroups][kLanes];
+  __shared__ float red_s[kAttnJoinThreads / 32];
+  extern __shared__ float weight_s[];  // a piece's
+  const int index = blockIdx.x / parts, part = blockIdx.x - index * parts;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = p.G * p.row_tiles;
+  const Deal<kAttnJoinThreads> d(p, false);
+  const AttnDeal deal{d.total, min(static_cast<int64_t>(p.ctas), d.total)};
+  int64_t first = 0;
+  int b = 0, u = 0, tiles = 0;
+  if (by_unit) {
+    b = index / units;
+    u = index - b * units;
+    tiles = tiles_of(request_tokens(p.pages, b, p.window, nullptr, false));
+    first = d.before(p, b) + u * counts(tiles);
+  } else if (index < deal.ctas) {
+    const Place place = d.find(p, deal.begin(index + 1) - 1);
+    b = place.b;
+    tiles = tiles_of(request_tokens(p.pages, b, p.window, nullptr, false));
+    u = static_cast<int>((deal.begin(index + 1) - 1 - place.first) / counts(tiles));
+    first = place.first + u * counts(tiles);
+    if (first < deal.begin(index)) tiles = 0;  // it began before
+  }
+  int c0 = 0, pieces = 1;
+  if (tiles > 0) {
+    c0 = static_cast<int>(deal.owner(first));
+    pieces = static_cast<int>(deal.owner(first + tiles - 1)) - c0 + 1;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: the call is over when this kernel is
-  if (c0 >= deal.ctas) return;
-  const int64_t begin = deal.begin(c0), end = deal.begin(c0 + 1);
-  const Place place = deal_find<kAttnJoinThreads>(p, end - 1);
-  const int tiles = tiles_of(request_tokens(p.pages, place.b, p.window, nullptr, false));
-  const int u = static_cast<int>((end - 1 - place.first) / tiles);
-  const int64_t first = place.first + static_cast<int64_t>(u) * tiles;
-  if (first + tiles <= end || first < begin) return;  // it ends here, or began before
-  const int pieces = static_cast<int>(deal.owner(first + tiles - 1)) - c0 + 1;
+  if (pieces == 1) return;
   const int g = u / p.row_tiles, rt = u - g * p.row_tiles, rows = min(kRows, p.per * p.window - rt * kRows);
-  const float* ml = p.part + 2 * static_cast<int64_t>(p.ctas) * kRows * DIM;
+  const float2* ml = reinterpret_cast<const float2*>(p.part + 2 * static_cast<int64_t>(p.ctas) * kRows * DIM);
   auto slot = [&](int i) { return 2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0); };
-  for (int r = part; r < rows; r += parts) {
-    float top = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) top = fmaxf(top, ml[(slot(i) * kRows + r) * 2]);
+  const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
+  auto all = [&](float v, auto op) {  // over the CTA
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float acc[kPer], sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
-#pragma unroll 4
-    for (int i = warp; i < pieces; i += kWarps) {
-      const int64_t at = slot(i) * kRows + r;
-      const float f = top == -INFINITY ? 0.0f : exp2_fast(ml[at * 2] - top);
-      sum = fmaf(ml[at * 2 + 1], f, sum);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(p.part[at * DIM + lane + 32 * k], f, acc[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc_s[warp][lane + 32 * k] = acc[k];
-    if (lane == 0) l_s[warp] = sum;
+    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     __syncthreads();
-    sum = 0.0f;
+    if (lane == 0) red_s[warp] = v;
+    __syncthreads();
+    v = red_s[0];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += l_s[w];
-    const int all = rt * kRows + r, t = all / p.per;
-    IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(place.b) * p.window + t) * p.H + g * p.per + all - t * p.per) * DIM;
+    for (int w = 1; w < kAttnJoinThreads / 32; ++w) v = op(v, red_s[w]);
+    return v;
+  };
+  for (int r = part; r < rows; r += parts) {
+    // a thread two pieces at most (p.ctas <= 2 kAttnJoinThreads)
+    float2 s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = threadIdx.x + k * kAttnJoinThreads;
+      s[k] = i < pieces ? ml[slot(i) * kRows + r] : make_float2(-INFINITY, 0.0f);
+    }
+    const float top = all(fmaxf(s[0].x, s[1].x), [](float x, float y) { return fmaxf(x, y); });
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = threadIdx.x + k * kAttnJoinThreads;
+      const float f = top == -INFINITY ? 0.0f : exp2_fast(s[k].x - top);
+      if (i < pieces) weight_s[i] = f;
+      sum = fmaf(s[k].y, i < pieces ? f : 0.0f, sum);
+    }
+    sum = all(sum, [](float x, float y) { return x + y; });
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = group; i < pieces; i += kGroups * kU) {
+      float4 v[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (i + k * kGroups < pieces) v[k] = reinterpret_cast<const float4*>(p.part + (slot(i + k * kGroups) * kRows + r) * DIM)[col];
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (i + k * kGroups < pieces) {
+          const float f = weight_s[i + k * kGroups];
+          y.x = fmaf(v[k].x, f, y.x), y.y = fmaf(v[k].y, f, y.y), y.z = fmaf(v[k].z, f, y.z), y.w = fmaf(v[k].w, f, y.w);
+        }
+    }
+    acc_s[group][col] = y;
+    __syncthreads();
+    const int row = rt * kRows + r, t = row / p.per;
+    IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(b) * p.window + t) * p.H + g * p.per + row - t * p.per) * DIM;
     for (int c = threadIdx.x; c < DIM; c += kAttnJoinThreads) {
-      float y = 0.0f;
+      float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) y += acc_s[w][c];
-      put(out + c, sum == 0.0f ? 0.0f : y / sum);
+      for (int w = 0; w < kGroups; ++w) v += reinterpret_cast<const float*>(acc_s[w])[c];
+      put(out + c, sum == 0.0f ? 0.0f : v / sum);
     }
     __syncthreads();
   }

@@ -137,7 +137,7 @@ int validate(const rsm_paged_attention_args* a, bool pointers) {
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_attn_ready[kMaxDevices][2][3][2];  // input type, dim 64, 128, 256, groups of rows
+bool g_attn_ready[kMaxDevices][2][3][4][2];  // input type, dim 64, 128, 256, eights of rows, boxes
 
 int device_sms(int* dev, int* sms) {
   cudaError_t e = cudaGetDevice(dev);
@@ -154,7 +154,7 @@ int device_sms(int* dev, int* sms) {
 
 // How a call runs on the tiled kernel.
 struct AttnPlan {
-  int groups;     // of 16 rows a unit; 0: the plain kernel
+  int rows;       // of a unit; 0: the plain kernel
   int row_tiles;  // units of a key head
   int ctas;
   int64_t units;
@@ -162,31 +162,72 @@ struct AttnPlan {
   int64_t bytes;  // of workspace
 };
 
-// The tiled kernel is for dims of 64, 128 and 256 (fp32: 64 and 128).  A unit has 16 rows or
-// 32: more than 32 are several units, which read the same keys and values (from the L2).
+// A unit has as many rows as the kernel takes, or the fewest eights that hold them all: more
+// than it takes are several units, which read the same keys and values (from the L2).
 AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   AttnPlan pl{};
+  const int most_rows = hybrid::attn_rows(a->input_dtype, a->dim);
   const int64_t rows = static_cast<int64_t>(a->num_heads / a->num_kv_heads) * a->window;
-  int groups = rows > 16 && hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, 2) != nullptr ? 2 : 1;
-  if (hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, groups) == nullptr) return pl;
-  const int64_t tiles = (rows + 16 * groups - 1) / (16 * groups);
-  if (rows > 0x7FFFFFF0LL || tiles * a->num_kv_heads > 0x7FFFFFFFLL) return pl;
-  pl.groups = groups;
-  pl.row_tiles = static_cast<int>(tiles);
-  pl.units = tiles * a->num_kv_heads * a->pages.requests;
+  if (most_rows == 0 || rows > 0x7FFFFF00LL) return pl;
+  const int64_t row_tiles = (rows + most_rows - 1) / most_rows;
+  if (row_tiles * a->num_kv_heads > 0x7FFFFFFFLL) return pl;
+  pl.row_tiles = static_cast<int>(row_tiles);
+  pl.rows = a->input_dtype == RSM_F32 ? 16 : static_cast<int>(((rows + row_tiles - 1) / row_tiles + 7) / 8 * 8);
+  pl.units = row_tiles * a->num_kv_heads * a->pages.requests;
   const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size;
-  const int64_t most = (longest + hybrid::kAttnTile - 1) / hybrid::kAttnTile;
+  const int64_t most = std::max<int64_t>((longest + hybrid::kAttnTile - 1) / hybrid::kAttnTile, 1);
   pl.split = most > 1;
-  const int64_t resident = static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(input_size(a->input_dtype), a->dim);
-  pl.ctas = static_cast<int>(std::max<int64_t>(1, std::min(resident, most > resident ? resident : pl.units * std::max<int64_t>(most, 1))));
-  if (pl.split) pl.bytes = 2LL * pl.ctas * 16 * groups * (a->dim + 2) * 4;
+  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(input_size(a->input_dtype), a->dim),
+                                             2 * hybrid::kAttnJoinThreads);
+  pl.ctas = static_cast<int>(most >= resident ? resident : std::min(resident, pl.units * most));
+  if (pl.split) pl.bytes = 2LL * pl.ctas * pl.rows * (a->dim + 2) * 4;
   return pl;
 }
 
-int launch_tiles(const rsm_paged_attention_args* a, hybrid::AttnParams& p, const AttnPlan& pl, int dev, void* stream) {
+using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+TensorMapEncodeFn tensor_map_encoder() {
+  static const TensorMapEncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<TensorMapEncodeFn>(nullptr);
+    return reinterpret_cast<TensorMapEncodeFn>(f);
+  }();
+  return fn;
+}
+
+// Tensor maps take strides from 16 bytes to 2^40; a stride that no second element needs is put at the least.
+bool box_stride(int64_t n, int64_t stride, cuuint64_t* out) {
+  *out = n <= 1 ? 16 : static_cast<cuuint64_t>(stride) * 2u;
+  return n <= 1 || (stride > 0 && stride < (int64_t{1} << 38));
+}
+
+// The boxes of 16 rows of one head, 64 columns each, of bf16 pages; false where a map cannot be made.
+bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int kv_heads, int dim, int64_t page, int64_t row, int64_t head) {
+  const TensorMapEncodeFn encode = tensor_map_encoder();
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(kv_heads), static_cast<cuuint64_t>(pg.page_size),
+                              static_cast<cuuint64_t>(pg.num_pages)};
+  cuuint64_t strides[3];
+  if (encode == nullptr || pg.num_pages < 1 || !box_stride(kv_heads, head, &strides[0]) || !box_stride(pg.page_size, row, &strides[1]) ||
+      !box_stride(pg.num_pages, page, &strides[2]))
+    return false;
+  const cuuint32_t box[4] = {64, 1, hybrid::kAttnStep, 1}, ones[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4u, const_cast<void*>(base), dims, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& base, const AttnPlan& pl, int dev, void* stream) {
   if (pl.split && (a->workspace == nullptr || a->workspace_bytes < pl.bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
     return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(pl.bytes));
   const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, a->dim);
+  hybrid::AttnTileParams tp{};
+  tp.p = base;
+  hybrid::AttnParams& p = tp.p;
   p.part = static_cast<float*>(a->workspace);
   p.row_tiles = pl.row_tiles;
   p.ctas = pl.ctas;
@@ -195,35 +236,39 @@ int launch_tiles(const rsm_paged_attention_args* a, hybrid::AttnParams& p, const
     if (a->pages.page_size == 1 << k) p.page_shift = k;
   p.q_pairs = reinterpret_cast<uintptr_t>(a->q) % 4 == 0 && (a->pages.requests == 1 || a->q_batch_stride % 2 == 0) &&
               (a->window == 1 || a->q_stride % 2 == 0);
-  const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, pl.groups);
+  const rsm_pages& pg = a->pages;
+  const bool boxes = a->input_dtype == RSM_BF16 && pg.page_size % hybrid::kAttnStep == 0 &&
+                     page_map(&tp.k_map, pg.k, pg, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
+                     page_map(&tp.v_map, pg.v, pg, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
+  const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, pl.rows, boxes);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    bool& ready = g_attn_ready[dev][a->input_dtype == RSM_F32][a->dim / 128][pl.groups - 1];
+    bool& ready = g_attn_ready[dev][a->input_dtype == RSM_F32][a->dim / 128][pl.rows / 8 - 1][boxes];
     if (!ready) {
       const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
       ready = true;
     }
   }
-  const int rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &p, stream, smem);
+  const int rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
   if (rc != RSM_OK || !pl.split) return rc;
-  // The join's CTAs come while the first kernel's finish, and wait for it.  A CTA of the first
-  // has one unit's first piece at most; where few units are in many pieces, their rows are
-  // shared out.
-  const int64_t pieces = pl.ctas / std::max<int64_t>(pl.units, 1) + 1;
-  const int rows = static_cast<int>(std::min<int64_t>(16 * pl.groups, static_cast<int64_t>(p.per) * p.window));
-  int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, pieces / 2)));
+  // The join's CTAs come while the first kernel's finish, and wait for it.  Where few units
+  // are in many pieces each, their rows are shared out.
+  const int64_t pieces = pl.ctas / pl.units + 1;
+  const int rows = static_cast<int>(std::min<int64_t>(pl.rows, static_cast<int64_t>(p.per) * p.window));
+  int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, pieces / 2))), by_unit = pl.units <= pl.ctas;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.ctas * parts));
+  cfg.gridDim = dim3(static_cast<unsigned>((by_unit ? pl.units : pl.ctas) * parts));
   cfg.blockDim = dim3(hybrid::kAttnJoinThreads);
+  cfg.dynamicSmemBytes = pl.ctas * sizeof(float);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  void* kargs[] = {&p, &parts};
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, hybrid::attn_join_kernel_of(a->input_dtype, a->dim, pl.groups), kargs);
+  void* kargs[] = {&p, &parts, &by_unit};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, hybrid::attn_join_kernel_of(a->input_dtype, a->dim, pl.rows), kargs);
   if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return done();
 }
@@ -370,7 +415,7 @@ int rsm_paged_attention(const rsm_paged_attention_args* a, void* stream) {
     rc = device_sms(&dev, &sms);
     if (rc != RSM_OK) return rc;
     const AttnPlan pl = plan_attention(a, sms);
-    if (pl.groups > 0) return launch_tiles(a, p, pl, dev, stream);
+    if (pl.rows > 0) return launch_tiles(a, p, pl, dev, stream);
   }
   return launch(hybrid::attn_plain_kernel(a->input_dtype), static_cast<int64_t>(a->pages.requests) * a->window * a->num_heads,
                 hybrid::kAttnPlainThreads, &p, stream);

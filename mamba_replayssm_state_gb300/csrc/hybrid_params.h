@@ -1,5 +1,7 @@
 // hybrid_params.h -- what the convolution, rotary, attention and page kernels are given.
 #pragma once
+#include <cuda.h>
+
 #include <cstdint>
 
 #include "../../include/replayssm_hybrid.h"
@@ -61,14 +63,23 @@ struct AttnParams {
 // The tiled kernel: a warp takes kAttnStep tokens at a time, a CTA's four warps kAttnTile; `stages`
 // of them are on the way at once, 96 KB a CTA where two of them share an SM.
 constexpr int kAttnThreads = 128, kAttnStep = 16, kAttnTile = 64, kAttnJoinThreads = 256;
+constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
 constexpr int attn_stages(int esize, int dim) { return esize * dim <= 128 ? 6 : 3; }
 constexpr int attn_smem(int esize, int dim) {
   return attn_stages(esize, dim) * kAttnTile * 2 * dim * esize + (esize == 4 ? 128 * dim : 0);
 }
 constexpr int attn_ctas_per_sm(int esize, int dim) { return attn_smem(esize, dim) > 112 * 1024 ? 1 : 2; }
-// dim 64 and 128, and 256 for bf16; groups of 16 rows, 1 or (bf16, dim up to 128) 2: null otherwise.
-const void* attn_tile_kernel_of(int input_dtype, int dim, int groups);
-const void* attn_join_kernel_of(int input_dtype, int dim, int groups);
+struct AttnTileParams {
+  AttnParams p;
+  CUtensorMap k_map, v_map;  // [pages, page_size, kv heads, dim], boxes of 16 rows of a head, 64 columns
+};
+// Rows of a unit at most: 0 where there is no tiled kernel.  dim 64, 128 and (bf16) 256.
+constexpr int attn_rows(int input_dtype, int dim) {
+  return input_dtype == RSM_F32 ? (dim == 64 || dim == 128 ? 16 : 0) : dim == 64 || dim == 128 ? 32 : dim == 256 ? 16 : 0;
+}
+// rows: of a unit, 16 for fp32 and a multiple of 8 for bf16.  boxes: loads by the tensor maps (bf16).
+const void* attn_tile_kernel_of(int input_dtype, int dim, int rows, bool boxes);
+const void* attn_join_kernel_of(int input_dtype, int dim, int rows);
 
 constexpr int kAttnPlainThreads = 128;
 const void* attn_plain_kernel(int input_dtype);
