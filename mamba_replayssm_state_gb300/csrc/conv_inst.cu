@@ -14,12 +14,12 @@ const void* pick(int width) {
   }
 }
 
-template <typename IT, int V, int N>
+template <typename IT, int V>
 const void* pick_step(int width) {
   switch (width) {
-    case 2: return reinterpret_cast<const void*>(&conv_step_kernel<IT, 2, V, N>);
-    case 3: return reinterpret_cast<const void*>(&conv_step_kernel<IT, 3, V, N>);
-    default: return reinterpret_cast<const void*>(&conv_step_kernel<IT, 4, V, N>);
+    case 2: return reinterpret_cast<const void*>(&conv_step_kernel<IT, 2, V>);
+    case 3: return reinterpret_cast<const void*>(&conv_step_kernel<IT, 3, V>);
+    default: return reinterpret_cast<const void*>(&conv_step_kernel<IT, 4, V>);
   }
 }
 
@@ -30,13 +30,9 @@ const void* conv_kernel(int input_dtype, int width, bool vec) {
   return vec ? pick<float, 4>(width) : pick<float, 1>(width);
 }
 
-const void* conv_step_kernel(int input_dtype, int width, bool vec, int requests) {
-  if (input_dtype == RSM_BF16) {
-    if (!vec) return pick_step<uint16_t, 1, 1>(width);
-    return requests == 1 ? pick_step<uint16_t, 8, 1>(width) : pick_step<uint16_t, 8, 2>(width);
-  }
-  if (!vec) return pick_step<float, 1, 1>(width);
-  return requests == 1 ? pick_step<float, 4, 1>(width) : pick_step<float, 4, 2>(width);
+const void* conv_step_kernel_of(int input_dtype, int width, bool vec) {
+  if (input_dtype == RSM_BF16) return vec ? pick_step<uint16_t, 8>(width) : pick_step<uint16_t, 1>(width);
+  return vec ? pick_step<float, 4>(width) : pick_step<float, 1>(width);
 }
 
 }  // namespace hybrid

@@ -51,6 +51,24 @@ int launch(const void* fn, int64_t grid, int threads, const void* params, void* 
   return done();
 }
 
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_sms[kMaxDevices];
+bool g_attn_ready[kMaxDevices][2][3][4][2];  // input type, dim 64, 128, 256, eights of rows, boxes
+
+int device_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (*dev < 0 || *dev >= kMaxDevices) return fail(RSM_ECUDA, "device ordinal %d out of range", *dev);
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_sms[*dev] == 0) {
+    e = cudaDeviceGetAttribute(&g_sms[*dev], cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) return fail(RSM_ECUDA, "device query failed: %s", cudaGetErrorString(e));
+  }
+  *sms = g_sms[*dev];
+  return RSM_OK;
+}
+
 // Rows of a tensor start on 16 bytes; a stride that no second row needs is not looked at.
 bool rows_fit(const void* base, int es, int64_t n0, int64_t s0, int64_t n1 = 1, int64_t s1 = 0, int64_t n2 = 1, int64_t s2 = 0) {
   return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (n0 <= 1 || s0 * es % 16 == 0) && (n1 <= 1 || s1 * es % 16 == 0) &&
@@ -132,24 +150,6 @@ int validate(const rsm_paged_attention_args* a, bool pointers) {
     if (rc == RSM_OK) rc = need_pages(a->pages);
   }
   return rc;
-}
-
-constexpr int kMaxDevices = 64;
-std::mutex g_mu;
-int g_sms[kMaxDevices];
-bool g_attn_ready[kMaxDevices][2][3][4][2];  // input type, dim 64, 128, 256, eights of rows, boxes
-
-int device_sms(int* dev, int* sms) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  if (*dev < 0 || *dev >= kMaxDevices) return fail(RSM_ECUDA, "device ordinal %d out of range", *dev);
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_sms[*dev] == 0) {
-    e = cudaDeviceGetAttribute(&g_sms[*dev], cudaDevAttrMultiProcessorCount, *dev);
-    if (e != cudaSuccess) return fail(RSM_ECUDA, "device query failed: %s", cudaGetErrorString(e));
-  }
-  *sms = g_sms[*dev];
-  return RSM_OK;
 }
 
 // How a call runs on the tiled kernel.
@@ -298,7 +298,12 @@ int rsm_causal_conv(const rsm_causal_conv_args* a, void* stream) {
   const bool vec = conv_vec(p, a->input_dtype, a->width);
   const int per = hybrid::kConvThreads * hybrid::conv_channels(a->input_dtype, vec);
   p.cblocks = (a->channels + per - 1) / per;
-  const int64_t blocks = (a->tokens + hybrid::kConvTokens - 1) / hybrid::kConvTokens;
+  int dev = 0, sms = 0;
+  rc = device_sms(&dev, &sms);
+  if (rc != RSM_OK) return rc;
+  // few tokens: blocks of eight, for the shortest way through; many: of 32, which read three rows twice
+  p.block = a->tokens * p.cblocks >= 32LL * 8 * sms ? 32 : 8;
+  const int64_t blocks = (a->tokens + p.block - 1) / p.block;
   return launch(hybrid::conv_kernel(a->input_dtype, a->width, vec), blocks * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
 
@@ -324,10 +329,13 @@ int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
   const bool vec = conv_vec(p, a->input_dtype, a->width);
   const int per = hybrid::kConvThreads * hybrid::conv_channels(a->input_dtype, vec);
   p.cblocks = (a->channels + per - 1) / per;
-  const int requests = vec && static_cast<int64_t>(a->batch) * p.cblocks > 1024 ? 2 : 1;
-  const int64_t groups = (a->batch + requests - 1) / requests;
-  return launch(hybrid::conv_step_kernel(a->input_dtype, a->width, vec, requests), groups * p.cblocks, hybrid::kConvThreads, &p,
-                stream);
+  int dev = 0, sms = 0;
+  rc = device_sms(&dev, &sms);
+  if (rc != RSM_OK) return rc;
+  // as many requests a CTA as leave four CTAs an SM
+  p.block = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(hybrid::kConvStepRequests, static_cast<int64_t>(a->batch) * p.cblocks / (4 * sms))));
+  const int64_t groups = (a->batch + p.block - 1) / p.block;
+  return launch(hybrid::conv_step_kernel_of(a->input_dtype, a->width, vec), groups * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
 
 int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
@@ -374,7 +382,11 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   const bool vec = a->dim % v == 0 && (a->interleaved ? a->rotary_dim : p.half) % v == 0 && rows_fit(p.q, es, b, p.q_bs, n, p.q_ts) &&
                    rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
                    rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads);
-  p.block_tokens = p.tokens >= 4096 ? 4 : 1;
+  // as many tokens a CTA as leave eight CTAs an SM
+  int dev = 0, sms = 0;
+  rc = device_sms(&dev, &sms);
+  if (rc != RSM_OK) return rc;
+  p.block_tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, p.tokens / (8 * sms))));
   return launch(hybrid::rotary_kernel(a->input_dtype, vec), (p.tokens + p.block_tokens - 1) / p.block_tokens, hybrid::kRotaryThreads, &p,
                 stream);
 }

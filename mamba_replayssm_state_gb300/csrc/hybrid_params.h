@@ -19,15 +19,15 @@ struct ConvParams {
   int64_t tokens, x_bs, x_ts, out_ts, cache_ss;
   int32_t seqs, window, num_slots, C, R, silu, pad;
   int32_t cblocks;  // CTAs across the channels
+  int32_t block;    // tokens, or requests, of a CTA
 };
 
 constexpr int kConvThreads = 128;
-constexpr int kConvTokens = 32;  // tokens of a CTA of the prompts' kernel
+constexpr int kConvStepRequests = 16;  // of a CTA at most
 
 // vec: eight bf16 or four fp32 channels a thread, on 16 bytes; else one channel.
 const void* conv_kernel(int input_dtype, int width, bool vec);
-// requests: of a thread, 1 or 2
-const void* conv_step_kernel(int input_dtype, int width, bool vec, int requests);
+const void* conv_step_kernel_of(int input_dtype, int width, bool vec);
 constexpr int conv_channels(int input_dtype, bool vec) { return !vec ? 1 : input_dtype == RSM_BF16 ? 8 : 4; }
 
 struct RotaryParams {

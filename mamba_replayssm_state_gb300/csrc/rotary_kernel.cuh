@@ -8,8 +8,9 @@
 // 2^-32 turns, and the upper 32 bits are what sine and cosine are taken of.
 //
 // Memory bounds it: q, k, v read once and written once.  A CTA takes a few tokens,
-// makes their sines and cosines once for all heads, and then moves 16 bytes (twice
-// that for two halves of a head) a thread at a time.
+// makes their sines and cosines once for all heads, and then a thread moves the same 16
+// bytes (twice that for two halves of a head) of one token after the other, four of them on
+// their way at a time.
 #pragma once
 #include "hybrid_device.cuh"
 
@@ -34,7 +35,7 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
 }
 
 template <typename IT, int V>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotaryThreads, 4) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
   __shared__ RotaryToken token[kRotaryMaxTokens];
   __shared__ uint64_t step[kRotaryMaxHalf];
   __shared__ float2 turn[kRotaryMaxTokens * kRotaryMaxHalf];
@@ -93,78 +94,76 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
   __syncthreads();
 
   // A head's parts: those that turn (V pairs from two halves, or V / 2 neighbouring
-  // ones), then those that are copied; a value head is copied whole.
-  const bool near = V > 1 && p.interleaved;
+  // ones), then those that are copied; a value head is copied whole.  A thread takes one part
+  // of a head for all the tokens, T of them at a time.
+  const bool near = V > 1 && p.interleaved, near_one = V == 1 && p.interleaved;
   const uint32_t turning = V > 1 ? (near ? 2 * p.half / V : p.half / V) : p.half;
   const uint32_t parts = turning + (p.dim - 2 * p.half) / V, copied = p.dim / V;
   const uint32_t heads = (p.H + p.G) * parts, per = heads + p.G * copied;
-  for (uint32_t i = threadIdx.x; i < nt * per; i += kRotaryThreads) {
-    const uint32_t t = i / per;
-    uint32_t r = i - t * per;
-    const RotaryToken& k = token[t];
-    if (k.live == 0) continue;
-    if (r >= heads) {
-      r -= heads;
-      if (k.v_row < 0) continue;
-      const uint32_t g = r / copied, part = r - g * copied;
-      Row<IT, V> row;
-      row.load(static_cast<const IT*>(p.v) + k.v + static_cast<int64_t>(g) * p.dim + part * V);
-      row.store(static_cast<IT*>(pg.v) + k.v_row + g * pg.v_head_stride + part * V);
-      continue;
-    }
-    const uint32_t h = r / parts, part = r - h * parts;
-    const bool key = h >= static_cast<uint32_t>(p.H);
-    if (key && k.k_row < 0) continue;
-    const IT* from = key ? static_cast<const IT*>(p.k) + k.k + static_cast<int64_t>(h - p.H) * p.dim
-                         : static_cast<const IT*>(p.q) + k.q + static_cast<int64_t>(h) * p.dim;
-    IT* to = key ? static_cast<IT*>(pg.k) + k.k_row + (h - p.H) * pg.k_head_stride
-                 : static_cast<IT*>(p.q_out) + k.out + static_cast<int64_t>(h) * p.dim;
-    const float2* cs = turn + t * p.half;
-    Row<IT, V> a, b;
-    if (k.live == 1) {  // a skipped request's queries
-      a.zero();
-      if (part >= turning) {
-        a.store(to + 2 * p.half + (part - turning) * V);
-      } else if (near) {
-        a.store(to + part * V);
-      } else {
-        const uint32_t ca = V == 1 && p.interleaved ? 2 * part : part * V;
-        a.store(to + ca);
-        a.store(to + (V == 1 && p.interleaved ? ca + 1 : ca + p.half));
-      }
-    } else if (part >= turning) {
-      a.load(from + 2 * p.half + (part - turning) * V);
-      a.store(to + 2 * p.half + (part - turning) * V);
-    } else if (near) {
-      float x[V], y[V];
-      a.load(from + part * V);
-      a.values(x);
+  for (uint32_t i = threadIdx.x; i < per; i += kRotaryThreads) {
+    const bool value = i >= heads;
+    const uint32_t in = value ? i - heads : i, h = in / (value ? copied : parts), part = in - h * (value ? copied : parts);
+    const bool key = !value && h >= static_cast<uint32_t>(p.H);
+    const uint32_t g = key ? h - p.H : h;
+    const bool turns = !value && part < turning;
+    // columns of the part, and of its other half
+    const uint32_t ca = value ? part * V : !turns ? 2 * p.half + (part - turning) * V : near_one ? 2 * part : part * V;
+    const uint32_t cb = near_one ? ca + 1 : ca + p.half;
+    const bool two = turns && !near;
+    const IT* const from = (value ? static_cast<const IT*>(p.v) : key ? static_cast<const IT*>(p.k) : static_cast<const IT*>(p.q)) +
+                           static_cast<int64_t>(g) * p.dim;
+    IT* const to = value ? static_cast<IT*>(pg.v) + g * pg.v_head_stride
+                   : key ? static_cast<IT*>(pg.k) + g * pg.k_head_stride
+                         : static_cast<IT*>(p.q_out) + static_cast<int64_t>(g) * p.dim;
+    auto source = [&](const RotaryToken& k) { return value ? k.v : key ? k.k : k.q; };
+    auto target = [&](const RotaryToken& k) { return value ? k.v_row : key ? k.k_row : k.live == 0 ? -1 : k.out; };
+    constexpr int T = 4;
+    for (int t0 = 0; t0 < nt; t0 += T) {
+      Row<IT, V> a[T], b[T];
 #pragma unroll
-      for (int j = 0; j + 1 < V; j += 2) {
-        const float2 w = cs[part * (V / 2) + j / 2];
-        y[j] = x[j] * w.x - x[j + 1] * w.y;
-        y[j + 1] = x[j + 1] * w.x + x[j] * w.y;
-      }
-      a.round(y);
-      a.store(to + part * V);
-    } else {
-      const uint32_t ca = V == 1 && p.interleaved ? 2 * part : part * V;
-      const uint32_t cb = V == 1 && p.interleaved ? ca + 1 : ca + p.half;
-      float x[V], y[V], u[V], v[V];
-      a.load(from + ca);
-      b.load(from + cb);
-      a.values(x);
-      b.values(y);
+      for (int t = 0; t < T; ++t)
+        if (t0 + t < nt) {
+          const RotaryToken& k = token[t0 + t];
+          if (k.live == 2) {
+            a[t].load(from + source(k) + ca);
+            if (two) b[t].load(from + source(k) + cb);
+          } else {
+            a[t].zero();  // a skipped request's queries
+            b[t].zero();
+          }
+        }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 w = cs[part * V + j];
-        u[j] = x[j] * w.x - y[j] * w.y;
-        v[j] = y[j] * w.x + x[j] * w.y;
-      }
-      a.round(u);
-      b.round(v);
-      a.store(to + ca);
-      b.store(to + cb);
+      for (int t = 0; t < T; ++t)
+        if (t0 + t < nt) {
+          const int64_t row = target(token[t0 + t]);
+          if (row < 0) continue;
+          if (turns) {
+            float x[V], y[V], u[V], v[V];
+            const float2* cs = turn + (t0 + t) * p.half;
+            a[t].values(x);
+            if (near) {
+#pragma unroll
+              for (int j = 0; j + 1 < V; j += 2) {
+                const float2 w = cs[part * (V / 2) + j / 2];
+                u[j] = x[j] * w.x - x[j + 1] * w.y;
+                u[j + 1] = x[j + 1] * w.x + x[j] * w.y;
+              }
+              a[t].round(u);
+            } else {
+              b[t].values(y);
+#pragma unroll
+              for (int j = 0; j < V; ++j) {
+                const float2 w = cs[part * V + j];
+                u[j] = x[j] * w.x - y[j] * w.y;
+                v[j] = y[j] * w.x + x[j] * w.y;
+              }
+              a[t].round(u);
+              b[t].round(v);
+              b[t].store(to + row + cb);
+            }
+          }
+          a[t].store(to + row + ca);
+        }
     }
   }
 }
