@@ -117,11 +117,6 @@ struct Deal {
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool yes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(yes ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // The box of 16 tokens and 128 bytes at (column, head, row, page).
 __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int column, int head, int row, int page, uint32_t bar) {

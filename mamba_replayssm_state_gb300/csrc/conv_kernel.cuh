@@ -7,9 +7,12 @@
 // instructions for 32 bytes, so these are kept few: channels in pairs (fma.rn.f32x2),
 // the fast exponential and reciprocal without the handling of denormals, whole groups
 // of tokens without a test in between.  A thread keeps its channels' weights and last
-// W-1 inputs in registers and walks along the tokens, the next ones' loads on their way.
+// W-1 inputs in registers and walks along the tokens.  The rows to come lie in shared memory, or are
+// on their way there (cp.async), each in a place that only its thread writes and reads: no barriers,
+// and more bytes in flight than registers would hold.
 #pragma once
 #include "hybrid_device.cuh"
+#include "rsm_ptx.cuh"
 
 namespace hybrid {
 
@@ -27,6 +30,16 @@ struct Lanes {
   __device__ __forceinline__ static T fma(T a, T b, T c) {
     T r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+  }
+  __device__ __forceinline__ static T mul(T a, T b) {
+    T r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+  }
+  __device__ __forceinline__ static T add(T a, T b) {
+    T r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
   }
   __device__ __forceinline__ static void from(const float (&f)[V], T (&t)[N]) {
@@ -47,19 +60,44 @@ struct Lanes<1> {
   __device__ __forceinline__ static void to(const T (&t)[1], float (&f)[1]) { f[0] = t[0]; }
 };
 
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp2_ftz(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // silu(v); for bf16 by the fast exponential and reciprocal, within 2^-17 for |v| < 80, far below
 // the output's own 2^-9.
 template <typename IT>
 __device__ __forceinline__ float silu(float v) {
-  if constexpr (sizeof(IT) == 2) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504088896340736f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return v * r;
-  } else {
+  if constexpr (sizeof(IT) == 2)
+    return v * rcp_ftz(1.0f + exp2_ftz(v * -kLog2e));
+  else
     return v / (1.0f + expf(-v));
-  }
 }
+
+// A thread's own places in shared memory, 16 bytes each, [place][thread].
+struct Places {
+  uint32_t base;
+  __device__ __forceinline__ explicit Places(const void* smem) : base(rsm::smem_addr(smem) + threadIdx.x * 16) {}
+  __device__ __forceinline__ uint32_t at(int place) const { return base + place * (kConvThreads * 16); }
+  template <typename T>
+  __device__ __forceinline__ void ask(int place, const T* from) const {
+    rsm::cp_async_16(at(place), from);
+  }
+  template <typename R>
+  __device__ __forceinline__ R get(int place) const {
+    R r;
+    *reinterpret_cast<uint4*>(r.v) = rsm::lds128(at(place));
+    return r;
+  }
+};
 
 template <int W, int V>
 struct Taps {
@@ -123,10 +161,24 @@ __device__ __forceinline__ Row<IT, V> conv_token(const Taps<W, V>& k, Past<W, V>
     for (int j = W - 2; j >= 1; --j) h.v[j][i] = h.v[j - 1][i];
     h.v[0][i] = x[i];
   }
-  L::to(y, f);
   if (act) {
+    if constexpr (V > 1 && sizeof(IT) == 2) {
+      const uint64_t scale = L::make(-kLog2e, -kLog2e), one = L::make(1.0f, 1.0f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = silu<IT>(f[i]);
+      for (int i = 0; i < L::N; ++i) {  // silu() of two at a time
+        float a, b;
+        L::split(L::mul(y[i], scale), a, b);
+        L::split(L::add(L::make(exp2_ftz(a), exp2_ftz(b)), one), a, b);
+        y[i] = L::mul(y[i], L::make(rcp_ftz(a), rcp_ftz(b)));
+      }
+      L::to(y, f);
+    } else {
+      L::to(y, f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = silu<IT>(f[i]);
+    }
+  } else {
+    L::to(y, f);
   }
   Row<IT, V> out;
   out.round(f);
@@ -134,13 +186,15 @@ __device__ __forceinline__ Row<IT, V> conv_token(const Taps<W, V>& k, Past<W, V>
 }
 
 // Packed prompts: a CTA takes p.block tokens of kConvThreads * V channels, four tokens at
-// a time.  The first W - 1 tokens of a sequence belong to the CTA in which it
-// starts, which so is the only one to look into the cache and to store there: it reads
-// before it writes.
+// a time, kConvAhead on their way.  The first W - 1 tokens of a sequence belong to the CTA in
+// which it starts, which so is the only one to look into the cache and to store
+// there: it reads before it writes.
 template <typename IT, int W, int V>
-__global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kernel(const __grid_constant__ ConvParams p) {
-  constexpr int U = 4;  // tokens at a time
+__global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 5) conv_prompt_kernel(const __grid_constant__ ConvParams p) {
+  constexpr int U = 4;
   constexpr int64_t kNever = int64_t{1} << 62;
+  static_assert(kConvAhead % U == 0);
+  __shared__ __align__(16) uint4 ring[V == 1 ? 1 : kConvAhead * kConvThreads];
   const uint32_t block = blockIdx.x / static_cast<uint32_t>(p.cblocks), cb = blockIdx.x - block * static_cast<uint32_t>(p.cblocks);
   const int64_t first = static_cast<int64_t>(block) * p.block, last = min(first + p.block, p.tokens);
   const int64_t c = (static_cast<int64_t>(cb) * kConvThreads + threadIdx.x) * V;
@@ -148,10 +202,20 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
   const IT* const x = static_cast<const IT*>(p.x) + c;
   IT* const out = static_cast<IT*>(p.out) + c;
   // what does not depend on the sequences is on its way before they are looked up
-  Row<IT, V> next[U], before[W - 1];
+  const Places place(ring);
+  auto ask = [&](int64_t t, int at) {  // tokens t .. t + U - 1 to the places from `at`
+    if constexpr (V > 1) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (mine && first + u < last) next[u].load(x + (first + u) * p.x_ts);
+      for (int u = 0; u < U; ++u)
+        if (t + u < last) place.ask(at + u, x + (t + u) * p.x_ts);
+      cp_async_commit();
+    }
+  };
+  if (mine) {
+#pragma unroll
+    for (int k = 0; k < kConvAhead; k += U) ask(first + k, k);
+  }
+  Row<IT, V> before[W - 1];
 #pragma unroll
   for (int j = 1; j < W; ++j) {
     before[j - 1].zero();
@@ -216,95 +280,140 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
     if (t >= own) y.store(out + t * p.out_ts);
   };
   advance(first);
+  int at = 0;
   for (int64_t t = first; t < last; t += U) {
-    Row<IT, V> in[U];
+    if constexpr (V > 1) cp_async_wait<kConvAhead / U - 1>();
+    if (V > 1 && t > s0 && t >= own && t + U <= min(s1, last)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) in[u] = next[u];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + U + u < last) next[u].load(x + (t + U + u) * p.x_ts);
-    if (t > s0 && t >= own && t + U <= min(s1, last)) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) conv_token<IT, W, V>(taps, h, in[u], act).store(out + (t + u) * p.out_ts);
+      for (int u = 0; u < U; ++u)
+        conv_token<IT, W, V>(taps, h, place.get<Row<IT, V>>(at + u), act).store(out + (t + u) * p.out_ts);
     } else {
       for (int64_t i = t; i < min(t + U, last); ++i) one(i);
     }
+    ask(t + kConvAhead, at);
+    at = at + U == kConvAhead ? 0 : at + U;
   }
+  if constexpr (V > 1) cp_async_wait<0>();
   // the rest of the first W - 1 tokens of a sequence that starts here
   if (own == s0)
     for (int64_t t = last; t < min(s1, s0 + (W - 1)); ++t) one(t);
 }
 
-// New tokens: a CTA takes p.block requests one after the other, the next one's loads on
-// their way.  Rows that are written are none that a window looks back to (R >= W - 1 + window).
+// New tokens: a CTA takes p.block requests one after the other, in items of up to U tokens,
+// the next two items' rows on their way.  Rows that are written are none that a window
+// looks back to (R >= W - 1 + window).
 template <typename IT, int W, int V>
 __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_step_kernel(const __grid_constant__ ConvParams p) {
-  __shared__ int slot_s[kConvStepRequests];
-  __shared__ int pos_s[kConvStepRequests];
+  constexpr int U = 4, kRows = W - 1 + U, kItems = 3;
+  struct Request {
+    int64_t back[W - 1];  // offsets in the cache of the rows before, -1: none
+    int64_t slot;         // of the slot, -1: skipped
+    uint32_t row;         // of the first token
+  };
+  __shared__ Request request[kConvStepRequests];
+  __shared__ __align__(16) uint4 ring[V == 1 ? 1 : kItems * kRows * kConvThreads];
   const uint32_t group = blockIdx.x / static_cast<uint32_t>(p.cblocks), cb = blockIdx.x - group * static_cast<uint32_t>(p.cblocks);
   const int64_t c = (static_cast<int64_t>(cb) * kConvThreads + threadIdx.x) * V, b0 = static_cast<int64_t>(group) * p.block;
   const int count = static_cast<int>(min(static_cast<int64_t>(p.block), p.seqs - b0));
   const uint32_t R = static_cast<uint32_t>(p.R);
+  const IT* const x = static_cast<const IT*>(p.x) + b0 * p.x_bs + c;
+  IT* const out = static_cast<IT*>(p.out) + b0 * p.window * p.out_ts + c;
+  IT* const cache = static_cast<IT*>(p.cache) + c;
+  const bool mine = c < p.C;
   if (static_cast<int>(threadIdx.x) < count) {
-    int slot = p.slots[b0 + threadIdx.x];
-    const int pos = p.positions[b0 + threadIdx.x];
+    Request r;
+    const int slot = p.slots[b0 + threadIdx.x], pos = p.positions[b0 + threadIdx.x];
+    r.slot = -1;
+    r.row = 0;
     if (slot == p.pad) {
-      slot = -1;
     } else if (slot < 0 || slot >= p.num_slots || pos < 0) {
       if (cb == 0) flag(p.status, slot < 0 || slot >= p.num_slots ? RSM_STATUS_BAD_SLOT : RSM_STATUS_BAD_POSITION);
-      slot = -1;
+    } else {
+      r.slot = slot * p.cache_ss;
+      r.row = static_cast<uint32_t>(pos) % R;
     }
-    slot_s[threadIdx.x] = slot;
-    pos_s[threadIdx.x] = pos;
-  }
-  __syncthreads();
-  if (c >= p.C) return;
-  const IT* const x = static_cast<const IT*>(p.x) + b0 * p.x_bs + c;
-  IT* out = static_cast<IT*>(p.out) + b0 * p.window * p.out_ts + c;
-  IT* const cache = static_cast<IT*>(p.cache) + c;
-  Row<IT, V> back[W - 1], in;
-  auto ask = [&](int n) {
-    const int slot = slot_s[n];
-    if (slot < 0) return;
-    const uint32_t pos = static_cast<uint32_t>(pos_s[n]);
-    in.load(x + n * p.x_bs);
-    uint32_t row = pos % R;
+    uint32_t row = r.row;
 #pragma unroll
     for (int j = 1; j < W; ++j) {
       row = row == 0 ? R - 1 : row - 1;
-      back[j - 1].zero();
-      if (pos >= static_cast<uint32_t>(j)) back[j - 1].load(cache + slot * p.cache_ss + static_cast<int64_t>(row) * p.C);
+      r.back[j - 1] = r.slot >= 0 && pos >= j ? r.slot + static_cast<int64_t>(row) * p.C : -1;
+    }
+    request[threadIdx.x] = r;
+  }
+  Taps<W, V> taps;
+  if (mine) taps.load(p.weight, p.bias, static_cast<int>(c));
+  __syncthreads();
+  if (!mine) return;
+  const bool act = p.silu != 0;
+  const Places place(ring);
+  const int chunks = (p.window + U - 1) / U;
+  // item: chunk k of request n; asked for in order
+  int ask_n = 0, ask_k = 0, ask_at = 0;
+  auto ask = [&]() {
+    if constexpr (V > 1) {
+      if (ask_n < count && request[ask_n].slot >= 0) {
+        if (ask_k == 0) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+            if (request[ask_n].back[j] >= 0) place.ask(ask_at + j, cache + request[ask_n].back[j]);
+        }
+        const IT* from = x + ask_n * p.x_bs + ask_k * U * p.x_ts;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (ask_k * U + u < p.window) place.ask(ask_at + W - 1 + u, from + u * p.x_ts);
+      }
+      cp_async_commit();
+      if (++ask_k == chunks) ask_k = 0, ++ask_n;
+      ask_at = ask_at + kRows == kItems * kRows ? 0 : ask_at + kRows;
     }
   };
-  ask(0);
-  Taps<W, V> taps;
-  taps.load(p.weight, p.bias, static_cast<int>(c));
-  const bool act = p.silu != 0;
-  for (int n = 0; n < count; ++n, out += p.window * p.out_ts) {
-    const int slot = slot_s[n];
-    Past<W, V> h;
-    Row<IT, V> now = in;
-    if (slot >= 0) {
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) h.set(j, back[j]);
-    }
-    if (n + 1 < count) ask(n + 1);
-    if (slot < 0) {
-      Row<IT, V> none;
-      none.zero();
-      for (int t = 0; t < p.window; ++t) none.store(out + t * p.out_ts);
-      continue;
-    }
-    uint32_t row = static_cast<uint32_t>(pos_s[n]) % R;
-    IT* const rows = cache + slot * p.cache_ss;
-    for (int t = 0; t < p.window; ++t) {
-      const Row<IT, V> cur = now;
-      if (t + 1 < p.window) now.load(x + n * p.x_bs + (t + 1) * p.x_ts);
-      cur.store(rows + static_cast<int64_t>(row) * p.C);
-      row = row + 1 == R ? 0 : row + 1;
-      conv_token<IT, W, V>(taps, h, cur, act).store(out + t * p.out_ts);
+  for (int i = 0; i < kItems - 1; ++i) ask();
+  int at = 0;
+  for (int n = 0; n < count; ++n) {
+    const int64_t slot = request[n].slot;
+    IT* y = out + n * p.window * p.out_ts;
+    uint32_t row = request[n].row;
+    Past<W, V> h;
+    for (int k = 0; k < chunks; ++k) {
+      ask();
+      if constexpr (V > 1) cp_async_wait<kItems - 1>();
+      if (k == 0) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          Row<IT, V> r;
+          r.zero();
+          if (request[n].back[j] >= 0) {
+            if constexpr (V > 1)
+              r = place.get<Row<IT, V>>(at + j);
+            else
+              r.load(cache + request[n].back[j]);
+          }
+          h.set(j, r);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k * U + u >= p.window) break;
+        Row<IT, V> in;
+        if (slot < 0) {
+          in.zero();
+          in.store(y);
+        } else {
+          if constexpr (V > 1)
+            in = place.get<Row<IT, V>>(at + W - 1 + u);
+          else
+            in.load(x + n * p.x_bs + (k * U + u) * p.x_ts);
+          in.store(cache + slot + static_cast<int64_t>(row) * p.C);
+          row = row + 1 == R ? 0 : row + 1;
+          conv_token<IT, W, V>(taps, h, in, act).store(y);
+        }
+        y += p.out_ts;
+      }
+      at = at + kRows == kItems * kRows ? 0 : at + kRows;
     }
   }
+  if constexpr (V > 1) cp_async_wait<0>();
 }
 
 }  // namespace hybrid

@@ -301,8 +301,8 @@ int rsm_causal_conv(const rsm_causal_conv_args* a, void* stream) {
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  // few tokens: blocks of eight, for the shortest way through; many: of 32, which read three rows twice
-  p.block = a->tokens * p.cblocks >= 32LL * 8 * sms ? 32 : 8;
+  // few tokens: blocks of eight, for the shortest way through; many: of 64, of which three rows are read twice
+  p.block = a->tokens * p.cblocks >= 64LL * 5 * sms ? 64 : 8;
   const int64_t blocks = (a->tokens + p.block - 1) / p.block;
   return launch(hybrid::conv_kernel(a->input_dtype, a->width, vec), blocks * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
@@ -332,8 +332,8 @@ int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  // as many requests a CTA as leave four CTAs an SM
-  p.block = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(hybrid::kConvStepRequests, static_cast<int64_t>(a->batch) * p.cblocks / (4 * sms))));
+  // as many requests a CTA as bring all CTAs onto the SMs at once, four each
+  p.block = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(hybrid::kConvStepRequests, (static_cast<int64_t>(a->batch) * p.cblocks + 4 * sms - 1) / (4 * sms))));
   const int64_t groups = (a->batch + p.block - 1) / p.block;
   return launch(hybrid::conv_step_kernel_of(a->input_dtype, a->width, vec), groups * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
@@ -382,13 +382,11 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   const bool vec = a->dim % v == 0 && (a->interleaved ? a->rotary_dim : p.half) % v == 0 && rows_fit(p.q, es, b, p.q_bs, n, p.q_ts) &&
                    rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
                    rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads);
-  // as many tokens a CTA as leave eight CTAs an SM
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  p.block_tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, p.tokens / (8 * sms))));
-  return launch(hybrid::rotary_kernel(a->input_dtype, vec), (p.tokens + p.block_tokens - 1) / p.block_tokens, hybrid::kRotaryThreads, &p,
-                stream);
+  return launch(hybrid::rotary_kernel(a->input_dtype, vec), std::min<int64_t>(p.tokens, hybrid::kRotaryCtas * sms), hybrid::kRotaryThreads,
+                &p, stream);
 }
 
 int64_t rsm_paged_attention_workspace(const rsm_paged_attention_args* a) {

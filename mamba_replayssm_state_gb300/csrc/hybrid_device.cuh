@@ -18,6 +18,12 @@ __device__ __forceinline__ float get(const uint16_t* p) { return __uint_as_float
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(rsm::pack_bf16x2(v, 0.0f)); }
 
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // V neighbouring values as they lie in memory: one, or 16 bytes.
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Row {

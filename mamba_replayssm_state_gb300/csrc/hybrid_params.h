@@ -23,6 +23,7 @@ struct ConvParams {
 };
 
 constexpr int kConvThreads = 128;
+constexpr int kConvAhead = 16;         // tokens whose rows are on their way, prompts
 constexpr int kConvStepRequests = 16;  // of a CTA at most
 
 // vec: eight bf16 or four fp32 channels a thread, on 16 bytes; else one channel.
@@ -40,10 +41,9 @@ struct RotaryParams {
   int64_t tokens, q_bs, q_ts, k_bs, k_ts, v_bs, v_ts, out_bs, out_ts;
   int32_t window, H, G, dim, half, interleaved;  // half: rotary_dim / 2
   float amplitude;
-  int32_t block_tokens;  // tokens of a CTA
 };
 
-constexpr int kRotaryThreads = 256;
+constexpr int kRotaryThreads = 288, kRotaryCtas = 3;  // CTAs an SM
 const void* rotary_kernel(int input_dtype, bool vec);
 
 struct AttnParams {
