@@ -9,9 +9,9 @@
 // each streams 16 tokens at a time through shared memory of its own, S stages ahead
 // (boxes of 16 rows by TMA where pages are whole groups of 16 tokens, else cp.async):
 // no barrier of the CTA holds a load back, and warps are joined only at the end of
-// a request's part.  The running maximum is one only to within 2^8: sums and outputs are
-// scaled anew where a score passes it by more, which takes a few steps of a request
-// instead of most.
+// a request's part.  The running maximum is one only to within 2^8: it is taken, and sums and
+// outputs scaled anew, where a score passes it by more, which takes a few steps of a
+// request instead of all.
 //
 // The products are m16n8k16 (bf16) and m16n8k8 (tf32) instructions on registers: with a
 // few rows a 128-row tcgen05 tile would be mostly empty.  bf16 takes the products the other
@@ -184,6 +184,7 @@ __device__ __forceinline__ int value_chunk(int token, int chunk) {
 }
 
 constexpr float kAttnSlack = 8.0f;
+constexpr float kAttnLowest = -3.402823466e38f;  // a maximum of nothing: no difference with it is NaN
 constexpr uint64_t kAttnTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
 
 template <typename IT, int DIM>
@@ -289,7 +290,7 @@ struct AttnBf16 {
     for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kAttnLowest;
       l[n][0] = l[n][1] = 0.0f;
     }
   }
@@ -335,10 +336,9 @@ struct AttnBf16 {
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float v = part[0][n][e];
+        s[n][e] = part[0][n][e];
 #pragma unroll
-        for (int c = 1; c < kChains; ++c) v += part[c][n][e];
-        s[n][e] = v * p.scale_log2;
+        for (int c = 1; c < kChains; ++c) s[n][e] += part[c][n][e];
       }
     if (a.differ || a.seen != (1u << kAttnStep) - 1u) {
 #pragma unroll
@@ -346,35 +346,37 @@ struct AttnBf16 {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = quad + 8 * (e >> 1);
-          if (!(a.seen >> j & 1u) || a.token0 + j > limit[n][e & 1]) s[n][e] = -INFINITY;
+          if (!(a.seen >> j & 1u) || a.token0 + j > limit[n][e & 1]) s[n][e] = p.hidden;
         }
     }
-    bool moved = false;
-    float keep[N][2];
+    bool above = false;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(s[n][e], s[n][e + 2]);
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        const float next = top > m[n][e] + kAttnSlack ? top : m[n][e], base = next == -INFINITY ? 0.0f : next;
-        keep[n][e] = exp2_fast(m[n][e] - base);
-        moved |= next != m[n][e];
-        m[n][e] = next;
-        s[n][e] = exp2_fast(s[n][e] - base);
-        s[n][e + 2] = exp2_fast(s[n][e + 2] - base);
-        l[n][e] = fmaf(l[n][e], keep[n][e], s[n][e] + s[n][e + 2]);
-      }
-    if (__any_sync(0xFFFFFFFFu, moved)) {
+      for (int e = 0; e < 4; ++e) above |= fmaf(s[n][e], p.scale_log2, -m[n][e & 1]) > kAttnSlack;
+    if (__any_sync(0xFFFFFFFFu, above)) {  // some row's maximum moves
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(s[n][e] * p.scale_log2, s[n][e + 2] * p.scale_log2);
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+          const float next = fmaxf(m[n][e], top), keep = exp2_fast(m[n][e] - next);
+          m[n][e] = next;
+          l[n][e] *= keep;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][n][e] *= keep[n][e & 1];
+          for (int i = 0; i < kSteps; ++i) o[i][n][e] *= keep, o[i][n][e + 2] *= keep;
+        }
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] = exp2_fast(fmaf(s[n][e], p.scale_log2, -m[n][e & 1]));
+        l[n][e & 1] += s[n][e];
+      }
     if (a.differ && p.window > 1)
       odd_values<IT, DIM>(a, lane, [&](int j) {
 #pragma unroll
@@ -447,7 +449,7 @@ struct AttnF32 {
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int n = 0; n < kN; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-    m[0] = m[1] = -INFINITY;
+    m[0] = m[1] = kAttnLowest;
     l[0] = l[1] = 0.0f;
   }
   // Q to shared memory: for each 8 columns the four registers of the left operand of every lane,
@@ -502,41 +504,41 @@ struct AttnF32 {
         }
       }
     }
-    const bool masked = a.differ || a.seen != (1u << kAttnStep) - 1u;
+    if (a.differ || a.seen != (1u << kAttnStep) - 1u) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 8 * n + 2 * four + (e & 1);
+          if (!(a.seen >> j & 1u) || a.token0 + j > limit[e >> 1]) s[n][e] = p.hidden;
+        }
+    }
+    bool above = false;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) above |= fmaf(s[n][e], p.scale_log2, -m[e >> 1]) > kAttnSlack;
+    if (__any_sync(0xFFFFFFFFu, above)) {  // some row's maximum moves
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = fmaxf(fmaxf(s[0][2 * h] * p.scale_log2, s[0][2 * h + 1] * p.scale_log2),
+                          fmaxf(s[1][2 * h] * p.scale_log2, s[1][2 * h + 1] * p.scale_log2));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const float next = fmaxf(m[h], top), keep = exp2_fast(m[h] - next);
+        m[h] = next;
+        l[h] *= keep;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) o[n][2 * h] *= keep, o[n][2 * h + 1] *= keep;
+      }
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = 8 * n + 2 * four + (e & 1);
-        s[n][e] = masked && (!(a.seen >> j & 1u) || a.token0 + j > limit[e >> 1]) ? -INFINITY : s[n][e] * p.scale_log2;
+        s[n][e] = exp2_fast(fmaf(s[n][e], p.scale_log2, -m[e >> 1]));
+        l[e >> 1] += s[n][e];
       }
-    bool moved = false;
-    float keep[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const float next = top > m[h] + kAttnSlack ? top : m[h], base = next == -INFINITY ? 0.0f : next;
-      keep[h] = exp2_fast(m[h] - base);
-      moved |= next != m[h];
-      m[h] = next;
-      float sum = 0.0f;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          s[n][2 * h + e] = exp2_fast(s[n][2 * h + e] - base);
-          sum += s[n][2 * h + e];
-        }
-      l[h] = fmaf(l[h], keep[h], sum);
-    }
-    if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] *= keep[e >> 1];
-    }
     if (a.differ && p.window > 1)
       odd_values<IT, DIM>(a, lane, [&](int j) {
 #pragma unroll
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
           float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float f = top == -INFINITY ? 0.0f : exp2_fast(m_s[w][r] - top);
+            const float f = exp2_fast(m_s[w][r] - top);
             const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(pass_at + w * (S * Shape::kStage)) + Math::place(row, col));
             y.x = fmaf(v.x, f, y.x), y.y = fmaf(v.y, f, y.y), y.z = fmaf(v.z, f, y.z), y.w = fmaf(v.w, f, y.w);
             sum = fmaf(l_s[w][r], f, sum);
@@ -837,7 +839,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
 
 // Units in pieces, `parts` CTAs each, which share the rows out.  By unit, where there
 // are no more of them than CTAs of the first kernel; else by such a CTA: it has at most one
-// unit's first piece.
+// unit's first piece.  A warp joins a row of up to 32 pieces by itself, a CTA one of more.
 template <typename Math, int DIM>
 __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p, int parts, int by_unit) {
   using IT = typename Math::IT;
@@ -876,6 +878,35 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
   const float2* ml = reinterpret_cast<const float2*>(p.part + 2 * static_cast<int64_t>(p.ctas) * kRows * DIM);
   auto slot = [&](int i) { return 2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0); };
   const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
+  const auto finish = [&](int r) {
+    const int row = rt * kRows + r, t = row / p.per;
+    return static_cast<IT*>(p.out) + ((static_cast<int64_t>(b) * p.window + t) * p.H + g * p.per + row - t * p.per) * DIM;
+  };
+  if (pieces <= 32) {
+    constexpr int kWarps = kAttnJoinThreads / 32, kCols = DIM / 32;
+    for (int r = part * kWarps + warp; r < rows; r += parts * kWarps) {
+      const float2 own = lane < pieces ? ml[slot(lane) * kRows + r] : make_float2(kAttnLowest, 0.0f);
+      float top = own.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const float f = exp2_fast(own.x - top);
+      float sum = own.y * f, y[kCols];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) y[k] = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < pieces; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, i);
+        const float* from = p.part + (slot(i) * kRows + r) * DIM + lane;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) y[k] = fmaf(from[32 * k], w, y[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) put(finish(r) + lane + 32 * k, sum == 0.0f ? 0.0f : y[k] / sum);
+    }
+    return;
+  }
   auto all = [&](float v, auto op) {  // over the CTA
 #pragma unroll
     for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
@@ -893,16 +924,16 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = threadIdx.x + k * kAttnJoinThreads;
-      s[k] = i < pieces ? ml[slot(i) * kRows + r] : make_float2(-INFINITY, 0.0f);
+      s[k] = i < pieces ? ml[slot(i) * kRows + r] : make_float2(kAttnLowest, 0.0f);
     }
     const float top = all(fmaxf(s[0].x, s[1].x), [](float x, float y) { return fmaxf(x, y); });
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = threadIdx.x + k * kAttnJoinThreads;
-      const float f = top == -INFINITY ? 0.0f : exp2_fast(s[k].x - top);
+      const float f = exp2_fast(s[k].x - top);
       if (i < pieces) weight_s[i] = f;
-      sum = fmaf(s[k].y, i < pieces ? f : 0.0f, sum);
+      sum = fmaf(s[k].y, f, sum);
     }
     sum = all(sum, [](float x, float y) { return x + y; });
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -920,8 +951,7 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
     }
     acc_s[group][col] = y;
     __syncthreads();
-    const int row = rt * kRows + r, t = row / p.per;
-    IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(b) * p.window + t) * p.H + g * p.per + row - t * p.per) * DIM;
+    IT* const out = finish(r);
     for (int c = threadIdx.x; c < DIM; c += kAttnJoinThreads) {
       float v = 0.0f;
 #pragma unroll

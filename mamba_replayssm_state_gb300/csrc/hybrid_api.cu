@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -229,6 +231,8 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   tp.p = base;
   hybrid::AttnParams& p = tp.p;
   p.part = static_cast<float*>(a->workspace);
+  p.hidden = p.scale_log2 < 0.0f ? INFINITY : -INFINITY;
+  if (p.scale_log2 == 0.0f) p.scale_log2 = FLT_MIN;  // (infinity times it stays infinity)
   p.row_tiles = pl.row_tiles;
   p.ctas = pl.ctas;
   p.page_shift = -1;
@@ -256,7 +260,7 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   // are in many pieces each, their rows are shared out.
   const int64_t pieces = pl.ctas / pl.units + 1;
   const int rows = static_cast<int>(std::min<int64_t>(pl.rows, static_cast<int64_t>(p.per) * p.window));
-  int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, pieces / 2))), by_unit = pl.units <= pl.ctas;
+  int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, pieces / 4))), by_unit = pl.units <= pl.ctas;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((by_unit ? pl.units : pl.ctas) * parts));
   cfg.blockDim = dim3(hybrid::kAttnJoinThreads);

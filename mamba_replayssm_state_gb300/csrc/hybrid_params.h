@@ -58,6 +58,7 @@ struct AttnParams {
   float* part;                     // partial outputs, then their maxima and sums
   int32_t row_tiles, ctas, page_shift;  // page_shift: log2(page_size), or -1
   int32_t q_pairs;                 // queries may be read two at a time
+  float hidden;                    // a score that times scale_log2 is -infinity
 };
 
 // The tiled kernel: a warp takes kAttnStep tokens at a time, a CTA's four warps kAttnTile; `stages`
