@@ -58,11 +58,12 @@ struct Deal {
     if (b >= p.pages.requests) return 0;
     return counts(tiles_of(request_tokens(p.pages, b, p.window, p.status, report))) * (p.G * p.row_tiles);
   }
+  // (One use for each WHICH: its place is written once.)
+  template <int WHICH>
   __device__ __forceinline__ static int64_t sum(int64_t n) {
     __shared__ int64_t sums[THREADS / 32];
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    __syncthreads();
     if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = n;
     __syncthreads();
     n = 0;
@@ -74,13 +75,13 @@ struct Deal {
     own = of(p, threadIdx.x, report);
     int64_t n = own;
     for (int b = threadIdx.x + THREADS; b < p.pages.requests; b += THREADS) n += of(p, b, report);
-    total = sum(n);
+    total = sum<0>(n);
   }
   // Tiles of the requests before b.
   __device__ __forceinline__ int64_t before(const AttnParams& p, int b) const {
     int64_t n = static_cast<int>(threadIdx.x) < b ? own : 0;
     for (int i = threadIdx.x + THREADS; i < b; i += THREADS) n += of(p, i, false);
-    return sum(n);
+    return sum<1>(n);
   }
   // The request that has tile number `tile` (below the total).
   __device__ __forceinline__ Place find(const AttnParams& p, int64_t tile) const {
@@ -124,9 +125,6 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(column), "r"(head), "r"(row), "r"(page), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
@@ -625,15 +623,17 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
     __syncwarp();
   }
 
-  for (int b = blockIdx.x; b < pg.requests; b += gridDim.x)  // rows of skipped requests
-    if (request_tokens(pg, b, p.window, nullptr, false) == 0) {
-      const int64_t n = static_cast<int64_t>(p.window) * p.H * DIM;
-      IT* out = static_cast<IT*>(p.out) + b * n;
-      for (int64_t i = threadIdx.x; i < n; i += kAttnThreads) out[i] = IT(0);
-    }
+  auto skipped = [&]() {  // rows of skipped requests
+    for (int b = blockIdx.x; b < pg.requests; b += gridDim.x)
+      if (request_tokens(pg, b, p.window, nullptr, false) == 0) {
+        const int64_t n = static_cast<int64_t>(p.window) * p.H * DIM;
+        IT* out = static_cast<IT*>(p.out) + b * n;
+        for (int64_t i = threadIdx.x; i < n; i += kAttnThreads) out[i] = IT(0);
+      }
+  };
   const Deal<kAttnThreads> requests(p, blockIdx.x == 0);
   const AttnDeal deal{requests.total, min(static_cast<int64_t>(gridDim.x), requests.total)};
-  if (blockIdx.x >= deal.ctas) return;
+  if (blockIdx.x >= deal.ctas) return skipped();
   const int64_t begin = deal.begin(blockIdx.x);
   const Place place = requests.find(p, begin);
   // `room` is what is left of this CTA's share where `at` stands.
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
     at.tile = tile;
     if (tile >= at.tiles) {  // the share begins in what a unit's end counts
       room -= counts(at.tiles) - tile;
-      if (room <= 0) return;
+      if (room <= 0) return skipped();
       at.next_unit(p);
     }
   }
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
         const uint32_t bar = full + stage * 8;
         if (good) {
           const int row = p.page_shift >= 0 ? token0 & (pg.page_size - 1) : token0 % pg.page_size;
-          arrive_expect(bar, Shape::kStage);
+          rsm::mbar_arrive_expect_tx(bar, Shape::kStage);
 #pragma unroll
           for (int c = 0; c < DIM / 64; ++c) {
             box_load(base + c * (kAttnStep * 128), &tp.k_map, 64 * c, g, row, page, bar);
@@ -738,6 +738,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   Math math;
   math.queries(p, at, lane, smem);
   math.reset();
+  skipped();
   int from = at.tile;  // the piece's first tile
   uint32_t phase = 0;
   for (int stage = 0;;) {

@@ -58,6 +58,19 @@ std::mutex g_mu;
 int g_sms[kMaxDevices];
 bool g_attn_ready[kMaxDevices][2][3][4][2];  // input type, dim 64, 128, 256, eights of rows, boxes
 
+bool g_rotary_ready[kMaxDevices][2];  // input type
+
+// Lets a kernel take up to `bytes` of dynamic shared memory: once, since the limit is the
+// kernel's and not the call's, and calls come from several threads.
+int allow_smem(bool* ready, const void* fn, int bytes) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (*ready) return RSM_OK;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  *ready = true;
+  return RSM_OK;
+}
+
 int device_sms(int* dev, int* sms) {
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
@@ -245,16 +258,9 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
                      page_map(&tp.k_map, pg.k, pg, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
                      page_map(&tp.v_map, pg.v, pg, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
   const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, pl.rows, boxes);
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    bool& ready = g_attn_ready[dev][a->input_dtype == RSM_F32][a->dim / 128][pl.rows / 8 - 1][boxes];
-    if (!ready) {
-      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return fail(RSM_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-      ready = true;
-    }
-  }
-  const int rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
+  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][a->dim / 128][pl.rows / 8 - 1][boxes], fn, smem);
+  if (rc != RSM_OK) return rc;
+  rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
   if (rc != RSM_OK || !pl.split) return rc;
   // The join's CTAs come while the first kernel's finish, and wait for it.  Where few units
   // are in many pieces each, their rows are shared out.
@@ -386,11 +392,18 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   const bool vec = a->dim % v == 0 && (a->interleaved ? a->rotary_dim : p.half) % v == 0 && rows_fit(p.q, es, b, p.q_bs, n, p.q_ts) &&
                    rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
                    rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads);
+  const int64_t token = (static_cast<int64_t>(a->num_heads) + 2LL * a->num_kv_heads) * a->dim * es, place = token + 8 * p.half;
+  if (!vec || 2 * place > hybrid::kRotaryRingAlone)
+    return launch(hybrid::rotary_kernel(a->input_dtype, false), p.tokens, hybrid::kRotaryThreads, &p, stream);
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  return launch(hybrid::rotary_kernel(a->input_dtype, vec), std::min<int64_t>(p.tokens, hybrid::kRotaryCtas * sms), hybrid::kRotaryThreads,
-                &p, stream);
+  const bool alone = 3 * place > hybrid::kRotaryRing;  // (three places: one in, one turned, one out)
+  p.stages = static_cast<int>(std::min<int64_t>(hybrid::kRotaryMaxStages, (alone ? hybrid::kRotaryRingAlone : hybrid::kRotaryRing) / place));
+  const void* fn = hybrid::rotary_kernel(a->input_dtype, true);
+  rc = allow_smem(&g_rotary_ready[dev][a->input_dtype == RSM_F32], fn, hybrid::kRotaryRingAlone);
+  if (rc != RSM_OK) return rc;
+  return launch(fn, std::min<int64_t>(p.tokens, (alone ? 1 : 2) * sms), hybrid::kRotaryThreads, &p, stream, p.stages * place);
 }
 
 int64_t rsm_paged_attention_workspace(const rsm_paged_attention_args* a) {

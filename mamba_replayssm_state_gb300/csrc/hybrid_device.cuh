@@ -89,6 +89,21 @@ __device__ __forceinline__ int live_sequences(const int32_t* cu, int seqs, int64
   return live;
 }
 
+// The same by one warp.
+__device__ __forceinline__ int live_sequences_warp(const int32_t* cu, int seqs, int64_t tokens, uint32_t* status, bool report) {
+  int live = seqs;
+  bool bad = false;
+  for (int s = threadIdx.x & 31; s < seqs; s += 32) {
+    const int a = cu[s], b = cu[s + 1];
+    if (ssm::goes_back(a, b)) live = min(live, s);
+    bad |= !ssm::within(a, b, tokens);
+  }
+  if (report && bad) flag(status, RSM_STATUS_BAD_SEQUENCE);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) live = min(live, __shfl_xor_sync(0xFFFFFFFFu, live, o));
+  return live;
+}
+
 // The first of `live` sequences that ends after token t (`live`: none does).
 __device__ __forceinline__ int sequence_at(const int32_t* cu, int live, int64_t t) {
   int lo = 0, hi = live;

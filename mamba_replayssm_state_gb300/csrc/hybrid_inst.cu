@@ -5,12 +5,10 @@
 
 namespace hybrid {
 
-const void* rotary_kernel(int input_dtype, bool vec) {
+const void* rotary_kernel(int input_dtype, bool ring) {
   if (input_dtype == RSM_BF16)
-    return vec ? reinterpret_cast<const void*>(&rotary_append_kernel<uint16_t, 8>)
-               : reinterpret_cast<const void*>(&rotary_append_kernel<uint16_t, 1>);
-  return vec ? reinterpret_cast<const void*>(&rotary_append_kernel<float, 4>)
-             : reinterpret_cast<const void*>(&rotary_append_kernel<float, 1>);
+    return ring ? reinterpret_cast<const void*>(&rotary_append_kernel<uint16_t>) : reinterpret_cast<const void*>(&rotary_plain_kernel<uint16_t>);
+  return ring ? reinterpret_cast<const void*>(&rotary_append_kernel<float>) : reinterpret_cast<const void*>(&rotary_plain_kernel<float>);
 }
 
 const void* copy_kernel() { return reinterpret_cast<const void*>(&copy_pages_kernel); }

@@ -41,10 +41,15 @@ struct RotaryParams {
   int64_t tokens, q_bs, q_ts, k_bs, k_ts, v_bs, v_ts, out_bs, out_ts;
   int32_t window, H, G, dim, half, interleaved;  // half: rotary_dim / 2
   float amplitude;
+  int32_t stages;  // tokens that a ring holds
 };
 
-constexpr int kRotaryThreads = 288, kRotaryCtas = 3;  // CTAs an SM
-const void* rotary_kernel(int input_dtype, bool vec);
+// A CTA's ring: up to kRotaryRing bytes where two CTAs share an SM, up to kRotaryRingAlone for long tokens.
+constexpr int kRotaryThreads = 160, kRotaryMaxStages = 8, kRotaryMaxHalf = 128;
+constexpr int kRotaryRing = 104 * 1024, kRotaryRingAlone = 216 * 1024;
+constexpr uint64_t kRotaryTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
+// ring: whole tokens through shared memory; else an element at a time.
+const void* rotary_kernel(int input_dtype, bool ring);
 
 struct AttnParams {
   const void* q;

@@ -7,17 +7,17 @@
 // times the position it wraps by itself: the error, a unit a position, stays below
 // 2^-32 turns, and the upper 32 bits are what sine and cosine are taken of.
 //
-// Memory bounds it: q, k, v read once and written once.  A CTA stays for a run of tokens,
-// kRotaryTokens at a time: eight warps move them, each thread the same 16 bytes (twice
-// that for two halves of a head) of a head for all the tokens; a ninth meanwhile
-// looks up where the next ones go, which takes three loads that wait for one another, and
-// makes their sines and cosines, once for all heads.
+// Memory bounds it: q, k, v read once and written once.  So whole tokens pass through
+// shared memory by bulk copies, a ring of them in a CTA that stays for a run of tokens: one
+// warp looks up where they go, makes their sines and cosines (once for all heads) and
+// issues the copies in and out; the others turn the pairs in place, and touch nothing
+// else.  Rows that are not whole 16-byte vectors, or too long for a ring, go through
+// rotary_plain_kernel, an element at a time.
 #pragma once
 #include "hybrid_device.cuh"
+#include "rsm_ptx.cuh"
 
 namespace hybrid {
-
-constexpr int kRotaryMaxHalf = 128, kRotaryTokens = 4;
 
 struct RotaryToken {
   int64_t q, k, v, out;   // element offsets of the token's rows
@@ -35,156 +35,262 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
   return f < 0.0f ? 0 - n : n;
 }
 
-template <typename IT, int V>
-__global__ void __launch_bounds__(kRotaryThreads, kRotaryCtas) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
-  constexpr int kMovers = kRotaryThreads - 32, T = kRotaryTokens;
-  __shared__ RotaryToken token_s[2][T];
-  __shared__ uint64_t step[kRotaryMaxHalf];
-  __shared__ float2 turn_s[2][T * kRotaryMaxHalf];
-  const int64_t begin = blockIdx.x * p.tokens / gridDim.x, end = (blockIdx.x + 1) * p.tokens / gridDim.x;
+// Where token i of the call is read and goes.
+__device__ __forceinline__ RotaryToken rotary_token(const RotaryParams& p, int live, int64_t i) {
   const rsm_pages& pg = p.pages;
-  int live = 0;
-  if (p.cu != nullptr) live = live_sequences(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
+  RotaryToken k;
+  int64_t b, t, n;
+  k.live = 1;
+  if (p.cu != nullptr) {
+    b = sequence_at(p.cu, live, i);
+    t = n = 0;
+    if (b == live || p.cu[b] < 0 || p.cu[b] > i || p.cu[b + 1] > p.tokens)
+      k.live = 0;
+    else
+      t = i - p.cu[b], n = p.cu[b + 1] - p.cu[b];
+    k.q = i * p.q_ts, k.k = i * p.k_ts, k.v = i * p.v_ts, k.out = i * p.out_ts;
+  } else {
+    b = i / p.window, t = i - b * p.window, n = p.window;
+    k.q = b * p.q_bs + t * p.q_ts, k.k = b * p.k_bs + t * p.k_ts, k.v = b * p.v_bs + t * p.v_ts;
+    k.out = b * p.out_bs + t * p.out_ts;
+  }
+  k.pos = 0;
+  k.k_row = k.v_row = -1;
+  if (k.live == 0) return k;
+  const int64_t len = pg.lengths[b];
+  if (len < n || len > static_cast<int64_t>(pg.table_width) * pg.page_size) {
+    if (len != 0) flag(p.status, RSM_STATUS_BAD_POSITION);
+    return k;
+  }
+  k.live = 2;
+  k.pos = static_cast<uint32_t>(len - n + t);
+  const uint32_t at = k.pos / static_cast<uint32_t>(pg.page_size);
+  const int64_t row = k.pos - at * static_cast<uint32_t>(pg.page_size);
+  const int page = pg.page_table[b * pg.table_stride + at];
+  if (page < 0 || page >= pg.num_pages)
+    flag(p.status, RSM_STATUS_BAD_PAGE);
+  else
+    k.k_row = page * pg.k_page_stride + row * pg.k_row_stride, k.v_row = page * pg.v_page_stride + row * pg.v_row_stride;
+  return k;
+}
 
-  // ---- the ninth warp: tokens first .. first + T - 1 ----
-  const int lane = threadIdx.x - kMovers;
-  auto look_up = [&](int64_t first, int to) {
-    if (lane < T && first + lane < end) {
-      RotaryToken k;
-      const int64_t i = first + lane;
-      int64_t b, t, n;
-      k.live = 1;
-      if (p.cu != nullptr) {
-        b = sequence_at(p.cu, live, i);
-        t = n = 0;
-        if (b == live || p.cu[b] < 0 || p.cu[b] > i || p.cu[b + 1] > p.tokens)
-          k.live = 0;
-        else
-          t = i - p.cu[b], n = p.cu[b + 1] - p.cu[b];
-        k.q = i * p.q_ts, k.k = i * p.k_ts, k.v = i * p.v_ts, k.out = i * p.out_ts;
-      } else {
-        b = i / p.window, t = i - b * p.window, n = p.window;
-        k.q = b * p.q_bs + t * p.q_ts, k.k = b * p.k_bs + t * p.k_ts, k.v = b * p.v_bs + t * p.v_ts;
-        k.out = b * p.out_bs + t * p.out_ts;
-      }
-      k.pos = 0;
-      k.k_row = k.v_row = -1;
-      if (k.live != 0) {
-        const int64_t len = pg.lengths[b];
-        if (len < n || len > static_cast<int64_t>(pg.table_width) * pg.page_size) {
-          if (len != 0) flag(p.status, RSM_STATUS_BAD_POSITION);
-        } else {
-          k.live = 2;
-          k.pos = static_cast<uint32_t>(len - n + t);
-          const uint32_t at = k.pos / static_cast<uint32_t>(pg.page_size);
-          const int64_t row = k.pos - at * static_cast<uint32_t>(pg.page_size);
-          const int page = pg.page_table[b * pg.table_stride + at];
-          if (page < 0 || page >= pg.num_pages)
-            flag(p.status, RSM_STATUS_BAD_PAGE);
-          else
-            k.k_row = page * pg.k_page_stride + row * pg.k_row_stride, k.v_row = page * pg.v_page_stride + row * pg.v_row_stride;
-        }
-      }
-      token_s[to][lane] = k;
-    }
-    __syncwarp();
-    for (int t = 0; t < T && first + t < end; ++t) {
-      const uint32_t pos = token_s[to][t].pos;
-      for (int j = lane; j < p.half; j += 32) {
-        const int32_t upper = static_cast<int32_t>(static_cast<uint32_t>((pos * step[j]) >> 32));
-        float s, c;
-        sincospif(static_cast<float>(upper) * 0x1p-31f, &s, &c);
-        turn_s[to][t * p.half + j] = make_float2(c * p.amplitude, s * p.amplitude);
-      }
-    }
-  };
+// Cosine and sine of `pos` times a step, with the amplitude.
+__device__ __forceinline__ float2 rotary_turn(uint32_t pos, uint64_t step, float amplitude) {
+  const int32_t upper = static_cast<int32_t>(static_cast<uint32_t>((pos * step) >> 32));
+  float s, c;
+  sincospif(static_cast<float>(upper) * 0x1p-31f, &s, &c);
+  return make_float2(c * amplitude, s * amplitude);
+}
 
-  // ---- the movers' parts of a head: those that turn (V pairs from two halves, or V / 2
-  // neighbouring ones), then those that are copied; a value head is copied whole ----
-  const bool near = V > 1 && p.interleaved, near_one = V == 1 && p.interleaved;
-  const uint32_t turning = V > 1 ? (near ? 2 * p.half / V : p.half / V) : p.half;
-  const uint32_t parts = turning + (p.dim - 2 * p.half) / V, copied = p.dim / V;
-  const uint32_t heads = (p.H + p.G) * parts, per = heads + p.G * copied;
-  auto move = [&](uint32_t i, int of, int nt) {
-    const bool value = i >= heads;
-    const uint32_t in = value ? i - heads : i, h = in / (value ? copied : parts), part = in - h * (value ? copied : parts);
-    const bool key = !value && h >= static_cast<uint32_t>(p.H);
-    const uint32_t g = key ? h - p.H : h;
-    const bool turns = !value && part < turning;
-    // columns of the part, and of its other half
-    const uint32_t ca = value ? part * V : !turns ? 2 * p.half + (part - turning) * V : near_one ? 2 * part : part * V;
-    const uint32_t cb = near_one ? ca + 1 : ca + p.half;
-    const bool two = turns && !near;
-    const IT* const from = (value ? static_cast<const IT*>(p.v) : key ? static_cast<const IT*>(p.k) : static_cast<const IT*>(p.q)) +
-                           static_cast<int64_t>(g) * p.dim;
-    IT* const to = value ? static_cast<IT*>(pg.v) + g * pg.v_head_stride
-                   : key ? static_cast<IT*>(pg.k) + g * pg.k_head_stride
-                         : static_cast<IT*>(p.q_out) + static_cast<int64_t>(g) * p.dim;
-    const RotaryToken* const token = token_s[of];
-    Row<IT, V> a[T], b[T];
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      if (t < nt) {
-        const RotaryToken& k = token[t];
-        if (k.live == 2) {
-          const IT* row = from + (value ? k.v : key ? k.k : k.q);
-          a[t].load(row + ca);
-          if (two) b[t].load(row + cb);
-        } else {
-          a[t].zero();  // a skipped request's queries
-          b[t].zero();
-        }
-      }
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      if (t < nt) {
-        const RotaryToken& k = token[t];
-        const int64_t row = value ? k.v_row : key ? k.k_row : k.live == 0 ? -1 : k.out;
-        if (row < 0) continue;
-        if (turns) {
-          float x[V], y[V], u[V], v[V];
-          const float2* cs = turn_s[of] + t * p.half;
-          a[t].values(x);
-          if (near) {
-#pragma unroll
-            for (int j = 0; j + 1 < V; j += 2) {
-              const float2 w = cs[part * (V / 2) + j / 2];
-              u[j] = x[j] * w.x - x[j + 1] * w.y;
-              u[j + 1] = x[j + 1] * w.x + x[j] * w.y;
-            }
-            a[t].round(u);
-          } else {
-            b[t].values(y);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const float2 w = cs[part * V + j];
-              u[j] = x[j] * w.x - y[j] * w.y;
-              v[j] = y[j] * w.x + x[j] * w.y;
-            }
-            a[t].round(u);
-            b[t].round(v);
-            b[t].store(to + row + cb);
-          }
-        }
-        a[t].store(to + row + ca);
-      }
-  };
+__device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the last N groups of this thread's stores have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 
-  if (lane >= 0) {
-    for (int j = lane; j < p.half; j += 32) step[j] = turns_per_position(p.inv_freq[j]);
-    __syncwarp();
-    look_up(begin, 0);
+template <typename IT>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
+  constexpr int V = 16 / sizeof(IT), kWarps = kRotaryThreads / 32 - 1;  // that turn
+  extern __shared__ __align__(128) char smem[];
+  __shared__ __align__(8) uint64_t full_s[kRotaryMaxStages], done_s[kRotaryMaxStages];
+  __shared__ int live_s[kRotaryMaxStages];
+  const rsm_pages& pg = p.pages;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, S = p.stages;
+  const int64_t begin = blockIdx.x * p.tokens / gridDim.x, count = (blockIdx.x + 1) * p.tokens / gridDim.x - begin;
+  const int qn = p.H * p.dim, kn = p.G * p.dim;
+  const uint32_t token_bytes = (qn + 2 * kn) * static_cast<uint32_t>(sizeof(IT)), ring = rsm::smem_addr(smem);
+  float2* const turns = reinterpret_cast<float2*>(smem + S * token_bytes);
+  const uint32_t full = rsm::smem_addr(full_s), done = rsm::smem_addr(done_s);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) rsm::mbar_init(full + 8 * s, 2), rsm::mbar_init(done + 8 * s, kWarps);
+    rsm::fence_mbar_init();
   }
   __syncthreads();
-  int of = 0;
-  for (int64_t first = begin; first < end; first += T, of ^= 1) {
-    if (lane >= 0) {
-      if (first + T < end) look_up(first + T, of ^ 1);
-    } else {
-      const int nt = static_cast<int>(min(static_cast<int64_t>(T), end - first));
-      for (uint32_t i = threadIdx.x; i < per; i += kMovers) move(i, of, nt);
+
+  if (warp == 0) {
+    // the rows come in whatever becomes of them
+    auto load = [&](int64_t i, int s) {
+      if (lane != 0) return;
+      const uint32_t at = ring + s * token_bytes, qb = qn * sizeof(IT), kb = kn * sizeof(IT);
+      int64_t q, k, v;
+      if (p.cu != nullptr) {
+        q = (begin + i) * p.q_ts, k = (begin + i) * p.k_ts, v = (begin + i) * p.v_ts;
+      } else {
+        const int64_t b = (begin + i) / p.window, t = begin + i - b * p.window;
+        q = b * p.q_bs + t * p.q_ts, k = b * p.k_bs + t * p.k_ts, v = b * p.v_bs + t * p.v_ts;
+      }
+      rsm::mbar_arrive_expect_tx(full + 8 * s, token_bytes);
+      rsm::bulk_g2s(at, static_cast<const IT*>(p.q) + q, qb, full + 8 * s);
+      rsm::bulk_g2s(at + qb, static_cast<const IT*>(p.k) + k, kb, full + 8 * s);
+      rsm::bulk_g2s(at + qb + kb, static_cast<const IT*>(p.v) + v, kb, full + 8 * s);
+    };
+    for (int i = 0; i < S - 1 && i < count; ++i) load(i, i);
+    uint64_t step[kRotaryMaxHalf / 32];
+#pragma unroll
+    for (int j = 0; j < kRotaryMaxHalf / 32; ++j) step[j] = lane + 32 * j < p.half ? turns_per_position(p.inv_freq[lane + 32 * j]) : 0;
+    const int live = p.cu == nullptr ? 0 : live_sequences_warp(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
+    RotaryToken mine{};  // of 32 tokens, a lane each
+    auto info = [&](int64_t i, int s) {
+      if (i % 32 == 0 && i + lane < count) mine = rotary_token(p, live, begin + i + lane);
+      const int from = static_cast<int>(i % 32);
+      const uint32_t pos = __shfl_sync(0xFFFFFFFFu, mine.pos, from);
+      const int state = __shfl_sync(0xFFFFFFFFu, mine.live, from);
+      if (lane == 0) live_s[s] = state;
+      if (state == 2) {
+#pragma unroll
+        for (int j = 0; j < kRotaryMaxHalf / 32; ++j)
+          if (lane + 32 * j < p.half) turns[s * p.half + lane + 32 * j] = rotary_turn(pos, step[j], p.amplitude);
+      }
+      __syncwarp();
+      if (lane == 0) rsm::mbar_arrive(full + 8 * s);
+    };
+    // info runs with the loads; where a token goes is asked of the 32 at hand, so the last
+    // round's places are kept for those still on their way out
+    RotaryToken last{};
+    auto prepare = [&](int64_t i, int s) {
+      if (i % 32 == 0) last = mine;
+      info(i, s);
+    };
+    for (int i = 0; i < S - 1 && i < count; ++i) prepare(i, i);
+    int64_t asked = min(static_cast<int64_t>(S - 1), count);
+    int s = 0, ask_s = S - 1;
+    uint32_t phase = 0;
+    for (int64_t i = 0; i < count; ++i) {
+      if (!rsm::mbar_wait(done + 8 * s, phase, kRotaryTimeoutNs)) {  // (never expected)
+        if (lane == 0) flag(p.status, RSM_STATUS_WAIT_TIMEOUT);
+        bulk_wait_read<0>();
+        for (int k = 0; k < S; ++k) (void)rsm::mbar_wait(full + 8 * k, k < s ? phase ^ 1u : phase, 1000000ull);  // copies on the way
+        return;
+      }
+      // round 32 of tokens i belongs to `last` once `mine` is of the next one
+      const bool old = i / 32 != (asked - 1) / 32;
+      const int from = static_cast<int>(i % 32);
+      auto of = [&](int64_t m, int64_t l) { return __shfl_sync(0xFFFFFFFFu, old ? l : m, from); };
+      const int64_t out = of(mine.out, last.out), kr = of(mine.k_row, last.k_row), vr = of(mine.v_row, last.v_row);
+      const int state = __shfl_sync(0xFFFFFFFFu, old ? last.live : mine.live, from);
+      const uint32_t at = ring + s * token_bytes, qb = qn * sizeof(IT), kb = kn * sizeof(IT), hb = p.dim * sizeof(IT);
+      if (lane == 0 && state != 0) bulk_store(static_cast<IT*>(p.q_out) + out, at, qb);
+      if (kr >= 0) {
+        if (pg.k_head_stride == p.dim || p.G == 1) {
+          if (lane == 1) bulk_store(static_cast<IT*>(pg.k) + kr, at + qb, kb);
+        } else {
+          for (int g = lane; g < p.G; g += 32) bulk_store(static_cast<IT*>(pg.k) + kr + g * pg.k_head_stride, at + qb + g * hb, hb);
+        }
+        if (pg.v_head_stride == p.dim || p.G == 1) {
+          if (lane == 2) bulk_store(static_cast<IT*>(pg.v) + vr, at + qb + kb, kb);
+        } else {
+          for (int g = lane; g < p.G; g += 32) bulk_store(static_cast<IT*>(pg.v) + vr + g * pg.v_head_stride, at + qb + kb + g * hb, hb);
+        }
+      }
+      bulk_commit();
+      if (asked < count) {
+        bulk_wait_read<1>();  // the token before this one has left its place
+        __syncwarp();
+        load(asked, ask_s);
+        prepare(asked, ask_s);
+        ++asked;
+        ask_s = ask_s + 1 == S ? 0 : ask_s + 1;
+      }
+      if (++s == S) s = 0, phase ^= 1u;
     }
-    __syncthreads();
+    bulk_wait_read<0>();
+    return;
+  }
+
+  // ---- the turning warps ----
+  const bool near = p.interleaved != 0;
+  const int parts = (near ? 2 * p.half : p.half) / V, items = (p.H + p.G) * parts;
+  int s = 0;
+  uint32_t phase = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (!rsm::mbar_wait(full + 8 * s, phase, kRotaryTimeoutNs)) {
+      flag(p.status, RSM_STATUS_WAIT_TIMEOUT);
+      return;
+    }
+    IT* const token = reinterpret_cast<IT*>(smem + s * token_bytes);
+    const int state = live_s[s];
+    if (state == 2) {
+      const float2* const turn = turns + s * p.half;
+      for (int k = threadIdx.x - 32; k < items; k += 32 * kWarps) {
+        const int h = k / parts, j = k - h * parts;
+        IT* const at = token + h * p.dim + j * V;
+        Row<IT, V> a, b;
+        float x[V], y[V], u[V], v[V];
+        a.load(at);
+        a.values(x);
+        if (near) {
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const float2 w = turn[j * (V / 2) + e / 2];
+            u[e] = x[e] * w.x - x[e + 1] * w.y;
+            u[e + 1] = x[e + 1] * w.x + x[e] * w.y;
+          }
+        } else {
+          b.load(at + p.half);
+          b.values(y);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float2 w = turn[j * V + e];
+            u[e] = x[e] * w.x - y[e] * w.y;
+            v[e] = y[e] * w.x + x[e] * w.y;
+          }
+          b.round(v);
+          b.store(at + p.half);
+        }
+        a.round(u);
+        a.store(at);
+      }
+    } else if (state == 1) {  // a skipped request's queries
+      for (int k = threadIdx.x - 32; k < qn / V; k += 32 * kWarps) *reinterpret_cast<uint4*>(token + k * V) = make_uint4(0, 0, 0, 0);
+    }
+    rsm::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) rsm::mbar_arrive(done + 8 * s);
+    if (++s == S) s = 0, phase ^= 1u;
+  }
+}
+
+// Any size, stride and alignment: a CTA a token.
+template <typename IT>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_plain_kernel(const __grid_constant__ RotaryParams p) {
+  __shared__ RotaryToken token;
+  __shared__ float2 turn[kRotaryMaxHalf];
+  const rsm_pages& pg = p.pages;
+  const int live = p.cu == nullptr ? 0 : live_sequences(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
+  if (threadIdx.x == 0) token = rotary_token(p, live, blockIdx.x);
+  __syncthreads();
+  const RotaryToken k = token;
+  if (k.live == 0) return;
+  for (int j = threadIdx.x; j < p.half; j += kRotaryThreads) turn[j] = rotary_turn(k.pos, turns_per_position(p.inv_freq[j]), p.amplitude);
+  __syncthreads();
+  const int heads = p.H + 2 * p.G, half = p.half, part = half + p.dim - 2 * half;  // pairs, then what stays
+  for (int i = threadIdx.x; i < heads * part; i += kRotaryThreads) {
+    const int h = i / part, j = i - h * part;
+    const bool key = h >= p.H && h < p.H + p.G, value = h >= p.H + p.G;
+    if ((key || value) && k.k_row < 0) continue;
+    const IT* from = value ? static_cast<const IT*>(p.v) + k.v + static_cast<int64_t>(h - p.H - p.G) * p.dim
+                     : key ? static_cast<const IT*>(p.k) + k.k + static_cast<int64_t>(h - p.H) * p.dim
+                           : static_cast<const IT*>(p.q) + k.q + static_cast<int64_t>(h) * p.dim;
+    IT* to = value ? static_cast<IT*>(pg.v) + k.v_row + (h - p.H - p.G) * pg.v_head_stride
+             : key ? static_cast<IT*>(pg.k) + k.k_row + (h - p.H) * pg.k_head_stride
+                   : static_cast<IT*>(p.q_out) + k.out + static_cast<int64_t>(h) * p.dim;
+    const int a = j >= half ? j + half : p.interleaved ? 2 * j : j, b = j >= half ? a : p.interleaved ? a + 1 : a + half;
+    if (k.live == 1) {
+      to[a] = to[b] = IT(0);
+    } else if (value || j >= half) {
+      const IT x = from[a], y = from[b];
+      to[a] = x;
+      to[b] = y;
+    } else {
+      const float x = get(from + a), y = get(from + b);
+      const float2 w = turn[j];
+      put(to + a, x * w.x - y * w.y);
+      put(to + b, y * w.x + x * w.y);
+    }
   }
 }
 
