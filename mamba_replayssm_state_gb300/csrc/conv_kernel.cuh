@@ -221,10 +221,10 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 5) conv_prompt_kern
     before[j - 1].zero();
     if (mine && first >= j) before[j - 1].load(x + (first - j) * p.x_ts);
   }
+  Taps<W, V> taps;
+  if (mine) taps.load(p.weight, p.bias, static_cast<int>(c));
   const int live = live_sequences(p.cu, p.seqs, p.tokens, p.status, blockIdx.x == 0);
   if (!mine) return;
-  Taps<W, V> taps;
-  taps.load(p.weight, p.bias, static_cast<int>(c));
   const bool act = p.silu != 0;
   Past<W, V> h;
 #pragma unroll
@@ -320,6 +320,20 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_step_kernel
   IT* const out = static_cast<IT*>(p.out) + b0 * p.window * p.out_ts + c;
   IT* const cache = static_cast<IT*>(p.cache) + c;
   const bool mine = c < p.C;
+  const Places place(ring);
+  const int chunks = (p.window + U - 1) / U;
+  auto ask_tokens = [&](int n, int k, int at) {  // of item (n, k), request n's chunk k
+    const IT* from = x + n * p.x_bs + k * U * p.x_ts;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k * U + u < p.window) place.ask(at + W - 1 + u, from + u * p.x_ts);
+  };
+  // the first items' own rows do not depend on where the requests are
+  if (V > 1 && mine) {
+#pragma unroll
+    for (int i = 0; i < kItems - 1; ++i)
+      if (i < count * chunks) ask_tokens(i / chunks, i % chunks, i * kRows);
+  }
   if (static_cast<int>(threadIdx.x) < count) {
     Request r;
     const int slot = p.slots[b0 + threadIdx.x], pos = p.positions[b0 + threadIdx.x];
@@ -345,11 +359,8 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_step_kernel
   __syncthreads();
   if (!mine) return;
   const bool act = p.silu != 0;
-  const Places place(ring);
-  const int chunks = (p.window + U - 1) / U;
-  // item: chunk k of request n; asked for in order
   int ask_n = 0, ask_k = 0, ask_at = 0;
-  auto ask = [&]() {
+  auto ask = [&](bool first) {  // the next item's rows
     if constexpr (V > 1) {
       if (ask_n < count && request[ask_n].slot >= 0) {
         if (ask_k == 0) {
@@ -357,10 +368,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_step_kernel
           for (int j = 0; j < W - 1; ++j)
             if (request[ask_n].back[j] >= 0) place.ask(ask_at + j, cache + request[ask_n].back[j]);
         }
-        const IT* from = x + ask_n * p.x_bs + ask_k * U * p.x_ts;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (ask_k * U + u < p.window) place.ask(ask_at + W - 1 + u, from + u * p.x_ts);
+        if (!first) ask_tokens(ask_n, ask_k, ask_at);
       }
       cp_async_commit();
       if (++ask_k == chunks) ask_k = 0, ++ask_n;
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_step_kernel
     }
   };
 #pragma unroll
-  for (int i = 0; i < kItems - 1; ++i) ask();
+  for (int i = 0; i < kItems - 1; ++i) ask(true);
   int at = 0;
   for (int n = 0; n < count; ++n) {
     const int64_t slot = request[n].slot;
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_step_kernel
     uint32_t row = request[n].row;
     Past<W, V> h;
     for (int k = 0; k < chunks; ++k) {
-      ask();
+      ask(false);
       if constexpr (V > 1) cp_async_wait<kItems - 1>();
       if (k == 0) {
 #pragma unroll

@@ -129,13 +129,17 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
       rsm::bulk_g2s(at + qb + kb, static_cast<const IT*>(p.v) + v, kb, full + 8 * s);
     };
     for (int i = 0; i < S - 1 && i < count; ++i) load(i, i);
-    uint64_t step[kRotaryMaxHalf / 32];
+    float freq[kRotaryMaxHalf / 32];  // (on their way while the first tokens are looked up)
 #pragma unroll
-    for (int j = 0; j < kRotaryMaxHalf / 32; ++j) step[j] = lane + 32 * j < p.half ? turns_per_position(p.inv_freq[lane + 32 * j]) : 0;
+    for (int j = 0; j < kRotaryMaxHalf / 32; ++j) freq[j] = lane + 32 * j < p.half ? p.inv_freq[lane + 32 * j] : 0.0f;
     const int live = p.cu == nullptr ? 0 : live_sequences_warp(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
     RotaryToken mine{};  // of 32 tokens, a lane each
+    if (lane < count) mine = rotary_token(p, live, begin + lane);
+    uint64_t step[kRotaryMaxHalf / 32];
+#pragma unroll
+    for (int j = 0; j < kRotaryMaxHalf / 32; ++j) step[j] = turns_per_position(freq[j]);
     auto info = [&](int64_t i, int s) {
-      if (i % 32 == 0 && i + lane < count) mine = rotary_token(p, live, begin + i + lane);
+      if (i > 0 && i % 32 == 0 && i + lane < count) mine = rotary_token(p, live, begin + i + lane);
       const int from = static_cast<int>(i % 32);
       const uint32_t pos = __shfl_sync(0xFFFFFFFFu, mine.pos, from);
       const int state = __shfl_sync(0xFFFFFFFFu, mine.live, from);
