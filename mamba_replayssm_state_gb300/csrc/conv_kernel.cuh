@@ -190,7 +190,7 @@ __device__ __forceinline__ Row<IT, V> conv_token(const Taps<W, V>& k, Past<W, V>
 // which it starts, which so is the only one to look into the cache and to store
 // there: it reads before it writes.
 template <typename IT, int W, int V>
-__global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 5) conv_prompt_kernel(const __grid_constant__ ConvParams p) {
+__global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kernel(const __grid_constant__ ConvParams p) {
   constexpr int U = 4;
   constexpr int64_t kNever = int64_t{1} << 62;
   static_assert(kConvAhead % U == 0);

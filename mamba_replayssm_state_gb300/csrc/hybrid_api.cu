@@ -311,8 +311,10 @@ int rsm_causal_conv(const rsm_causal_conv_args* a, void* stream) {
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  // few tokens: blocks of eight, for the shortest way through; many: of 64, of which three rows are read twice
-  p.block = a->tokens * p.cblocks >= 64LL * 5 * sms ? 64 : 8;
+  // Few tokens: blocks of four, for the shortest way through (37 tokens of 5376 channels: 5.1 us, 5.8 of
+  // eight, 7.2 of 16); many: of 48, which read three rows twice (8192 tokens of 18432 channels: 95.3 us, 96.0
+  // of 32, 97.0 of 64).
+  p.block = a->tokens * p.cblocks >= 48LL * 4 * sms ? 48 : 4;
   const int64_t blocks = (a->tokens + p.block - 1) / p.block;
   return launch(hybrid::conv_kernel(a->input_dtype, a->width, vec), blocks * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
@@ -347,6 +349,10 @@ int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
   const int64_t groups = (a->batch + p.block - 1) / p.block;
   return launch(hybrid::conv_step_kernel_of(a->input_dtype, a->width, vec), groups * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
+
+// Tokens an SM up to which each has a CTA of its own: 1, 64, 608, 2000 and 4096 tokens (32 heads and 8 of 128, bf16) take
+// 3.3, 3.5, 5.5, 15.7 and 27.8 us so, and 5.5, 5.8, 8.1, 18.1 and 26.3 in rings.
+constexpr int kRotaryFew = 16;
 
 int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
@@ -393,14 +399,14 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
                    rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
                    rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads);
   const int64_t token = (static_cast<int64_t>(a->num_heads) + 2LL * a->num_kv_heads) * a->dim * es, place = token + 8 * p.half;
-  if (!vec || 2 * place > hybrid::kRotaryRingAlone)
-    return launch(hybrid::rotary_kernel(a->input_dtype, false), p.tokens, hybrid::kRotaryThreads, &p, stream);
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
+  if (!vec || p.tokens <= kRotaryFew * sms || 2 * place > hybrid::kRotaryRingAlone)
+    return launch(hybrid::rotary_token_kernel_of(a->input_dtype, vec), p.tokens, hybrid::kRotaryPlainThreads, &p, stream);
   const bool alone = 3 * place > hybrid::kRotaryRing;  // (three places: one in, one turned, one out)
   p.stages = static_cast<int>(std::min<int64_t>(hybrid::kRotaryMaxStages, (alone ? hybrid::kRotaryRingAlone : hybrid::kRotaryRing) / place));
-  const void* fn = hybrid::rotary_kernel(a->input_dtype, true);
+  const void* fn = hybrid::rotary_kernel(a->input_dtype);
   rc = allow_smem(&g_rotary_ready[dev][a->input_dtype == RSM_F32], fn, hybrid::kRotaryRingAlone);
   if (rc != RSM_OK) return rc;
   return launch(fn, std::min<int64_t>(p.tokens, (alone ? 1 : 2) * sms), hybrid::kRotaryThreads, &p, stream, p.stages * place);

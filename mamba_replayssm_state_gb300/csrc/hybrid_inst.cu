@@ -5,10 +5,15 @@
 
 namespace hybrid {
 
-const void* rotary_kernel(int input_dtype, bool ring) {
+const void* rotary_kernel(int input_dtype) {
+  return input_dtype == RSM_BF16 ? reinterpret_cast<const void*>(&rotary_append_kernel<uint16_t>)
+                                 : reinterpret_cast<const void*>(&rotary_append_kernel<float>);
+}
+
+const void* rotary_token_kernel_of(int input_dtype, bool vec) {
   if (input_dtype == RSM_BF16)
-    return ring ? reinterpret_cast<const void*>(&rotary_append_kernel<uint16_t>) : reinterpret_cast<const void*>(&rotary_plain_kernel<uint16_t>);
-  return ring ? reinterpret_cast<const void*>(&rotary_append_kernel<float>) : reinterpret_cast<const void*>(&rotary_plain_kernel<float>);
+    return vec ? reinterpret_cast<const void*>(&rotary_token_kernel<uint16_t, 8>) : reinterpret_cast<const void*>(&rotary_token_kernel<uint16_t, 1>);
+  return vec ? reinterpret_cast<const void*>(&rotary_token_kernel<float, 4>) : reinterpret_cast<const void*>(&rotary_token_kernel<float, 1>);
 }
 
 const void* copy_kernel() { return reinterpret_cast<const void*>(&copy_pages_kernel); }

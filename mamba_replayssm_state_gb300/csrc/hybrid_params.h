@@ -45,11 +45,12 @@ struct RotaryParams {
 };
 
 // A CTA's ring: up to kRotaryRing bytes where two CTAs share an SM, up to kRotaryRingAlone for long tokens.
-constexpr int kRotaryThreads = 160, kRotaryMaxStages = 8, kRotaryMaxHalf = 128;
+constexpr int kRotaryThreads = 160, kRotaryMaxStages = 8, kRotaryMaxHalf = 128, kRotaryPlainThreads = 256;
 constexpr int kRotaryRing = 104 * 1024, kRotaryRingAlone = 216 * 1024;
 constexpr uint64_t kRotaryTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
-// ring: whole tokens through shared memory; else an element at a time.
-const void* rotary_kernel(int input_dtype, bool ring);
+const void* rotary_kernel(int input_dtype);
+// vec: 16 bytes at a time, else an element.
+const void* rotary_token_kernel_of(int input_dtype, bool vec);
 
 struct AttnParams {
   const void* q;

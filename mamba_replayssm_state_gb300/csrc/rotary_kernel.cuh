@@ -11,8 +11,8 @@
 // shared memory by bulk copies, a ring of them in a CTA that stays for a run of tokens: one
 // warp looks up where they go, makes their sines and cosines (once for all heads) and
 // issues the copies in and out; the others turn the pairs in place, and touch nothing
-// else.  Rows that are not whole 16-byte vectors, or too long for a ring, go through
-// rotary_plain_kernel, an element at a time.
+// else.  Few tokens, rows that are not whole 16-byte vectors and rows too long for a ring go
+// through rotary_token_kernel.
 #pragma once
 #include "hybrid_device.cuh"
 #include "rsm_ptx.cuh"
@@ -258,43 +258,85 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
   }
 }
 
-// Any size, stride and alignment: a CTA a token.
-template <typename IT>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_plain_kernel(const __grid_constant__ RotaryParams p) {
+// A CTA a token: few tokens, whose way through is shorter than a ring's, and with V = 1 any
+// size, stride and alignment.  A thread's first row is on its way before the token is looked up.
+template <typename IT, int V>
+__global__ void __launch_bounds__(kRotaryPlainThreads) rotary_token_kernel(const __grid_constant__ RotaryParams p) {
   __shared__ RotaryToken token;
   __shared__ float2 turn[kRotaryMaxHalf];
   const rsm_pages& pg = p.pages;
+  // A head's parts: V pairs of two halves (or V columns of neighbouring pairs), then V columns that stay
+  const bool near = V > 1 && p.interleaved, near_one = V == 1 && p.interleaved;
+  const int turning = (near ? 2 * p.half : p.half) / V, parts = turning + (p.dim - 2 * p.half) / V, items = (p.H + 2 * p.G) * parts;
+  struct Item {
+    Row<IT, V> a, b;
+    int h, part, ca, cb;
+  };
+  int64_t q, k, v;
+  if (p.cu != nullptr) {
+    q = blockIdx.x * p.q_ts, k = blockIdx.x * p.k_ts, v = blockIdx.x * p.v_ts;
+  } else {
+    const int64_t b = blockIdx.x / static_cast<uint32_t>(p.window), t = blockIdx.x - b * p.window;
+    q = b * p.q_bs + t * p.q_ts, k = b * p.k_bs + t * p.k_ts, v = b * p.v_bs + t * p.v_ts;
+  }
+  auto load = [&](int i) {
+    Item it;
+    it.h = i / parts;
+    it.part = i - it.h * parts;
+    it.ca = it.part >= turning ? 2 * p.half + (it.part - turning) * V : near_one ? 2 * it.part : it.part * V;
+    it.cb = it.part >= turning || near ? it.ca : near_one ? it.ca + 1 : it.ca + p.half;
+    const IT* from = it.h >= p.H + p.G ? static_cast<const IT*>(p.v) + v + static_cast<int64_t>(it.h - p.H - p.G) * p.dim
+                     : it.h >= p.H     ? static_cast<const IT*>(p.k) + k + static_cast<int64_t>(it.h - p.H) * p.dim
+                                       : static_cast<const IT*>(p.q) + q + static_cast<int64_t>(it.h) * p.dim;
+    it.a.load(from + it.ca);
+    if (it.cb != it.ca) it.b.load(from + it.cb);
+    return it;
+  };
+  Item it;
+  if (static_cast<int>(threadIdx.x) < items) it = load(threadIdx.x);
+  uint64_t step = 0;
+  if (static_cast<int>(threadIdx.x) < p.half) step = turns_per_position(p.inv_freq[threadIdx.x]);
   const int live = p.cu == nullptr ? 0 : live_sequences(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
-  if (threadIdx.x == 0) token = rotary_token(p, live, blockIdx.x);
+  if (threadIdx.x == kRotaryPlainThreads - 1) token = rotary_token(p, live, blockIdx.x);
   __syncthreads();
-  const RotaryToken k = token;
-  if (k.live == 0) return;
-  for (int j = threadIdx.x; j < p.half; j += kRotaryThreads) turn[j] = rotary_turn(k.pos, turns_per_position(p.inv_freq[j]), p.amplitude);
+  const RotaryToken to = token;
+  if (to.live == 0) return;
+  if (static_cast<int>(threadIdx.x) < p.half) turn[threadIdx.x] = rotary_turn(to.pos, step, p.amplitude);
   __syncthreads();
-  const int heads = p.H + 2 * p.G, half = p.half, part = half + p.dim - 2 * half;  // pairs, then what stays
-  for (int i = threadIdx.x; i < heads * part; i += kRotaryThreads) {
-    const int h = i / part, j = i - h * part;
-    const bool key = h >= p.H && h < p.H + p.G, value = h >= p.H + p.G;
-    if ((key || value) && k.k_row < 0) continue;
-    const IT* from = value ? static_cast<const IT*>(p.v) + k.v + static_cast<int64_t>(h - p.H - p.G) * p.dim
-                     : key ? static_cast<const IT*>(p.k) + k.k + static_cast<int64_t>(h - p.H) * p.dim
-                           : static_cast<const IT*>(p.q) + k.q + static_cast<int64_t>(h) * p.dim;
-    IT* to = value ? static_cast<IT*>(pg.v) + k.v_row + (h - p.H - p.G) * pg.v_head_stride
-             : key ? static_cast<IT*>(pg.k) + k.k_row + (h - p.H) * pg.k_head_stride
-                   : static_cast<IT*>(p.q_out) + k.out + static_cast<int64_t>(h) * p.dim;
-    const int a = j >= half ? j + half : p.interleaved ? 2 * j : j, b = j >= half ? a : p.interleaved ? a + 1 : a + half;
-    if (k.live == 1) {
-      to[a] = to[b] = IT(0);
-    } else if (value || j >= half) {
-      const IT x = from[a], y = from[b];
-      to[a] = x;
-      to[b] = y;
-    } else {
-      const float x = get(from + a), y = get(from + b);
-      const float2 w = turn[j];
-      put(to + a, x * w.x - y * w.y);
-      put(to + b, y * w.x + x * w.y);
+  for (int i = threadIdx.x; i < items; i += kRotaryPlainThreads) {
+    if (i >= kRotaryPlainThreads) it = load(i);
+    const bool query = it.h < p.H, value = it.h >= p.H + p.G;
+    if (!query && to.k_row < 0) continue;
+    IT* const row = query   ? static_cast<IT*>(p.q_out) + to.out + static_cast<int64_t>(it.h) * p.dim
+                    : value ? static_cast<IT*>(pg.v) + to.v_row + (it.h - p.H - p.G) * pg.v_head_stride
+                            : static_cast<IT*>(pg.k) + to.k_row + (it.h - p.H) * pg.k_head_stride;
+    if (to.live == 1) {  // a skipped request's queries
+      it.a.zero();
+      it.b.zero();
+    } else if (!value && it.part < turning) {
+      float x[V], y[V], u[V], w[V];
+      it.a.values(x);
+      if (near) {
+#pragma unroll
+        for (int e = 0; e + 1 < V; e += 2) {
+          const float2 cs = turn[it.part * (V / 2) + e / 2];
+          u[e] = x[e] * cs.x - x[e + 1] * cs.y;
+          u[e + 1] = x[e + 1] * cs.x + x[e] * cs.y;
+        }
+      } else {
+        it.b.values(y);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 cs = turn[it.part * V + e];
+          u[e] = x[e] * cs.x - y[e] * cs.y;
+          w[e] = y[e] * cs.x + x[e] * cs.y;
+        }
+        it.b.round(w);
+      }
+      it.a.round(u);
     }
+    it.a.store(row + it.ca);
+    if (it.cb != it.ca) it.b.store(row + it.cb);
   }
 }
 
