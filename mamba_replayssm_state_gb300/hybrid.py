@@ -22,7 +22,7 @@ import math
 import torch
 
 from . import _dtype_code, load_library
-from .block import (_F32, _I32, _INPUTS, _check_device, _check_grad, _check_out, _check_rows, _check_vector, _handle,
+from .block import (_F32, _I32, _INPUTS, _STATES, _check_device, _check_grad, _check_out, _check_rows, _check_vector, _handle,
                     _int32, _like, _mirror, _need, _new_on, _status, ReplaySSMError)
 
 __all__ = ["causal_conv", "causal_conv_step", "rotary_append", "paged_attention", "copy_pages", "rotary_frequencies"]
@@ -334,7 +334,9 @@ def copy_pages(page_ptrs, page_strides, src_pages, dst_pages, *, dtype, page_ele
     pair with a negative page is skipped.  Destinations are distinct and no pair's source.
     """
     lib = _lib or _load()
-    code = _dtype_code(dtype)
+    code = _STATES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
     if stream is None and device_status is None:
         r = _calls.copy(page_ptrs, page_strides, src_pages, dst_pages, code, page_elements, num_pages)
         if r is not None:
