@@ -138,8 +138,8 @@ RSM_API int rsm_rotary_append(const rsm_rotary_append_args *args, void *stream);
  * Attention of new tokens over their requests' pages: for new token t at position p
  * and head h (key head h / (num_heads / num_kv_heads)),
  *     out = sum_{i <= p} softmax_i(scale q . k_i) v_i
- * Tokens in a page out of range are not seen, and flagged; a row that sees none is
- * zero.  dim: 1 .. 256.
+ * Tokens in a page out of range are not seen, and flagged; a row that sees none, or none
+ * with a score above -infinity, is zero.  dim: 1 .. 256.
  *
  * Arithmetic.  Scores, maxima and sums fp32.  With bf16 inputs and dim 64, 128 or 256
  * whose rows are whole 16-byte vectors, the weights (each softmax's numerators) are

@@ -163,6 +163,14 @@ __device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) 
   hi = to_tf32(v);
   lo = to_tf32(v - __uint_as_float(hi));
 }
+// The same for keys and values, which may be infinite: then lo is 0, and so is `other`, elsewhere hi,
+// which is what the other operand's lo is multiplied with (its sign would make the sum NaN).
+__device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo, uint32_t& other) {
+  split_tf32(v, hi, lo);
+  const bool finite = (hi & 0x7F800000u) != 0x7F800000u;
+  lo = finite ? lo : 0u;
+  other = finite ? hi : 0u;
+}
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -481,14 +489,14 @@ struct AttnF32 {
     const uint32_t qs = rsm::smem_addr(smem) + lane * 16;
 #pragma unroll 4
     for (int kk = 0; kk < DIM / 16; ++kk) {
-      uint32_t hi[2][4], lo[2][4];
+      uint32_t hi[2][4], lo[2][4], fin[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const uint4 v = rsm::lds128(a.keys + key_chunk<IT>(8 * n + quad, 4 * kk + four));
-        split_tf32(__uint_as_float(v.x), hi[n][0], lo[n][0]);
-        split_tf32(__uint_as_float(v.y), hi[n][1], lo[n][1]);
-        split_tf32(__uint_as_float(v.z), hi[n][2], lo[n][2]);
-        split_tf32(__uint_as_float(v.w), hi[n][3], lo[n][3]);
+        split_tf32(__uint_as_float(v.x), hi[n][0], lo[n][0], fin[n][0]);
+        split_tf32(__uint_as_float(v.y), hi[n][1], lo[n][1], fin[n][1]);
+        split_tf32(__uint_as_float(v.z), hi[n][2], lo[n][2], fin[n][2]);
+        split_tf32(__uint_as_float(v.w), hi[n][3], lo[n][3], fin[n][3]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -496,7 +504,7 @@ struct AttnF32 {
         const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          mma_tf32(s[n], al, hi[n][2 * e], hi[n][2 * e + 1]);
+          mma_tf32(s[n], al, fin[n][2 * e], fin[n][2 * e + 1]);
           mma_tf32(s[n], ah, lo[n][2 * e], lo[n][2 * e + 1]);
           mma_tf32(s[n], ah, hi[n][2 * e], hi[n][2 * e + 1]);
         }
@@ -568,10 +576,10 @@ struct AttnF32 {
         const uint32_t va[4] = {x.x, x.y, x.z, x.w}, vb[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t h0, l0, h1, l1;
-          split_tf32(__uint_as_float(va[k]), h0, l0);
-          split_tf32(__uint_as_float(vb[k]), h1, l1);
-          mma_tf32(o[n + k], pl, h0, h1);
+          uint32_t h0, l0, f0, h1, l1, f1;
+          split_tf32(__uint_as_float(va[k]), h0, l0, f0);
+          split_tf32(__uint_as_float(vb[k]), h1, l1, f1);
+          mma_tf32(o[n + k], pl, f0, f1);
           mma_tf32(o[n + k], ph, l0, l1);
           mma_tf32(o[n + k], ph, h0, h1);
         }

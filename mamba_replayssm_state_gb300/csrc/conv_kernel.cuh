@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
   auto advance = [&](int64_t t) {  // to the first sequence that ends after t
     while (s1 <= t) {
       if (++s >= live) {
-        s0 = s1 = own = kNever;
+        s0 = s1 = kNever;  // (own is not s0: nothing starts here)
+        own = kNever + 1;
         return;
       }
       s0 = p.cu[s], s1 = p.cu[s + 1];
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
   }
   if constexpr (V > 1) cp_async_wait<0>();
   // the rest of the first W - 1 tokens of a sequence that starts here
-  if (own == s0)
+  if (own == s0 && s0 < last)
     for (int64_t t = last; t < min(s1, s0 + (W - 1)); ++t) one(t);
 }
 

@@ -1,0 +1,469 @@
+"""The operators of hybrid stacks where a call's sizes, values or callers are unusual.  Bounds and references are
+test_hybrid_ops_gpu's, or stated at the test."""
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import hybrid_reference as ref  # noqa: E402
+import mamba_replayssm_state_gb300 as rsm  # noqa: E402
+import test_hybrid_ops_gpu as base  # noqa: E402
+from mamba_replayssm_state_gb300 import hybrid  # noqa: E402
+from test_hybrid_ops_gpu import BF16, F32, close, gen, i32, rand, word  # noqa: E402
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+def calls(dtype=BF16, dim=64, seed=1):
+    """Every operator on small tensors: (function of the keyword arguments, its tensors by name, those it writes)."""
+    g = gen(seed)
+    C, b, T, H, G, page = 264, 3, 2, 4, 2, 16
+    conv = dict(x=rand(g, 40, C, dtype=dtype), weight=rand(g, C, 4), cu_seqlens=i32([0, 1, 33, 40]), bias=rand(g, C),
+                cache=rand(g, b, 6, C, dtype=dtype), slots=i32([2, 0, 1]), positions=i32([0, 2, 7]))
+    step = dict(x=rand(g, b, T, C, dtype=dtype), weight=rand(g, C, 4), cache=rand(g, b, 6, C, dtype=dtype),
+                slots=i32([1, 2, 0]), positions=i32([0, 5, 9]), bias=rand(g, C))
+    lengths, table = i32([100, 3, 70]), ref.table([100, 3, 70], page, 8, torch.Generator().manual_seed(1))
+    pages = dict(k_cache=rand(g, table[1], page, G, dim, dtype=dtype), v_cache=rand(g, table[1], page, G, dim, dtype=dtype),
+                 page_table=table[0], lengths=lengths)
+    rot = dict(q=rand(g, b, T, H, dim, dtype=dtype), k=rand(g, b, T, G, dim, dtype=dtype), v=rand(g, b, T, G, dim, dtype=dtype),
+               inv_freq=rand(g, dim // 2).abs(), **{k: v.clone() for k, v in pages.items()})
+    att = dict(q=rand(g, b, T, H, dim, dtype=dtype), **pages)
+    return {"causal_conv": (rsm.causal_conv, conv, ["cache"]), "causal_conv_step": (rsm.causal_conv_step, step, ["cache"]),
+            "rotary_append": (rsm.rotary_append, rot, ["k_cache", "v_cache"]), "paged_attention": (rsm.paged_attention, att, [])}
+
+
+NAMES = ["causal_conv", "causal_conv_step", "rotary_append", "paged_attention"]
+
+
+def run(name, change=None, **kw):
+    """(output, tensors written) of the operator on fresh tensors; `change`: {argument: tensor}."""
+    f, t, written = calls()[name]
+    t = t | (change or {})
+    return f(**t, **kw), [t[n] for n in written]
+
+
+def same(a, b):
+    return torch.equal(a[0], b[0]) and all(torch.equal(x, y) for x, y in zip(a[1], b[1]))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_both_ways_into_the_library(name):
+    """The C++ side's calls and Python's give the same bits: results allocated or passed, a status word, a stream."""
+    want = run(name)
+    assert same(run(name, out=torch.empty_like(want[0])), want)
+    status = word()
+    assert same(run(name, device_status=status), want) and int(status) == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    got = run(name, stream=side)
+    torch.cuda.synchronize()
+    assert same(got, want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_raw_stream_needs_results(name):
+    side = torch.cuda.Stream()
+    with pytest.raises(ValueError, match="raw stream"):
+        run(name, stream=side.cuda_stream)
+
+
+@pytest.mark.parametrize("name", ["causal_conv", "causal_conv_step"])
+@pytest.mark.parametrize("pad", [2 ** 32 - 1, 2 ** 31, -2 ** 31 - 1, 2 ** 70])
+def test_a_pad_slot_past_32_bits_is_refused(name, pad):
+    with pytest.raises(ValueError, match="pad_slot_id"):
+        run(name, pad_slot_id=pad)
+
+
+@pytest.mark.parametrize("name,args", [("causal_conv", ["x", "weight", "bias", "cache"]),
+                                       ("causal_conv_step", ["x", "weight", "bias", "cache"]),
+                                       ("rotary_append", ["q", "k", "v", "inv_freq", "k_cache", "v_cache"]),
+                                       ("paged_attention", ["q", "k_cache", "v_cache"])])
+def test_a_gradient_that_would_be_lost_is_refused(name, args):
+    want = run(name)
+    for arg in args:
+        t = {arg: calls()[name][1][arg].clone().requires_grad_()}
+        for way in ({}, {"out": torch.empty_like(want[0])}):
+            with pytest.raises(ValueError, match="forward only"):
+                run(name, t, **way)
+            with torch.no_grad():
+                t[arg] = calls()[name][1][arg].clone().requires_grad_()
+                assert same(run(name, t, **way), want)
+
+
+@pytest.mark.parametrize("name,change,msg", [
+    ("causal_conv", dict(cache=lambda t: t["cache"][:1].expand(3, 6, 264)), "overlap"),
+    ("causal_conv_step", dict(cache=lambda t: t["cache"][:1].expand(3, 6, 264)), "overlap"),
+    ("causal_conv", dict(cache=lambda t: t["cache"].float()), "cache must be"),
+    ("causal_conv", dict(slots=lambda t: None, positions=lambda t: None), "go together"),
+    ("causal_conv", dict(cache=lambda t: None, slots=lambda t: None), "positions need a cache"),
+    ("causal_conv", dict(cache=lambda t: t["cache"][:, :2].contiguous()), "cache_rows"),
+    ("causal_conv_step", dict(cache=lambda t: t["cache"][:, :4].contiguous()), "cache_rows"),
+    ("causal_conv", dict(weight=lambda t: t["weight"].repeat(1, 2)), "width"),
+    ("causal_conv_step", dict(slots=lambda t: t["slots"].long()), "slots must be"),
+    ("causal_conv_step", dict(positions=lambda t: t["positions"][:2]), "positions must be"),
+    ("rotary_append", dict(k_cache=lambda t: t["k_cache"][:1].expand_as(t["k_cache"])), "overlap"),
+    ("rotary_append", dict(v_cache=lambda t: t["v_cache"][:, :8]), "one shape"),
+    ("rotary_append", dict(inv_freq=lambda t: torch.ones(33, device="cuda")), "rotary_dim"),
+    ("paged_attention", dict(k_cache=lambda t: t["k_cache"].transpose(2, 3).contiguous().transpose(2, 3)), "contiguous"),
+    ("paged_attention", dict(page_table=lambda t: t["page_table"].long()), "page_table must be"),
+    ("paged_attention", dict(page_table=lambda t: t["page_table"].t().contiguous().t()), "page_table must be"),
+    ("paged_attention", dict(page_table=lambda t: t["page_table"][:2]), "page_table must be"),
+    ("paged_attention", dict(lengths=lambda t: t["lengths"].long()), "lengths must be"),
+    ("paged_attention", dict(q=lambda t: t["q"][:, :, :3].contiguous()), "num_kv_heads"),
+    ("paged_attention", dict(k_cache=lambda t: t["k_cache"].float()), "k_cache must be")])
+def test_refusals(name, change, msg):
+    t = calls()[name][1]
+    with pytest.raises((ValueError, rsm.ReplaySSMError), match=msg):
+        run(name, {k: f(t) for k, f in change.items()})
+
+
+def test_results_that_overlap_are_refused():
+    t = calls()["causal_conv"][1]
+    with pytest.raises(rsm.ReplaySSMError, match="out must not be x"):
+        rsm.causal_conv(**t, out=t["x"])
+    with pytest.raises(ValueError, match="rows of out overlap"):
+        rsm.causal_conv(**t, out=torch.empty(264, device="cuda", dtype=BF16).expand(40, 264))
+    t = calls()["rotary_append"][1]
+    with pytest.raises(ValueError, match="overlap"):
+        rsm.rotary_append(**t, out=torch.empty(4, 64, device="cuda", dtype=BF16).expand(3, 2, 4, 64))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_and_replayed_on_changed_inputs(name):
+    """A captured call reads its tensors when it is replayed: other values, and other lengths and positions."""
+    f, t, written = calls()[name]
+    keep = {k: v.clone() for k, v in t.items()}
+    f(**t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f(**t)
+    other = calls(seed=5)[name][1]
+    for change in ({}, dict(positions=i32([3, 0, 1])), dict(lengths=i32([2, 90, 0])), dict(lengths=i32([128, 128, 128]))):
+        for k in t:
+            if k not in ("page_table", "cu_seqlens", "slots"):
+                t[k].copy_(change.get(k, other[k] if change else keep[k]))
+        if "page_table" in t:
+            t["page_table"].copy_(torch.arange(24, device="cuda", dtype=torch.int32).view(3, 8) % t["k_cache"].shape[0])
+            if name == "rotary_append":  # (requests write to pages of their own)
+                t["page_table"].copy_(torch.arange(3, device="cuda", dtype=torch.int32)[:, None].expand(3, 8))
+        fresh = {k: v.clone() for k, v in t.items()}
+        graph.replay()
+        want = f(**fresh)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and all(torch.equal(t[n], fresh[n]) for n in written), change
+
+
+def test_calls_from_two_threads_on_their_streams():
+    """Each thread's calls get what they get alone, whichever kernel is set up first."""
+    want = {n: run(n) for n in NAMES}
+    wrong = []
+
+    def work():
+        torch.cuda.set_device(0)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for k in range(60):
+                for n in NAMES:
+                    got = run(n)
+                    torch.cuda.current_stream().synchronize()
+                    if not same(got, want[n]):
+                        wrong.append((n, k))
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
+
+
+# ----------------------------------------------------------------------------
+# convolution
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("C", [264, 33])
+def test_conv_values_of_other_sequences_do_not_matter(C):
+    """NaN in a neighbour's tokens, in rows outside every sequence, in cache rows of no use and in other slots."""
+    nan = float("nan")
+    cu = [0, 9, 50, 50, 51, 90]
+    x, w, b, cache = base.conv_world(C, 4, 6, 5, 100, BF16, 3)
+    pos = [0, 2, 5, 1, 3]
+    x[9:50] = nan
+    x[90:] = nan
+    cache[2:] = nan
+    cache[1, [r for r in range(6) if r not in (9 % 6, 8 % 6, 7 % 6)]] = nan  # (position 0: nothing is looked up)
+    cache[4, 0] = 1.0  # position 1 looks back to row 0 only
+    cache[5, [0, 1, 2]] = 0.5
+    y, m, want = ref.conv(x, w, b, cache, [1, 2, 3, 4, 5], pos, list(zip(cu, cu[1:])), True, 3)
+    out = torch.full_like(x, 7.0)
+    rsm.causal_conv(x, w, i32(cu), b, cache, i32([1, 2, 3, 4, 5]), i32(pos), out=out)
+    good = [i for i in range(90) if not 9 <= i < 50]
+    close(out[good], y[good], base.conv_bound(y, m, 4, BF16, 1)[good])
+    assert bool((out[90:] == 7).all()) and bool(out[9:50].isnan().all())
+    assert torch.equal(cache.isnan(), want.isnan()) and torch.equal(cache.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("C", [264, 33])
+@pytest.mark.parametrize("cu", [[70, 75, 90], [1, 1, 3], [95, 96, 100], [47, 50, 51], [3, 3, 3], [0, 0, 100]])
+def test_conv_rows_outside_the_sequences(C, cu):
+    """Tokens before the first sequence and behind the last are nobody's: their rows stay, and a sequence is read and
+    its inputs are stored once, wherever blocks of tokens begin."""
+    x, w, b, cache = base.conv_world(C, 4, 3, 2, 100, BF16, 3)
+    spans = list(zip(cu, cu[1:]))
+    y, m, want = ref.conv(x, w, b, cache, [1, 2], [4, 7], spans, True, 3)
+    out, status = torch.full_like(x, 7.0), word()
+    rsm.causal_conv(x, w, i32(cu), b, cache, i32([1, 2]), i32([4, 7]), out=out, device_status=status)
+    inside = [i for a, e in spans for i in range(a, e)]
+    close(out[inside], y[inside], base.conv_bound(y, m, 4, BF16, 1)[inside])
+    outside = [i for i in range(100) if i not in inside]
+    assert bool((out[outside] == 7).all()) and torch.equal(cache, want) and int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_conv_extreme_values(dtype):
+    """silu far out: large inputs come through, large negative ones are -0 or tiny; infinities as the formula has it."""
+    big = 3e38 if dtype == F32 else 3e38
+    x = torch.tensor([[0.0], [100.0], [-100.0], [1e4], [-1e4], [big], [-big], [float("inf")]], device="cuda").to(dtype).repeat(1, 8)
+    w = torch.zeros(8, 4, device="cuda")
+    w[:, 3] = 1.0
+    y = rsm.causal_conv(x, w, i32([0, 8]))
+    v = x.double()
+    want = v * torch.sigmoid(v)
+    ok = want.isfinite()
+    close(torch.where(ok, y, 0), torch.where(ok, want, 0.0), 2.0 ** -7 * want.abs().nan_to_num(0, 0, 0) * (1 if dtype == BF16 else 2.0 ** -12) + 1e-30)
+    assert bool((y[7] == float("inf")).all() | y[7].isnan().all())
+
+
+def test_conv_positions_wrap_in_the_cache():
+    """A step at every phase of a ring of seven rows equals one prompt."""
+    x, w, b, cache = base.conv_world(264, 4, 7, 1, 40, BF16, 9)
+    whole = rsm.causal_conv(x, w, i32([0, 40]), b)
+    outs = [rsm.causal_conv_step(x[t:t + 1], w, cache, i32([1]), i32([t]), b) for t in range(40)]
+    assert torch.equal(torch.cat(outs), whole)
+
+
+def test_conv_more_than_2_31_values():
+    """A cache and a prompt whose offsets pass 32 bits; only the ends are looked at."""
+    C, R = 32768, 8
+    S = 2 ** 31 // (C * R) + 3
+    cache = torch.zeros(S, R, C, device="cuda", dtype=BF16)
+    T = 2 ** 31 // C + 37
+    x = torch.zeros(T, C, device="cuda", dtype=BF16)
+    x[-20:] = rand(gen(1), 20, C, dtype=BF16)
+    cache[S - 1] = rand(gen(2), R, C, dtype=BF16)
+    before = cache[S - 1].clone()
+    w, b = rand(gen(3), C, 4), rand(gen(4), C)
+    y = rsm.causal_conv(x, w, i32([0, T - 20, T]), b, cache, i32([-1, S - 1]), i32([0, 5]))
+    small = before[None].clone()
+    want = rsm.causal_conv(x[-20:].clone(), w, i32([0, 20]), b, small, i32([0]), i32([5]))
+    assert torch.equal(y[-20:], want) and torch.equal(cache[S - 1], small[0])
+    got = rsm.causal_conv_step(x[-1:], w, cache, i32([S - 1]), i32([25]), b)
+    assert torch.equal(got, rsm.causal_conv_step(x[-1:].clone(), w, small, i32([0]), i32([25]), b))
+
+
+# ----------------------------------------------------------------------------
+# rotary
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tokens", [1, 2431, 2433, 5000])
+def test_rotary_few_and_many_tokens(tokens):
+    """The two kernels, on either side of where they take turns (16 tokens an SM), skipped requests among them."""
+    H, G, dim, n, page = 4, 2, 64, 32, 64
+    b = 3 if tokens > 3 else 1
+    cu = [0, tokens // 3, tokens // 3, tokens] if b == 3 else [0, 1]
+    new = [q - p for p, q in zip(cu, cu[1:])]
+    lengths = [7 + m for m in new]
+    table, pages = ref.table(lengths, page, 0, torch.Generator().manual_seed(1))
+    if b == 3:
+        lengths[0] = 0
+    g = gen(tokens)
+    kc, vc = base.pools(g, pages, page, G, dim, BF16, True)
+    before = kc.clone(), vc.clone()
+    q, k, v = rand(g, tokens, H, dim, dtype=BF16), rand(g, tokens, G, dim, dtype=BF16), rand(g, tokens, G, dim, dtype=BF16)
+    freq, _ = rsm.rotary_frequencies(2 * n)
+    status = word()
+    got = rsm.rotary_append(q, k, v, freq, kc, vc, table, i32(lengths), i32(cu), device_status=status)
+    assert int(status) == 0
+    base.rotary_check(q, k, v, freq, list(zip(cu, cu[1:])), lengths, table, kc, vc, False, 1.0, got, before,
+                      (0,) if b == 3 else ())
+
+
+def test_rotary_negative_and_large_frequencies():
+    """A frequency of any sign and size counts modulo a turn."""
+    dim, page, far = 64, 16, 1000000
+    freq = torch.linspace(-40.0, 40.0, dim // 2, device="cuda") + 0.01
+    q, k, v = (rand(gen(i), 2, 2, dim) for i in (1, 2, 3))
+    table = torch.full((2, far // page + 1), -1, dtype=torch.int32)
+    table[0, (far - 1) // page], table[1, 0] = 0, 1
+    kc, vc = base.pools(gen(4), 2, page, 2, dim, F32, False)
+    before = kc.clone(), vc.clone()
+    got = rsm.rotary_append(q, k, v, freq, kc, vc, table.cuda(), i32([far, 2]))
+    base.rotary_check(q, k, v, freq, [(0, 1), (1, 2)], [far, 2], table.cuda(), kc, vc, False, 1.0, got, before)
+
+
+@pytest.mark.parametrize("H,G,dim", [(128, 16, 256), (300, 50, 256)])
+def test_rotary_long_tokens(H, G, dim):
+    """Tokens of which a ring holds few, and of which it holds none (fp32)."""
+    T = 2600
+    g = gen(1)
+    lengths = [T]
+    table, pages = ref.table(lengths, 64, 0, torch.Generator().manual_seed(1))
+    kc, vc = base.pools(g, pages, 64, G, dim, F32, False)
+    before = kc.clone(), vc.clone()
+    q, k, v = rand(g, T, H, dim), rand(g, T, G, dim), rand(g, T, G, dim)
+    freq, _ = rsm.rotary_frequencies(dim)
+    got = rsm.rotary_append(q, k, v, freq, kc, vc, table, i32(lengths), i32([0, T]), interleaved=True)
+    base.rotary_check(q, k, v, freq, [(0, T)], lengths, table, kc, vc, True, 1.0, got, before)
+
+
+# ----------------------------------------------------------------------------
+# attention
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (F32, 64), (BF16, 40)])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30, 3.0])
+def test_attention_scales(dtype, dim, scale):
+    lengths = [200, 33, 64]
+    q, kc, vc, table = base.attention_world(lengths, 2, 4, 2, dim, 16, dtype, False, 21)
+    base.attention_check(q, kc, vc, table, lengths, rsm.paged_attention(q, kc, vc, table, i32(lengths), scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("T", [33, 130])
+def test_attention_many_new_tokens(T, dtype, dim):
+    """Windows whose rows are several units of a key head, from the request's first token on."""
+    lengths = [T, 200, T + 1]
+    q, kc, vc, table = base.attention_world(lengths, T, 6, 2, dim, 16, dtype, True, T)
+    base.attention_check(q, kc, vc, table, lengths, rsm.paged_attention(q, kc, vc, table, i32(lengths)))
+
+
+def test_attention_does_the_same_twice():
+    lengths = [3001, 17, 900, 64]
+    q, kc, vc, table = base.attention_world(lengths, 2, 8, 2, 128, 16, BF16, False, 5)
+    want = rsm.paged_attention(q, kc, vc, table, i32(lengths))
+    for _ in range(20):
+        assert torch.equal(rsm.paged_attention(q, kc, vc, table, i32(lengths)), want)
+
+
+def workspace_bytes(q, kc, table):
+    a = hybrid.PagedAttentionArgs()
+    a.requests, a.table_width, a.num_pages, a.page_size = *table.shape, *kc.shape[:2]
+    a.window, a.num_heads, a.num_kv_heads, a.dim, a.input_dtype = q.shape[1], q.shape[2], kc.shape[2], q.shape[3], rsm.RSM_BF16
+    return hybrid._load().rsm_paged_attention_workspace(bytes(a))
+
+
+def test_attention_workspace():
+    """One of the bytes asked for is enough, and what lies behind it stays; less, or off 256 bytes, is refused; a table
+    of one tile needs none."""
+    lengths = [3001, 17, 900, 64]
+    q, kc, vc, table = base.attention_world(lengths, 2, 8, 2, 128, 16, BF16, False, 5)
+    want, n = rsm.paged_attention(q, kc, vc, table, i32(lengths)), workspace_bytes(q, kc, table)
+    room = torch.full((n + 4096,), 77, dtype=torch.uint8, device="cuda")
+    got = rsm.paged_attention(q, kc, vc, table, i32(lengths), workspace=room[:n])
+    assert torch.equal(got, want) and bool((room[n:] == 77).all())
+    for bad in (room[:n - 1], room[16:16 + n]):
+        with pytest.raises(rsm.ReplaySSMError, match="workspace"):
+            rsm.paged_attention(q, kc, vc, table, i32(lengths), workspace=bad)
+    assert workspace_bytes(q, kc, table[:, :4]) == 0
+
+
+def test_attention_lengths_past_the_first_tile_of_many_requests():
+    """More requests than a CTA has threads, most of them empty or short, some long: where the work is dealt out."""
+    g = torch.Generator().manual_seed(3)
+    lengths = [int(n) for n in torch.randint(0, 4, (700,), generator=g)]
+    for r, n in ((0, 900), (127, 65), (128, 640), (300, 64), (511, 2000), (699, 130)):
+        lengths[r] = n
+    q, kc, vc, table = base.attention_world(lengths, 1, 4, 2, 64, 16, BF16, False, 5)
+    base.attention_check(q, kc, vc, table, lengths, rsm.paged_attention(q, kc, vc, table, i32(lengths)))
+
+
+def test_attention_table_rows_apart():
+    """A page table that is a slice of a wider one, and K and V that are slices of layers' common pool."""
+    lengths = [100, 3, 65]
+    q, kc, vc, table = base.attention_world(lengths, 1, 4, 2, 64, 16, BF16, False, 5)
+    wide = torch.full((3, 50), 10 ** 6, dtype=torch.int32, device="cuda")
+    wide[:, 7:7 + table.shape[1]] = table
+    both = torch.stack([torch.zeros_like(kc), kc, vc], 1)
+    got = rsm.paged_attention(q, both[:, 1], both[:, 2], wide[:, 7:7 + table.shape[1]], i32(lengths))
+    assert torch.equal(got, rsm.paged_attention(q, kc, vc, table, i32(lengths)))
+
+
+@pytest.mark.parametrize("page", [16, 8])
+def test_attention_pages_past_2_31_values(page):
+    """Pages whose offsets pass 32 bits, by boxes and by rows."""
+    G, dim, n = 16, 128, 300
+    pages = 2 ** 31 // (page * G * dim) + 40
+    kc, vc = (torch.zeros(pages, page, G, dim, device="cuda", dtype=BF16) for _ in range(2))
+    need = -(-n // page)
+    at = torch.arange(pages - need, pages, device="cuda")
+    kc[at], vc[at] = rand(gen(1), need, page, G, dim, dtype=BF16), rand(gen(2), need, page, G, dim, dtype=BF16)
+    q = rand(gen(3), 1, 1, 32, dim, dtype=BF16, scale=2.0)
+    got = rsm.paged_attention(q, kc, vc, at[None].int(), i32([n]))
+    few = torch.arange(need, device="cuda", dtype=torch.int32)[None]
+    assert torch.equal(got, rsm.paged_attention(q, kc[at].clone(), vc[at].clone(), few, i32([n])))
+    freq, _ = rsm.rotary_frequencies(dim)
+    new = [rand(gen(i), 1, 1, h, dim, dtype=BF16) for i, h in ((5, 32), (6, G), (7, G))]
+    k2, v2 = kc[at].clone(), vc[at].clone()
+    a = rsm.rotary_append(*new, freq, kc, vc, at[None].int(), i32([n]))
+    assert torch.equal(a, rsm.rotary_append(*new, freq, k2, v2, few, i32([n])))
+    assert torch.equal(kc[at], k2) and torch.equal(vc[at], v2)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (F32, 64), (BF16, 40)])
+def test_attention_scores_that_are_infinite(dtype, dim):
+    """A key that makes a score -infinity takes no weight; one that makes it +infinity makes the row NaN, as the
+    quotient of infinities is; other heads and requests are as ever."""
+    lengths = [70, 70]
+    q, kc, vc, table = base.attention_world(lengths, 1, 4, 4, dim, 16, dtype, False, 5)
+    q = q.abs() + 0.1
+    want = rsm.paged_attention(q, kc, vc, table, i32(lengths))
+    k2 = kc.clone()
+    k2[table[0, 1].item(), 3, 1] = -float("inf")
+    got = rsm.paged_attention(q, k2, vc, table, i32(lengths))
+    lone = [i for i in range(70) if i != 19]
+    p = torch.tensor(lone, device="cuda")
+    k = kc[table[0, p // 16].long(), p % 16, 1].double()
+    w = torch.softmax(k @ q[0, 0, 1].double() * dim ** -0.5, 0)
+    v = vc[table[0, p // 16].long(), p % 16, 1].double()
+    m = w @ v.abs()
+    top = (k.abs() @ q[0, 0, 1].double().abs()).max() * dim ** -0.5
+    close(got[0, 0, 1], w @ v, base.attention_bound(w @ v, m, top, dim, 70, dtype))
+    k2[table[0, 1].item(), 3, 1] = float("inf")
+    odd = rsm.paged_attention(q, k2, vc, table, i32(lengths))
+    assert bool(odd[0, 0, 1].isnan().all())
+    for y in (got, odd):
+        y[0, 0, 1] = want[0, 0, 1]
+        assert torch.equal(y, want)
+
+
+def test_nothing_to_do():
+    z = lambda *s, t=BF16: torch.zeros(s, device="cuda", dtype=t)  # noqa: E731
+    w, none = z(8, 4, t=F32), torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert rsm.causal_conv(z(0, 8), w, i32([0])).shape == (0, 8)
+    assert rsm.causal_conv(z(0, 8), w, i32([0, 0]), None, z(1, 3, 8), i32([0])).shape == (0, 8)
+    assert rsm.causal_conv_step(z(0, 8), w, z(1, 4, 8), none, none).shape == (0, 8)
+    kc, table = z(2, 4, 1, 8), torch.zeros(0, 1, dtype=torch.int32, device="cuda")
+    assert rsm.rotary_append(z(0, 2, 8), z(0, 1, 8), z(0, 1, 8), z(4, t=F32), kc, kc.clone(), table, none).shape == (0, 2, 8)
+    assert rsm.paged_attention(z(0, 2, 8), kc, kc, table, none).shape == (0, 2, 8)
+    y = rsm.paged_attention(torch.ones(2, 2, 64, device="cuda"), z(0, 4, 1, 64, t=F32), z(0, 4, 1, 64, t=F32),
+                            torch.zeros(2, 0, dtype=torch.int32, device="cuda"), i32([0, 0]))
+    assert bool((y == 0).all())
+    rsm.copy_pages(rsm.pointer_table([kc]), rsm.stride_table([kc]), none, none, dtype=BF16, page_elements=32, num_pages=2)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (F32, 64), (F32, 128), (BF16, 40)])
+@pytest.mark.parametrize("inf", [float("inf"), -float("inf")])
+def test_attention_values_that_are_infinite(dtype, dim, inf):
+    """An infinite value that a row sees makes its column infinite, and no other."""
+    lengths = [150, 70]
+    q, kc, vc, table = base.attention_world(lengths, 3, 4, 2, dim, 16, dtype, False, 5)
+    want = rsm.paged_attention(q, kc, vc, table, i32(lengths))
+    v2 = vc.clone()
+    v2[table[0, 2].item(), 3, 1, 7] = inf      # token 35 of request 0, seen by all its rows
+    v2[table[1, 4].item(), 4, 0, 3] = inf      # token 68 of request 1: seen by its last two
+    got = rsm.paged_attention(q, kc, v2, table, i32(lengths))
+    assert bool((got[0, :, 2:, 7] == inf).all()) and bool((got[1, 1:, :2, 3] == inf).all())
+    got[0, :, 2:, 7], got[1, 1:, :2, 3] = want[0, :, 2:, 7], want[1, 1:, :2, 3]
+    assert torch.equal(got, want)
