@@ -9,33 +9,35 @@ struct Kernels {
   const void *tiles, *boxes, *join;
 };
 
-template <int DIM, int N>
-Kernels bf16() {
-  using Math = AttnBf16<DIM, N>;
+template <typename Math, int DIM>
+Kernels kernels() {
   return {reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, false>), reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, true>),
           reinterpret_cast<const void*>(&attn_join_kernel<Math, DIM>)};
 }
 
 template <int DIM>
-Kernels f32() {
-  using Math = AttnF32<DIM>;
-  return {reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, false>), nullptr, reinterpret_cast<const void*>(&attn_join_kernel<Math, DIM>)};
+Kernels bf16(int rows) {
+  if (rows == 8) return kernels<AttnBf16<DIM, 1>, DIM>();
+  if constexpr (DIM < 256) {
+    if (rows == 24) return kernels<AttnBf16<DIM, 3>, DIM>();
+    if (rows == 32) return kernels<AttnBf16<DIM, 4>, DIM>();
+  }
+  return kernels<AttnBf16<DIM, 2>, DIM>();
 }
 
 template <int DIM>
-Kernels pick_rows(int rows) {
-  switch (rows) {
-    case 8: return bf16<DIM, 1>();
-    case 16: return bf16<DIM, 2>();
-    case 24: return bf16<DIM, 3>();
-    default: return bf16<DIM, 4>();
+Kernels f32(int rows) {
+  if (rows == 1) return kernels<AttnF32<DIM, 1>, DIM>();
+  if (rows == 2) return kernels<AttnF32<DIM, 2>, DIM>();
+  if constexpr (DIM < 256) {
+    if (rows == 8) return kernels<AttnF32<DIM, 8>, DIM>();
   }
+  return kernels<AttnF32<DIM, 4>, DIM>();
 }
 
 Kernels pick(int input_dtype, int dim, int rows) {
-  if (input_dtype == RSM_F32) return dim == 64 ? f32<64>() : f32<128>();
-  if (dim == 256) return rows == 8 ? bf16<256, 1>() : bf16<256, 2>();
-  return dim == 64 ? pick_rows<64>(rows) : pick_rows<128>(rows);
+  if (input_dtype == RSM_F32) return dim == 64 ? f32<64>(rows) : dim == 128 ? f32<128>(rows) : f32<256>(rows);
+  return dim == 64 ? bf16<64>(rows) : dim == 128 ? bf16<128>(rows) : bf16<256>(rows);
 }
 
 }  // namespace

@@ -6,19 +6,23 @@
 //
 // Memory bounds it: 8 rows of 128 columns make 8 multiplications of a byte of keys and
 // values.  So the cache is what is organised.  A CTA has four warps, and
-// each streams 16 tokens at a time through shared memory of its own, S stages ahead
-// (boxes of 16 rows by TMA where pages are whole groups of 16 tokens, else cp.async):
-// no barrier of the CTA holds a load back, and warps are joined only at the end of
+// each streams a step of 8 to 32 tokens (16 KB or 8) at a time through shared memory of its
+// own, S stages ahead (boxes of a step's rows by TMA where pages are whole steps, else
+// cp.async): no barrier of the CTA holds a load back, and warps are joined only at the end of
 // a request's part.  The running maximum is one only to within 2^8: it is taken, and sums and
 // outputs scaled anew, where a score passes it by more, which takes a few steps of a
 // request instead of all.
 //
-// The products are m16n8k16 (bf16) and m16n8k8 (tf32) instructions on registers: with a
-// few rows a 128-row tcgen05 tile would be mostly empty.  bf16 takes the products the other
-// way round, S^T = K Q^T and O^T = V^T P^T, so that rows come in eights, and turns P^T
-// between them with movmatrix.
+// The bf16 products are m16n8k16 instructions on registers: with a few rows a 128-row tcgen05
+// tile would be mostly empty.  They are taken the other way round, S^T = K Q^T and
+// O^T = V^T P^T, so that rows come in eights, with P^T turned between them by
+// movmatrix.  The fp32 products run on the CUDA cores, in pairs (fma.rn.f32x2): three tf32
+// products each would take three times the instructions, most of them to split the operands.
 //
-// The work of a call is its (request, key head, group of rows) units' tiles of 64 tokens,
+// Head sizes between the compiled ones (64, 128, 256) are padded with zeros on the chip; the
+// padding is not read from memory.
+//
+// The work of a call is its (request, key head, group of rows) units' tiles of four steps,
 // one after the other, and with each unit kAttnUnit tiles more for what its end takes; every CTA
 // takes the same number of them, wherever they begin and end, so that lengths (which only
 // the device knows) may differ as they like.  A unit that a CTA has to itself is finished
@@ -32,7 +36,9 @@
 
 namespace hybrid {
 
-__device__ __forceinline__ int tiles_of(int64_t len) { return static_cast<int>((len + kAttnTile - 1) / kAttnTile); }
+__device__ __forceinline__ int tiles_of(const AttnParams& p, int64_t len) {
+  return static_cast<int>((len + (1 << p.tile_shift) - 1) >> p.tile_shift);
+}
 
 // What a unit of that many tiles counts.
 __device__ __forceinline__ int64_t counts(int tiles) { return tiles == 0 ? 0 : tiles + kAttnUnit; }
@@ -56,7 +62,7 @@ struct Deal {
   int64_t own, total;  // own: of request threadIdx.x
   __device__ __forceinline__ static int64_t of(const AttnParams& p, int b, bool report) {
     if (b >= p.pages.requests) return 0;
-    return counts(tiles_of(request_tokens(p.pages, b, p.window, p.status, report))) * (p.G * p.row_tiles);
+    return counts(tiles_of(p, request_tokens(p.pages, b, p.window, p.status, report))) * (p.G * p.row_tiles);
   }
   // (One use for each WHICH: its place is written once.)
   template <int WHICH>
@@ -142,34 +148,11 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Lane 4 i + j's values (i, 2 j) and (i, 2 j + 1) of an 8 x 8 matrix become (2 j, i) and (2 j + 1, i).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
-}
-__device__ __forceinline__ uint32_t to_tf32(float v) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-  return r;
-}
-// v = hi + lo to 22 bits
-__device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) {
-  hi = to_tf32(v);
-  lo = to_tf32(v - __uint_as_float(hi));
-}
-// The same for keys and values, which may be infinite: then lo is 0, and so is `other`, elsewhere hi,
-// which is what the other operand's lo is multiplied with (its sign would make the sum NaN).
-__device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo, uint32_t& other) {
-  split_tf32(v, hi, lo);
-  const bool finite = (hi & 0x7F800000u) != 0x7F800000u;
-  lo = finite ? lo : 0u;
-  other = finite ? hi : 0u;
 }
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
@@ -177,16 +160,12 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
-// Where a 16-byte chunk of a token's row lies: boxes of 16 rows of 128 bytes, the chunks
-// of a row in an order of its own (the boxes' 128-byte swizzle; keys of fp32 another), so
-// that what the lanes of an instruction read lies in different banks.
-template <typename IT>
-__device__ __forceinline__ int key_chunk(int token, int chunk) {
-  const int order = sizeof(IT) == 2 ? token & 7 : (token & 1) << 2 | (token >> 1 & 3);
-  return (chunk >> 3) * (kAttnStep * 128) + token * 128 + ((chunk & 7) ^ order) * 16;
-}
-__device__ __forceinline__ int value_chunk(int token, int chunk) {
-  return (chunk >> 3) * (kAttnStep * 128) + token * 128 + ((chunk & 7) ^ (token & 7)) * 16;
+// Where a 16-byte chunk of a token's row lies: boxes of a step's rows of 128 bytes, the chunks
+// of a row in the order of the boxes' 128-byte swizzle, so that what the lanes of an
+// instruction read lies in different banks.
+template <int STEP>
+__device__ __forceinline__ int chunk_at(int token, int chunk) {
+  return (chunk >> 3) * (STEP * 128) + token * 128 + ((chunk & 7) ^ (token & 7)) * 16;
 }
 
 constexpr float kAttnSlack = 8.0f;
@@ -195,11 +174,12 @@ constexpr uint64_t kAttnTimeoutNs = 2000000000ull;  // of a wait that takes micr
 
 template <typename IT, int DIM>
 struct AttnShape {
+  static constexpr int kStep = attn_step(sizeof(IT), DIM);                 // a warp's tokens of a stage
   static constexpr int kChunks = DIM * static_cast<int>(sizeof(IT)) / 16;  // of a row
-  static constexpr int kHalf = kAttnStep * DIM * static_cast<int>(sizeof(IT));  // a warp's keys of a stage
+  static constexpr int kHalf = kStep * DIM * static_cast<int>(sizeof(IT));  // a warp's keys of a stage
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = attn_stages(sizeof(IT), DIM);
-  static constexpr int kQuery = sizeof(IT) == 4 ? 2 * 16 * DIM * 4 : 0;    // fp32: Q's parts as the products take them
+  static constexpr int kStages = kAttnStages;
+  static constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : (1u << kStep) - 1u;
 };
 
 // A place among the tiles, as one walks along them: request, key head, rows, tile.
@@ -207,7 +187,7 @@ struct AttnCursor {
   int b, g, rt, tile, tiles, len;
   __device__ __forceinline__ void at_request(const AttnParams& p) {
     len = static_cast<int>(request_tokens(p.pages, b, p.window, nullptr, false));
-    tiles = tiles_of(len);
+    tiles = tiles_of(p, len);
   }
   __device__ __forceinline__ void next_unit(const AttnParams& p) {
     tile = 0;
@@ -224,34 +204,37 @@ struct AttnCursor {
     if (++tile == tiles) next_unit(p);
   }
   // Row r of the unit: its queries (null: there is none) and the last token that it sees.
-  template <typename IT, int DIM>
+  template <typename IT>
   __device__ __forceinline__ const IT* query(const AttnParams& p, int rows, int row, int& last) const {
     const int r = rt * rows + row, t = r / p.per;
     last = len - p.window + t;
     if (r >= p.per * p.window) return nullptr;
-    return static_cast<const IT*>(p.q) + b * p.q_bs + t * p.q_ts + static_cast<int64_t>(g * p.per + r - t * p.per) * DIM;
+    return static_cast<const IT*>(p.q) + b * p.q_bs + t * p.q_ts + static_cast<int64_t>(g * p.per + r - t * p.per) * p.dim;
   }
 };
 
-// What a warp has seen of a step: 16 tokens at token0, those of the bits `seen`.
+// A stage of a warp as its products take it: the tokens from `row`, the first of which is the
+// request's token0; those of the bits `seen` (from bit 0 on) are there.
 struct AttnStep {
   uint32_t keys, values;  // shared memory
   char* held;             // the values, to change them
   uint32_t seen;
-  int token0;
+  int row, token0;
   bool differ;            // rows differ in what they see
-  int first_new;          // of the 16, the first that is not seen by all rows
+  int first_new;          // of these tokens, the first that is not seen by all rows
 };
 
 // New tokens' values that are not finite go to the rows that see them, by add(token), and not
-// into the product, where a weight of zero would not keep them from the others.
-template <typename IT, int DIM, typename F>
+// into the product, where a weight of zero would not keep them from the others.  TOKENS from a.row on.
+template <typename IT, int DIM, int TOKENS, typename F>
 __device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
-  constexpr int kChunks = AttnShape<IT, DIM>::kChunks;
+  using Shape = AttnShape<IT, DIM>;
+  constexpr int kChunks = Shape::kChunks;
   bool odd = false;
-  for (int c = lane; c < kAttnStep * kChunks; c += 32) {
-    if ((c >> 3) % kAttnStep < a.first_new) continue;
-    const uint4 v = rsm::lds128(a.values + c * 16);
+  for (int c = lane; c < TOKENS * kChunks; c += 32) {
+    const int j = c / kChunks;
+    if (j < a.first_new) continue;
+    const uint4 v = rsm::lds128(a.values + chunk_at<Shape::kStep>(a.row + j, c % kChunks));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -260,12 +243,13 @@ __device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
     }
   }
   if (!__any_sync(0xFFFFFFFFu, odd)) return;
-  for (int j = a.first_new; j < kAttnStep; ++j)
+  for (int j = a.first_new; j < TOKENS; ++j)
     if (a.seen >> j & 1u) add(j);
   __syncwarp();
-  for (int c = lane; c < kAttnStep * kChunks; c += 32) {
-    if ((c >> 3) % kAttnStep < a.first_new) continue;
-    IT* v = reinterpret_cast<IT*>(a.held + c * 16);
+  for (int c = lane; c < TOKENS * kChunks; c += 32) {
+    const int j = c / kChunks;
+    if (j < a.first_new) continue;
+    IT* v = reinterpret_cast<IT*>(a.held + chunk_at<Shape::kStep>(a.row + j, c % kChunks));
 #pragma unroll
     for (int k = 0; k < 16 / static_cast<int>(sizeof(IT)); ++k)
       if (!isfinite(get(v + k))) v[k] = IT(0);
@@ -274,20 +258,26 @@ __device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
   __syncwarp();
 }
 
-template <typename IT>
+template <typename IT, int DIM>
 __device__ __forceinline__ float held_value(const AttnStep& a, int token, int column) {
   const int c = column * static_cast<int>(sizeof(IT));
-  return get(reinterpret_cast<const IT*>(a.held + value_chunk(token, c / 16) + c % 16));
+  return get(reinterpret_cast<const IT*>(a.held + chunk_at<AttnShape<IT, DIM>::kStep>(a.row + token, c / 16) + c % 16));
 }
 
 // A warp's part of a unit, bf16: 8 N rows.  Lane (quad, four) holds of S^T tokens quad and quad
-// + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.
+// + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.  Up to 16
+// rows' queries stay in registers, those of more (whose outputs take half of them) in shared memory.
 template <int DIM, int N>
 struct AttnBf16 {
   using IT = uint16_t;
-  static constexpr int kRows = 8 * N, kSteps = DIM / 16;
-  static constexpr int kChains = N == 1 ? 4 : N == 2 ? 2 : 1;  // sums that do not wait for one another
-  uint32_t q[N][kSteps][2];
+  using Shape = AttnShape<IT, DIM>;
+  static constexpr int kRows = 8 * N, kSteps = DIM / 16, kTokens = 16, kStep = Shape::kStep;
+  static constexpr bool kShared = attn_shared_queries(DIM, kRows);
+  static constexpr int kQuery = attn_query(2, DIM, kRows);
+  static constexpr int kChains = N == 1 ? 4 : 2;  // sums that do not wait for one another
+  static constexpr int kOwn = kShared ? (kRows * DIM / 8 + kAttnThreads - 1) / kAttnThreads : 1;  // a thread's chunks of the queries
+  uint32_t q[kShared ? 1 : N][kShared ? 1 : kSteps][2];
+  uint4 next[kOwn];
   int limit[N][2];
   float o[kSteps][N][4], m[N][2], l[N][2];
 
@@ -300,28 +290,60 @@ struct AttnBf16 {
       l[n][0] = l[n][1] = 0.0f;
     }
   }
-  __device__ __forceinline__ void queries(const AttnParams& p, const AttnCursor& at, int lane, char*) {
-    const int quad = lane >> 2, four = lane & 3;
+  // A unit's queries: asked for by fetch(), there after commit().
+  __device__ __forceinline__ void fetch(const AttnParams& p, const AttnCursor& at, int lane) {
+    if constexpr (kShared) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      int last;
+      for (int k = 0; k < kOwn; ++k) {
+        const int c = threadIdx.x + k * kAttnThreads, row = c / (DIM / 8), col = c % (DIM / 8) * 8;
+        next[k] = make_uint4(0, 0, 0, 0);
+        if (c >= kRows * DIM / 8 || col >= p.dim) continue;
+        int last;
+        const IT* from = at.query<IT>(p, kRows, row, last);
+        if (from == nullptr) continue;
+        if (p.q_wide) {
+          next[k] = *reinterpret_cast<const uint4*>(from + col);
+        } else {
+          uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) (void)at.query<IT, DIM>(p, kRows, 8 * n + 2 * four + e, limit[n][e]);
-      const IT* from = at.query<IT, DIM>(p, kRows, 8 * n + quad, last);
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t v = 0;
-          if (from != nullptr) {
-            const IT* s = from + 16 * ks + 8 * e + 2 * four;
-            v = p.q_pairs ? *reinterpret_cast<const uint32_t*>(s) : static_cast<uint32_t>(s[0]) | static_cast<uint32_t>(s[1]) << 16;
-          }
-          q[n][ks][e] = v;
+          for (int e = 0; e < 4; ++e) w[e] = static_cast<uint32_t>(from[col + 2 * e]) | static_cast<uint32_t>(from[col + 2 * e + 1]) << 16;
+          next[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+    } else {
+      const int quad = lane >> 2, four = lane & 3;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        int last;
+        const IT* from = at.query<IT>(p, kRows, 8 * n + quad, last);
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t v = 0;
+            const int c = 16 * ks + 8 * e + 2 * four;
+            if (from != nullptr && c < p.dim)
+              v = p.q_pairs ? *reinterpret_cast<const uint32_t*>(from + c) : static_cast<uint32_t>(from[c]) | static_cast<uint32_t>(from[c + 1]) << 16;
+            q[n][ks][e] = v;
+          }
+      }
     }
   }
-  __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, int lane, const char*) {
+  __device__ __forceinline__ void commit(const AttnParams& p, const AttnCursor& at, int lane, char* smem) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) (void)at.query<IT>(p, kRows, 8 * n + 2 * (lane & 3) + e, limit[n][e]);
+    if constexpr (kShared) {
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k) {
+        const int c = threadIdx.x + k * kAttnThreads, row = c / (DIM / 8), chunk = c % (DIM / 8);
+        if (c < kRows * DIM / 8) *reinterpret_cast<uint4*>(smem + row * (2 * DIM) + ((chunk & ~7) | ((chunk ^ row) & 7)) * 16) = next[k];
+      }
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, const AttnCursor&, int lane, const char* smem) {
     const int quad = lane >> 2, four = lane & 3;
     float part[kChains][N][4], s[N][4];
 #pragma unroll
@@ -329,13 +351,31 @@ struct AttnBf16 {
 #pragma unroll
       for (int n = 0; n < N; ++n) part[c][n][0] = part[c][n][1] = part[c][n][2] = part[c][n][3] = 0.0f;
     {
-      const int token = lane & 15, odd = lane >> 4;
+      const int token = a.row + (lane & 15), odd = lane >> 4;
+      if constexpr (kShared) {
+        const uint32_t queries = rsm::smem_addr(smem) + (lane & 7) * (2 * DIM);
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {
-        uint32_t ka[4];
-        ldmatrix4(ka, a.keys + key_chunk<IT>(token, 2 * ks + odd));
+        for (int kk = 0; kk < kSteps / 2; ++kk) {
+          uint32_t k0[4], k1[4];
+          ldmatrix4(k0, a.keys + chunk_at<kStep>(token, 4 * kk + odd));
+          ldmatrix4(k1, a.keys + chunk_at<kStep>(token, 4 * kk + 2 + odd));
+          const int chunk = 4 * kk + (lane >> 3);
 #pragma unroll
-        for (int n = 0; n < N; ++n) mma_bf16(part[ks % kChains][n], ka, q[n][ks][0], q[n][ks][1]);
+          for (int n = 0; n < N; ++n) {
+            uint32_t qb[4];
+            ldmatrix4(qb, queries + n * (16 * DIM) + ((chunk & ~7) | ((chunk ^ lane) & 7)) * 16);
+            mma_bf16(part[0][n], k0, qb[0], qb[1]);
+            mma_bf16(part[kChains - 1][n], k1, qb[2], qb[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+          uint32_t ka[4];
+          ldmatrix4(ka, a.keys + chunk_at<kStep>(token, 2 * ks + odd));
+#pragma unroll
+          for (int n = 0; n < N; ++n) mma_bf16(part[ks % kChains][n], ka, q[n][ks][0], q[n][ks][1]);
+        }
       }
     }
 #pragma unroll
@@ -346,7 +386,7 @@ struct AttnBf16 {
 #pragma unroll
         for (int c = 1; c < kChains; ++c) s[n][e] += part[c][n][e];
       }
-    if (a.differ || a.seen != (1u << kAttnStep) - 1u) {
+    if (a.differ || (a.seen & 0xFFFFu) != 0xFFFFu) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -384,7 +424,7 @@ struct AttnBf16 {
         l[n][e & 1] += s[n][e];
       }
     if (a.differ && p.window > 1)
-      odd_values<IT, DIM>(a, lane, [&](int j) {
+      odd_values<IT, DIM, kTokens>(a, lane, [&](int j) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -395,7 +435,7 @@ struct AttnBf16 {
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float v = held_value<IT>(a, j, 16 * i + 8 * h + quad);
+                const float v = held_value<IT, DIM>(a, j, 16 * i + 8 * h + quad);
                 if (!isfinite(v)) o[i][n][2 * h + e] += w * v;
               }
           }
@@ -405,11 +445,11 @@ struct AttnBf16 {
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) pb[n][h] = transpose8(rsm::pack_bf16x2(s[n][2 * h], s[n][2 * h + 1]));
-    const int token = (lane >> 4) * 8 + (lane & 7), odd = lane >> 3 & 1;
+    const int token = a.row + (lane >> 4) * 8 + (lane & 7), odd = lane >> 3 & 1;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       uint32_t va[4];
-      ldmatrix4_trans(va, a.values + value_chunk(token, 2 * i + odd));
+      ldmatrix4_trans(va, a.values + chunk_at<kStep>(token, 2 * i + odd));
 #pragma unroll
       for (int n = 0; n < N; ++n) mma_bf16(o[i][n], va, pb[n][0], pb[n][1]);
     }
@@ -440,179 +480,242 @@ struct AttnBf16 {
   }
 };
 
-// The same for fp32, 16 rows: each product is three of tf32 (hi hi, hi lo, lo hi).  Lane
-// (quad, four) holds of S rows quad and quad + 8, tokens 8 n + 2 four + {0, 1}; of O the same rows.
-template <int DIM>
+// The same for fp32, R rows (1, 2, 4 or 8), all tokens of a stage.  For the scores lane (slice, group) = (lane & 7,
+// lane >> 3) sums over the 16-byte chunks slice + 8 j of a quarter of the tokens, `group`'s, and
+// the slices are then added up in halves, so that each lane ends with a token and half of the rows;
+// the weights go through shared memory, and a lane adds its columns' values for all rows.
+template <int DIM, int R>
 struct AttnF32 {
   using IT = float;
-  static constexpr int kRows = 16, kN = DIM / 8;
-  int limit[2];
-  float o[kN][4], m[2], l[2];
+  using Shape = AttnShape<IT, DIM>;
+  static constexpr int kRows = R, kStep = Shape::kStep, kTokens = kStep, kQuery = attn_query(4, DIM, R);
+  static constexpr int kTake = kStep / 4;             // a group's tokens
+  static constexpr int kChunks = DIM / 32;            // a slice's
+  static constexpr int kHalf = R > 1 ? R / 2 : 1;     // rows that a lane ends with
+  static constexpr int kCols = DIM / 32;              // columns of a lane
+  static_assert(kTake == 2 || kTake == 4);
+  uint64_t q[R][kChunks][2];
+  int limit[kHalf];
+  uint64_t o[R][kCols / 2];
+  float m[kHalf], l[kHalf];
 
-  // The column of o[n][e], e = 0 or 1: values are taken four columns at a time.
-  __device__ __forceinline__ static int column(int four, int n, int e) { return 32 * (n / 4) + 4 * (2 * four + e) + (n & 3); }
+  __device__ __forceinline__ static uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+  }
+  __device__ __forceinline__ static float2 both(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+  __device__ __forceinline__ static uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+  }
+  __device__ __forceinline__ static void lds_pairs(uint32_t at, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at));
+  }
+  // The token of the stage and the first row that lane ends with.
+  __device__ __forceinline__ static int own_token(int lane) {
+    return kTake == 4 ? (lane >> 3) * 4 + (lane & 1) * 2 + (lane >> 1 & 1) : (lane >> 3) * 2 + (lane & 1);
+  }
+  // (Two tokens a group: the second bit takes a half of the rows too.)
+  __device__ __forceinline__ static int own_row(int lane) {
+    if (kTake == 4) return R > 1 ? (lane >> 2 & 1) * kHalf : 0;
+    return R > 2 ? (lane >> 1 & 1) * (R / 2) + (lane >> 2 & 1) * (R / 4) : R > 1 ? (lane >> 1 & 1) : 0;
+  }
+  static constexpr int kKept = kTake == 4 ? kHalf : R > 2 ? R / 4 : 1;  // rows that a lane ends with, kHalf or fewer
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
-    for (int n = 0; n < kN; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-    m[0] = m[1] = kAttnLowest;
-    l[0] = l[1] = 0.0f;
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < kCols / 2; ++c) o[r][c] = 0;
+#pragma unroll
+    for (int h = 0; h < kKept; ++h) m[h] = kAttnLowest, l[h] = 0.0f;
   }
-  // Q to shared memory: for each 8 columns the four registers of the left operand of every lane,
-  // hi and then lo; columns 16 kk + 4 f + {0, 1} and {2, 3} are those of four = f in two products.
-  __device__ __forceinline__ void queries(const AttnParams& p, const AttnCursor& at, int lane, char* smem) {
+  __device__ __forceinline__ void fetch(const AttnParams& p, const AttnCursor& at, int lane) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) (void)at.query<IT, DIM>(p, kRows, 8 * h + (lane >> 2), limit[h]);
-    __syncthreads();  // the last unit's are read
-    for (int i = threadIdx.x; i < 32 * (DIM / 8); i += kAttnThreads) {
-      const int ks = i / 32, ln = i & 31, qd = ln >> 2, fr = ln & 3;
-      uint32_t hi[4], lo[4];
+    for (int r = 0; r < R; ++r) {
+      int last;
+      const IT* from = at.query<IT>(p, R, r, last);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int last;
-        const IT* q = at.query<IT, DIM>(p, kRows, 8 * h + qd, last);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          split_tf32(q == nullptr ? 0.0f : q[16 * (ks / 2) + 4 * fr + 2 * (ks & 1) + e], hi[2 * e + h], lo[2 * e + h]);
-      }
-      uint4* to = reinterpret_cast<uint4*>(smem) + 2 * 32 * ks + ln;
-      to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      to[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-    __syncthreads();
-  }
-  __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, int lane, const char* smem) {
-    const int quad = lane >> 2, four = lane & 3;
-    float s[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-    const uint32_t qs = rsm::smem_addr(smem) + lane * 16;
-#pragma unroll 4
-    for (int kk = 0; kk < DIM / 16; ++kk) {
-      uint32_t hi[2][4], lo[2][4], fin[2][4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const uint4 v = rsm::lds128(a.keys + key_chunk<IT>(8 * n + quad, 4 * kk + four));
-        split_tf32(__uint_as_float(v.x), hi[n][0], lo[n][0], fin[n][0]);
-        split_tf32(__uint_as_float(v.y), hi[n][1], lo[n][1], fin[n][1]);
-        split_tf32(__uint_as_float(v.z), hi[n][2], lo[n][2], fin[n][2]);
-        split_tf32(__uint_as_float(v.w), hi[n][3], lo[n][3], fin[n][3]);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint4 h4 = rsm::lds128(qs + (2 * kk + e) * 1024), l4 = rsm::lds128(qs + (2 * kk + e) * 1024 + 512);
-        const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          mma_tf32(s[n], al, fin[n][2 * e], fin[n][2 * e + 1]);
-          mma_tf32(s[n], ah, lo[n][2 * e], lo[n][2 * e + 1]);
-          mma_tf32(s[n], ah, hi[n][2 * e], hi[n][2 * e + 1]);
+      for (int j = 0; j < kChunks; ++j) {
+        const int c = 4 * ((lane & 7) + 8 * j);
+        q[r][j][0] = q[r][j][1] = 0;
+        if (from == nullptr || c >= p.dim) continue;
+        if (p.q_wide) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(from + c);
+          q[r][j][0] = v.x, q[r][j][1] = v.y;
+        } else {
+          q[r][j][0] = pair(from[c], from[c + 1]), q[r][j][1] = pair(from[c + 2], from[c + 3]);
         }
       }
     }
-    if (a.differ || a.seen != (1u << kAttnStep) - 1u) {
+  }
+  __device__ __forceinline__ void commit(const AttnParams& p, const AttnCursor& at, int lane, char*) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+    for (int h = 0; h < kKept; ++h) (void)at.query<IT>(p, R, own_row(lane) + h, limit[h]);
+  }
+  __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, const AttnCursor& at, int lane, char* smem) {
+    const int slice = lane & 7, group = lane >> 3;
+    float v[kTake * R];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * n + 2 * four + (e & 1);
-          if (!(a.seen >> j & 1u) || a.token0 + j > limit[e >> 1]) s[n][e] = p.hidden;
-        }
+    for (int t = 0; t < kTake; ++t) {
+      const int token = group * kTake + t;
+      uint64_t acc[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = 0;
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        uint64_t k0, k1;
+        lds_pairs(a.keys + chunk_at<kStep>(token, slice + 8 * j), k0, k1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = fma2(k1, q[r][j][1], fma2(k0, q[r][j][0], acc[r]));
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 x = both(acc[r]);
+        v[t * R + r] = x.x + x.y;
+      }
+    }
+    // the slices' sums: each exchange adds and halves what a lane has, while it has more than one
+    int have = kTake * R;
+#pragma unroll
+    for (int bit = 1; bit < 8; bit <<= 1) {
+      const bool upper = lane & bit;
+      if (have > 1) {
+        have /= 2;
+#pragma unroll
+        for (int i = 0; i < kTake * R / 2; ++i)
+          if (i < have) {
+            const float send = upper ? v[i] : v[i + have], keep = upper ? v[i + have] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, bit);
+          }
+      } else {
+        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], bit);
+      }
+    }
+    const int j = own_token(lane);
+    if (a.differ || a.seen != Shape::kAll) {
+#pragma unroll
+      for (int h = 0; h < kKept; ++h)
+        if (!(a.seen >> j & 1u) || a.token0 + j > limit[h]) v[h] = p.hidden;
     }
     bool above = false;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) above |= fmaf(s[n][e], p.scale_log2, -m[e >> 1]) > kAttnSlack;
+    for (int h = 0; h < kKept; ++h) above |= fmaf(v[h], p.scale_log2, -m[h]) > kAttnSlack;
     if (__any_sync(0xFFFFFFFFu, above)) {  // some row's maximum moves
+      float keep[kKept];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float top = fmaxf(fmaxf(s[0][2 * h] * p.scale_log2, s[0][2 * h + 1] * p.scale_log2),
-                          fmaxf(s[1][2 * h] * p.scale_log2, s[1][2 * h + 1] * p.scale_log2));
+      for (int h = 0; h < kKept; ++h) {
+        float top = v[h] * p.scale_log2;
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const float next = fmaxf(m[h], top), keep = exp2_fast(m[h] - next);
+        if (kTake == 4) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        const float next = fmaxf(m[h], top);
+        keep[h] = exp2_fast(m[h] - next);
         m[h] = next;
-        l[h] *= keep;
+        l[h] *= keep[h];
+      }
 #pragma unroll
-        for (int n = 0; n < kN; ++n) o[n][2 * h] *= keep, o[n][2 * h + 1] *= keep;
+      for (int r = 0; r < R; ++r) {  // from a lane that has row r
+        const int from = kTake == 4 ? (R > 1 ? r / kHalf * 4 : 0) : R > 2 ? r / (R / 2) * 2 + r / (R / 4) % 2 * 4 : R > 1 ? r * 2 : 0;
+        const float f = __shfl_sync(0xFFFFFFFFu, keep[r % kKept], from);
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) {
+          const float2 x = both(o[r][c]);
+          o[r][c] = pair(x.x * f, x.y * f);
+        }
       }
     }
+    // weights, each twice, [token][row]
+    const uint32_t weights = rsm::smem_addr(smem) + (threadIdx.x >> 5) * (kStep * R * 8);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = exp2_fast(fmaf(s[n][e], p.scale_log2, -m[e >> 1]));
-        l[e >> 1] += s[n][e];
-      }
+    for (int h = 0; h < kKept; ++h) {
+      const float w = exp2_fast(fmaf(v[h], p.scale_log2, -m[h]));
+      // (a token and row that two lanes end with counts once)
+      l[h] += kTake == 4 ? (R > 1 || !(lane & 4) ? w : 0.0f) : (R > 2 || !(lane & 4)) && (R > 1 || !(lane & 2)) ? w : 0.0f;
+      asm volatile("st.shared.v2.f32 [%0], {%1, %1};" ::"r"(weights + (j * R + own_row(lane) + h) * 8), "f"(w) : "memory");
+    }
+    __syncwarp();
     if (a.differ && p.window > 1)
-      odd_values<IT, DIM>(a, lane, [&](int j) {
+      odd_values<IT, DIM, kTokens>(a, lane, [&](int t) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float even = j & 8 ? s[1][2 * h] : s[0][2 * h], other = j & 8 ? s[1][2 * h + 1] : s[0][2 * h + 1];
-          const float w = __shfl_sync(0xFFFFFFFFu, j & 1 ? other : even, (lane & ~3) + (j & 7) / 2);
-          if (a.token0 + j > limit[h]) continue;
+        for (int r = 0; r < R; ++r) {
+          int last;
+          (void)at.query<IT>(p, R, r, last);
+          float w;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(weights + (t * R + r) * 8));
+          if (a.token0 + t > last) continue;
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float v = held_value<IT>(a, j, column(four, n, e));
-              if (!isfinite(v)) o[n][2 * h + e] += w * v;
-            }
+          for (int c = 0; c < kCols / 2; ++c) {
+            float2 x = both(o[r][c]);
+            const float v0 = held_value<IT, DIM>(a, t, column(lane, 2 * c)), v1 = held_value<IT, DIM>(a, t, column(lane, 2 * c + 1));
+            if (!isfinite(v0)) x.x += w * v0;
+            if (!isfinite(v1)) x.y += w * v1;
+            o[r][c] = pair(x.x, x.y);
+          }
         }
       });
-    // tokens 2 f and 2 f + 1 of eight are those of four = f, as S's columns are
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      uint32_t ph[4], pl[4];
-      split_tf32(s[kt][0], ph[0], pl[0]);
-      split_tf32(s[kt][2], ph[1], pl[1]);
-      split_tf32(s[kt][1], ph[2], pl[2]);
-      split_tf32(s[kt][3], ph[3], pl[3]);
-      const int t0 = 8 * kt + 2 * four, t1 = t0 + 1;
+    for (int t = 0; t < kStep; ++t) {
+      uint64_t x[kCols / 2];
 #pragma unroll
-      for (int n = 0; n < kN; n += 4) {
-        const uint4 x = rsm::lds128(a.values + value_chunk(t0, 2 * n + quad)), y = rsm::lds128(a.values + value_chunk(t1, 2 * n + quad));
-        const uint32_t va[4] = {x.x, x.y, x.z, x.w}, vb[4] = {y.x, y.y, y.z, y.w};
+      for (int c = 0; c < kCols / 4; ++c) lds_pairs(a.values + chunk_at<kStep>(t, lane + 32 * c), x[2 * c], x[2 * c + 1]);
+      if constexpr (kCols == 2) asm volatile("ld.shared.b64 %0, [%1];" : "=l"(x[0]) : "r"(a.values + chunk_at<kStep>(t, lane >> 1) + (lane & 1) * 8));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h0, l0, f0, h1, l1, f1;
-          split_tf32(__uint_as_float(va[k]), h0, l0, f0);
-          split_tf32(__uint_as_float(vb[k]), h1, l1, f1);
-          mma_tf32(o[n + k], pl, f0, f1);
-          mma_tf32(o[n + k], ph, l0, l1);
-          mma_tf32(o[n + k], ph, h0, h1);
+      for (int r = 0; r < R; r += 2) {
+        uint64_t w0, w1 = 0;
+        if constexpr (R > 1)
+          lds_pairs(weights + (t * R + r) * 8, w0, w1);
+        else
+          asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w0) : "r"(weights + t * 8));
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) {
+          o[r][c] = fma2(w0, x[c], o[r][c]);
+          if (R > 1) o[r + (R > 1)][c] = fma2(w1, x[c], o[r + (R > 1)][c]);
         }
       }
     }
   }
+  // The column of a lane's c-th.
+  __device__ __forceinline__ static int column(int lane, int c) { return kCols == 2 ? 2 * lane + c : 4 * (lane + 32 * (c / 4)) + c % 4; }
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) const {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kKept; ++h) {
       float sum = l[h];
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-      if ((lane & 3) == 0) ms[8 * h + (lane >> 2)] = m[h], ls[8 * h + (lane >> 2)] = sum;
+      if (kTake == 4 || R == 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      if ((kTake == 4 && R == 1) || (kTake == 2 && R <= 2)) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+      if ((lane & 25) == 0) ms[own_row(lane) + h] = m[h], ls[own_row(lane) + h] = sum;
     }
   }
-  __device__ __forceinline__ static int place(int row, int column) { return row * DIM + (column ^ (row & 3) << 3); }
+  __device__ __forceinline__ static int place(int row, int column) { return row * DIM + column; }
   template <int PASS>
   __device__ __forceinline__ void outputs(float* own, int lane) const {
 #pragma unroll
-    for (int n = 0; n < kN; ++n)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) own[place(8 * (e >> 1) + (lane >> 2), column(lane & 3, n, e & 1))] = o[n][e];
+      for (int c = 0; c < kCols / 2; ++c) *reinterpret_cast<float2*>(own + place(r, column(lane, 2 * c))) = both(o[r][c]);
   }
 };
 
-// BOXES: loads by TMA; the pages are whole groups of 16 tokens.
+// BOXES: loads by TMA, in boxes of attn_box() rows; the pages are whole boxes.
 template <typename Math, int DIM, bool BOXES>
 __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM))
     attn_tile_kernel(const __grid_constant__ AttnTileParams tp) {
   using IT = typename Math::IT;
   using Shape = AttnShape<IT, DIM>;
   constexpr int kWarps = kAttnThreads / 32, kRows = Math::kRows, S = Shape::kStages, kChunks = Shape::kChunks;
-  constexpr uint32_t kAll = (1u << kAttnStep) - 1u;
+  constexpr int kStep = Shape::kStep, kTile = 4 * kStep, kTokens = Math::kTokens, kBox = 128 / static_cast<int>(sizeof(IT));  // columns of a box
+  constexpr int kBoxRows = attn_box(sizeof(IT), DIM), kParts = BOXES ? kStep / kBoxRows : 1;  // a step's boxes of rows
+  constexpr uint32_t kAll = Shape::kAll;
   extern __shared__ __align__(1024) char smem[];
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
   __shared__ uint32_t seen_s[kWarps][S];
@@ -634,7 +737,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   auto skipped = [&]() {  // rows of skipped requests
     for (int b = blockIdx.x; b < pg.requests; b += gridDim.x)
       if (request_tokens(pg, b, p.window, nullptr, false) == 0) {
-        const int64_t n = static_cast<int64_t>(p.window) * p.H * DIM;
+        const int64_t n = static_cast<int64_t>(p.window) * p.H * p.dim;
         IT* out = static_cast<IT*>(p.out) + b * n;
         for (int64_t i = threadIdx.x; i < n; i += kAttnThreads) out[i] = IT(0);
       }
@@ -664,25 +767,27 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   AttnCursor ask = at;
   int64_t ask_room = room;
 
-  // ---- loads: a warp's 16 tokens of a tile ----
-  const uint32_t ring = rsm::smem_addr(smem) + Shape::kQuery + warp * (S * Shape::kStage);
+  // ---- loads: a warp's step of a tile ----
+  const uint32_t ring = rsm::smem_addr(smem) + Math::kQuery + warp * (S * Shape::kStage);
   const uint32_t full = rsm::smem_addr(&full_s[warp][0]);
-  const bool one_page = BOXES || pg.page_size % kAttnStep == 0;  // the 16 tokens lie in one page
+  const bool one_page = BOXES || pg.page_size % kStep == 0;  // a step, or a box, lies in one page
+  auto first_bits = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
   auto page_at = [&](int64_t token) {
     if (token >= ask.len) return -1;  // no token
     const int i = p.page_shift >= 0 ? static_cast<int>(token) >> p.page_shift : static_cast<int>(token) / pg.page_size;
     return __ldg(pg.page_table + ask.b * pg.table_stride + i);
   };
-  // One page a step: a lane looks up that of the tile lane of each 32, all at once; else a lane a token, a step ahead.
+  // One page a step (or box): a lane looks up that of a tile's, 32 at once; else a lane a token, a step ahead.
+  constexpr int kLook = 32 / kParts;  // tiles
   int looked = -1, pages = -1;
   auto look_up = [&](bool request) {
     if (one_page) {
-      const int group = ask.tile >> 5;
+      const int group = ask.tile / kLook;
       if (!request && group == looked) return;
       looked = group;
-      pages = page_at((static_cast<int64_t>(group) * 32 + lane) * kAttnTile + warp * kAttnStep);
+      pages = page_at((static_cast<int64_t>(group) * kLook + lane / kParts) * kTile + warp * kStep + lane % kParts * kBoxRows);
     } else {
-      pages = page_at(static_cast<int64_t>(ask.tile) * kAttnTile + warp * kAttnStep + lane % kAttnStep);
+      pages = page_at(static_cast<int64_t>(ask.tile) * kTile + warp * kStep + lane % kStep);
     }
   };
   look_up(true);
@@ -691,44 +796,57 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       if constexpr (!BOXES) cp_async_commit();
       return;
     }
-    const int g = ask.g, token0 = ask.tile * kAttnTile + warp * kAttnStep;
-    const int page = one_page ? __shfl_sync(0xFFFFFFFFu, pages, ask.tile & 31) : pages;
-    const bool good = page >= 0 && page < pg.num_pages;
-    if (!good && token0 + (one_page ? 0 : lane % kAttnStep) < ask.len) flag(p.status, RSM_STATUS_BAD_PAGE);
+    const int g = ask.g, token0 = ask.tile * kTile + warp * kStep;
     const uint32_t base = ring + stage * Shape::kStage;
-    uint32_t seen;
+    uint32_t seen = 0;
     if constexpr (BOXES) {
-      seen = good ? (1u << min(kAttnStep, ask.len - token0)) - 1u : 0u;
+      int page[kParts];
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) {
+        const int token = token0 + h * kBoxRows;
+        page[h] = __shfl_sync(0xFFFFFFFFu, pages, ask.tile % kLook * kParts + h);
+        if (page[h] >= 0 && page[h] < pg.num_pages) {
+          seen |= first_bits(min(kBoxRows, ask.len - token)) << (h * kBoxRows);
+        } else {
+          page[h] = -1;
+          if (token < ask.len) flag(p.status, RSM_STATUS_BAD_PAGE);
+        }
+      }
       if (lane == 0) {
         const uint32_t bar = full + stage * 8;
-        if (good) {
-          const int row = p.page_shift >= 0 ? token0 & (pg.page_size - 1) : token0 % pg.page_size;
-          rsm::mbar_arrive_expect_tx(bar, Shape::kStage);
+        uint32_t bytes = 0;
 #pragma unroll
-          for (int c = 0; c < DIM / 64; ++c) {
-            box_load(base + c * (kAttnStep * 128), &tp.k_map, 64 * c, g, row, page, bar);
-            box_load(base + Shape::kHalf + c * (kAttnStep * 128), &tp.v_map, 64 * c, g, row, page, bar);
+        for (int h = 0; h < kParts; ++h) bytes += page[h] >= 0 ? Shape::kStage / kParts : 0;
+        rsm::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          if (page[h] < 0) continue;
+          const int token = token0 + h * kBoxRows, row = p.page_shift >= 0 ? token & (pg.page_size - 1) : token % pg.page_size;
+#pragma unroll
+          for (int c = 0; c < DIM / kBox; ++c) {
+            const uint32_t to = base + c * (kStep * 128) + h * (kBoxRows * 128);
+            box_load(to, &tp.k_map, kBox * c, g, row, page[h], bar);
+            box_load(to + Shape::kHalf, &tp.v_map, kBox * c, g, row, page[h], bar);
           }
-        } else {
-          rsm::mbar_arrive(bar);
         }
       }
     } else {
-      constexpr int kAt = 32 / kChunks;  // rows at a time
-      const int row0 = lane / kChunks, chunk = lane % kChunks;
-      const int token = token0 + (one_page ? 0 : lane % kAttnStep);
+      const int page = one_page ? __shfl_sync(0xFFFFFFFFu, pages, ask.tile % kLook) : pages;
+      const bool good = page >= 0 && page < pg.num_pages;
+      if (!good && token0 + (one_page ? 0 : lane % kStep) < ask.len) flag(p.status, RSM_STATUS_BAD_PAGE);
+      const int token = token0 + (one_page ? 0 : lane % kStep), chunks = p.dim * static_cast<int>(sizeof(IT)) / 16;
       const int row = p.page_shift >= 0 ? token & (pg.page_size - 1) : token % pg.page_size;
-      seen = one_page ? (good ? (1u << min(kAttnStep, ask.len - token0)) - 1u : 0u) : __ballot_sync(0xFFFFFFFFu, good) & kAll;
+      seen = one_page ? (good ? first_bits(min(kStep, ask.len - token0)) : 0u) : __ballot_sync(0xFFFFFFFFu, good) & kAll;
 #pragma unroll 4
-      for (int i = 0; i < kAttnStep / kAt; ++i) {
-        const int r = i * kAt + row0;
+      for (int i = 0; i < kStep * kChunks / 32; ++i) {
+        const int f = i * 32 + lane, r = f / kChunks, chunk = f % kChunks;
         int pr = page, rr = row + r;
         if (!one_page) pr = __shfl_sync(0xFFFFFFFFu, page, r), rr = __shfl_sync(0xFFFFFFFFu, row, r);
-        const bool yes = seen >> r & 1u;
+        const bool yes = (seen >> r & 1u) && chunk < chunks;
         const IT* kr = static_cast<const IT*>(pg.k) + (yes ? pr * pg.k_page_stride + rr * pg.k_row_stride + g * pg.k_head_stride : 0);
         const IT* vr = static_cast<const IT*>(pg.v) + (yes ? pr * pg.v_page_stride + rr * pg.v_row_stride + g * pg.v_head_stride : 0);
-        cp_async_16_or_zero(base + key_chunk<IT>(r, chunk), reinterpret_cast<const char*>(kr) + chunk * 16, yes);
-        cp_async_16_or_zero(base + Shape::kHalf + value_chunk(r, chunk), reinterpret_cast<const char*>(vr) + chunk * 16, yes);
+        cp_async_16_or_zero(base + chunk_at<kStep>(r, chunk), reinterpret_cast<const char*>(kr) + (yes ? chunk * 16 : 0), yes);
+        cp_async_16_or_zero(base + Shape::kHalf + chunk_at<kStep>(r, chunk), reinterpret_cast<const char*>(vr) + (yes ? chunk * 16 : 0), yes);
       }
       cp_async_commit();
     }
@@ -744,9 +862,10 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   for (int s = 0; s < S - 1; ++s) load(s);
 
   Math math;
-  math.queries(p, at, lane, smem);
-  math.reset();
+  math.fetch(p, at, lane);
   skipped();
+  math.commit(p, at, lane, smem);
+  math.reset();
   int from = at.tile;  // the piece's first tile
   uint32_t phase = 0;
   for (int stage = 0;;) {
@@ -767,18 +886,25 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       a.keys = ring + stage * Shape::kStage;
       a.values = a.keys + Shape::kHalf;
       a.held = smem + (a.values - rsm::smem_addr(smem));
-      a.token0 = at.tile * kAttnTile + warp * kAttnStep;
-      a.differ = a.token0 + kAttnStep - 1 > at.len - p.window;
-      a.first_new = max(at.len - p.window + 1 - a.token0, 0);
       if constexpr (BOXES) {  // rows behind the last token came with the box
         if (a.seen != kAll) {
-          for (int c = lane; c < kAttnStep * kChunks; c += 32)
-            if (!(a.seen >> ((c >> 3) % kAttnStep) & 1u)) *reinterpret_cast<uint4*>(a.held + c * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = lane; c < kStep * kChunks; c += 32)
+            if (!(a.seen >> ((c >> 3) % kStep) & 1u)) *reinterpret_cast<uint4*>(a.held + c * 16) = make_uint4(0, 0, 0, 0);
           rsm::fence_proxy_async_smem();
           __syncwarp();
         }
       }
-      math.step(p, a, lane, smem);
+      const uint32_t all_seen = a.seen;
+#pragma unroll
+      for (int sub = 0; sub < kStep / kTokens; ++sub) {
+        a.row = sub * kTokens;
+        a.seen = all_seen >> a.row;
+        if (sub > 0 && a.seen == 0) break;
+        a.token0 = at.tile * kTile + warp * kStep + a.row;
+        a.differ = a.token0 + kTokens - 1 > at.len - p.window;
+        a.first_new = max(at.len - p.window + 1 - a.token0, 0);
+        math.step(p, a, at, lane, smem);
+      }
     }
 
     // ---- the end of a unit, or of this CTA's part of it ----
@@ -790,20 +916,19 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       const bool whole = from == 0 && last_tile;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
       math.stats(m_s[warp], l_s[warp], lane);
-      // the next unit's queries are on their way meanwhile (fp32: see below)
-      if (!over) {
+      if (!over) {  // the next unit's queries are on their way meanwhile
         at.next(p);
-        if constexpr (Shape::kQuery == 0) math.queries(p, at, lane, smem);
+        math.fetch(p, at, lane);
       }
       // the warps' outputs pass through the stages just read, 16 rows at a time
-      char* const pass_at = smem + Shape::kQuery + stage * Shape::kStage;
+      char* const pass_at = smem + Math::kQuery + stage * Shape::kStage;
       auto pass = [&](auto index) {
         constexpr int kPass = decltype(index)::value, kHere = kRows - 16 * kPass < 16 ? kRows - 16 * kPass : 16;
         math.template outputs<kPass>(reinterpret_cast<float*>(pass_at + warp * (S * Shape::kStage)), lane);
         __syncthreads();
         for (int c = threadIdx.x; c < kHere * DIM / 4; c += kAttnThreads) {
           const int row = c / (DIM / 4), col = (c - row * (DIM / 4)) * 4, r = 16 * kPass + row, all = was.rt * kRows + r;
-          if (all >= p.per * p.window) continue;
+          if (all >= p.per * p.window || col >= p.dim) continue;
           float top = -INFINITY, sum = 0.0f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][r]);
@@ -818,7 +943,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
           if (whole) {
             const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
             const int t = all / p.per;
-            IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(was.b) * p.window + t) * p.H + was.g * p.per + all - t * p.per) * DIM + col;
+            IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(was.b) * p.window + t) * p.H + was.g * p.per + all - t * p.per) * p.dim + col;
             if constexpr (sizeof(IT) == 4)
               *reinterpret_cast<float4*>(out) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
             else
@@ -835,7 +960,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       pass(std::integral_constant<int, 0>{});
       if constexpr (kRows > 16) pass(std::integral_constant<int, 1>{});
       if (over) break;
-      if constexpr (Shape::kQuery != 0) math.queries(p, at, lane, smem);
+      math.commit(p, at, lane, smem);
       math.reset();
       from = 0;
     } else {
@@ -866,12 +991,12 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
   if (by_unit) {
     b = index / units;
     u = index - b * units;
-    tiles = tiles_of(request_tokens(p.pages, b, p.window, nullptr, false));
+    tiles = tiles_of(p, request_tokens(p.pages, b, p.window, nullptr, false));
     first = d.before(p, b) + u * counts(tiles);
   } else if (index < deal.ctas) {
     const Place place = d.find(p, deal.begin(index + 1) - 1);
     b = place.b;
-    tiles = tiles_of(request_tokens(p.pages, b, p.window, nullptr, false));
+    tiles = tiles_of(p, request_tokens(p.pages, b, p.window, nullptr, false));
     u = static_cast<int>((deal.begin(index + 1) - 1 - place.first) / counts(tiles));
     first = place.first + u * counts(tiles);
     if (first < deal.begin(index)) tiles = 0;  // it began before
@@ -889,7 +1014,7 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
   const int group = threadIdx.x / kLanes, col = threadIdx.x % kLanes;
   const auto finish = [&](int r) {
     const int row = rt * kRows + r, t = row / p.per;
-    return static_cast<IT*>(p.out) + ((static_cast<int64_t>(b) * p.window + t) * p.H + g * p.per + row - t * p.per) * DIM;
+    return static_cast<IT*>(p.out) + ((static_cast<int64_t>(b) * p.window + t) * p.H + g * p.per + row - t * p.per) * p.dim;
   };
   if (pieces <= 32) {
     constexpr int kWarps = kAttnJoinThreads / 32, kCols = DIM / 32;
@@ -912,7 +1037,8 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
         for (int k = 0; k < kCols; ++k) y[k] = fmaf(from[32 * k], w, y[k]);
       }
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) put(finish(r) + lane + 32 * k, sum == 0.0f ? 0.0f : y[k] / sum);
+      for (int k = 0; k < kCols; ++k)
+        if (lane + 32 * k < p.dim) put(finish(r) + lane + 32 * k, sum == 0.0f ? 0.0f : y[k] / sum);
     }
     return;
   }
@@ -961,7 +1087,7 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
     acc_s[group][col] = y;
     __syncthreads();
     IT* const out = finish(r);
-    for (int c = threadIdx.x; c < DIM; c += kAttnJoinThreads) {
+    for (int c = threadIdx.x; c < p.dim; c += kAttnJoinThreads) {
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kGroups; ++w) v += reinterpret_cast<const float*>(acc_s[w])[c];

@@ -56,7 +56,7 @@ int launch(const void* fn, int64_t grid, int threads, const void* params, void* 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_attn_ready[kMaxDevices][2][3][4][2];  // input type, dim 64, 128, 256, eights of rows, boxes
+bool g_attn_ready[kMaxDevices][2][3][33][2];  // input type, dim 64, 128, 256, rows, boxes
 
 bool g_rotary_ready[kMaxDevices][2];  // input type
 
@@ -169,7 +169,8 @@ int validate(const rsm_paged_attention_args* a, bool pointers) {
 
 // How a call runs on the tiled kernel.
 struct AttnPlan {
-  int rows;       // of a unit; 0: the plain kernel
+  int dim;        // columns that the kernel is compiled for
+  int rows;       // of a unit
   int row_tiles;  // units of a key head
   int ctas;
   int64_t units;
@@ -177,25 +178,31 @@ struct AttnPlan {
   int64_t bytes;  // of workspace
 };
 
-// A unit has as many rows as the kernel takes, or the fewest eights that hold them all: more
-// than it takes are several units, which read the same keys and values (from the L2).
+// Rows of the caches and heads are whole 16-byte vectors.
+bool uses_tiles(const rsm_paged_attention_args* a) {
+  const int64_t rows = static_cast<int64_t>(a->num_heads / a->num_kv_heads) * a->window;
+  return a->dim * input_size(a->input_dtype) % 16 == 0 && rows <= 0x7FFFFF00LL;
+}
+
+// A unit has as many rows as the kernel takes, or the fewest that hold them all (bf16: in eights;
+// fp32: 1, 2, 4 or 8): more than it takes are several units, which read the same keys and values
+// (from the L2).
 AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   AttnPlan pl{};
-  const int most_rows = hybrid::attn_rows(a->input_dtype, a->dim);
+  const int es = input_size(a->input_dtype);
+  pl.dim = hybrid::attn_dim(a->dim);
+  const int most_rows = hybrid::attn_rows(es, pl.dim);
   const int64_t rows = static_cast<int64_t>(a->num_heads / a->num_kv_heads) * a->window;
-  if (most_rows == 0 || rows > 0x7FFFFF00LL) return pl;
-  const int64_t row_tiles = (rows + most_rows - 1) / most_rows;
-  if (row_tiles * a->num_kv_heads > 0x7FFFFFFFLL) return pl;
+  const int64_t row_tiles = (rows + most_rows - 1) / most_rows, each = (rows + row_tiles - 1) / row_tiles;
   pl.row_tiles = static_cast<int>(row_tiles);
-  pl.rows = a->input_dtype == RSM_F32 ? 16 : static_cast<int>(((rows + row_tiles - 1) / row_tiles + 7) / 8 * 8);
+  pl.rows = es == 2 ? static_cast<int>((each + 7) / 8 * 8) : each > 4 ? 8 : each > 2 ? 4 : static_cast<int>(each);
   pl.units = row_tiles * a->num_kv_heads * a->pages.requests;
-  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size;
-  const int64_t most = std::max<int64_t>((longest + hybrid::kAttnTile - 1) / hybrid::kAttnTile, 1);
+  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size, tile = 4 * hybrid::attn_step(es, pl.dim);
+  const int64_t most = std::max<int64_t>((longest + tile - 1) / tile, 1);
   pl.split = most > 1;
-  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(input_size(a->input_dtype), a->dim),
-                                             2 * hybrid::kAttnJoinThreads);
+  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(es, pl.dim), 2 * hybrid::kAttnJoinThreads);
   pl.ctas = static_cast<int>(most >= resident ? resident : std::min(resident, pl.units * most));
-  if (pl.split) pl.bytes = 2LL * pl.ctas * pl.rows * (a->dim + 2) * 4;
+  if (pl.split) pl.bytes = 2LL * pl.ctas * pl.rows * (pl.dim + 2) * 4;
   return pl;
 }
 
@@ -216,22 +223,23 @@ TensorMapEncodeFn tensor_map_encoder() {
 }
 
 // Tensor maps take strides from 16 bytes to 2^40; a stride that no second element needs is put at the least.
-bool box_stride(int64_t n, int64_t stride, cuuint64_t* out) {
-  *out = n <= 1 ? 16 : static_cast<cuuint64_t>(stride) * 2u;
-  return n <= 1 || (stride > 0 && stride < (int64_t{1} << 38));
+bool box_stride(int64_t n, int64_t stride, int es, cuuint64_t* out) {
+  *out = n <= 1 ? 16 : static_cast<cuuint64_t>(stride) * es;
+  return n <= 1 || (stride > 0 && stride < (int64_t{1} << 37));
 }
 
-// The boxes of 16 rows of one head, 64 columns each, of bf16 pages; false where a map cannot be made.
-bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int kv_heads, int dim, int64_t page, int64_t row, int64_t head) {
+// The boxes of `rows` rows of one head, 128 bytes of columns each; false where a map cannot be made.
+bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int es, int rows, int kv_heads, int dim, int64_t page, int64_t row,
+              int64_t head) {
   const TensorMapEncodeFn encode = tensor_map_encoder();
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(kv_heads), static_cast<cuuint64_t>(pg.page_size),
                               static_cast<cuuint64_t>(pg.num_pages)};
   cuuint64_t strides[3];
-  if (encode == nullptr || pg.num_pages < 1 || !box_stride(kv_heads, head, &strides[0]) || !box_stride(pg.page_size, row, &strides[1]) ||
-      !box_stride(pg.num_pages, page, &strides[2]))
+  if (encode == nullptr || pg.num_pages < 1 || !box_stride(kv_heads, head, es, &strides[0]) ||
+      !box_stride(pg.page_size, row, es, &strides[1]) || !box_stride(pg.num_pages, page, es, &strides[2]))
     return false;
-  const cuuint32_t box[4] = {64, 1, hybrid::kAttnStep, 1}, ones[4] = {1, 1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4u, const_cast<void*>(base), dims, strides, box, ones,
+  const cuuint32_t box[4] = {128u / es, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
+  return encode(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4u, const_cast<void*>(base), dims, strides, box, ones,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -239,7 +247,7 @@ bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int kv_he
 int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& base, const AttnPlan& pl, int dev, void* stream) {
   if (pl.split && (a->workspace == nullptr || a->workspace_bytes < pl.bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
     return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(pl.bytes));
-  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, a->dim);
+  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, pl.dim, pl.rows), step = hybrid::attn_step(es, pl.dim);
   hybrid::AttnTileParams tp{};
   tp.p = base;
   hybrid::AttnParams& p = tp.p;
@@ -248,17 +256,20 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   if (p.scale_log2 == 0.0f) p.scale_log2 = FLT_MIN;  // (infinity times it stays infinity)
   p.row_tiles = pl.row_tiles;
   p.ctas = pl.ctas;
+  p.tile_shift = step == 8 ? 5 : step == 16 ? 6 : 7;
   p.page_shift = -1;
   for (int k = 0; k < 31; ++k)
     if (a->pages.page_size == 1 << k) p.page_shift = k;
   p.q_pairs = reinterpret_cast<uintptr_t>(a->q) % 4 == 0 && (a->pages.requests == 1 || a->q_batch_stride % 2 == 0) &&
               (a->window == 1 || a->q_stride % 2 == 0);
   const rsm_pages& pg = a->pages;
-  const bool boxes = a->input_dtype == RSM_BF16 && pg.page_size % hybrid::kAttnStep == 0 &&
-                     page_map(&tp.k_map, pg.k, pg, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
-                     page_map(&tp.v_map, pg.v, pg, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
-  const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, a->dim, pl.rows, boxes);
-  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][a->dim / 128][pl.rows / 8 - 1][boxes], fn, smem);
+  const int box = hybrid::attn_box(es, pl.dim);
+  const bool boxes = pg.page_size % box == 0 &&
+                     page_map(&tp.k_map, pg.k, pg, es, box, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
+                     page_map(&tp.v_map, pg.v, pg, es, box, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
+  p.q_wide = rows_fit(a->q, es, a->pages.requests, a->q_batch_stride, a->window, a->q_stride);
+  const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, pl.dim, pl.rows, boxes);
+  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][boxes], fn, smem);
   if (rc != RSM_OK) return rc;
   rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
   if (rc != RSM_OK || !pl.split) return rc;
@@ -278,7 +289,7 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   void* kargs[] = {&p, &parts, &by_unit};
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, hybrid::attn_join_kernel_of(a->input_dtype, a->dim, pl.rows), kargs);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, hybrid::attn_join_kernel_of(a->input_dtype, pl.dim, pl.rows), kargs);
   if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return done();
 }
@@ -420,7 +431,7 @@ int64_t rsm_paged_attention_workspace(const rsm_paged_attention_args* a) {
     int dev = 0, sms = 0;
     rc = device_sms(&dev, &sms);
     if (rc != RSM_OK) return rc;
-    bytes = plan_attention(a, sms).bytes;
+    if (uses_tiles(a)) bytes = plan_attention(a, sms).bytes;
   }
   done();
   return bytes;
@@ -443,12 +454,11 @@ int rsm_paged_attention(const rsm_paged_attention_args* a, void* stream) {
   p.per = a->num_heads / a->num_kv_heads;
   p.dim = a->dim;
   p.scale_log2 = a->scale * 1.44269504088896340736f;
-  if (pages_fit(a->pages, input_size(a->input_dtype), a->num_kv_heads)) {
+  if (uses_tiles(a) && pages_fit(a->pages, input_size(a->input_dtype), a->num_kv_heads)) {
     int dev = 0, sms = 0;
     rc = device_sms(&dev, &sms);
     if (rc != RSM_OK) return rc;
-    const AttnPlan pl = plan_attention(a, sms);
-    if (pl.rows > 0) return launch_tiles(a, p, pl, dev, stream);
+    return launch_tiles(a, p, plan_attention(a, sms), dev, stream);
   }
   return launch(hybrid::attn_plain_kernel(a->input_dtype), static_cast<int64_t>(a->pages.requests) * a->window * a->num_heads,
                 hybrid::kAttnPlainThreads, &p, stream);

@@ -62,29 +62,37 @@ struct AttnParams {
   float scale_log2;                // scale * log2(e)
   // the tiled kernel
   float* part;                     // partial outputs, then their maxima and sums
-  int32_t row_tiles, ctas, page_shift;  // page_shift: log2(page_size), or -1
-  int32_t q_pairs;                 // queries may be read two at a time
+  int32_t row_tiles, ctas, page_shift, tile_shift;  // page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
+  int32_t q_pairs, q_wide;         // queries may be read two at a time, and 16 bytes
   float hidden;                    // a score that times scale_log2 is -infinity
 };
 
-// The tiled kernel: a warp takes kAttnStep tokens at a time, a CTA's four warps kAttnTile; `stages`
-// of them are on the way at once, 96 KB a CTA where two of them share an SM.
-constexpr int kAttnThreads = 128, kAttnStep = 16, kAttnTile = 64, kAttnJoinThreads = 256;
+// The tiled kernel, for heads of up to 64, 128 and 256 columns (`dim`, here, is the one of these that holds
+// a head): a warp takes attn_step() tokens at a time, a CTA's four warps a tile of four times as
+// many; kAttnStages of them are on the way at once, 96 KB a CTA where two of them share an SM.
+constexpr int kAttnThreads = 128, kAttnJoinThreads = 256;
 constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
-constexpr int attn_stages(int esize, int dim) { return esize * dim <= 128 ? 6 : 3; }
-constexpr int attn_smem(int esize, int dim) {
-  return attn_stages(esize, dim) * kAttnTile * 2 * dim * esize + (esize == 4 ? 128 * dim : 0);
+constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+constexpr int attn_step(int esize, int dim) { return esize * dim <= 128 ? 32 : esize * dim <= 512 ? 16 : 8; }
+constexpr int kAttnStages = 3;
+constexpr int attn_box(int esize, int dim) { return attn_step(esize, dim) < 16 ? attn_step(esize, dim) : 16; }  // tokens of a TMA box
+// The rows of a unit at most, for the one type and the other.
+constexpr int attn_rows(int esize, int dim) { return esize == 4 ? (dim == 256 ? 4 : 8) : dim == 256 ? 16 : 32; }
+// bf16 queries that lie in shared memory
+constexpr bool attn_shared_queries(int dim, int rows) { return dim * rows > 2048; }
+// What lies before the stages: those queries, or fp32's weights (each twice).
+constexpr int attn_query(int esize, int dim, int rows) {
+  return esize == 4 ? (4 * attn_step(4, dim) * rows * 8 + 1023) / 1024 * 1024 : attn_shared_queries(dim, rows) ? 2 * dim * rows : 0;
 }
-constexpr int attn_ctas_per_sm(int esize, int dim) { return attn_smem(esize, dim) > 112 * 1024 ? 1 : 2; }
+constexpr int attn_smem(int esize, int dim, int rows) {
+  return kAttnStages * 4 * attn_step(esize, dim) * 2 * dim * esize + attn_query(esize, dim, rows);
+}
+constexpr int attn_ctas_per_sm(int esize, int dim) { return attn_smem(esize, dim, attn_rows(esize, dim)) > 110 * 1024 ? 1 : 2; }
 struct AttnTileParams {
   AttnParams p;
-  CUtensorMap k_map, v_map;  // [pages, page_size, kv heads, dim], boxes of 16 rows of a head, 64 columns
+  CUtensorMap k_map, v_map;  // [pages, page_size, kv heads, dim], boxes of attn_box() rows of a head, 128 bytes of columns
 };
-// Rows of a unit at most: 0 where there is no tiled kernel.  dim 64, 128 and (bf16) 256.
-constexpr int attn_rows(int input_dtype, int dim) {
-  return input_dtype == RSM_F32 ? (dim == 64 || dim == 128 ? 16 : 0) : dim == 64 || dim == 128 ? 32 : dim == 256 ? 16 : 0;
-}
-// rows: of a unit, 16 for fp32 and a multiple of 8 for bf16.  boxes: loads by the tensor maps (bf16).
+// rows: of a unit, 1, 2, 4 or 8 for fp32 and a multiple of 8 for bf16.  boxes: loads by the tensor maps.
 const void* attn_tile_kernel_of(int input_dtype, int dim, int rows, bool boxes);
 const void* attn_join_kernel_of(int input_dtype, int dim, int rows);
 
