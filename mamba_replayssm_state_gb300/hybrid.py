@@ -282,7 +282,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, *, scale=None, out
     up to its own; H is a multiple of the G key heads.  scale defaults to
     dim ** -0.5.  Returns the outputs, shaped like q; rows of a request of length 0 are
     zero.  A call that may be split over the caches' length needs a workspace, which is
-    allocated where `workspace` (a contiguous uint8 CUDA tensor) is not given.
+    allocated where `workspace` (a contiguous uint8 CUDA tensor, which belongs to one call at a time) is not given.
     """
     lib = _lib or _load()
     if stream is None and out is None and workspace is None and device_status is None:

@@ -9,8 +9,8 @@ Bounds.  A rounding is off by at most half a step: U = finfo.eps / 2 of the valu
                amplitude one rounding more; two products and a sum: 3 2^-24: together below 16 2^-24 of m, the
                amplitude times the pair's absolute values; then the output's rounding.
   attention    a score: dim products and their sums, 2^-23 each of the sum of absolute values (a tensor core may cut
-               off where it sums), for fp32 inputs 2^-20 more (three tf32 products); its product with the scale and the
-               distance from the maximum: two roundings of it.  A weight's relative error is the score's error
+               off where it sums); its product with the scale and the distance from the maximum: two roundings of it,
+               2^-22 with room.  A weight's relative error is the score's error
                (and 2^-21 of the exponential), in numerator and denominator: twice that of m, the weights' sum of
                |v|.  The weights' rounding to bf16: U m.  n sums: 2^-23 n m.  Then the output's rounding.
 """
@@ -326,8 +326,8 @@ def test_rotary_bad_sequences_and_in_place():
 # ----------------------------------------------------------------------------
 
 def attention_bound(y, m, top, dim, n, dtype):
-    score = top * (dim * 2.0 ** -23 + (2.0 ** -20 if dtype == F32 else 0.0) + 2.0 ** -22)
-    weight = 2 * (score + 2.0 ** -21) + n * 2.0 ** -23 + (U[BF16] if dtype == BF16 else 2.0 ** -20)
+    score = top * (dim * 2.0 ** -23 + 2.0 ** -22)
+    weight = 2 * (score + 2.0 ** -21) + n * 2.0 ** -23 + (U[BF16] if dtype == BF16 else 0.0)
     return U[dtype] * y.abs() * 1.01 + weight * m
 
 
