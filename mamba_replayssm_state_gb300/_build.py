@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libreplayssm.so")
 SOURCES = ["rsm_api.cu", "rsm_inst_f32.cu", "rsm_inst_bf16.cu", "rsm_inst_f16.cu", "rsm_inst_q8.cu", "rsm_inst_q8sr.cu",
            "rsm_inst_tc.cu", "rsm_inst_q8tc.cu", "gdn_inst.cu", "block_api.cu", "ssm_inst.cu", "ssm_tc_inst.cu", "ssm_token_bf16.cu", "ssm_token_f32.cu",
-           "norm_inst.cu", "hybrid_api.cu", "hybrid_inst.cu", "conv_inst.cu", "attn_inst.cu"]
+           "norm_inst.cu", "hybrid_api.cu", "hybrid_inst.cu", "conv_inst.cu",
+           "attn_bf16_64.cu", "attn_bf16_128.cu", "attn_bf16_256.cu", "attn_f32_64.cu", "attn_f32_128.cu", "attn_f32_256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

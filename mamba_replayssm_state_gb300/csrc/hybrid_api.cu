@@ -206,6 +206,11 @@ AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   return pl;
 }
 
+hybrid::AttnKernels attention_kernels(int input_dtype, int dim, int rows) {
+  if (input_dtype == RSM_F32) return dim == 64 ? hybrid::attn_f32_64(rows) : dim == 128 ? hybrid::attn_f32_128(rows) : hybrid::attn_f32_256(rows);
+  return dim == 64 ? hybrid::attn_bf16_64(rows) : dim == 128 ? hybrid::attn_bf16_128(rows) : hybrid::attn_bf16_256(rows);
+}
+
 using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                        const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                        CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -268,7 +273,8 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
                      page_map(&tp.k_map, pg.k, pg, es, box, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
                      page_map(&tp.v_map, pg.v, pg, es, box, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
   p.q_wide = rows_fit(a->q, es, a->pages.requests, a->q_batch_stride, a->window, a->q_stride);
-  const void* fn = hybrid::attn_tile_kernel_of(a->input_dtype, pl.dim, pl.rows, boxes);
+  const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl.dim, pl.rows);
+  const void* fn = boxes ? kernels.boxes : kernels.tiles;
   int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][boxes], fn, smem);
   if (rc != RSM_OK) return rc;
   rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
@@ -289,7 +295,7 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   void* kargs[] = {&p, &parts, &by_unit};
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, hybrid::attn_join_kernel_of(a->input_dtype, pl.dim, pl.rows), kargs);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernels.join, kargs);
   if (e != cudaSuccess) return fail(RSM_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return done();
 }

@@ -93,8 +93,15 @@ struct AttnTileParams {
   CUtensorMap k_map, v_map;  // [pages, page_size, kv heads, dim], boxes of attn_box() rows of a head, 128 bytes of columns
 };
 // rows: of a unit, 1, 2, 4 or 8 for fp32 and a multiple of 8 for bf16.  boxes: loads by the tensor maps.
-const void* attn_tile_kernel_of(int input_dtype, int dim, int rows, bool boxes);
-const void* attn_join_kernel_of(int input_dtype, int dim, int rows);
+struct AttnKernels {
+  const void *tiles, *boxes, *join;
+};
+AttnKernels attn_bf16_64(int rows);
+AttnKernels attn_bf16_128(int rows);
+AttnKernels attn_bf16_256(int rows);
+AttnKernels attn_f32_64(int rows);
+AttnKernels attn_f32_128(int rows);
+AttnKernels attn_f32_256(int rows);
 
 constexpr int kAttnPlainThreads = 128;
 const void* attn_plain_kernel(int input_dtype);
