@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
         uint32_t bytes = 0;
 #pragma unroll
         for (int h = 0; h < kParts; ++h) bytes += page[h] >= 0 ? Shape::kStage / kParts : 0;
-        rsm::mbar_arrive_expect_tx(bar, bytes);
+        mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
           if (page[h] < 0) continue;

@@ -4,7 +4,9 @@
 // tensors are not the usual ones, which hybrid.py then goes over itself.
 #include "callutil.h"
 
+#include <algorithm>
 #include <cmath>
+#include <utility>
 
 namespace {
 
@@ -100,14 +102,26 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// No two rows of pages [pages, page_size, heads, dim] share memory, whatever their order.
+bool apart(const Tensor& t, int64_t need) {
+  std::pair<int64_t, int64_t> d[3];
+  for (int i = 0; i < 3; ++i) d[i] = {t.stride(i), t.size(i)};
+  std::sort(d, d + 3);
+  for (const auto& [stride, n] : d) {
+    if (n < 2) continue;
+    if (stride < need) return false;
+    need = stride * n;
+  }
+  return true;
+}
+
 // The pages of `b` requests for heads of x's type and size `dim`.
 bool fill_pages(rsm_pages& g, const Tensor& k, const Tensor& v, const Tensor& table, const Tensor& lengths, const Tensor& x, int64_t b) {
   const int64_t dim = x.size(-1);
   if (k.scalar_type() != x.scalar_type() || v.scalar_type() != x.scalar_type() || k.dim() != 4 || v.sizes() != k.sizes() || k.size(3) != dim ||
       k.stride(3) != 1 || v.stride(3) != 1 || !fits(k.size(0)) || !fits(k.size(1)) || !fits(k.size(2)))
     return false;
-  for (int i = 0; i < 3; ++i)
-    if (k.size(i) > 1 && (k.stride(i) < dim || v.stride(i) < dim)) return false;
+  if (!apart(k, dim) || !apart(v, dim)) return false;
   if (table.scalar_type() != at::kInt || table.dim() != 2 || table.size(0) != b || !fits(b) || !fits(table.size(1)) ||
       (table.size(1) > 1 && table.stride(1) != 1) || !vector(lengths, b, at::kInt))
     return false;

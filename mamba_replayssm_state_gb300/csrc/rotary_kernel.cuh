@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
         const int64_t b = (begin + i) / p.window, t = begin + i - b * p.window;
         q = b * p.q_bs + t * p.q_ts, k = b * p.k_bs + t * p.k_ts, v = b * p.v_bs + t * p.v_ts;
       }
-      rsm::mbar_arrive_expect_tx(full + 8 * s, token_bytes);
+      mbar_arrive_expect_tx(full + 8 * s, token_bytes);
       rsm::bulk_g2s(at, static_cast<const IT*>(p.q) + q, qb, full + 8 * s);
       rsm::bulk_g2s(at + qb, static_cast<const IT*>(p.k) + k, kb, full + 8 * s);
       rsm::bulk_g2s(at + qb + kb, static_cast<const IT*>(p.v) + v, kb, full + 8 * s);

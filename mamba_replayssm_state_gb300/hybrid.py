@@ -201,7 +201,10 @@ def _pages(k_cache, v_cache, page_table, lengths, dtype, dim, requests):
         _need(t.dtype == dtype and t.dim() == 4 and t.shape[3] == dim and t.shape == k_cache.shape,
               f"{name} must be {dtype} [pages, page_size, kv_heads, {dim}], and k_cache and v_cache of one shape")
         _need(dim == 1 or t.stride(3) == 1, f"{name} must be contiguous in its last dimension")
-        _need(all(n < 2 or s >= dim for n, s in zip(t.shape[:3], t.stride())), f"rows of {name} overlap")
+        need = dim
+        for stride, n in sorted((s, n) for n, s in zip(t.shape[:3], t.stride()) if n > 1):
+            _need(stride >= need, f"rows of {name} overlap")
+            need = stride * n
     _need(page_table.dtype == _I32 and page_table.dim() == 2 and page_table.shape[0] == requests
           and (page_table.shape[1] < 2 or page_table.stride(1) == 1),
           f"page_table must be an int32 tensor [{requests}, pages of a request] with contiguous rows")
@@ -348,9 +351,11 @@ def copy_pages(page_ptrs, page_strides, src_pages, dst_pages, *, dtype, page_ele
     _check_vector(src_pages, "src_pages", pairs, _I32)
     _check_vector(dst_pages, "dst_pages", pairs, _I32)
     _check_device(page_ptrs, page_strides, src_pages, dst_pages, device_status)
+    page_elements = int(page_elements)
+    _need(abs(page_elements) < 2 ** 63, f"page_elements must fit 64 bits, got {page_elements}")
     rc = lib.rsm_copy_pages(_pack_copy(
         page_ptrs.data_ptr(), page_strides.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), _status(device_status),
-        int(page_elements), pools, pairs, _int32(num_pages, "num_pages"), code), _handle(stream, page_ptrs.get_device()))
+        page_elements, pools, pairs, _int32(num_pages, "num_pages"), code), _handle(stream, page_ptrs.get_device()))
     if rc != 0:
         _raise("copy_pages", rc)
 

@@ -104,6 +104,8 @@ def test_a_gradient_that_would_be_lost_is_refused(name, args):
     ("causal_conv_step", dict(slots=lambda t: t["slots"].long()), "slots must be"),
     ("causal_conv_step", dict(positions=lambda t: t["positions"][:2]), "positions must be"),
     ("rotary_append", dict(k_cache=lambda t: t["k_cache"][:1].expand_as(t["k_cache"])), "overlap"),
+    ("rotary_append", dict(k_cache=lambda t: t["k_cache"].as_strided(t["k_cache"].shape, (64, 128, 64, 1))), "overlap"),
+    ("paged_attention", dict(v_cache=lambda t: t["v_cache"].as_strided(t["v_cache"].shape, (2048, 64, 64, 1))), "overlap"),
     ("rotary_append", dict(v_cache=lambda t: t["v_cache"][:, :8]), "one shape"),
     ("rotary_append", dict(inv_freq=lambda t: torch.ones(33, device="cuda")), "rotary_dim"),
     ("paged_attention", dict(k_cache=lambda t: t["k_cache"].transpose(2, 3).contiguous().transpose(2, 3)), "contiguous"),
@@ -117,6 +119,13 @@ def test_refusals(name, change, msg):
     t = calls()[name][1]
     with pytest.raises((ValueError, rsm.ReplaySSMError), match=msg):
         run(name, {k: f(t) for k, f in change.items()})
+
+
+@pytest.mark.parametrize("n", [2 ** 63, -2 ** 70])
+def test_a_page_past_64_bits_is_refused(n):
+    t = torch.zeros(2, 8, device="cuda")
+    with pytest.raises(ValueError, match="64 bits"):
+        rsm.copy_pages(rsm.pointer_table([t]), rsm.stride_table([t]), i32([0]), i32([1]), dtype=F32, page_elements=n, num_pages=2)
 
 
 def test_results_that_overlap_are_refused():
