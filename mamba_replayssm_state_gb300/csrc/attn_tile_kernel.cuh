@@ -38,6 +38,7 @@
 // them together.
 #pragma once
 #include <type_traits>
+#include <utility>
 
 #include "attn_plain_kernel.cuh"
 #include "rsm_ptx.cuh"
@@ -141,20 +142,37 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+template <int OFFSET>
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
+               : "r"(at), "n"(OFFSET));
 }
+template <int OFFSET>
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
+               : "r"(at), "n"(OFFSET));
+}
+// f(0), f(1), ... f(N - 1), each with a constant of its own.
+template <typename F, int... I>
+__device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each(f, std::make_integer_sequence<int, N>{});
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The first of a sum.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Lane 4 i + j's values (i, 2 j) and (i, 2 j + 1) of an 8 x 8 matrix become (2 j, i) and (2 j + 1, i).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -285,7 +303,7 @@ struct AttnBf16 {
   static constexpr int kRows = 8 * N, kSteps = DIM / 16, kTokens = 16, kStep = Shape::kStep;
   static constexpr bool kShared = attn_shared_queries(DIM, kRows);
   static constexpr int kQuery = attn_query(2, DIM, kRows);
-  static constexpr int kChains = N == 1 ? 4 : 2;  // sums that do not wait for one another
+  static constexpr int kChains = N == 1 ? 4 : N == 2 ? 2 : 1;  // sums that do not wait for one another
   static constexpr int kOwn = kShared ? (kRows * DIM / 8 + kAttnThreads - 1) / kAttnThreads : 1;  // a thread's chunks of the queries
   uint32_t q[kShared ? 1 : N][kShared ? 1 : kSteps][2];
   uint4 next[kOwn];
@@ -357,37 +375,32 @@ struct AttnBf16 {
   __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, const AttnCursor&, int lane, const char* smem) {
     const int quad = lane >> 2, four = lane & 3;
     float part[kChains][N][4], s[N][4];
-#pragma unroll
-    for (int c = 0; c < kChains; ++c)
-#pragma unroll
-      for (int n = 0; n < N; ++n) part[c][n][0] = part[c][n][1] = part[c][n][2] = part[c][n][3] = 0.0f;
+    [[maybe_unused]] uint32_t pair[kShared ? N : 1][4];  // queries' chunks for two steps
     {
+      // Chunks 2 ks and 2 ks + 1 of a token's row: the swizzle turns a chunk's number's lowest three bits by the
+      // token's, so that beside the lane's own bits a step is one more turn, or an offset.
       const int token = a.row + (lane & 15), odd = lane >> 4;
-      if constexpr (kShared) {
-        const uint32_t queries = rsm::smem_addr(smem) + (lane & 7) * (2 * DIM);
-#pragma unroll
-        for (int kk = 0; kk < kSteps / 2; ++kk) {
-          uint32_t k0[4], k1[4];
-          ldmatrix4(k0, a.keys + chunk_at<kStep>(token, 4 * kk + odd));
-          ldmatrix4(k1, a.keys + chunk_at<kStep>(token, 4 * kk + 2 + odd));
-          const int chunk = 4 * kk + (lane >> 3);
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            uint32_t qb[4];
-            ldmatrix4(qb, queries + n * (16 * DIM) + ((chunk & ~7) | ((chunk ^ lane) & 7)) * 16);
-            mma_bf16(part[0][n], k0, qb[0], qb[1]);
-            mma_bf16(part[kChains - 1][n], k1, qb[2], qb[3]);
+      const uint32_t keys = a.keys + token * 128 + ((odd ^ token) & 7) * 16;
+      const uint32_t queries = rsm::smem_addr(smem) + (lane & 7) * (2 * DIM) + (((lane >> 3) ^ lane) & 7) * 16;
+      each<kSteps>([&](auto index) {
+        constexpr int ks = decltype(index)::value;
+        uint32_t ka[4];
+        ldmatrix4<(ks / 4) * (kStep * 128)>(ka, keys ^ (ks % 4 * 32));
+        each<N>([&](auto which) {
+          constexpr int n = decltype(which)::value;
+          uint32_t b0, b1;
+          if constexpr (kShared) {
+            if constexpr (ks % 2 == 0) ldmatrix4<n * (16 * DIM) + (ks / 4) * 128>(pair[n], queries ^ (ks / 2 % 2 * 64));
+            b0 = pair[n][ks % 2 * 2], b1 = pair[n][ks % 2 * 2 + 1];
+          } else {
+            b0 = q[n][ks][0], b1 = q[n][ks][1];
           }
-        }
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          uint32_t ka[4];
-          ldmatrix4(ka, a.keys + chunk_at<kStep>(token, 2 * ks + odd));
-#pragma unroll
-          for (int n = 0; n < N; ++n) mma_bf16(part[ks % kChains][n], ka, q[n][ks][0], q[n][ks][1]);
-        }
-      }
+          if constexpr (ks < kChains)
+            mma_bf16_first(part[ks][n], ka, b0, b1);
+          else
+            mma_bf16(part[ks % kChains][n], ka, b0, b1);
+        });
+      });
     }
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -406,11 +419,16 @@ struct AttnBf16 {
           if (!(a.seen >> j & 1u) || a.token0 + j > limit[n][e & 1]) s[n][e] = p.hidden;
         }
     }
+    // t = log2 of the weights
     bool above = false;
+    float t[N][4];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) above |= fmaf(s[n][e], p.scale_log2, -m[n][e & 1]) > kAttnSlack;
+      for (int e = 0; e < 4; ++e) {
+        t[n][e] = fmaf(s[n][e], p.scale_log2, -m[n][e & 1]);
+        above |= t[n][e] > kAttnSlack;
+      }
     if (__any_sync(0xFFFFFFFFu, above)) {  // some row's maximum moves
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -423,6 +441,8 @@ struct AttnBf16 {
           const float next = fmaxf(m[n][e], top), keep = exp2_fast(m[n][e] - next);
           m[n][e] = next;
           l[n][e] *= keep;
+          t[n][e] = fmaf(s[n][e], p.scale_log2, -next);
+          t[n][e + 2] = fmaf(s[n][e + 2], p.scale_log2, -next);
 #pragma unroll
           for (int i = 0; i < kSteps; ++i) o[i][n][e] *= keep, o[i][n][e + 2] *= keep;
         }
@@ -431,7 +451,7 @@ struct AttnBf16 {
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[n][e] = exp2_fast(fmaf(s[n][e], p.scale_log2, -m[n][e & 1]));
+        s[n][e] = exp2_fast(t[n][e]);
         l[n][e & 1] += s[n][e];
       }
     if (a.differ && p.window > 1)
@@ -457,13 +477,14 @@ struct AttnBf16 {
 #pragma unroll
       for (int h = 0; h < 2; ++h) pb[n][h] = transpose8(rsm::pack_bf16x2(s[n][2 * h], s[n][2 * h + 1]));
     const int token = a.row + (lane >> 4) * 8 + (lane & 7), odd = lane >> 3 & 1;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    const uint32_t values = a.values + token * 128 + ((odd ^ token) & 7) * 16;
+    each<kSteps>([&](auto index) {
+      constexpr int i = decltype(index)::value;
       uint32_t va[4];
-      ldmatrix4_trans(va, a.values + chunk_at<kStep>(token, 2 * i + odd));
+      ldmatrix4_trans<(i / 4) * (kStep * 128)>(va, values ^ (i % 4 * 32));
 #pragma unroll
       for (int n = 0; n < N; ++n) mma_bf16(o[i][n], va, pb[n][0], pb[n][1]);
-    }
+    });
   }
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) const {
 #pragma unroll
