@@ -26,9 +26,9 @@
 // Measured on a GB300 (graphs of calls on changing caches): that batch, 64 requests, bf16,
 // 128 us, 6.4 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
 // seven microseconds of lookups and first loads, and the join are a third of it); drafts of 4
-// tokens, 20 rows, 80000 tokens, 68 us, 4.8 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
+// tokens, 20 rows, 80000 tokens, 67 us, 4.9 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
 // TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 103 us where
-// 4 take 75, and more go at 150 TFLOP/s.
+// 4 take 76, and more go at 160 TFLOP/s.
 //
 // The work of a call is its (request, key head, group of rows) units' tiles of four steps,
 // one after the other, and with each unit kAttnUnit tiles more for what its end takes; every CTA

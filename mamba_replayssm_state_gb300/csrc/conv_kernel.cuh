@@ -13,7 +13,7 @@
 //
 // Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens of 18432 bf16 channels 95 us, 6.3
 // TB/s (129 with the rows to come in registers); 256 requests'
-// single tokens 13.4 us, 4.3 TB/s with the launch's 2.3; 37 tokens of 5376 channels 5.1 us.
+// single tokens 13.4 us, 4.3 TB/s with the launch's 2.3; 37 tokens of 5376 channels 4.6 us.
 #pragma once
 #include "hybrid_device.cuh"
 #include "rsm_ptx.cuh"
@@ -275,12 +275,16 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
         r.store(rows + static_cast<int64_t>((pos + n - j) % R) * p.C);
       }
   };
-  auto one = [&](int64_t t) {  // any token
+  auto one = [&](int64_t t, int at) {  // any token, one of the block's in place `at`
     advance(t);
     if (t < s0) return;
     if (t == s0 && own == s0) start();
     Row<IT, V> in;
-    in.load(x + t * p.x_ts);
+    if (V == 1 || t >= last) {
+      in.load(x + t * p.x_ts);
+    } else if constexpr (V > 1) {
+      in = place.get<Row<IT, V>>(at);
+    }
     const Row<IT, V> y = conv_token<IT, W, V>(taps, h, in, act);
     if (t >= own) y.store(out + t * p.out_ts);
   };
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
       for (int u = 0; u < U; ++u)
         conv_token<IT, W, V>(taps, h, place.get<Row<IT, V>>(at + u), act).store(out + (t + u) * p.out_ts);
     } else {
-      for (int64_t i = t; i < min(t + U, last); ++i) one(i);
+      for (int64_t i = t; i < min(t + U, last); ++i) one(i, at + static_cast<int>(i - t));
     }
     ask(t + kConvAhead, at);
     at = at + U == kConvAhead ? 0 : at + U;
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
   if constexpr (V > 1) cp_async_wait<0>();
   // the rest of the first W - 1 tokens of a sequence that starts here
   if (own == s0 && s0 < last)
-    for (int64_t t = last; t < min(s1, s0 + (W - 1)); ++t) one(t);
+    for (int64_t t = last; t < min(s1, s0 + (W - 1)); ++t) one(t, 0);
 }
 
 // New tokens: a CTA takes p.block requests one after the other, in items of up to U tokens,
