@@ -989,7 +989,9 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
             const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
             const int t = all / p.per;
             IT* out = static_cast<IT*>(p.out) + ((static_cast<int64_t>(was.b) * p.window + t) * p.H + was.g * p.per + all - t * p.per) * p.dim + col;
-            if constexpr (sizeof(IT) == 4)
+            if (!p.out_wide)
+              put(out, y.x * f), put(out + 1, y.y * f), put(out + 2, y.z * f), put(out + 3, y.w * f);
+            else if constexpr (sizeof(IT) == 4)
               *reinterpret_cast<float4*>(out) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
             else
               *reinterpret_cast<uint2*>(out) = make_uint2(rsm::pack_bf16x2(y.x * f, y.y * f), rsm::pack_bf16x2(y.z * f, y.w * f));

@@ -273,6 +273,7 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
                      page_map(&tp.k_map, pg.k, pg, es, box, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
                      page_map(&tp.v_map, pg.v, pg, es, box, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
   p.q_wide = rows_fit(a->q, es, a->pages.requests, a->q_batch_stride, a->window, a->q_stride);
+  p.out_wide = reinterpret_cast<uintptr_t>(a->out) % 16 == 0;  // (a head is whole 16-byte vectors)
   const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl.dim, pl.rows);
   const void* fn = boxes ? kernels.boxes : kernels.tiles;
   int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][boxes], fn, smem);

@@ -64,6 +64,7 @@ struct AttnParams {
   float* part;                     // partial outputs, then their maxima and sums
   int32_t row_tiles, ctas, page_shift, tile_shift;  // page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
   int32_t q_pairs, q_wide;         // queries may be read two at a time, and 16 bytes
+  int32_t out_wide;                // the outputs' rows start on 16 bytes
   float hidden;                    // a score that times scale_log2 is -infinity
 };
 

@@ -62,6 +62,56 @@ def test_both_ways_into_the_library(name):
     assert same(got, want)
 
 
+def off(t):
+    """t an element further on than an allocation starts."""
+    moved = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+    return moved.copy_(t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_at_any_address(name, dtype):
+    """Each tensor, results among them, may start at any element.
+
+    Other paths may serve such a call, and two results of one formula differ by two roundings, a step:
+    2 (eps / 2) |y|.  Beside them, for values around 1: sums of few fp32 terms, 1e-5; attention in fp32, whose
+    scores are off by 64 2^-24 sum |q k| / 8 (3e-5 where that sum is 60), on two sides, in the numerator and the
+    denominator, times |v| up to 4: 5e-4; and with bf16 weights 2^-8 of the largest |v|."""
+    f, t, written = calls(dtype)[name]
+    first = {k: v.clone() for k, v in t.items()}
+    want, kept = f(**first), [first[n] for n in written]
+    atol = 1e-5 if name != "paged_attention" else 5e-4 if dtype == F32 else 2.0 ** -8 * float(t["v_cache"].abs().max())
+    tol = dict(rtol=torch.finfo(dtype).eps, atol=atol)
+    for which in (*t, "out"):
+        args = {k: off(v) if k == which else v.clone() for k, v in t.items()}
+        if which == "out":
+            room = torch.full((want.numel() + 17,), 7.0, dtype=dtype, device="cuda")
+            for at in (1, 2, 4):
+                room.fill_(7.0)
+                args = {k: v.clone() for k, v in t.items()}
+                out = room[at:at + want.numel()].view(want.shape)
+                assert f(**args, out=out) is out
+                torch.testing.assert_close(out, want, **tol)
+                assert bool((room[:at] == 7.0).all()) and bool((room[at + want.numel():] == 7.0).all())
+        else:
+            torch.testing.assert_close(f(**args), want, **tol)
+        for n, k in zip(written, kept):
+            torch.testing.assert_close(args[n], k, **tol)
+
+
+@pytest.mark.parametrize("dtype,dim,T", [(BF16, 128, 4), (BF16, 256, 1), (F32, 128, 1), (F32, 64, 9), (BF16, 24, 1)])
+def test_attention_outputs_at_any_address(dtype, dim, T):
+    """The stores of units in one piece and of those in several, heads of every compiled size."""
+    lengths = [9000, 40, 70, 0, 64]
+    q, kc, vc, table = base.attention_world(lengths, T, 8, 2, dim, 16, dtype, True, 31)
+    want = rsm.paged_attention(q, kc, vc, table, i32(lengths))
+    for at in (1, 2, 4, 8):
+        room = torch.full((want.numel() + 17,), 7.0, dtype=dtype, device="cuda")
+        out = room[at:at + want.numel()].view(want.shape)
+        assert torch.equal(rsm.paged_attention(q, kc, vc, table, i32(lengths), out=out), want)
+        assert bool((room[:at] == 7.0).all()) and bool((room[at + want.numel():] == 7.0).all())
+
+
 @pytest.mark.parametrize("name", NAMES)
 def test_a_raw_stream_needs_results(name):
     side = torch.cuda.Stream()
