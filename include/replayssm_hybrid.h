@@ -19,6 +19,9 @@
  * Types.  Token tensors, caches and outputs: input_dtype (RSM_BF16 or RSM_F32);
  * weights, biases and frequencies fp32.  Sums are fp32 everywhere, and an output is
  * rounded to its type once; what attention rounds on the way stands at its call.
+ *
+ * Sizes.  Sequences, requests, a window, a window's heads (attention) and a token's values
+ * (rsm_rotary_append) are at most 2^30 each; tokens, pages and pools may be more than 2^31 elements.
  */
 #ifndef REPLAYSSM_HYBRID_H
 #define REPLAYSSM_HYBRID_H

@@ -41,6 +41,13 @@ int need(const Named (&list)[K]) {
   return RSM_OK;
 }
 
+// Requests, sequences, windows and a token's or request's rows are counted in 32 bits on the device,
+// with room for the step of a loop.
+constexpr int64_t kMost = int64_t{1} << 30;
+int at_most(int64_t n, const char* name) {
+  return n <= kMost ? RSM_OK : fail(RSM_ENOTSUP, "%s (%lld) must be at most 2^30", name, static_cast<long long>(n));
+}
+
 bool is_input(int dt) { return dt == RSM_F32 || dt == RSM_BF16; }
 int input_size(int dt) { return dt == RSM_F32 ? 4 : 2; }
 
@@ -143,7 +150,7 @@ int check_pages(const rsm_pages& pg, int heads, int kv_heads, int dim, int dt) {
   if (pg.requests < 0) return fail(RSM_EINVAL, "requests must be >= 0 (got %d)", pg.requests);
   if (pg.page_size < 1) return fail(RSM_EINVAL, "page_size must be >= 1 (got %d)", pg.page_size);
   if (pg.num_pages < 0 || pg.table_width < 0) return fail(RSM_EINVAL, "num_pages and table_width must be >= 0");
-  return RSM_OK;
+  return at_most(pg.requests, "requests");
 }
 
 int need_pages(const rsm_pages& pg) {
@@ -160,6 +167,7 @@ int validate(const rsm_paged_attention_args* a, bool pointers) {
   if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
   if (a->window < 1) return fail(RSM_EINVAL, "window must be >= 1 (got %d)", a->window);
   int rc = check_pages(a->pages, a->num_heads, a->num_kv_heads, a->dim, a->input_dtype);
+  if (rc == RSM_OK) rc = at_most(static_cast<int64_t>(a->num_heads) * a->window, "num_heads * window");
   if (rc == RSM_OK && pointers && a->pages.requests > 0) {
     rc = need({{a->q, "q"}, {a->out, "out"}});
     if (rc == RSM_OK) rc = need_pages(a->pages);
@@ -179,10 +187,7 @@ struct AttnPlan {
 };
 
 // Rows of the caches and heads are whole 16-byte vectors.
-bool uses_tiles(const rsm_paged_attention_args* a) {
-  const int64_t rows = static_cast<int64_t>(a->num_heads / a->num_kv_heads) * a->window;
-  return a->dim * input_size(a->input_dtype) % 16 == 0 && rows <= 0x7FFFFF00LL;
-}
+bool uses_tiles(const rsm_paged_attention_args* a) { return a->dim * input_size(a->input_dtype) % 16 == 0; }
 
 // A unit has as many rows as the kernel takes, or the fewest that hold them all (bf16: in eights;
 // fp32: 1, 2, 4 or 8): more than it takes are several units, which read the same keys and values
@@ -309,6 +314,7 @@ int rsm_causal_conv(const rsm_causal_conv_args* a, void* stream) {
   if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
   if (a->num_seqs < 0 || a->tokens < 0) return fail(RSM_EINVAL, "num_seqs and tokens must be >= 0");
   int rc = check_conv(a);
+  if (rc == RSM_OK) rc = at_most(a->num_seqs, "num_seqs");
   if (rc != RSM_OK) return rc;
   if (a->cache != nullptr && a->cache_rows < a->width - 1)
     return fail(RSM_EINVAL, "cache_rows (%d) must be at least width - 1 (%d)", a->cache_rows, a->width - 1);
@@ -347,6 +353,8 @@ int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
   if (a->cache_rows < static_cast<int64_t>(a->width) - 1 + a->window)
     return fail(RSM_EINVAL, "cache_rows (%d) must be at least width - 1 + window (%lld)", a->cache_rows,
                 static_cast<long long>(a->width) - 1 + a->window);
+  rc = at_most(a->window, "window");
+  if (rc != RSM_OK) return rc;
   if (a->batch == 0) return done();
   rc = need({{a->x, "x"}, {a->weight, "weight"}, {a->out, "out"}, {a->cache, "cache"}, {a->slots, "slots"}, {a->positions, "positions"}});
   if (rc != RSM_OK) return rc;
@@ -382,6 +390,9 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   if (rc != RSM_OK) return rc;
   if (a->rotary_dim < 0 || a->rotary_dim % 2 != 0 || a->rotary_dim > a->dim)
     return fail(RSM_EINVAL, "rotary_dim (%d) must be even and at most dim (%d)", a->rotary_dim, a->dim);
+  rc = at_most((static_cast<int64_t>(a->num_heads) + 2LL * a->num_kv_heads) * a->dim, "a token's values");
+  if (rc == RSM_OK && !packed) rc = at_most(a->window, "window");
+  if (rc != RSM_OK) return rc;
   if (a->pages.requests == 0 || (packed && a->tokens == 0)) return done();
   rc = need({{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->q_out, "q_out"}});
   if (rc == RSM_OK && a->rotary_dim > 0) rc = need({{a->inv_freq, "inv_freq"}});

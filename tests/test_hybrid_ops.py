@@ -38,6 +38,7 @@ def filled(cls, names, **values):
     return a
 
 
+MOST = 2 ** 30  # of what the kernels count in 32 bits
 PAGES = dict(table_width=4, num_pages=9, page_size=16, requests=2)
 
 
@@ -92,6 +93,23 @@ REFUSALS = (
         ("dst_pages", None, -1, "dst_pages"), ("page_elements", 0, -1, "page_elements"), ("page_elements", 2 ** 62, -1, "2^40"),
         ("num_pools", -1, -1, "num_pools"), ("num_pairs", -1, -1, "num_pairs"), ("num_pages", -1, -1, "num_pages"),
         ("num_pools", 2 ** 31 - 1, -1, "blocks"), ("dtype", 5, -1, "dtype"), ("dtype", -1, -1, "dtype")]])
+
+
+@pytest.mark.parametrize("name,make,fields,msg", [
+    ("rsm_causal_conv", conv_args, dict(num_seqs=MOST + 1), "num_seqs"),
+    ("rsm_causal_conv_step", step_args, dict(window=MOST + 1, cache_rows=2 ** 31 - 1), "window"),
+    ("rsm_rotary_append", rotary_args, dict(requests=MOST + 1), "requests"),
+    ("rsm_rotary_append", rotary_args, dict(window=MOST + 1), "window"),
+    ("rsm_rotary_append", rotary_args, dict(num_heads=2 ** 24), "a token's values"),
+    ("rsm_paged_attention", attention_args, dict(requests=MOST + 1), "requests"),
+    ("rsm_paged_attention", attention_args, dict(window=MOST // 4 + 1), "num_heads"),
+    ("rsm_paged_attention", attention_args, dict(num_heads=2 ** 31 - 2, window=2 ** 31 - 1), "num_heads")])
+def test_sizes_past_32_bits_are_refused(lib, name, make, fields, msg):
+    a = make()
+    for f, v in fields.items():
+        setattr(a, f, v)
+    assert getattr(lib, name)(bytes(a), None) == -2
+    assert msg in lib.rsm_hybrid_last_error().decode() and "2^30" in lib.rsm_hybrid_last_error().decode()
 
 
 @pytest.mark.parametrize("name,make,field,value,code,msg", REFUSALS,
