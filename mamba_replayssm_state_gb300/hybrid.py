@@ -371,6 +371,7 @@ def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, or
     """
     _need(rotary_dim > 0 and rotary_dim % 2 == 0, "rotary_dim must be even and positive")
     _need(factor > 0, "factor must be positive")
+    _need(base > 0, "base must be positive")
     _need(scaling in (None, "linear", "ntk", "yarn"), f"unknown scaling {scaling!r}")
     if scaling == "ntk":
         _need(rotary_dim > 2, "ntk scaling needs a rotary_dim above 2")
@@ -380,7 +381,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, or
     if scaling == "linear":
         f = f / factor
     elif scaling == "yarn":
-        _need(original_length is not None, "yarn scaling needs original_length")
+        _need(original_length is not None and original_length > 0, "yarn scaling needs original_length, which is positive")
+        _need(fast > slow, "fast must be above slow")
         keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
         f = f * keep + f / factor * (1 - keep)
         amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0

@@ -237,6 +237,13 @@ def test_frequencies_yarn():
     assert torch.allclose(ratio[between], (mix + (1 - mix) / s)[between], rtol=1e-5) and int(between.sum()) > 10
 
 
+@pytest.mark.parametrize("kw,msg", [(dict(slow=4.0, fast=4.0), "above slow"), (dict(original_length=0), "positive"),
+                                    (dict(base=0.0), "base")])
+def test_frequencies_that_are_no_numbers_are_refused(kw, msg):
+    with pytest.raises(ValueError, match=msg):
+        rsm.rotary_frequencies(8, scaling="yarn", device="cpu", **(dict(original_length=4096, factor=2.0) | kw))
+
+
 @pytest.mark.parametrize("args,kw,msg", [((7,), {}, "even"), ((0,), {}, "even"), ((8,), dict(scaling="other"), "unknown"),
                                          ((8,), dict(factor=0.0), "factor"), ((8,), dict(scaling="yarn"), "original_length"),
                                          ((2,), dict(scaling="ntk"), "above 2")])
