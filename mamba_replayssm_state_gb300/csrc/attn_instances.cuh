@@ -7,7 +7,9 @@ namespace hybrid {
 
 template <typename Math, int DIM>
 AttnKernels attn_kernels() {
-  return {reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, false>), reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, true>),
+  return {{reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, AttnLoads::kRows>),
+           reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, AttnLoads::kBoxes>),
+           reinterpret_cast<const void*>(&attn_tile_kernel<Math, DIM, AttnLoads::kGather>)},
           reinterpret_cast<const void*>(&attn_join_kernel<Math, DIM>)};
 }
 

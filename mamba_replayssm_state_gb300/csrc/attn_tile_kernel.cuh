@@ -7,10 +7,11 @@
 // Memory bounds it: 8 rows of 128 columns make 8 multiplications of a byte of keys and
 // values.  So the cache is what is organised.  A CTA has four warps, and
 // each streams a step of 8 to 32 tokens (16 KB or 8) at a time through shared memory of its
-// own, three stages of it (TMA boxes of up to 16 tokens where pages are whole boxes, else
-// cp.async: a ragged batch of 200000 tokens, 8 key heads of 128, takes 129 us and 158): no
-// barrier of the CTA holds a load back, and warps are joined only at the end of a
-// request's part.  The running maximum is one only to within 2^8: it is taken, and sums and
+// own, three stages of it (TMA boxes of up to 16 tokens where pages are whole boxes; else gathers of
+// four rows, a lane each, where the pages make one matrix of rows; else cp.async.  100000 tokens, 8
+// key heads of 128, bf16, in pages of 16, 7 and 1 take 69, 74 and 80 us by boxes and gathers, 104 and
+// 109 by cp.async of pages of 7 and 1): no barrier of the CTA holds a load back, and warps are joined
+// only at the end of a request's part.  The running maximum is one only to within 2^8: it is taken, and sums and
 // outputs scaled anew, where a score passes it by more, which takes a few steps of a
 // request instead of all.
 //
@@ -23,7 +24,7 @@
 // Head sizes between the compiled ones (64, 128, 256) are padded with zeros on the chip; the
 // padding is not read from memory.
 //
-// Measured on a GB300 (graphs of calls on changing caches): that batch, 64 requests, bf16,
+// Measured on a GB300 (graphs of calls on changing caches): 200000 tokens in 64 requests, 8 key heads of 128, bf16,
 // 128 us, 6.4 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
 // seven microseconds of lookups and first loads, and the join are a third of it); drafts of 4
 // tokens, 20 rows, 80000 tokens, 67 us, 4.9 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
@@ -152,6 +153,14 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(column), "r"(head), "r"(row), "r"(page), "r"(bar)
+      : "memory");
+}
+
+// 128 bytes of each of four rows.
+__device__ __forceinline__ void gather_load(uint32_t dst, const CUtensorMap* map, int column, const int (&row)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(column), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
       : "memory");
 }
 
@@ -751,25 +760,27 @@ struct AttnF32 {
   }
 };
 
-// BOXES: loads by TMA, in boxes of attn_box() rows; the pages are whole boxes.
-template <typename Math, int DIM, bool BOXES>
+// LOADS: by TMA in boxes of attn_box() rows, where the pages are whole boxes, or four rows at a time from
+// anywhere; or by cp.async.
+template <typename Math, int DIM, AttnLoads LOADS>
 __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM))
     attn_tile_kernel(const __grid_constant__ AttnTileParams tp) {
   using IT = typename Math::IT;
   using Shape = AttnShape<IT, DIM>;
   constexpr int kWarps = kAttnThreads / 32, kRows = Math::kRows, S = Shape::kStages, kChunks = Shape::kChunks;
   constexpr int kStep = Shape::kStep, kTile = 4 * kStep, kTokens = Math::kTokens, kBox = 128 / static_cast<int>(sizeof(IT));  // columns of a box
+  constexpr bool BOXES = LOADS == AttnLoads::kBoxes, GATHER = LOADS == AttnLoads::kGather, TMA = BOXES || GATHER;
   constexpr int kBoxRows = attn_box(sizeof(IT), DIM), kParts = BOXES ? kStep / kBoxRows : 1;  // a step's boxes of rows
   constexpr uint32_t kAll = Shape::kAll;
   extern __shared__ __align__(1024) char smem[];
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
   __shared__ uint32_t seen_s[kWarps][S];
-  __shared__ __align__(8) uint64_t full_s[kWarps][S];  // BOXES: a stage's loads
+  __shared__ __align__(8) uint64_t full_s[kWarps][S];  // TMA: a stage's loads
   const AttnParams& p = tp.p;
   const rsm_pages& pg = p.pages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if constexpr (BOXES) {
+  if constexpr (TMA) {
     if (lane == 0) {
       for (int i = 0; i < S; ++i) rsm::mbar_init(rsm::smem_addr(&full_s[warp][i]), 1);
       rsm::fence_mbar_init();
@@ -815,7 +826,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   // ---- loads: a warp's step of a tile ----
   const uint32_t ring = rsm::smem_addr(smem) + Math::kQuery + warp * (S * Shape::kStage);
   const uint32_t full = rsm::smem_addr(&full_s[warp][0]);
-  const bool one_page = BOXES || pg.page_size % kStep == 0;  // a step, or a box, lies in one page
+  const bool one_page = BOXES || (!GATHER && pg.page_size % kStep == 0);  // a step, or a box, lies in one page
   auto first_bits = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
   auto page_at = [&](int64_t token) {
     if (token >= ask.len) return -1;  // no token
@@ -838,7 +849,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   look_up(true);
   auto load = [&](int stage) {
     if (ask_room <= 0) {
-      if constexpr (!BOXES) cp_async_commit();
+      if constexpr (!TMA) cp_async_commit();
       return;
     }
     const int g = ask.g, token0 = ask.tile * kTile + warp * kStep;
@@ -875,6 +886,26 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
           }
         }
       }
+    } else if constexpr (GATHER) {
+      // a lane a token's row, then a lane four rows' 128 bytes of keys or of values
+      const bool good = pages >= 0 && pages < pg.num_pages;
+      const int token = token0 + lane % kStep;
+      if (!good && token < ask.len) flag(p.status, RSM_STATUS_BAD_PAGE);
+      const int row = p.page_shift >= 0 ? token & (pg.page_size - 1) : token % pg.page_size;
+      const int index = good ? pages * p.page_rows + row + g * p.head_rows : 0;  // (the first row stands in for none)
+      seen = __ballot_sync(0xFFFFFFFFu, good) & kAll;
+      constexpr int kGroups = kStep / 4, kColumns = DIM / kBox;
+      static_assert(2 * kGroups * kColumns <= 32);
+      const int group = lane % kGroups, column = lane / kGroups % kColumns, value = lane / (kGroups * kColumns);
+      const uint32_t bar = full + stage * 8;
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc((seen | seen >> 1 | seen >> 2 | seen >> 3) & 0x11111111u) * (Shape::kStage / kGroups));
+      int rows[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rows[k] = __shfl_sync(0xFFFFFFFFu, index, 4 * group + k);
+      __syncwarp();
+      if (value < 2 && (seen >> (4 * group) & 15u) != 0)
+        gather_load(base + value * Shape::kHalf + column * (kStep * 128) + group * 512, value == 0 ? &tp.k_map : &tp.v_map,
+                    g * p.head_columns + kBox * column, rows, bar);
     } else {
       const int page = one_page ? __shfl_sync(0xFFFFFFFFu, pages, ask.tile % kLook) : pages;
       const bool good = page >= 0 && page < pg.num_pages;
@@ -914,7 +945,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   int from = at.tile;  // the piece's first tile
   uint32_t phase = 0;
   for (int stage = 0;;) {
-    if constexpr (BOXES) {
+    if constexpr (TMA) {
       if (!rsm::mbar_wait(full + stage * 8, phase, kAttnTimeoutNs)) {  // (never expected)
         flag(p.status, RSM_STATUS_WAIT_TIMEOUT);
         for (int k = 0; k < S; ++k) (void)rsm::mbar_wait(full + k * 8, k < stage ? phase ^ 1u : phase, 1000000ull);  // copies on the way
@@ -931,7 +962,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       a.keys = ring + stage * Shape::kStage;
       a.values = a.keys + Shape::kHalf;
       a.held = smem + (a.values - rsm::smem_addr(smem));
-      if constexpr (BOXES) {  // rows behind the last token came with the box
+      if constexpr (TMA) {  // rows behind the last token came with the others
         if (a.seen != kAll) {
           for (int c = lane; c < kStep * kChunks; c += 32)
             if (!(a.seen >> ((c >> 3) % kStep) & 1u)) *reinterpret_cast<uint4*>(a.held + c * 16) = make_uint4(0, 0, 0, 0);
@@ -1001,7 +1032,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
               *reinterpret_cast<float2*>(p.part + 2 * static_cast<int64_t>(p.ctas) * kRows * DIM + (slot * kRows + r) * 2) = make_float2(top, sum);
           }
         }
-        if constexpr (BOXES) rsm::fence_proxy_async_smem();  // the boxes to come write here too
+        if constexpr (TMA) rsm::fence_proxy_async_smem();  // the loads to come write here too
         __syncthreads();
       };
       pass(std::integral_constant<int, 0>{});
@@ -1015,7 +1046,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
     }
     if (++stage == S) stage = 0, phase ^= 1u;
   }
-  if constexpr (!BOXES) cp_async_wait<0>();
+  if constexpr (!TMA) cp_async_wait<0>();
 }
 
 // Units in pieces, `parts` CTAs each, which share the rows out.  By unit, where there

@@ -63,7 +63,7 @@ int launch(const void* fn, int64_t grid, int threads, const void* params, void* 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_attn_ready[kMaxDevices][2][3][33][2];  // input type, dim 64, 128, 256, rows, boxes
+bool g_attn_ready[kMaxDevices][2][3][33][3];  // input type, dim 64, 128, 256, rows, loads
 
 bool g_rotary_ready[kMaxDevices][2];  // input type
 
@@ -254,6 +254,71 @@ bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int es, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows from anywhere: the pages as one matrix of rows, of which a token's is page * page_rows + row
+// + head * head_rows, its columns from head * head_columns on.
+struct RowGrid {
+  int64_t pitch, rows, columns, page_rows, head_rows, head_columns;
+  bool operator==(const RowGrid& o) const {
+    return pitch == o.pitch && rows == o.rows && columns == o.columns && page_rows == o.page_rows && head_rows == o.head_rows &&
+           head_columns == o.head_columns;
+  }
+};
+
+// False where the strides do not make one.
+bool row_grid(RowGrid* r, const rsm_pages& pg, int kv_heads, int dim, int64_t page, int64_t row, int64_t head) {
+  *r = {pg.page_size > 1 ? row : pg.num_pages > 1 ? page : dim, 0, dim, 0, 0, 0};
+  if (r->pitch < dim || pg.num_pages < 1) return false;
+  if (pg.num_pages > 1) {
+    if (page % r->pitch != 0) return false;
+    r->page_rows = page / r->pitch;
+  }
+  if (kv_heads > 1) {
+    if (head >= dim && head < r->pitch)
+      r->head_columns = head, r->columns = (kv_heads - 1) * head + dim;
+    else if (head >= r->pitch && head % r->pitch == 0)
+      r->head_rows = head / r->pitch;
+    else
+      return false;
+  }
+  if (r->columns > r->pitch || r->page_rows < 0 || r->page_rows > 0x7FFFFFFF || r->head_rows > 0x7FFFFFFF) return false;
+  const int64_t pages = pg.num_pages - 1, heads = kv_heads - 1;  // (each product < 2^62)
+  r->rows = pages * r->page_rows;
+  if (r->rows > 0x7FFFFFFF || heads * r->head_rows > 0x7FFFFFFF) return false;
+  r->rows += heads * r->head_rows + pg.page_size;
+  return r->rows <= 0x7FFFFFFF;
+}
+
+bool row_map(CUtensorMap* map, const void* base, const RowGrid& r, int es) {
+  const TensorMapEncodeFn encode = tensor_map_encoder();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(r.columns), static_cast<cuuint64_t>(r.rows)};
+  cuuint64_t stride;
+  if (encode == nullptr || !box_stride(2, r.pitch, es, &stride)) return false;
+  const cuuint32_t box[2] = {128u / es, 1}, ones[2] = {1, 1};
+  return encode(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2u, const_cast<void*>(base), dims, &stride, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call's keys and values are loaded, and its maps.
+hybrid::AttnLoads choose_loads(const rsm_paged_attention_args* a, const AttnPlan& pl, hybrid::AttnTileParams* tp) {
+  const rsm_pages& pg = a->pages;
+  const int es = input_size(a->input_dtype), box = hybrid::attn_box(es, pl.dim), G = a->num_kv_heads;
+  if (pg.page_size % box == 0 && page_map(&tp->k_map, pg.k, pg, es, box, G, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
+      page_map(&tp->v_map, pg.v, pg, es, box, G, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride))
+    return hybrid::AttnLoads::kBoxes;
+  // (columns behind a padded head would be the next one's)
+  RowGrid k, v;
+  if (a->dim == pl.dim && row_grid(&k, pg, G, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
+      row_grid(&v, pg, G, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride) && k == v && row_map(&tp->k_map, pg.k, k, es) &&
+      row_map(&tp->v_map, pg.v, v, es)) {
+    tp->p.page_rows = static_cast<int32_t>(k.page_rows);
+    tp->p.head_rows = static_cast<int32_t>(k.head_rows);
+    tp->p.head_columns = static_cast<int32_t>(k.head_columns);
+    return hybrid::AttnLoads::kGather;
+  }
+  return hybrid::AttnLoads::kRows;
+}
+
 int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& base, const AttnPlan& pl, int dev, void* stream) {
   if (pl.split && (a->workspace == nullptr || a->workspace_bytes < pl.bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
     return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(pl.bytes));
@@ -272,16 +337,12 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
     if (a->pages.page_size == 1 << k) p.page_shift = k;
   p.q_pairs = reinterpret_cast<uintptr_t>(a->q) % 4 == 0 && (a->pages.requests == 1 || a->q_batch_stride % 2 == 0) &&
               (a->window == 1 || a->q_stride % 2 == 0);
-  const rsm_pages& pg = a->pages;
-  const int box = hybrid::attn_box(es, pl.dim);
-  const bool boxes = pg.page_size % box == 0 &&
-                     page_map(&tp.k_map, pg.k, pg, es, box, a->num_kv_heads, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
-                     page_map(&tp.v_map, pg.v, pg, es, box, a->num_kv_heads, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride);
+  const hybrid::AttnLoads loads = choose_loads(a, pl, &tp);
   p.q_wide = rows_fit(a->q, es, a->pages.requests, a->q_batch_stride, a->window, a->q_stride);
   p.out_wide = reinterpret_cast<uintptr_t>(a->out) % 16 == 0;  // (a head is whole 16-byte vectors)
   const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl.dim, pl.rows);
-  const void* fn = boxes ? kernels.boxes : kernels.tiles;
-  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][boxes], fn, smem);
+  const void* fn = kernels.tiles[static_cast<int>(loads)];
+  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][static_cast<int>(loads)], fn, smem);
   if (rc != RSM_OK) return rc;
   rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
   if (rc != RSM_OK || !pl.split) return rc;

@@ -65,6 +65,7 @@ struct AttnParams {
   int32_t row_tiles, ctas, page_shift, tile_shift;  // page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
   int32_t q_pairs, q_wide;         // queries may be read two at a time, and 16 bytes
   int32_t out_wide;                // the outputs' rows start on 16 bytes
+  int32_t page_rows, head_rows, head_columns;  // loads of rows from anywhere: a page's and a head's distance in the maps' rows and columns
   float hidden;                    // a score that times scale_log2 is -infinity
 };
 
@@ -91,11 +92,13 @@ constexpr int attn_smem(int esize, int dim, int rows) {
 constexpr int attn_ctas_per_sm(int esize, int dim) { return attn_smem(esize, dim, attn_rows(esize, dim)) > 110 * 1024 ? 1 : 2; }
 struct AttnTileParams {
   AttnParams p;
-  CUtensorMap k_map, v_map;  // [pages, page_size, kv heads, dim], boxes of attn_box() rows of a head, 128 bytes of columns
+  // boxes: [pages, page_size, kv heads, dim], of attn_box() rows of a head, 128 bytes of columns; gathers: [rows, columns]
+  CUtensorMap k_map, v_map;
 };
-// rows: of a unit, 1, 2, 4 or 8 for fp32 and a multiple of 8 for bf16.  boxes: loads by the tensor maps.
+enum class AttnLoads { kRows, kBoxes, kGather };
+// rows: of a unit, 1, 2, 4 or 8 for fp32 and a multiple of 8 for bf16.  tiles: by AttnLoads.
 struct AttnKernels {
-  const void *tiles, *boxes, *join;
+  const void *tiles[3], *join;
 };
 AttnKernels attn_bf16_64(int rows);
 AttnKernels attn_bf16_128(int rows);

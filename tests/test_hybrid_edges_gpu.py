@@ -449,6 +449,64 @@ def test_attention_table_rows_apart():
     assert torch.equal(got, rsm.paged_attention(q, kc, vc, table, i32(lengths)))
 
 
+def laid_out(t, how):
+    """The pages' values in another layout."""
+    P, page, G, dim = t.shape
+    if how == "heads first":
+        return t.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    if how == "padded":  # pages that are no multiple of their rows apart
+        room = torch.zeros(P, page * G * dim + 8, dtype=t.dtype, device="cuda")
+        room[:, :page * G * dim] = t.reshape(P, -1)
+        return room[:, :page * G * dim].unflatten(1, (page, G, dim))
+    if how == "joined":
+        return torch.stack([t, torch.full_like(t, float("nan"))], 2)[:, :, 0]
+    if how == "rows last":  # a page's rows further apart than pages
+        return t.transpose(0, 1).contiguous().transpose(0, 1)
+    return t
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 128), (BF16, 256), (BF16, 72), (F32, 64), (F32, 128), (F32, 256)])
+@pytest.mark.parametrize("page", [1, 3, 7, 16, 40])
+def test_attention_layouts_of_the_pages(page, dtype, dim):
+    """Tokens in pages of any size and layout, of one head and several: the same bits as from pages of 16, wherever
+    boxes, gathers or single rows are loaded; what lies beside them is not a number, pages out of range are not seen."""
+    lengths, T = [700, 33, 0, 5, 64, 129], 2
+    for G in (1, 3):
+        q, kc, vc, table = base.attention_world(lengths, T, 4 * G, G, dim, 16, dtype, False, 31 + G)
+        want = rsm.paged_attention(q, kc, vc, table, i32(lengths))
+        width = -(-700 // page)
+        order = torch.randperm(len(lengths) * width, generator=torch.Generator().manual_seed(3)).to("cuda")
+        other = order.view(len(lengths), width).int()
+        pools = [torch.full((len(order), page, G, dim), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+        for b, n in enumerate(lengths):
+            at = torch.arange(n, device="cuda")
+            for pool, c in zip(pools, (kc, vc)):
+                pool[other[b, at // page].long(), at % page] = c[table[b, at // 16].long(), at % 16]
+        for hk, hv in (("", ""), ("heads first", "heads first"), ("padded", "padded"), ("joined", "joined"), ("", "heads first"),
+                       ("rows last", "rows last"), ("padded", "joined")):
+            k, v = laid_out(pools[0], hk), laid_out(pools[1], hv)
+            status = word()
+            got = rsm.paged_attention(q, k, v, other, i32(lengths), device_status=status)
+            assert torch.equal(got, want) and int(status) == 0, (G, hk, hv)
+        bad = other.clone()
+        bad[0, width // 2] = len(order)
+        bad[4, 0] = -1
+        got = rsm.paged_attention(q, pools[0], pools[1], bad, i32(lengths), device_status=status)
+        assert int(status) == 128 and torch.equal(got[[1, 2, 3, 5]], want[[1, 2, 3, 5]]) and bool(torch.isfinite(got).all())
+        live = torch.ones(700, dtype=torch.bool)
+        live[width // 2 * page:(width // 2 + 1) * page] = False
+        at = torch.arange(700, device="cuda")
+        for h in range(4 * G):
+            s = (pools[0][other[0, at // page].long(), at % page, h // 4].double() @ q[0, :, h].double().T) * dim ** -0.5
+            for t in range(T):
+                see = live.to("cuda") & (at <= 700 - T + t)
+                w = torch.softmax(s[:, t].masked_fill(~see, -torch.inf), 0)
+                vals = vc[table[0, at // 16].long(), at % 16, h // 4].double()
+                y, m = w @ vals, w @ vals.abs()
+                bound = (2.0 ** -8 * (y.abs() + m) if dtype == BF16 else 0 * m) + 1e-4 * (1 + m)
+                assert bool(((got[0, t, h].double() - y).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("page", [16, 8])
 def test_attention_pages_past_2_31_values(page):
     """Pages whose offsets pass 32 bits, by boxes and by rows."""
