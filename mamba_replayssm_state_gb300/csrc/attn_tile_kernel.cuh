@@ -28,7 +28,7 @@
 // 128 us, 6.4 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
 // seven microseconds of lookups and first loads, and the join are a third of it); drafts of 4
 // tokens, 20 rows, 80000 tokens, 67 us, 4.9 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
-// TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 103 us where
+// TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 99 us where
 // 4 take 76, and more go at 160 TFLOP/s.
 //
 // The work of a call is its (request, key head, group of rows) units' tiles of four steps,
@@ -327,6 +327,9 @@ struct AttnBf16 {
   static constexpr int kQuery = attn_query(2, DIM, kRows);
   static constexpr int kChains = N == 1 ? 4 : N == 2 ? 2 : 1;  // sums that do not wait for one another
   static constexpr int kOwn = kShared ? (kRows * DIM / 8 + kAttnThreads - 1) / kAttnThreads : 1;  // a thread's chunks of the queries
+  // The next unit's queries are asked for before this one's last products, where they come to shared memory
+  // (32 rows, 100000 tokens: 106 -> 99 us; in registers, which that takes more of, no difference).
+  static constexpr bool kEarly = kShared;
   uint32_t q[kShared ? 1 : N][kShared ? 1 : kSteps][2];
   uint4 next[kOwn];
   int limit[N][2];
@@ -580,6 +583,7 @@ struct AttnF32 {
     if (kTake == 4) return R > 1 ? (lane >> 2 & 1) * kHalf : 0;
     return R > 2 ? (lane >> 1 & 1) * (R / 2) + (lane >> 2 & 1) * (R / 4) : R > 1 ? (lane >> 1 & 1) : 0;
   }
+  static constexpr bool kEarly = false;
   static constexpr int kKept = kTake == 4 ? kHalf : R > 2 ? R / 4 : 1;  // rows that a lane ends with, kHalf or fewer
 
   __device__ __forceinline__ void reset() {
@@ -945,6 +949,13 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   int from = at.tile;  // the piece's first tile
   uint32_t phase = 0;
   for (int stage = 0;;) {
+    AttnCursor then = at;  // the unit after this one
+    if constexpr (Math::kEarly) {
+      if (at.tile + 1 == at.tiles && room > 1 + kAttnUnit) {
+        then.next_unit(p);
+        math.fetch(p, then, lane);
+      }
+    }
     if constexpr (TMA) {
       if (!rsm::mbar_wait(full + stage * 8, phase, kAttnTimeoutNs)) {  // (never expected)
         flag(p.status, RSM_STATUS_WAIT_TIMEOUT);
@@ -993,8 +1004,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
       math.stats(m_s[warp], l_s[warp], lane);
       if (!over) {  // the next unit's queries are on their way meanwhile
-        at.next(p);
-        math.fetch(p, at, lane);
+        if constexpr (Math::kEarly) {
+          at = then;
+        } else {
+          at.next(p);
+          math.fetch(p, at, lane);
+        }
       }
       // the warps' outputs pass through the stages just read, 16 rows at a time
       char* const pass_at = smem + Math::kQuery + stage * Shape::kStage;
