@@ -65,7 +65,7 @@ std::mutex g_mu;
 int g_sms[kMaxDevices];
 bool g_attn_ready[kMaxDevices][2][3][33][3];  // input type, dim 64, 128, 256, rows, loads
 
-bool g_rotary_ready[kMaxDevices][2];  // input type
+bool g_rotary_ready[kMaxDevices][2][2];  // input type, 16 bytes at a time
 
 // Lets a kernel take up to `bytes` of dynamic shared memory: once, since the limit is the
 // kernel's and not the call's, and calls come from several threads.
@@ -486,19 +486,22 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   p.interleaved = a->interleaved != 0;
   p.amplitude = a->amplitude;
   const int es = input_size(a->input_dtype), v = 16 / es;
-  const bool vec = a->dim % v == 0 && (a->interleaved ? a->rotary_dim : p.half) % v == 0 && rows_fit(p.q, es, b, p.q_bs, n, p.q_ts) &&
-                   rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
-                   rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads);
+  const bool aligned = rows_fit(p.q, es, b, p.q_bs, n, p.q_ts) && rows_fit(p.k, es, b, p.k_bs, n, p.k_ts) && rows_fit(p.v, es, b, p.v_bs, n, p.v_ts) &&
+                       rows_fit(p.q_out, es, b, p.out_bs, n, p.out_ts) && pages_fit(p.pages, es, a->num_kv_heads) && a->dim % v == 0;
+  // 16 bytes of pairs at a time; bf16 halves that are not whole 16 bytes, as 24 turned columns', 8 (4 values); else one,
+  // without rings (8 and 8000 tokens of 56 heads of 128, 24 turned columns: 5.5 and 45 us by fours, 12.6 and 209 by one)
+  const int turned = a->interleaved ? a->rotary_dim : p.half;
+  const int at_once = !aligned ? 1 : turned % v == 0 ? v : turned % 4 == 0 ? 4 : 1;
   const int64_t token = (static_cast<int64_t>(a->num_heads) + 2LL * a->num_kv_heads) * a->dim * es, place = token + 8 * p.half;
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  if (!vec || p.tokens <= kRotaryFew * sms || 2 * place > hybrid::kRotaryRingAlone)
-    return launch(hybrid::rotary_token_kernel_of(a->input_dtype, vec), p.tokens, hybrid::kRotaryPlainThreads, &p, stream);
+  if (at_once == 1 || p.tokens <= kRotaryFew * sms || 2 * place > hybrid::kRotaryRingAlone)
+    return launch(hybrid::rotary_token_kernel_of(a->input_dtype, at_once), p.tokens, hybrid::kRotaryPlainThreads, &p, stream);
   const bool alone = 3 * place > hybrid::kRotaryRing;  // (three places: one in, one turned, one out)
   p.stages = static_cast<int>(std::min<int64_t>(hybrid::kRotaryMaxStages, (alone ? hybrid::kRotaryRingAlone : hybrid::kRotaryRing) / place));
-  const void* fn = hybrid::rotary_kernel(a->input_dtype);
-  rc = allow_smem(&g_rotary_ready[dev][a->input_dtype == RSM_F32], fn, hybrid::kRotaryRingAlone);
+  const void* fn = hybrid::rotary_kernel(a->input_dtype, at_once);
+  rc = allow_smem(&g_rotary_ready[dev][a->input_dtype == RSM_F32][at_once == v], fn, hybrid::kRotaryRingAlone);
   if (rc != RSM_OK) return rc;
   return launch(fn, std::min<int64_t>(p.tokens, (alone ? 1 : 2) * sms), hybrid::kRotaryThreads, &p, stream, p.stages * place);
 }

@@ -29,20 +29,25 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// V neighbouring values as they lie in memory: one, or 16 bytes.
+// V neighbouring values as they lie in memory: one, 8 bytes or 16.
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Row {
-  static_assert(V == 1 || V * sizeof(T) == 16);
+  static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  static_assert(V == 1 || kBytes == 8 || kBytes == 16);
   T v[V];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (V == 1)
       v[0] = *p;
+    else if constexpr (kBytes == 8)
+      *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
     else
       *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (V == 1)
       *p = v[0];
+    else if constexpr (kBytes == 8)
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
     else
       *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
   }

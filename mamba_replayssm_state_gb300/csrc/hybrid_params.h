@@ -48,9 +48,9 @@ struct RotaryParams {
 constexpr int kRotaryThreads = 160, kRotaryMaxStages = 8, kRotaryMaxHalf = 128, kRotaryPlainThreads = 256;
 constexpr int kRotaryRing = 104 * 1024, kRotaryRingAlone = 216 * 1024;
 constexpr uint64_t kRotaryTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
-const void* rotary_kernel(int input_dtype);
-// vec: 16 bytes at a time, else an element.
-const void* rotary_token_kernel_of(int input_dtype, bool vec);
+// at_once: values that a thread takes, 1 (the kernel of a CTA a token alone), 4 or (bf16) 8.
+const void* rotary_kernel(int input_dtype, int at_once);
+const void* rotary_token_kernel_of(int input_dtype, int at_once);
 
 struct AttnParams {
   const void* q;

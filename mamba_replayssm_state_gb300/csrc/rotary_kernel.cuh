@@ -96,9 +96,10 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-template <typename IT>
+// V: values that a thread turns at once.
+template <typename IT, int V>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
-  constexpr int V = 16 / sizeof(IT), kWarps = kRotaryThreads / 32 - 1;  // that turn
+  constexpr int kWide = 16 / sizeof(IT), kWarps = kRotaryThreads / 32 - 1;  // that turn
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(8) uint64_t full_s[kRotaryMaxStages], done_s[kRotaryMaxStages];
   __shared__ int live_s[kRotaryMaxStages];
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
         a.store(at);
       }
     } else if (state == 1) {  // a skipped request's queries
-      for (int k = threadIdx.x - 32; k < qn / V; k += 32 * kWarps) *reinterpret_cast<uint4*>(token + k * V) = make_uint4(0, 0, 0, 0);
+      for (int k = threadIdx.x - 32; k < qn / kWide; k += 32 * kWarps) *reinterpret_cast<uint4*>(token + k * kWide) = make_uint4(0, 0, 0, 0);
     }
     rsm::fence_proxy_async_smem();
     __syncwarp();
@@ -263,7 +264,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
 }
 
 // A CTA a token: few tokens, whose way through is shorter than a ring's, and with V = 1 any
-// size, stride and alignment.  A thread's first row is on its way before the token is looked up.
+// size, stride and alignment.  A thread's first row is on its way before the token is looked up, its next
+// one before it stores (8 tokens of 56 fp32 heads of 128: 5.1 us, 5.6 of one row after the other).
 template <typename IT, int V>
 __global__ void __launch_bounds__(kRotaryPlainThreads) rotary_token_kernel(const __grid_constant__ RotaryParams p) {
   __shared__ RotaryToken token;
@@ -307,8 +309,9 @@ __global__ void __launch_bounds__(kRotaryPlainThreads) rotary_token_kernel(const
   if (to.live == 0) return;
   if (static_cast<int>(threadIdx.x) < p.half) turn[threadIdx.x] = rotary_turn(to.pos, step, p.amplitude);
   __syncthreads();
-  for (int i = threadIdx.x; i < items; i += kRotaryPlainThreads) {
-    if (i >= kRotaryPlainThreads) it = load(i);
+  Item ahead;
+  for (int i = threadIdx.x; i < items; i += kRotaryPlainThreads, it = ahead) {
+    if (i + kRotaryPlainThreads < items) ahead = load(i + kRotaryPlainThreads);
     const bool query = it.h < p.H, value = it.h >= p.H + p.G;
     if (!query && to.k_row < 0) continue;
     IT* const row = query   ? static_cast<IT*>(p.q_out) + to.out + static_cast<int64_t>(it.h) * p.dim

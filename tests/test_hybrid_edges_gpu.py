@@ -349,6 +349,30 @@ def test_rotary_few_and_many_tokens(tokens):
                       (0,) if b == 3 else ())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,turned", [(128, 24), (64, 8), (64, 16), (128, 20), (40, 40), (128, 6), (96, 0), (36, 24), (256, 120)])
+def test_rotary_widths_of_the_pairs(dim, turned, interleaved, dtype):
+    """Halves of whole 16 bytes, of 8, of none, by a CTA a token and in rings, a skipped request among them."""
+    H, G, page = 5, 5, 64
+    for tokens in (40, 2600):
+        cu = [0, tokens // 3, tokens - 4, tokens]
+        new = [b - a for a, b in zip(cu, cu[1:])]
+        lengths = [0, 9 + new[1], 100000 + new[2]]
+        g = gen(tokens + dim)
+        table, pages = ref.table([9 + n for n in new], page, 1600, torch.Generator().manual_seed(1))
+        table[2, 1562:1566] = torch.arange(pages, pages + 4, dtype=torch.int32)
+        kc, vc = base.pools(g, pages + 4, page, G, dim, dtype, True)
+        before = kc.clone(), vc.clone()
+        q, k, v = (rand(g, tokens, n, dim, dtype=dtype) for n in (H, G, G))
+        freq = rand(g, turned // 2).abs()
+        status = word()
+        got = rsm.rotary_append(q, k, v, freq, kc, vc, table, i32(lengths), i32(cu), interleaved=interleaved, amplitude=1.25,
+                                device_status=status)
+        assert int(status) == 0
+        base.rotary_check(q, k, v, freq, list(zip(cu, cu[1:])), lengths, table, kc, vc, interleaved, 1.25, got, before, (0,))
+
+
 def test_rotary_negative_and_large_frequencies():
     """A frequency of any sign and size counts modulo a turn."""
     dim, page, far = 64, 16, 1000000
