@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
 
 // A CTA a token: few tokens, whose way through is shorter than a ring's, and with V = 1 any
 // size, stride and alignment.  A thread's first row is on its way before the token is looked up, its next
-// one before it stores (8 tokens of 56 fp32 heads of 128: 5.1 us, 5.6 of one row after the other).
+// one before it stores (256 tokens of 56 fp32 heads of 128: 5.1 us, 5.6 of one row after the other).
 template <typename IT, int V>
 __global__ void __launch_bounds__(kRotaryPlainThreads) rotary_token_kernel(const __grid_constant__ RotaryParams p) {
   __shared__ RotaryToken token;
