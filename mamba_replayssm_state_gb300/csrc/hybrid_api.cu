@@ -238,6 +238,12 @@ bool box_stride(int64_t n, int64_t stride, int es, cuuint64_t* out) {
   return n <= 1 || (stride > 0 && stride < (int64_t{1} << 37));
 }
 
+// What the L2 fetches for a row of a head: no more than the row, behind which lies another head's
+// (400000 tokens of 8 heads of 64, bf16, whose rows are 128 bytes: 150 us, 184 by 256 bytes).
+CUtensorMapL2promotion row_promotion(int dim, int es) {
+  return dim * es % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : dim * es % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+}
+
 // The boxes of `rows` rows of one head, 128 bytes of columns each; false where a map cannot be made.
 bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int es, int rows, int kv_heads, int dim, int64_t page, int64_t row,
               int64_t head) {
@@ -250,7 +256,7 @@ bool page_map(CUtensorMap* map, const void* base, const rsm_pages& pg, int es, i
     return false;
   const cuuint32_t box[4] = {128u / es, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
   return encode(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4u, const_cast<void*>(base), dims, strides, box, ones,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, row_promotion(dim, es),
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -288,14 +294,14 @@ bool row_grid(RowGrid* r, const rsm_pages& pg, int kv_heads, int dim, int64_t pa
   return r->rows <= 0x7FFFFFFF;
 }
 
-bool row_map(CUtensorMap* map, const void* base, const RowGrid& r, int es) {
+bool row_map(CUtensorMap* map, const void* base, const RowGrid& r, int es, int dim) {
   const TensorMapEncodeFn encode = tensor_map_encoder();
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(r.columns), static_cast<cuuint64_t>(r.rows)};
   cuuint64_t stride;
   if (encode == nullptr || !box_stride(2, r.pitch, es, &stride)) return false;
   const cuuint32_t box[2] = {128u / es, 1}, ones[2] = {1, 1};
   return encode(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2u, const_cast<void*>(base), dims, &stride, box, ones,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, row_promotion(dim, es),
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -309,8 +315,8 @@ hybrid::AttnLoads choose_loads(const rsm_paged_attention_args* a, const AttnPlan
   // (columns behind a padded head would be the next one's)
   RowGrid k, v;
   if (a->dim == pl.dim && row_grid(&k, pg, G, a->dim, pg.k_page_stride, pg.k_row_stride, pg.k_head_stride) &&
-      row_grid(&v, pg, G, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride) && k == v && row_map(&tp->k_map, pg.k, k, es) &&
-      row_map(&tp->v_map, pg.v, v, es)) {
+      row_grid(&v, pg, G, a->dim, pg.v_page_stride, pg.v_row_stride, pg.v_head_stride) && k == v && row_map(&tp->k_map, pg.k, k, es, a->dim) &&
+      row_map(&tp->v_map, pg.v, v, es, a->dim)) {
     tp->p.page_rows = static_cast<int32_t>(k.page_rows);
     tp->p.head_rows = static_cast<int32_t>(k.head_rows);
     tp->p.head_columns = static_cast<int32_t>(k.head_columns);
