@@ -220,9 +220,9 @@ constexpr float kAttnSlack = 8.0f;
 constexpr float kAttnLowest = -3.402823466e38f;  // a maximum of nothing: no difference with it is NaN
 constexpr uint64_t kAttnTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
 
-template <typename IT, int DIM>
+template <typename IT, int DIM, int ROWS>
 struct AttnShape {
-  static constexpr int kStep = attn_step(sizeof(IT), DIM);                 // a warp's tokens of a stage
+  static constexpr int kStep = attn_step(sizeof(IT), DIM, ROWS);           // a warp's tokens of a stage
   static constexpr int kChunks = DIM * static_cast<int>(sizeof(IT)) / 16;  // of a row
   static constexpr int kHalf = kStep * DIM * static_cast<int>(sizeof(IT));  // a warp's keys of a stage
   static constexpr int kStage = 2 * kHalf;
@@ -277,15 +277,14 @@ struct AttnStep {
 
 // New tokens' values that are not finite go to the rows that see them, by add(token), and not
 // into the product, where a weight of zero would not keep them from the others.  TOKENS from a.row on.
-template <typename IT, int DIM, int TOKENS, typename F>
+template <typename IT, int DIM, int STEP, int TOKENS, typename F>
 __device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
-  using Shape = AttnShape<IT, DIM>;
-  constexpr int kChunks = Shape::kChunks;
+  constexpr int kChunks = DIM * static_cast<int>(sizeof(IT)) / 16;
   bool odd = false;
   for (int c = lane; c < TOKENS * kChunks; c += 32) {
     const int j = c / kChunks;
     if (j < a.first_new) continue;
-    const uint4 v = rsm::lds128(a.values + chunk_at<Shape::kStep>(a.row + j, c % kChunks));
+    const uint4 v = rsm::lds128(a.values + chunk_at<STEP>(a.row + j, c % kChunks));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -300,7 +299,7 @@ __device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
   for (int c = lane; c < TOKENS * kChunks; c += 32) {
     const int j = c / kChunks;
     if (j < a.first_new) continue;
-    IT* v = reinterpret_cast<IT*>(a.held + chunk_at<Shape::kStep>(a.row + j, c % kChunks));
+    IT* v = reinterpret_cast<IT*>(a.held + chunk_at<STEP>(a.row + j, c % kChunks));
 #pragma unroll
     for (int k = 0; k < 16 / static_cast<int>(sizeof(IT)); ++k)
       if (!isfinite(get(v + k))) v[k] = IT(0);
@@ -309,10 +308,10 @@ __device__ __forceinline__ void odd_values(const AttnStep& a, int lane, F add) {
   __syncwarp();
 }
 
-template <typename IT, int DIM>
+template <typename IT, int STEP>
 __device__ __forceinline__ float held_value(const AttnStep& a, int token, int column) {
   const int c = column * static_cast<int>(sizeof(IT));
-  return get(reinterpret_cast<const IT*>(a.held + chunk_at<AttnShape<IT, DIM>::kStep>(a.row + token, c / 16) + c % 16));
+  return get(reinterpret_cast<const IT*>(a.held + chunk_at<STEP>(a.row + token, c / 16) + c % 16));
 }
 
 // A warp's part of a unit, bf16: 8 N rows.  Lane (quad, four) holds of S^T tokens quad and quad
@@ -321,7 +320,7 @@ __device__ __forceinline__ float held_value(const AttnStep& a, int token, int co
 template <int DIM, int N>
 struct AttnBf16 {
   using IT = uint16_t;
-  using Shape = AttnShape<IT, DIM>;
+  using Shape = AttnShape<IT, DIM, 8 * N>;
   static constexpr int kRows = 8 * N, kSteps = DIM / 16, kTokens = 16, kStep = Shape::kStep;
   static constexpr bool kShared = attn_shared_queries(DIM, kRows);
   static constexpr int kQuery = attn_query(2, DIM, kRows);
@@ -480,7 +479,7 @@ struct AttnBf16 {
         l[n][e & 1] += s[n][e];
       }
     if (a.differ && p.window > 1)
-      odd_values<IT, DIM, kTokens>(a, lane, [&](int j) {
+      odd_values<IT, DIM, kStep, kTokens>(a, lane, [&](int j) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -491,7 +490,7 @@ struct AttnBf16 {
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float v = held_value<IT, DIM>(a, j, 16 * i + 8 * h + quad);
+                const float v = held_value<IT, kStep>(a, j, 16 * i + 8 * h + quad);
                 if (!isfinite(v)) o[i][n][2 * h + e] += w * v;
               }
           }
@@ -544,7 +543,7 @@ struct AttnBf16 {
 template <int DIM, int R>
 struct AttnF32 {
   using IT = float;
-  using Shape = AttnShape<IT, DIM>;
+  using Shape = AttnShape<IT, DIM, R>;
   static constexpr int kRows = R, kStep = Shape::kStep, kTokens = kStep, kQuery = attn_query(4, DIM, R);
   static constexpr int kTake = kStep / 4;             // a group's tokens
   static constexpr int kChunks = DIM / 32;            // a slice's
@@ -701,7 +700,7 @@ struct AttnF32 {
     }
     __syncwarp();
     if (a.differ && p.window > 1)
-      odd_values<IT, DIM, kTokens>(a, lane, [&](int t) {
+      odd_values<IT, DIM, kStep, kTokens>(a, lane, [&](int t) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           int last;
@@ -712,7 +711,7 @@ struct AttnF32 {
 #pragma unroll
           for (int c = 0; c < kCols / 2; ++c) {
             float2 x = both(o[r][c]);
-            const float v0 = held_value<IT, DIM>(a, t, column(lane, 2 * c)), v1 = held_value<IT, DIM>(a, t, column(lane, 2 * c + 1));
+            const float v0 = held_value<IT, kStep>(a, t, column(lane, 2 * c)), v1 = held_value<IT, kStep>(a, t, column(lane, 2 * c + 1));
             if (!isfinite(v0)) x.x += w * v0;
             if (!isfinite(v1)) x.y += w * v1;
             o[r][c] = pair(x.x, x.y);
@@ -767,10 +766,10 @@ struct AttnF32 {
 // LOADS: by TMA in boxes of attn_box() rows, where the pages are whole boxes, or four rows at a time from
 // anywhere; or by cp.async.
 template <typename Math, int DIM, AttnLoads LOADS>
-__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM))
+__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM, Math::kRows))
     attn_tile_kernel(const __grid_constant__ AttnTileParams tp) {
   using IT = typename Math::IT;
-  using Shape = AttnShape<IT, DIM>;
+  using Shape = typename Math::Shape;
   constexpr int kWarps = kAttnThreads / 32, kRows = Math::kRows, S = Shape::kStages, kChunks = Shape::kChunks;
   constexpr int kStep = Shape::kStep, kTile = 4 * kStep, kTokens = Math::kTokens, kBox = 128 / static_cast<int>(sizeof(IT));  // columns of a box
   constexpr bool BOXES = LOADS == AttnLoads::kBoxes, GATHER = LOADS == AttnLoads::kGather, TMA = BOXES || GATHER;

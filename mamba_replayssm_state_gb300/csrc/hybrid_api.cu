@@ -202,10 +202,10 @@ AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   pl.row_tiles = static_cast<int>(row_tiles);
   pl.rows = es == 2 ? static_cast<int>((each + 7) / 8 * 8) : each > 4 ? 8 : each > 2 ? 4 : static_cast<int>(each);
   pl.units = row_tiles * a->num_kv_heads * a->pages.requests;
-  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size, tile = 4 * hybrid::attn_step(es, pl.dim);
+  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size, tile = 4 * hybrid::attn_step(es, pl.dim, pl.rows);
   const int64_t most = std::max<int64_t>((longest + tile - 1) / tile, 1);
   pl.split = most > 1;
-  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(es, pl.dim), 2 * hybrid::kAttnJoinThreads);
+  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(es, pl.dim, pl.rows), 2 * hybrid::kAttnJoinThreads);
   pl.ctas = static_cast<int>(most >= resident ? resident : std::min(resident, pl.units * most));
   if (pl.split) pl.bytes = 2LL * pl.ctas * pl.rows * (pl.dim + 2) * 4;
   return pl;
@@ -328,7 +328,7 @@ hybrid::AttnLoads choose_loads(const rsm_paged_attention_args* a, const AttnPlan
 int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& base, const AttnPlan& pl, int dev, void* stream) {
   if (pl.split && (a->workspace == nullptr || a->workspace_bytes < pl.bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
     return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(pl.bytes));
-  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, pl.dim, pl.rows), step = hybrid::attn_step(es, pl.dim);
+  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, pl.dim, pl.rows), step = hybrid::attn_step(es, pl.dim, pl.rows);
   hybrid::AttnTileParams tp{};
   tp.p = base;
   hybrid::AttnParams& p = tp.p;

@@ -71,25 +71,33 @@ struct AttnParams {
 
 // The tiled kernel, for heads of up to 64, 128 and 256 columns (`dim`, here, is the one of these that holds
 // a head): a warp takes attn_step() tokens at a time, a CTA's four warps a tile of four times as
-// many; kAttnStages of them are on the way at once, 96 KB a CTA where two of them share an SM.
+// many; kAttnStages of them are on the way at once, 96 KB a CTA where two of them share an SM, 48 where three do.
 constexpr int kAttnThreads = 128, kAttnJoinThreads = 256;
 constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
 constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-constexpr int attn_step(int esize, int dim) { return esize * dim <= 128 ? 32 : esize * dim <= 512 ? 16 : 8; }
+// bf16 heads of 64: 8 rows leave registers for a third CTA an SM, which takes shorter steps (8 key heads: 100000 tokens
+// in 256 requests 41 us, 47 by steps of 32 of two; one request of 16000, which more CTAs share, 12.6 and 17.2); more rows
+// keep to two, and longer steps (12 rows, 100000 tokens: 43 us, 45 by steps of 16).
+constexpr bool attn_three(int esize, int dim, int rows) { return esize == 2 && dim == 64 && rows == 8; }
+constexpr int attn_step(int esize, int dim, int rows) {
+  return esize * dim > 512 ? 8 : esize * dim > 128 || attn_three(esize, dim, rows) ? 16 : 32;
+}
 constexpr int kAttnStages = 3;
-constexpr int attn_box(int esize, int dim) { return attn_step(esize, dim) < 16 ? attn_step(esize, dim) : 16; }  // tokens of a TMA box
+constexpr int attn_box(int esize, int dim) { return esize * dim > 512 ? 8 : 16; }  // tokens of a TMA box
 // The rows of a unit at most, for the one type and the other.
 constexpr int attn_rows(int esize, int dim) { return esize == 4 ? (dim == 256 ? 4 : 8) : dim == 256 ? 16 : 32; }
 // bf16 queries that lie in shared memory
 constexpr bool attn_shared_queries(int dim, int rows) { return dim * rows > 2048; }
 // What lies before the stages: those queries, or fp32's weights (each twice).
 constexpr int attn_query(int esize, int dim, int rows) {
-  return esize == 4 ? (4 * attn_step(4, dim) * rows * 8 + 1023) / 1024 * 1024 : attn_shared_queries(dim, rows) ? 2 * dim * rows : 0;
+  return esize == 4 ? (4 * attn_step(4, dim, rows) * rows * 8 + 1023) / 1024 * 1024 : attn_shared_queries(dim, rows) ? 2 * dim * rows : 0;
 }
 constexpr int attn_smem(int esize, int dim, int rows) {
-  return kAttnStages * 4 * attn_step(esize, dim) * 2 * dim * esize + attn_query(esize, dim, rows);
+  return kAttnStages * 4 * attn_step(esize, dim, rows) * 2 * dim * esize + attn_query(esize, dim, rows);
 }
-constexpr int attn_ctas_per_sm(int esize, int dim) { return attn_smem(esize, dim, attn_rows(esize, dim)) > 110 * 1024 ? 1 : 2; }
+constexpr int attn_ctas_per_sm(int esize, int dim, int rows) {
+  return attn_three(esize, dim, rows) ? 3 : attn_smem(esize, dim, attn_rows(esize, dim)) > 110 * 1024 ? 1 : 2;
+}
 struct AttnTileParams {
   AttnParams p;
   // boxes: [pages, page_size, kv heads, dim], of attn_box() rows of a head, 128 bytes of columns; gathers: [rows, columns]
