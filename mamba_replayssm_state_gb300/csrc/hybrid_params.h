@@ -77,7 +77,7 @@ constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
 constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 // bf16 heads of 64: 8 rows leave registers for a third CTA an SM, which takes shorter steps (8 key heads: 100000 tokens
 // in 256 requests 41 us, 47 by steps of 32 of two; one request of 16000, which more CTAs share, 12.6 and 17.2); more rows
-// keep to two, and longer steps (12 rows, 100000 tokens: 43 us, 45 by steps of 16).
+// keep to two, and longer steps (12 rows, 100000 tokens: 45.3 us, 46.9 by steps of 16).
 constexpr bool attn_three(int esize, int dim, int rows) { return esize == 2 && dim == 64 && rows == 8; }
 constexpr int attn_step(int esize, int dim, int rows) {
   return esize * dim > 512 ? 8 : esize * dim > 128 || attn_three(esize, dim, rows) ? 16 : 32;
