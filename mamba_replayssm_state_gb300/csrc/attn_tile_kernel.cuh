@@ -7,7 +7,7 @@
 // Memory bounds it: 8 rows of 128 columns make 8 multiplications of a byte of keys and
 // values.  So the cache is what is organised.  A CTA has four warps, and
 // each streams a step of 8 to 32 tokens (16 KB or 8) at a time through shared memory of its
-// own, three stages of it (TMA boxes of up to 16 tokens where pages are whole boxes; else gathers of
+// own, two or three stages of it (TMA boxes of up to 16 tokens where pages are whole boxes; else gathers of
 // four rows, a lane each, where the pages make one matrix of rows; else cp.async.  100000 tokens, 8
 // key heads of 128, bf16, in pages of 16, 7 and 1 take 69, 74 and 80 us by boxes and gathers, 104 and
 // 109 by cp.async of pages of 7 and 1): no barrier of the CTA holds a load back, and warps are joined
@@ -25,7 +25,7 @@
 // padding is not read from memory.
 //
 // Measured on a GB300 (graphs of calls on changing caches): 200000 tokens in 64 requests, 8 key heads of 128, bf16,
-// 128 us, 6.4 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
+// 125 us, 6.5 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
 // seven microseconds of lookups and first loads, and the join are a third of it); drafts of 4
 // tokens, 20 rows, 80000 tokens, 67 us, 4.9 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
 // TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 99 us where
@@ -220,13 +220,13 @@ constexpr float kAttnSlack = 8.0f;
 constexpr float kAttnLowest = -3.402823466e38f;  // a maximum of nothing: no difference with it is NaN
 constexpr uint64_t kAttnTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
 
-template <typename IT, int DIM, int ROWS>
+template <typename IT, int DIM, bool THREE>
 struct AttnShape {
-  static constexpr int kStep = attn_step(sizeof(IT), DIM, ROWS);           // a warp's tokens of a stage
+  static constexpr int kStep = attn_step(sizeof(IT), DIM, THREE);          // a warp's tokens of a stage
   static constexpr int kChunks = DIM * static_cast<int>(sizeof(IT)) / 16;  // of a row
   static constexpr int kHalf = kStep * DIM * static_cast<int>(sizeof(IT));  // a warp's keys of a stage
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = kAttnStages;
+  static constexpr int kStages = attn_stages(sizeof(IT), DIM, THREE);
   static constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : (1u << kStep) - 1u;
 };
 
@@ -317,10 +317,11 @@ __device__ __forceinline__ float held_value(const AttnStep& a, int token, int co
 // A warp's part of a unit, bf16: 8 N rows.  Lane (quad, four) holds of S^T tokens quad and quad
 // + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.  Up to 16
 // rows' queries stay in registers, those of more (whose outputs take half of them) in shared memory.
-template <int DIM, int N>
+template <int DIM, int N, bool THREE>
 struct AttnBf16 {
   using IT = uint16_t;
-  using Shape = AttnShape<IT, DIM, 8 * N>;
+  using Shape = AttnShape<IT, DIM, THREE>;
+  static constexpr bool kThree = THREE;
   static constexpr int kRows = 8 * N, kSteps = DIM / 16, kTokens = 16, kStep = Shape::kStep;
   static constexpr bool kShared = attn_shared_queries(DIM, kRows);
   static constexpr int kQuery = attn_query(2, DIM, kRows);
@@ -543,7 +544,8 @@ struct AttnBf16 {
 template <int DIM, int R>
 struct AttnF32 {
   using IT = float;
-  using Shape = AttnShape<IT, DIM, R>;
+  using Shape = AttnShape<IT, DIM, false>;
+  static constexpr bool kThree = false;
   static constexpr int kRows = R, kStep = Shape::kStep, kTokens = kStep, kQuery = attn_query(4, DIM, R);
   static constexpr int kTake = kStep / 4;             // a group's tokens
   static constexpr int kChunks = DIM / 32;            // a slice's
@@ -766,7 +768,7 @@ struct AttnF32 {
 // LOADS: by TMA in boxes of attn_box() rows, where the pages are whole boxes, or four rows at a time from
 // anywhere; or by cp.async.
 template <typename Math, int DIM, AttnLoads LOADS>
-__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM, Math::kRows))
+__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename Math::IT), DIM, Math::kThree))
     attn_tile_kernel(const __grid_constant__ AttnTileParams tp) {
   using IT = typename Math::IT;
   using Shape = typename Math::Shape;

@@ -63,7 +63,7 @@ int launch(const void* fn, int64_t grid, int threads, const void* params, void* 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_attn_ready[kMaxDevices][2][3][33][3];  // input type, dim 64, 128, 256, rows, loads
+bool g_attn_ready[kMaxDevices][2][3][33][2][3];  // input type, dim 64, 128, 256, rows, three CTAs an SM, loads
 
 bool g_rotary_ready[kMaxDevices][2][2];  // input type, 16 bytes at a time
 
@@ -182,6 +182,7 @@ struct AttnPlan {
   int row_tiles;  // units of a key head
   int ctas;
   int64_t units;
+  bool three;     // CTAs an SM
   bool split;     // units may have more than one tile, so the join has to run
   int64_t bytes;  // of workspace
 };
@@ -202,18 +203,19 @@ AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   pl.row_tiles = static_cast<int>(row_tiles);
   pl.rows = es == 2 ? static_cast<int>((each + 7) / 8 * 8) : each > 4 ? 8 : each > 2 ? 4 : static_cast<int>(each);
   pl.units = row_tiles * a->num_kv_heads * a->pages.requests;
-  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size, tile = 4 * hybrid::attn_step(es, pl.dim, pl.rows);
+  pl.three = hybrid::attn_three(es, pl.dim, pl.rows, pl.units >= 2 * sms);
+  const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size, tile = 4 * hybrid::attn_step(es, pl.dim, pl.three);
   const int64_t most = std::max<int64_t>((longest + tile - 1) / tile, 1);
   pl.split = most > 1;
-  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(es, pl.dim, pl.rows), 2 * hybrid::kAttnJoinThreads);
+  const int64_t resident = std::min<int64_t>(static_cast<int64_t>(sms) * hybrid::attn_ctas_per_sm(es, pl.dim, pl.three), 2 * hybrid::kAttnJoinThreads);
   pl.ctas = static_cast<int>(most >= resident ? resident : std::min(resident, pl.units * most));
   if (pl.split) pl.bytes = 2LL * pl.ctas * pl.rows * (pl.dim + 2) * 4;
   return pl;
 }
 
-hybrid::AttnKernels attention_kernels(int input_dtype, int dim, int rows) {
+hybrid::AttnKernels attention_kernels(int input_dtype, int dim, int rows, bool three) {
   if (input_dtype == RSM_F32) return dim == 64 ? hybrid::attn_f32_64(rows) : dim == 128 ? hybrid::attn_f32_128(rows) : hybrid::attn_f32_256(rows);
-  return dim == 64 ? hybrid::attn_bf16_64(rows) : dim == 128 ? hybrid::attn_bf16_128(rows) : hybrid::attn_bf16_256(rows);
+  return dim == 64 ? hybrid::attn_bf16_64(rows) : dim == 128 ? hybrid::attn_bf16_128(rows, three) : hybrid::attn_bf16_256(rows);
 }
 
 using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -328,7 +330,7 @@ hybrid::AttnLoads choose_loads(const rsm_paged_attention_args* a, const AttnPlan
 int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& base, const AttnPlan& pl, int dev, void* stream) {
   if (pl.split && (a->workspace == nullptr || a->workspace_bytes < pl.bytes || reinterpret_cast<uintptr_t>(a->workspace) % 256 != 0))
     return fail(RSM_EINVAL, "workspace of %lld bytes, 256-byte aligned, is needed", static_cast<long long>(pl.bytes));
-  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, pl.dim, pl.rows), step = hybrid::attn_step(es, pl.dim, pl.rows);
+  const int es = input_size(a->input_dtype), smem = hybrid::attn_smem(es, pl.dim, pl.rows, pl.three), step = hybrid::attn_step(es, pl.dim, pl.three);
   hybrid::AttnTileParams tp{};
   tp.p = base;
   hybrid::AttnParams& p = tp.p;
@@ -346,9 +348,9 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   const hybrid::AttnLoads loads = choose_loads(a, pl, &tp);
   p.q_wide = rows_fit(a->q, es, a->pages.requests, a->q_batch_stride, a->window, a->q_stride);
   p.out_wide = reinterpret_cast<uintptr_t>(a->out) % 16 == 0;  // (a head is whole 16-byte vectors)
-  const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl.dim, pl.rows);
+  const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl.dim, pl.rows, pl.three);
   const void* fn = kernels.tiles[static_cast<int>(loads)];
-  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][static_cast<int>(loads)], fn, smem);
+  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][pl.three][static_cast<int>(loads)], fn, smem);
   if (rc != RSM_OK) return rc;
   rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
   if (rc != RSM_OK || !pl.split) return rc;

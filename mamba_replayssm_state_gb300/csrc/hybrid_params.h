@@ -71,18 +71,19 @@ struct AttnParams {
 
 // The tiled kernel, for heads of up to 64, 128 and 256 columns (`dim`, here, is the one of these that holds
 // a head): a warp takes attn_step() tokens at a time, a CTA's four warps a tile of four times as
-// many; kAttnStages of them are on the way at once, 96 KB a CTA where two of them share an SM, 48 where three do.
+// many; attn_stages() of them are on the way at once, 96 KB a CTA where two of them share an SM, 48 or 64 where three do.
 constexpr int kAttnThreads = 128, kAttnJoinThreads = 256;
 constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
 constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-// bf16 heads of 64: 8 rows leave registers for a third CTA an SM, which takes shorter steps (8 key heads: 100000 tokens
-// in 256 requests 41 us, 47 by steps of 32 of two; one request of 16000, which more CTAs share, 12.6 and 17.2); more rows
-// keep to two, and longer steps (12 rows, 100000 tokens: 45.3 us, 46.9 by steps of 16).
-constexpr bool attn_three(int esize, int dim, int rows) { return esize == 2 && dim == 64 && rows == 8; }
-constexpr int attn_step(int esize, int dim, int rows) {
-  return esize * dim > 512 ? 8 : esize * dim > 128 || attn_three(esize, dim, rows) ? 16 : 32;
-}
-constexpr int kAttnStages = 3;
+// Eight rows of bf16 heads of 64 and 128 leave registers for a third CTA an SM (`three`).  Heads of 64 take it, with shorter
+// steps (8 key heads: 100000 tokens in 256 requests 41 us, 47 by steps of 32 of two CTAs; one request of 16000, which
+// more CTAs share, 12.6 and 17.2).  Heads of 128, with two stages, where there are two units an SM or more (64 requests, 200000
+// tokens, 8 key heads: 125.5 us, 130.5 of two CTAs; 256 of 78 tokens each 27.7 and 31.1, of 390 73.6 and 72.8); with fewer
+// units there are more pieces to join (8 requests of 1000 tokens 13.6 us, 14.9 of three; one of 131072 29.7 and 30.6).
+// More rows keep to two (12 rows of 64, 100000 tokens: 45.3 us, 46.9 by steps of 16).
+constexpr bool attn_three(int esize, int dim, int rows, bool many) { return esize == 2 && rows == 8 && (dim == 64 || (dim == 128 && many)); }
+constexpr int attn_step(int esize, int dim, bool three) { return esize * dim > 512 ? 8 : esize * dim > 128 || three ? 16 : 32; }
+constexpr int attn_stages(int esize, int dim, bool three) { return three && esize * dim > 128 ? 2 : 3; }
 constexpr int attn_box(int esize, int dim) { return esize * dim > 512 ? 8 : 16; }  // tokens of a TMA box
 // The rows of a unit at most, for the one type and the other.
 constexpr int attn_rows(int esize, int dim) { return esize == 4 ? (dim == 256 ? 4 : 8) : dim == 256 ? 16 : 32; }
@@ -90,13 +91,13 @@ constexpr int attn_rows(int esize, int dim) { return esize == 4 ? (dim == 256 ? 
 constexpr bool attn_shared_queries(int dim, int rows) { return dim * rows > 2048; }
 // What lies before the stages: those queries, or fp32's weights (each twice).
 constexpr int attn_query(int esize, int dim, int rows) {
-  return esize == 4 ? (4 * attn_step(4, dim, rows) * rows * 8 + 1023) / 1024 * 1024 : attn_shared_queries(dim, rows) ? 2 * dim * rows : 0;
+  return esize == 4 ? (4 * attn_step(4, dim, false) * rows * 8 + 1023) / 1024 * 1024 : attn_shared_queries(dim, rows) ? 2 * dim * rows : 0;
 }
-constexpr int attn_smem(int esize, int dim, int rows) {
-  return kAttnStages * 4 * attn_step(esize, dim, rows) * 2 * dim * esize + attn_query(esize, dim, rows);
+constexpr int attn_smem(int esize, int dim, int rows, bool three) {
+  return attn_stages(esize, dim, three) * 4 * attn_step(esize, dim, three) * 2 * dim * esize + attn_query(esize, dim, rows);
 }
-constexpr int attn_ctas_per_sm(int esize, int dim, int rows) {
-  return attn_three(esize, dim, rows) ? 3 : attn_smem(esize, dim, attn_rows(esize, dim)) > 110 * 1024 ? 1 : 2;
+constexpr int attn_ctas_per_sm(int esize, int dim, bool three) {
+  return three ? 3 : attn_smem(esize, dim, attn_rows(esize, dim), false) > 110 * 1024 ? 1 : 2;
 }
 struct AttnTileParams {
   AttnParams p;
@@ -109,7 +110,7 @@ struct AttnKernels {
   const void *tiles[3], *join;
 };
 AttnKernels attn_bf16_64(int rows);
-AttnKernels attn_bf16_128(int rows);
+AttnKernels attn_bf16_128(int rows, bool three);
 AttnKernels attn_bf16_256(int rows);
 AttnKernels attn_f32_64(int rows);
 AttnKernels attn_f32_128(int rows);
