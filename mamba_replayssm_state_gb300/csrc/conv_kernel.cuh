@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
   constexpr int U = 4;
   constexpr int64_t kNever = int64_t{1} << 62;
   static_assert(kConvAhead % U == 0);
-  __shared__ __align__(16) uint4 ring[V == 1 ? 1 : kConvAhead * kConvThreads];
+  __shared__ __align__(16) uint4 ring[V == 1 ? 1 : (kConvAhead + W - 1) * kConvThreads];
   const uint32_t block = blockIdx.x / static_cast<uint32_t>(p.cblocks), cb = blockIdx.x - block * static_cast<uint32_t>(p.cblocks);
   const int64_t first = static_cast<int64_t>(block) * p.block, last = min(first + p.block, p.tokens);
   const int64_t c = (static_cast<int64_t>(cb) * kConvThreads + threadIdx.x) * V;
@@ -260,18 +260,32 @@ __global__ void __launch_bounds__(kConvThreads, V == 1 ? 8 : 4) conv_prompt_kern
     }
     IT* const rows = static_cast<IT*>(p.cache) + slot * p.cache_ss + c;
     const uint32_t pos = static_cast<uint32_t>(at), R = static_cast<uint32_t>(p.R), n = static_cast<uint32_t>(s1 - s0);
+    // All are asked for at once, the last inputs, which only pass through, by way of places of their own (8192 tokens of
+    // 5376 channels in 512 and 2048 sequences: 54 and 101 us, 64 and 131 of one row after the other; through
+    // registers 55 and 97, but then 4096 tokens of four sequences 24 instead of 21.5).
+    if constexpr (V > 1) {
 #pragma unroll
-    for (int j = 1; j < W; ++j)
-      if (at >= j) {
-        Row<IT, V> r;
-        r.load(rows + static_cast<int64_t>((pos - j) % R) * p.C);
-        h.set(j - 1, r);
-      }
+      for (int j = 1; j < W; ++j)
+        if (n >= static_cast<uint32_t>(j)) place.ask(kConvAhead + j - 1, x + (s1 - j) * p.x_ts);
+      cp_async_commit();
+    }
+    Row<IT, V> was[W - 1];
+#pragma unroll
+    for (int j = 1; j < W; ++j) {
+      was[j - 1].zero();
+      if (at >= j) was[j - 1].load(rows + static_cast<int64_t>((pos - j) % R) * p.C);
+    }
+#pragma unroll
+    for (int j = 1; j < W; ++j) h.set(j - 1, was[j - 1]);
+    if constexpr (V > 1) cp_async_wait<0>();
 #pragma unroll
     for (int j = 1; j < W; ++j)
       if (n >= static_cast<uint32_t>(j)) {
         Row<IT, V> r;
-        r.load(x + (s1 - j) * p.x_ts);
+        if constexpr (V > 1)
+          r = place.get<Row<IT, V>>(kConvAhead + j - 1);
+        else
+          r.load(x + (s1 - j) * p.x_ts);
         r.store(rows + static_cast<int64_t>((pos + n - j) % R) * p.C);
       }
   };
