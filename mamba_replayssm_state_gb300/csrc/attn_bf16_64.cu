@@ -3,6 +3,6 @@
 
 namespace hybrid {
 
-AttnKernels attn_bf16_64(int rows) { return attn_bf16<64>(rows, rows == 8); }
+AttnKernels attn_bf16_64(int rows) { return attn_bf16<64>(rows, rows <= 16); }
 
 }  // namespace hybrid

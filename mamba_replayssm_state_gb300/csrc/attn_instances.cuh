@@ -16,14 +16,14 @@ AttnKernels attn_kernels() {
 template <int DIM>
 AttnKernels attn_bf16(int rows, bool three) {
   if constexpr (DIM < 256) {
-    if (three) return attn_kernels<AttnBf16<DIM, 1, true>, DIM>();
+    if (three && rows == 8) return attn_kernels<AttnBf16<DIM, 1, true>, DIM>();
     if (rows == 24) return attn_kernels<AttnBf16<DIM, 3, false>, DIM>();
     if (rows == 32) return attn_kernels<AttnBf16<DIM, 4, false>, DIM>();
   }
   if constexpr (DIM > 64) {
     if (rows == 8) return attn_kernels<AttnBf16<DIM, 1, false>, DIM>();
   }
-  return attn_kernels<AttnBf16<DIM, 2, false>, DIM>();
+  return attn_kernels<AttnBf16<DIM, 2, DIM == 64>, DIM>();
 }
 
 template <int DIM>

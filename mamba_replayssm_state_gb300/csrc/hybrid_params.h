@@ -75,13 +75,13 @@ struct AttnParams {
 constexpr int kAttnThreads = 128, kAttnJoinThreads = 256;
 constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
 constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-// Eight rows of bf16 heads of 64 and 128 leave registers for a third CTA an SM (`three`).  Heads of 64 take it, with shorter
-// steps (8 key heads: 100000 tokens in 256 requests 41 us, 47 by steps of 32 of two CTAs; one request of 16000, which
-// more CTAs share, 12.6 and 17.2).  Heads of 128, with two stages, where there are two units an SM or more (64 requests, 200000
+// Up to 16 rows of bf16 heads of 64 and eight of 128 leave registers for a third CTA an SM (`three`).  Heads of 64 take
+// it, with shorter steps (8 key heads: 100000 tokens in 256 requests 41 us, 47 by steps of 32 of two CTAs; one request of
+// 16000, which more CTAs share, 12.6 and 17.2; 16 rows, 400000 tokens, 145 and 152, but 4 requests of 1000 12.7 and 11.3).
+// Heads of 128, with two stages, where there are two units an SM or more (64 requests, 200000
 // tokens, 8 key heads: 125.5 us, 130.5 of two CTAs; 256 of 78 tokens each 27.7 and 31.1, of 390 73.6 and 72.8); with fewer
 // units there are more pieces to join (8 requests of 1000 tokens 13.6 us, 14.9 of three; one of 131072 29.7 and 30.6).
-// More rows keep to two (12 rows of 64, 100000 tokens: 45.3 us, 46.9 by steps of 16).
-constexpr bool attn_three(int esize, int dim, int rows, bool many) { return esize == 2 && rows == 8 && (dim == 64 || (dim == 128 && many)); }
+constexpr bool attn_three(int esize, int dim, int rows, bool many) { return esize == 2 && (dim == 64 ? rows <= 16 : rows == 8 && dim == 128 && many); }
 constexpr int attn_step(int esize, int dim, bool three) { return esize * dim > 512 ? 8 : esize * dim > 128 || three ? 16 : 32; }
 constexpr int attn_stages(int esize, int dim, bool three) { return three && esize * dim > 128 ? 2 : 3; }
 constexpr int attn_box(int esize, int dim) { return esize * dim > 512 ? 8 : 16; }  // tokens of a TMA box
