@@ -28,11 +28,11 @@
 // 125 us, 6.5 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
 // seven microseconds of lookups and first loads, and the join are a third of it); drafts of 4
 // tokens, 20 rows, 80000 tokens, 67 us, 4.9 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
-// TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 99 us where
-// 4 take 76, and more go at 160 TFLOP/s.
+// TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 85 us where
+// 4 take 75, and more go at 190 TFLOP/s.
 //
 // The work of a call is its (request, key head, group of rows) units' tiles of four steps,
-// one after the other, and with each unit kAttnUnit tiles more for what its end takes; every CTA
+// one after the other, and with each unit two to four tiles more for what its end takes; every CTA
 // takes the same number of them, wherever they begin and end, so that lengths (which only
 // the device knows) may differ as they like.  A unit that a CTA has to itself is finished
 // by it; pieces of others go to the workspace, two a CTA at most, and attn_join_kernel puts
@@ -51,7 +51,7 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, int64_t len) {
 }
 
 // What a unit of that many tiles counts.
-__device__ __forceinline__ int64_t counts(int tiles) { return tiles == 0 ? 0 : tiles + kAttnUnit; }
+__device__ __forceinline__ int64_t counts(const AttnParams& p, int tiles) { return tiles == 0 ? 0 : tiles + p.unit_end; }
 
 // a / b; mostly of numbers of 32 bits, which take a fourth of the time.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -85,7 +85,7 @@ struct Deal {
   int64_t own, total;  // own: of request threadIdx.x
   __device__ __forceinline__ static int64_t of(const AttnParams& p, int b, bool report) {
     if (b >= p.pages.requests) return 0;
-    return counts(tiles_of(p, request_tokens(p.pages, b, p.window, p.status, report))) * (p.G * p.row_tiles);
+    return counts(p, tiles_of(p, request_tokens(p.pages, b, p.window, p.status, report))) * (p.G * p.row_tiles);
   }
   // (One use for each WHICH: its place is written once.)
   template <int WHICH>
@@ -815,12 +815,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   at.at_request(p);
   {
     const int64_t into = begin - place.first;
-    const int unit = static_cast<int>(quotient(into, counts(at.tiles))), tile = static_cast<int>(into - unit * counts(at.tiles));
+    const int unit = static_cast<int>(quotient(into, counts(p, at.tiles))), tile = static_cast<int>(into - unit * counts(p, at.tiles));
     at.g = unit / p.row_tiles;
     at.rt = unit - at.g * p.row_tiles;
     at.tile = tile;
     if (tile >= at.tiles) {  // the share begins in what a unit's end counts
-      room -= counts(at.tiles) - tile;
+      room -= counts(p, at.tiles) - tile;
       if (room <= 0) return skipped();
       at.next_unit(p);
     }
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
       cp_async_commit();
     }
     if (lane == 0) seen_s[warp][stage] = seen;
-    ask_room -= ask.tile + 1 == ask.tiles ? 1 + kAttnUnit : 1;
+    ask_room -= ask.tile + 1 == ask.tiles ? 1 + p.unit_end : 1;
     if (ask_room > 0) {
       const int b = ask.b;
       ask.next(p);
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
   for (int stage = 0;;) {
     AttnCursor then = at;  // the unit after this one
     if constexpr (Math::kEarly) {
-      if (at.tile + 1 == at.tiles && room > 1 + kAttnUnit) {
+      if (at.tile + 1 == at.tiles && room > 1 + p.unit_end) {
         then.next_unit(p);
         math.fetch(p, then, lane);
       }
@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(sizeof(typename
 
     // ---- the end of a unit, or of this CTA's part of it ----
     const bool last_tile = at.tile + 1 == at.tiles;
-    room -= last_tile ? 1 + kAttnUnit : 1;
+    room -= last_tile ? 1 + p.unit_end : 1;
     const bool over = room <= 0;
     if (last_tile || over) {
       const AttnCursor was = at;
@@ -1086,13 +1086,13 @@ __global__ void __launch_bounds__(kAttnJoinThreads) attn_join_kernel(const __gri
     b = index / units;
     u = index - b * units;
     tiles = tiles_of(p, request_tokens(p.pages, b, p.window, nullptr, false));
-    first = d.before(p, b) + u * counts(tiles);
+    first = d.before(p, b) + u * counts(p, tiles);
   } else if (index < deal.ctas) {
     const Place place = d.find(p, deal.begin(index + 1) - 1);
     b = place.b;
     tiles = tiles_of(p, request_tokens(p.pages, b, p.window, nullptr, false));
-    u = static_cast<int>(quotient(deal.begin(index + 1) - 1 - place.first, counts(tiles)));
-    first = place.first + u * counts(tiles);
+    u = static_cast<int>(quotient(deal.begin(index + 1) - 1 - place.first, counts(p, tiles)));
+    first = place.first + u * counts(p, tiles);
     if (first < deal.begin(index)) tiles = 0;  // it began before
   }
   int c0 = 0, pieces = 1;

@@ -338,6 +338,7 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   p.hidden = p.scale_log2 < 0.0f ? INFINITY : -INFINITY;
   if (p.scale_log2 == 0.0f) p.scale_log2 = FLT_MIN;  // (infinity times it stays infinity)
   p.row_tiles = pl.row_tiles;
+  p.unit_end = hybrid::attn_unit_end(es, pl.dim, pl.rows);
   p.ctas = pl.ctas;
   p.tile_shift = step == 8 ? 5 : step == 16 ? 6 : 7;
   p.page_shift = -1;

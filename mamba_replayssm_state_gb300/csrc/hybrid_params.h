@@ -62,7 +62,7 @@ struct AttnParams {
   float scale_log2;                // scale * log2(e)
   // the tiled kernel
   float* part;                     // partial outputs, then their maxima and sums
-  int32_t row_tiles, ctas, page_shift, tile_shift;  // page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
+  int32_t row_tiles, unit_end, ctas, page_shift, tile_shift;  // unit_end: tiles that the end of a unit counts; page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
   int32_t q_pairs, q_wide;         // queries may be read two at a time, and 16 bytes
   int32_t out_wide;                // the outputs' rows start on 16 bytes
   int32_t page_rows, head_rows, head_columns;  // loads of rows from anywhere: a page's and a head's distance in the maps' rows and columns
@@ -73,7 +73,14 @@ struct AttnParams {
 // a head): a warp takes attn_step() tokens at a time, a CTA's four warps a tile of four times as
 // many; attn_stages() of them are on the way at once, 96 KB a CTA where two of them share an SM, 48 or 64 where three do.
 constexpr int kAttnThreads = 128, kAttnJoinThreads = 256;
-constexpr int kAttnUnit = 2;  // tiles that the end of a unit counts
+// Tiles that the end of a unit counts: the more, the more values its warps have to put together (100000 tokens of 8 key
+// heads of 128: 32 rows in 32 requests 85 us with four tiles, 99 with two; 24 rows in 128 83 and 99; 16 in 128 78 with
+// three, 87 with two; heads of 256, 50000 tokens: 8 rows 74 with three, 79 with two, 16 rows 81 with four, 84 with three.
+// One tile: 20 rows 77 us, 67 with more; six or eight: 24 rows in 128 requests 87 and 94).
+constexpr int attn_unit_end(int esize, int dim, int rows) {
+  const int values = dim * rows;  // of an output
+  return esize == 4 ? 2 : rows > 16 || values > 2048 ? 4 : rows > 8 || values > 1024 ? 3 : 2;
+}
 constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 // Up to 16 rows of bf16 heads of 64 and eight of 128 leave registers for a third CTA an SM (`three`).  Heads of 64 take
 // it, with shorter steps (8 key heads: 100000 tokens in 256 requests 41 us, 47 by steps of 32 of two CTAs; one request of
