@@ -447,9 +447,13 @@ int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
   return launch(hybrid::conv_step_kernel_of(a->input_dtype, a->width, vec), groups * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
 
-// Tokens an SM up to which each has a CTA of its own: 1, 64, 608, 2000 and 4096 tokens (32 heads and 8 of 128, bf16) take
-// 3.3, 3.5, 5.5, 15.7 and 27.8 us so, and 5.5, 5.8, 8.1, 18.1 and 26.3 in rings.
-constexpr int kRotaryFew = 16;
+// Tokens an SM up to which each has a CTA of its own; us so and in rings, 32 heads and 8, bf16 where not said:
+//   heads of 128 turned whole, halves    2500 tokens 18.6 and 20.8, 3600 23.9 and 24.4, 6000 36.4 and 33.8
+//   the same, fp32 (rings of few tokens) 3000 27.9 and 31.1, 8192 64.3 and 74.0, 16000 120.7 and 138.0
+//   the same, neighbours                 3000 23.5 and 22.4, 6000 42.1 and 33.9
+//   64 of 128 turned                     1200 12.2 and 11.0, 3000 22.9 and 18.6; fp32 1200 16.8 and 15.8
+//   24 of 128 (by fours, in halves)      300 6.5 and 6.5, 600 8.2 and 7.5, 2000 24.2 and 15.2
+int64_t rotary_few(bool whole, bool interleaved, int es) { return !whole ? 6 : interleaved ? 16 : es == 2 ? 24 : INT32_MAX; }
 
 int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
@@ -505,7 +509,7 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  if (at_once == 1 || p.tokens <= kRotaryFew * sms || 2 * place > hybrid::kRotaryRingAlone)
+  if (at_once == 1 || p.tokens <= rotary_few(a->rotary_dim == a->dim && at_once == v, a->interleaved != 0, es) * sms || 2 * place > hybrid::kRotaryRingAlone)
     return launch(hybrid::rotary_token_kernel_of(a->input_dtype, at_once), p.tokens, hybrid::kRotaryPlainThreads, &p, stream);
   const bool alone = 3 * place > hybrid::kRotaryRing;  // (three places: one in, one turned, one out)
   p.stages = static_cast<int>(std::min<int64_t>(hybrid::kRotaryMaxStages, (alone ? hybrid::kRotaryRingAlone : hybrid::kRotaryRing) / place));

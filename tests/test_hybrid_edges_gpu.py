@@ -328,7 +328,7 @@ def test_conv_more_than_2_31_values():
 
 @pytest.mark.parametrize("tokens", [1, 2431, 2433, 5000])
 def test_rotary_few_and_many_tokens(tokens):
-    """The two kernels, on either side of where they take turns (16 tokens an SM), skipped requests among them."""
+    """The two kernels, skipped requests among them."""
     H, G, dim, n, page = 4, 2, 64, 32, 64
     b = 3 if tokens > 3 else 1
     cu = [0, tokens // 3, tokens // 3, tokens] if b == 3 else [0, 1]
@@ -347,6 +347,23 @@ def test_rotary_few_and_many_tokens(tokens):
     assert int(status) == 0
     base.rotary_check(q, k, v, freq, list(zip(cu, cu[1:])), lengths, table, kc, vc, False, 1.0, got, before,
                       (0,) if b == 3 else ())
+
+
+@pytest.mark.parametrize("turned,an_sm", [(64, 24), (32, 6)])
+@pytest.mark.parametrize("more", [0, 1])
+def test_rotary_where_the_kernels_take_turns(turned, an_sm, more):
+    """The last number of tokens that have a CTA each, and the first that share rings, of one request and empty ones."""
+    tokens = an_sm * torch.cuda.get_device_properties(0).multi_processor_count + more
+    H, G, dim, page = 3, 1, 64, 16
+    cu, lengths = [0, 0, tokens, tokens], [5, tokens + 3, 1]
+    table, pages = ref.table(lengths, page, 0, torch.Generator().manual_seed(1))
+    g = gen(tokens)
+    kc, vc = base.pools(g, pages, page, G, dim, BF16, False)
+    before = kc.clone(), vc.clone()
+    q, k, v = (rand(g, tokens, n, dim, dtype=BF16) for n in (H, G, G))
+    freq = rand(g, turned // 2).abs()
+    got = rsm.rotary_append(q, k, v, freq, kc, vc, table, i32(lengths), i32(cu))
+    base.rotary_check(q, k, v, freq, list(zip(cu, cu[1:])), lengths, table, kc, vc, False, 1.0, got, before)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
