@@ -62,7 +62,8 @@ struct AttnParams {
   float scale_log2;                // scale * log2(e)
   // the tiled kernel
   float* part;                     // partial outputs, then their maxima and sums
-  int32_t row_tiles, unit_end, ctas, page_shift, tile_shift;  // unit_end: tiles that the end of a unit counts; page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
+  int32_t row_tiles, ctas, page_shift, tile_shift;  // page_shift: log2(page_size), or -1; tile_shift: of a tile's tokens
+  int32_t unit_end;                // tiles that the end of a unit counts
   int32_t q_pairs, q_wide;         // queries may be read two at a time, and 16 bytes
   int32_t out_wide;                // the outputs' rows start on 16 bytes
   int32_t page_rows, head_rows, head_columns;  // loads of rows from anywhere: a page's and a head's distance in the maps' rows and columns
