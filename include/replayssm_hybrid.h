@@ -148,7 +148,8 @@ RSM_API int rsm_rotary_append(const rsm_rotary_append_args *args, void *stream);
  * and rows of whole 16-byte vectors, the weights (each softmax's numerators) are rounded to
  * bf16 for the product with v: with M the sum of the absolute values of an output's terms it is
  * within 2^-8 |y| + 2^-8 M.
- * Values that are not finite reach the rows whose token sees them, and no others.
+ * Values that are not finite reach the rows whose token sees them, and no others; a numerator is at most one
+ * where it meets its value, so an output is finite where the number of tokens times the largest value is.
  */
 typedef struct rsm_paged_attention_args {
   const void *q;   /* [requests, window, num_heads, dim] */

@@ -11,9 +11,10 @@
 // four rows, a lane each, where the pages make one matrix of rows; else cp.async.  100000 tokens, 8
 // key heads of 128, bf16, in pages of 16, 7 and 1 take 69, 74 and 80 us by boxes and gathers, 104 and
 // 109 by cp.async of pages of 7 and 1): no barrier of the CTA holds a load back, and warps are joined
-// only at the end of a request's part.  The running maximum is one only to within 2^8: it is taken, and sums and
-// outputs scaled anew, where a score passes it by more, which takes a few steps of a
-// request instead of all.
+// only at the end of a request's part.  Weights are taken against a bound of the running maximum: where a score passes
+// it, that row's bound becomes 2^8 times its maximum, and its sum and outputs are scaled anew, which takes a few steps of
+// a request instead of all.  So a weight is at most one, and sums of large values do not overflow before their row's
+// quotient would; the largest weight of a row is at least 2^-8, far from where fp32 and bf16 end.
 //
 // The bf16 products are m16n8k16 instructions on registers: with a few rows a 128-row tcgen05
 // tile would be mostly empty.  They are taken the other way round, S^T = K Q^T and
@@ -216,7 +217,7 @@ __device__ __forceinline__ int chunk_at(int token, int chunk) {
   return (chunk >> 3) * (STEP * 128) + token * 128 + ((chunk & 7) ^ (token & 7)) * 16;
 }
 
-constexpr float kAttnSlack = 8.0f;
+constexpr float kAttnRoom = 8.0f;  // log2 of how far the bound is above the maximum that it is taken of
 constexpr float kAttnLowest = -3.402823466e38f;  // a maximum of nothing: no difference with it is NaN
 constexpr uint64_t kAttnTimeoutNs = 2000000000ull;  // of a wait that takes microseconds
 
@@ -452,9 +453,9 @@ struct AttnBf16 {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         t[n][e] = fmaf(s[n][e], p.scale_log2, -m[n][e & 1]);
-        above |= t[n][e] > kAttnSlack;
+        above |= t[n][e] > 0.0f;
       }
-    if (__any_sync(0xFFFFFFFFu, above)) {  // some row's maximum moves
+    if (__any_sync(0xFFFFFFFFu, above)) {  // some row's bound moves
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -463,7 +464,7 @@ struct AttnBf16 {
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-          const float next = fmaxf(m[n][e], top), keep = exp2_fast(m[n][e] - next);
+          const float next = top > m[n][e] ? top + kAttnRoom : m[n][e], keep = exp2_fast(m[n][e] - next);
           m[n][e] = next;
           l[n][e] *= keep;
           t[n][e] = fmaf(s[n][e], p.scale_log2, -next);
@@ -665,8 +666,8 @@ struct AttnF32 {
     }
     bool above = false;
 #pragma unroll
-    for (int h = 0; h < kKept; ++h) above |= fmaf(v[h], p.scale_log2, -m[h]) > kAttnSlack;
-    if (__any_sync(0xFFFFFFFFu, above)) {  // some row's maximum moves
+    for (int h = 0; h < kKept; ++h) above |= fmaf(v[h], p.scale_log2, -m[h]) > 0.0f;
+    if (__any_sync(0xFFFFFFFFu, above)) {  // some row's bound moves
       float keep[kKept];
 #pragma unroll
       for (int h = 0; h < kKept; ++h) {
@@ -675,7 +676,7 @@ struct AttnF32 {
         if (kTake == 4) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        const float next = fmaxf(m[h], top);
+        const float next = top > m[h] ? top + kAttnRoom : m[h];
         keep[h] = exp2_fast(m[h] - next);
         m[h] = next;
         l[h] *= keep[h];
