@@ -14,6 +14,7 @@ kernels on the current CUDA stream, or on `stream`.  Results and workspaces
 that the caller does not pass are allocated on that stream.  There is no
 fallback: without the library the calls raise.  While gradients are recorded,
 a tensor that requires one is refused: there is no backward pass to take it.
+So is a tensor with a tangent of forward-mode differentiation.
 
 The usual calls (the current stream, results allocated, no status word, tensors
 as the kernels take them) are checked and marshalled by _blockcall, a C++
@@ -27,6 +28,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import RSM_F32, ReplaySSMError, _dtype_code, load_library
 
@@ -133,10 +135,13 @@ def _check_device(*tensors):
 
 
 def _check_grad(*tensors):
-    """None wants a gradient that the call would not pass on."""
+    """None wants a gradient that the call would not pass on, or has a tangent (which no_grad() keeps) that it would drop."""
     if torch.is_grad_enabled():
         _need(not any(t is not None and t.requires_grad for t in tensors),
               "the operators are forward only, and a tensor requires a gradient: detach it, or call under torch.no_grad()")
+    if _forward_ad._current_level >= 0:
+        _need(not any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors),
+              "the operators are forward only, and a tensor has a tangent: unpack it first")
 
 
 def _check_rows(t, name, shape, inner, dtype):
