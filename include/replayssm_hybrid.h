@@ -153,7 +153,7 @@ RSM_API int rsm_rotary_append(const rsm_rotary_append_args *args, void *stream);
  */
 typedef struct rsm_paged_attention_args {
   const void *q;   /* [requests, window, num_heads, dim] */
-  void *out;       /* the same, contiguous */
+  void *out;       /* the same, contiguous; may be q itself where that is contiguous */
   void *workspace; /* rsm_paged_attention_workspace() bytes, 256-byte aligned; one call's at a time */
   uint32_t *device_status;
   rsm_pages pages; /* read only */

@@ -283,7 +283,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, *, scale=None, out
     and lengths as for rotary_append, which has put the new tokens' keys and values in.
     New token t of request b is at position lengths[b] - window + t and sees all tokens
     up to its own; H is a multiple of the G key heads.  scale defaults to
-    dim ** -0.5.  Returns the outputs, shaped like q; rows of a request of length 0 are
+    dim ** -0.5.  Returns the outputs, shaped like q (out may be q); rows of a request of length 0 are
     zero.  A call that may be split over the caches' length needs a workspace, which is
     allocated where `workspace` (a contiguous uint8 CUDA tensor, which belongs to one call at a time) is not given.
     """
