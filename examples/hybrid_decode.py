@@ -61,13 +61,23 @@ class Stack:
         self.tables += [rsm.pointer_table([w["A"] for k, w in zip(layers, self.w) if k == "M"]), None, None]
         self.kv, self.conv = tab(of("A", "k") + of("A", "v")), tab(of("M", "conv"))
         self.table, self.free = torch.full((n, pages), -1, dtype=torch.int32), list(range(pages))
+        self.holders = [0] * pages  # requests in whose table a page is
         self.slot = list(range(n))
 
     def hold(self, r, length):
         """Request r gets the pages that `length` tokens need."""
         for i in range(-(-length // self.page)):
             if self.table[r, i] < 0:
-                self.table[r, i] = self.free.pop()
+                page = self.free.pop()
+                self.table[r, i], self.holders[page] = page, 1
+
+    def release(self, r):
+        """Request r gives its pages back: those that no other request holds are free."""
+        for page in self.table[r, self.table[r] >= 0].tolist():
+            self.holders[page] -= 1
+            if self.holders[page] == 0:
+                self.free.append(page)
+        self.table[r] = -1
 
     def __call__(self, x, mamba, attend):
         """x [rows, width] through the layers; mamba(i, xBC, dt) and attend(i, q, k, v) work on the rows."""
@@ -147,13 +157,15 @@ class Stack:
         self.slot = new
 
     def fork(self, r, to, length):
-        """Request `to` becomes a copy of request r, whose `length` tokens are all committed: full pages are shared, the
-        last one, the convolutions' caches and the checkpoints are copied."""
+        """Request `to` becomes a copy of another request r, whose `length` tokens are all committed: full pages are
+        shared, the last one, the convolutions' caches and the checkpoints are copied."""
         full = length // self.page
-        self.table[to] = -1
+        self.release(to)
         self.table[to, :full] = self.table[r, :full]
+        for page in self.table[to, :full].tolist():
+            self.holders[page] += 1
         if length % self.page:
-            self.table[to, full] = self.free.pop()
+            self.hold(to, length)
             p = self.pools[self.layers.index("A")]["k"]
             rsm.copy_pages(*self.kv, i32([int(self.table[r, full])]), i32([int(self.table[to, full])]), dtype=BF16,
                            page_elements=p[0].numel(), num_pages=len(p))
