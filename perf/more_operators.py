@@ -221,7 +221,8 @@ def prepare(case, seed):
         src, dst = order[torch.randint(c["n"], c["pages"] - 1, (c["n"],), generator=h)], order[:c["n"]]
         skip = torch.randperm(c["n"], generator=h)[:c["skipped"]]
         src[skip], dst[skip] = -1, -1
-        s.update(store=store, pools=pools, src=src.to(torch.int32).cuda(), dst=dst.to(torch.int32).cuda())
+        s.update(store=store, pools=pools, src=src.to(torch.int32).cuda(), dst=dst.to(torch.int32).cuda(),
+                 elements=c["page"] * c["G"] * c["dim"])  # of a page
         if own:
             import mamba_replayssm_state_gb300 as rsm
             s.update(ptrs=rsm.pointer_table(pools), strides=rsm.stride_table(pools))
@@ -280,8 +281,8 @@ def _run_own(s):
         return {"q": q, "k_cache": s["k_cache"], "v_cache": s["v_cache"]}
     if s["op"] == "attn":
         return {"y": rsm.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["table"], s["lengths"])}
-    rsm.copy_pages(s["ptrs"], s["strides"], s["src"], s["dst"], dtype=s["pools"][0].dtype,
-                   page_elements=s["pools"][0][0].numel(), num_pages=s["pools"][0].shape[0])
+    rsm.copy_pages(s["ptrs"], s["strides"], s["src"], s["dst"], dtype=s["store"].dtype, page_elements=s["elements"],
+                   num_pages=s["store"].shape[1])
     return {"pools": s["store"]}
 
 
