@@ -24,7 +24,7 @@
 namespace hybrid {
 
 struct RotaryToken {
-  int64_t q, k, v, out;   // element offsets of the token's rows
+  int64_t out;            // element offset of the token's queries in the results
   int64_t k_row, v_row;   // of its rows in the pages; -1: none
   uint32_t pos;
   int live;               // 0: no sequence's, 1: a skipped request's, 2: to be done
@@ -39,7 +39,7 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
   return f < 0.0f ? 0 - n : n;
 }
 
-// Where token i of the call is read and goes.
+// Where token i of the call goes.
 __device__ __forceinline__ RotaryToken rotary_token(const RotaryParams& p, int live, int64_t i) {
   const rsm_pages& pg = p.pages;
   RotaryToken k;
@@ -52,10 +52,9 @@ __device__ __forceinline__ RotaryToken rotary_token(const RotaryParams& p, int l
       k.live = 0;
     else
       t = i - p.cu[b], n = p.cu[b + 1] - p.cu[b];
-    k.q = i * p.q_ts, k.k = i * p.k_ts, k.v = i * p.v_ts, k.out = i * p.out_ts;
+    k.out = i * p.out_ts;
   } else {
     b = i / p.window, t = i - b * p.window, n = p.window;
-    k.q = b * p.q_bs + t * p.q_ts, k.k = b * p.k_bs + t * p.k_ts, k.v = b * p.v_bs + t * p.v_ts;
     k.out = b * p.out_bs + t * p.out_ts;
   }
   k.pos = 0;
