@@ -144,10 +144,12 @@ RSM_API int rsm_rotary_append(const rsm_rotary_append_args *args, void *stream);
  * Tokens in a page out of range are not seen, and flagged; a row that sees none, or none
  * with a score above -infinity, is zero.  dim: 1 .. 256.
  *
- * Arithmetic.  Scores, maxima and sums fp32; the exponentials within 2^-21.  With bf16 inputs
- * and rows of whole 16-byte vectors, the weights (each softmax's numerators) are rounded to
- * bf16 for the product with v: with M the sum of the absolute values of an output's terms it is
- * within 2^-8 |y| + 2^-8 M.
+ * Arithmetic.  Scores, maxima and sums fp32, and the weights (each softmax's numerators) where inputs are fp32 or rows
+ * are no whole 16-byte vectors.  With bf16 inputs the weights meet v with 16 bits where num_heads / num_kv_heads * window
+ * is at most 24 (8 if dim is above 128), else rounded to bf16.  So, with u = 2^-8 for bf16 outputs and 2^-24 for fp32,
+ * r = 0, 2^-15 or 2^-8 for the weights, s the largest sum over |scale q_c k_c| of a score of the row, n its tokens
+ * and M the sum of the absolute values of an output's terms, the output is, to first order, within
+ *     u |y| + (r + 2 s (dim + 2) 2^-23 + 2^-20 + n 2^-23) M.
  * Values that are not finite reach the rows whose token sees them, and no others; a numerator is at most one
  * where it meets its value, so an output is finite where the number of tokens times the largest value is.
  */

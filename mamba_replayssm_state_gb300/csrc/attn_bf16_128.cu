@@ -3,6 +3,6 @@
 
 namespace hybrid {
 
-AttnKernels attn_bf16_128(int rows, bool three) { return attn_bf16<128>(rows, three); }
+AttnKernels attn_bf16_128(int rows, bool three, bool low) { return attn_bf16<128>(rows, three, low); }
 
 }  // namespace hybrid

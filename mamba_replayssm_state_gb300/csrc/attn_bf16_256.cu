@@ -3,6 +3,6 @@
 
 namespace hybrid {
 
-AttnKernels attn_bf16_256(int rows) { return attn_bf16<256>(rows, false); }
+AttnKernels attn_bf16_256(int rows) { return attn_bf16<256>(rows, false, false); }
 
 }  // namespace hybrid

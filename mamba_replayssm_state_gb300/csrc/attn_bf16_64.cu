@@ -3,6 +3,6 @@
 
 namespace hybrid {
 
-AttnKernels attn_bf16_64(int rows) { return attn_bf16<64>(rows, rows <= 16); }
+AttnKernels attn_bf16_64(int rows, bool low) { return attn_bf16<64>(rows, rows <= 16, low); }
 
 }  // namespace hybrid

@@ -14,16 +14,16 @@ AttnKernels attn_kernels() {
 }
 
 template <int DIM>
-AttnKernels attn_bf16(int rows, bool three) {
+AttnKernels attn_bf16(int rows, bool three, bool low) {
   if constexpr (DIM < 256) {
-    if (three && rows == 8) return attn_kernels<AttnBf16<DIM, 1, true>, DIM>();
-    if (rows == 24) return attn_kernels<AttnBf16<DIM, 3, false>, DIM>();
-    if (rows == 32) return attn_kernels<AttnBf16<DIM, 4, false>, DIM>();
+    if (three && rows == 8) return attn_kernels<AttnBf16<DIM, 1, true, true>, DIM>();
+    if (rows == 24) return low ? attn_kernels<AttnBf16<DIM, 3, false, true>, DIM>() : attn_kernels<AttnBf16<DIM, 3, false, false>, DIM>();
+    if (rows == 32) return attn_kernels<AttnBf16<DIM, 4, false, false>, DIM>();
   }
   if constexpr (DIM > 64) {
-    if (rows == 8) return attn_kernels<AttnBf16<DIM, 1, false>, DIM>();
+    if (rows == 8) return attn_kernels<AttnBf16<DIM, 1, false, true>, DIM>();
   }
-  return attn_kernels<AttnBf16<DIM, 2, DIM == 64>, DIM>();
+  return attn_kernels<AttnBf16<DIM, 2, DIM == 64, DIM < 256>, DIM>();
 }
 
 template <int DIM>

@@ -19,7 +19,7 @@
 // The bf16 products are m16n8k16 instructions on registers: with a few rows a 128-row tcgen05
 // tile would be mostly empty.  They are taken the other way round, S^T = K Q^T and
 // O^T = V^T P^T, so that rows come in eights, with P^T turned between them by
-// movmatrix.  The fp32 products run on the CUDA cores, in pairs (fma.rn.f32x2): three tf32
+// movmatrix, as two bf16 parts up to 24 rows (attn_low()).  The fp32 products run on the CUDA cores, in pairs (fma.rn.f32x2): three tf32
 // products each would take three times the instructions, most of them to split the operands.
 //
 // Head sizes between the compiled ones (64, 128, 256) are padded with zeros on the chip; the
@@ -318,7 +318,8 @@ __device__ __forceinline__ float held_value(const AttnStep& a, int token, int co
 // A warp's part of a unit, bf16: 8 N rows.  Lane (quad, four) holds of S^T tokens quad and quad
 // + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.  Up to 16
 // rows' queries stay in registers, those of more (whose outputs take half of them) in shared memory.
-template <int DIM, int N, bool THREE>
+// LOW: weights meet the values as sums of two bf16 values, 16 bits of them, else rounded to 8.
+template <int DIM, int N, bool THREE, bool LOW>
 struct AttnBf16 {
   using IT = uint16_t;
   using Shape = AttnShape<IT, DIM, THREE>;
@@ -397,6 +398,11 @@ struct AttnBf16 {
       }
       __syncthreads();
     }
+  }
+  // What is left of weight w, bits b, behind its upper 16 bits.  Not zero where the weight is not: an infinite
+  // value times either part is infinite.
+  __device__ __forceinline__ static float rest(float w, uint32_t b) {
+    return fmaxf(w - __uint_as_float(b & 0xFFFF0000u), fminf(w, 1.17549435e-38f));
   }
   __device__ __forceinline__ void step(const AttnParams& p, const AttnStep& a, const AttnCursor&, int lane, const char* smem) {
     const int quad = lane >> 2, four = lane & 3;
@@ -498,10 +504,20 @@ struct AttnBf16 {
           }
       });
     uint32_t pb[N][2];
+    [[maybe_unused]] uint32_t low[LOW ? N : 1][2];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) pb[n][h] = transpose8(rsm::pack_bf16x2(s[n][2 * h], s[n][2 * h + 1]));
+      for (int h = 0; h < 2; ++h) {
+        const float w0 = s[n][2 * h], w1 = s[n][2 * h + 1];
+        if constexpr (LOW) {
+          const uint32_t b0 = __float_as_uint(w0), b1 = __float_as_uint(w1);
+          pb[n][h] = transpose8(__byte_perm(b0, b1, 0x7632));
+          low[n][h] = transpose8(rsm::pack_bf16x2(rest(w0, b0), rest(w1, b1)));
+        } else {
+          pb[n][h] = transpose8(rsm::pack_bf16x2(w0, w1));
+        }
+      }
     const int token = a.row + (lane >> 4) * 8 + (lane & 7), odd = lane >> 3 & 1;
     const uint32_t values = a.values + token * 128 + ((odd ^ token) & 7) * 16;
     each<kSteps>([&](auto index) {
@@ -509,7 +525,10 @@ struct AttnBf16 {
       uint32_t va[4];
       ldmatrix4_trans<(i / 4) * (kStep * 128)>(va, values ^ (i % 4 * 32));
 #pragma unroll
-      for (int n = 0; n < N; ++n) mma_bf16(o[i][n], va, pb[n][0], pb[n][1]);
+      for (int n = 0; n < N; ++n) {
+        mma_bf16(o[i][n], va, pb[n][0], pb[n][1]);
+        if constexpr (LOW) mma_bf16(o[i][n], va, low[n][0], low[n][1]);
+      }
     });
   }
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) const {

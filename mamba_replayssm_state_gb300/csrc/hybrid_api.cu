@@ -63,7 +63,7 @@ int launch(const void* fn, int64_t grid, int threads, const void* params, void* 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_attn_ready[kMaxDevices][2][3][33][2][3];  // input type, dim 64, 128, 256, rows, three CTAs an SM, loads
+bool g_attn_ready[kMaxDevices][2][3][33][2][2][3];  // input type, dim 64, 128, 256, rows, three CTAs an SM, low, loads
 
 bool g_rotary_ready[kMaxDevices][2][2];  // input type, 16 bytes at a time
 
@@ -183,6 +183,7 @@ struct AttnPlan {
   int ctas;
   int64_t units;
   bool three;     // CTAs an SM
+  bool low;       // bf16 weights as two values
   bool split;     // units may have more than one tile, so the join has to run
   int64_t bytes;  // of workspace
 };
@@ -204,6 +205,7 @@ AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   pl.rows = es == 2 ? static_cast<int>((each + 7) / 8 * 8) : each > 4 ? 8 : each > 2 ? 4 : static_cast<int>(each);
   pl.units = row_tiles * a->num_kv_heads * a->pages.requests;
   pl.three = hybrid::attn_three(es, pl.dim, pl.rows, pl.units >= 2 * sms);
+  pl.low = hybrid::attn_low(pl.dim, rows);
   const int64_t longest = static_cast<int64_t>(a->pages.table_width) * a->pages.page_size, tile = 4 * hybrid::attn_step(es, pl.dim, pl.three);
   const int64_t most = std::max<int64_t>((longest + tile - 1) / tile, 1);
   pl.split = most > 1;
@@ -213,9 +215,11 @@ AttnPlan plan_attention(const rsm_paged_attention_args* a, int sms) {
   return pl;
 }
 
-hybrid::AttnKernels attention_kernels(int input_dtype, int dim, int rows, bool three) {
-  if (input_dtype == RSM_F32) return dim == 64 ? hybrid::attn_f32_64(rows) : dim == 128 ? hybrid::attn_f32_128(rows) : hybrid::attn_f32_256(rows);
-  return dim == 64 ? hybrid::attn_bf16_64(rows) : dim == 128 ? hybrid::attn_bf16_128(rows, three) : hybrid::attn_bf16_256(rows);
+hybrid::AttnKernels attention_kernels(int input_dtype, const AttnPlan& pl) {
+  if (input_dtype == RSM_F32) return pl.dim == 64 ? hybrid::attn_f32_64(pl.rows) : pl.dim == 128 ? hybrid::attn_f32_128(pl.rows) : hybrid::attn_f32_256(pl.rows);
+  return pl.dim == 64    ? hybrid::attn_bf16_64(pl.rows, pl.low)
+         : pl.dim == 128 ? hybrid::attn_bf16_128(pl.rows, pl.three, pl.low)
+                         : hybrid::attn_bf16_256(pl.rows);
 }
 
 using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -349,9 +353,9 @@ int launch_tiles(const rsm_paged_attention_args* a, const hybrid::AttnParams& ba
   const hybrid::AttnLoads loads = choose_loads(a, pl, &tp);
   p.q_wide = rows_fit(a->q, es, a->pages.requests, a->q_batch_stride, a->window, a->q_stride);
   p.out_wide = reinterpret_cast<uintptr_t>(a->out) % 16 == 0;  // (a head is whole 16-byte vectors)
-  const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl.dim, pl.rows, pl.three);
+  const hybrid::AttnKernels kernels = attention_kernels(a->input_dtype, pl);
   const void* fn = kernels.tiles[static_cast<int>(loads)];
-  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][pl.three][static_cast<int>(loads)], fn, smem);
+  int rc = allow_smem(&g_attn_ready[dev][a->input_dtype == RSM_F32][pl.dim / 128][pl.rows][pl.three][pl.low][static_cast<int>(loads)], fn, smem);
   if (rc != RSM_OK) return rc;
   rc = launch(fn, pl.ctas, hybrid::kAttnThreads, &tp, stream, smem);
   if (rc != RSM_OK || !pl.split) return rc;

@@ -90,6 +90,13 @@ constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256
 // tokens, 8 key heads: 125.5 us, 130.5 of two CTAs; 256 of 78 tokens each 27.7 and 31.1, of 390 73.6 and 72.8); with fewer
 // units there are more pieces to join (8 requests of 1000 tokens 13.6 us, 14.9 of three; one of 131072 29.7 and 30.6).
 constexpr bool attn_three(int esize, int dim, int rows, bool many) { return esize == 2 && (dim == 64 ? rows <= 16 : rows == 8 && dim == 128 && many); }
+// Whether bf16 weights meet the values with 16 bits (`low`; rows: all of a key head): the outputs are then as near to 64
+// bits as of fp32 weights (64 ragged requests: 0.0017 of the norm, which is their own rounding; 0.0020 of weights rounded
+// to 8 bits).  Memory hides the second product up to 16 rows (8 key heads of 128, 100000 tokens in 32 requests: 8 rows
+// 71.2 us, 70.9 of one product, 16 rows 75.9 and 75.3; of 64, 200000 tokens, 16 rows 78.6 and 78.1), nearly so up to 24 (80.4 and 79.7, of 64
+// 85.0 and 83.8; in 128 requests 91.5 and 84.0).  More rows are bound by their products: 32 rows 86 us and, of two, 90, windows of 64
+// and 128 rows 137 and 262 and 157 and 297, 40 rows in two units 117 and 133; so are 16 of heads of 256 (50000 tokens: 81 and 87).
+constexpr bool attn_low(int dim, int64_t rows) { return rows <= (dim == 256 ? 8 : 24); }
 constexpr int attn_step(int esize, int dim, bool three) { return esize * dim > 512 ? 8 : esize * dim > 128 || three ? 16 : 32; }
 constexpr int attn_stages(int esize, int dim, bool three) { return three && esize * dim > 128 ? 2 : 3; }
 constexpr int attn_box(int esize, int dim) { return esize * dim > 512 ? 8 : 16; }  // tokens of a TMA box
@@ -117,8 +124,8 @@ enum class AttnLoads { kRows, kBoxes, kGather };
 struct AttnKernels {
   const void *tiles[3], *join;
 };
-AttnKernels attn_bf16_64(int rows);
-AttnKernels attn_bf16_128(int rows, bool three);
+AttnKernels attn_bf16_64(int rows, bool low);
+AttnKernels attn_bf16_128(int rows, bool three, bool low);
 AttnKernels attn_bf16_256(int rows);
 AttnKernels attn_f32_64(int rows);
 AttnKernels attn_f32_128(int rows);

@@ -4,6 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import hybrid_reference as ref  # noqa: E402
 import mamba_replayssm_state_gb300 as rsm  # noqa: E402
 import test_hybrid_ops_gpu as base  # noqa: E402
 from test_hybrid_ops_gpu import BF16, F32, i32  # noqa: E402
@@ -31,3 +32,17 @@ def test_attention_values_near_the_largest(sign, H, dtype, dim):
     got = rsm.paged_attention(q, kc, vc, table, i32(lengths), scale=1.0)
     assert bool(got.isfinite().all())
     base.attention_check(q, kc, vc, table, lengths, got, scale=1.0)
+
+
+@pytest.mark.parametrize("H,T,dim", [(H, T, dim) for H, T in ((4, 1), (8, 4), (16, 1), (16, 2), (16, 4), (20, 4), (16, 6), (24, 4))
+                                     for dim in (64, 72, 128, 256) if H // 4 * T <= (8 if dim == 256 else 24)])
+def test_attention_weights_are_not_rounded_to_bf16(H, T, dim):
+    """Up to 24 rows a key head (8 of heads above 128), bf16: weights are sums of two bf16 values, cut off and then rounded, so
+    off by 2^-7 2^-8 at most.  Values of both signs make outputs that are small beside the sum of their terms, where
+    2^-8 of each weight would show."""
+    lengths = [T + n for n in (1, 7, 16, 40, 64, 90, 200, 700)]
+    q, kc, vc, table = base.attention_world(lengths, T, H, 4, dim, 16, BF16, False, dim + H + T)
+    got = rsm.paged_attention(q, kc, vc, table, i32(lengths))
+    y, m, top = ref.attention(q, kc, vc, table, lengths, dim ** -0.5)
+    exact = base.attention_bound(y, m, top, dim, max(lengths), F32) - base.U[F32] * y.abs() * 1.01
+    base.close(got, y, base.U[BF16] * y.abs() * 1.01 + exact + 2.0 ** -15 * m)
