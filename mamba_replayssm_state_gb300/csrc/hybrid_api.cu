@@ -451,13 +451,21 @@ int rsm_causal_conv_step(const rsm_causal_conv_step_args* a, void* stream) {
   return launch(hybrid::conv_step_kernel_of(a->input_dtype, a->width, vec), groups * p.cblocks, hybrid::kConvThreads, &p, stream);
 }
 
-// Tokens an SM up to which each has a CTA of its own; us so and in rings, 32 heads and 8, bf16 where not said:
-//   heads of 128 turned whole, halves    2500 tokens 18.6 and 20.8, 3600 23.9 and 24.4, 6000 36.4 and 33.8
-//   the same, fp32 (rings of few tokens) 3000 27.9 and 31.1, 8192 64.3 and 74.0, 16000 120.7 and 138.0
-//   the same, neighbours                 3000 23.5 and 22.4, 6000 42.1 and 33.9
-//   64 of 128 turned                     1200 12.2 and 11.0, 3000 22.9 and 18.6; fp32 1200 16.8 and 15.8
-//   24 of 128 (by fours, in halves)      300 6.5 and 6.5, 600 8.2 and 7.5, 2000 24.2 and 15.2
-int64_t rotary_few(bool whole, bool interleaved, int es) { return !whole ? 6 : interleaved ? 16 : es == 2 ? 24 : INT32_MAX; }
+// Tokens an SM up to which each has a CTA of its own; us so and in rings, 32 heads and 8 of 128:
+//   bf16, turned whole, halves           2432 tokens 18.8 and 20.1, 3648 23.7 and 24.4, 6000 36.0 and 33.8
+//   the same, heads of 72 (by fours)     912 6.5 and 9.1, 2000 13.2 and 14.5, 4000 21.9 and 22.2
+//   the same, neighbours                 2000 17.7 and 18.5, 2432 20.9 and 20.3, 6000 42.0 and 34.0
+//   64 of 128, either                    608 6.2 and 7.5, 760 7.2 and 8.5, 800 9.5 and 8.5, 2000 17.3 and 15.5
+//   24 of 128, by fours (halves)         300 6.8 and 6.7, 450 7.3 and 7.2, 608 8.2 and 7.3, 2000 24.3 and 15.0
+//   fp32, turned whole, halves           760 10.4 and 14.2, 3000 27.4 and 30.8, 16000 120.6 and 138.4 (rings of few tokens)
+//   the same, neighbours                 760 12.2 and 13.4, 800 15.7 and 13.4, 2432 30.8 and 25.7, 16000 160.0 and 132.2
+//   64 of 128, either                    608 10.5 and 10.7, 760 11.4 and 12.1, 800 14.6 and 12.4, 2000 23.8 and 21.9
+// Five an SM are as many CTAs as it takes at once.
+int64_t rotary_few(bool whole, bool by_fours, bool interleaved, int es) {
+  if (!whole) return es == 2 && by_fours ? 3 : 5;
+  if (es == 4) return interleaved ? 5 : INT32_MAX;
+  return interleaved ? 14 : 24;
+}
 
 int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   if (a == nullptr) return fail(RSM_EINVAL, "args is NULL");
@@ -513,7 +521,7 @@ int rsm_rotary_append(const rsm_rotary_append_args* a, void* stream) {
   int dev = 0, sms = 0;
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
-  if (at_once == 1 || p.tokens <= rotary_few(a->rotary_dim == a->dim && at_once == v, a->interleaved != 0, es) * sms || 2 * place > hybrid::kRotaryRingAlone)
+  if (at_once == 1 || p.tokens <= rotary_few(a->rotary_dim == a->dim, at_once == 4, a->interleaved != 0, es) * sms || 2 * place > hybrid::kRotaryRingAlone)
     return launch(hybrid::rotary_token_kernel_of(a->input_dtype, at_once), p.tokens, hybrid::kRotaryPlainThreads, &p, stream);
   const bool alone = 3 * place > hybrid::kRotaryRing;  // (three places: one in, one turned, one out)
   p.stages = static_cast<int>(std::min<int64_t>(hybrid::kRotaryMaxStages, (alone ? hybrid::kRotaryRingAlone : hybrid::kRotaryRing) / place));

@@ -11,8 +11,8 @@
 // shared memory by bulk copies, a ring of them in a CTA that stays for a run of tokens: one
 // warp looks up where they go, makes their sines and cosines (once for all heads) and
 // issues the copies in and out; the others turn the pairs in place, and touch nothing
-// else.  Few tokens, whole fp32 heads, rows that are not whole 16-byte vectors and rows too long for a ring go
-// through rotary_token_kernel.
+// else.  Few tokens (rotary_few()), fp32 heads turned whole in halves, rows that are not whole 16-byte vectors and rows too
+// long for a ring go through rotary_token_kernel.
 //
 // Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens, 32 heads and 8 of 128, half of each
 // turned, bf16: 38 us, 5.3 TB/s (43 through registers, 16 bytes a thread and four tokens ahead); one token

@@ -78,6 +78,19 @@ def test_rotary_rings(H, G, dim, turned, interleaved, form, joined, dtype):
         base.rotary_check(old, k, v, freq, spans, lengths, table, kc, vc, interleaved, 1.25, got.reshape(q.shape), before)
 
 
+@pytest.mark.parametrize("dtype,dim,turned,interleaved,an_sm", [
+    (BF16, 64, 64, False, 24), (BF16, 64, 64, True, 14), (BF16, 64, 32, False, 5), (BF16, 64, 32, True, 5), (BF16, 64, 24, False, 3),
+    (BF16, 40, 40, False, 24), (F32, 64, 64, True, 5), (F32, 64, 32, False, 5), (F32, 64, 64, False, 5)])
+@pytest.mark.parametrize("more", [0, 1])
+def test_rotary_where_rings_begin(dtype, dim, turned, interleaved, an_sm, more):
+    """The last number of tokens that have a CTA each, and the first that share rings (but fp32 halves turned whole, which never do)."""
+    H, G, n = 3, 1, an_sm * sms() + more
+    q, k, v, kc, vc, table, lengths = requests([0, n], 16, H, G, dim, dtype, False, [5, 3], 2, False)
+    before, freq = (kc.clone(), vc.clone()), rand(gen(6), turned // 2).abs()
+    got = rsm.rotary_append(q, k, v, freq, kc, vc, table, i32(lengths), i32([0, 0, n]), interleaved=interleaved)
+    base.rotary_check(q, k, v, freq, [(0, 0), (0, n)], lengths, table, kc, vc, interleaved, 1.0, got, before)
+
+
 @pytest.mark.parametrize("dtype", **TYPES)
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("H,G,dim,turned,stages", [(128, 16, 256, 128, 2), (96, 8, 256, 128, 3), (64, 8, 256, 64, 5)])
