@@ -117,7 +117,7 @@ typedef struct rsm_pages {
  * with the angle exact to 2^-24 of a turn at every position; rotary_dim is even and at most dim, dim at most 256; the other columns stay.  q goes to
  * q_out, k and v to their pages.  The tokens are packed, request b's new ones
  * cu_seqlens[b] .. cu_seqlens[b+1]-1 (any number, also none), or `window` of each request (cu_seqlens NULL).
- * The tokens of different requests lie in different rows of the pages.  A token whose
+ * The tokens of different requests lie in different rows of the pages, and keys in other rows than values.  A token whose
  * page is out of range is flagged, and its k and v are not kept.  Output rows outside every sequence are
  * not written; sequences outside [0, tokens], and all from where cu_seqlens goes back, are skipped and flagged.
  * q_out may be q.

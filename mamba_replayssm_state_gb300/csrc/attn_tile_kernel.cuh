@@ -6,7 +6,7 @@
 //
 // Memory bounds it: 8 rows of 128 columns make 8 multiplications of a byte of keys and
 // values.  So the cache is what is organised.  A CTA has four warps, and
-// each streams a step of 8 to 32 tokens (16 KB or 8) at a time through shared memory of its
+// each streams a step of 8 to 32 tokens (4 to 16 KB of keys and values) at a time through shared memory of its
 // own, two or three stages of it (TMA boxes of up to 16 tokens where pages are whole boxes; else gathers of
 // four rows, a lane each, where the pages make one matrix of rows; else cp.async.  100000 tokens, 8
 // key heads of 128, bf16, in pages of 16, 7 and 1 take 69, 74 and 80 us by boxes and gathers, 104 and
@@ -16,21 +16,22 @@
 // a request instead of all.  So a weight is at most one, and sums of large values do not overflow before their row's
 // quotient would; the largest weight of a row is at least 2^-8, far from where fp32 and bf16 end.
 //
-// The bf16 products are m16n8k16 instructions on registers: with a few rows a 128-row tcgen05
-// tile would be mostly empty.  They are taken the other way round, S^T = K Q^T and
+// The bf16 products are m16n8k16 instructions on registers, taken the other way round, S^T = K Q^T and
 // O^T = V^T P^T, so that rows come in eights, with P^T turned between them by
-// movmatrix, as two bf16 parts up to 24 rows (attn_low()).  The fp32 products run on the CUDA cores, in pairs (fma.rn.f32x2): three tf32
+// movmatrix, as two bf16 parts up to 24 rows (attn_low()).  Up to 16 rows memory hides them.  (tcgen05 takes this form too, 128
+// tokens or columns by rows in eights, with sums in tensor memory; that has not been built, so what it would give
+// where products bind, from 24 rows on, is not known.)  The fp32 products run on the CUDA cores, in pairs (fma.rn.f32x2): three tf32
 // products each would take three times the instructions, most of them to split the operands.
 //
 // Head sizes between the compiled ones (64, 128, 256) are padded with zeros on the chip; the
 // padding is not read from memory.
 //
 // Measured on a GB300 (graphs of calls on changing caches): 200000 tokens in 64 requests, 8 key heads of 128, bf16,
-// 125 us, 6.5 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
+// 126 to 129 us, 6.4 TB/s; one request of 131072 tokens, 2 key heads, 30 us, 4.5 TB/s (a call's start,
 // seven microseconds of lookups and first loads, and the join are a third of it); drafts of 4
 // tokens, 20 rows, 80000 tokens, 67 us, 4.9 TB/s; 50000 tokens, 8 heads of 128 in fp32, 70 us, 5.8
-// TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 85 us where
-// 4 take 75, and more go at 190 TFLOP/s.
+// TB/s.  From 32 rows on the products bind it: 8 new tokens of 4 heads a key head take 86 us where
+// 4 take 76, and more go at 190 TFLOP/s.
 //
 // The work of a call is its (request, key head, group of rows) units' tiles of four steps,
 // one after the other, and with each unit two to four tiles more for what its end takes; every CTA
@@ -149,7 +150,7 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* sr
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(yes ? 16 : 0) : "memory");
 }
 
-// The box of 16 tokens and 128 bytes at (column, head, row, page).
+// The box of attn_box() tokens and 128 bytes at (column, head, row, page).
 __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int column, int head, int row, int page, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
@@ -316,8 +317,8 @@ __device__ __forceinline__ float held_value(const AttnStep& a, int token, int co
 }
 
 // A warp's part of a unit, bf16: 8 N rows.  Lane (quad, four) holds of S^T tokens quad and quad
-// + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.  Up to 16
-// rows' queries stay in registers, those of more (whose outputs take half of them) in shared memory.
+// + 8, rows 8 n + 2 four + {0, 1}; of O^T columns 16 i + quad and + 8, the same rows.  Queries stay in
+// registers where outputs leave room for them (attn_shared_queries()), else in shared memory.
 // LOW: weights meet the values as sums of two bf16 values, 16 bits of them, else rounded to 8.
 template <int DIM, int N, bool THREE, bool LOW>
 struct AttnBf16 {

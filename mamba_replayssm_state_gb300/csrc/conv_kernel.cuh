@@ -11,9 +11,10 @@
 // on their way there (cp.async), each in a place that only its thread writes and reads: no barriers,
 // and more bytes in flight than registers would hold.
 //
-// Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens of 18432 bf16 channels 95 us, 6.3
-// TB/s (129 with the rows to come in registers); 256 requests'
-// single tokens 13.4 us, 4.3 TB/s with the launch's 2.3; 37 tokens of 5376 channels 4.6 us.
+// Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens of 18432 bf16 channels 96 us, 6.3
+// TB/s (129 with the rows to come in registers), of fp32 190 us, 6.4 TB/s; 256 requests'
+// single tokens 13.5 us, 4.2 TB/s with the launch's 2.3; 37 tokens of 5376 channels 4.8 us.  One channel a thread,
+// where rows are no whole 16 bytes: 8192 tokens of 5377 bf16 channels 151 us, 1.2 TB/s.
 #pragma once
 #include "hybrid_device.cuh"
 #include "rsm_ptx.cuh"

@@ -410,9 +410,9 @@ int rsm_causal_conv(const rsm_causal_conv_args* a, void* stream) {
   rc = device_sms(&dev, &sms);
   if (rc != RSM_OK) return rc;
   // As many tokens a CTA as leave four CTAs an SM, in fours: at least four, for the shortest way through (37
-  // tokens of 5376 channels: 5.1 us, 5.8 of eight, 7.2 of 16), at most 48, of which three rows are read
-  // twice (8192 tokens of 18432 channels: 95.3 us, 96.0 of 32, 97.0 of 64).  In between (1024 and 4096 tokens of
-  // 5376 channels) 12 and 44 take 9.7 and 21.4 us, four 14.8 and 43.7.
+  // tokens of 5376 channels: 4.9 us, 5.3 of eight, 6.3 of 16), at most 48, of which three rows are read
+  // twice (8192 tokens of 18432 channels: 96.2 us, 96.3 of 32, 97.0 of 64).  In between (1024 and 4096 tokens of
+  // 5376 channels) 12 and 44 take 9.7 and 22.6 us, four 14.2 and 43.9.
   p.block = static_cast<int>(std::min<int64_t>(48, std::max<int64_t>(1, (a->tokens * p.cblocks / (4 * sms) + 3) / 4) * 4));
   const int64_t blocks = (a->tokens + p.block - 1) / p.block;
   return launch(hybrid::conv_kernel(a->input_dtype, a->width, vec), blocks * p.cblocks, hybrid::kConvThreads, &p, stream);

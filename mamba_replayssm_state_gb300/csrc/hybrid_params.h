@@ -77,7 +77,9 @@ constexpr int kAttnThreads = 128, kAttnJoinThreads = 256;
 // Tiles that the end of a unit counts: the more, the more values its warps have to put together (100000 tokens of 8 key
 // heads of 128: 32 rows in 32 requests 85 us with four tiles, 99 with two; 24 rows in 128 83 and 99; 16 in 128 78 with
 // three, 87 with two; heads of 256, 50000 tokens: 8 rows 74 with three, 79 with two, 16 rows 81 with four, 84 with three.
-// One tile: 20 rows 77 us, 67 with more; six or eight: 24 rows in 128 requests 87 and 94).
+// One tile: 20 rows 77 us, 67 with more; six or eight: 24 rows in 128 requests 87 and 94.  fp32, 1, 2 and 3 tiles: heads of 128, 50000
+// tokens, 8 rows in 32 requests 99, 95 and 94, in 128 123, 118 and 119, 1 row in 32 67.6, 67.9 and 69.0, in 128 70, 71 and 73; heads of
+// 64, 100000 tokens, 8 rows in 128 93, 84 and 86; heads of 256, 25000 tokens, 1 row in 128 75, 78 and 81, 4 rows 96, 94 and 99).
 constexpr int attn_unit_end(int esize, int dim, int rows) {
   const int values = dim * rows;  // of an output
   return esize == 4 ? 2 : rows > 16 || values > 2048 ? 4 : rows > 8 || values > 1024 ? 3 : 2;
@@ -90,12 +92,14 @@ constexpr int attn_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256
 // tokens, 8 key heads: 125.5 us, 130.5 of two CTAs; 256 of 78 tokens each 27.7 and 31.1, of 390 73.6 and 72.8); with fewer
 // units there are more pieces to join (8 requests of 1000 tokens 13.6 us, 14.9 of three; one of 131072 29.7 and 30.6).
 constexpr bool attn_three(int esize, int dim, int rows, bool many) { return esize == 2 && (dim == 64 ? rows <= 16 : rows == 8 && dim == 128 && many); }
-// Whether bf16 weights meet the values with 16 bits (`low`; rows: all of a key head): the outputs are then as near to 64
-// bits as of fp32 weights (64 ragged requests: 0.0017 of the norm, which is their own rounding; 0.0020 of weights rounded
-// to 8 bits).  Memory hides the second product up to 16 rows (8 key heads of 128, 100000 tokens in 32 requests: 8 rows
-// 71.2 us, 70.9 of one product, 16 rows 75.9 and 75.3; of 64, 200000 tokens, 16 rows 78.6 and 78.1), nearly so up to 24 (80.4 and 79.7, of 64
-// 85.0 and 83.8; in 128 requests 91.5 and 84.0).  More rows are bound by their products: 32 rows 86 us and, of two, 90, windows of 64
-// and 128 rows 137 and 262 and 157 and 297, 40 rows in two units 117 and 133; so are 16 of heads of 256 (50000 tokens: 81 and 87).
+// Whether bf16 weights meet the values with 16 bits (`low`; rows: all of a key head), as sums of two bf16 values: outputs are
+// then as near to 64 bits as with fp32 weights (64 ragged requests: 0.00165 of the norm, their own rounding; 0.0020 with
+// weights rounded to 8 bits).  us with one product and with two, 8 key heads of 128, 100000 tokens in 32 requests:
+//   8 rows 70.9 and 71.2, 16 rows 75.3 and 76.1, 24 rows 80.1 and 80.3: memory hides the second
+//   24 rows in 128 requests 84 and 91.5; 32 rows 86 and 90; windows of 64 and 128 rows 137 and 157, 262 and 297; 40 rows, two
+//   units of 24, 117 and 133: the products bind
+// Heads of 64, 200000 tokens: 16 rows 79.3 and 80.3, 24 rows 85.2 and 85.0, 32 rows 86.5 and 99.7; of 256, 50000 tokens: 8 rows 74.7
+// and 75.3, 16 rows 81 and 86.
 constexpr bool attn_low(int dim, int64_t rows) { return rows <= (dim == 256 ? 8 : 24); }
 constexpr int attn_step(int esize, int dim, bool three) { return esize * dim > 512 ? 8 : esize * dim > 128 || three ? 16 : 32; }
 constexpr int attn_stages(int esize, int dim, bool three) { return three && esize * dim > 128 ? 2 : 3; }

@@ -15,8 +15,8 @@
 // long for a ring go through rotary_token_kernel.
 //
 // Measured on a GB300 (graphs of calls on changing inputs): 8192 tokens, 32 heads and 8 of 128, half of each
-// turned, bf16: 38 us, 5.3 TB/s (43 through registers, 16 bytes a thread and four tokens ahead); one token
-// 3.3 us, of which a launch is 2.3.
+// turned, bf16: 38 to 39 us, 5.2 TB/s (43 through registers, 16 bytes a thread and four tokens ahead); one token
+// 3.3 to 3.8 us, of which a launch is 2.3.  A value at a time, where pairs or rows are no whole vectors (6 of 128 turned): 179 us.
 #pragma once
 #include "hybrid_device.cuh"
 #include "rsm_ptx.cuh"

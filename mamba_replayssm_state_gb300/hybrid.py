@@ -367,7 +367,10 @@ def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, or
     scaling None: as they are; "linear": all divided by factor; "ntk": a base that divides the
     lowest by factor and leaves the highest; "yarn" (Peng et al., 2023): a frequency that makes fewer
     than `slow` turns over original_length tokens is divided by factor, one that makes more
-    than `fast` is left, those between are mixed, and the amplitude is 0.1 ln(factor) + 1.
+    than `fast` is left, one with r turns between is mixed by the paper's equation, keep f + (1 - keep) f / factor
+    with keep = (r - slow) / (fast - slow), linear in r, and the amplitude is 0.1 ln(factor) + 1.  Programs that take
+    `keep` as linear in the pair's index j instead, between rounded bounds, get other frequencies there: a model that
+    was trained so needs those, which go to rotary_append as any vector does.
     """
     _need(rotary_dim > 0 and rotary_dim % 2 == 0, "rotary_dim must be even and positive")
     _need(factor > 0, "factor must be positive")
