@@ -114,7 +114,8 @@ typedef struct rsm_pages {
  * (2j, 2j + 1) where `interleaved`, else (j, j + rotary_dim / 2); at position p pair
  * (a, b) becomes
  *     amplitude (a cos(p f_j) - b sin(p f_j),  b cos(p f_j) + a sin(p f_j)),   f = inv_freq
- * with the angle exact to 2^-24 of a turn at every position; rotary_dim is even and at most dim, dim at most 256; the other columns stay.  q goes to
+ * with the angle exact to 2^-24 of a turn at every position; where |f_j| is not below 2^40 the pair becomes NaN.
+ * rotary_dim is even and at most dim, dim at most 256; the other columns stay.  q goes to
  * q_out, k and v to their pages.  The tokens are packed, request b's new ones
  * cu_seqlens[b] .. cu_seqlens[b+1]-1 (any number, also none), or `window` of each request (cu_seqlens NULL).
  * The tokens of different requests lie in different rows of the pages, and keys in other rows than values.  A token whose

@@ -30,7 +30,8 @@ struct RotaryToken {
   int live;               // 0: no sequence's, 1: a skipped request's, 2: to be done
 };
 
-// f / (2 pi) mod 1 in units of 2^-64.  1 / (2 pi) is given to 106 bits, as the sum of two doubles.
+// f / (2 pi) mod 1 in units of 2^-64.  1 / (2 pi) is given to 106 bits, as the sum of two doubles: below 2^40 what they
+// leave out, times 2^31 positions, stays below 2^-24 turns.
 __device__ __forceinline__ uint64_t turns_per_position(float f) {
   constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
   const double d = fabs(static_cast<double>(f)), t = d * hi, e = fma(d, hi, -t) + d * lo;
@@ -38,6 +39,9 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
   const uint64_t n = __double2ull_rz(part * 0x1p64) + static_cast<uint64_t>(__double2ll_rn(e * 0x1p64));
   return f < 0.0f ? 0 - n : n;
 }
+
+// Of a frequency that is none, or 2^40 or more, every turn is NaN.
+__device__ __forceinline__ float amplitude_of(float f, float amplitude) { return fabsf(f) < 0x1p40f ? amplitude : __int_as_float(0x7FFFFFFF); }
 
 // Where token i of the call goes.
 __device__ __forceinline__ RotaryToken rotary_token(const RotaryParams& p, int live, int64_t i) {
@@ -140,8 +144,9 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
     RotaryToken mine{};  // of 32 tokens, a lane each
     if (lane < count) mine = rotary_token(p, live, begin + lane);
     uint64_t step[kRotaryMaxHalf / 32];
+    float amplitude[kRotaryMaxHalf / 32];
 #pragma unroll
-    for (int j = 0; j < kRotaryMaxHalf / 32; ++j) step[j] = turns_per_position(freq[j]);
+    for (int j = 0; j < kRotaryMaxHalf / 32; ++j) step[j] = turns_per_position(freq[j]), amplitude[j] = amplitude_of(freq[j], p.amplitude);
     auto info = [&](int64_t i, int s) {
       if (i > 0 && i % 32 == 0 && i + lane < count) mine = rotary_token(p, live, begin + i + lane);
       const int from = static_cast<int>(i % 32);
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const __g
       if (state == 2) {
 #pragma unroll
         for (int j = 0; j < kRotaryMaxHalf / 32; ++j)
-          if (lane + 32 * j < p.half) turns[s * p.half + lane + 32 * j] = rotary_turn(pos, step[j], p.amplitude);
+          if (lane + 32 * j < p.half) turns[s * p.half + lane + 32 * j] = rotary_turn(pos, step[j], amplitude[j]);
       }
       __syncwarp();
       if (lane == 0) rsm::mbar_arrive(full + 8 * s);
@@ -300,13 +305,17 @@ __global__ void __launch_bounds__(kRotaryPlainThreads) rotary_token_kernel(const
   Item it;
   if (static_cast<int>(threadIdx.x) < items) it = load(threadIdx.x);
   uint64_t step = 0;
-  if (static_cast<int>(threadIdx.x) < p.half) step = turns_per_position(p.inv_freq[threadIdx.x]);
+  float amplitude = 0.0f;
+  if (static_cast<int>(threadIdx.x) < p.half) {
+    const float f = p.inv_freq[threadIdx.x];
+    step = turns_per_position(f), amplitude = amplitude_of(f, p.amplitude);
+  }
   const int live = p.cu == nullptr ? 0 : live_sequences(p.cu, pg.requests, p.tokens, p.status, blockIdx.x == 0);
   if (threadIdx.x == kRotaryPlainThreads - 1) token = rotary_token(p, live, blockIdx.x);
   __syncthreads();
   const RotaryToken to = token;
   if (to.live == 0) return;
-  if (static_cast<int>(threadIdx.x) < p.half) turn[threadIdx.x] = rotary_turn(to.pos, step, p.amplitude);
+  if (static_cast<int>(threadIdx.x) < p.half) turn[threadIdx.x] = rotary_turn(to.pos, step, amplitude);
   __syncthreads();
   Item ahead;
   for (int i = threadIdx.x; i < items; i += kRotaryPlainThreads, it = ahead) {

@@ -46,3 +46,35 @@ def test_attention_weights_are_not_rounded_to_bf16(H, T, dim):
     y, m, top = ref.attention(q, kc, vc, table, lengths, dim ** -0.5)
     exact = base.attention_bound(y, m, top, dim, max(lengths), F32) - base.U[F32] * y.abs() * 1.01
     base.close(got, y, base.U[BF16] * y.abs() * 1.01 + exact + 2.0 ** -15 * m)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim", [64, 22])
+@pytest.mark.parametrize("tokens", [40, 6000])
+def test_rotary_frequencies_that_are_no_numbers(tokens, dim, interleaved, dtype):
+    """Pairs of a frequency that is not a number, infinite or 2^40 and more become NaN, by each kernel; the others, one just
+    below 2^40 among them, are as ever."""
+    H, G, page, n = 3, 1, 64, 10
+    table = torch.arange(-(-tokens // page), device="cuda", dtype=torch.int32)[None]
+    kc, vc = base.pools(base.gen(1), table.numel(), page, G, dim, dtype, False)
+    q, k, v = (base.rand(base.gen(i), tokens, h, dim, dtype=dtype) for i, h in ((2, H), (3, G), (4, G)))
+    freq = base.rand(base.gen(5), n).abs()
+    freq[2] = 2.0 ** 40 - 2.0 ** 17
+    odd = [1, 4, 5, 8]
+    freq[odd] = torch.tensor([float("nan"), float("inf"), -float("inf"), -2.0 ** 40], device="cuda")
+    cu, status = i32([0, tokens]), base.word()
+    got = rsm.rotary_append(q, k, v, freq, kc, vc, table, i32([tokens]), cu, interleaved=interleaved, device_status=status)
+    assert int(status) == 0
+    columns = [c for j in odd for c in ((2 * j, 2 * j + 1) if interleaved else (j, j + n))]
+    at = torch.arange(tokens, device="cuda")
+    to = table[0, at // page].long(), at % page
+    keys = kc[to]
+    assert bool(got[..., columns].isnan().all()) and bool(keys[..., columns].isnan().all())
+    good = torch.where(freq.abs() < 2.0 ** 40, freq, 0.0)
+    wq, mq = ref.rotate(q, at, good, interleaved, 1.0)
+    wk, mk = ref.rotate(k, at, good, interleaved, 1.0)
+    others = [c for c in range(dim) if c not in columns]
+    for y, w, m in ((got, wq, mq), (keys, wk, mk)):
+        base.close(y[..., others], w[..., others], (base.U[dtype] * w.abs() * 1.01 + 16 * base.E * m)[..., others])
+    assert torch.equal(vc[to], v)
