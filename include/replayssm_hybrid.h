@@ -151,8 +151,9 @@ RSM_API int rsm_rotary_append(const rsm_rotary_append_args *args, void *stream);
  * r = 0, 2^-15 or 2^-8 for the weights, s the largest sum over |scale q_c k_c| of a score of the row, n its tokens
  * and M the sum of the absolute values of an output's terms, the output is, to first order, within
  *     u |y| + (r + 2 s (dim + 2) 2^-23 + 2^-20 + n 2^-23) M.
- * Values that are not finite reach the rows whose token sees them, and no others; a numerator is at most one
- * where it meets its value, so an output is finite where the number of tokens times the largest value is.
+ * Values that are not finite reach the rows whose token sees them, and no others; a numerator is at most one,
+ * to within its score's rounding, where it meets its value, so an output is finite where the number of tokens times
+ * the largest value is well below the largest fp32 value.
  */
 typedef struct rsm_paged_attention_args {
   const void *q;   /* [requests, window, num_heads, dim] */
